@@ -247,17 +247,17 @@ def _handles(st):
         st["desc"] = E.QkNormRopeDesc(c["batch"], c["rows"], c["hq"], c["hkv"], c["dim"], c["rot"],
                                       (c["hq"] + 2 * c["hkv"]) * c["dim"] + c["pad"], int(c["interleaved"]), 1e-6, dt)
     elif c["op"] in ("write", "read"):
-        st["desc"] = E.Kv8Desc(c["batch"], c["hkv"], c["dim"], c["cap"], c["rows"], dt)
+        st["desc"] = E.KvqDesc(c["batch"], c["hkv"], c["dim"], c["cap"], c["rows"], dt)
     elif c["op"] == "commit":
         st["desc"] = E.CommitDesc(c["layers"], c["batch"], c["hkv"], c["dim"], c["rows"], c["cap"], c["depth"], dt, 0,
                                   dt)
-        st["layers"] = E.Kv8LayerPointers(*[list(st[n].unbind(0)) for n in ("k8", "ks", "v8", "vs", "tk", "tv")])
+        st["layers"] = E.KvqLayerPointers(*[list(st[n].unbind(0)) for n in ("k8", "ks", "v8", "vs", "tk", "tv")])
     else:
         f32 = c["out"] == "f32"
         st["desc"] = E.AttnDesc(c["batch"], c["rows"], c["hq"], c["hkv"], c["dim"], st["k8"].shape[2],
                                 1.0 / math.sqrt(c["dim"]), E.EAGLE_BF16, 0, E.EAGLE_F32 if f32 else E.EAGLE_BF16,
                                 E.EAGLE_ATTN_PRECISE if f32 else E.EAGLE_ATTN_FAST)
-        st["ws"] = torch.zeros(E.workspace_size(E.EAGLE_WS_TREE_ATTN_KV8, st["desc"]), device="cuda", dtype=torch.uint8)
+        st["ws"] = torch.zeros(E.workspace_size(E.EAGLE_WS_TREE_ATTN_KVQ, st["desc"]), device="cuda", dtype=torch.uint8)
 
 
 # ------------------------------------------------------------------------------- one pass
@@ -270,19 +270,19 @@ def run(st):
                                  st["k"], st["v"])
             return st["q"], st["k"], st["v"]
         if op == "write":
-            E.eagle_kv8_write(st["desc"], st["k"], st["v"], st["start"], st["count"], st["k8"], st["ks"], st["v8"],
+            E.eagle_kvq_write(st["desc"], st["k"], st["v"], st["start"], st["count"], st["k8"], st["ks"], st["v8"],
                               st["vs"], st["status"])
             return st["k8"], st["ks"], st["v8"], st["vs"], st["status"]
         if op == "read":
-            E.eagle_kv8_read(st["desc"], st["k8"], st["ks"], st["v8"], st["vs"], st["start"], st["count"], st["k"],
+            E.eagle_kvq_read(st["desc"], st["k8"], st["ks"], st["v8"], st["vs"], st["start"], st["count"], st["k"],
                              st["v"], st["status"])
             return st["k"], st["v"], st["status"]
         if op == "commit":
             st["seq"].copy_(st["seq0"])  # the same step again
-            E.eagle_kv8_commit(st["desc"], st["layers"], st["n_acc"], st["path"], st["seq"], st["pos"],
+            E.eagle_kvq_commit(st["desc"], st["layers"], st["n_acc"], st["path"], st["seq"], st["pos"],
                                status=st["status"])
             return st["k8"], st["ks"], st["v8"], st["vs"], st["seq"], st["pos"], st["status"]
-        E.eagle_tree_attn_kv8(st["desc"], st["qq"], st["k8"], st["ks"], st["v8"], st["vs"], st["tk"], st["tv"],
+        E.eagle_tree_attn_kvq(st["desc"], st["qq"], st["k8"], st["ks"], st["v8"], st["vs"], st["tk"], st["tv"],
                               st["seq"], st["mask"], st["out"], st["lse"], st["ws"], n_nodes=st["nodes"])
         return st["out"], st["lse"]
     return {"rope": _rope, "write": _write, "read": _read, "commit": _commit, "attn": _attn}[op](st)
