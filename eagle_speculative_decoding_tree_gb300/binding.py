@@ -32,7 +32,9 @@ EXPORTED_SYMBOLS = ("eagle_tree_build", "eagle_tree_attn", "eagle_accept", "eagl
                     "eagle_workspace_size", "eagle_status_string", "eagle_version",
                     "eagle_tree_frontier_rows", "eagle_tree_max_frontier", "eagle_last_cuda_error",
                     "eagle_last_cuda_error_string", "eagle_tree_attn_plan", "eagle_accept_noalloc",
-                    "eagle_selftest_ff_log", "eagle_lmhead_stats", "eagle_ttt_attn", "eagle_tree_build_head")
+                    "eagle_selftest_ff_log", "eagle_lmhead_stats", "eagle_ttt_attn", "eagle_tree_build_head",
+                    "eagle_kvq_write", "eagle_kvq_read", "eagle_kvq_commit", "eagle_tree_attn_kvq",
+                    "eagle_qk_norm_rope")
 
 
 class TreeDesc(ctypes.Structure):
@@ -86,6 +88,20 @@ class CommitDesc(ctypes.Structure):
                                               "max_depth", "dtype", "feat_dim", "feat_dtype")]
 
 
+EAGLE_WS_TREE_ATTN_KVQ = 5
+EAGLE_KVQ_BLOCK = 64  # rows of an 8-bit cache block that share a scale
+
+
+class KvqDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "n_kv_heads", "head_dim", "max_seq", "rows", "dtype")]
+
+
+class QkNormRopeDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "rows", "n_q_heads", "n_kv_heads", "head_dim", "rot_dim",
+                                              "row_stride", "interleaved")] + \
+               [("eps", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
 # ----------------------------------------------------------------------------- loading
 _lib = None
 
@@ -115,6 +131,11 @@ def load() -> ctypes.CDLL:
         L.eagle_ttt_attn.argtypes = [ctypes.POINTER(TttDesc), vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.eagle_tree_build_head.argtypes = [ctypes.POINTER(TreeDesc), i32, vp, vp, i32, vp, vp, vp, sz,
                                             ctypes.POINTER(TreeOut), vp, vp]
+        L.eagle_kvq_write.argtypes = [ctypes.POINTER(KvqDesc)] + [vp] * 10
+        L.eagle_kvq_read.argtypes = [ctypes.POINTER(KvqDesc)] + [vp] * 10
+        L.eagle_kvq_commit.argtypes = [ctypes.POINTER(CommitDesc)] + [vp] * 14
+        L.eagle_tree_attn_kvq.argtypes = [ctypes.POINTER(AttnDesc)] + [vp] * 13 + [sz, vp]
+        L.eagle_qk_norm_rope.argtypes = [ctypes.POINTER(QkNormRopeDesc)] + [vp] * 10
         L.eagle_workspace_size.argtypes = [i32, vp]
         L.eagle_workspace_size.restype = sz
         L.eagle_status_string.argtypes = [i32]
@@ -128,7 +149,8 @@ def load() -> ctypes.CDLL:
                                            ctypes.POINTER(ctypes.c_int32)]
         for f in (L.eagle_tree_build, L.eagle_tree_build_head, L.eagle_tree_attn, L.eagle_accept, L.eagle_kv_commit,
                   L.eagle_tree_frontier_rows, L.eagle_tree_max_frontier, L.eagle_tree_attn_plan,
-                  L.eagle_accept_noalloc):
+                  L.eagle_accept_noalloc, L.eagle_kvq_write, L.eagle_kvq_read, L.eagle_kvq_commit,
+                  L.eagle_tree_attn_kvq, L.eagle_qk_norm_rope):
             f.restype = ctypes.c_int
         _lib = L
     return _lib
@@ -378,3 +400,80 @@ def eagle_ttt_attn(desc: TttDesc, q, k_trunk, v_trunk, k_branch, v_branch, out, 
         _ptr(v_trunk, torch.bfloat16, "v_trunk"), _ptr(k_branch, torch.bfloat16, "k_branch"),
         _ptr(v_branch, torch.bfloat16, "v_branch"), _ptr(out, FLOATS, "out"), _ptr(lse, torch.float32, "lse"),
         _ptr(ws, name="ws"), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+# ----------------------------------------------------------------------------- 8-bit KV cache
+CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def eagle_kvq_write(desc: KvqDesc, k, v, start, count: Optional[torch.Tensor], k_codes, k_scale, v_codes, v_scale,
+                    status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Quantise K/V rows into the 8-bit cache (see eagle.h: eagle_kvq_write).  Codes are
+    uint8 or float8_e4m3fn tensors [B][Hkv][P][D], scales fp32 [B][Hkv][ceil(P / 64)]."""
+    _check("eagle_kvq_write", load().eagle_kvq_write(
+        ctypes.byref(desc), _ptr(k, FLOATS, "k"), _ptr(v, FLOATS, "v"), _ptr(start, torch.int32, "start"),
+        _ptr(count, torch.int32, "count"), _ptr(k_codes, CODES, "k_codes"), _ptr(k_scale, torch.float32, "k_scale"),
+        _ptr(v_codes, CODES, "v_codes"), _ptr(v_scale, torch.float32, "v_scale"), _ptr(status, torch.int32, "status"),
+        _stream(stream)))
+
+
+def eagle_kvq_read(desc: KvqDesc, k_codes, k_scale, v_codes, v_scale, start, count: Optional[torch.Tensor], k, v,
+                   status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Read rows of the 8-bit cache back (see eagle.h: eagle_kvq_read)."""
+    _check("eagle_kvq_read", load().eagle_kvq_read(
+        ctypes.byref(desc), _ptr(k_codes, CODES, "k_codes"), _ptr(k_scale, torch.float32, "k_scale"),
+        _ptr(v_codes, CODES, "v_codes"), _ptr(v_scale, torch.float32, "v_scale"), _ptr(start, torch.int32, "start"),
+        _ptr(count, torch.int32, "count"), _ptr(k, FLOATS, "k"), _ptr(v, FLOATS, "v"),
+        _ptr(status, torch.int32, "status"), _stream(stream)))
+
+
+class KvqLayerPointers:
+    """HOST arrays of per-layer device pointers for eagle_kvq_commit (built once, reused)."""
+
+    def __init__(self, k_codes: Sequence[torch.Tensor], k_scale: Sequence[torch.Tensor],
+                 v_codes: Sequence[torch.Tensor], v_scale: Sequence[torch.Tensor], tree_k: Sequence[torch.Tensor],
+                 tree_v: Sequence[torch.Tensor]):
+        n = len(k_codes)
+        mk = lambda ts, dt, nm: (ctypes.c_void_p * n)(*[_ptr(t, dt, nm) for t in ts])
+        f32 = torch.float32
+        self.k, self.ks = mk(k_codes, CODES, "k_codes"), mk(k_scale, f32, "k_scale")
+        self.v, self.vs = mk(v_codes, CODES, "v_codes"), mk(v_scale, f32, "v_scale")
+        self.tk, self.tv = mk(tree_k, FLOATS, "tree_k"), mk(tree_v, FLOATS, "tree_v")
+        self.tensors = [list(t) for t in (k_codes, k_scale, v_codes, v_scale, tree_k, tree_v)]
+
+
+def eagle_kvq_commit(desc: CommitDesc, layers: KvqLayerPointers, n_acc, path, seq_len, commit_pos,
+                     feat_cache=None, tree_feat=None, status=None, stream=None) -> None:
+    """Commit the accepted path into 8-bit caches (see eagle.h: eagle_kvq_commit)."""
+    _check("eagle_kvq_commit", load().eagle_kvq_commit(
+        ctypes.byref(desc), layers.k, layers.ks, layers.v, layers.vs, layers.tk, layers.tv,
+        _ptr(n_acc, torch.int32, "n_acc"), _ptr(path, torch.int32, "path"), _ptr(seq_len, torch.int32, "seq_len"),
+        _ptr(commit_pos, torch.int32, "commit_pos"), _ptr(feat_cache, FLOATS, "feat_cache"),
+        _ptr(tree_feat, FLOATS, "tree_feat"), _ptr(status, torch.int32, "status"), _stream(stream)))
+
+
+def eagle_tree_attn_kvq(desc: AttnDesc, q, k_codes, k_scale, v_codes, v_scale, tree_k, tree_v, seq_len, anc_mask,
+                        out, lse: Optional[torch.Tensor], ws: torch.Tensor, stream=None,
+                        n_nodes: Optional[torch.Tensor] = None) -> None:
+    """One layer of tree attention over the 8-bit cache (see eagle.h: eagle_tree_attn_kvq)."""
+    bf16 = torch.bfloat16
+    _check("eagle_tree_attn_kvq", load().eagle_tree_attn_kvq(
+        ctypes.byref(desc), _ptr(q, bf16, "q"), _ptr(k_codes, CODES, "k_codes"),
+        _ptr(k_scale, torch.float32, "k_scale"), _ptr(v_codes, CODES, "v_codes"),
+        _ptr(v_scale, torch.float32, "v_scale"), _ptr(tree_k, bf16, "tree_k"), _ptr(tree_v, bf16, "tree_v"),
+        _ptr(seq_len, torch.int32, "seq_len"), _ptr(n_nodes, torch.int32, "n_nodes"),
+        _ptr(anc_mask, torch.int64, "anc_mask"), _ptr(out, FLOATS, "out"), _ptr(lse, torch.float32, "lse"),
+        _ptr(ws, name="ws"), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+# ----------------------------------------------------------------------------- norms and rotation
+def eagle_qk_norm_rope(desc: QkNormRopeDesc, qkv, q_weight: Optional[torch.Tensor],
+                       k_weight: Optional[torch.Tensor], inv_freq, pos_id, q, k, v, stream=None,
+                       n_nodes: Optional[torch.Tensor] = None) -> None:
+    """Norms of the query and key heads, rotation and tree layout (see eagle.h:
+    eagle_qk_norm_rope)."""
+    _check("eagle_qk_norm_rope", load().eagle_qk_norm_rope(
+        ctypes.byref(desc), _ptr(qkv, FLOATS, "qkv"), _ptr(q_weight, FLOATS, "q_weight"),
+        _ptr(k_weight, FLOATS, "k_weight"), _ptr(inv_freq, torch.float32, "inv_freq"),
+        _ptr(pos_id, torch.int32, "pos_id"), _ptr(n_nodes, torch.int32, "n_nodes"), _ptr(q, FLOATS, "q"),
+        _ptr(k, FLOATS, "k"), _ptr(v, FLOATS, "v"), _stream(stream)))

@@ -106,6 +106,33 @@ int check_accept_desc(const eagle_accept_desc* d) {
   return EAGLE_OK;
 }
 
+// eagle_tree_attn's envelope, bf16 only; TMA row coordinates are 32-bit.
+int check_kvq_attn_desc(const eagle_attn_desc* d) {
+  const int rc = check_attn_desc(d);
+  if (rc != EAGLE_OK) return rc;
+  if (d->dtype != EAGLE_BF16 || d->fault_test != 0) return EAGLE_ERR_UNSUPPORTED;
+  if (d->engine != EAGLE_ENGINE_AUTO && d->engine != EAGLE_ENGINE_MMA_SYNC) return EAGLE_ERR_INVALID_ARG;
+  if (static_cast<long long>(d->batch) * d->n_kv_heads * d->max_seq >= (1ll << 31)) return EAGLE_ERR_UNSUPPORTED;
+  return EAGLE_OK;
+}
+
+int check_kvq_desc(const eagle_kvq_desc* d) {
+  if (!d || d->batch < 1 || d->n_kv_heads < 1 || d->max_seq < 1 || d->rows < 1) return EAGLE_ERR_INVALID_ARG;
+  if (d->head_dim != 64 && d->head_dim != 128) return d->head_dim < 1 ? EAGLE_ERR_INVALID_ARG : EAGLE_ERR_UNSUPPORTED;
+  if (!dtype_ok(d->dtype) || static_cast<long long>(d->batch) * d->n_kv_heads > 65535) return EAGLE_ERR_UNSUPPORTED;
+  return EAGLE_OK;
+}
+
+// Pointers of an eagle_kvq_write / eagle_kvq_read call.
+int check_kvq_pointers(const void* k, const void* v, const int32_t* start, const int32_t* count, const void* k8,
+                       const float* ks, const void* v8, const float* vs, const uint32_t* status) {
+  if (!k || !v || !start || !k8 || !ks || !v8 || !vs) return EAGLE_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k8, 16) || !aligned(v8, 16) || !aligned(ks, 4) ||
+      !aligned(vs, 4) || !aligned(start, 4) || (count && !aligned(count, 4)) || (status && !aligned(status, 4)))
+    return EAGLE_ERR_ALIGNMENT;
+  return EAGLE_OK;
+}
+
 }  // namespace
 
 // Records a CUDA error for eagle_last_cuda_error() and returns EAGLE_ERR_CUDA (EAGLE_OK
@@ -154,6 +181,13 @@ size_t eagle_workspace_size(int which, const void* desc) {
       if (check_accept_desc(d) != EAGLE_OK) return 0;
       AcceptPlan p;
       plan_accept(d, &p);
+      return p.total;
+    }
+    case EAGLE_WS_TREE_ATTN_KVQ: {
+      const eagle_attn_desc* d = static_cast<const eagle_attn_desc*>(desc);
+      if (check_kvq_attn_desc(d) != EAGLE_OK) return 0;
+      KvqAttnPlan p;
+      plan_kvq_attn(d, num_sms(), &p);
       return p.total;
     }
     case EAGLE_WS_TTT_ATTN:
@@ -338,6 +372,105 @@ int eagle_lmhead_stats(const eagle_lmhead_desc* d, const void* hidden, const voi
   return cuda_status(launch_lmhead_stats(d->rows, d->hidden, d->vocab, d->tree_rows, d->temperature, hidden, weight,
                                          tree_tokens, tree_parent, records, tree_tokens ? child_logit : nullptr,
                                          status, num_sms(), static_cast<cudaStream_t>(stream)));
+}
+
+int eagle_tree_attn_kvq(const eagle_attn_desc* d, const void* q, const void* k_codes, const float* k_scale,
+                        const void* v_codes, const float* v_scale, const void* tree_k, const void* tree_v,
+                        const int32_t* seq_len, const int32_t* n_nodes, const uint64_t* anc_mask, void* out,
+                        float* lse, void* ws, size_t ws_bytes, void* stream) {
+  const int rc = check_kvq_attn_desc(d);
+  if (rc != EAGLE_OK) return rc;
+  if (!q || !k_codes || !k_scale || !v_codes || !v_scale || !tree_k || !tree_v || !seq_len || !anc_mask || !out)
+    return EAGLE_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(tree_k, 16) ||
+      !aligned(tree_v, 16) || !aligned(out, 16) || !aligned(ws, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4) ||
+      !aligned(seq_len, 4) || !aligned(anc_mask, 8) || (lse && !aligned(lse, 4)) || (n_nodes && !aligned(n_nodes, 4)))
+    return EAGLE_ERR_ALIGNMENT;
+  KvqAttnPlan p;
+  plan_kvq_attn(d, num_sms(), &p);
+  if (!ws || ws_bytes < p.total) return EAGLE_ERR_WORKSPACE;
+  return cuda_status(launch_kvq_attn(p, q, k_codes, k_scale, v_codes, v_scale, tree_k, tree_v, seq_len, n_nodes,
+                                     anc_mask, out, lse, ws, static_cast<cudaStream_t>(stream)));
+}
+
+int eagle_kvq_write(const eagle_kvq_desc* d, const void* k, const void* v, const int32_t* start,
+                    const int32_t* count, void* k_codes, float* k_scale, void* v_codes, float* v_scale,
+                    uint32_t* status, void* stream) {
+  int rc = check_kvq_desc(d);
+  if (rc == EAGLE_OK) rc = check_kvq_pointers(k, v, start, count, k_codes, k_scale, v_codes, v_scale, status);
+  if (rc != EAGLE_OK) return rc;
+  return cuda_status(launch_kvq_write(*d, k, v, start, count, static_cast<uint8_t*>(k_codes), k_scale,
+                                      static_cast<uint8_t*>(v_codes), v_scale, status,
+                                      static_cast<cudaStream_t>(stream)));
+}
+
+int eagle_kvq_read(const eagle_kvq_desc* d, const void* k_codes, const float* k_scale, const void* v_codes,
+                   const float* v_scale, const int32_t* start, const int32_t* count, void* k, void* v,
+                   uint32_t* status, void* stream) {
+  int rc = check_kvq_desc(d);
+  if (rc == EAGLE_OK) rc = check_kvq_pointers(k, v, start, count, k_codes, k_scale, v_codes, v_scale, status);
+  if (rc != EAGLE_OK) return rc;
+  return cuda_status(launch_kvq_read(*d, static_cast<const uint8_t*>(k_codes), k_scale,
+                                     static_cast<const uint8_t*>(v_codes), v_scale, start, count, k, v, status,
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+int eagle_kvq_commit(const eagle_commit_desc* d, void* const* k_codes_layers, float* const* k_scale_layers,
+                     void* const* v_codes_layers, float* const* v_scale_layers, const void* const* tree_k_layers,
+                     const void* const* tree_v_layers, const int32_t* n_acc, const int32_t* path, int32_t* seq_len,
+                     int32_t* commit_pos, void* feat_cache, const void* tree_feat, uint32_t* status, void* stream) {
+  if (!d || d->layers < 1 || d->batch < 1 || d->n_kv_heads < 1 || d->head_dim < 1 || d->rows < 1 || d->max_seq < 1 ||
+      d->max_depth < 0 || d->feat_dim < 0)
+    return EAGLE_ERR_INVALID_ARG;
+  if (d->layers > kMaxLayers || d->rows > kMaxRows || d->max_depth >= kMaxRows || !dtype_ok(d->dtype) ||
+      (d->feat_dim > 0 && !dtype_ok(d->feat_dtype)) || (d->head_dim != 64 && d->head_dim != 128) ||
+      d->batch > 65535 || d->n_kv_heads > 65535)
+    return EAGLE_ERR_UNSUPPORTED;
+  if (!k_codes_layers || !k_scale_layers || !v_codes_layers || !v_scale_layers || !tree_k_layers || !tree_v_layers ||
+      !n_acc || !path || !seq_len)
+    return EAGLE_ERR_INVALID_ARG;
+  if (d->feat_dim > 0 && (!feat_cache || !tree_feat)) return EAGLE_ERR_INVALID_ARG;
+  KvqCommitArgs a;
+  memset(&a, 0, sizeof a);
+  for (int l = 0; l < d->layers; ++l) {
+    a.k8[l] = k_codes_layers[l];
+    a.ks[l] = k_scale_layers[l];
+    a.v8[l] = v_codes_layers[l];
+    a.vs[l] = v_scale_layers[l];
+    a.tree_k[l] = tree_k_layers[l];
+    a.tree_v[l] = tree_v_layers[l];
+    if (!a.k8[l] || !a.ks[l] || !a.v8[l] || !a.vs[l] || !a.tree_k[l] || !a.tree_v[l]) return EAGLE_ERR_INVALID_ARG;
+    if (!aligned(a.k8[l], 16) || !aligned(a.v8[l], 16) || !aligned(a.tree_k[l], 16) || !aligned(a.tree_v[l], 16) ||
+        !aligned(a.ks[l], 4) || !aligned(a.vs[l], 4))
+      return EAGLE_ERR_ALIGNMENT;
+  }
+  if (d->feat_dim > 0) {
+    const size_t rb = static_cast<size_t>(d->feat_dim) * (d->feat_dtype == EAGLE_F32 ? 4 : 2);
+    if (rb % 16 == 0 && (!aligned(feat_cache, 16) || !aligned(tree_feat, 16))) return EAGLE_ERR_ALIGNMENT;
+  }
+  return cuda_status(launch_kvq_commit(*d, a, n_acc, path, seq_len, commit_pos, feat_cache, tree_feat, status,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+int eagle_qk_norm_rope(const eagle_qk_norm_rope_desc* d, const void* qkv, const void* q_weight,
+                       const void* k_weight, const float* inv_freq, const int32_t* pos_id, const int32_t* n_nodes,
+                       void* q, void* k, void* v, void* stream) {
+  if (!d || d->batch < 1 || d->rows < 1 || d->n_q_heads < 1 || d->n_kv_heads < 1 || d->head_dim < 1 ||
+      d->rot_dim < 0 || d->row_stride < 0 || !(d->eps >= 0.f) || !isfinite(d->eps) ||
+      (d->interleaved != 0 && d->interleaved != 1))
+    return EAGLE_ERR_INVALID_ARG;
+  if ((d->head_dim != 64 && d->head_dim != 128) || d->rot_dim % 16 || !dtype_ok(d->dtype) || d->batch > 65535)
+    return EAGLE_ERR_UNSUPPORTED;
+  const long long width = (static_cast<long long>(d->n_q_heads) + 2ll * d->n_kv_heads) * d->head_dim;
+  if (width > (1ll << 30)) return EAGLE_ERR_UNSUPPORTED;
+  if (d->rot_dim > d->head_dim || (d->row_stride > 0 && d->row_stride < width)) return EAGLE_ERR_INVALID_ARG;
+  if (d->row_stride % 8) return EAGLE_ERR_ALIGNMENT;
+  if (!qkv || !inv_freq || !pos_id || !q || !k || !v) return EAGLE_ERR_INVALID_ARG;
+  if (!aligned(qkv, 16) || !aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(q, 16) || !aligned(k, 16) ||
+      !aligned(v, 16) || !aligned(inv_freq, 4) || !aligned(pos_id, 4) || (n_nodes && !aligned(n_nodes, 4)))
+    return EAGLE_ERR_ALIGNMENT;
+  return cuda_status(launch_qk_norm_rope(*d, qkv, q_weight, k_weight, inv_freq, pos_id, n_nodes, q, k, v,
+                                         static_cast<cudaStream_t>(stream)));
 }
 
 int eagle_selftest_ff_log(const float* z_hi, const float* z_lo, float* out_hi, float* out_lo, int32_t n,

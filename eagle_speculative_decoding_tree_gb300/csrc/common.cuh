@@ -134,6 +134,13 @@ __device__ __forceinline__ ff warp_sum_ff(ff v) {
 // A compensated fp32 sum as a float-float value.
 __device__ __forceinline__ ff csum_ff(const CSum& a) { return two_sum(a.s, a.c); }
 
+// Whether request b's accepted path (root + n_acc drafts) fits behind its seq_len rows.
+__device__ __forceinline__ bool commit_fits(const eagle_commit_desc& d, const int32_t* n_acc, const int32_t* seq_len,
+                                            int b) {
+  const int na = n_acc[b], L = seq_len[b];
+  return na >= 0 && na <= d.max_depth && L >= 0 && L <= d.max_seq - 1 - na;
+}
+
 // (value desc, index asc) order: true if (va, ia) comes before (vb, ib).
 __device__ __forceinline__ bool before(float va, int ia, float vb, int ib) {
   return va > vb || (va == vb && ia < ib);

@@ -20,19 +20,12 @@
 namespace eagle {
 namespace {
 
-__device__ __forceinline__ bool commit_ok(const eagle_commit_desc& d, const int32_t* n_acc, const int32_t* seq_len,
-                                          int b) {
-  const int na = n_acc[b];
-  const int L = seq_len[b];
-  return na >= 0 && na <= d.max_depth && L >= 0 && L + na + 1 <= d.max_seq;
-}
-
 __global__ void __launch_bounds__(128) kv_commit_copy_kernel(const eagle_commit_desc d, const CommitArgs a,
                                                              const int32_t* n_acc, const int32_t* path,
                                                              const int32_t* seq_len, void* feat_cache,
                                                              const void* tree_feat) {
   const int b = blockIdx.x, m = blockIdx.y, l = blockIdx.z;
-  if (!commit_ok(d, n_acc, seq_len, b) || m > n_acc[b]) return;
+  if (!commit_fits(d, n_acc, seq_len, b) || m > n_acc[b]) return;
   const int node = path[static_cast<size_t>(b) * (d.max_depth + 1) + m];
   if (node < 0 || node >= d.rows) return;  // flagged by the finalize kernel
   const int dst_row = seq_len[b] + m;
@@ -67,12 +60,13 @@ __global__ void __launch_bounds__(128) kv_commit_copy_kernel(const eagle_commit_
 __global__ void kv_commit_finalize_kernel(const eagle_commit_desc d, const int32_t* n_acc, const int32_t* path,
                                           int32_t* seq_len, int32_t* commit_pos, uint32_t* status) {
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the copies have read the old seq_len
   if (b >= d.batch) return;
   const int maxp = d.max_depth + 1;
   const int na = n_acc[b];
   const int L = seq_len[b];
   unsigned st = 0;
-  const bool ok = commit_ok(d, n_acc, seq_len, b);
+  const bool ok = commit_fits(d, n_acc, seq_len, b);
   if (!ok) st |= EAGLE_STATUS_CACHE_FULL;
   for (int m = 0; m < maxp; ++m) {
     const bool on = ok && m <= na;
@@ -97,6 +91,21 @@ cudaError_t launch_kv_commit(const eagle_commit_desc* d, const CommitArgs& a, co
   if (e != cudaSuccess) return e;
   kv_commit_finalize_kernel<<<(d->batch + 127) / 128, 128, 0, s>>>(*d, n_acc, path, seq_len, commit_pos, status);
   return cudaGetLastError();
+}
+
+cudaError_t launch_commit_finalize(const eagle_commit_desc& d, const int32_t* n_acc, const int32_t* path,
+                                   int32_t* seq_len, int32_t* commit_pos, uint32_t* status, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((d.batch + 127) / 128, 1, 1);
+  cfg.blockDim = dim3(128, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_commit_finalize_kernel, d, n_acc, path, seq_len, commit_pos, status);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace eagle

@@ -1,0 +1,60 @@
+// kvq.cuh -- the 8-bit KV cache format shared by its kernels.
+//
+// A cache row holds e4m3 codes; the EAGLE_KVQ_BLOCK rows of an aligned block share one
+// fp32 scale for each head, value = code * scale.  The writers choose the scale as the
+// smallest power of two s with amax <= 448 s: dividing by it is exact, so a stored value
+// is the nearest e4m3 value and nothing else is rounded, and a scale that grows later
+// moves the codes already stored without rounding them again (below the new scale's
+// normal range they lose the bits that e4m3's subnormals do not have).
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace eagle {
+
+constexpr int kQB = EAGLE_KVQ_BLOCK;
+
+// Smallest power of two s >= 2^-126 with amax <= 448 s; 0 for amax == 0.  448 = 1.75 * 2^8:
+// with amax = f 2^x, 1 <= f < 2, s = 2^(x - 8) if f <= 1.75, else 2^(x - 7).
+__device__ __forceinline__ float kvq_scale(float amax) {
+  if (!(amax > 0.f)) return 0.f;
+  const uint32_t u = __float_as_uint(amax);
+  const int x = static_cast<int>(u >> 23) - ((u & 0x7fffffu) <= 0x600000u ? 8 : 7);  // biased exponent of s
+  return __uint_as_float(static_cast<uint32_t>(x < 1 ? 1 : x) << 23);
+}
+
+// 1 / s for a power-of-two scale (1 for the scale of a block of zeros).
+__device__ __forceinline__ float kvq_inverse(float s) { return s > 0.f ? 1.f / s : 1.f; }
+
+// Two floats to e4m3 codes, nearest even, `lo` in the low byte.  A value that is not finite
+// becomes the NaN code: it must not read back as an ordinary number.
+__device__ __forceinline__ uint32_t kvq_code2(float lo, float hi) {
+  const float nan = __uint_as_float(0x7fffffffu);
+  lo = fabsf(lo) <= 3.402823466e38f ? lo : nan;
+  hi = fabsf(hi) <= 3.402823466e38f ? hi : nan;
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Two e4m3 codes (the low 16 bits of w) as packed halves; exact.
+__device__ __forceinline__ uint32_t kvq_half2(uint32_t w) {
+  uint32_t r;
+  asm("{\n .reg .b16 t;\n cvt.u16.u32 t, %1;\n cvt.rn.f16x2.e4m3x2 %0, t;\n}\n" : "=r"(r) : "r"(w));
+  return r;
+}
+
+__device__ __forceinline__ float2 kvq_float2(uint32_t w) {
+  const uint32_t h = kvq_half2(w);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// Four codes of one scale to the codes of a larger one: ratio = old scale / new scale.
+__device__ __forceinline__ uint32_t kvq_move4(uint32_t w, float ratio) {
+  const float2 a = kvq_float2(w), b = kvq_float2(w >> 16);
+  return kvq_code2(a.x * ratio, a.y * ratio) | (kvq_code2(b.x * ratio, b.y * ratio) << 16);
+}
+
+}  // namespace eagle

@@ -138,5 +138,68 @@ struct CommitArgs {
 cudaError_t launch_kv_commit(const eagle_commit_desc* d, const CommitArgs& a, const int32_t* n_acc,
                              const int32_t* path, int32_t* seq_len, int32_t* commit_pos, void* feat_cache,
                              const void* tree_feat, uint32_t* status, cudaStream_t s);
+// The second half of a commit (commit_pos, seq_len, status) behind another copy kernel, as a
+// programmatic launch.
+cudaError_t launch_commit_finalize(const eagle_commit_desc& d, const int32_t* n_acc, const int32_t* path,
+                                   int32_t* seq_len, int32_t* commit_pos, uint32_t* status, cudaStream_t s);
+
+// ------------------------------------------------------------------ 8-bit KV cache
+struct KvqCommitArgs {
+  void* k8[kMaxLayers];
+  float* ks[kMaxLayers];
+  void* v8[kMaxLayers];
+  float* vs[kMaxLayers];
+  const void* tree_k[kMaxLayers];
+  const void* tree_v[kMaxLayers];
+};
+cudaError_t launch_kvq_write(const eagle_kvq_desc& d, const void* k, const void* v, const int32_t* start,
+                             const int32_t* count, uint8_t* k8, float* ks, uint8_t* v8, float* vs, uint32_t* status,
+                             cudaStream_t s);
+cudaError_t launch_kvq_read(const eagle_kvq_desc& d, const uint8_t* k8, const float* ks, const uint8_t* v8,
+                            const float* vs, const int32_t* start, const int32_t* count, void* k, void* v,
+                            uint32_t* status, cudaStream_t s);
+cudaError_t launch_kvq_commit(const eagle_commit_desc& d, const KvqCommitArgs& a, const int32_t* n_acc,
+                              const int32_t* path, int32_t* seq_len, int32_t* commit_pos, void* feat_cache,
+                              const void* tree_feat, uint32_t* status, cudaStream_t s);
+
+// Tree attention over the 8-bit cache (see eagle.h: eagle_tree_attn_kvq).
+struct KvqAttnPlan {
+  int B, R, Hq, Hkv, G, D, P, W, out_f32;
+  bool terms2;      // P as two half terms (EAGLE_ATTN_PRECISE)
+  float scale;
+  int mt, wr;       // 16-row tiles per warp, warps along the rows (8 / wr split a tile's keys)
+  int rows_per_cta, row_blocks, rows_pad;
+  int splits, tps;  // split s takes 128-key units [s tps, (s + 1) tps) of its request
+  size_t off_err, off_o, off_ml, total;
+};
+void plan_kvq_attn(const eagle_attn_desc* d, int num_sms, KvqAttnPlan* p);
+struct KvqAttnArgs {
+  const uint16_t* q;
+  const uint8_t* k8;
+  const float* ks;
+  const uint8_t* v8;
+  const float* vs;
+  const uint16_t* tk;
+  const uint16_t* tv;
+  const int32_t* seq_len;
+  const int32_t* n_nodes;  // [B] tree rows per request (NULL: all R)
+  const uint64_t* anc_mask;
+  void* out;
+  float* lse;
+  float* part_o;   // [B*Hkv][splits][rows_pad][D]
+  float* part_ml;  // [B*Hkv][splits][rows_pad][2]: max in log2 units, sum
+  int* err;
+  int B, R, Hq, Hkv, G, P, W, splits, tps, rows_pad, out_f32, wr;
+  float scale, scale_log2;
+};
+cudaError_t launch_kvq_attn(const KvqAttnPlan& p, const void* q, const void* k8, const float* ks, const void* v8,
+                            const float* vs, const void* tree_k, const void* tree_v, const int32_t* seq_len,
+                            const int32_t* n_nodes, const uint64_t* anc_mask, void* out, float* lse, void* ws,
+                            cudaStream_t s);
+
+// ------------------------------------------------------------------ norms and rotation
+cudaError_t launch_qk_norm_rope(const eagle_qk_norm_rope_desc& d, const void* qkv, const void* wq, const void* wk,
+                                const float* inv_freq, const int32_t* pos_id, const int32_t* n_nodes, void* q,
+                                void* k, void* v, cudaStream_t s);
 
 }  // namespace eagle

@@ -1,0 +1,730 @@
+// tree_attn_kvq.cu -- tree attention over the 8-bit KV cache.
+//
+// The operation of tree_attn.cu (EAGLE review, terms "tree attention"; lesson glossary "Tree
+// attention") with the prefix keys and values held as e4m3 codes with one scale per 64 rows:
+//     s = scale q (code ks)        prefix key        s = scale q k        tree key (bf16)
+//     out = sum 2^(s log2e - m) (code vs or v) / sum 2^(s log2e - m)
+//
+// How the 8-bit operands meet the tensor cores.  A code is exact as a half, so the prefix
+// products run in half precision inputs with fp32 accumulators and the scales stay outside:
+//   - a query row is multiplied by a power of two that puts its largest element in
+//     [2^14, 2^15): bf16 to half is then exact down to 2^-39 of that element;
+//   - ks multiplies the scores of its block (fp32);
+//   - vs / vref, vref the largest vs of the CTA's key range, goes into the exponent of P, so
+//     one accumulator serves blocks of different scales; the row sum takes it out again.
+//     P <= 2^15 in half: 11 significant bits down to 2^-25 of the largest p, steps of 2^-35
+//     of it below.
+// The reference maximum is kept in log2 units and rounded up to an integer, so that with
+// power-of-two scales every exponent offset is exact.
+//
+// Kernel (the split-KV shape of tree_attn.cu).  One CTA per (row block, split, request x KV
+// head): 128-key tiles of codes stream through a TMA ring (128-byte swizzle; 64-byte for
+// head_dim 64; one thread refills a stage once every warp is past it), eight warps take 16-key steps: codes go from shared memory to
+// registers once and become mma.sync m16n8k16 half fragments there, which is cheaper than
+// writing a half tile back for few rows (they are the bytes-bound case: R G <= 32 rows of one
+// decode or chain step).  The fragments' orders are free choices: a thread's 16 bytes of a key
+// are 16 head dims of the contraction, Q is stored to match; keys within a step are permuted
+// by exchanging bits 0 and 2 so that the swizzled reads fall in different banks.
+// Rows: wr warps side by side along the rows, 8 / wr along a tile's keys; their states merge
+// in shared memory at the end, splits in kvq_combine_kernel.
+#include <algorithm>
+
+#include "common.cuh"
+#include "kvq.cuh"
+#include "launch.h"
+#include "sm100.cuh"
+#include "tmap.h"
+
+namespace eagle {
+namespace {
+
+using namespace sm100;
+
+constexpr int KT = 128;       // keys per tile
+constexpr int NST = 4;        // ring stages
+constexpr int CW = 8;         // compute warps
+// A row's reference moves when its maximum grew by more than 2^kLazy, and P is stored as
+// p 2^PB <= 2^15: a half's smallest step then is 2^-35 of the largest p.  A larger kLazy saves
+// rescales, which are rare already at 2^4, and costs that range.
+constexpr float kLazy = 4.f;
+constexpr int PB = 11;
+
+enum : int { ERR_FULL = 1, ERR_EMPTY = 2 };
+
+struct Maps {
+  CUtensorMap k, v;
+};
+
+__device__ __forceinline__ int prefix_len(const KvqAttnArgs& a, int b) {
+  const int L = a.seq_len[b];
+  return L < 0 ? 0 : (L > a.P ? a.P : L);
+}
+__device__ __forceinline__ int tree_rows(const KvqAttnArgs& a, int b) {
+  if (!a.n_nodes) return a.R;
+  const int n = a.n_nodes[b];
+  return n < 0 ? 0 : (n > a.R ? a.R : n);
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_half(uint32_t w) { return __half22float2(*reinterpret_cast<__half2*>(&w)); }
+__device__ __forceinline__ uint32_t pack_bf(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// One warp's rows: MT tiles of 16 (thread rows g and g + 8 of each), running state.
+template <int D, int MT>
+struct RowState {
+  float o[MT][D / 8][4];
+  float m[MT][2], l[MT][2];
+};
+
+// Scores t (log2 units, masked -inf) of 16 keys x MT tiles: moves the reference maxima if
+// they must, turns t into p 2^lr (in place) and adds the row sums.
+template <int D, int MT>
+__device__ __forceinline__ void soften(RowState<D, MT>& st, float (&t)[MT][2][4], float lr) {
+  const float back = ex2(-lr);
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    float m_new[2];
+    bool move = false;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float mx = fmaxf(fmaxf(t[mt][0][2 * i], t[mt][0][2 * i + 1]), fmaxf(t[mt][1][2 * i], t[mt][1][2 * i + 1]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const bool up = mx > st.m[mt][i] + kLazy || (st.m[mt][i] == -INFINITY && mx > -INFINITY);
+      m_new[i] = up ? ceilf(mx) : st.m[mt][i];
+      move |= up;
+    }
+    if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float al = st.m[mt][i] == -INFINITY ? 0.f : ex2(st.m[mt][i] - m_new[i]);
+        st.m[mt][i] = m_new[i];
+        st.l[mt][i] *= al;
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) {
+          st.o[mt][j][2 * i] *= al;
+          st.o[mt][j][2 * i + 1] *= al;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float off = lr - (st.m[mt][i] == -INFINITY ? 0.f : st.m[mt][i]);
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 2 * i; e < 2 * i + 2; ++e) {
+          t[mt][j][e] = ex2(t[mt][j][e] + off);
+          sum += t[mt][j][e];
+        }
+      st.l[mt][i] = fmaf(sum, back, st.l[mt][i]);
+    }
+  }
+}
+
+template <int D>
+__host__ __device__ constexpr int q_stride() { return D * 2 + 8; }  // bytes; 2 words past a bank row per row
+
+template <int D, int MT, bool TERMS2>
+__global__ void __launch_bounds__(CW * 32, 1)
+    tree_attn_kvq_kernel(const __grid_constant__ Maps tm, const KvqAttnArgs a) {
+  constexpr int TILE = KT * D;  // bytes of one K or V tile
+  constexpr int CH = D / 16;    // 16-byte chunks of a row of codes
+  constexpr int KS = D / 16;    // k-steps of QK^T
+  constexpr int VB = D / 8;     // head dims of a thread's V column
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sq = ring + NST * 2 * TILE;
+  __shared__ uint64_t full[NST], empty[NST];
+  __shared__ float s_qs[CW * 32], s_m[CW][32], s_l[CW][32], s_vr[CW];
+
+  const int rb = blockIdx.x, split = blockIdx.y, bh = blockIdx.z;
+  const int b = bh / a.Hkv, h = bh % a.Hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, c = lane & 3;
+  const int wr = a.wr, wk = CW / wr, rows_cta = wr * MT * 16;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], CW);
+    }
+    fence_barrier_init();
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  const int L = prefix_len(a, b), Rb = tree_rows(a, b);
+  const int RG = Rb * a.G;
+  const int n_pref = (L + KT - 1) / KT;
+  const int u0 = split * a.tps, u1 = min(n_pref + 1, u0 + a.tps);
+  const int n_pt = max(0, min(u1, n_pref) - u0);
+  const bool tree = u0 <= n_pref && u1 == n_pref + 1;
+  if (u0 > n_pref || rb * rows_cta >= RG) return;  // nothing of this request here (the combine skips it)
+  const int blk0 = u0 * (KT / kQB);
+  const int n_blk = n_pt > 0 ? (min(L, (u0 + n_pt) * KT) + kQB - 1) / kQB - blk0 : 0;
+  const int nblk_all = (a.P + kQB - 1) / kQB;
+  const float* ks = a.ks + static_cast<size_t>(bh) * nblk_all + blk0;
+  const float* vs = a.vs + static_cast<size_t>(bh) * nblk_all + blk0;
+  __syncthreads();  // barriers initialised
+
+  const uint64_t policy = policy_evict_first();
+  auto load_tile = [&](int t) {
+    const int s = t % NST, y = bh * a.P + (u0 + t) * KT;
+    mbar_arrive_expect_tx(&full[s], 2 * TILE);
+    tma_load_2d_hint(ring + s * 2 * TILE, &tm.k, 0, y, &full[s], policy);
+    tma_load_2d_hint(ring + s * 2 * TILE + TILE, &tm.v, 0, y, &full[s], policy);
+  };
+  int issued = 0;  // thread 0: tiles whose loads have gone out; the first before anything else is read
+  if (threadIdx.x == 0)
+    for (; issued < min(n_pt, NST); ++issued) load_tile(issued);
+  // vref: the largest V scale of the key range
+  float vm = 0.f;
+  for (int i = threadIdx.x; i < n_blk; i += CW * 32) vm = fmaxf(vm, __ldg(vs + i));
+  vm = warp_max(vm);
+  if (lane == 0) s_vr[warp] = vm;
+
+  // Q rows as scaled halves: row r, element e at r * stride + 2 e
+  for (int r = warp; r < rows_cta; r += CW) {
+    const int row = rb * rows_cta + r;
+    float f[D / 32];
+    float am = 0.f;
+    if (row < RG) {
+      const uint16_t* src =
+          a.q + ((static_cast<size_t>(b) * a.R + row / a.G) * a.Hq + h * a.G + row % a.G) * D + lane * (D / 32);
+#pragma unroll
+      for (int e = 0; e < D / 32; e += 2) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(src + e);
+        f[e] = __uint_as_float(w << 16);
+        f[e + 1] = __uint_as_float(w & 0xffff0000u);
+      }
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) am = fmaxf(am, fabsf(f[e]) <= 3.402823466e38f ? fabsf(f[e]) : 0.f);
+    } else {
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) f[e] = 0.f;
+    }
+    am = warp_max(am);
+    // am = f 2^x: multiply by 2^(14 - x); x at least -100 keeps both powers normal
+    const int x = am > 0.f ? max(static_cast<int>(__float_as_uint(am) >> 23) - 127, -100) : 14;
+    const float mul = __uint_as_float(static_cast<uint32_t>(127 + 14 - x) << 23);
+#pragma unroll
+    for (int e = 0; e < D / 32; e += 2)
+      *reinterpret_cast<uint32_t*>(sq + r * q_stride<D>() + (lane * (D / 32) + e) * 2) =
+          pack_half(f[e] * mul, f[e + 1] * mul);
+    if (lane == 0) s_qs[r] = __uint_as_float(static_cast<uint32_t>(127 + x - 14) << 23);
+  }
+  __syncthreads();
+  float vref = s_vr[0];
+#pragma unroll
+  for (int w = 1; w < CW; ++w) vref = fmaxf(vref, s_vr[w]);
+  if (!(vref > 0.f)) vref = 1.f;
+  const float vinv = 1.f / vref;
+
+  bool ok = true;
+  const int wrow = warp % wr, wkey = warp / wr;
+  const int r0 = wrow * MT * 16;  // first row of the warp within the CTA
+  RowState<D, MT> st;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j) st.o[mt][j][0] = st.o[mt][j][1] = st.o[mt][j][2] = st.o[mt][j][3] = 0.f;
+    st.m[mt][0] = st.m[mt][1] = -INFINITY;
+    st.l[mt][0] = st.l[mt][1] = 0.f;
+  }
+  float cr[MT][2];  // row factors of the scores
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) cr[mt][i] = a.scale_log2 * s_qs[r0 + mt * 16 + g + 8 * i];
+
+  // ---- prefix: 16-key steps wkey, wkey + wk, ... of every tile
+  const int gs = (g & 2) | ((g & 1) << 2) | (g >> 2);      // key of column g within 8: bits 0 and 2 exchanged
+  const int cs = ((2 * c) & 2) | ((2 * c) >> 2);           // key of column 2 c; column 2 c + 1 is cs + 4
+  const int swz = D == 128 ? gs : (gs >> 1) & 3;           // chunk swizzle of key gs (and gs + 8)
+  const uint32_t qrow = smem_u32(sq) + static_cast<uint32_t>((r0 + g) * q_stride<D>() + 32 * c);
+  float ks_n = 0.f, vs_n = 0.f;
+  {
+    const int kb = min(wkey * 16 / kQB, n_blk - 1);
+    if (n_pt > 0) ks_n = __ldg(ks + kb), vs_n = __ldg(vs + kb);
+  }
+  for (int t = 0; t < n_pt && ok; ++t) {
+    const int s = t % NST;
+    ok = __all_sync(0xffffffffu, wait_parity(&full[s], (t / NST) & 1, a.err, ERR_FULL));
+    if (!ok) break;
+    const int nv = min(KT, L - (u0 + t) * KT);
+    const uint8_t* tk = ring + s * 2 * TILE;
+    const uint8_t* tv = tk + TILE;
+    for (int step = wkey; step < KT / 16; step += wk) {
+      const float ksb = ks_n, vsb = vs_n;
+      {  // the next step's scales
+        const int nx = step + wk < KT / 16 ? t * KT + (step + wk) * 16 : (t + 1) * KT + wkey * 16;
+        const int kb = min(nx / kQB, n_blk - 1);
+        ks_n = __ldg(ks + kb);
+        vs_n = __ldg(vs + kb);
+      }
+      const int nk = nv - step * 16;  // valid keys of the step
+      if (nk <= 0) continue;
+      float sc[MT][2][4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint8_t* kr = tk + (step * 16 + 8 * j + gs) * D;
+        uint32_t w[KS];
+#pragma unroll
+        for (int i = 0; i < CH / 4; ++i) {
+          const uint4 u = *reinterpret_cast<const uint4*>(kr + (((c + 4 * i) ^ swz) << 4));
+          w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) sc[mt][j][0] = sc[mt][j][1] = sc[mt][j][2] = sc[mt][j][3] = 0.f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const uint32_t b0 = kvq_half2(w[k]), b1 = kvq_half2(w[k] >> 16);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            uint32_t qa[4];
+            const uint32_t at = qrow + mt * 16 * q_stride<D>() + (k >> 2) * 128 + (k & 3) * 8;
+            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(qa[0]), "=r"(qa[2]) : "r"(at));
+            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(qa[1]), "=r"(qa[3]) : "r"(at + 8 * q_stride<D>()));
+            mma_f16(sc[mt][j], qa, b0, b1);
+          }
+        }
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            sc[mt][j][e] *= cr[mt][e >> 1] * ksb;
+            if (nk < 16 && 8 * j + cs + 4 * (e & 1) >= nk) sc[mt][j][e] = -INFINITY;
+          }
+      const float lr = fmaxf(__log2f(vsb * vinv), -100.f) + PB;
+      soften<D, MT>(st, sc, lr);
+      uint32_t pa[MT][4], pl[MT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float x0 = sc[mt][k >> 1][2 * (k & 1)], x1 = sc[mt][k >> 1][2 * (k & 1) + 1];
+          pa[mt][k] = pack_half(x0, x1);
+          if (TERMS2) {
+            const float2 hi = unpack_half(pa[mt][k]);
+            pl[mt][k] = pack_half(x0 - hi.x, x1 - hi.y);
+          }
+        }
+      // V: this thread's column g is head dims VB g .. VB g + VB - 1; its keys are columns
+      // 2 c, 2 c + 1 of both 8-key halves
+      uint32_t vw[4][VB / 4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int kk = (i >> 1) * 8 + cs + 4 * (i & 1);
+        const int sw = D == 128 ? kk & 7 : (kk >> 1) & 3;
+        const uint8_t* vr = tv + (step * 16 + kk) * D;
+        if (D == 128) {
+          const uint4 u = *reinterpret_cast<const uint4*>(vr + ((g ^ sw) << 4));
+          vw[i][0] = u.x, vw[i][1] = u.y, vw[i][VB / 4 - 2] = u.z, vw[i][VB / 4 - 1] = u.w;
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2*>(vr + (((g >> 1) ^ sw) << 4) + (g & 1) * 8);
+          vw[i][0] = u.x, vw[i][1] = u.y;
+        }
+        if (nk < 16 && kk >= nk) {
+#pragma unroll
+          for (int q = 0; q < VB / 4; ++q) vw[i][q] = 0u;
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < VB / 4; ++q) {
+        uint32_t e[2][2];  // [key half][bytes 0 1 / 2 3 of word q], as (key, key + 1) pairs
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          e[hf][0] = __byte_perm(vw[2 * hf][q], vw[2 * hf + 1][q], 0x5140);
+          e[hf][1] = __byte_perm(vw[2 * hf][q], vw[2 * hf + 1][q], 0x7362);
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const uint32_t b0 = kvq_half2(e[0][y >> 1] >> (16 * (y & 1)));
+          const uint32_t b1 = kvq_half2(e[1][y >> 1] >> (16 * (y & 1)));
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            mma_f16(st.o[mt][4 * q + y], pa[mt], b0, b1);
+            if (TERMS2) mma_f16(st.o[mt][4 * q + y], pl[mt], b0, b1);
+          }
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[s]);
+    // refill the stage of the tile before this one: the other warps are past it by now
+    if (threadIdx.x == 0 && t > 0 && issued < n_pt) {
+      if (wait_parity(&empty[(t - 1) % NST], ((t - 1) / NST) & 1, a.err, ERR_EMPTY))
+        load_tile(issued++);
+      else
+        ok = false;
+    }
+    ok = __all_sync(0xffffffffu, ok);
+  }
+  // no copy may still be landing when the ring is used for the merge or the CTA ends
+  if (threadIdx.x == 0)
+    for (int s = 0; s < NST && s < issued; ++s)
+      (void)wait_parity(&full[s], ((issued - 1 - s) / NST) & 1, a.err, ERR_FULL);
+
+  // ---- the tree's own K/V (bf16, straight from global memory): 16-key steps shared out in
+  // the same way; P always as two bf16 terms
+  if (tree && ok) {
+    const uint16_t* kb = a.tk + static_cast<size_t>(bh) * a.R * D;
+    const uint16_t* vb = a.tv + static_cast<size_t>(bh) * a.R * D;
+    const uint16_t* qp[MT][2];
+    const uint64_t* mp[MT][2];
+    bool live[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = rb * rows_cta + r0 + mt * 16 + g + 8 * i;
+        live[mt][i] = row < RG;
+        const int node = live[mt][i] ? row / a.G : 0, hq = h * a.G + (live[mt][i] ? row % a.G : 0);
+        qp[mt][i] = a.q + ((static_cast<size_t>(b) * a.R + node) * a.Hq + hq) * D + 16 * c;
+        mp[mt][i] = a.anc_mask + (static_cast<size_t>(b) * a.R + node) * a.W;
+      }
+    const float lr = PB - __log2f(vref);
+    for (int step = wkey; step * 16 < Rb; step += wk) {
+      float sc[MT][2][4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int key = step * 16 + 8 * j + g;
+        const uint16_t* kr = kb + static_cast<size_t>(min(key, Rb - 1)) * D + 16 * c;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) sc[mt][j][0] = sc[mt][j][1] = sc[mt][j][2] = sc[mt][j][3] = 0.f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const uint2 kw = *reinterpret_cast<const uint2*>(kr + (k >> 2) * 64 + (k & 3) * 4);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const uint2 q0 = *reinterpret_cast<const uint2*>(qp[mt][0] + (k >> 2) * 64 + (k & 3) * 4);
+            const uint2 q1 = *reinterpret_cast<const uint2*>(qp[mt][1] + (k >> 2) * 64 + (k & 3) * 4);
+            const uint32_t qa[4] = {q0.x, q1.x, q0.y, q1.y};
+            mma_bf16(sc[mt][j], qa, kw.x, kw.y);
+          }
+        }
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int k0 = step * 16;
+          const uint64_t word = live[mt][i] ? mp[mt][i][k0 >> 6] : 0ull;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int key = k0 + 8 * j + 2 * c + e;
+              const bool on = key < Rb && ((word >> (key & 63)) & 1ull);
+              sc[mt][j][2 * i + e] = on ? sc[mt][j][2 * i + e] * a.scale_log2 : -INFINITY;
+            }
+        }
+      soften<D, MT>(st, sc, lr);
+      uint32_t pa[MT][4], pl[MT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float x0 = sc[mt][k >> 1][2 * (k & 1)], x1 = sc[mt][k >> 1][2 * (k & 1) + 1];
+          pa[mt][k] = pack_bf(x0, x1);
+          pl[mt][k] = pack_bf(x0 - __uint_as_float(pa[mt][k] << 16), x1 - __uint_as_float(pa[mt][k] & 0xffff0000u));
+        }
+#pragma unroll
+      for (int q = 0; q < VB / 4; ++q) {  // 4 head dims at a time
+        uint2 w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = step * 16 + (i >> 1) * 8 + 2 * c + (i & 1);
+          w[i] = key < Rb ? *reinterpret_cast<const uint2*>(vb + static_cast<size_t>(key) * D + VB * g + 4 * q)
+                          : make_uint2(0u, 0u);
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const uint32_t sel = (y & 1) ? 0x7632 : 0x5410;
+          const uint32_t b0 = __byte_perm(y < 2 ? w[0].x : w[0].y, y < 2 ? w[1].x : w[1].y, sel);
+          const uint32_t b1 = __byte_perm(y < 2 ? w[2].x : w[2].y, y < 2 ? w[3].x : w[3].y, sel);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            mma_bf16(st.o[mt][4 * q + y], pa[mt], b0, b1);
+            mma_bf16(st.o[mt][4 * q + y], pl[mt], b0, b1);
+          }
+        }
+      }
+    }
+  }
+
+  // ---- merge the key warps of the CTA: the row's states meet in shared memory
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      st.l[mt][i] += __shfl_xor_sync(0xffffffffu, st.l[mt][i], 1);
+      st.l[mt][i] += __shfl_xor_sync(0xffffffffu, st.l[mt][i], 2);
+      if (c == 0) {
+        s_m[warp][mt * 16 + g + 8 * i] = st.m[mt][i];
+        s_l[warp][mt * 16 + g + 8 * i] = st.l[mt][i];
+      }
+    }
+  __syncthreads();  // the ring is free
+  float* so = reinterpret_cast<float*>(ring) + static_cast<size_t>(warp) * (MT * 16 * D);
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int j = 0; j < VB; j += 4)  // chunk index XORed with the row: the quads' rows fall in different banks
+          *reinterpret_cast<float4*>(so + (mt * 16 + g + 8 * i) * D +
+                                     ((((VB * (2 * c + e) + j) >> 2) ^ g) << 2)) =
+              make_float4(st.o[mt][j][2 * i + e], st.o[mt][j + 1][2 * i + e], st.o[mt][j + 2][2 * i + e],
+                          st.o[mt][j + 3][2 * i + e]);
+  __syncthreads();
+  const float unit = vref * (1.f / (1 << PB));
+  constexpr int QD = D / 4;  // threads of a row, 4 dims each
+  for (int idx = threadIdx.x; idx < rows_cta * QD; idx += CW * 32) {
+    const int r = idx / QD, q = idx % QD;
+    const int row = rb * rows_cta + r;
+    if (row >= RG) break;
+    const int w0 = r / (MT * 16), rr = r % (MT * 16);
+    float M = -INFINITY;
+    for (int k = 0; k < wk; ++k) M = fmaxf(M, s_m[w0 + k * wr][rr]);
+    float lsum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < wk; ++k) {
+      const int w = w0 + k * wr;
+      const float f = s_m[w][rr] == -INFINITY ? 0.f : ex2(s_m[w][rr] - M);
+      const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(ring) +
+                                                        static_cast<size_t>(w) * (MT * 16 * D) + rr * D +
+                                                        ((q ^ (rr & 7)) << 2));
+      lsum = fmaf(f, s_l[w][rr], lsum);
+      if (f != 0.f) {
+        acc.x = fmaf(f, x.x, acc.x), acc.y = fmaf(f, x.y, acc.y);
+        acc.z = fmaf(f, x.z, acc.z), acc.w = fmaf(f, x.w, acc.w);
+      }
+    }
+    if (a.splits > 1) {
+      const size_t prow = (static_cast<size_t>(bh) * a.splits + split) * a.rows_pad + row;
+      *reinterpret_cast<float4*>(a.part_o + prow * D + 4 * q) =
+          make_float4(acc.x * unit, acc.y * unit, acc.z * unit, acc.w * unit);
+      if (q == 0) *reinterpret_cast<float2*>(a.part_ml + prow * 2) = make_float2(M, lsum);
+    } else {
+      const float inv = lsum == 0.f ? 0.f : unit / lsum;  // a row whose mask leaves nothing: zeros, lse -inf
+      const size_t orow = (static_cast<size_t>(b) * a.R + row / a.G) * a.Hq + h * a.G + row % a.G;
+      if (a.out_f32)
+        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow * D + 4 * q) =
+            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+      else
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + 4 * q) =
+            make_uint2(pack_bf(acc.x * inv, acc.y * inv), pack_bf(acc.z * inv, acc.w * inv));
+      if (a.lse && q == 0) a.lse[orow] = (M + log2f(lsum)) * 0.69314718055994531f;
+    }
+  }
+}
+
+// Merge the splits of a row: M = max m_s, out = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s.
+// A warp per row, D / 32 dims per lane, the partial rows of eight splits in flight.
+template <int D>
+__global__ void __launch_bounds__(128) kvq_combine_kernel(const KvqAttnArgs a) {
+  constexpr int PER = D / 32;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = blockIdx.x * 4 + warp, bh = blockIdx.y;
+  const int b = bh / a.Hkv, h = bh % a.Hkv;
+  if (r >= tree_rows(a, b) * a.G) return;
+  const int units = (prefix_len(a, b) + KT - 1) / KT + 1;
+  const int n = min(a.splits, (units + a.tps - 1) / a.tps);
+  const size_t base = static_cast<size_t>(bh) * a.splits * a.rows_pad + r;
+  float M = -INFINITY;
+  for (int s = lane; s < n; s += 32) M = fmaxf(M, a.part_ml[(base + static_cast<size_t>(s) * a.rows_pad) * 2]);
+  M = warp_max(M);
+  float acc[PER], lsum = 0.f;
+#pragma unroll
+  for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+  for (int s0 = 0; s0 < n; s0 += 8) {
+    float x[8][PER];
+    float2 ml[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const size_t at = base + static_cast<size_t>(min(s0 + u, n - 1)) * a.rows_pad;
+      ml[u] = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
+#pragma unroll
+      for (int e = 0; e < PER; e += 2) {
+        const float2 t = *reinterpret_cast<const float2*>(a.part_o + at * D + lane * PER + e);
+        x[u][e] = t.x;
+        x[u][e + 1] = t.y;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (s0 + u >= n) continue;
+      const float f = ml[u].x == -INFINITY ? 0.f : ex2(ml[u].x - M);
+      lsum = fmaf(f, ml[u].y, lsum);
+      if (f == 0.f) continue;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) acc[e] = fmaf(f, x[u][e], acc[e]);
+    }
+  }
+  const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+  const size_t orow = (static_cast<size_t>(b) * a.R + r / a.G) * a.Hq + h * a.G + r % a.G;
+#pragma unroll
+  for (int e = 0; e < PER; e += 2) {
+    const size_t at = orow * D + lane * PER + e;
+    if (a.out_f32)
+      *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at) = make_float2(acc[e] * inv, acc[e + 1] * inv);
+    else
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at) = pack_bf(acc[e] * inv, acc[e + 1] * inv);
+  }
+  if (a.lse && lane == 0) a.lse[orow] = (M + log2f(lsum)) * 0.69314718055994531f;
+}
+
+template <int D, int MT, bool T2>
+cudaError_t launch_mma(const KvqAttnPlan& p, const Maps& tm, const KvqAttnArgs& a, cudaStream_t s) {
+  auto kern = tree_attn_kvq_kernel<D, MT, T2>;
+  const int smem = 1024 + NST * 2 * KT * D + p.rows_per_cta * q_stride<D>();
+  const int most = 1024 + NST * 2 * KT * D + CW * MT * 16 * q_stride<D>();
+  // opt in to the largest size once per device (not a stream operation)
+  static unsigned long long configured = 0;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(__atomic_load_n(&configured, __ATOMIC_ACQUIRE) & (1ull << dev))) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) __atomic_fetch_or(&configured, 1ull << dev, __ATOMIC_RELEASE);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(p.row_blocks, p.splits, p.B * p.Hkv);
+  cfg.blockDim = dim3(CW * 32);
+  cfg.dynamicSmemBytes = smem;
+  e = cudaLaunchKernelEx(&cfg, kern, tm, a);
+  if (e != cudaSuccess || p.splits == 1) return e;
+  cfg.gridDim = dim3((p.R * p.G + 3) / 4, p.B * p.Hkv);
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, kvq_combine_kernel<D>, a);
+}
+
+}  // namespace
+
+void plan_kvq_attn(const eagle_attn_desc* d, int num_sms, KvqAttnPlan* p) {
+  p->B = d->batch;
+  p->R = d->rows;
+  p->Hq = d->n_q_heads;
+  p->Hkv = d->n_kv_heads;
+  p->G = d->n_q_heads / d->n_kv_heads;
+  p->D = d->head_dim;
+  p->P = d->max_seq;
+  p->W = (d->rows + 63) / 64;
+  p->out_f32 = d->out_dtype == EAGLE_F32;
+  p->terms2 = d->precision == EAGLE_ATTN_PRECISE;
+  p->scale = d->scale;
+  const int RG = p->R * p->G;
+  // rows of a CTA: as few warps along the rows as cover them, up to 8 x 32
+  p->mt = RG <= 16 ? 1 : 2;
+  p->wr = 1;
+  while (p->wr < CW && p->wr * p->mt * 16 < RG) p->wr *= 2;
+  p->rows_per_cta = p->wr * p->mt * 16;
+  p->row_blocks = (RG + p->rows_per_cta - 1) / p->rows_per_cta;
+  p->rows_pad = p->row_blocks * p->rows_per_cta;
+  // pieces of tps 128-key units (the tree counts as one): one wave of CTAs when the groups
+  // are few, pieces of at least 16 units when they are many
+  const int units = (p->P + KT - 1) / KT + 1;
+  const long long base = static_cast<long long>(p->B) * p->Hkv * p->row_blocks;
+  long long splits = d->num_splits > 0 ? d->num_splits : std::max<long long>(1, num_sms / base);
+  if (d->num_splits <= 0 && p->B > 1) splits = std::max<long long>(splits, units / 16);
+  splits = std::min<long long>(std::min<long long>(splits, units), 256);
+  p->tps = static_cast<int>((units + splits - 1) / splits);
+  p->splits = (units + p->tps - 1) / p->tps;
+  p->off_err = 0;
+  size_t off = 256;
+  p->off_o = p->off_ml = 0;
+  if (p->splits > 1) {
+    const size_t rows = static_cast<size_t>(p->B) * p->Hkv * p->splits * p->rows_pad;
+    p->off_o = off;
+    off += (rows * p->D * 4 + 255) / 256 * 256;
+    p->off_ml = off;
+    off += rows * 8;
+  }
+  p->total = off;
+}
+
+cudaError_t launch_kvq_attn(const KvqAttnPlan& p, const void* q, const void* k8, const float* ks, const void* v8,
+                            const float* vs, const void* tree_k, const void* tree_v, const int32_t* seq_len,
+                            const int32_t* n_nodes, const uint64_t* anc_mask, void* out, float* lse, void* ws,
+                            cudaStream_t s) {
+  KvqAttnArgs a;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k8 = static_cast<const uint8_t*>(k8);
+  a.ks = ks;
+  a.v8 = static_cast<const uint8_t*>(v8);
+  a.vs = vs;
+  a.tk = static_cast<const uint16_t*>(tree_k);
+  a.tv = static_cast<const uint16_t*>(tree_v);
+  a.seq_len = seq_len;
+  a.n_nodes = n_nodes;
+  a.anc_mask = anc_mask;
+  a.out = out;
+  a.lse = lse;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  a.part_o = reinterpret_cast<float*>(w + p.off_o);
+  a.part_ml = reinterpret_cast<float*>(w + p.off_ml);
+  a.err = reinterpret_cast<int*>(w + p.off_err);
+  a.B = p.B;
+  a.R = p.R;
+  a.Hq = p.Hq;
+  a.Hkv = p.Hkv;
+  a.G = p.G;
+  a.P = p.P;
+  a.W = p.W;
+  a.splits = p.splits;
+  a.tps = p.tps;
+  a.rows_pad = p.rows_pad;
+  a.out_f32 = p.out_f32;
+  a.wr = p.wr;
+  a.scale = p.scale;
+  a.scale_log2 = p.scale * kLog2e;
+  Maps tm;
+  const unsigned long long rows = static_cast<unsigned long long>(p.B) * p.Hkv * p.P;
+  const CUtensorMapSwizzle sw = p.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  if (!make_tmap_2d(&tm.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, k8, p.D, rows, p.D, KT, sw) ||
+      !make_tmap_2d(&tm.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, v8, p.D, rows, p.D, KT, sw))
+    return cudaErrorInvalidValue;
+  if (p.D == 64) {
+    if (p.mt == 1) return p.terms2 ? launch_mma<64, 1, true>(p, tm, a, s) : launch_mma<64, 1, false>(p, tm, a, s);
+    return p.terms2 ? launch_mma<64, 2, true>(p, tm, a, s) : launch_mma<64, 2, false>(p, tm, a, s);
+  }
+  if (p.mt == 1) return p.terms2 ? launch_mma<128, 1, true>(p, tm, a, s) : launch_mma<128, 1, false>(p, tm, a, s);
+  return p.terms2 ? launch_mma<128, 2, true>(p, tm, a, s) : launch_mma<128, 2, false>(p, tm, a, s);
+}
+
+}  // namespace eagle

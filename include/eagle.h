@@ -119,7 +119,13 @@ enum {
 enum { EAGLE_ENGINE_AUTO = 0, EAGLE_ENGINE_MMA_SYNC = 1 };
 
 /* Workspace kinds for eagle_workspace_size() */
-enum { EAGLE_WS_TREE_BUILD = 1, EAGLE_WS_TREE_ATTN = 2, EAGLE_WS_ACCEPT = 3, EAGLE_WS_TTT_ATTN = 4 };
+enum {
+  EAGLE_WS_TREE_BUILD = 1,
+  EAGLE_WS_TREE_ATTN = 2,
+  EAGLE_WS_ACCEPT = 3,
+  EAGLE_WS_TTT_ATTN = 4,
+  EAGLE_WS_TREE_ATTN_KVQ = 5 /* desc: eagle_attn_desc, as eagle_tree_attn_kvq takes it */
+};
 
 /* ---------------------------------------------------------------- tree build */
 typedef struct {
@@ -261,6 +267,63 @@ int eagle_tree_attn(const eagle_attn_desc* d, const void* q, const void* k_cache
  * when a separate kernel merges the splits).  Either pointer may be NULL.  Returns
  * EAGLE_OK, or the status eagle_tree_attn would return for a bad descriptor. */
 int eagle_tree_attn_plan(const eagle_attn_desc* d, int32_t* splits, int32_t* kernels);
+
+/* eagle_tree_attn over the 8-bit cache (see "8-bit KV cache" below for its format):
+ *     out = softmax(scale * q k^T) v,   lse = ln sum exp(scale * q k^T)
+ * with prefix keys and values code * scale and the tree's own K/V (not yet committed) in
+ * bf16.  q, tree_k, tree_v, seq_len, n_nodes, anc_mask, out and lse as eagle_tree_attn; d
+ * the same descriptor with dtype EAGLE_BF16.  A row with no key at all (seq_len 0 and an
+ * empty mask) gets zeros and lse -inf.  Cache rows behind seq_len may hold anything; the
+ * tree rows of existing nodes and the cache rows before seq_len take part in products with
+ * weight 0 where a mask hides them, so a value there that is not finite spoils other rows.
+ *   precision  EAGLE_ATTN_FAST: P enters the product with the prefix values as one half
+ *              (11 significant bits: an error of 2^-11 of sum p |v| at most, an eighth of a
+ *              bf16 output's own rounding); EAGLE_ATTN_PRECISE: as two halves (22 bits), either
+ *              with a floor of 2^-35 of the row's largest p.  The tree's part always takes two
+ *              bf16 terms.  Scores, softmax and sums are fp32.
+ * ws: eagle_workspace_size(EAGLE_WS_TREE_ATTN_KVQ, d) bytes, zero-filled before its first
+ * use; one workspace serves one stream at a time.  Its first 4 bytes are an error word as in
+ * eagle_tree_attn.
+ * Unsupported: dtype not EAGLE_BF16, head_dim not 64 / 128, R > 128, Hq % Hkv != 0,
+ * B * Hkv > 65535, B * Hkv * P >= 2^31, fault_test. */
+int eagle_tree_attn_kvq(const eagle_attn_desc* d, const void* q, const void* k_codes, const float* k_scale,
+                        const void* v_codes, const float* v_scale, const void* tree_k, const void* tree_v,
+                        const int32_t* seq_len, const int32_t* n_nodes, const uint64_t* anc_mask, void* out,
+                        float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------- query / key norms, rotation */
+/* What stands between the verify pass's QKV projection and tree attention, in one pass:
+ * each query and key head's RMS norm, the rotation at the node's position (a node's
+ * position is its prefix length plus its depth: pos_id of eagle_tree_build), and the layout
+ * tree attention reads.  For one head x of q or k:
+ *     y = x / sqrt(mean(x^2) + eps) * weight           (weight NULL: y = x)
+ *     (a, b) -> (a cos t - b sin t, a sin t + b cos t)   t = pos * inv_freq[i]
+ * for pair i of the first rot_dim elements: (i, i + rot_dim / 2), or (2 i, 2 i + 1) if
+ * interleaved; v is moved as it is.  fp32 arithmetic (the angle is reduced in fp64), one
+ * rounding at the end.
+ *   qkv [B][R] rows of (Hq + 2 Hkv) heads x D (all of q, then k, then v), row_stride
+ *   elements apart; q_weight, k_weight [D] of the element type, may be NULL; inv_freq
+ *   [rot_dim / 2] fp32; pos_id [B][R] int32; n_nodes [B] int32, may be NULL (rows
+ *   i >= n_nodes[b] of the outputs are left as they were); q [B][R][Hq][D]; k, v [B][Hkv][R][D].
+ * R is not limited to a tree's rows: a prompt's rows go the same way, into eagle_kvq_write.
+ * Inputs and outputs must not overlap. */
+typedef struct {
+  int32_t batch;       /* B, 1..65535 */
+  int32_t rows;        /* R >= 1 */
+  int32_t n_q_heads;   /* Hq */
+  int32_t n_kv_heads;  /* Hkv */
+  int32_t head_dim;    /* D: 64 or 128 */
+  int32_t rot_dim;     /* rotated elements of a head, a multiple of 16, 0..D */
+  int32_t row_stride;  /* elements from one row of qkv to the next, a multiple of 8 and at
+                          least (Hq + 2 Hkv) D; 0: exactly that */
+  int32_t interleaved; /* 0: pairs (i, i + rot_dim / 2); 1: (2 i, 2 i + 1) */
+  float eps;           /* >= 0 */
+  int32_t dtype;       /* element type of qkv, the weights and the outputs */
+} eagle_qk_norm_rope_desc;
+
+int eagle_qk_norm_rope(const eagle_qk_norm_rope_desc* d, const void* qkv, const void* q_weight,
+                       const void* k_weight, const float* inv_freq, const int32_t* pos_id, const int32_t* n_nodes,
+                       void* q, void* k, void* v, void* stream);
 
 /* ---------------------------------------------------------------- acceptance */
 typedef struct {
@@ -425,6 +488,58 @@ int eagle_kv_commit(const eagle_commit_desc* d, void* const* k_cache_layers, voi
                     const void* const* tree_k_layers, const void* const* tree_v_layers,
                     const int32_t* n_acc, const int32_t* path, int32_t* seq_len, int32_t* commit_pos,
                     void* feat_cache, const void* tree_feat, uint32_t* status, void* stream);
+
+/* ---------------------------------------------------------------- 8-bit KV cache */
+/* The prefix K/V cache in 8 bits: half the bytes that tree attention streams (the method
+ * keeps it in 16 bits; the pages have no counterpart).  Per layer and for K and V each
+ *     codes  uint8 [B][Hkv][P][D]                 e4m3 (4 significant bits, largest 448)
+ *     scale  fp32  [B][Hkv][ceil(P / EAGLE_KVQ_BLOCK)]
+ * and row r holds code * scale[r / EAGLE_KVQ_BLOCK].  The writers below choose a block's
+ * scale as the smallest power of two s with amax <= 448 s (amax over the block's finite
+ * values; 0 for a block of zeros, >= 2^-126), so a stored value is the nearest e4m3 multiple of s
+ * and an error of at most 2^-4 of the value, or 2^-10 s where it is small.  A value that
+ * is not finite is stored as NaN.  eagle_tree_attn_kvq and eagle_kvq_read take any finite
+ * scale >= 0 (0: the block is zeros). */
+#define EAGLE_KVQ_BLOCK 64
+
+typedef struct {
+  int32_t batch;      /* B, B * Hkv <= 65535 */
+  int32_t n_kv_heads; /* Hkv */
+  int32_t head_dim;   /* D: 64 or 128 */
+  int32_t max_seq;    /* P: cache capacity per request */
+  int32_t rows;       /* N: rows per request of k / v */
+  int32_t dtype;      /* element type of k / v */
+} eagle_kvq_desc;
+
+/* Quantise rows 0 .. count[b] - 1 of k, v [B][Hkv][N][D] into cache rows start[b] ..
+ * start[b] + count[b] - 1 (a prompt, or a chunk of one).  Rows before start[b] stay; where
+ * they share the first block, its scale is the larger of its old one and the new rows' own,
+ * and if it grew their codes are moved to it (a code that becomes subnormal loses bits, no
+ * other does).  Rows behind the written ones are free space: their bytes are left as they
+ * were, but the scale of the last block no longer counts for them.
+ *   start [B], count [B] int32 DEVICE (count NULL: N rows each).  A request whose span is not
+ *   inside [0, P], or whose count is not in [0, N], is left untouched and
+ *   EAGLE_STATUS_CACHE_FULL is ORed into status (DEVICE, may be NULL). */
+int eagle_kvq_write(const eagle_kvq_desc* d, const void* k, const void* v, const int32_t* start,
+                    const int32_t* count, void* k_codes, float* k_scale, void* v_codes, float* v_scale,
+                    uint32_t* status, void* stream);
+
+/* The inverse: k, v [B][Hkv][N][D] rows 0 .. count[b] - 1 = the cache's rows from start[b],
+ * code * scale rounded once to the element type; rows behind them are left as they were.
+ * Same conditions on start and count as eagle_kvq_write. */
+int eagle_kvq_read(const eagle_kvq_desc* d, const void* k_codes, const float* k_scale, const void* v_codes,
+                   const float* v_scale, const int32_t* start, const int32_t* count, void* k, void* v,
+                   uint32_t* status, void* stream);
+
+/* eagle_kv_commit into 8-bit caches: the accepted path's rows are quantised behind
+ * seq_len[b] as eagle_kvq_write does (the scale of a begun block only grows), everything
+ * else as eagle_kv_commit.  k_codes_layers, k_scale_layers, v_codes_layers, v_scale_layers,
+ * tree_k_layers, tree_v_layers: HOST arrays of `layers` DEVICE pointers; d->dtype is the
+ * tree K/V's element type and d->head_dim 64 or 128, batch and n_kv_heads <= 65535. */
+int eagle_kvq_commit(const eagle_commit_desc* d, void* const* k_codes_layers, float* const* k_scale_layers,
+                     void* const* v_codes_layers, float* const* v_scale_layers, const void* const* tree_k_layers,
+                     const void* const* tree_v_layers, const int32_t* n_acc, const int32_t* path, int32_t* seq_len,
+                     int32_t* commit_pos, void* feat_cache, const void* tree_feat, uint32_t* status, void* stream);
 
 /* ---------------------------------------------------------------- misc */
 /* Scratch bytes a call needs (which = EAGLE_WS_*, desc = the matching desc); 0 on a
