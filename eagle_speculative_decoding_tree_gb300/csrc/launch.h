@@ -167,9 +167,13 @@ struct KvqAttnPlan {
   int B, R, Hq, Hkv, G, D, P, W, out_f32;
   bool terms2;      // P as two half terms (EAGLE_ATTN_PRECISE)
   float scale;
-  int mt, wr;       // 16-row tiles per warp, warps along the rows (8 / wr split a tile's keys)
+  bool tc;          // tcgen05 kernel
+  int mt, wr;       // mma.sync: 16-row tiles per warp, warps along the rows (8 / wr split a tile's
+                    // keys); tcgen05: wr row tiles of 128
   int rows_per_cta, row_blocks, rows_pad;
-  int splits, tps;  // split s takes 128-key units [s tps, (s + 1) tps) of its request
+  int splits, tps;  // mma.sync: split s takes 128-key units [s tps, (s + 1) tps) of its request, the
+                    // tree being the last; tcgen05: piece 0 is the tree, piece s the prefix tiles
+                    // [(s - 1) tps, s tps)
   size_t off_err, off_o, off_ml, total;
 };
 void plan_kvq_attn(const eagle_attn_desc* d, int num_sms, KvqAttnPlan* p);
@@ -189,9 +193,10 @@ struct KvqAttnArgs {
   float* part_o;   // [B*Hkv][splits][rows_pad][D]
   float* part_ml;  // [B*Hkv][splits][rows_pad][2]: max in log2 units, sum
   int* err;
-  int B, R, Hq, Hkv, G, P, W, splits, tps, rows_pad, out_f32, wr;
+  int B, R, Hq, Hkv, G, P, W, splits, tps, rows_pad, out_f32, wr, tc;
   float scale, scale_log2;
 };
+cudaError_t launch_kvq_attn_tc(const KvqAttnPlan& p, const KvqAttnArgs& a, cudaStream_t s);
 cudaError_t launch_kvq_attn(const KvqAttnPlan& p, const void* q, const void* k8, const float* ks, const void* v8,
                             const float* vs, const void* tree_k, const void* tree_v, const int32_t* seq_len,
                             const int32_t* n_nodes, const uint64_t* anc_mask, void* out, float* lse, void* ws,

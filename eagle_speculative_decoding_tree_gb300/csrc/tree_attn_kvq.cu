@@ -555,8 +555,8 @@ __global__ void __launch_bounds__(128) kvq_combine_kernel(const KvqAttnArgs a) {
   const int r = blockIdx.x * 4 + warp, bh = blockIdx.y;
   const int b = bh / a.Hkv, h = bh % a.Hkv;
   if (r >= tree_rows(a, b) * a.G) return;
-  const int units = (prefix_len(a, b) + KT - 1) / KT + 1;
-  const int n = min(a.splits, (units + a.tps - 1) / a.tps);
+  const int tiles = (prefix_len(a, b) + KT - 1) / KT;
+  const int n = min(a.splits, a.tc ? 1 + (tiles + a.tps - 1) / a.tps : (tiles + a.tps) / a.tps);
   const size_t base = static_cast<size_t>(bh) * a.splits * a.rows_pad + r;
   float M = -INFINITY;
   for (int s = lane; s < n; s += 32) M = fmaxf(M, a.part_ml[(base + static_cast<size_t>(s) * a.rows_pad) * 2]);
@@ -601,6 +601,21 @@ __global__ void __launch_bounds__(128) kvq_combine_kernel(const KvqAttnArgs a) {
   if (a.lse && lane == 0) a.lse[orow] = (M + log2f(lsum)) * 0.69314718055994531f;
 }
 
+template <int D>
+cudaError_t launch_combine(const KvqAttnPlan& p, const KvqAttnArgs& a, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((p.R * p.G + 3) / 4, p.B * p.Hkv);
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kvq_combine_kernel<D>, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 template <int D, int MT, bool T2>
 cudaError_t launch_mma(const KvqAttnPlan& p, const Maps& tm, const KvqAttnArgs& a, cudaStream_t s) {
   auto kern = tree_attn_kvq_kernel<D, MT, T2>;
@@ -628,10 +643,7 @@ cudaError_t launch_mma(const KvqAttnPlan& p, const Maps& tm, const KvqAttnArgs& 
   cfg.dynamicSmemBytes = smem;
   e = cudaLaunchKernelEx(&cfg, kern, tm, a);
   if (e != cudaSuccess || p.splits == 1) return e;
-  cfg.gridDim = dim3((p.R * p.G + 3) / 4, p.B * p.Hkv);
-  cfg.blockDim = dim3(128);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, kvq_combine_kernel<D>, a);
+  return launch_combine<D>(p, a, s);
 }
 
 }  // namespace
@@ -649,22 +661,39 @@ void plan_kvq_attn(const eagle_attn_desc* d, int num_sms, KvqAttnPlan* p) {
   p->terms2 = d->precision == EAGLE_ATTN_PRECISE;
   p->scale = d->scale;
   const int RG = p->R * p->G;
-  // rows of a CTA: as few warps along the rows as cover them, up to 8 x 32
-  p->mt = RG <= 16 ? 1 : 2;
-  p->wr = 1;
-  while (p->wr < CW && p->wr * p->mt * 16 < RG) p->wr *= 2;
-  p->rows_per_cta = p->wr * p->mt * 16;
-  p->row_blocks = (RG + p->rows_per_cta - 1) / p->rows_per_cta;
+  const int tiles = (p->P + KT - 1) / KT;
+  // the tcgen05 kernel's row tiles are 128 rows whether or not they are filled
+  p->tc = d->engine == EAGLE_ENGINE_AUTO && p->D == 128 && RG > 32;
+  if (p->tc) {
+    p->mt = 0;
+    p->wr = RG > 128 ? 2 : 1;
+    p->rows_per_cta = p->wr * 128;
+    p->row_blocks = (RG + p->rows_per_cta - 1) / p->rows_per_cta;
+    // one wave of CTAs (one per SM: all of TMEM) while the groups leave room for a prefix
+    // piece and the tree each, pieces of 16 tiles when they do not
+    const long long base = static_cast<long long>(p->B) * p->Hkv * p->row_blocks;
+    long long pieces = d->num_splits > 0 ? d->num_splits : num_sms / base - 1;
+    if (pieces < 1) pieces = (tiles + 15) / 16;
+    pieces = std::min<long long>(std::min<long long>(pieces, tiles), 255);
+    p->tps = static_cast<int>((tiles + pieces - 1) / pieces);
+    p->splits = (tiles + p->tps - 1) / p->tps + 1;
+  } else {
+    // rows of a CTA: as few warps along the rows as cover them, up to 8 x 32
+    p->mt = RG <= 16 ? 1 : 2;
+    p->wr = 1;
+    while (p->wr < CW && p->wr * p->mt * 16 < RG) p->wr *= 2;
+    p->rows_per_cta = p->wr * p->mt * 16;
+    p->row_blocks = (RG + p->rows_per_cta - 1) / p->rows_per_cta;
+    // pieces of tps 128-key units (the tree counts as one): one wave of CTAs when the groups
+    // are few, pieces of at least 16 units when they are many
+    const long long base = static_cast<long long>(p->B) * p->Hkv * p->row_blocks;
+    long long splits = d->num_splits > 0 ? d->num_splits : std::max<long long>(1, num_sms / base);
+    if (d->num_splits <= 0 && p->B > 1) splits = std::max<long long>(splits, (tiles + 1) / 16);
+    splits = std::min<long long>(std::min<long long>(splits, tiles + 1), 256);
+    p->tps = static_cast<int>((tiles + splits) / splits);
+    p->splits = (tiles + p->tps) / p->tps;
+  }
   p->rows_pad = p->row_blocks * p->rows_per_cta;
-  // pieces of tps 128-key units (the tree counts as one): one wave of CTAs when the groups
-  // are few, pieces of at least 16 units when they are many
-  const int units = (p->P + KT - 1) / KT + 1;
-  const long long base = static_cast<long long>(p->B) * p->Hkv * p->row_blocks;
-  long long splits = d->num_splits > 0 ? d->num_splits : std::max<long long>(1, num_sms / base);
-  if (d->num_splits <= 0 && p->B > 1) splits = std::max<long long>(splits, units / 16);
-  splits = std::min<long long>(std::min<long long>(splits, units), 256);
-  p->tps = static_cast<int>((units + splits - 1) / splits);
-  p->splits = (units + p->tps - 1) / p->tps;
   p->off_err = 0;
   size_t off = 256;
   p->off_o = p->off_ml = 0;
@@ -711,8 +740,13 @@ cudaError_t launch_kvq_attn(const KvqAttnPlan& p, const void* q, const void* k8,
   a.rows_pad = p.rows_pad;
   a.out_f32 = p.out_f32;
   a.wr = p.wr;
+  a.tc = p.tc ? 1 : 0;
   a.scale = p.scale;
   a.scale_log2 = p.scale * kLog2e;
+  if (p.tc) {
+    const cudaError_t e = launch_kvq_attn_tc(p, a, s);
+    return e != cudaSuccess ? e : launch_combine<128>(p, a, s);
+  }
   Maps tm;
   const unsigned long long rows = static_cast<unsigned long long>(p.B) * p.Hkv * p.P;
   const CUtensorMapSwizzle sw = p.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;

@@ -1,0 +1,613 @@
+// tree_attn_kvq_tc.cu -- tree attention over the 8-bit KV cache on the tcgen05 tensor cores
+// (head_dim 128), for trees of many rows; tree_attn_kvq.cu has the operation and the
+// few-row kernel.
+//
+// Q K^T takes the codes as they come: kind::f8f6f4 with both operands e4m3.  A query row is
+// multiplied by a power of two that puts its largest element in (224, 448] and split into two
+// e4m3 terms, q = hi + lo: four bits each hold bf16's eight exactly, down to elements of 2^-11
+// of the largest, and 2^-19 of it below.  Two products at twice the half rate cost what one
+// half product would, and K is never converted.  P V takes halves (11 bits in one term, against
+// the four of an e4m3 P): three warps widen each V tile from e4m3 to half, exactly, into a
+// second ring.  The scales stay outside as in tree_attn_kvq.cu: ks on the scores of its 64
+// keys, vs / vref in the exponent of P.
+//
+// One CTA per (piece, request x KV head, row block), 384 threads:
+//   warps 0-3, 4-7  softmax warpgroups; a thread owns one row (its TMEM lane) and reads a
+//                   tile's 128 scores twice: once for the maximum, once for the exponentials,
+//                   so it never holds more than 64 of them (168 registers a thread).
+//   warps 8-10      V widening; one lane of warp 8 refills the V ring, one of warp 9 the K ring.
+//   warp 11         issues every tcgen05.mma: QK0 QK1 | PV0 QK2 | PV1 QK3 | ...
+// Items alternate between the warpgroups, so one tile's products run under the other's softmax.
+// With more than 128 rows (A) warpgroup w has rows 128 w .. and both take every tile: the
+// codes are read and widened once for 256 rows.  With fewer (B) both have the same rows and
+// take alternate tiles; their states merge in the epilogue.
+// TMEM: S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512); P overwrites S in place.
+//
+// Piece 0 is the tree itself (bf16 Q, K, V and P in two bf16 terms, one tile); the others are
+// tps 128-key tiles of the prefix.  Pieces write fp32 partials (TMA stores) that
+// kvq_combine_kernel merges.
+#include "common.cuh"
+#include "kvq.cuh"
+#include "launch.h"
+#include "sm100.cuh"
+#include "tmap.h"
+
+namespace eagle {
+namespace {
+
+using namespace sm100;
+
+constexpr int KT = 128;
+constexpr int T8 = KT * 128;    // a tile of codes, 16 KB
+constexpr int T16 = 2 * T8;     // a tile of halves, 32 KB: two 64-dim halves of 128-byte rows
+constexpr int KST = 3, VST = 3; // ring stages of K and V codes
+constexpr int SM_Q = 0;                 // two row tiles: hi | lo codes (or bf16 halves), 64 KB
+constexpr int SM_K = SM_Q + 2 * T16;
+constexpr int SM_V = SM_K + KST * T8;
+constexpr int SM_W = SM_V + VST * T8;   // widened V, two stages
+constexpr int SMEM = SM_W + 2 * T16 + 1024;
+constexpr int NT = 384;
+constexpr float kLazy = 4.f;            // as in tree_attn_kvq.cu
+constexpr int PB = 11;
+
+enum : int { ERR_K = 1, ERR_KE = 2, ERR_V = 4, ERR_W = 8, ERR_WE = 16, ERR_S = 32, ERR_P = 64, ERR_O = 128, ERR_Q = 512 };
+
+struct Maps {
+  CUtensorMap k, v, po;
+};
+
+__device__ __forceinline__ uint32_t col_s(int w) { return static_cast<uint32_t>(w) * 128u; }
+__device__ __forceinline__ uint32_t col_o(int w) { return 256u + static_cast<uint32_t>(w) * 128u; }
+
+// Instruction descriptors: fp32 accumulator; operand formats in bits 7 and 10 (f8f6f4: e4m3 0;
+// f16: half 0, bf16 1).
+__host__ __device__ constexpr uint32_t idesc(int fmt, int b_mn) {
+  return (1u << 4) | (static_cast<uint32_t>(fmt) << 7) | (static_cast<uint32_t>(fmt) << 10) |
+         (static_cast<uint32_t>(b_mn) << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_f8_ss(uint32_t d, uint64_t ad, uint64_t bd, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(id), "r"(acc)
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t bf2_bits(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float max32(const uint32_t (&a)[32]) {
+  float m[11];
+#pragma unroll
+  for (int i = 0; i < 10; ++i)
+    m[i] = max3(__uint_as_float(a[3 * i]), __uint_as_float(a[3 * i + 1]), __uint_as_float(a[3 * i + 2]));
+  m[10] = fmaxf(__uint_as_float(a[30]), __uint_as_float(a[31]));
+  return fmaxf(max3(max3(m[0], m[1], m[2]), max3(m[3], m[4], m[5]), max3(m[6], m[7], m[8])), fmaxf(m[9], m[10]));
+}
+
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
+}
+
+// 32 scores -> P in columns col .. (TERMS 1: 16 of them, TERMS 2: hi 16, lo 16), p = 2^(s c + o);
+// keys whose bit is clear get 0.  Returns the fp32 sum.
+template <int TERMS, bool BF>
+__device__ __forceinline__ float emit(const uint32_t (&r)[32], uint32_t col, float c, float o, bool full, uint32_t bits) {
+  const uint64_t c2 = f32x2(__float_as_uint(c), __float_as_uint(c)), o2 = f32x2(__float_as_uint(o), __float_as_uint(o));
+  uint64_t acc = 0ull;
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    uint32_t hi[8], lo[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int k = 16 * g + 2 * j;
+      float x0, x1;
+      f32x2_split(fma_f32x2(f32x2(r[k], r[k + 1]), c2, o2), x0, x1);
+      float p0 = ex2(x0), p1 = ex2(x1);
+      if (!full) {
+        p0 = (bits >> k) & 1u ? p0 : 0.f;
+        p1 = (bits >> (k + 1)) & 1u ? p1 : 0.f;
+      }
+      acc = add_f32x2(acc, f32x2(__float_as_uint(p0), __float_as_uint(p1)));
+      if (BF) {
+        hi[j] = bf2_bits(p0, p1);
+        if (TERMS == 2) lo[j] = bf2_bits(p0 - __uint_as_float(hi[j] << 16), p1 - __uint_as_float(hi[j] & 0xffff0000u));
+      } else {
+        hi[j] = half2_bits(p0, p1);
+        if (TERMS == 2) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi[j]));
+          lo[j] = half2_bits(p0 - f.x, p1 - f.y);
+        }
+      }
+    }
+    tmem_st8(col + 8 * g, hi);
+    if (TERMS == 2) tmem_st8(col + 16 + 8 * g, lo);
+  }
+  float a0, a1;
+  f32x2_split(acc, a0, a1);
+  return a0 + a1;
+}
+
+struct Range {
+  int L, Rb, tile0, n;  // the piece's prefix tiles [tile0, tile0 + n); n = 1 for the tree
+  bool tree;
+};
+
+template <int TERMS>
+__global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_constant__ Maps tm, const KvqAttnArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t k_full[KST], k_empty[KST], v_full[VST], w_full[2], w_empty[2], s_full[2], p_full[2], q_full, o_full;
+  __shared__ uint32_t tmem_base;
+  // row maxima and sums of the two warpgroups, exchanged in the epilogue (the widened V's area,
+  // free by then)
+  float (*s_m)[128] = reinterpret_cast<float (*)[128]>(smem + SM_W);
+  float (*s_l)[128] = reinterpret_cast<float (*)[128]>(smem + SM_W + 1024);
+
+  const int piece = blockIdx.x, bh = blockIdx.y, rb = blockIdx.z;
+  const int b = bh / a.Hkv, h = bh % a.Hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool two = a.wr == 2;            // A: two row tiles
+  const int row0 = rb * (two ? 256 : 128);
+
+  if (warp == 11) {
+    tmem_alloc(&tmem_base, 512);
+    tmem_relinquish();
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < KST; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+    }
+    for (int s = 0; s < VST; ++s) mbar_init(&v_full[s], 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&w_full[s], 3);
+      mbar_init(&w_empty[s], 1);
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], 128);
+    }
+    mbar_init(&q_full, 8);
+    mbar_init(&o_full, 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  tc_fence_after();
+  griddep_wait();
+  griddep_launch_dependents();
+
+  Range r;
+  r.L = a.seq_len[b];
+  r.L = r.L < 0 ? 0 : (r.L > a.P ? a.P : r.L);
+  r.Rb = a.n_nodes ? min(max(a.n_nodes[b], 0), a.R) : a.R;
+  r.tree = piece == 0;
+  const int n_pref = (r.L + KT - 1) / KT;
+  r.tile0 = (piece - 1) * a.tps;
+  r.n = r.tree ? 1 : max(0, min(a.tps, n_pref - r.tile0));
+  const int RG = r.Rb * a.G;
+  const bool work = r.n > 0 && row0 < RG;
+  const int items = work ? (two ? 2 * r.n : r.n) : 0;
+  auto tile_of = [&](int i) { return two ? i >> 1 : i; };
+  auto last_of = [&](int i) { return !two || (i & 1); };  // the tile's last item
+  const uint32_t tb = tmem_base;
+  const int nblk = (a.P + kQB - 1) / kQB;
+
+  if (warp >= 8 && warp < 11) {
+    // ------------------------------------------------------------ V widening, ring refills
+    if (work && !r.tree) {
+      const uint64_t policy = policy_evict_first();
+      const int y0 = bh * a.P + r.tile0 * KT;
+      const bool vload = warp == 8 && lane == 0, kload = warp == 9 && lane == 0;
+      auto load = [&](const CUtensorMap& m, int at, uint64_t* bar, int t) {
+        mbar_arrive_expect_tx(bar, T8);
+        tma_load_2d_hint(smem + at, &m, 0, y0 + t * KT, bar, policy);
+      };
+      if (kload)
+        for (int t = 0; t < min(KST, r.n); ++t) load(tm.k, SM_K + t * T8, &k_full[t], t);
+      if (vload)
+        for (int t = 0; t < min(VST, r.n); ++t) load(tm.v, SM_V + t * T8, &v_full[t], t);
+      int k_in = min(KST, r.n), v_in = min(VST, r.n);  // loads issued
+      bool ok = true;
+      const int id = threadIdx.x - 256;  // 0 .. 95
+      for (int t = 0; t < r.n && ok; ++t) {
+        const int s = t % VST, w = t & 1;
+        bool mine = wait_parity(&v_full[s], (t / VST) & 1, a.err, ERR_V);
+        if (mine && t >= 2) mine = wait_parity(&w_empty[w], ((t >> 1) - 1) & 1, a.err, ERR_WE);
+        ok = __all_sync(0xffffffffu, mine);
+        if (!ok) break;
+        const int nv = min(KT, r.L - (r.tile0 + t) * KT);
+        const uint8_t* src = smem + SM_V + s * T8;
+        uint8_t* dst = smem + SM_W + w * T16;
+#pragma unroll 4
+        for (int i = id; i < KT * 8; i += 96) {
+          const int row = i & 127, c = i >> 7;
+          const uint4 u = row < nv ? *reinterpret_cast<const uint4*>(src + row * 128 + ((c ^ (row & 7)) << 4))
+                                   : make_uint4(0, 0, 0, 0);  // rows past the prefix: zeros, whatever they hold
+          uint8_t* d = dst + (c >> 2) * T8 + row * 128;
+          const int p = 2 * (c & 3);
+          *reinterpret_cast<uint4*>(d + ((p ^ (row & 7)) << 4)) =
+              make_uint4(kvq_half2(u.x), kvq_half2(u.x >> 16), kvq_half2(u.y), kvq_half2(u.y >> 16));
+          *reinterpret_cast<uint4*>(d + (((p + 1) ^ (row & 7)) << 4)) =
+              make_uint4(kvq_half2(u.z), kvq_half2(u.z >> 16), kvq_half2(u.w), kvq_half2(u.w >> 16));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&w_full[w]);
+        if (vload && v_in < r.n) {  // every widening warp is past stage s
+          if (wait_parity(&w_full[w], (t >> 1) & 1, a.err, ERR_W)) {
+            load(tm.v, SM_V + s * T8, &v_full[s], v_in);
+            ++v_in;
+          } else {
+            ok = false;
+          }
+        }
+        if (kload && k_in < r.n) {
+          if (wait_parity(&k_empty[t % KST], (t / KST) & 1, a.err, ERR_KE)) {
+            load(tm.k, SM_K + (t % KST) * T8, &k_full[t % KST], k_in);
+            ++k_in;
+          } else {
+            ok = false;
+          }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      // no copy may still be landing when the CTA ends
+      if (kload)
+        for (int s = 0; s < KST && s < k_in; ++s) (void)wait_parity(&k_full[s], ((k_in - 1 - s) / KST) & 1, a.err, ERR_K);
+      if (vload)
+        for (int s = 0; s < VST && s < v_in; ++s) (void)wait_parity(&v_full[s], ((v_in - 1 - s) / VST) & 1, a.err, ERR_V);
+    } else if (work) {
+      // the tree's K and V tile as they are (bf16), zeros behind its rows
+      const uint16_t* kg = a.tk + static_cast<size_t>(bh) * a.R * 128;
+      const uint16_t* vg = a.tv + static_cast<size_t>(bh) * a.R * 128;
+      for (int i = threadIdx.x - 256; i < KT * 16; i += 96) {
+        const int row = i >> 4, c = i & 15;
+        uint4 x = make_uint4(0, 0, 0, 0), y = x;
+        if (row < r.Rb) {
+          x = __ldg(reinterpret_cast<const uint4*>(kg + static_cast<size_t>(row) * 128) + c);
+          y = __ldg(reinterpret_cast<const uint4*>(vg + static_cast<size_t>(row) * 128) + c);
+        }
+        const int at = (c >> 3) * T8 + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+        *reinterpret_cast<uint4*>(smem + SM_K + at) = x;
+        *reinterpret_cast<uint4*>(smem + SM_W + at) = y;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&w_full[0]);
+    }
+  } else if (warp == 11) {
+    // ------------------------------------------------------------ tcgen05.mma issue (lane 0)
+    if (lane == 0 && items > 0) {
+      bool ok = wait_parity(&q_full, 0, a.err, ERR_Q);
+      if (r.tree && ok) ok = wait_parity(&w_full[0], 0, a.err, ERR_W);  // K and V both
+      auto qk = [&](int i) {
+        const int t = tile_of(i), w = i & 1, s = t % KST;
+        if (!r.tree && !wait_parity(&k_full[s], (t / KST) & 1, a.err, ERR_K)) return false;
+        tc_fence_after();
+        const uint32_t q = smem_u32(smem + SM_Q) + (two ? w * T16 : 0);
+        const uint32_t k = smem_u32(smem + SM_K) + (r.tree ? 0 : s * T8);
+        if (r.tree) {
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks) {
+            const uint32_t off = (ks >> 2) * T8 + (ks & 3) * 32;
+            mma_ss(tb + col_s(w), smem_desc_sw128(q + off, 16, 1024), smem_desc_sw128(k + off, 16, 1024), idesc(1, 0),
+                   ks > 0);
+          }
+        } else {
+#pragma unroll
+          for (int term = 0; term < 2; ++term)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma_f8_ss(tb + col_s(w), smem_desc_sw128(q + term * T8 + ks * 32, 16, 1024),
+                        smem_desc_sw128(k + ks * 32, 16, 1024), idesc(0, 0), term + ks > 0);
+        }
+        mma_commit(&s_full[w]);
+        if (!r.tree && last_of(i)) mma_commit(&k_empty[s]);
+        return true;
+      };
+      auto pv = [&](int i) {
+        const int t = tile_of(i), w = i & 1;
+        if (!r.tree && !wait_parity(&w_full[t & 1], (t >> 1) & 1, a.err, ERR_W)) return false;
+        if (!wait_parity(&p_full[w], (i >> 1) & 1, a.err, ERR_P)) return false;
+        tc_fence_after();
+        const uint32_t v = smem_u32(smem + SM_W) + (t & 1) * T16;
+        const bool tw = r.tree || TERMS == 2;  // two terms: hi 16 columns, lo 16
+        const uint32_t id = idesc(r.tree ? 1 : 0, 1);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+          const uint64_t bd = smem_desc_sw128(v + ks * 2048, T8, 1024);
+          const uint32_t ac = tb + col_s(w) + (tw ? (ks >> 1) * 32 + (ks & 1) * 8 : ks * 8);
+          mma_ts(tb + col_o(w), ac, bd, id, (i >= 2 || ks > 0) ? 1u : 0u);
+          if (tw) mma_ts(tb + col_o(w), ac + 16, bd, id, 1u);
+        }
+        if (!r.tree && last_of(i)) mma_commit(&w_empty[t & 1]);
+        return true;
+      };
+      ok = ok && qk(0) && (items < 2 || qk(1));
+      for (int i = 0; i < items && ok; ++i) ok = pv(i) && (i + 2 >= items || qk(i + 2));
+      mma_commit(&o_full);
+    }
+    __syncwarp();
+  } else if (work) {
+    // ------------------------------------------------------------ softmax
+    const int w = warp >> 2, qd = warp & 3;
+    const int rl = qd * 32 + lane;  // TMEM lane, row of the warpgroup's tile
+    const int row = row0 + (two ? w * 128 : 0) + rl;
+    const bool live = row < RG;
+    const int node = live ? row / a.G : 0;
+    // Q: A every warpgroup stages its rows; B warpgroup 0 alone (the rows are the same), but
+    // both need the row factor
+    float qs = 1.f;
+    {
+      uint4 x[16];
+      const uint4* src = reinterpret_cast<const uint4*>(
+          a.q + ((static_cast<size_t>(b) * a.R + node) * a.Hq + h * a.G + (live ? row % a.G : 0)) * 128);
+#pragma unroll
+      for (int c = 0; c < 16; ++c) x[c] = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+      uint8_t* dst = smem + SM_Q + (two ? w * T16 : 0) + rl * 128;
+      const bool put = two || w == 0;
+      if (r.tree) {
+        if (put)
+#pragma unroll
+          for (int c = 0; c < 16; ++c) *reinterpret_cast<uint4*>(dst + (c >> 3) * T8 + (((c & 7) ^ (rl & 7)) << 4)) = x[c];
+      } else {
+        float am = 0.f;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const uint32_t u[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float f0 = fabsf(__uint_as_float(u[e] << 16)), f1 = fabsf(__uint_as_float(u[e] & 0xffff0000u));
+            am = fmaxf(am, fmaxf(f0 <= 3.402823466e38f ? f0 : 0.f, f1 <= 3.402823466e38f ? f1 : 0.f));
+          }
+        }
+        // largest element in (224, 448]: the power of two of a cache block's scale
+        qs = kvq_scale(fmaxf(am, 0x1p-100f));
+        const float mul = 1.f / qs;
+        if (put) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t u[2] = {e < 2 ? (e == 0 ? x[2 * c].x : x[2 * c].z) : (e == 2 ? x[2 * c + 1].x : x[2 * c + 1].z),
+                                     e < 2 ? (e == 0 ? x[2 * c].y : x[2 * c].w) : (e == 2 ? x[2 * c + 1].y : x[2 * c + 1].w)};
+              hi[e] = lo[e] = 0u;
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const float f0 = __uint_as_float(u[z] << 16) * mul, f1 = __uint_as_float(u[z] & 0xffff0000u) * mul;
+                const uint32_t c2 = kvq_code2(f0, f1);
+                const float2 back = kvq_float2(c2);
+                hi[e] |= c2 << (16 * z);
+                lo[e] |= kvq_code2(f0 - back.x, f1 - back.y) << (16 * z);
+              }
+            }
+            const int at = (c ^ (rl & 7)) << 4;
+            *reinterpret_cast<uint4*>(dst + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(dst + T8 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full);
+    }
+    // vref: the largest V scale of the piece
+    const float* ks = a.ks + static_cast<size_t>(bh) * nblk + r.tile0 * (KT / kQB);
+    const float* vs = a.vs + static_cast<size_t>(bh) * nblk + r.tile0 * (KT / kQB);
+    int n_blk = 0;
+    float vref = 1.f;
+    if (!r.tree) {
+      n_blk = (min(r.L, (r.tile0 + r.n) * KT) + kQB - 1) / kQB - r.tile0 * (KT / kQB);
+      float m = 0.f;
+      for (int i = lane; i < n_blk; i += 32) m = fmaxf(m, __ldg(vs + i));
+      m = warp_max(m);
+      if (m > 0.f) vref = m;
+    }
+    const float vinv = 1.f / vref;
+    uint32_t tw[4] = {0u, 0u, 0u, 0u};  // the tree's visible keys
+    if (r.tree && live) {
+      const uint64_t* mp = a.anc_mask + (static_cast<size_t>(b) * a.R + node) * a.W;
+      const uint64_t w0 = mp[0], w1 = a.W > 1 ? mp[1] : 0ull;
+      tw[0] = static_cast<uint32_t>(w0) & low_bits(r.Rb);
+      tw[1] = static_cast<uint32_t>(w0 >> 32) & low_bits(r.Rb - 32);
+      tw[2] = static_cast<uint32_t>(w1) & low_bits(r.Rb - 64);
+      tw[3] = static_cast<uint32_t>(w1 >> 32) & low_bits(r.Rb - 96);
+    }
+    const float cr = a.scale_log2 * qs;
+    const uint32_t lb = tb + (static_cast<uint32_t>(qd * 32) << 16);
+    const uint32_t sc = lb + col_s(w), oc = lb + col_o(w);
+    float m_ref = -INFINITY, l = 0.f;
+    bool ok = true;
+    float kn[2] = {0.f, 0.f}, vn[2] = {0.f, 0.f};  // the next tile's scales
+    auto fetch = [&](int t) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int kb = min(2 * t + u, n_blk - 1);
+        kn[u] = __ldg(ks + kb);
+        vn[u] = __ldg(vs + kb);
+      }
+    };
+    if (!r.tree) fetch(min(tile_of(w), r.n - 1));
+    for (int i = w; i < items; i += 2) {
+      const int t = tile_of(i);
+      float ck[2] = {cr, cr}, lr[2] = {0.f, 0.f};
+      if (!r.tree) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          ck[u] = cr * kn[u];
+          lr[u] = fmaxf(__log2f(vn[u] * vinv), -100.f) + PB;
+        }
+        fetch(min(tile_of(i + 2), r.n - 1));
+      }
+      const int nv = r.tree ? 0 : min(KT, r.L - (r.tile0 + t) * KT);
+      uint32_t km[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) km[c] = r.tree ? tw[c] : low_bits(nv - 32 * c);
+      const bool full = !r.tree && nv == KT;
+      ok = __all_sync(0xffffffffu, wait_parity(&s_full[w], (i >> 1) & 1, a.err, ERR_S));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t x[32], y[32];
+      float mx[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        tmem_ld32(sc + 64 * u, x);
+        tmem_ld32(sc + 64 * u + 32, y);
+        tmem_ld_wait();
+        if (!full) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            x[k] = (km[2 * u] >> k) & 1u ? x[k] : 0xff800000u;
+            y[k] = (km[2 * u + 1] >> k) & 1u ? y[k] : 0xff800000u;
+          }
+        }
+        mx[u] = fmaxf(max32(x), max32(y));
+        mx[u] = mx[u] == -INFINITY ? mx[u] : mx[u] * ck[u];
+      }
+      const float top = fmaxf(mx[0], mx[1]);
+      const bool up = top > m_ref + kLazy || (m_ref == -INFINITY && top > -INFINITY);
+      const bool scale_o = up && m_ref != -INFINITY;
+      const float m_new = up ? ceilf(top) : m_ref;
+      if (__any_sync(0xffffffffu, scale_o)) {
+        // O of this warpgroup's earlier tiles: their PV finished before S of this one did
+        const float al = scale_o ? ex2(m_ref - m_new) : 1.f;
+        l *= al;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld32(oc + 32 * c, x);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * al);
+          tmem_st32(oc + 32 * c, x);
+        }
+        tmem_st_wait();
+      }
+      m_ref = m_new;
+      const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        tmem_ld32(sc + 64 * u, x);
+        tmem_ld32(sc + 64 * u + 32, y);
+        tmem_ld_wait();
+        const float off = lr[u] - mu;
+        float sum;
+        if (r.tree) {
+          sum = emit<2, true>(x, sc + 64 * u, ck[u], off, false, km[2 * u]);
+          sum += emit<2, true>(y, sc + 64 * u + 32, ck[u], off, false, km[2 * u + 1]);
+        } else {
+          sum = emit<TERMS, false>(x, sc + (TERMS == 2 ? 64 : 32) * u, ck[u], off, full, km[2 * u]);
+          sum += emit<TERMS, false>(y, sc + (TERMS == 2 ? 64 * u + 32 : 32 * u + 16), ck[u], off, full, km[2 * u + 1]);
+        }
+        l = fmaf(sum, ex2(-lr[u]), l);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&p_full[w]);
+    }
+    // ---- epilogue: partial rows (A: 128 dims of the own row; B: 64 dims of the merged row)
+    ok = __all_sync(0xffffffffu, ok && wait_parity(&o_full, 0, a.err, ERR_O));
+    tc_fence_after();
+    s_m[w][rl] = m_ref;
+    s_l[w][rl] = l;
+    ok = bar_and(1, 256, ok);
+    if (ok) {
+      const float unit = r.tree ? 1.f : vref * (1.f / (1 << PB));
+      float M = m_ref, Lsum = l, fa = unit, fb = 0.f;
+      const bool other = !two && items > 1;
+      if (!two) {
+        const float m0 = s_m[0][rl], m1 = s_m[1][rl];
+        M = fmaxf(m0, m1);
+        fa = m0 == -INFINITY ? 0.f : ex2(m0 - M);
+        fb = m1 == -INFINITY ? 0.f : ex2(m1 - M);
+        Lsum = fa * s_l[0][rl] + fb * s_l[1][rl];
+        fa *= unit;
+        fb *= unit;
+      }
+      // slices of 32 dims staged as 128-byte-swizzled rows over the Q area and both code
+      // rings (every product has finished), then one TMA store each
+      for (int c = two ? 0 : 2 * w; c < (two ? 4 : 2 * w + 2); ++c) {
+        uint32_t x[32], y[32];
+        tmem_ld32(lb + col_o(two ? w : 0) + 32 * c, x);
+        if (other) tmem_ld32(lb + col_o(1) + 32 * c, y);
+        tmem_ld_wait();
+        uint8_t* dst = smem + ((two ? 4 * w : 0) + c) * T8 + rl * 128;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          float f[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            f[e] = __uint_as_float(x[4 * q + e]) * fa;
+            if (other) f[e] = fmaf(__uint_as_float(y[4 * q + e]), fb, f[e]);
+          }
+          *reinterpret_cast<float4*>(dst + ((q ^ (rl & 7)) << 4)) = make_float4(f[0], f[1], f[2], f[3]);
+        }
+      }
+      const size_t prow = (static_cast<size_t>(bh) * a.splits + piece) * a.rows_pad + row0;
+      if (live && (two || w == 0))
+        *reinterpret_cast<float2*>(a.part_ml + (prow + (two ? w * 128 : 0) + rl) * 2) = make_float2(M, Lsum);
+      fence_proxy_async_smem();
+      bar_sync(2 + (two ? w : 0), two ? 128 : 256);
+      if (qd == 0 && lane == 0 && (two || w == 0)) {
+        for (int c = 0; c < 4; ++c)
+          tma_store_2d(&tm.po, smem + ((two ? 4 * w : 0) + c) * T8, 32 * c,
+                       static_cast<int>(prow) + (two ? w * 128 : 0));
+        bulk_commit();
+        bulk_wait_read0();  // the combine kernel reads the rows once this grid has completed
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 11) {
+    tc_fence_after();
+    tmem_dealloc(tb, 512);
+  }
+}
+
+template <int TERMS>
+cudaError_t launch_tc(const KvqAttnPlan& p, const Maps& tm, const KvqAttnArgs& a, cudaStream_t s) {
+  auto kern = tree_attn_kvq_tc_kernel<TERMS>;
+  static unsigned long long configured = 0;  // shared memory opt-in, once per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(__atomic_load_n(&configured, __ATOMIC_ACQUIRE) & (1ull << dev))) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) __atomic_fetch_or(&configured, 1ull << dev, __ATOMIC_RELEASE);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.splits, p.B * p.Hkv, p.row_blocks);
+  cfg.blockDim = dim3(NT);
+  cfg.dynamicSmemBytes = SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, tm, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kvq_attn_tc(const KvqAttnPlan& p, const KvqAttnArgs& a, cudaStream_t s) {
+  Maps tm;
+  const unsigned long long rows = static_cast<unsigned long long>(p.B) * p.Hkv * p.P;
+  const unsigned long long prows = static_cast<unsigned long long>(p.B) * p.Hkv * p.splits * p.rows_pad;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  if (!make_tmap_2d(&tm.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.k8, 128, rows, 128, KT, sw) ||
+      !make_tmap_2d(&tm.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.v8, 128, rows, 128, KT, sw) ||
+      !make_tmap_2d(&tm.po, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, a.part_o, 128, prows, 32, 128, sw))
+    return cudaErrorInvalidValue;
+  return p.terms2 ? launch_tc<2>(p, tm, a, s) : launch_tc<1>(p, tm, a, s);
+}
+
+}  // namespace eagle
