@@ -66,10 +66,34 @@ __host__ __device__ constexpr uint32_t idesc(int fmt, int b_mn) {
          (static_cast<uint32_t>(b_mn) << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 }
 
+// tcgen05.mma and commit by one elected lane of a converged warp: the whole warp computes the
+// descriptors, so they stay in uniform registers.  (Issued from a lane == 0 branch each product
+// took about 150 cycles to issue, more than it runs.)
 __device__ __forceinline__ void mma_f8_ss(uint32_t d, uint64_t ad, uint64_t bd, uint32_t id, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
       "l"(ad), "l"(bd), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t ad, uint64_t bd, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t at, uint64_t bd, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(at), "l"(bd), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar))
       : "memory");
 }
 
@@ -80,6 +104,17 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
 __device__ __forceinline__ uint32_t bf2_bits(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Two halves to e4m3 codes (nearest even, saturating); the difference of two pairs.
+__device__ __forceinline__ uint32_t e4m3x2_of_half2(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+__device__ __forceinline__ uint32_t sub_half2(uint32_t a, uint32_t b) {
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&d);
 }
 
 __device__ __forceinline__ float max32(const uint32_t (&a)[32]) {
@@ -96,9 +131,9 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
 }
 
 // 32 scores -> P in columns col .. (TERMS 1: 16 of them, TERMS 2: hi 16, lo 16), p = 2^(s c + o);
-// keys whose bit is clear get 0.  Returns the fp32 sum.
-template <int TERMS, bool BF>
-__device__ __forceinline__ float emit(const uint32_t (&r)[32], uint32_t col, float c, float o, bool full, uint32_t bits) {
+// unless FULL, keys whose bit is clear get 0.  Returns the fp32 sum.
+template <int TERMS, bool BF, bool FULL>
+__device__ __forceinline__ float emit(const uint32_t (&r)[32], uint32_t col, float c, float o, uint32_t bits) {
   const uint64_t c2 = f32x2(__float_as_uint(c), __float_as_uint(c)), o2 = f32x2(__float_as_uint(o), __float_as_uint(o));
   uint64_t acc = 0ull;
 #pragma unroll
@@ -110,7 +145,7 @@ __device__ __forceinline__ float emit(const uint32_t (&r)[32], uint32_t col, flo
       float x0, x1;
       f32x2_split(fma_f32x2(f32x2(r[k], r[k + 1]), c2, o2), x0, x1);
       float p0 = ex2(x0), p1 = ex2(x1);
-      if (!full) {
+      if (!FULL) {
         p0 = (bits >> k) & 1u ? p0 : 0.f;
         p1 = (bits >> (k + 1)) & 1u ? p1 : 0.f;
       }
@@ -145,6 +180,7 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t k_full[KST], k_empty[KST], v_full[VST], w_full[2], w_empty[2], s_full[2], p_full[2], q_full, o_full;
   __shared__ uint32_t tmem_base;
+  __shared__ float s_q[2][128];  // the query rows' factors
   // row maxima and sums of the two warpgroups, exchanged in the epilogue (the widened V's area,
   // free by then)
   float (*s_m)[128] = reinterpret_cast<float (*)[128]>(smem + SM_W);
@@ -152,7 +188,7 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
 
   const int piece = blockIdx.x, bh = blockIdx.y, rb = blockIdx.z;
   const int b = bh / a.Hkv, h = bh % a.Hkv;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const bool two = a.wr == 2;            // A: two row tiles
   const int row0 = rb * (two ? 256 : 128);
 
@@ -223,17 +259,27 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
         const int nv = min(KT, r.L - (r.tile0 + t) * KT);
         const uint8_t* src = smem + SM_V + s * T8;
         uint8_t* dst = smem + SM_W + w * T16;
-#pragma unroll 4
-        for (int i = id; i < KT * 8; i += 96) {
-          const int row = i & 127, c = i >> 7;
-          const uint4 u = row < nv ? *reinterpret_cast<const uint4*>(src + row * 128 + ((c ^ (row & 7)) << 4))
-                                   : make_uint4(0, 0, 0, 0);  // rows past the prefix: zeros, whatever they hold
-          uint8_t* d = dst + (c >> 2) * T8 + row * 128;
-          const int p = 2 * (c & 3);
-          *reinterpret_cast<uint4*>(d + ((p ^ (row & 7)) << 4)) =
-              make_uint4(kvq_half2(u.x), kvq_half2(u.x >> 16), kvq_half2(u.y), kvq_half2(u.y >> 16));
-          *reinterpret_cast<uint4*>(d + (((p + 1) ^ (row & 7)) << 4)) =
-              make_uint4(kvq_half2(u.z), kvq_half2(u.z >> 16), kvq_half2(u.w), kvq_half2(u.w >> 16));
+        // 16 codes at a time; four loads in flight (the stores could alias them, so the order is
+        // written out)
+        for (int i0 = id; i0 < KT * 8; i0 += 4 * 96) {
+          uint4 u[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = i0 + 96 * e, row = i & 127;
+            u[e] = make_uint4(0, 0, 0, 0);  // rows past the prefix: zeros, whatever they hold
+            if (i < KT * 8 && row < nv)
+              u[e] = *reinterpret_cast<const uint4*>(src + row * 128 + (((i >> 7) ^ (row & 7)) << 4));
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = i0 + 96 * e, row = i & 127, c = i >> 7, p = 2 * (c & 3);
+            if (i >= KT * 8) break;
+            uint8_t* d = dst + (c >> 2) * T8 + row * 128;
+            *reinterpret_cast<uint4*>(d + ((p ^ (row & 7)) << 4)) =
+                make_uint4(kvq_half2(u[e].x), kvq_half2(u[e].x >> 16), kvq_half2(u[e].y), kvq_half2(u[e].y >> 16));
+            *reinterpret_cast<uint4*>(d + (((p + 1) ^ (row & 7)) << 4)) =
+                make_uint4(kvq_half2(u[e].z), kvq_half2(u[e].z >> 16), kvq_half2(u[e].w), kvq_half2(u[e].w >> 16));
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -246,9 +292,12 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
             ok = false;
           }
         }
-        if (kload && k_in < r.n) {
-          if (wait_parity(&k_empty[t % KST], (t / KST) & 1, a.err, ERR_KE)) {
-            load(tm.k, SM_K + (t % KST) * T8, &k_full[t % KST], k_in);
+        // K's stage of the tile before (its QK is done, or nearly: waiting for this tile's would
+        // hold the next widening back behind it)
+        if (kload && t > 0 && k_in < r.n) {
+          const int ps = (t - 1) % KST;
+          if (wait_parity(&k_empty[ps], ((t - 1) / KST) & 1, a.err, ERR_KE)) {
+            load(tm.k, SM_K + ps * T8, &k_full[ps], k_in);
             ++k_in;
           } else {
             ok = false;
@@ -281,58 +330,76 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
       if (lane == 0) mbar_arrive(&w_full[0]);
     }
   } else if (warp == 11) {
-    // ------------------------------------------------------------ tcgen05.mma issue (lane 0)
-    if (lane == 0 && items > 0) {
-      bool ok = wait_parity(&q_full, 0, a.err, ERR_Q);
-      if (r.tree && ok) ok = wait_parity(&w_full[0], 0, a.err, ERR_W);  // K and V both
-      auto qk = [&](int i) {
-        const int t = tile_of(i), w = i & 1, s = t % KST;
-        if (!r.tree && !wait_parity(&k_full[s], (t / KST) & 1, a.err, ERR_K)) return false;
-        tc_fence_after();
-        const uint32_t q = smem_u32(smem + SM_Q) + (two ? w * T16 : 0);
-        const uint32_t k = smem_u32(smem + SM_K) + (r.tree ? 0 : s * T8);
-        if (r.tree) {
-#pragma unroll
+    // ------------------------------------------------------------ tcgen05.mma issue
+    if (items > 0) {
+      // every lane waits (and sees the same outcome): the warp stays converged for the elections
+      auto wait = [&](uint64_t* bar, int parity, int code) {
+        return __all_sync(0xffffffffu, wait_parity(bar, parity, a.err, code)) != 0;
+      };
+      const uint32_t tu = __shfl_sync(0xffffffffu, tb, 0);
+      const int n = __shfl_sync(0xffffffffu, items, 0);
+      const uint64_t dq = smem_desc_sw128(smem_u32(smem + SM_Q), 16, 1024);
+      const uint64_t dk = smem_desc_sw128(smem_u32(smem + SM_K), 16, 1024);
+      const uint64_t dv = smem_desc_sw128(smem_u32(smem + SM_W), T8, 1024);
+      bool ok = wait(&q_full, 0, ERR_Q);
+      if (r.tree) {
+        ok = ok && wait(&w_full[0], 0, ERR_W);  // K and V both
+        for (int w = 0; w < n && ok; ++w) {
+          tc_fence_after();
+#pragma unroll 1
           for (int ks = 0; ks < 8; ++ks) {
-            const uint32_t off = (ks >> 2) * T8 + (ks & 3) * 32;
-            mma_ss(tb + col_s(w), smem_desc_sw128(q + off, 16, 1024), smem_desc_sw128(k + off, 16, 1024), idesc(1, 0),
-                   ks > 0);
+            const uint64_t off = (ks >> 2) * (T8 >> 4) + (ks & 3) * 2;
+            mma_f16_ss(tu + col_s(w), dq + w * (T16 >> 4) + off, dk + off, idesc(1, 0), ks > 0);
           }
-        } else {
+          commit(&s_full[w]);
+        }
+        for (int w = 0; w < n && ok; ++w) {
+          ok = wait(&p_full[w], 0, ERR_P);
+          tc_fence_after();
+#pragma unroll 1
+          for (int ks = 0; ks < 8; ++ks) {  // hi 16 columns, lo 16
+            const uint32_t ac = tu + col_s(w) + (ks >> 1) * 32 + (ks & 1) * 8;
+            mma_f16_ts(tu + col_o(w), ac, dv + ks * 128, idesc(1, 1), ks > 0);
+            mma_f16_ts(tu + col_o(w), ac + 16, dv + ks * 128, idesc(1, 1), 1u);
+          }
+        }
+      } else {
+        auto qk = [&](int i) {
+          const int t = tile_of(i), w = i & 1, s = t % KST;
+          if (!wait(&k_full[s], (t / KST) & 1, ERR_K)) return false;
+          tc_fence_after();
+          const uint64_t q = dq + (two ? w * (T16 >> 4) : 0), k = dk + s * (T8 >> 4);
 #pragma unroll
           for (int term = 0; term < 2; ++term)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              mma_f8_ss(tb + col_s(w), smem_desc_sw128(q + term * T8 + ks * 32, 16, 1024),
-                        smem_desc_sw128(k + ks * 32, 16, 1024), idesc(0, 0), term + ks > 0);
-        }
-        mma_commit(&s_full[w]);
-        if (!r.tree && last_of(i)) mma_commit(&k_empty[s]);
-        return true;
-      };
-      auto pv = [&](int i) {
-        const int t = tile_of(i), w = i & 1;
-        if (!r.tree && !wait_parity(&w_full[t & 1], (t >> 1) & 1, a.err, ERR_W)) return false;
-        if (!wait_parity(&p_full[w], (i >> 1) & 1, a.err, ERR_P)) return false;
-        tc_fence_after();
-        const uint32_t v = smem_u32(smem + SM_W) + (t & 1) * T16;
-        const bool tw = r.tree || TERMS == 2;  // two terms: hi 16 columns, lo 16
-        const uint32_t id = idesc(r.tree ? 1 : 0, 1);
+              mma_f8_ss(tu + col_s(w), q + term * (T8 >> 4) + ks * 2, k + ks * 2, idesc(0, 0), term + ks > 0);
+          commit(&s_full[w]);
+          if (last_of(i)) commit(&k_empty[s]);
+          return true;
+        };
+        auto pv = [&](int i) {
+          const int t = tile_of(i), w = i & 1;
+          if (!wait(&w_full[t & 1], (t >> 1) & 1, ERR_W)) return false;
+          if (!wait(&p_full[w], (i >> 1) & 1, ERR_P)) return false;
+          tc_fence_after();
+          const uint64_t v = dv + (t & 1) * (T16 >> 4);
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          const uint64_t bd = smem_desc_sw128(v + ks * 2048, T8, 1024);
-          const uint32_t ac = tb + col_s(w) + (tw ? (ks >> 1) * 32 + (ks & 1) * 8 : ks * 8);
-          mma_ts(tb + col_o(w), ac, bd, id, (i >= 2 || ks > 0) ? 1u : 0u);
-          if (tw) mma_ts(tb + col_o(w), ac + 16, bd, id, 1u);
-        }
-        if (!r.tree && last_of(i)) mma_commit(&w_empty[t & 1]);
-        return true;
-      };
-      ok = ok && qk(0) && (items < 2 || qk(1));
-      for (int i = 0; i < items && ok; ++i) ok = pv(i) && (i + 2 >= items || qk(i + 2));
-      mma_commit(&o_full);
+          for (int ks = 0; ks < 8; ++ks) {
+            // two terms: hi 16 columns, lo 16
+            const uint32_t ac = tu + col_s(w) + (TERMS == 2 ? (ks >> 1) * 32 + (ks & 1) * 8 : ks * 8);
+            mma_f16_ts(tu + col_o(w), ac, v + ks * 128, idesc(0, 1), (i >= 2 || ks > 0) ? 1u : 0u);
+            if (TERMS == 2) mma_f16_ts(tu + col_o(w), ac + 16, v + ks * 128, idesc(0, 1), 1u);
+          }
+          if (last_of(i)) commit(&w_empty[t & 1]);
+          return true;
+        };
+        ok = ok && qk(0) && (n < 2 || qk(1));
+#pragma unroll 1
+        for (int i = 0; i < n && ok; ++i) ok = pv(i) && (i + 2 >= n || qk(i + 2));
+      }
+      commit(&o_full);
     }
-    __syncwarp();
   } else if (work) {
     // ------------------------------------------------------------ softmax
     const int w = warp >> 2, qd = warp & 3;
@@ -340,62 +407,66 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
     const int row = row0 + (two ? w * 128 : 0) + rl;
     const bool live = row < RG;
     const int node = live ? row / a.G : 0;
-    // Q: A every warpgroup stages its rows; B warpgroup 0 alone (the rows are the same), but
-    // both need the row factor
-    float qs = 1.f;
-    {
-      uint4 x[16];
-      const uint4* src = reinterpret_cast<const uint4*>(
-          a.q + ((static_cast<size_t>(b) * a.R + node) * a.Hq + h * a.G + (live ? row % a.G : 0)) * 128);
+    // Q: A every warpgroup stages its rows; B warpgroup 0 alone (the rows are the same).  Eight
+    // lanes take a row, 16 elements each, four rows of a warp at a time and four such in flight.
+    if (two || w == 0) {
+      uint8_t* dst = smem + SM_Q + w * T16;
+      const int c = lane & 7, sub = lane >> 3;
+#pragma unroll 1
+      for (int g = 0; g < 2; ++g) {
+        uint4 x[4][2];
 #pragma unroll
-      for (int c = 0; c < 16; ++c) x[c] = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-      uint8_t* dst = smem + SM_Q + (two ? w * T16 : 0) + rl * 128;
-      const bool put = two || w == 0;
-      if (r.tree) {
-        if (put)
-#pragma unroll
-          for (int c = 0; c < 16; ++c) *reinterpret_cast<uint4*>(dst + (c >> 3) * T8 + (((c & 7) ^ (rl & 7)) << 4)) = x[c];
-      } else {
-        float am = 0.f;
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const uint32_t u[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float f0 = fabsf(__uint_as_float(u[e] << 16)), f1 = fabsf(__uint_as_float(u[e] & 0xffff0000u));
-            am = fmaxf(am, fmaxf(f0 <= 3.402823466e38f ? f0 : 0.f, f1 <= 3.402823466e38f ? f1 : 0.f));
-          }
+        for (int e = 0; e < 4; ++e) {
+          const int qr = row0 + w * 128 + qd * 32 + g * 16 + e * 4 + sub;
+          const uint4* src = reinterpret_cast<const uint4*>(
+              a.q + ((static_cast<size_t>(b) * a.R + qr / a.G) * a.Hq + h * a.G + qr % a.G) * 128 + 16 * c);
+          x[e][0] = qr < RG ? __ldg(src) : make_uint4(0, 0, 0, 0);
+          x[e][1] = qr < RG ? __ldg(src + 1) : make_uint4(0, 0, 0, 0);
         }
-        // largest element in (224, 448]: the power of two of a cache block's scale
-        qs = kvq_scale(fmaxf(am, 0x1p-100f));
-        const float mul = 1.f / qs;
-        if (put) {
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t u[2] = {e < 2 ? (e == 0 ? x[2 * c].x : x[2 * c].z) : (e == 2 ? x[2 * c + 1].x : x[2 * c + 1].z),
-                                     e < 2 ? (e == 0 ? x[2 * c].y : x[2 * c].w) : (e == 2 ? x[2 * c + 1].y : x[2 * c + 1].w)};
-              hi[e] = lo[e] = 0u;
-#pragma unroll
-              for (int z = 0; z < 2; ++z) {
-                const float f0 = __uint_as_float(u[z] << 16) * mul, f1 = __uint_as_float(u[z] & 0xffff0000u) * mul;
-                const uint32_t c2 = kvq_code2(f0, f1);
-                const float2 back = kvq_float2(c2);
-                hi[e] |= c2 << (16 * z);
-                lo[e] |= kvq_code2(f0 - back.x, f1 - back.y) << (16 * z);
-              }
-            }
-            const int at = (c ^ (rl & 7)) << 4;
-            *reinterpret_cast<uint4*>(dst + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(dst + T8 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        for (int e = 0; e < 4; ++e) {
+          const int lr = qd * 32 + g * 16 + e * 4 + sub;
+          if (r.tree) {
+            uint8_t* d = dst + (c >> 2) * T8 + lr * 128;
+            *reinterpret_cast<uint4*>(d + (((2 * (c & 3)) ^ (lr & 7)) << 4)) = x[e][0];
+            *reinterpret_cast<uint4*>(d + (((2 * (c & 3) + 1) ^ (lr & 7)) << 4)) = x[e][1];
+            continue;
           }
+          const uint32_t u[8] = {x[e][0].x, x[e][0].y, x[e][0].z, x[e][0].w,
+                                 x[e][1].x, x[e][1].y, x[e][1].z, x[e][1].w};
+          uint32_t am = 0;  // the row's largest magnitude, as bf16 bits (ordered as integers)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) am = max(am, max((u[k] << 16) & 0x7fff0000u, u[k] & 0x7fff0000u));
+#pragma unroll
+          for (int o = 4; o > 0; o >>= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
+          // largest element in (224, 448]: the power of two of a cache block's scale; a row with
+          // an element that is not finite gets NaN scores
+          const float qs = kvq_scale(fmaxf(__uint_as_float(min(am, 0x7f7f0000u)), 0x1p-100f));
+          const float mul = 1.f / qs;
+          if (c == 0) s_q[w][lr] = am < 0x7f800000u ? qs : __uint_as_float(0x7fffffffu);
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            // exact as halves (bf16's 8 bits, magnitudes up to 448), and so is what hi leaves
+            const uint32_t q2 = half2_bits(__uint_as_float(u[k] << 16) * mul, __uint_as_float(u[k] & 0xffff0000u) * mul);
+            const uint32_t h8 = e4m3x2_of_half2(q2);
+            const uint32_t l8 = e4m3x2_of_half2(sub_half2(q2, kvq_half2(h8)));
+            hi[k >> 1] = (k & 1) ? hi[k >> 1] | (h8 << 16) : h8;
+            lo[k >> 1] = (k & 1) ? lo[k >> 1] | (l8 << 16) : l8;
+          }
+          uint8_t* d = dst + lr * 128 + ((c ^ (lr & 7)) << 4);
+          *reinterpret_cast<uint4*>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(d + T8) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full);
+    }
+    if (lane == 0) mbar_arrive(&q_full);
+    float qs = 1.f;
+    if (!r.tree) {
+      if (!two) bar_sync(1, 256);  // (A: the warp staged its own rows)
+      qs = s_q[two ? w : 0][rl];
     }
     // vref: the largest V scale of the piece
     const float* ks = a.ks + static_cast<size_t>(bh) * nblk + r.tile0 * (KT / kQB);
@@ -454,23 +525,25 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
       if (!ok) break;
       tc_fence_after();
       uint32_t x[32], y[32];
-      float mx[2];
-#pragma unroll
+      float top = -INFINITY;
+      // (the passes' loops stay rolled: with both halves of the tile written out the three roles'
+      // code no longer fits the instruction caches, and the product issue waits for its own)
+#pragma unroll 1
       for (int u = 0; u < 2; ++u) {
         tmem_ld32(sc + 64 * u, x);
         tmem_ld32(sc + 64 * u + 32, y);
         tmem_ld_wait();
         if (!full) {
+          const uint32_t b0 = u ? km[2] : km[0], b1 = u ? km[3] : km[1];
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
-            x[k] = (km[2 * u] >> k) & 1u ? x[k] : 0xff800000u;
-            y[k] = (km[2 * u + 1] >> k) & 1u ? y[k] : 0xff800000u;
+            x[k] = (b0 >> k) & 1u ? x[k] : 0xff800000u;
+            y[k] = (b1 >> k) & 1u ? y[k] : 0xff800000u;
           }
         }
-        mx[u] = fmaxf(max32(x), max32(y));
-        mx[u] = mx[u] == -INFINITY ? mx[u] : mx[u] * ck[u];
+        const float mx = fmaxf(max32(x), max32(y));
+        if (mx != -INFINITY) top = fmaxf(top, mx * (u ? ck[1] : ck[0]));
       }
-      const float top = fmaxf(mx[0], mx[1]);
       const bool up = top > m_ref + kLazy || (m_ref == -INFINITY && top > -INFINITY);
       const bool scale_o = up && m_ref != -INFINITY;
       const float m_new = up ? ceilf(top) : m_ref;
@@ -490,21 +563,22 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
       }
       m_ref = m_new;
       const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-#pragma unroll
+#pragma unroll 1
       for (int u = 0; u < 2; ++u) {
         tmem_ld32(sc + 64 * u, x);
         tmem_ld32(sc + 64 * u + 32, y);
         tmem_ld_wait();
-        const float off = lr[u] - mu;
+        const float cu = u ? ck[1] : ck[0], lu = u ? lr[1] : lr[0], off = lu - mu;
+        const uint32_t b0 = u ? km[2] : km[0], b1 = u ? km[3] : km[1];
+        const uint32_t c0 = sc + (TERMS == 2 ? 64 : 32) * u, c1 = c0 + (TERMS == 2 ? 32 : 16);
         float sum;
-        if (r.tree) {
-          sum = emit<2, true>(x, sc + 64 * u, ck[u], off, false, km[2 * u]);
-          sum += emit<2, true>(y, sc + 64 * u + 32, ck[u], off, false, km[2 * u + 1]);
-        } else {
-          sum = emit<TERMS, false>(x, sc + (TERMS == 2 ? 64 : 32) * u, ck[u], off, full, km[2 * u]);
-          sum += emit<TERMS, false>(y, sc + (TERMS == 2 ? 64 * u + 32 : 32 * u + 16), ck[u], off, full, km[2 * u + 1]);
-        }
-        l = fmaf(sum, ex2(-lr[u]), l);
+        if (full)
+          sum = emit<TERMS, false, true>(x, c0, cu, off, 0u) + emit<TERMS, false, true>(y, c1, cu, off, 0u);
+        else if (r.tree)
+          sum = emit<2, true, false>(x, sc + 64 * u, cu, off, b0) + emit<2, true, false>(y, sc + 64 * u + 32, cu, off, b1);
+        else
+          sum = emit<TERMS, false, false>(x, c0, cu, off, b0) + emit<TERMS, false, false>(y, c1, cu, off, b1);
+        l = fmaf(sum, ex2(-lu), l);
       }
       tmem_st_wait();
       tc_fence_before();
