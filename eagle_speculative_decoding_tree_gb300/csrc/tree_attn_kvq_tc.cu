@@ -7,16 +7,19 @@
 // e4m3 terms, q = hi + lo: four bits each hold bf16's eight exactly, down to elements of 2^-11
 // of the largest, and 2^-19 of it below.  Two products at twice the half rate cost what one
 // half product would, and K is never converted.  P V takes halves (11 bits in one term, against
-// the four of an e4m3 P): three warps widen each V tile from e4m3 to half, exactly, into a
+// the four of an e4m3 P): six warps widen each V tile from e4m3 to half, exactly, into a
 // second ring.  The scales stay outside as in tree_attn_kvq.cu: ks on the scores of its 64
 // keys, vs / vref in the exponent of P.
 //
-// One CTA per (piece, request x KV head, row block), 384 threads:
-//   warps 0-3, 4-7  softmax warpgroups; a thread owns one row (its TMEM lane) and reads a
-//                   tile's 128 scores twice: once for the maximum, once for the exponentials,
-//                   so it never holds more than 64 of them (168 registers a thread).
-//   warps 8-10      V widening; one lane of warp 8 refills the V ring, one of warp 9 the K ring.
-//   warp 11         issues every tcgen05.mma: QK0 QK1 | PV0 QK2 | PV1 QK3 | ...
+// One CTA per (piece, request x KV head, row block), 512 threads:
+//   warps 0-3, 4-7  softmax warpgroups; a thread owns one row (its TMEM lane) and a tile's 128
+//                   scores.  With one term of P it takes them in one pass: exponentials against
+//                   the row's reference as it stands, P in registers until the maximum has
+//                   confirmed the reference; else (first tiles, masked tiles, two terms) in two
+//                   passes, maximum first.
+//   warps 8-13      V widening.
+//   warp 14         TMA producer of the two code rings.
+//   warp 15         issues every tcgen05.mma: QK0 QK1 | PV0 QK2 | PV1 QK3 | ...
 // Items alternate between the warpgroups, so one tile's products run under the other's softmax.
 // With more than 128 rows (A) warpgroup w has rows 128 w .. and both take every tile: the
 // codes are read and widened once for 256 rows.  With fewer (B) both have the same rows and
@@ -46,11 +49,12 @@ constexpr int SM_K = SM_Q + 2 * T16;
 constexpr int SM_V = SM_K + KST * T8;
 constexpr int SM_W = SM_V + VST * T8;   // widened V, two stages
 constexpr int SMEM = SM_W + 2 * T16 + 1024;
-constexpr int NT = 384;
+constexpr int NT = 512;
+constexpr int WT = 192;                 // widening threads (six warps)
 constexpr float kLazy = 4.f;            // as in tree_attn_kvq.cu
 constexpr int PB = 11;
 
-enum : int { ERR_K = 1, ERR_KE = 2, ERR_V = 4, ERR_W = 8, ERR_WE = 16, ERR_S = 32, ERR_P = 64, ERR_O = 128, ERR_Q = 512 };
+enum : int { ERR_K = 1, ERR_KE = 2, ERR_V = 4, ERR_W = 8, ERR_WE = 16, ERR_S = 32, ERR_P = 64, ERR_O = 128, ERR_Q = 512, ERR_VE = 1024 };
 
 struct Maps {
   CUtensorMap k, v, po;
@@ -169,6 +173,23 @@ __device__ __forceinline__ float emit(const uint32_t (&r)[32], uint32_t col, flo
   return a0 + a1;
 }
 
+// 32 scores -> P as 16 packed halves, p = 2^(s c + o); returns the fp32 sum.
+__device__ __forceinline__ float to_half(const uint32_t (&r)[32], uint32_t (&p)[32], int at, float c, float o) {
+  const uint64_t c2 = f32x2(__float_as_uint(c), __float_as_uint(c)), o2 = f32x2(__float_as_uint(o), __float_as_uint(o));
+  uint64_t acc = 0ull;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    float x0, x1;
+    f32x2_split(fma_f32x2(f32x2(r[2 * j], r[2 * j + 1]), c2, o2), x0, x1);
+    const float p0 = ex2(x0), p1 = ex2(x1);
+    acc = add_f32x2(acc, f32x2(__float_as_uint(p0), __float_as_uint(p1)));
+    p[at + j] = half2_bits(p0, p1);
+  }
+  float a0, a1;
+  f32x2_split(acc, a0, a1);
+  return a0 + a1;
+}
+
 struct Range {
   int L, Rb, tile0, n;  // the piece's prefix tiles [tile0, tile0 + n); n = 1 for the tree
   bool tree;
@@ -178,7 +199,7 @@ template <int TERMS>
 __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_constant__ Maps tm, const KvqAttnArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t k_full[KST], k_empty[KST], v_full[VST], w_full[2], w_empty[2], s_full[2], p_full[2], q_full, o_full;
+  __shared__ uint64_t k_full[KST], k_empty[KST], v_full[VST], v_empty[VST], w_full[2], w_empty[2], s_full[2], p_full[2], q_full, o_full;
   __shared__ uint32_t tmem_base;
   __shared__ float s_q[2][128];  // the query rows' factors
   // row maxima and sums of the two warpgroups, exchanged in the epilogue (the widened V's area,
@@ -192,7 +213,7 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
   const bool two = a.wr == 2;            // A: two row tiles
   const int row0 = rb * (two ? 256 : 128);
 
-  if (warp == 11) {
+  if (warp == 15) {
     tmem_alloc(&tmem_base, 512);
     tmem_relinquish();
   }
@@ -201,9 +222,12 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
       mbar_init(&k_full[s], 1);
       mbar_init(&k_empty[s], 1);
     }
-    for (int s = 0; s < VST; ++s) mbar_init(&v_full[s], 1);
+    for (int s = 0; s < VST; ++s) {
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], WT / 32);
+    }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&w_full[s], 3);
+      mbar_init(&w_full[s], WT / 32);
       mbar_init(&w_empty[s], 1);
       mbar_init(&s_full[s], 1);
       mbar_init(&p_full[s], 128);
@@ -233,46 +257,58 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
   const uint32_t tb = tmem_base;
   const int nblk = (a.P + kQB - 1) / kQB;
 
-  if (warp >= 8 && warp < 11) {
-    // ------------------------------------------------------------ V widening, ring refills
-    if (work && !r.tree) {
-      const uint64_t policy = policy_evict_first();
-      const int y0 = bh * a.P + r.tile0 * KT;
-      const bool vload = warp == 8 && lane == 0, kload = warp == 9 && lane == 0;
-      auto load = [&](const CUtensorMap& m, int at, uint64_t* bar, int t) {
-        mbar_arrive_expect_tx(bar, T8);
-        tma_load_2d_hint(smem + at, &m, 0, y0 + t * KT, bar, policy);
-      };
-      if (kload)
-        for (int t = 0; t < min(KST, r.n); ++t) load(tm.k, SM_K + t * T8, &k_full[t], t);
-      if (vload)
-        for (int t = 0; t < min(VST, r.n); ++t) load(tm.v, SM_V + t * T8, &v_full[t], t);
-      int k_in = min(KST, r.n), v_in = min(VST, r.n);  // loads issued
-      bool ok = true;
-      const int id = threadIdx.x - 256;  // 0 .. 95
-      for (int t = 0; t < r.n && ok; ++t) {
-        const int s = t % VST, w = t & 1;
-        bool mine = wait_parity(&v_full[s], (t / VST) & 1, a.err, ERR_V);
-        if (mine && t >= 2) mine = wait_parity(&w_empty[w], ((t >> 1) - 1) & 1, a.err, ERR_WE);
-        ok = __all_sync(0xffffffffu, mine);
-        if (!ok) break;
-        const int nv = min(KT, r.L - (r.tile0 + t) * KT);
-        const uint8_t* src = smem + SM_V + s * T8;
-        uint8_t* dst = smem + SM_W + w * T16;
-        // 16 codes at a time; four loads in flight (the stores could alias them, so the order is
-        // written out)
-        for (int i0 = id; i0 < KT * 8; i0 += 4 * 96) {
-          uint4 u[4];
+  // registers: 128 a thread at launch (65536); the softmax takes 176 each, the others keep 80
+  // (256 x 176 + 256 x 80 = 65536)
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == 14) {
+      // ------------------------------------------------------------ TMA producer (lane 0)
+      if (lane == 0 && work && !r.tree) {
+        const uint64_t policy = policy_evict_first();
+        const int y0 = bh * a.P + r.tile0 * KT;
+        auto load = [&](const CUtensorMap& m, int at, uint64_t* bar, int t) {
+          mbar_arrive_expect_tx(bar, T8);
+          tma_load_2d_hint(smem + at, &m, 0, y0 + t * KT, bar, policy);
+        };
+        int k_in = 0, v_in = 0;  // loads issued
+        for (int t = 0; t < r.n; ++t) {
+          const int s = t % KST, sv = t % VST;
+          if (t >= KST && !wait_parity(&k_empty[s], (t / KST - 1) & 1, a.err, ERR_KE)) break;
+          load(tm.k, SM_K + s * T8, &k_full[s], t);
+          ++k_in;
+          if (t >= VST && !wait_parity(&v_empty[sv], (t / VST - 1) & 1, a.err, ERR_VE)) break;
+          load(tm.v, SM_V + sv * T8, &v_full[sv], t);
+          ++v_in;
+        }
+        // no copy may still be landing when the CTA ends
+        for (int s = 0; s < KST && s < k_in; ++s) (void)wait_parity(&k_full[s], ((k_in - 1 - s) / KST) & 1, a.err, ERR_K);
+        for (int s = 0; s < VST && s < v_in; ++s) (void)wait_parity(&v_full[s], ((v_in - 1 - s) / VST) & 1, a.err, ERR_V);
+      }
+    } else if (warp >= 8 && warp < 14) {
+      // ------------------------------------------------------------ V widening
+      const int id = threadIdx.x - 256;
+      if (work && !r.tree) {
+        for (int t = 0; t < r.n; ++t) {
+          const int s = t % VST, w = t & 1;
+          bool ok = wait_parity(&v_full[s], (t / VST) & 1, a.err, ERR_V);
+          if (ok && t >= 2) ok = wait_parity(&w_empty[w], ((t >> 1) - 1) & 1, a.err, ERR_WE);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          const int nv = min(KT, r.L - (r.tile0 + t) * KT);
+          const uint8_t* src = smem + SM_V + s * T8;
+          uint8_t* dst = smem + SM_W + w * T16;
+          // 16 codes at a time; all of a thread's loads first (the stores could alias them)
+          constexpr int N = (KT * 8 + WT - 1) / WT;
+          uint4 u[N];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int i = i0 + 96 * e, row = i & 127;
+          for (int e = 0; e < N; ++e) {
+            const int i = id + WT * e, row = i & 127;
             u[e] = make_uint4(0, 0, 0, 0);  // rows past the prefix: zeros, whatever they hold
             if (i < KT * 8 && row < nv)
               u[e] = *reinterpret_cast<const uint4*>(src + row * 128 + (((i >> 7) ^ (row & 7)) << 4));
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int i = i0 + 96 * e, row = i & 127, c = i >> 7, p = 2 * (c & 3);
+          for (int e = 0; e < N; ++e) {
+            const int i = id + WT * e, row = i & 127, c = i >> 7, p = 2 * (c & 3);
             if (i >= KT * 8) break;
             uint8_t* d = dst + (c >> 2) * T8 + row * 128;
             *reinterpret_cast<uint4*>(d + ((p ^ (row & 7)) << 4)) =
@@ -280,160 +316,146 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
             *reinterpret_cast<uint4*>(d + (((p + 1) ^ (row & 7)) << 4)) =
                 make_uint4(kvq_half2(u[e].z), kvq_half2(u[e].z >> 16), kvq_half2(u[e].w), kvq_half2(u[e].w >> 16));
           }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&w_full[w]);
+            mbar_arrive(&v_empty[s]);
+          }
+        }
+      } else if (work) {
+        // the tree's K and V tile as they are (bf16), zeros behind its rows
+        const uint16_t* kg = a.tk + static_cast<size_t>(bh) * a.R * 128;
+        const uint16_t* vg = a.tv + static_cast<size_t>(bh) * a.R * 128;
+#pragma unroll 2
+        for (int i = id; i < KT * 16; i += WT) {
+          const int row = i >> 4, c = i & 15;
+          uint4 x = make_uint4(0, 0, 0, 0), y = x;
+          if (row < r.Rb) {
+            x = __ldg(reinterpret_cast<const uint4*>(kg + static_cast<size_t>(row) * 128) + c);
+            y = __ldg(reinterpret_cast<const uint4*>(vg + static_cast<size_t>(row) * 128) + c);
+          }
+          const int at = (c >> 3) * T8 + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+          *reinterpret_cast<uint4*>(smem + SM_K + at) = x;
+          *reinterpret_cast<uint4*>(smem + SM_W + at) = y;
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&w_full[w]);
-        if (vload && v_in < r.n) {  // every widening warp is past stage s
-          if (wait_parity(&w_full[w], (t >> 1) & 1, a.err, ERR_W)) {
-            load(tm.v, SM_V + s * T8, &v_full[s], v_in);
-            ++v_in;
-          } else {
-            ok = false;
-          }
-        }
-        // K's stage of the tile before (its QK is done, or nearly: waiting for this tile's would
-        // hold the next widening back behind it)
-        if (kload && t > 0 && k_in < r.n) {
-          const int ps = (t - 1) % KST;
-          if (wait_parity(&k_empty[ps], ((t - 1) / KST) & 1, a.err, ERR_KE)) {
-            load(tm.k, SM_K + ps * T8, &k_full[ps], k_in);
-            ++k_in;
-          } else {
-            ok = false;
-          }
-        }
-        ok = __all_sync(0xffffffffu, ok);
+        if (lane == 0) mbar_arrive(&w_full[0]);
       }
-      // no copy may still be landing when the CTA ends
-      if (kload)
-        for (int s = 0; s < KST && s < k_in; ++s) (void)wait_parity(&k_full[s], ((k_in - 1 - s) / KST) & 1, a.err, ERR_K);
-      if (vload)
-        for (int s = 0; s < VST && s < v_in; ++s) (void)wait_parity(&v_full[s], ((v_in - 1 - s) / VST) & 1, a.err, ERR_V);
-    } else if (work) {
-      // the tree's K and V tile as they are (bf16), zeros behind its rows
-      const uint16_t* kg = a.tk + static_cast<size_t>(bh) * a.R * 128;
-      const uint16_t* vg = a.tv + static_cast<size_t>(bh) * a.R * 128;
-      for (int i = threadIdx.x - 256; i < KT * 16; i += 96) {
-        const int row = i >> 4, c = i & 15;
-        uint4 x = make_uint4(0, 0, 0, 0), y = x;
-        if (row < r.Rb) {
-          x = __ldg(reinterpret_cast<const uint4*>(kg + static_cast<size_t>(row) * 128) + c);
-          y = __ldg(reinterpret_cast<const uint4*>(vg + static_cast<size_t>(row) * 128) + c);
-        }
-        const int at = (c >> 3) * T8 + row * 128 + (((c & 7) ^ (row & 7)) << 4);
-        *reinterpret_cast<uint4*>(smem + SM_K + at) = x;
-        *reinterpret_cast<uint4*>(smem + SM_W + at) = y;
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&w_full[0]);
-    }
-  } else if (warp == 11) {
-    // ------------------------------------------------------------ tcgen05.mma issue
-    if (items > 0) {
-      // every lane waits (and sees the same outcome): the warp stays converged for the elections
-      auto wait = [&](uint64_t* bar, int parity, int code) {
-        return __all_sync(0xffffffffu, wait_parity(bar, parity, a.err, code)) != 0;
-      };
-      const uint32_t tu = __shfl_sync(0xffffffffu, tb, 0);
-      const int n = __shfl_sync(0xffffffffu, items, 0);
-      const uint64_t dq = smem_desc_sw128(smem_u32(smem + SM_Q), 16, 1024);
-      const uint64_t dk = smem_desc_sw128(smem_u32(smem + SM_K), 16, 1024);
-      const uint64_t dv = smem_desc_sw128(smem_u32(smem + SM_W), T8, 1024);
-      bool ok = wait(&q_full, 0, ERR_Q);
-      if (r.tree) {
-        ok = ok && wait(&w_full[0], 0, ERR_W);  // K and V both
-        for (int w = 0; w < n && ok; ++w) {
-          tc_fence_after();
-#pragma unroll 1
-          for (int ks = 0; ks < 8; ++ks) {
-            const uint64_t off = (ks >> 2) * (T8 >> 4) + (ks & 3) * 2;
-            mma_f16_ss(tu + col_s(w), dq + w * (T16 >> 4) + off, dk + off, idesc(1, 0), ks > 0);
-          }
-          commit(&s_full[w]);
-        }
-        for (int w = 0; w < n && ok; ++w) {
-          ok = wait(&p_full[w], 0, ERR_P);
-          tc_fence_after();
-#pragma unroll 1
-          for (int ks = 0; ks < 8; ++ks) {  // hi 16 columns, lo 16
-            const uint32_t ac = tu + col_s(w) + (ks >> 1) * 32 + (ks & 1) * 8;
-            mma_f16_ts(tu + col_o(w), ac, dv + ks * 128, idesc(1, 1), ks > 0);
-            mma_f16_ts(tu + col_o(w), ac + 16, dv + ks * 128, idesc(1, 1), 1u);
-          }
-        }
-      } else {
-        auto qk = [&](int i) {
-          const int t = tile_of(i), w = i & 1, s = t % KST;
-          if (!wait(&k_full[s], (t / KST) & 1, ERR_K)) return false;
-          tc_fence_after();
-          const uint64_t q = dq + (two ? w * (T16 >> 4) : 0), k = dk + s * (T8 >> 4);
-#pragma unroll
-          for (int term = 0; term < 2; ++term)
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              mma_f8_ss(tu + col_s(w), q + term * (T8 >> 4) + ks * 2, k + ks * 2, idesc(0, 0), term + ks > 0);
-          commit(&s_full[w]);
-          if (last_of(i)) commit(&k_empty[s]);
-          return true;
+    } else if (warp == 15) {
+      // ------------------------------------------------------------ tcgen05.mma issue
+      if (items > 0) {
+        // every lane waits (and sees the same outcome): the warp stays converged for the elections
+        auto wait = [&](uint64_t* bar, int parity, int code) {
+          return __all_sync(0xffffffffu, wait_parity(bar, parity, a.err, code)) != 0;
         };
-        auto pv = [&](int i) {
-          const int t = tile_of(i), w = i & 1;
-          if (!wait(&w_full[t & 1], (t >> 1) & 1, ERR_W)) return false;
-          if (!wait(&p_full[w], (i >> 1) & 1, ERR_P)) return false;
-          tc_fence_after();
-          const uint64_t v = dv + (t & 1) * (T16 >> 4);
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks) {
-            // two terms: hi 16 columns, lo 16
-            const uint32_t ac = tu + col_s(w) + (TERMS == 2 ? (ks >> 1) * 32 + (ks & 1) * 8 : ks * 8);
-            mma_f16_ts(tu + col_o(w), ac, v + ks * 128, idesc(0, 1), (i >= 2 || ks > 0) ? 1u : 0u);
-            if (TERMS == 2) mma_f16_ts(tu + col_o(w), ac + 16, v + ks * 128, idesc(0, 1), 1u);
+        const uint32_t tu = __shfl_sync(0xffffffffu, tb, 0);
+        const int n = __shfl_sync(0xffffffffu, items, 0);
+        const uint64_t dq = smem_desc_sw128(smem_u32(smem + SM_Q), 16, 1024);
+        const uint64_t dk = smem_desc_sw128(smem_u32(smem + SM_K), 16, 1024);
+        const uint64_t dv = smem_desc_sw128(smem_u32(smem + SM_W), T8, 1024);
+        bool ok = wait(&q_full, 0, ERR_Q);
+        if (r.tree) {
+          ok = ok && wait(&w_full[0], 0, ERR_W);  // K and V both
+          for (int w = 0; w < n && ok; ++w) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int ks = 0; ks < 8; ++ks) {
+              const uint64_t off = (ks >> 2) * (T8 >> 4) + (ks & 3) * 2;
+              mma_f16_ss(tu + col_s(w), dq + w * (T16 >> 4) + off, dk + off, idesc(1, 0), ks > 0);
+            }
+            commit(&s_full[w]);
           }
-          if (last_of(i)) commit(&w_empty[t & 1]);
-          return true;
-        };
-        ok = ok && qk(0) && (n < 2 || qk(1));
+          for (int w = 0; w < n && ok; ++w) {
+            ok = wait(&p_full[w], 0, ERR_P);
+            tc_fence_after();
 #pragma unroll 1
-        for (int i = 0; i < n && ok; ++i) ok = pv(i) && (i + 2 >= n || qk(i + 2));
-      }
-      commit(&o_full);
-    }
-  } else if (work) {
-    // ------------------------------------------------------------ softmax
-    const int w = warp >> 2, qd = warp & 3;
-    const int rl = qd * 32 + lane;  // TMEM lane, row of the warpgroup's tile
-    const int row = row0 + (two ? w * 128 : 0) + rl;
-    const bool live = row < RG;
-    const int node = live ? row / a.G : 0;
-    // Q: A every warpgroup stages its rows; B warpgroup 0 alone (the rows are the same).  Eight
-    // lanes take a row, 16 elements each, four rows of a warp at a time and four such in flight.
-    if (two || w == 0) {
-      uint8_t* dst = smem + SM_Q + w * T16;
-      const int c = lane & 7, sub = lane >> 3;
-#pragma unroll 1
-      for (int g = 0; g < 2; ++g) {
-        uint4 x[4][2];
+            for (int ks = 0; ks < 8; ++ks) {  // hi 16 columns, lo 16
+              const uint32_t ac = tu + col_s(w) + (ks >> 1) * 32 + (ks & 1) * 8;
+              mma_f16_ts(tu + col_o(w), ac, dv + ks * 128, idesc(1, 1), ks > 0);
+              mma_f16_ts(tu + col_o(w), ac + 16, dv + ks * 128, idesc(1, 1), 1u);
+            }
+          }
+        } else {
+          auto qk = [&](int i) {
+            const int t = tile_of(i), w = i & 1, s = t % KST;
+            if (!wait(&k_full[s], (t / KST) & 1, ERR_K)) return false;
+            tc_fence_after();
+            const uint64_t q = dq + (two ? w * (T16 >> 4) : 0), k = dk + s * (T8 >> 4);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int qr = row0 + w * 128 + qd * 32 + g * 16 + e * 4 + sub;
+            for (int term = 0; term < 2; ++term)
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                mma_f8_ss(tu + col_s(w), q + term * (T8 >> 4) + ks * 2, k + ks * 2, idesc(0, 0), term + ks > 0);
+            commit(&s_full[w]);
+            if (last_of(i)) commit(&k_empty[s]);
+            return true;
+          };
+          auto pv = [&](int i) {
+            const int t = tile_of(i), w = i & 1;
+            if (!wait(&w_full[t & 1], (t >> 1) & 1, ERR_W)) return false;
+            if (!wait(&p_full[w], (i >> 1) & 1, ERR_P)) return false;
+            tc_fence_after();
+            const uint64_t v = dv + (t & 1) * (T16 >> 4);
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+              // two terms: hi 16 columns, lo 16
+              const uint32_t ac = tu + col_s(w) + (TERMS == 2 ? (ks >> 1) * 32 + (ks & 1) * 8 : ks * 8);
+              mma_f16_ts(tu + col_o(w), ac, v + ks * 128, idesc(0, 1), (i >= 2 || ks > 0) ? 1u : 0u);
+              if (TERMS == 2) mma_f16_ts(tu + col_o(w), ac + 16, v + ks * 128, idesc(0, 1), 1u);
+            }
+            if (last_of(i)) commit(&w_empty[t & 1]);
+            return true;
+          };
+          ok = ok && qk(0) && (n < 2 || qk(1));
+#pragma unroll 1
+          for (int i = 0; i < n && ok; ++i) ok = pv(i) && (i + 2 >= n || qk(i + 2));
+        }
+        commit(&o_full);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    if (work) {
+      // ------------------------------------------------------------ softmax
+      const int w = warp >> 2, qd = warp & 3;
+      const int rl = qd * 32 + lane;  // TMEM lane, row of the warpgroup's tile
+      const int row = row0 + (two ? w * 128 : 0) + rl;
+      const bool live = row < RG;
+      const int node = live ? row / a.G : 0;
+      // Q: A every warpgroup stages its rows; B warpgroup 0 alone (the rows are the same).  Eight
+      // lanes take a row, 16 elements each, four rows of a warp at a time, two such loads ahead.
+      if (two || w == 0) {
+        uint8_t* dst = smem + SM_Q + w * T16;
+        const int c = lane & 7, sub = lane >> 3;
+        // (rolled: straight-line code that runs once costs its instruction fetches)
+        uint4 x[2], y[2];
+        auto fetch_q = [&](int e, uint4 (&t)[2]) {
+          const int qr = row0 + w * 128 + qd * 32 + e * 4 + sub;
           const uint4* src = reinterpret_cast<const uint4*>(
               a.q + ((static_cast<size_t>(b) * a.R + qr / a.G) * a.Hq + h * a.G + qr % a.G) * 128 + 16 * c);
-          x[e][0] = qr < RG ? __ldg(src) : make_uint4(0, 0, 0, 0);
-          x[e][1] = qr < RG ? __ldg(src + 1) : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int lr = qd * 32 + g * 16 + e * 4 + sub;
+          t[0] = t[1] = make_uint4(0, 0, 0, 0);
+          if (e < 8 && qr < RG) {
+            t[0] = __ldg(src);
+            t[1] = __ldg(src + 1);
+          }
+        };
+        fetch_q(0, x);
+        fetch_q(1, y);
+#pragma unroll 1
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t u[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+          x[0] = y[0];
+          x[1] = y[1];
+          fetch_q(e + 2, y);
+          const int lr = qd * 32 + e * 4 + sub;
           if (r.tree) {
             uint8_t* d = dst + (c >> 2) * T8 + lr * 128;
-            *reinterpret_cast<uint4*>(d + (((2 * (c & 3)) ^ (lr & 7)) << 4)) = x[e][0];
-            *reinterpret_cast<uint4*>(d + (((2 * (c & 3) + 1) ^ (lr & 7)) << 4)) = x[e][1];
+            *reinterpret_cast<uint4*>(d + (((2 * (c & 3)) ^ (lr & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+            *reinterpret_cast<uint4*>(d + (((2 * (c & 3) + 1) ^ (lr & 7)) << 4)) = make_uint4(u[4], u[5], u[6], u[7]);
             continue;
           }
-          const uint32_t u[8] = {x[e][0].x, x[e][0].y, x[e][0].z, x[e][0].w,
-                                 x[e][1].x, x[e][1].y, x[e][1].z, x[e][1].w};
           uint32_t am = 0;  // the row's largest magnitude, as bf16 bits (ordered as integers)
 #pragma unroll
           for (int k = 0; k < 8; ++k) am = max(am, max((u[k] << 16) & 0x7fff0000u, u[k] & 0x7fff0000u));
@@ -458,187 +480,219 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
           *reinterpret_cast<uint4*>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
           *reinterpret_cast<uint4*>(d + T8) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
+        fence_proxy_async_smem();
+        __syncwarp();
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-    }
-    if (lane == 0) mbar_arrive(&q_full);
-    float qs = 1.f;
-    if (!r.tree) {
-      if (!two) bar_sync(1, 256);  // (A: the warp staged its own rows)
-      qs = s_q[two ? w : 0][rl];
-    }
-    // vref: the largest V scale of the piece
-    const float* ks = a.ks + static_cast<size_t>(bh) * nblk + r.tile0 * (KT / kQB);
-    const float* vs = a.vs + static_cast<size_t>(bh) * nblk + r.tile0 * (KT / kQB);
-    int n_blk = 0;
-    float vref = 1.f;
-    if (!r.tree) {
-      n_blk = (min(r.L, (r.tile0 + r.n) * KT) + kQB - 1) / kQB - r.tile0 * (KT / kQB);
-      float m = 0.f;
-      for (int i = lane; i < n_blk; i += 32) m = fmaxf(m, __ldg(vs + i));
-      m = warp_max(m);
-      if (m > 0.f) vref = m;
-    }
-    const float vinv = 1.f / vref;
-    uint32_t tw[4] = {0u, 0u, 0u, 0u};  // the tree's visible keys
-    if (r.tree && live) {
-      const uint64_t* mp = a.anc_mask + (static_cast<size_t>(b) * a.R + node) * a.W;
-      const uint64_t w0 = mp[0], w1 = a.W > 1 ? mp[1] : 0ull;
-      tw[0] = static_cast<uint32_t>(w0) & low_bits(r.Rb);
-      tw[1] = static_cast<uint32_t>(w0 >> 32) & low_bits(r.Rb - 32);
-      tw[2] = static_cast<uint32_t>(w1) & low_bits(r.Rb - 64);
-      tw[3] = static_cast<uint32_t>(w1 >> 32) & low_bits(r.Rb - 96);
-    }
-    const float cr = a.scale_log2 * qs;
-    const uint32_t lb = tb + (static_cast<uint32_t>(qd * 32) << 16);
-    const uint32_t sc = lb + col_s(w), oc = lb + col_o(w);
-    float m_ref = -INFINITY, l = 0.f;
-    bool ok = true;
-    float kn[2] = {0.f, 0.f}, vn[2] = {0.f, 0.f};  // the next tile's scales
-    auto fetch = [&](int t) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int kb = min(2 * t + u, n_blk - 1);
-        kn[u] = __ldg(ks + kb);
-        vn[u] = __ldg(vs + kb);
-      }
-    };
-    if (!r.tree) fetch(min(tile_of(w), r.n - 1));
-    for (int i = w; i < items; i += 2) {
-      const int t = tile_of(i);
-      float ck[2] = {cr, cr}, lr[2] = {0.f, 0.f};
+      if (lane == 0) mbar_arrive(&q_full);
+      float qs = 1.f;
       if (!r.tree) {
+        if (!two) bar_sync(1, 256);  // (A: the warp staged its own rows)
+        qs = s_q[two ? w : 0][rl];
+      }
+      // vref: the largest V scale of the piece
+      const float* ks = a.ks + static_cast<size_t>(bh) * nblk + r.tile0 * (KT / kQB);
+      const float* vs = a.vs + static_cast<size_t>(bh) * nblk + r.tile0 * (KT / kQB);
+      int n_blk = 0;
+      float vref = 1.f;
+      if (!r.tree) {
+        n_blk = (min(r.L, (r.tile0 + r.n) * KT) + kQB - 1) / kQB - r.tile0 * (KT / kQB);
+        float m = 0.f;
+        for (int i = lane; i < n_blk; i += 32) m = fmaxf(m, __ldg(vs + i));
+        m = warp_max(m);
+        if (m > 0.f) vref = m;
+      }
+      const float vinv = 1.f / vref;
+      uint32_t tw[4] = {0u, 0u, 0u, 0u};  // the tree's visible keys
+      if (r.tree && live) {
+        const uint64_t* mp = a.anc_mask + (static_cast<size_t>(b) * a.R + node) * a.W;
+        const uint64_t w0 = mp[0], w1 = a.W > 1 ? mp[1] : 0ull;
+        tw[0] = static_cast<uint32_t>(w0) & low_bits(r.Rb);
+        tw[1] = static_cast<uint32_t>(w0 >> 32) & low_bits(r.Rb - 32);
+        tw[2] = static_cast<uint32_t>(w1) & low_bits(r.Rb - 64);
+        tw[3] = static_cast<uint32_t>(w1 >> 32) & low_bits(r.Rb - 96);
+      }
+      const float cr = a.scale_log2 * qs;
+      const uint32_t lb = tb + (static_cast<uint32_t>(qd * 32) << 16);
+      const uint32_t sc = lb + col_s(w), oc = lb + col_o(w);
+      float m_ref = -INFINITY, l = 0.f;
+      bool ok = true;
+      float kn[2] = {0.f, 0.f}, vn[2] = {0.f, 0.f};  // the next tile's scales
+      auto fetch = [&](int t) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          ck[u] = cr * kn[u];
-          lr[u] = fmaxf(__log2f(vn[u] * vinv), -100.f) + PB;
+          const int kb = min(2 * t + u, n_blk - 1);
+          kn[u] = __ldg(ks + kb);
+          vn[u] = __ldg(vs + kb);
         }
-        fetch(min(tile_of(i + 2), r.n - 1));
-      }
-      const int nv = r.tree ? 0 : min(KT, r.L - (r.tile0 + t) * KT);
-      uint32_t km[4];
+      };
+      if (!r.tree) fetch(min(tile_of(w), r.n - 1));
+      for (int i = w; i < items; i += 2) {
+        const int t = tile_of(i);
+        float ck[2] = {cr, cr}, lr[2] = {0.f, 0.f};
+        if (!r.tree) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) km[c] = r.tree ? tw[c] : low_bits(nv - 32 * c);
-      const bool full = !r.tree && nv == KT;
-      ok = __all_sync(0xffffffffu, wait_parity(&s_full[w], (i >> 1) & 1, a.err, ERR_S));
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t x[32], y[32];
-      float top = -INFINITY;
-      // (the passes' loops stay rolled: with both halves of the tile written out the three roles'
-      // code no longer fits the instruction caches, and the product issue waits for its own)
-#pragma unroll 1
-      for (int u = 0; u < 2; ++u) {
-        tmem_ld32(sc + 64 * u, x);
-        tmem_ld32(sc + 64 * u + 32, y);
-        tmem_ld_wait();
-        if (!full) {
-          const uint32_t b0 = u ? km[2] : km[0], b1 = u ? km[3] : km[1];
+          for (int u = 0; u < 2; ++u) {
+            ck[u] = cr * kn[u];
+            lr[u] = fmaxf(__log2f(vn[u] * vinv), -100.f) + PB;
+          }
+          fetch(min(tile_of(i + 2), r.n - 1));
+        }
+        const int nv = r.tree ? 0 : min(KT, r.L - (r.tile0 + t) * KT);
+        uint32_t km[4];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            x[k] = (b0 >> k) & 1u ? x[k] : 0xff800000u;
-            y[k] = (b1 >> k) & 1u ? y[k] : 0xff800000u;
+        for (int c = 0; c < 4; ++c) km[c] = r.tree ? tw[c] : low_bits(nv - 32 * c);
+        const bool full = !r.tree && nv == KT;
+        ok = __all_sync(0xffffffffu, wait_parity(&s_full[w], (i >> 1) & 1, a.err, ERR_S));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t x[32], y[32];
+        if (TERMS == 1 && full && i >= 2) {
+          // One pass: the exponentials against the reference as it stands, P held in registers
+          // until the maximum has confirmed it (nearly always, after the first tiles); otherwise
+          // S is still there for the two passes below.
+          uint32_t p0[32], p1[32];
+          const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+          tmem_ld32(sc, x);
+          tmem_ld32(sc + 32, y);
+          tmem_ld_wait();
+          float mx = max32(x);
+          float s0 = to_half(x, p0, 0, ck[0], lr[0] - mu);
+          tmem_ld32(sc + 64, x);
+          mx = fmaxf(mx, max32(y)) * ck[0];
+          s0 += to_half(y, p0, 16, ck[0], lr[0] - mu);
+          tmem_ld_wait();
+          tmem_ld32(sc + 96, y);
+          float mz = max32(x);
+          float s1 = to_half(x, p1, 0, ck[1], lr[1] - mu);
+          tmem_ld_wait();
+          mz = fmaxf(mz, max32(y)) * ck[1];
+          s1 += to_half(y, p1, 16, ck[1], lr[1] - mu);
+          const float top = fmaxf(mx, mz);
+          if (!__any_sync(0xffffffffu, !(top <= m_ref + kLazy))) {
+            tmem_st32(sc, p0);
+            tmem_st32(sc + 32, p1);
+            l = fmaf(s0, ex2(-lr[0]), fmaf(s1, ex2(-lr[1]), l));
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&p_full[w]);
+            continue;
           }
         }
-        const float mx = fmaxf(max32(x), max32(y));
-        if (mx != -INFINITY) top = fmaxf(top, mx * (u ? ck[1] : ck[0]));
-      }
-      const bool up = top > m_ref + kLazy || (m_ref == -INFINITY && top > -INFINITY);
-      const bool scale_o = up && m_ref != -INFINITY;
-      const float m_new = up ? ceilf(top) : m_ref;
-      if (__any_sync(0xffffffffu, scale_o)) {
-        // O of this warpgroup's earlier tiles: their PV finished before S of this one did
-        const float al = scale_o ? ex2(m_ref - m_new) : 1.f;
-        l *= al;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_ld32(oc + 32 * c, x);
+        float top = -INFINITY;
+        // (the passes' loops stay rolled: with both halves of the tile written out the three roles'
+        // code no longer fits the instruction caches, and the product issue waits for its own)
+#pragma unroll 1
+        for (int u = 0; u < 2; ++u) {
+          tmem_ld32(sc + 64 * u, x);
+          tmem_ld32(sc + 64 * u + 32, y);
           tmem_ld_wait();
+          if (!full) {
+            const uint32_t b0 = u ? km[2] : km[0], b1 = u ? km[3] : km[1];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * al);
-          tmem_st32(oc + 32 * c, x);
+            for (int k = 0; k < 32; ++k) {
+              x[k] = (b0 >> k) & 1u ? x[k] : 0xff800000u;
+              y[k] = (b1 >> k) & 1u ? y[k] : 0xff800000u;
+            }
+          }
+          const float mx = fmaxf(max32(x), max32(y));
+          if (mx != -INFINITY) top = fmaxf(top, mx * (u ? ck[1] : ck[0]));
+        }
+        const bool up = top > m_ref + kLazy || (m_ref == -INFINITY && top > -INFINITY);
+        const bool scale_o = up && m_ref != -INFINITY;
+        const float m_new = up ? ceilf(top) : m_ref;
+        if (__any_sync(0xffffffffu, scale_o)) {
+          // O of this warpgroup's earlier tiles: their PV finished before S of this one did
+          const float al = scale_o ? ex2(m_ref - m_new) : 1.f;
+          l *= al;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld32(oc + 32 * c, x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * al);
+            tmem_st32(oc + 32 * c, x);
+          }
+          tmem_st_wait();
+        }
+        m_ref = m_new;
+        const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+#pragma unroll 1
+        for (int u = 0; u < 2; ++u) {
+          tmem_ld32(sc + 64 * u, x);
+          tmem_ld32(sc + 64 * u + 32, y);
+          tmem_ld_wait();
+          const float cu = u ? ck[1] : ck[0], lu = u ? lr[1] : lr[0], off = lu - mu;
+          const uint32_t b0 = u ? km[2] : km[0], b1 = u ? km[3] : km[1];
+          const uint32_t c0 = sc + (TERMS == 2 ? 64 : 32) * u, c1 = c0 + (TERMS == 2 ? 32 : 16);
+          float sum;
+          if (full)
+            sum = emit<TERMS, false, true>(x, c0, cu, off, 0u) + emit<TERMS, false, true>(y, c1, cu, off, 0u);
+          else if (r.tree)
+            sum = emit<2, true, false>(x, sc + 64 * u, cu, off, b0) + emit<2, true, false>(y, sc + 64 * u + 32, cu, off, b1);
+          else
+            sum = emit<TERMS, false, false>(x, c0, cu, off, b0) + emit<TERMS, false, false>(y, c1, cu, off, b1);
+          l = fmaf(sum, ex2(-lu), l);
         }
         tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&p_full[w]);
       }
-      m_ref = m_new;
-      const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-#pragma unroll 1
-      for (int u = 0; u < 2; ++u) {
-        tmem_ld32(sc + 64 * u, x);
-        tmem_ld32(sc + 64 * u + 32, y);
-        tmem_ld_wait();
-        const float cu = u ? ck[1] : ck[0], lu = u ? lr[1] : lr[0], off = lu - mu;
-        const uint32_t b0 = u ? km[2] : km[0], b1 = u ? km[3] : km[1];
-        const uint32_t c0 = sc + (TERMS == 2 ? 64 : 32) * u, c1 = c0 + (TERMS == 2 ? 32 : 16);
-        float sum;
-        if (full)
-          sum = emit<TERMS, false, true>(x, c0, cu, off, 0u) + emit<TERMS, false, true>(y, c1, cu, off, 0u);
-        else if (r.tree)
-          sum = emit<2, true, false>(x, sc + 64 * u, cu, off, b0) + emit<2, true, false>(y, sc + 64 * u + 32, cu, off, b1);
-        else
-          sum = emit<TERMS, false, false>(x, c0, cu, off, b0) + emit<TERMS, false, false>(y, c1, cu, off, b1);
-        l = fmaf(sum, ex2(-lu), l);
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(&p_full[w]);
-    }
-    // ---- epilogue: partial rows (A: 128 dims of the own row; B: 64 dims of the merged row)
-    ok = __all_sync(0xffffffffu, ok && wait_parity(&o_full, 0, a.err, ERR_O));
-    tc_fence_after();
-    s_m[w][rl] = m_ref;
-    s_l[w][rl] = l;
-    ok = bar_and(1, 256, ok);
-    if (ok) {
-      const float unit = r.tree ? 1.f : vref * (1.f / (1 << PB));
-      float M = m_ref, Lsum = l, fa = unit, fb = 0.f;
-      const bool other = !two && items > 1;
-      if (!two) {
-        const float m0 = s_m[0][rl], m1 = s_m[1][rl];
-        M = fmaxf(m0, m1);
-        fa = m0 == -INFINITY ? 0.f : ex2(m0 - M);
-        fb = m1 == -INFINITY ? 0.f : ex2(m1 - M);
-        Lsum = fa * s_l[0][rl] + fb * s_l[1][rl];
-        fa *= unit;
-        fb *= unit;
-      }
-      // slices of 32 dims staged as 128-byte-swizzled rows over the Q area and both code
-      // rings (every product has finished), then one TMA store each
-      for (int c = two ? 0 : 2 * w; c < (two ? 4 : 2 * w + 2); ++c) {
-        uint32_t x[32], y[32];
-        tmem_ld32(lb + col_o(two ? w : 0) + 32 * c, x);
-        if (other) tmem_ld32(lb + col_o(1) + 32 * c, y);
-        tmem_ld_wait();
-        uint8_t* dst = smem + ((two ? 4 * w : 0) + c) * T8 + rl * 128;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          float f[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            f[e] = __uint_as_float(x[4 * q + e]) * fa;
-            if (other) f[e] = fmaf(__uint_as_float(y[4 * q + e]), fb, f[e]);
-          }
-          *reinterpret_cast<float4*>(dst + ((q ^ (rl & 7)) << 4)) = make_float4(f[0], f[1], f[2], f[3]);
+      // ---- epilogue: partial rows (A: 128 dims of the own row; B: 64 dims of the merged row)
+      ok = __all_sync(0xffffffffu, ok && wait_parity(&o_full, 0, a.err, ERR_O));
+      tc_fence_after();
+      s_m[w][rl] = m_ref;
+      s_l[w][rl] = l;
+      ok = bar_and(1, 256, ok);
+      if (ok) {
+        const float unit = r.tree ? 1.f : vref * (1.f / (1 << PB));
+        float M = m_ref, Lsum = l, fa = unit, fb = 0.f;
+        const bool other = !two && items > 1;
+        if (!two) {
+          const float m0 = s_m[0][rl], m1 = s_m[1][rl];
+          M = fmaxf(m0, m1);
+          fa = m0 == -INFINITY ? 0.f : ex2(m0 - M);
+          fb = m1 == -INFINITY ? 0.f : ex2(m1 - M);
+          Lsum = fa * s_l[0][rl] + fb * s_l[1][rl];
+          fa *= unit;
+          fb *= unit;
         }
-      }
-      const size_t prow = (static_cast<size_t>(bh) * a.splits + piece) * a.rows_pad + row0;
-      if (live && (two || w == 0))
-        *reinterpret_cast<float2*>(a.part_ml + (prow + (two ? w * 128 : 0) + rl) * 2) = make_float2(M, Lsum);
-      fence_proxy_async_smem();
-      bar_sync(2 + (two ? w : 0), two ? 128 : 256);
-      if (qd == 0 && lane == 0 && (two || w == 0)) {
-        for (int c = 0; c < 4; ++c)
-          tma_store_2d(&tm.po, smem + ((two ? 4 * w : 0) + c) * T8, 32 * c,
-                       static_cast<int>(prow) + (two ? w * 128 : 0));
-        bulk_commit();
-        bulk_wait_read0();  // the combine kernel reads the rows once this grid has completed
+        // slices of 32 dims staged as 128-byte-swizzled rows over the Q area and both code
+        // rings (every product has finished), then one TMA store each
+        for (int c = two ? 0 : 2 * w; c < (two ? 4 : 2 * w + 2); ++c) {
+          uint32_t x[32], y[32];
+          tmem_ld32(lb + col_o(two ? w : 0) + 32 * c, x);
+          if (other) tmem_ld32(lb + col_o(1) + 32 * c, y);
+          tmem_ld_wait();
+          uint8_t* dst = smem + ((two ? 4 * w : 0) + c) * T8 + rl * 128;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            float f[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              f[e] = __uint_as_float(x[4 * q + e]) * fa;
+              if (other) f[e] = fmaf(__uint_as_float(y[4 * q + e]), fb, f[e]);
+            }
+            *reinterpret_cast<float4*>(dst + ((q ^ (rl & 7)) << 4)) = make_float4(f[0], f[1], f[2], f[3]);
+          }
+        }
+        const size_t prow = (static_cast<size_t>(bh) * a.splits + piece) * a.rows_pad + row0;
+        if (live && (two || w == 0))
+          *reinterpret_cast<float2*>(a.part_ml + (prow + (two ? w * 128 : 0) + rl) * 2) = make_float2(M, Lsum);
+        fence_proxy_async_smem();
+        bar_sync(2 + (two ? w : 0), two ? 128 : 256);
+        if (qd == 0 && lane == 0 && (two || w == 0)) {
+          for (int c = 0; c < 4; ++c)
+            tma_store_2d(&tm.po, smem + ((two ? 4 * w : 0) + c) * T8, 32 * c,
+                         static_cast<int>(prow) + (two ? w * 128 : 0));
+          bulk_commit();
+          bulk_wait_read0();  // the combine kernel reads the rows once this grid has completed
+        }
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 11) {
+  if (warp == 15) {
     tc_fence_after();
     tmem_dealloc(tb, 512);
   }
