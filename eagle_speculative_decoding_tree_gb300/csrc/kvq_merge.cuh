@@ -1,0 +1,67 @@
+// kvq_merge.cuh -- merging a row's partial states (tree attention over the 8-bit cache).
+#pragma once
+
+#include "common.cuh"
+#include "launch.h"
+#include "sm100.cuh"
+
+namespace eagle {
+
+// Partial rows come through L2 (other SMs wrote them); volatile, so that the loads of a batch
+// stay ahead of everything that uses them.
+__device__ __forceinline__ void ld_part(const float* p, float (&x)[4]) {
+  asm volatile("ld.global.cg.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "l"(p));
+}
+__device__ __forceinline__ void ld_part(const float* p, float (&x)[2]) {
+  asm volatile("ld.global.cg.v2.f32 {%0,%1}, [%2];" : "=f"(x[0]), "=f"(x[1]) : "l"(p));
+}
+
+// One warp: M = max m_s, out = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s over partials s < n at
+// rows base + s rows_pad; D / 32 dims per lane, lane s holds piece s's weight.  BATCH partial rows
+// are in flight together (up to 32 pieces a round).  A row with no key gets zeros and lse -inf.
+template <int D, int BATCH>
+__device__ __forceinline__ void kvq_merge_row(const KvqAttnArgs& a, size_t base, int n, size_t orow, int lane) {
+  constexpr int PER = D / 32;
+  const float* po = a.part_o + base * D + lane * PER;
+  const size_t step = static_cast<size_t>(a.rows_pad);
+  float M = -INFINITY, lsum = 0.f, acc[PER];
+#pragma unroll
+  for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+#pragma unroll 1
+  for (int s0 = 0; s0 < n; s0 += BATCH) {
+    float x[BATCH][PER];
+    const int mine = s0 + lane;
+    float ml[2] = {-INFINITY, 0.f};
+    if (lane < BATCH && mine < n) ld_part(a.part_ml + (base + static_cast<size_t>(mine) * step) * 2, ml);
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) ld_part(po + static_cast<size_t>(min(s0 + u, n - 1)) * step * D, x[u]);
+    const float top = fmaxf(M, warp_max(ml[0]));
+    const float old = M == -INFINITY ? 0.f : sm100::ex2(M - top);
+    const float f = ml[0] == -INFINITY ? 0.f : sm100::ex2(ml[0] - top);
+    M = top;
+    lsum = fmaf(lsum, old, warp_sum(f * ml[1]));  // (0 * NaN keeps a poisoned row poisoned)
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] *= old;
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) {
+      // no branch on the weight: the loads would sink into it, one after the other
+      const float g = __shfl_sync(0xffffffffu, f, u);
+#pragma unroll
+      for (int e = 0; e < PER; ++e) acc[e] = fmaf(g, x[u][e], acc[e]);
+    }
+  }
+  const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+  const size_t at = orow * D + lane * PER;
+#pragma unroll
+  for (int e = 0; e < PER; e += 2) {
+    if (a.out_f32) {
+      *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at + e) = make_float2(acc[e] * inv, acc[e + 1] * inv);
+    } else {
+      const __nv_bfloat162 t = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
+      *reinterpret_cast<__nv_bfloat162*>(static_cast<uint16_t*>(a.out) + at + e) = t;
+    }
+  }
+  if (a.lse && lane == 0) a.lse[orow] = (M + log2f(lsum)) * 0.69314718055994531f;
+}
+
+}  // namespace eagle

@@ -174,7 +174,8 @@ struct KvqAttnPlan {
   int splits, tps;  // mma.sync: split s takes 128-key units [s tps, (s + 1) tps) of its request, the
                     // tree being the last; tcgen05: piece 0 is the tree, piece s the prefix tiles
                     // [(s - 1) tps, s tps)
-  size_t off_err, off_o, off_ml, total;
+  bool coop;        // tcgen05: the whole grid fits on the SMs, pieces merge in the kernel
+  size_t off_err, off_cnt, off_o, off_ml, total;
 };
 void plan_kvq_attn(const eagle_attn_desc* d, int num_sms, KvqAttnPlan* p);
 struct KvqAttnArgs {
@@ -193,7 +194,9 @@ struct KvqAttnArgs {
   float* part_o;   // [B*Hkv][splits][rows_pad][D]
   float* part_ml;  // [B*Hkv][splits][rows_pad][2]: max in log2 units, sum
   int* err;
-  int B, R, Hq, Hkv, G, P, W, splits, tps, rows_pad, out_f32, wr, tc;
+  int* cnt;        // coop: [groups][2] published / finished pieces, zero between calls
+  int B, R, Hq, Hkv, G, P, W, splits, tps, rows_pad, out_f32, wr, tc, coop;
+  uint32_t g_inv;  // ceil(2^32 / G) for G > 1
   float scale, scale_log2;
 };
 cudaError_t launch_kvq_attn_tc(const KvqAttnPlan& p, const KvqAttnArgs& a, cudaStream_t s);

@@ -31,6 +31,7 @@
 
 #include "common.cuh"
 #include "kvq.cuh"
+#include "kvq_merge.cuh"
 #include "launch.h"
 #include "sm100.cuh"
 #include "tmap.h"
@@ -544,11 +545,9 @@ __global__ void __launch_bounds__(CW * 32, 1)
   }
 }
 
-// Merge the splits of a row: M = max m_s, out = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s.
-// A warp per row, D / 32 dims per lane, the partial rows of eight splits in flight.
+// Merge the splits of every row, a warp per row.
 template <int D>
 __global__ void __launch_bounds__(128) kvq_combine_kernel(const KvqAttnArgs a) {
-  constexpr int PER = D / 32;
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -557,48 +556,8 @@ __global__ void __launch_bounds__(128) kvq_combine_kernel(const KvqAttnArgs a) {
   if (r >= tree_rows(a, b) * a.G) return;
   const int tiles = (prefix_len(a, b) + KT - 1) / KT;
   const int n = min(a.splits, a.tc ? 1 + (tiles + a.tps - 1) / a.tps : (tiles + a.tps) / a.tps);
-  const size_t base = static_cast<size_t>(bh) * a.splits * a.rows_pad + r;
-  float M = -INFINITY;
-  for (int s = lane; s < n; s += 32) M = fmaxf(M, a.part_ml[(base + static_cast<size_t>(s) * a.rows_pad) * 2]);
-  M = warp_max(M);
-  float acc[PER], lsum = 0.f;
-#pragma unroll
-  for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-  for (int s0 = 0; s0 < n; s0 += 8) {
-    float x[8][PER];
-    float2 ml[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const size_t at = base + static_cast<size_t>(min(s0 + u, n - 1)) * a.rows_pad;
-      ml[u] = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
-#pragma unroll
-      for (int e = 0; e < PER; e += 2) {
-        const float2 t = *reinterpret_cast<const float2*>(a.part_o + at * D + lane * PER + e);
-        x[u][e] = t.x;
-        x[u][e + 1] = t.y;
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      if (s0 + u >= n) continue;
-      const float f = ml[u].x == -INFINITY ? 0.f : ex2(ml[u].x - M);
-      lsum = fmaf(f, ml[u].y, lsum);
-      if (f == 0.f) continue;
-#pragma unroll
-      for (int e = 0; e < PER; ++e) acc[e] = fmaf(f, x[u][e], acc[e]);
-    }
-  }
-  const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
-  const size_t orow = (static_cast<size_t>(b) * a.R + r / a.G) * a.Hq + h * a.G + r % a.G;
-#pragma unroll
-  for (int e = 0; e < PER; e += 2) {
-    const size_t at = orow * D + lane * PER + e;
-    if (a.out_f32)
-      *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at) = make_float2(acc[e] * inv, acc[e + 1] * inv);
-    else
-      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at) = pack_bf(acc[e] * inv, acc[e + 1] * inv);
-  }
-  if (a.lse && lane == 0) a.lse[orow] = (M + log2f(lsum)) * 0.69314718055994531f;
+  kvq_merge_row<D, 16>(a, static_cast<size_t>(bh) * a.splits * a.rows_pad + r, n,
+                       (static_cast<size_t>(b) * a.R + r / a.G) * a.Hq + h * a.G + r % a.G, lane);
 }
 
 template <int D>
@@ -663,7 +622,8 @@ void plan_kvq_attn(const eagle_attn_desc* d, int num_sms, KvqAttnPlan* p) {
   const int RG = p->R * p->G;
   const int tiles = (p->P + KT - 1) / KT;
   // the tcgen05 kernel's row tiles are 128 rows whether or not they are filled
-  p->tc = d->engine == EAGLE_ENGINE_AUTO && p->D == 128 && RG > 32;
+  p->tc = d->engine == EAGLE_ENGINE_AUTO && p->D == 128 && RG > 32 && p->G <= 4096;
+  p->coop = false;
   if (p->tc) {
     p->mt = 0;
     p->wr = RG > 128 ? 2 : 1;
@@ -677,6 +637,7 @@ void plan_kvq_attn(const eagle_attn_desc* d, int num_sms, KvqAttnPlan* p) {
     pieces = std::min<long long>(std::min<long long>(pieces, tiles), 255);
     p->tps = static_cast<int>((tiles + pieces - 1) / pieces);
     p->splits = (tiles + p->tps - 1) / p->tps + 1;
+    p->coop = base * p->splits <= num_sms;
   } else {
     // rows of a CTA: as few warps along the rows as cover them, up to 8 x 32
     p->mt = RG <= 16 ? 1 : 2;
@@ -696,6 +657,8 @@ void plan_kvq_attn(const eagle_attn_desc* d, int num_sms, KvqAttnPlan* p) {
   p->rows_pad = p->row_blocks * p->rows_per_cta;
   p->off_err = 0;
   size_t off = 256;
+  p->off_cnt = off;
+  if (p->coop) off += (static_cast<size_t>(p->B) * p->Hkv * p->row_blocks * 8 + 255) / 256 * 256;
   p->off_o = p->off_ml = 0;
   if (p->splits > 1) {
     const size_t rows = static_cast<size_t>(p->B) * p->Hkv * p->splits * p->rows_pad;
@@ -728,6 +691,8 @@ cudaError_t launch_kvq_attn(const KvqAttnPlan& p, const void* q, const void* k8,
   a.part_o = reinterpret_cast<float*>(w + p.off_o);
   a.part_ml = reinterpret_cast<float*>(w + p.off_ml);
   a.err = reinterpret_cast<int*>(w + p.off_err);
+  a.cnt = reinterpret_cast<int*>(w + p.off_cnt);
+  a.coop = p.coop ? 1 : 0;
   a.B = p.B;
   a.R = p.R;
   a.Hq = p.Hq;
@@ -741,11 +706,12 @@ cudaError_t launch_kvq_attn(const KvqAttnPlan& p, const void* q, const void* k8,
   a.out_f32 = p.out_f32;
   a.wr = p.wr;
   a.tc = p.tc ? 1 : 0;
+  a.g_inv = p.G > 1 ? static_cast<uint32_t>(((1ull << 32) + p.G - 1) / p.G) : 0u;
   a.scale = p.scale;
   a.scale_log2 = p.scale * kLog2e;
   if (p.tc) {
     const cudaError_t e = launch_kvq_attn_tc(p, a, s);
-    return e != cudaSuccess ? e : launch_combine<128>(p, a, s);
+    return e != cudaSuccess || p.coop ? e : launch_combine<128>(p, a, s);
   }
   Maps tm;
   const unsigned long long rows = static_cast<unsigned long long>(p.B) * p.Hkv * p.P;

@@ -27,10 +27,12 @@
 // TMEM: S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512); P overwrites S in place.
 //
 // Piece 0 is the tree itself (bf16 Q, K, V and P in two bf16 terms, one tile); the others are
-// tps 128-key tiles of the prefix.  Pieces write fp32 partials (TMA stores) that
-// kvq_combine_kernel merges.
+// tps 128-key tiles of the prefix.  Pieces write fp32 partials (TMA stores).  When the whole
+// grid fits on the SMs the launch is cooperative and the pieces of a group merge their rows in
+// the kernel (a second launch costs several microseconds); otherwise kvq_combine_kernel does.
 #include "common.cuh"
 #include "kvq.cuh"
+#include "kvq_merge.cuh"
 #include "launch.h"
 #include "sm100.cuh"
 #include "tmap.h"
@@ -54,7 +56,8 @@ constexpr int WT = 192;                 // widening threads (six warps)
 constexpr float kLazy = 4.f;            // as in tree_attn_kvq.cu
 constexpr int PB = 11;
 
-enum : int { ERR_K = 1, ERR_KE = 2, ERR_V = 4, ERR_W = 8, ERR_WE = 16, ERR_S = 32, ERR_P = 64, ERR_O = 128, ERR_Q = 512, ERR_VE = 1024 };
+enum : int { ERR_K = 1, ERR_KE = 2, ERR_V = 4, ERR_W = 8, ERR_WE = 16, ERR_S = 32, ERR_P = 64, ERR_O = 128, ERR_GROUP = 256, ERR_Q = 512,
+             ERR_VE = 1024 };
 
 struct Maps {
   CUtensorMap k, v, po;
@@ -190,6 +193,12 @@ __device__ __forceinline__ float to_half(const uint32_t (&r)[32], uint32_t (&p)[
   return a0 + a1;
 }
 
+// row / G for row < 2^16: a multiplication by ceil(2^32 / G) (a division costs as much as the
+// rest of a row's staging).
+__device__ __forceinline__ int node_of(const KvqAttnArgs& a, int row) {
+  return a.G == 1 ? row : static_cast<int>(__umulhi(static_cast<uint32_t>(row), a.g_inv));
+}
+
 struct Range {
   int L, Rb, tile0, n;  // the piece's prefix tiles [tile0, tile0 + n); n = 1 for the tree
   bool tree;
@@ -201,6 +210,7 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t k_full[KST], k_empty[KST], v_full[VST], v_empty[VST], w_full[2], w_empty[2], s_full[2], p_full[2], q_full, o_full;
   __shared__ uint32_t tmem_base;
+  __shared__ int go;             // group merge: every piece counted in time
   __shared__ float s_q[2][128];  // the query rows' factors
   // row maxima and sums of the two warpgroups, exchanged in the epilogue (the widened V's area,
   // free by then)
@@ -279,6 +289,9 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
           if (t >= VST && !wait_parity(&v_empty[sv], (t / VST - 1) & 1, a.err, ERR_VE)) break;
           load(tm.v, SM_V + sv * T8, &v_full[sv], t);
           ++v_in;
+          // the first tile first: with the whole ring's loads ahead of it the query tile would
+          // arrive last, and nothing can start without it
+          if (t == 0 && !wait_parity(&q_full, 0, a.err, ERR_Q)) break;
         }
         // no copy may still be landing when the CTA ends
         for (int s = 0; s < KST && s < k_in; ++s) (void)wait_parity(&k_full[s], ((k_in - 1 - s) / KST) & 1, a.err, ERR_K);
@@ -423,39 +436,35 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
       const int rl = qd * 32 + lane;  // TMEM lane, row of the warpgroup's tile
       const int row = row0 + (two ? w * 128 : 0) + rl;
       const bool live = row < RG;
-      const int node = live ? row / a.G : 0;
+      const int node = live ? node_of(a, row) : 0;
       // Q: A every warpgroup stages its rows; B warpgroup 0 alone (the rows are the same).  Eight
-      // lanes take a row, 16 elements each, four rows of a warp at a time, two such loads ahead.
+      // lanes take a row.
       if (two || w == 0) {
         uint8_t* dst = smem + SM_Q + w * T16;
         const int c = lane & 7, sub = lane >> 3;
-        // (rolled: straight-line code that runs once costs its instruction fetches)
-        uint4 x[2], y[2];
-        auto fetch_q = [&](int e, uint4 (&t)[2]) {
-          const int qr = row0 + w * 128 + qd * 32 + e * 4 + sub;
-          const uint4* src = reinterpret_cast<const uint4*>(
-              a.q + ((static_cast<size_t>(b) * a.R + qr / a.G) * a.Hq + h * a.G + qr % a.G) * 128 + 16 * c);
-          t[0] = t[1] = make_uint4(0, 0, 0, 0);
-          if (e < 8 && qr < RG) {
-            t[0] = __ldg(src);
-            t[1] = __ldg(src + 1);
-          }
-        };
-        fetch_q(0, x);
-        fetch_q(1, y);
+        // All copies are asynchronous, the whole tile in flight, 128 bytes of a row by its eight
+        // lanes: dims 8 c .. and 64 + 8 c .. in swizzled rows of 64 bf16 dims.  That is the tree's
+        // final form; a prefix piece's codes (128 to a row) then replace them in place.
+        // (Loops rolled: straight-line code that runs once costs its instruction fetches.)
+        const uint32_t d0 = smem_u32(dst);
 #pragma unroll 1
         for (int e = 0; e < 8; ++e) {
-          const uint32_t u[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
-          x[0] = y[0];
-          x[1] = y[1];
-          fetch_q(e + 2, y);
+          const int lr = qd * 32 + e * 4 + sub, qr = row0 + w * 128 + lr;
+          const int nd = node_of(a, qr), n16 = qr < RG ? 16 : 0;  // 0: zero fill, nothing read
+          const uint16_t* src =
+              n16 ? a.q + ((static_cast<size_t>(b) * a.R + nd) * a.Hq + h * a.G + (qr - nd * a.G)) * 128 + 8 * c : a.q;
+          const uint32_t at = d0 + lr * 128 + ((c ^ (lr & 7)) << 4);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(src), "r"(n16) : "memory");
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at + T8), "l"(src + 64), "r"(n16) : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+#pragma unroll 2
+        for (int e = 0; e < 8 && !r.tree; ++e) {
           const int lr = qd * 32 + e * 4 + sub;
-          if (r.tree) {
-            uint8_t* d = dst + (c >> 2) * T8 + lr * 128;
-            *reinterpret_cast<uint4*>(d + (((2 * (c & 3)) ^ (lr & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
-            *reinterpret_cast<uint4*>(d + (((2 * (c & 3) + 1) ^ (lr & 7)) << 4)) = make_uint4(u[4], u[5], u[6], u[7]);
-            continue;
-          }
+          const uint8_t* d = dst + lr * 128 + ((c ^ (lr & 7)) << 4);
+          const uint4 x0 = *reinterpret_cast<const uint4*>(d), x1 = *reinterpret_cast<const uint4*>(d + T8);
+          const uint32_t u[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
           uint32_t am = 0;  // the row's largest magnitude, as bf16 bits (ordered as integers)
 #pragma unroll
           for (int k = 0; k < 8; ++k) am = max(am, max((u[k] << 16) & 0x7fff0000u, u[k] & 0x7fff0000u));
@@ -464,9 +473,9 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
           // largest element in (224, 448]: the power of two of a cache block's scale; a row with
           // an element that is not finite gets NaN scores
           const float qs = kvq_scale(fmaxf(__uint_as_float(min(am, 0x7f7f0000u)), 0x1p-100f));
-          const float mul = 1.f / qs;
+          const float mul = __uint_as_float((254u << 23) - __float_as_uint(qs));  // 1 / qs, a power of two
           if (c == 0) s_q[w][lr] = am < 0x7f800000u ? qs : __uint_as_float(0x7fffffffu);
-          uint32_t hi[4], lo[4];
+          uint32_t hi[4], lo[4];  // words 0, 1: dims 8 c ..; 2, 3: dims 64 + 8 c ..
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             // exact as halves (bf16's 8 bits, magnitudes up to 448), and so is what hi leaves
@@ -476,9 +485,13 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
             hi[k >> 1] = (k & 1) ? hi[k >> 1] | (h8 << 16) : h8;
             lo[k >> 1] = (k & 1) ? lo[k >> 1] | (l8 << 16) : l8;
           }
-          uint8_t* d = dst + lr * 128 + ((c ^ (lr & 7)) << 4);
-          *reinterpret_cast<uint4*>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(d + T8) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          // (every lane of the row has its elements: the maximum's shuffles came between)
+          uint8_t* d1 = dst + lr * 128 + (((c >> 1) ^ (lr & 7)) << 4) + 8 * (c & 1);
+          uint8_t* d2 = dst + lr * 128 + ((((c >> 1) + 4) ^ (lr & 7)) << 4) + 8 * (c & 1);
+          *reinterpret_cast<uint2*>(d1) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(d2) = make_uint2(hi[2], hi[3]);
+          *reinterpret_cast<uint2*>(d1 + T8) = make_uint2(lo[0], lo[1]);
+          *reinterpret_cast<uint2*>(d2 + T8) = make_uint2(lo[2], lo[3]);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -685,7 +698,48 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
             tma_store_2d(&tm.po, smem + ((two ? 4 * w : 0) + c) * T8, 32 * c,
                          static_cast<int>(prow) + (two ? w * 128 : 0));
           bulk_commit();
-          bulk_wait_read0();  // the combine kernel reads the rows once this grid has completed
+          if (a.coop)
+            bulk_wait0();  // other CTAs of this launch read the rows
+          else
+            bulk_wait_read0();  // the combine kernel reads them once this grid has completed
+          fence_proxy_async_global();
+        }
+      }
+      if (a.coop) {
+        // The group's merge: count this piece into its group (request, KV head, row block), wait
+        // until every piece that has work has counted, then merge an even share of its rows from
+        // L2, a warp per row.  A piece that gave up counts too: the others need not wait for it.
+        const int need = 1 + min(a.splits - 1, (n_pref + a.tps - 1) / a.tps);
+        int* cnt = a.cnt + 2 * (bh * gridDim.z + rb);
+        __threadfence();
+        bar_sync(1, 256);
+        if (threadIdx.x == 0) {
+          atomicAdd(cnt, 1);
+          const uint64_t t0 = global_ns();
+          bool all = ld_acquire_gpu(cnt) >= need;
+          while (!all && global_ns() - t0 < 2000000000ull) {
+            __nanosleep(64);
+            all = ld_acquire_gpu(cnt) >= need;
+          }
+          if (!all) atomicOr(a.err, ERR_GROUP);
+          go = all ? 1 : 0;
+          // past the wait: the last piece to get here returns both counters to zero
+          if (atomicAdd(cnt + 1, 1) == need - 1) {
+            atomicExch(cnt, 0);
+            atomicExch(cnt + 1, 0);
+          }
+        }
+        bar_sync(1, 256);
+        if (go) {
+          const int n = min(two ? 256 : 128, RG - row0);
+          const int hi = (piece + 1) * n / need;
+#pragma unroll 1
+          for (int k = piece * n / need + warp; k < hi; k += 8) {
+            const size_t base = (static_cast<size_t>(bh) * a.splits) * a.rows_pad + row0 + k;
+            const int nd = node_of(a, row0 + k);
+            kvq_merge_row<128, 20>(a, base, need, (static_cast<size_t>(b) * a.R + nd) * a.Hq + h * a.G + (row0 + k - nd * a.G),
+                                   lane);
+          }
         }
       }
     }
@@ -715,11 +769,13 @@ cudaError_t launch_tc(const KvqAttnPlan& p, const Maps& tm, const KvqAttnArgs& a
   cfg.blockDim = dim3(NT);
   cfg.dynamicSmemBytes = SMEM;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeCooperative;  // all CTAs resident, or the launch fails
+  attr[1].val.cooperative = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = p.coop ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, kern, tm, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
