@@ -173,6 +173,10 @@ def _check(fn: str, status: int):
 def _ptr(t: Optional[torch.Tensor], dtype=None, name: str = "tensor") -> Optional[int]:
     if t is None:
         return None
+    if t.is_cuda and t.is_contiguous():  # the usual case, in as few attribute reads as it takes
+        d = t.dtype
+        if dtype is None or d is dtype or (type(dtype) is tuple and d in dtype):
+            return t.data_ptr()
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (libeagle runs on the GPU only)")
     if not t.is_contiguous():
@@ -182,8 +186,16 @@ def _ptr(t: Optional[torch.Tensor], dtype=None, name: str = "tensor") -> Optiona
     return t.data_ptr()
 
 
+# The current stream's handle without building a torch.cuda.Stream object, which takes longer
+# than a kernel launch; the public call where torch does not have it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device_index = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None and _device_index is not None and torch.cuda.is_initialized():
+            return _raw_stream(_device_index())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 

@@ -400,7 +400,7 @@ int eagle_kvq_write(const eagle_kvq_desc* d, const void* k, const void* v, const
   if (rc == EAGLE_OK) rc = check_kvq_pointers(k, v, start, count, k_codes, k_scale, v_codes, v_scale, status);
   if (rc != EAGLE_OK) return rc;
   return cuda_status(launch_kvq_write(*d, k, v, start, count, static_cast<uint8_t*>(k_codes), k_scale,
-                                      static_cast<uint8_t*>(v_codes), v_scale, status,
+                                      static_cast<uint8_t*>(v_codes), v_scale, status, num_sms(),
                                       static_cast<cudaStream_t>(stream)));
 }
 
@@ -469,7 +469,7 @@ int eagle_qk_norm_rope(const eagle_qk_norm_rope_desc* d, const void* qkv, const 
   if (!aligned(qkv, 16) || !aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(q, 16) || !aligned(k, 16) ||
       !aligned(v, 16) || !aligned(inv_freq, 4) || !aligned(pos_id, 4) || (n_nodes && !aligned(n_nodes, 4)))
     return EAGLE_ERR_ALIGNMENT;
-  return cuda_status(launch_qk_norm_rope(*d, qkv, q_weight, k_weight, inv_freq, pos_id, n_nodes, q, k, v,
+  return cuda_status(launch_qk_norm_rope(*d, qkv, q_weight, k_weight, inv_freq, pos_id, n_nodes, q, k, v, num_sms(),
                                          static_cast<cudaStream_t>(stream)));
 }
 

@@ -5,16 +5,22 @@
 // accepted tokens are appended; lesson "KV cache rollback"); the pages keep the cache in 16
 // bits, the 8-bit form halves the bytes that tree attention streams.
 //
-// One thread group owns one 64-row block of one head, so a block's scale has one writer:
-//   1. it loads the rows that fall into the block (all of them in flight at once, kept in
-//      registers) and takes their largest magnitude;
+// One owner per 64-row block of one head (a CTA when writing, a warp when committing), so a
+// block's scale has one writer:
+//   1. it loads the rows that fall into the block (kept in registers) and takes their largest
+//      magnitude;
 //   2. the scale: that maximum's power of two, or the block's old scale if rows before the
 //      first new one stay in the block and theirs is larger;
 //   3. if the scale grew, the rows that stay are moved to it (their codes, not their
 //      original values, which are gone);
 //   4. the new rows' codes are stored.
-// Each element is read once and written once; the write and read kernels are bound by HBM,
-// the commit (a few rows per block) by the latency of its dependent loads.
+// Each element is read once and written once.  Writing and reading are bound by HBM: the write
+// kernel's CTAs are persistent and hold the next block's rows in flight while they finish one
+// (one block at a time leaves HBM idle through every block's reduction).  A commit is a few rows
+// for each of layers x requests x heads blocks, bound by the latency of its dependent loads
+// (lengths, path, rows), so it takes a warp per block and all of them at once.
+#include <algorithm>
+
 #include "common.cuh"
 #include "kvq.cuh"
 #include "launch.h"
@@ -53,68 +59,38 @@ struct Chunk<float> {
   }
 };
 
-// Rows [lo, hi) of the block that begins at cache row `base`, by NT threads (tid in
-// [0, NT), a multiple of 32; `red` NT / 32 floats; `bar` their named barrier): row r comes
-// from src(r) (nullptr: the row is not written).  codes: the head's cache rows; scale: the
-// block's entry.  D is a multiple of 8 and 64 * D / 8 chunks fit MAXC per thread.
-template <typename T, int NT, int MAXC, typename Src>
-__device__ __forceinline__ void put_block(int tid, float* red, int bar, int D, int base, int lo, int hi, Src src,
-                                          uint8_t* codes, float* scale) {
-  const int per = D / 8, total = (hi - lo) * per;
-  Chunk<T> x[MAXC];
-  bool on[MAXC];
-  float amax = 0.f;
+__device__ __forceinline__ float finite_abs(float x) {  // the scale follows the finite values
+  const float m = fabsf(x);
+  return m <= 3.402823466e38f ? m : 0.f;
+}
+
+template <typename T>
+__device__ __forceinline__ float chunk_max(const Chunk<T>& x) {
+  float f[8], m = 0.f;
+  x.get(f);
 #pragma unroll
-  for (int i = 0; i < MAXC; ++i) {
-    const int c = tid + i * NT;
-    const T* p = c < total ? src(lo + c / per) : nullptr;
-    on[i] = p != nullptr;
-    if (on[i])
-      x[i].load(p + (c % per) * 8);
-    else
-      x[i].zero();
+  for (int e = 0; e < 8; ++e) m = fmaxf(m, finite_abs(f[e]));
+  return m;
+}
+
+template <typename T>
+__device__ __forceinline__ uint2 chunk_codes(const Chunk<T>& x, float inv) {
+  float f[8];
+  x.get(f);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] *= inv;
+  return make_uint2(kvq_code2(f[0], f[1]) | (kvq_code2(f[2], f[3]) << 16),
+                    kvq_code2(f[4], f[5]) | (kvq_code2(f[6], f[7]) << 16));
+}
+
+// The rows [base, lo) that stay in a block whose scale grew, ratio = old scale / new, by threads
+// tid of n.
+__device__ __forceinline__ void move_rows(uint8_t* codes, int D, int base, int lo, float ratio, int tid, int n) {
+  uint2* old = reinterpret_cast<uint2*>(codes + static_cast<size_t>(base) * D);
+  for (int c = tid; c < (lo - base) * (D / 8); c += n) {
+    const uint2 w = old[c];
+    old[c] = make_uint2(kvq_move4(w.x, ratio), kvq_move4(w.y, ratio));
   }
-#pragma unroll
-  for (int i = 0; i < MAXC; ++i) {
-    float f[8];
-    x[i].get(f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float m = fabsf(f[e]);
-      amax = fmaxf(amax, m <= 3.402823466e38f ? m : 0.f);  // the scale follows the finite values
-    }
-  }
-  const bool holds = lo > base;  // rows before `lo` stay
-  const float s_old = holds ? *scale : 0.f;
-  amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-  if ((tid & 31) == 0) red[tid >> 5] = amax;
-  sm100::bar_sync(bar, NT);
-#pragma unroll
-  for (int w = 0; w < NT / 32; ++w) amax = fmaxf(amax, red[w]);
-  const float s = fmaxf(kvq_scale(amax), s_old);
-  const float inv = kvq_inverse(s);
-  if (s > s_old && s_old > 0.f) {
-    const float ratio = s_old * inv;
-    uint2* old = reinterpret_cast<uint2*>(codes + static_cast<size_t>(base) * D);
-    for (int c = tid; c < (lo - base) * per; c += NT) {
-      const uint2 w = old[c];
-      old[c] = make_uint2(kvq_move4(w.x, ratio), kvq_move4(w.y, ratio));
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < MAXC; ++i) {
-    if (!on[i]) continue;
-    const int c = tid + i * NT;
-    float f[8];
-    x[i].get(f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] *= inv;
-    *reinterpret_cast<uint2*>(codes + static_cast<size_t>(lo) * D + static_cast<size_t>(c) * 8) =
-        make_uint2(kvq_code2(f[0], f[1]) | (kvq_code2(f[2], f[3]) << 16),
-                   kvq_code2(f[4], f[5]) | (kvq_code2(f[6], f[7]) << 16));
-  }
-  sm100::bar_sync(bar, NT);  // every thread has read the old scale and `red`
-  if (tid == 0) *scale = s;
 }
 
 // A request's row span: valid if it lies inside the cache.
@@ -125,29 +101,83 @@ __device__ __forceinline__ bool span(const eagle_kvq_desc& d, const int32_t* sta
   return first >= 0 && n >= 0 && n <= d.rows && first <= d.max_seq - n;
 }
 
-// grid (blocks a span can touch, B Hkv, K / V) x 256
+// One block of the write kernel's work list (which: K or V; block of the request's span).
 template <typename T>
-__global__ void __launch_bounds__(256) kvq_write_kernel(const eagle_kvq_desc d, const T* k, const T* v,
-                                                        const int32_t* start, const int32_t* count, uint8_t* k8,
-                                                        float* ks, uint8_t* v8, float* vs, uint32_t* status) {
-  __shared__ float red[8];
-  const int bh = blockIdx.y, b = bh / d.n_kv_heads;
-  int first, n;
-  if (!span(d, start, count, b, first, n)) {
-    if (status && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(status, EAGLE_STATUS_CACHE_FULL);
-    return;
+struct WriteItem {
+  static constexpr int C = 4;  // 16-byte (bf16) chunks of a thread: 64 x 128 / 8 / 256
+  Chunk<T> x[C];
+  uint8_t* codes;  // the head's rows
+  float* scale;
+  int base, lo, hi;  // empty: lo >= hi
+
+  __device__ __forceinline__ void fetch(const eagle_kvq_desc& d, int item, int per_head, int items, const T* k, const T* v,
+                                        const int32_t* start, const int32_t* count, uint8_t* k8, float* ks,
+                                        uint8_t* v8, float* vs, uint32_t* status) {
+    lo = hi = 0;
+    if (item >= items) return;
+    const int j = item % per_head, hv = item / per_head;
+    const int which = hv & 1, bh = hv >> 1, b = bh / d.n_kv_heads;
+    int first, n;
+    if (!span(d, start, count, b, first, n)) {
+      if (status && j == 0 && threadIdx.x == 0) atomicOr(status, EAGLE_STATUS_CACHE_FULL);
+      return;
+    }
+    const int blk = first / kQB + j;
+    base = blk * kQB;
+    lo = max(first, base);
+    hi = min(first + n, base + kQB);
+    if (lo >= hi) return;
+    const T* src = (which ? v : k) + (static_cast<size_t>(bh) * d.rows + (lo - first)) * d.head_dim;
+    const int total = (hi - lo) * (d.head_dim / 8);
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int c = threadIdx.x + i * 256;
+      if (c < total)
+        x[i].load(src + static_cast<size_t>(c) * 8);
+      else
+        x[i].zero();
+    }
+    codes = (which ? v8 : k8) + static_cast<size_t>(bh) * d.max_seq * d.head_dim;
+    scale = (which ? vs : ks) + static_cast<size_t>(bh) * ((d.max_seq + kQB - 1) / kQB) + blk;
   }
-  const int blk = first / kQB + blockIdx.x;
-  const int base = blk * kQB;
-  const int lo = max(first, base), hi = min(first + n, base + kQB);
-  if (lo >= hi) return;
-  const T* x = (blockIdx.z ? v : k) + static_cast<size_t>(bh) * d.rows * d.head_dim;
-  const int nblk = (d.max_seq + kQB - 1) / kQB;
-  put_block<T, 256, 4>(
-      threadIdx.x, red, 1, d.head_dim, base, lo, hi,
-      [&](int r) { return x + static_cast<size_t>(r - first) * d.head_dim; },
-      (blockIdx.z ? v8 : k8) + static_cast<size_t>(bh) * d.max_seq * d.head_dim,
-      (blockIdx.z ? vs : ks) + static_cast<size_t>(bh) * nblk + blk);
+};
+
+// Persistent: CTA c takes the blocks c, c + grid, ... of the list
+template <typename T>
+__global__ void __launch_bounds__(256) kvq_write_kernel(const eagle_kvq_desc d, int per_head, int items, const T* k,
+                                                        const T* v, const int32_t* start, const int32_t* count,
+                                                        uint8_t* k8, float* ks, uint8_t* v8, float* vs,
+                                                        uint32_t* status) {
+  __shared__ float red[2][8];
+  WriteItem<T> cur, nxt;
+  cur.fetch(d, blockIdx.x, per_head, items, k, v, start, count, k8, ks, v8, vs, status);
+  int turn = 0;
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    nxt.fetch(d, item + gridDim.x, per_head, items, k, v, start, count, k8, ks, v8, vs, status);
+    if (cur.lo < cur.hi) {  // the same for the whole CTA
+      float amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < cur.C; ++i) amax = fmaxf(amax, chunk_max(cur.x[i]));
+      const float s_old = cur.lo > cur.base ? *cur.scale : 0.f;
+      amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+      if ((threadIdx.x & 31) == 0) red[turn][threadIdx.x >> 5] = amax;
+      __syncthreads();  // (the old scale has been read; the other half of `red` is the next block's)
+#pragma unroll
+      for (int w = 0; w < 8; ++w) amax = fmaxf(amax, red[turn][w]);
+      turn ^= 1;
+      const float s = fmaxf(kvq_scale(amax), s_old), inv = kvq_inverse(s);
+      if (s > s_old && s_old > 0.f) move_rows(cur.codes, d.head_dim, cur.base, cur.lo, s_old * inv, threadIdx.x, 256);
+      const int total = (cur.hi - cur.lo) * (d.head_dim / 8);
+      uint2* dst = reinterpret_cast<uint2*>(cur.codes + static_cast<size_t>(cur.lo) * d.head_dim);
+#pragma unroll
+      for (int i = 0; i < cur.C; ++i) {
+        const int c = threadIdx.x + i * 256;
+        if (c < total) dst[c] = chunk_codes(cur.x[i], inv);
+      }
+      if (threadIdx.x == 0) *cur.scale = s;
+    }
+    cur = nxt;
+  }
 }
 
 // Read back: a thread takes 16 output bytes at a time (8 bf16 or 4 fp32 elements), four of
@@ -203,52 +233,108 @@ __global__ void __launch_bounds__(256) kvq_read_kernel(const eagle_kvq_desc d, c
   }
 }
 
-// grid (Hkv, B, layers) x 256: threads 0..127 take K, 128..255 V of one head.
+// A warp per (layer, request, KV head): the path's rows of K and V into the one or two blocks
+// they fall in.  16 bytes (bf16) of a row per lane: two rows of 128 at a time, four such loads of
+// K and of V in flight; paths longer than that take further rounds, read twice.
 template <typename T>
-__global__ void __launch_bounds__(256) kvq_commit_kernel(const eagle_commit_desc d,
+__global__ void __launch_bounds__(128) kvq_commit_kernel(const eagle_commit_desc d,
                                                          const __grid_constant__ KvqCommitArgs a,
                                                          const int32_t* n_acc, const int32_t* path,
                                                          const int32_t* seq_len, void* feat_cache,
                                                          const void* tree_feat) {
-  __shared__ float red[8];
-  __shared__ int node[kMaxRows];
-  const int h = blockIdx.x, b = blockIdx.y, l = blockIdx.z;
+  constexpr int C = 4;
+  const int lane = threadIdx.x & 31;
+  const long long id = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int per = d.n_kv_heads * d.batch;
+  const int l = static_cast<int>(id / per), bh = static_cast<int>(id % per), b = bh / d.n_kv_heads, h = bh % d.n_kv_heads;
   sm100::griddep_wait();
   sm100::griddep_launch_dependents();
-  if (!commit_fits(d, n_acc, seq_len, b)) return;
-  const int first = seq_len[b], n = n_acc[b] + 1;
-  for (int m = threadIdx.x; m < n; m += 256) {
-    const int r = path[static_cast<size_t>(b) * (d.max_depth + 1) + m];
-    node[m] = r >= 0 && r < d.rows ? r : -1;  // a bad node is flagged by the finalize kernel, its row left as it was
-  }
-  __syncthreads();
-  const int half = threadIdx.x >> 7, tid = threadIdx.x & 127, D = d.head_dim;
-  const size_t bh = static_cast<size_t>(b) * d.n_kv_heads + h;
+  if (l >= d.layers || !commit_fits(d, n_acc, seq_len, b)) return;
+  const int first = seq_len[b], n = n_acc[b] + 1, D = d.head_dim;
+  const int32_t* nodes = path + static_cast<size_t>(b) * (d.max_depth + 1);
+  const int lanes = D / 8, rpp = 32 / lanes, sub = lane / lanes, col = (lane % lanes) * 8;
   const int nblk = (d.max_seq + kQB - 1) / kQB;
-  const T* tree = static_cast<const T*>(half ? a.tree_v[l] : a.tree_k[l]) + bh * d.rows * D;
-  uint8_t* codes = static_cast<uint8_t*>(half ? a.v8[l] : a.k8[l]) + bh * d.max_seq * D;
-  float* scale = (half ? a.vs[l] : a.ks[l]) + bh * nblk;
+  const size_t hb = static_cast<size_t>(bh);
   for (int blk = first / kQB; blk * kQB < first + n; ++blk) {
-    const int base = blk * kQB;
-    put_block<T, 128, 8>(
-        tid, red + 4 * half, 1 + half, D, base, max(first, base), min(first + n, base + kQB),
-        [&](int r) -> const T* {
-          const int nd = node[r - first];
-          return nd < 0 ? nullptr : tree + static_cast<size_t>(nd) * D;
-        },
-        codes, scale + blk);
+    const int base = blk * kQB, lo = max(first, base), hi = min(first + n, base + kQB);
+    const T* tree[2] = {static_cast<const T*>(a.tree_k[l]) + hb * d.rows * D + col,
+                        static_cast<const T*>(a.tree_v[l]) + hb * d.rows * D + col};
+    uint8_t* codes[2] = {static_cast<uint8_t*>(a.k8[l]) + hb * d.max_seq * D,
+                         static_cast<uint8_t*>(a.v8[l]) + hb * d.max_seq * D};
+    float* scale[2] = {a.ks[l] + hb * nblk + blk, a.vs[l] + hb * nblk + blk};
+    // rows lo + r0 + sub + rpp i; a bad node (flagged by the finalize kernel) writes nothing
+    Chunk<T> x[2][C];
+    int row[C];
+    auto fetch = [&](int r0) {
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        const int r = lo + r0 + sub + rpp * i;
+        row[i] = -1;
+        if (r < hi) {
+          const int nd = __ldg(nodes + (r - first));
+          if (nd >= 0 && nd < d.rows) row[i] = nd;
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+          if (row[i] >= 0)
+            x[w][i].load(tree[w] + static_cast<size_t>(row[i]) * D);
+          else
+            x[w][i].zero();
+        }
+    };
+    fetch(0);
+    float s_old[2] = {0.f, 0.f}, amax[2] = {0.f, 0.f}, s[2];
+    if (lo > base) {
+      s_old[0] = *scale[0];
+      s_old[1] = *scale[1];
+    }
+    const int round = C * rpp, rounds = (hi - lo + round - 1) / round;
+    for (int g = 0; g < rounds; ++g) {
+      if (g > 0) fetch(g * round);
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int i = 0; i < C; ++i) amax[w] = fmaxf(amax[w], chunk_max(x[w][i]));
+    }
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      amax[w] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax[w])));
+      s[w] = fmaxf(kvq_scale(amax[w]), s_old[w]);
+      if (s[w] > s_old[w] && s_old[w] > 0.f) move_rows(codes[w], D, base, lo, s_old[w] * kvq_inverse(s[w]), lane, 32);
+    }
+    for (int g = rounds - 1; g >= 0; --g) {  // (the last round's rows are still in registers)
+      if (g < rounds - 1) fetch(g * round);
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+          if (row[i] >= 0)
+            *reinterpret_cast<uint2*>(codes[w] + static_cast<size_t>(lo + g * round + sub + rpp * i) * D + col) =
+                chunk_codes(x[w][i], kvq_inverse(s[w]));
+    }
+    __syncwarp();  // every lane has read the old scales
+    if (lane < 2) *(lane ? scale[1] : scale[0]) = lane ? s[1] : s[0];
   }
-  if (h == 0 && l == 0 && d.feat_dim > 0) {
+  if (d.feat_dim > 0) {
+    // feature rows in pieces of 2 KB, shared out over the request's warps
     const size_t bytes = static_cast<size_t>(d.feat_dim) * (d.feat_dtype == EAGLE_F32 ? 4 : 2);
-    for (int m = 0; m < n; ++m) {
-      if (node[m] < 0) continue;
-      const uint8_t* s = static_cast<const uint8_t*>(tree_feat) + (static_cast<size_t>(b) * d.rows + node[m]) * bytes;
-      uint8_t* t = static_cast<uint8_t*>(feat_cache) + (static_cast<size_t>(b) * d.max_seq + first + m) * bytes;
-      if (bytes % 16 == 0)
-        for (size_t i = threadIdx.x; i < bytes / 16; i += 256)
-          reinterpret_cast<uint4*>(t)[i] = reinterpret_cast<const uint4*>(s)[i];
-      else
-        for (size_t i = threadIdx.x; i < bytes; i += 256) t[i] = s[i];
+    const int pieces = static_cast<int>((bytes + 2047) / 2048);
+    for (int u = l * d.n_kv_heads + h; u < n * pieces; u += d.layers * d.n_kv_heads) {
+      const int m = u / pieces, nd = nodes[m];
+      if (nd < 0 || nd >= d.rows) continue;
+      const size_t off = static_cast<size_t>(u % pieces) * 2048, end = off + 2048 < bytes ? off + 2048 : bytes;
+      const uint8_t* src = static_cast<const uint8_t*>(tree_feat) + (static_cast<size_t>(b) * d.rows + nd) * bytes;
+      uint8_t* dst = static_cast<uint8_t*>(feat_cache) + (static_cast<size_t>(b) * d.max_seq + first + m) * bytes;
+      if (bytes % 16 == 0) {
+#pragma unroll 4
+        for (size_t i = off + lane * 16; i < end; i += 512)
+          *reinterpret_cast<uint4*>(dst + i) = __ldg(reinterpret_cast<const uint4*>(src + i));
+      } else {
+        for (size_t i = off + lane; i < end; i += 32) dst[i] = src[i];
+      }
     }
   }
 }
@@ -274,13 +360,16 @@ cudaError_t launch(void (*k)(P...), dim3 grid, int threads, cudaStream_t s, bool
 
 cudaError_t launch_kvq_write(const eagle_kvq_desc& d, const void* k, const void* v, const int32_t* start,
                              const int32_t* count, uint8_t* k8, float* ks, uint8_t* v8, float* vs, uint32_t* status,
-                             cudaStream_t s) {
-  const dim3 grid((d.rows + 2 * kQB - 2) / kQB, d.batch * d.n_kv_heads, 2);
+                             int num_sms, cudaStream_t s) {
+  const int per_head = static_cast<int>((d.rows + 2ll * kQB - 2) / kQB);  // blocks a span of `rows` can touch
+  const long long items = 2ll * per_head * d.batch * d.n_kv_heads;
+  if (items > (1ll << 30)) return cudaErrorInvalidValue;
+  const int grid = static_cast<int>(std::min<long long>(items, (d.dtype == EAGLE_F32 ? 2ll : 3ll) * num_sms));  // CTAs that fit
   if (d.dtype == EAGLE_F32)
-    return launch(kvq_write_kernel<float>, grid, 256, s, false, d, static_cast<const float*>(k),
-                  static_cast<const float*>(v), start, count, k8, ks, v8, vs, status);
-  return launch(kvq_write_kernel<uint16_t>, grid, 256, s, false, d, static_cast<const uint16_t*>(k),
-                static_cast<const uint16_t*>(v), start, count, k8, ks, v8, vs, status);
+    return launch(kvq_write_kernel<float>, dim3(grid), 256, s, false, d, per_head, static_cast<int>(items),
+                  static_cast<const float*>(k), static_cast<const float*>(v), start, count, k8, ks, v8, vs, status);
+  return launch(kvq_write_kernel<uint16_t>, dim3(grid), 256, s, false, d, per_head, static_cast<int>(items),
+                static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), start, count, k8, ks, v8, vs, status);
 }
 
 cudaError_t launch_kvq_read(const eagle_kvq_desc& d, const uint8_t* k8, const float* ks, const uint8_t* v8,
@@ -296,11 +385,12 @@ cudaError_t launch_kvq_read(const eagle_kvq_desc& d, const uint8_t* k8, const fl
 cudaError_t launch_kvq_commit(const eagle_commit_desc& d, const KvqCommitArgs& a, const int32_t* n_acc,
                               const int32_t* path, int32_t* seq_len, int32_t* commit_pos, void* feat_cache,
                               const void* tree_feat, uint32_t* status, cudaStream_t s) {
-  const dim3 grid(d.n_kv_heads, d.batch, d.layers);
+  const long long warps = static_cast<long long>(d.layers) * d.batch * d.n_kv_heads;
+  const dim3 grid(static_cast<unsigned>((warps + 3) / 4));
   const int32_t* len = seq_len;
   cudaError_t e = d.dtype == EAGLE_F32
-                      ? launch(kvq_commit_kernel<float>, grid, 256, s, true, d, a, n_acc, path, len, feat_cache, tree_feat)
-                      : launch(kvq_commit_kernel<uint16_t>, grid, 256, s, true, d, a, n_acc, path, len, feat_cache,
+                      ? launch(kvq_commit_kernel<float>, grid, 128, s, true, d, a, n_acc, path, len, feat_cache, tree_feat)
+                      : launch(kvq_commit_kernel<uint16_t>, grid, 128, s, true, d, a, n_acc, path, len, feat_cache,
                                tree_feat);
   if (e != cudaSuccess) return e;
   return launch_commit_finalize(d, n_acc, path, seq_len, commit_pos, status, s);

@@ -154,7 +154,7 @@ struct KvqCommitArgs {
 };
 cudaError_t launch_kvq_write(const eagle_kvq_desc& d, const void* k, const void* v, const int32_t* start,
                              const int32_t* count, uint8_t* k8, float* ks, uint8_t* v8, float* vs, uint32_t* status,
-                             cudaStream_t s);
+                             int num_sms, cudaStream_t s);
 cudaError_t launch_kvq_read(const eagle_kvq_desc& d, const uint8_t* k8, const float* ks, const uint8_t* v8,
                             const float* vs, const int32_t* start, const int32_t* count, void* k, void* v,
                             uint32_t* status, cudaStream_t s);
@@ -168,13 +168,13 @@ struct KvqAttnPlan {
   bool terms2;      // P as two half terms (EAGLE_ATTN_PRECISE)
   float scale;
   bool tc;          // tcgen05 kernel
-  int mt, wr;       // mma.sync: 16-row tiles per warp, warps along the rows (8 / wr split a tile's
-                    // keys); tcgen05: wr row tiles of 128
+  int wr;           // mma.sync: warps of 16 rows side by side (16 / wr share the keys); tcgen05: wr
+                    // row tiles of 128
   int rows_per_cta, row_blocks, rows_pad;
   int splits, tps;  // mma.sync: split s takes 128-key units [s tps, (s + 1) tps) of its request, the
                     // tree being the last; tcgen05: piece 0 is the tree, piece s the prefix tiles
                     // [(s - 1) tps, s tps)
-  bool coop;        // tcgen05: the whole grid fits on the SMs, pieces merge in the kernel
+  bool coop;        // the whole grid fits on the SMs: splits merge in the kernel
   size_t off_err, off_cnt, off_o, off_ml, total;
 };
 void plan_kvq_attn(const eagle_attn_desc* d, int num_sms, KvqAttnPlan* p);
@@ -195,7 +195,7 @@ struct KvqAttnArgs {
   float* part_ml;  // [B*Hkv][splits][rows_pad][2]: max in log2 units, sum
   int* err;
   int* cnt;        // coop: [groups][2] published / finished pieces, zero between calls
-  int B, R, Hq, Hkv, G, P, W, splits, tps, rows_pad, out_f32, wr, tc, coop;
+  int B, R, Hq, Hkv, G, P, W, splits, tps, rows_pad, out_f32, wr, tc, coop, nst;
   uint32_t g_inv;  // ceil(2^32 / G) for G > 1
   float scale, scale_log2;
 };
@@ -208,6 +208,6 @@ cudaError_t launch_kvq_attn(const KvqAttnPlan& p, const void* q, const void* k8,
 // ------------------------------------------------------------------ norms and rotation
 cudaError_t launch_qk_norm_rope(const eagle_qk_norm_rope_desc& d, const void* qkv, const void* wq, const void* wk,
                                 const float* inv_freq, const int32_t* pos_id, const int32_t* n_nodes, void* q,
-                                void* k, void* v, cudaStream_t s);
+                                void* k, void* v, int num_sms, cudaStream_t s);
 
 }  // namespace eagle

@@ -9,19 +9,27 @@
 // node's position is its prefix length plus its depth (pos_id of the tree build), so the
 // nodes of one row block sit at few distinct positions, in no order.
 //
-// Bound by HBM for long inputs, by latency for one tree.  One CTA per row: its 16 half-warps
-// take the Hq + 2 Hkv heads in turn (16 lanes x 8 elements = a head of 128; two heads of 64),
-// the loads of the first heads are in flight while the row's rot / 2 sines and cosines are
-// computed once, into shared memory, for every head.  The angle is reduced in fp64 turns
-// (pos * inv_freq / 2 pi, minus the nearest integer): in fp32 the product alone would be off
-// by 2^-24 of the angle, 4e-3 rad at position 65536.  Everything else is fp32, rounded once.
+// Bound by HBM for long inputs, by latency for one tree.  A warp takes one row, or a run of its
+// heads when the rows alone would leave SMs empty (16 lanes x 8 elements = a head of 128, two
+// heads a pass; four heads of 64), with four passes' loads in
+// flight (a slot is loaded again as soon as its elements are in use).  Warps need nothing of one
+// another, so one warp's loads, another's sines and a third's stores overlap: 47 us for 8192 rows
+// of 48 heads (201 MB, 4.25 TB/s; a device copy of as many bytes takes 65 us).  A CTA per row with
+// the sines shared over its heads took 76 us, every CTA going through its load, barrier and store
+// phases alone.  The row's rot / 2 sines and cosines are computed two a lane into the warp's table
+// while the first loads are on their way to L2.
+// The angle is reduced in fp64 turns (pos * inv_freq / 2 pi, minus the nearest integer): in fp32
+// the product alone would be off by 2^-24 of the angle, 4e-3 rad at position 65536.  Everything
+// else is fp32, rounded once.
+#include <algorithm>
+
 #include "common.cuh"
 #include "launch.h"
 
 namespace eagle {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 struct RopeArgs {
   const void* qkv;
@@ -34,6 +42,8 @@ struct RopeArgs {
   void* k;
   void* v;
   int rows, hq, hkv, rot, interleaved;
+  int run, runs;  // heads a warp takes, runs of them in a row
+  long long units;
   long long stride;
   float eps;
 };
@@ -53,6 +63,15 @@ struct Lane8<false> {
       f[2 * i] = __uint_as_float(w[i] << 16);
       f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
+  }
+  // the elements that lane `src` of the group holds
+  __device__ __forceinline__ Lane8 from(int src, int width) const {
+    Lane8 r;
+    r.u.x = __shfl_sync(0xffffffffu, u.x, src, width);
+    r.u.y = __shfl_sync(0xffffffffu, u.y, src, width);
+    r.u.z = __shfl_sync(0xffffffffu, u.z, src, width);
+    r.u.w = __shfl_sync(0xffffffffu, u.w, src, width);
+    return r;
   }
   static __device__ __forceinline__ void store(void* p, size_t e, const float (&f)[8]) {
     uint32_t w[4];
@@ -76,6 +95,16 @@ struct Lane8<true> {
     f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
     f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
   }
+  __device__ __forceinline__ Lane8 from(int src, int width) const {
+    Lane8 r;
+    float f[8];
+    get(f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = __shfl_sync(0xffffffffu, f[e], src, width);
+    r.a = make_float4(f[0], f[1], f[2], f[3]);
+    r.b = make_float4(f[4], f[5], f[6], f[7]);
+    return r;
+  }
   static __device__ __forceinline__ void store(void* p, size_t e, const float (&f)[8]) {
     float4* d = reinterpret_cast<float4*>(static_cast<float*>(p) + e);
     d[0] = make_float4(f[0], f[1], f[2], f[3]);
@@ -84,97 +113,106 @@ struct Lane8<true> {
 };
 
 template <bool F32, int D>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a) {
-  constexpr int LANES = D / 8;              // lanes of a head
-  constexpr int GROUPS = kThreads / LANES;  // heads of a CTA pass
-  constexpr int U = 4;                      // passes whose loads are in flight together
-  __shared__ float2 cs[D / 2];
-  const int b = blockIdx.y, r = blockIdx.x;
+__global__ void __launch_bounds__(kThreads, F32 ? 5 : 7) qk_norm_rope_kernel(const RopeArgs a) {
+  constexpr int LANES = D / 8;       // lanes of a head
+  constexpr int HPP = 32 / LANES;    // heads of a pass
+  constexpr int U = F32 ? 2 : 4;     // passes whose loads are in flight together
+  __shared__ __align__(16) float2 table[kThreads / 32][D / 2];
+  const int warp = threadIdx.x >> 5;
+  const long long unit = static_cast<long long>(blockIdx.x) * (kThreads / 32) + warp;
+  if (unit >= a.units) return;
+  const size_t row = static_cast<size_t>(unit / a.runs);
+  const int b = static_cast<int>(row / a.rows), r = static_cast<int>(row % a.rows);
   if (a.n_nodes && r >= a.n_nodes[b]) return;  // rows past the request's tree are not written
-  const int grp = threadIdx.x / LANES, lane = threadIdx.x % LANES;
-  const int heads = a.hq + 2 * a.hkv;
-  const size_t row = static_cast<size_t>(b) * a.rows + r;
+  const int sub = (threadIdx.x & 31) / LANES, lane = threadIdx.x % LANES;
+  const int h_begin = static_cast<int>(unit % a.runs) * a.run;
+  const int h_end = min(h_begin + a.run, a.hq + 2 * a.hkv);
   const size_t src = row * a.stride + static_cast<size_t>(lane) * 8;
-  Lane8<F32> x[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (grp + u * GROUPS < heads) x[u].load(a.qkv, src + static_cast<size_t>(grp + u * GROUPS) * D);
+  if (h_begin + sub < h_end)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t*>(a.qkv) +
+                                                  (src + static_cast<size_t>(h_begin + sub) * D) * (F32 ? 4 : 2)));
   const int half = a.rot / 2;
-  if (threadIdx.x < half) {
-    const double turns = static_cast<double>(a.pos[row]) * static_cast<double>(a.inv_freq[threadIdx.x]) *
-                         0.15915494309189533577;  // 1 / (2 pi)
+  const double pos = static_cast<double>(a.pos[row]) * 0.15915494309189533577;  // 1 / (2 pi)
+  for (int i = threadIdx.x & 31; i < half; i += 32) {
+    const double turns = pos * static_cast<double>(a.inv_freq[i]);
     float s, c;
     sincospif(2.f * static_cast<float>(turns - rint(turns)), &s, &c);
-    cs[threadIdx.x] = make_float2(c, s);
+    table[warp][i] = make_float2(c, s);
   }
-  float w[2][8];  // the lane's norm weights of q and k
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const void* p = t ? a.wk : a.wq;
-    Lane8<F32> y;
-    if (p) {
-      y.load(p, static_cast<size_t>(lane) * 8);
-      y.get(w[t]);
-    }
-  }
-  __syncthreads();
-  // the lane's 8 rotation pairs: in the split form all of them are first or all second
-  // elements (rot is a multiple of 16), whose partners a lane rot / 16 away holds
+  __syncwarp();
+  // y = g (x c + p s): g the head's norm, p the rotation partner, c and s the lane's 8 cosines
+  // and signed sines times the norm weights of x and p (reloaded when the heads turn from q to
+  // k).  In the split form all 8 elements are first or all second ones (rot is a multiple of 16)
+  // and a lane rot / 16 away has the partners; interleaved they are neighbours within the lane.
   const bool in = lane * 8 < a.rot;
   const bool second = !a.interleaved && lane * 8 >= half;
   const int far = !in || a.interleaved ? 0 : (second ? -(half / 8) : half / 8);
-  for (int h0 = grp; h0 - grp < heads; h0 += U * GROUPS) {
-    if (h0 != grp) {
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (h0 + u * GROUPS < heads) x[u].load(a.qkv, src + static_cast<size_t>(h0 + u * GROUPS) * D);
-    }
+#pragma unroll 1
+  for (int kind = 0; kind < 3; ++kind) {  // q, k, v heads of the run
+    const int first = kind == 0 ? 0 : (kind == 1 ? a.hq : a.hq + a.hkv);
+    const int k0 = max(h_begin, first), k1 = min(h_end, kind == 0 ? a.hq : first + a.hkv);
+    if (k0 >= k1) continue;
+    Lane8<F32> x[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * GROUPS;
-      if (h - grp >= heads) break;  // the same for the whole CTA: the shuffles below are warp-wide
-      const bool live = h < heads;
-      const bool is_q = h < a.hq, is_k = !is_q && h < a.hq + a.hkv;
-      float f[8];
-      x[u].get(f);
-      float ss = 0.f;
+      const int h = k0 + u * HPP + sub;
+      if (h < k1) x[u].load(a.qkv, src + static_cast<size_t>(h) * D);
+    }
+    const void* weight = kind == 0 ? a.wq : (kind == 1 ? a.wk : nullptr);
+    float c[8], s[8];
+    if (kind < 2) {
+      Lane8<F32> t;
+      float w[8], wp[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
-#pragma unroll
-      for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, LANES);
-      if (is_q ? a.wq != nullptr : (is_k && a.wk != nullptr)) {
-        const float g = 1.f / sqrtf(ss * (1.f / D) + a.eps);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= g * (is_q ? w[0][e] : w[1][e]);
+      for (int e = 0; e < 8; ++e) w[e] = wp[e] = 1.f;
+      if (weight) {
+        t.load(weight, static_cast<size_t>(lane) * 8);
+        t.get(w);
+        t.load(weight, static_cast<size_t>(lane + far) * 8);
+        t.get(wp);
       }
-      float p[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) p[e] = __shfl_sync(0xffffffffu, f[e], lane + far, LANES);
-      if ((is_q || is_k) && in) {
-        if (a.interleaved) {
+      for (int e = 0; e < 8; ++e) {
+        float2 v = make_float2(1.f, 0.f);
+        if (in) v = table[warp][a.interleaved ? lane * 4 + e / 2 : lane * 8 + e - (second ? half : 0)];
+        c[e] = w[e] * v.x;
+        s[e] = (a.interleaved ? w[e ^ 1] : wp[e]) * ((a.interleaved ? (e & 1) != 0 : second) ? v.y : -v.y);
+      }
+    }
+    // this lane's 16 bytes (bf16) of head h in the output of its kind
+    uint8_t* out = static_cast<uint8_t*>(kind == 0 ? a.q : (kind == 1 ? a.k : a.v));
+    const size_t head0 = kind == 0 ? row * a.hq : static_cast<size_t>(b) * a.hkv * a.rows + r;
+    const size_t step = kind == 0 ? 1 : a.rows;
+    for (int h0 = k0; h0 < k1; h0 += U * HPP) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 t = cs[lane * 4 + e];
-            const float u0 = f[2 * e], u1 = f[2 * e + 1];
-            f[2 * e] = u0 * t.x - u1 * t.y;
-            f[2 * e + 1] = u0 * t.y + u1 * t.x;
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * HPP + sub;
+        if (h - sub >= k1) break;  // the same for the whole warp: the shuffles below are warp-wide
+        float f[8];
+        x[u].get(f);
+        if (kind < 2) {
+          float p[8];
+          if (a.interleaved) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] = f[e ^ 1];
+          } else {
+            x[u].from(lane + far, LANES).get(p);
           }
-        } else {
-          const int i0 = lane * 8 - (second ? half : 0);
+          float g = 1.f;
+          if (weight) {
+            float ss = 0.f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float2 t = cs[i0 + e];
-            f[e] = second ? p[e] * t.y + f[e] * t.x : f[e] * t.x - p[e] * t.y;
+            for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
+#pragma unroll
+            for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, LANES);
+            g = rsqrtf(ss * (1.f / D) + a.eps);
           }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = (in ? fmaf(f[e], c[e], p[e] * s[e]) : f[e] * c[e]) * g;
         }
-      }
-      if (!live) continue;
-      if (is_q) {
-        Lane8<F32>::store(a.q, (row * a.hq + h) * D + lane * 8, f);
-      } else {
-        const int kh = h - a.hq - (is_k ? 0 : a.hkv);
-        Lane8<F32>::store(is_k ? a.k : a.v,
-                          ((static_cast<size_t>(b) * a.hkv + kh) * a.rows + r) * D + lane * 8, f);
+        const int next = h + U * HPP;  // the slot's next head
+        if (next < k1) x[u].load(a.qkv, src + static_cast<size_t>(next) * D);
+        if (h < k1) Lane8<F32>::store(out, (head0 + (h - first) * step) * D + lane * 8, f);
       }
     }
   }
@@ -184,7 +222,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
 
 cudaError_t launch_qk_norm_rope(const eagle_qk_norm_rope_desc& d, const void* qkv, const void* wq, const void* wk,
                                 const float* inv_freq, const int32_t* pos_id, const int32_t* n_nodes, void* q,
-                                void* k, void* v, cudaStream_t s) {
+                                void* k, void* v, int num_sms, cudaStream_t s) {
   RopeArgs a;
   a.qkv = qkv;
   a.wq = wq;
@@ -202,14 +240,24 @@ cudaError_t launch_qk_norm_rope(const eagle_qk_norm_rope_desc& d, const void* qk
   a.interleaved = d.interleaved;
   a.stride = d.row_stride > 0 ? d.row_stride : static_cast<long long>(d.n_q_heads + 2 * d.n_kv_heads) * d.head_dim;
   a.eps = d.eps;
-  const dim3 grid(d.rows, d.batch);
+  // a whole row to a warp when that makes 16 warps an SM or more, else shorter runs of heads
+  // (whole passes of 128 / D x 2 heads)
+  const int heads = d.n_q_heads + 2 * d.n_kv_heads, pass = 256 / d.head_dim;
+  const long long rows = static_cast<long long>(d.rows) * d.batch;
+  const long long want = 16ll * num_sms;
+  long long split = std::min<long long>((want + rows - 1) / rows, (heads + pass - 1) / pass);
+  a.run = static_cast<int>(((heads + split - 1) / split + pass - 1) / pass * pass);
+  a.runs = (heads + a.run - 1) / a.run;
+  a.units = rows * a.runs;
+  const long long grid = (a.units + kThreads / 32 - 1) / (kThreads / 32);
+  if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
   const bool f32 = d.dtype == EAGLE_F32;
   if (d.head_dim == 64)
-    f32 ? qk_norm_rope_kernel<true, 64><<<grid, kThreads, 0, s>>>(a)
-        : qk_norm_rope_kernel<false, 64><<<grid, kThreads, 0, s>>>(a);
+    f32 ? qk_norm_rope_kernel<true, 64><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a)
+        : qk_norm_rope_kernel<false, 64><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a);
   else
-    f32 ? qk_norm_rope_kernel<true, 128><<<grid, kThreads, 0, s>>>(a)
-        : qk_norm_rope_kernel<false, 128><<<grid, kThreads, 0, s>>>(a);
+    f32 ? qk_norm_rope_kernel<true, 128><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a)
+        : qk_norm_rope_kernel<false, 128><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 

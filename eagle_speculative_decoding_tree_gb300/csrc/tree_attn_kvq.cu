@@ -18,15 +18,18 @@
 // power-of-two scales every exponent offset is exact.
 //
 // Kernel (the split-KV shape of tree_attn.cu).  One CTA per (row block, split, request x KV
-// head): 128-key tiles of codes stream through a TMA ring (128-byte swizzle; 64-byte for
-// head_dim 64; one thread refills a stage once every warp is past it), eight warps take 16-key steps: codes go from shared memory to
-// registers once and become mma.sync m16n8k16 half fragments there, which is cheaper than
-// writing a half tile back for few rows (they are the bytes-bound case: R G <= 32 rows of one
-// decode or chain step).  The fragments' orders are free choices: a thread's 16 bytes of a key
-// are 16 head dims of the contraction, Q is stored to match; keys within a step are permuted
-// by exchanging bits 0 and 2 so that the swizzled reads fall in different banks.
-// Rows: wr warps side by side along the rows, 8 / wr along a tile's keys; their states merge
-// in shared memory at the end, splits in kvq_combine_kernel.
+// head), sixteen warps of 16 query rows each: 128-key tiles of codes stream through a TMA ring
+// (128-byte swizzle, 64-byte for head_dim 64; one thread refills a stage once its warps are past
+// it), and a warp takes 16-key steps of them: the codes go from shared memory to registers once
+// and become mma.sync m16n8k16 half fragments there, which is cheaper than writing a half tile
+// back when there are few rows.  That is the bytes-bound case (R G <= 32 rows of a decode or
+// chain step); a step is a chain of some 2000 cycles, so it takes sixteen warps' steps to keep
+// up with HBM.  The fragments' orders are free choices: a thread's 16 bytes of a key are 16 head
+// dims of the contraction, Q is stored to match; keys within a step are permuted by exchanging
+// bits 0 and 2 so that the swizzled reads fall in different banks.
+// wr warps stand side by side along the rows, 16 / wr along the keys; their states merge in
+// shared memory at the end.  Splits write fp32 partials; when the whole grid fits on the SMs
+// (cooperative launch) they merge in the kernel, else in kvq_combine_kernel.
 #include <algorithm>
 
 #include "common.cuh"
@@ -42,15 +45,15 @@ namespace {
 using namespace sm100;
 
 constexpr int KT = 128;       // keys per tile
-constexpr int NST = 4;        // ring stages
-constexpr int CW = 8;         // compute warps
+constexpr int MAX_ST = 6;     // ring stages: 6 up to 64 rows a CTA, 4 beyond (the query rows' space)
+constexpr int CW = 16;        // warps
 // A row's reference moves when its maximum grew by more than 2^kLazy, and P is stored as
 // p 2^PB <= 2^15: a half's smallest step then is 2^-35 of the largest p.  A larger kLazy saves
 // rescales, which are rare already at 2^4, and costs that range.
 constexpr float kLazy = 4.f;
 constexpr int PB = 11;
 
-enum : int { ERR_FULL = 1, ERR_EMPTY = 2 };
+enum : int { ERR_FULL = 1, ERR_EMPTY = 2, ERR_GROUP = 256 };
 
 struct Maps {
   CUtensorMap k, v;
@@ -88,64 +91,61 @@ __device__ __forceinline__ uint32_t pack_bf(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// One warp's rows: MT tiles of 16 (thread rows g and g + 8 of each), running state.
-template <int D, int MT>
+// A warp's 16 rows (thread rows g and g + 8): running state.
+template <int D>
 struct RowState {
-  float o[MT][D / 8][4];
-  float m[MT][2], l[MT][2];
+  float o[D / 8][4];
+  float m[2], l[2];
 };
 
-// Scores t (log2 units, masked -inf) of 16 keys x MT tiles: moves the reference maxima if
-// they must, turns t into p 2^lr (in place) and adds the row sums.
-template <int D, int MT>
-__device__ __forceinline__ void soften(RowState<D, MT>& st, float (&t)[MT][2][4], float lr) {
+// Scores t (log2 units, masked -inf) of 16 keys: moves the reference maxima if they must, turns
+// t into p 2^lr (in place) and adds the row sums.
+template <int D>
+__device__ __forceinline__ void soften(RowState<D>& st, float (&t)[2][4], float lr) {
   const float back = ex2(-lr);
+  float m_new[2];
+  bool move = false;
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    float m_new[2];
-    bool move = false;
+  for (int i = 0; i < 2; ++i) {
+    float mx = fmaxf(fmaxf(t[0][2 * i], t[0][2 * i + 1]), fmaxf(t[1][2 * i], t[1][2 * i + 1]));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    const bool up = mx > st.m[i] + kLazy || (st.m[i] == -INFINITY && mx > -INFINITY);
+    m_new[i] = up ? ceilf(mx) : st.m[i];
+    move |= up;
+  }
+  if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      float mx = fmaxf(fmaxf(t[mt][0][2 * i], t[mt][0][2 * i + 1]), fmaxf(t[mt][1][2 * i], t[mt][1][2 * i + 1]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const bool up = mx > st.m[mt][i] + kLazy || (st.m[mt][i] == -INFINITY && mx > -INFINITY);
-      m_new[i] = up ? ceilf(mx) : st.m[mt][i];
-      move |= up;
-    }
-    if (__any_sync(0xffffffffu, move)) {
+      const float al = st.m[i] == -INFINITY ? 0.f : ex2(st.m[i] - m_new[i]);
+      st.m[i] = m_new[i];
+      st.l[i] *= al;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float al = st.m[mt][i] == -INFINITY ? 0.f : ex2(st.m[mt][i] - m_new[i]);
-        st.m[mt][i] = m_new[i];
-        st.l[mt][i] *= al;
-#pragma unroll
-        for (int j = 0; j < D / 8; ++j) {
-          st.o[mt][j][2 * i] *= al;
-          st.o[mt][j][2 * i + 1] *= al;
-        }
+      for (int j = 0; j < D / 8; ++j) {
+        st.o[j][2 * i] *= al;
+        st.o[j][2 * i + 1] *= al;
       }
     }
+  }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float off = lr - (st.m[mt][i] == -INFINITY ? 0.f : st.m[mt][i]);
-      float sum = 0.f;
+  for (int i = 0; i < 2; ++i) {
+    const float off = lr - (st.m[i] == -INFINITY ? 0.f : st.m[i]);
+    float sum = 0.f;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int e = 2 * i; e < 2 * i + 2; ++e) {
-          t[mt][j][e] = ex2(t[mt][j][e] + off);
-          sum += t[mt][j][e];
-        }
-      st.l[mt][i] = fmaf(sum, back, st.l[mt][i]);
-    }
+      for (int e = 2 * i; e < 2 * i + 2; ++e) {
+        t[j][e] = ex2(t[j][e] + off);
+        sum += t[j][e];
+      }
+    st.l[i] = fmaf(sum, back, st.l[i]);
   }
 }
 
 template <int D>
 __host__ __device__ constexpr int q_stride() { return D * 2 + 8; }  // bytes; 2 words past a bank row per row
 
-template <int D, int MT, bool TERMS2>
+template <int D, bool TERMS2>
 __global__ void __launch_bounds__(CW * 32, 1)
     tree_attn_kvq_kernel(const __grid_constant__ Maps tm, const KvqAttnArgs a) {
   constexpr int TILE = KT * D;  // bytes of one K or V tile
@@ -154,20 +154,22 @@ __global__ void __launch_bounds__(CW * 32, 1)
   constexpr int VB = D / 8;     // head dims of a thread's V column
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sq = ring + NST * 2 * TILE;
-  __shared__ uint64_t full[NST], empty[NST];
-  __shared__ float s_qs[CW * 32], s_m[CW][32], s_l[CW][32], s_vr[CW];
+  const int nst = a.nst;
+  uint8_t* sq = ring + nst * 2 * TILE;
+  __shared__ uint64_t full[MAX_ST], empty[MAX_ST];
+  __shared__ float s_qs[CW * 16], s_m[CW][16], s_l[CW][16], s_vr[CW];
+  __shared__ int go;
 
   const int rb = blockIdx.x, split = blockIdx.y, bh = blockIdx.z;
   const int b = bh / a.Hkv, h = bh % a.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
-  const int wr = a.wr, wk = CW / wr, rows_cta = wr * MT * 16;
+  const int wr = a.wr, wk = CW / wr, rows_cta = wr * 16;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < NST; ++s) {
+    for (int s = 0; s < nst; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], CW);
+      mbar_init(&empty[s], min(CW, wr * 8));  // the warps with a step in a tile
     }
     fence_barrier_init();
   }
@@ -189,14 +191,14 @@ __global__ void __launch_bounds__(CW * 32, 1)
 
   const uint64_t policy = policy_evict_first();
   auto load_tile = [&](int t) {
-    const int s = t % NST, y = bh * a.P + (u0 + t) * KT;
+    const int s = t % nst, y = bh * a.P + (u0 + t) * KT;
     mbar_arrive_expect_tx(&full[s], 2 * TILE);
     tma_load_2d_hint(ring + s * 2 * TILE, &tm.k, 0, y, &full[s], policy);
     tma_load_2d_hint(ring + s * 2 * TILE + TILE, &tm.v, 0, y, &full[s], policy);
   };
   int issued = 0;  // thread 0: tiles whose loads have gone out; the first before anything else is read
   if (threadIdx.x == 0)
-    for (; issued < min(n_pt, NST); ++issued) load_tile(issued);
+    for (; issued < min(n_pt, nst); ++issued) load_tile(issued);
   // vref: the largest V scale of the key range
   float vm = 0.f;
   for (int i = threadIdx.x; i < n_blk; i += CW * 32) vm = fmaxf(vm, __ldg(vs + i));
@@ -242,96 +244,84 @@ __global__ void __launch_bounds__(CW * 32, 1)
 
   bool ok = true;
   const int wrow = warp % wr, wkey = warp / wr;
-  const int r0 = wrow * MT * 16;  // first row of the warp within the CTA
-  RowState<D, MT> st;
+  const int r0 = wrow * 16;  // first row of the warp within the CTA
+  RowState<D> st;
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
+  for (int j = 0; j < D / 8; ++j) st.o[j][0] = st.o[j][1] = st.o[j][2] = st.o[j][3] = 0.f;
+  st.m[0] = st.m[1] = -INFINITY;
+  st.l[0] = st.l[1] = 0.f;
+  float cr[2];  // row factors of the scores
 #pragma unroll
-    for (int j = 0; j < D / 8; ++j) st.o[mt][j][0] = st.o[mt][j][1] = st.o[mt][j][2] = st.o[mt][j][3] = 0.f;
-    st.m[mt][0] = st.m[mt][1] = -INFINITY;
-    st.l[mt][0] = st.l[mt][1] = 0.f;
-  }
-  float cr[MT][2];  // row factors of the scores
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) cr[mt][i] = a.scale_log2 * s_qs[r0 + mt * 16 + g + 8 * i];
+  for (int i = 0; i < 2; ++i) cr[i] = a.scale_log2 * s_qs[r0 + g + 8 * i];
 
-  // ---- prefix: 16-key steps wkey, wkey + wk, ... of every tile
+  // ---- prefix: of the piece's 16-key steps (8 to a tile) those with index wkey modulo wk
   const int gs = (g & 2) | ((g & 1) << 2) | (g >> 2);      // key of column g within 8: bits 0 and 2 exchanged
   const int cs = ((2 * c) & 2) | ((2 * c) >> 2);           // key of column 2 c; column 2 c + 1 is cs + 4
   const int swz = D == 128 ? gs : (gs >> 1) & 3;           // chunk swizzle of key gs (and gs + 8)
   const uint32_t qrow = smem_u32(sq) + static_cast<uint32_t>((r0 + g) * q_stride<D>() + 32 * c);
   float ks_n = 0.f, vs_n = 0.f;
-  {
+  if (n_pt > 0) {
     const int kb = min(wkey * 16 / kQB, n_blk - 1);
-    if (n_pt > 0) ks_n = __ldg(ks + kb), vs_n = __ldg(vs + kb);
+    ks_n = __ldg(ks + kb);
+    vs_n = __ldg(vs + kb);
   }
-  for (int t = 0; t < n_pt && ok; ++t) {
-    const int s = t % NST;
-    ok = __all_sync(0xffffffffu, wait_parity(&full[s], (t / NST) & 1, a.err, ERR_FULL));
+  for (int sx = wkey; sx < n_pt * 8 && ok;) {
+    const int t = sx >> 3, s = t % nst;
+    ok = __all_sync(0xffffffffu, wait_parity(&full[s], (t / nst) & 1, a.err, ERR_FULL));
     if (!ok) break;
     const int nv = min(KT, L - (u0 + t) * KT);
     const uint8_t* tk = ring + s * 2 * TILE;
     const uint8_t* tv = tk + TILE;
-    for (int step = wkey; step < KT / 16; step += wk) {
+    for (; sx < 8 * t + 8; sx += wk) {
+      const int step = sx & 7;
       const float ksb = ks_n, vsb = vs_n;
       {  // the next step's scales
-        const int nx = step + wk < KT / 16 ? t * KT + (step + wk) * 16 : (t + 1) * KT + wkey * 16;
-        const int kb = min(nx / kQB, n_blk - 1);
+        const int kb = min((sx + wk) * 16 / kQB, n_blk - 1);
         ks_n = __ldg(ks + kb);
         vs_n = __ldg(vs + kb);
       }
       const int nk = nv - step * 16;  // valid keys of the step
       if (nk <= 0) continue;
-      float sc[MT][2][4];
+      float sc[2][4];
+      uint32_t kw[2][KS];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const uint8_t* kr = tk + (step * 16 + 8 * j + gs) * D;
-        uint32_t w[KS];
 #pragma unroll
         for (int i = 0; i < CH / 4; ++i) {
           const uint4 u = *reinterpret_cast<const uint4*>(kr + (((c + 4 * i) ^ swz) << 4));
-          w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+          kw[j][4 * i] = u.x, kw[j][4 * i + 1] = u.y, kw[j][4 * i + 2] = u.z, kw[j][4 * i + 3] = u.w;
         }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) sc[mt][j][0] = sc[mt][j][1] = sc[mt][j][2] = sc[mt][j][3] = 0.f;
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const uint32_t b0 = kvq_half2(w[k]), b1 = kvq_half2(w[k] >> 16);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            uint32_t qa[4];
-            const uint32_t at = qrow + mt * 16 * q_stride<D>() + (k >> 2) * 128 + (k & 3) * 8;
-            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(qa[0]), "=r"(qa[2]) : "r"(at));
-            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(qa[1]), "=r"(qa[3]) : "r"(at + 8 * q_stride<D>()));
-            mma_f16(sc[mt][j], qa, b0, b1);
-          }
-        }
+        sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
       }
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int k = 0; k < KS; ++k) {
+        uint32_t qa[4];
+        const uint32_t at = qrow + (k >> 2) * 128 + (k & 3) * 8;
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(qa[0]), "=r"(qa[2]) : "r"(at));
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(qa[1]), "=r"(qa[3]) : "r"(at + 8 * q_stride<D>()));
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 2; ++j) mma_f16(sc[j], qa, kvq_half2(kw[j][k]), kvq_half2(kw[j][k] >> 16));
+      }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            sc[mt][j][e] *= cr[mt][e >> 1] * ksb;
-            if (nk < 16 && 8 * j + cs + 4 * (e & 1) >= nk) sc[mt][j][e] = -INFINITY;
-          }
-      const float lr = fmaxf(__log2f(vsb * vinv), -100.f) + PB;
-      soften<D, MT>(st, sc, lr);
-      uint32_t pa[MT][4], pl[MT][4];
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float x0 = sc[mt][k >> 1][2 * (k & 1)], x1 = sc[mt][k >> 1][2 * (k & 1) + 1];
-          pa[mt][k] = pack_half(x0, x1);
-          if (TERMS2) {
-            const float2 hi = unpack_half(pa[mt][k]);
-            pl[mt][k] = pack_half(x0 - hi.x, x1 - hi.y);
-          }
+        for (int e = 0; e < 4; ++e) {
+          sc[j][e] *= cr[e >> 1] * ksb;
+          if (nk < 16 && 8 * j + cs + 4 * (e & 1) >= nk) sc[j][e] = -INFINITY;
         }
+      const float lr = fmaxf(__log2f(vsb * vinv), -100.f) + PB;
+      soften<D>(st, sc, lr);
+      uint32_t pa[4], pl[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float x0 = sc[k >> 1][2 * (k & 1)], x1 = sc[k >> 1][2 * (k & 1) + 1];
+        pa[k] = pack_half(x0, x1);
+        if (TERMS2) {
+          const float2 hi = unpack_half(pa[k]);
+          pl[k] = pack_half(x0 - hi.x, x1 - hi.y);
+        }
+      }
       // V: this thread's column g is head dims VB g .. VB g + VB - 1; its keys are columns
       // 2 c, 2 c + 1 of both 8-key halves
       uint32_t vw[4][VB / 4];
@@ -364,94 +354,84 @@ __global__ void __launch_bounds__(CW * 32, 1)
         for (int y = 0; y < 4; ++y) {
           const uint32_t b0 = kvq_half2(e[0][y >> 1] >> (16 * (y & 1)));
           const uint32_t b1 = kvq_half2(e[1][y >> 1] >> (16 * (y & 1)));
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            mma_f16(st.o[mt][4 * q + y], pa[mt], b0, b1);
-            if (TERMS2) mma_f16(st.o[mt][4 * q + y], pl[mt], b0, b1);
-          }
+          mma_f16(st.o[4 * q + y], pa, b0, b1);
+          if (TERMS2) mma_f16(st.o[4 * q + y], pl, b0, b1);
         }
       }
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[s]);
-    // refill the stage of the tile before this one: the other warps are past it by now
-    if (threadIdx.x == 0 && t > 0 && issued < n_pt) {
-      if (wait_parity(&empty[(t - 1) % NST], ((t - 1) / NST) & 1, a.err, ERR_EMPTY))
+    // refill the stage of the last tile that this warp was past before: the others are too by now
+    if (threadIdx.x == 0) {
+      while (issued < n_pt && issued - nst < t) {
+        if (!wait_parity(&empty[issued % nst], (issued / nst - 1) & 1, a.err, ERR_EMPTY)) {
+          ok = false;
+          break;
+        }
         load_tile(issued++);
-      else
-        ok = false;
+      }
     }
     ok = __all_sync(0xffffffffu, ok);
   }
   // no copy may still be landing when the ring is used for the merge or the CTA ends
   if (threadIdx.x == 0)
-    for (int s = 0; s < NST && s < issued; ++s)
-      (void)wait_parity(&full[s], ((issued - 1 - s) / NST) & 1, a.err, ERR_FULL);
+    for (int s = 0; s < nst && s < issued; ++s)
+      (void)wait_parity(&full[s], ((issued - 1 - s) / nst) & 1, a.err, ERR_FULL);
 
   // ---- the tree's own K/V (bf16, straight from global memory): 16-key steps shared out in
   // the same way; P always as two bf16 terms
   if (tree && ok) {
     const uint16_t* kb = a.tk + static_cast<size_t>(bh) * a.R * D;
     const uint16_t* vb = a.tv + static_cast<size_t>(bh) * a.R * D;
-    const uint16_t* qp[MT][2];
-    const uint64_t* mp[MT][2];
-    bool live[MT][2];
+    const uint16_t* qp[2];
+    const uint64_t* mp[2];
+    bool live[2];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = rb * rows_cta + r0 + mt * 16 + g + 8 * i;
-        live[mt][i] = row < RG;
-        const int node = live[mt][i] ? row / a.G : 0, hq = h * a.G + (live[mt][i] ? row % a.G : 0);
-        qp[mt][i] = a.q + ((static_cast<size_t>(b) * a.R + node) * a.Hq + hq) * D + 16 * c;
-        mp[mt][i] = a.anc_mask + (static_cast<size_t>(b) * a.R + node) * a.W;
-      }
+    for (int i = 0; i < 2; ++i) {
+      const int row = rb * rows_cta + r0 + g + 8 * i;
+      live[i] = row < RG;
+      const int node = live[i] ? row / a.G : 0, hq = h * a.G + (live[i] ? row % a.G : 0);
+      qp[i] = a.q + ((static_cast<size_t>(b) * a.R + node) * a.Hq + hq) * D + 16 * c;
+      mp[i] = a.anc_mask + (static_cast<size_t>(b) * a.R + node) * a.W;
+    }
     const float lr = PB - __log2f(vref);
     for (int step = wkey; step * 16 < Rb; step += wk) {
-      float sc[MT][2][4];
+      float sc[2][4];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int key = step * 16 + 8 * j + g;
         const uint16_t* kr = kb + static_cast<size_t>(min(key, Rb - 1)) * D + 16 * c;
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) sc[mt][j][0] = sc[mt][j][1] = sc[mt][j][2] = sc[mt][j][3] = 0.f;
+        sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           const uint2 kw = *reinterpret_cast<const uint2*>(kr + (k >> 2) * 64 + (k & 3) * 4);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            const uint2 q0 = *reinterpret_cast<const uint2*>(qp[mt][0] + (k >> 2) * 64 + (k & 3) * 4);
-            const uint2 q1 = *reinterpret_cast<const uint2*>(qp[mt][1] + (k >> 2) * 64 + (k & 3) * 4);
-            const uint32_t qa[4] = {q0.x, q1.x, q0.y, q1.y};
-            mma_bf16(sc[mt][j], qa, kw.x, kw.y);
-          }
+          const uint2 q0 = *reinterpret_cast<const uint2*>(qp[0] + (k >> 2) * 64 + (k & 3) * 4);
+          const uint2 q1 = *reinterpret_cast<const uint2*>(qp[1] + (k >> 2) * 64 + (k & 3) * 4);
+          const uint32_t qa[4] = {q0.x, q1.x, q0.y, q1.y};
+          mma_bf16(sc[j], qa, kw.x, kw.y);
         }
       }
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int i = 0; i < 2; ++i) {
+        const int k0 = step * 16;
+        const uint64_t word = live[i] ? mp[i][k0 >> 6] : 0ull;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int k0 = step * 16;
-          const uint64_t word = live[mt][i] ? mp[mt][i][k0 >> 6] : 0ull;
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int e = 0; e < 2; ++e) {
+            const int key = k0 + 8 * j + 2 * c + e;
+            const bool on = key < Rb && ((word >> (key & 63)) & 1ull);
+            sc[j][2 * i + e] = on ? sc[j][2 * i + e] * a.scale_log2 : -INFINITY;
+          }
+      }
+      soften<D>(st, sc, lr);
+      uint32_t pa[4], pl[4];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int key = k0 + 8 * j + 2 * c + e;
-              const bool on = key < Rb && ((word >> (key & 63)) & 1ull);
-              sc[mt][j][2 * i + e] = on ? sc[mt][j][2 * i + e] * a.scale_log2 : -INFINITY;
-            }
-        }
-      soften<D, MT>(st, sc, lr);
-      uint32_t pa[MT][4], pl[MT][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float x0 = sc[mt][k >> 1][2 * (k & 1)], x1 = sc[mt][k >> 1][2 * (k & 1) + 1];
-          pa[mt][k] = pack_bf(x0, x1);
-          pl[mt][k] = pack_bf(x0 - __uint_as_float(pa[mt][k] << 16), x1 - __uint_as_float(pa[mt][k] & 0xffff0000u));
-        }
+      for (int k = 0; k < 4; ++k) {
+        const float x0 = sc[k >> 1][2 * (k & 1)], x1 = sc[k >> 1][2 * (k & 1) + 1];
+        pa[k] = pack_bf(x0, x1);
+        pl[k] = pack_bf(x0 - __uint_as_float(pa[k] << 16), x1 - __uint_as_float(pa[k] & 0xffff0000u));
+      }
 #pragma unroll
       for (int q = 0; q < VB / 4; ++q) {  // 4 head dims at a time
         uint2 w[4];
@@ -466,11 +446,8 @@ __global__ void __launch_bounds__(CW * 32, 1)
           const uint32_t sel = (y & 1) ? 0x7632 : 0x5410;
           const uint32_t b0 = __byte_perm(y < 2 ? w[0].x : w[0].y, y < 2 ? w[1].x : w[1].y, sel);
           const uint32_t b1 = __byte_perm(y < 2 ? w[2].x : w[2].y, y < 2 ? w[3].x : w[3].y, sel);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            mma_bf16(st.o[mt][4 * q + y], pa[mt], b0, b1);
-            mma_bf16(st.o[mt][4 * q + y], pl[mt], b0, b1);
-          }
+          mma_bf16(st.o[4 * q + y], pa, b0, b1);
+          mma_bf16(st.o[4 * q + y], pl, b0, b1);
         }
       }
     }
@@ -478,30 +455,24 @@ __global__ void __launch_bounds__(CW * 32, 1)
 
   // ---- merge the key warps of the CTA: the row's states meet in shared memory
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      st.l[mt][i] += __shfl_xor_sync(0xffffffffu, st.l[mt][i], 1);
-      st.l[mt][i] += __shfl_xor_sync(0xffffffffu, st.l[mt][i], 2);
-      if (c == 0) {
-        s_m[warp][mt * 16 + g + 8 * i] = st.m[mt][i];
-        s_l[warp][mt * 16 + g + 8 * i] = st.l[mt][i];
-      }
+  for (int i = 0; i < 2; ++i) {
+    st.l[i] += __shfl_xor_sync(0xffffffffu, st.l[i], 1);
+    st.l[i] += __shfl_xor_sync(0xffffffffu, st.l[i], 2);
+    if (c == 0) {
+      s_m[warp][g + 8 * i] = st.m[i];
+      s_l[warp][g + 8 * i] = st.l[i];
     }
+  }
   __syncthreads();  // the ring is free
-  float* so = reinterpret_cast<float*>(ring) + static_cast<size_t>(warp) * (MT * 16 * D);
+  float* so = reinterpret_cast<float*>(ring) + static_cast<size_t>(warp) * (16 * D);
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int e = 0; e < 2; ++e)
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int j = 0; j < VB; j += 4)  // chunk index XORed with the row: the quads' rows fall in different banks
-          *reinterpret_cast<float4*>(so + (mt * 16 + g + 8 * i) * D +
-                                     ((((VB * (2 * c + e) + j) >> 2) ^ g) << 2)) =
-              make_float4(st.o[mt][j][2 * i + e], st.o[mt][j + 1][2 * i + e], st.o[mt][j + 2][2 * i + e],
-                          st.o[mt][j + 3][2 * i + e]);
+      for (int j = 0; j < VB; j += 4)  // chunk index XORed with the row: the quads' rows fall in different banks
+        *reinterpret_cast<float4*>(so + (g + 8 * i) * D + ((((VB * (2 * c + e) + j) >> 2) ^ g) << 2)) =
+            make_float4(st.o[j][2 * i + e], st.o[j + 1][2 * i + e], st.o[j + 2][2 * i + e], st.o[j + 3][2 * i + e]);
   __syncthreads();
   const float unit = vref * (1.f / (1 << PB));
   constexpr int QD = D / 4;  // threads of a row, 4 dims each
@@ -509,7 +480,7 @@ __global__ void __launch_bounds__(CW * 32, 1)
     const int r = idx / QD, q = idx % QD;
     const int row = rb * rows_cta + r;
     if (row >= RG) break;
-    const int w0 = r / (MT * 16), rr = r % (MT * 16);
+    const int w0 = r / 16, rr = r % 16;
     float M = -INFINITY;
     for (int k = 0; k < wk; ++k) M = fmaxf(M, s_m[w0 + k * wr][rr]);
     float lsum = 0.f;
@@ -518,13 +489,10 @@ __global__ void __launch_bounds__(CW * 32, 1)
       const int w = w0 + k * wr;
       const float f = s_m[w][rr] == -INFINITY ? 0.f : ex2(s_m[w][rr] - M);
       const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<float*>(ring) +
-                                                        static_cast<size_t>(w) * (MT * 16 * D) + rr * D +
-                                                        ((q ^ (rr & 7)) << 2));
+                                                        static_cast<size_t>(w) * (16 * D) + rr * D + ((q ^ (rr & 7)) << 2));
       lsum = fmaf(f, s_l[w][rr], lsum);
-      if (f != 0.f) {
-        acc.x = fmaf(f, x.x, acc.x), acc.y = fmaf(f, x.y, acc.y);
-        acc.z = fmaf(f, x.z, acc.z), acc.w = fmaf(f, x.w, acc.w);
-      }
+      acc.x = fmaf(f, x.x, acc.x), acc.y = fmaf(f, x.y, acc.y);
+      acc.z = fmaf(f, x.z, acc.z), acc.w = fmaf(f, x.w, acc.w);
     }
     if (a.splits > 1) {
       const size_t prow = (static_cast<size_t>(bh) * a.splits + split) * a.rows_pad + row;
@@ -541,6 +509,23 @@ __global__ void __launch_bounds__(CW * 32, 1)
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + 4 * q) =
             make_uint2(pack_bf(acc.x * inv, acc.y * inv), pack_bf(acc.z * inv, acc.w * inv));
       if (a.lse && q == 0) a.lse[orow] = (M + log2f(lsum)) * 0.69314718055994531f;
+    }
+  }
+  if (a.coop) {
+    // the group's merge (request, KV head, row block): an even share of its rows, a warp per row
+    const int need = min(a.splits, (n_pref + a.tps) / a.tps);
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0)
+      go = kvq_group_wait(a.cnt + 2 * (bh * gridDim.x + rb), need, a.err, ERR_GROUP) ? 1 : 0;
+    __syncthreads();
+    if (go) {
+      const int n = min(rows_cta, RG - rb * rows_cta), hi = (split + 1) * n / need;
+      for (int k = split * n / need + warp; k < hi; k += CW) {
+        const int row = rb * rows_cta + k;
+        kvq_merge_row<D, 16>(a, static_cast<size_t>(bh) * a.splits * a.rows_pad + row, need,
+                             (static_cast<size_t>(b) * a.R + row / a.G) * a.Hq + h * a.G + row % a.G, lane);
+      }
     }
   }
 }
@@ -575,11 +560,11 @@ cudaError_t launch_combine(const KvqAttnPlan& p, const KvqAttnArgs& a, cudaStrea
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int D, int MT, bool T2>
+template <int D, bool T2>
 cudaError_t launch_mma(const KvqAttnPlan& p, const Maps& tm, const KvqAttnArgs& a, cudaStream_t s) {
-  auto kern = tree_attn_kvq_kernel<D, MT, T2>;
-  const int smem = 1024 + NST * 2 * KT * D + p.rows_per_cta * q_stride<D>();
-  const int most = 1024 + NST * 2 * KT * D + CW * MT * 16 * q_stride<D>();
+  auto kern = tree_attn_kvq_kernel<D, T2>;
+  const int smem = 1024 + a.nst * 2 * KT * D + p.rows_per_cta * q_stride<D>();
+  const int most = 1024 + std::max(4 * 2 * KT * D + CW * 16 * q_stride<D>(), MAX_ST * 2 * KT * D + 64 * q_stride<D>());
   // opt in to the largest size once per device (not a stream operation)
   static unsigned long long configured = 0;
   int dev = 0;
@@ -592,16 +577,18 @@ cudaError_t launch_mma(const KvqAttnPlan& p, const Maps& tm, const KvqAttnArgs& 
   }
   cudaLaunchConfig_t cfg = {};
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeCooperative;  // all CTAs resident, or the launch fails
+  attr[1].val.cooperative = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = p.coop ? 2 : 1;
   cfg.gridDim = dim3(p.row_blocks, p.splits, p.B * p.Hkv);
   cfg.blockDim = dim3(CW * 32);
   cfg.dynamicSmemBytes = smem;
   e = cudaLaunchKernelEx(&cfg, kern, tm, a);
-  if (e != cudaSuccess || p.splits == 1) return e;
+  if (e != cudaSuccess || p.splits == 1 || p.coop) return e;
   return launch_combine<D>(p, a, s);
 }
 
@@ -625,7 +612,6 @@ void plan_kvq_attn(const eagle_attn_desc* d, int num_sms, KvqAttnPlan* p) {
   p->tc = d->engine == EAGLE_ENGINE_AUTO && p->D == 128 && RG > 32 && p->G <= 4096;
   p->coop = false;
   if (p->tc) {
-    p->mt = 0;
     p->wr = RG > 128 ? 2 : 1;
     p->rows_per_cta = p->wr * 128;
     p->row_blocks = (RG + p->rows_per_cta - 1) / p->rows_per_cta;
@@ -639,11 +625,10 @@ void plan_kvq_attn(const eagle_attn_desc* d, int num_sms, KvqAttnPlan* p) {
     p->splits = (tiles + p->tps - 1) / p->tps + 1;
     p->coop = base * p->splits <= num_sms;
   } else {
-    // rows of a CTA: as few warps along the rows as cover them, up to 8 x 32
-    p->mt = RG <= 16 ? 1 : 2;
+    // rows of a CTA: as few warps along the rows as cover them, up to 16 x 16
     p->wr = 1;
-    while (p->wr < CW && p->wr * p->mt * 16 < RG) p->wr *= 2;
-    p->rows_per_cta = p->wr * p->mt * 16;
+    while (p->wr < CW && p->wr * 16 < RG) p->wr *= 2;
+    p->rows_per_cta = p->wr * 16;
     p->row_blocks = (RG + p->rows_per_cta - 1) / p->rows_per_cta;
     // pieces of tps 128-key units (the tree counts as one): one wave of CTAs when the groups
     // are few, pieces of at least 16 units when they are many
@@ -653,6 +638,7 @@ void plan_kvq_attn(const eagle_attn_desc* d, int num_sms, KvqAttnPlan* p) {
     splits = std::min<long long>(std::min<long long>(splits, tiles + 1), 256);
     p->tps = static_cast<int>((tiles + splits) / splits);
     p->splits = (tiles + p->tps) / p->tps;
+    p->coop = p->splits > 1 && base * p->splits <= num_sms;
   }
   p->rows_pad = p->row_blocks * p->rows_per_cta;
   p->off_err = 0;
@@ -706,6 +692,7 @@ cudaError_t launch_kvq_attn(const KvqAttnPlan& p, const void* q, const void* k8,
   a.out_f32 = p.out_f32;
   a.wr = p.wr;
   a.tc = p.tc ? 1 : 0;
+  a.nst = p.rows_per_cta <= 64 ? MAX_ST : 4;
   a.g_inv = p.G > 1 ? static_cast<uint32_t>(((1ull << 32) + p.G - 1) / p.G) : 0u;
   a.scale = p.scale;
   a.scale_log2 = p.scale * kLog2e;
@@ -719,12 +706,8 @@ cudaError_t launch_kvq_attn(const KvqAttnPlan& p, const void* q, const void* k8,
   if (!make_tmap_2d(&tm.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, k8, p.D, rows, p.D, KT, sw) ||
       !make_tmap_2d(&tm.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, v8, p.D, rows, p.D, KT, sw))
     return cudaErrorInvalidValue;
-  if (p.D == 64) {
-    if (p.mt == 1) return p.terms2 ? launch_mma<64, 1, true>(p, tm, a, s) : launch_mma<64, 1, false>(p, tm, a, s);
-    return p.terms2 ? launch_mma<64, 2, true>(p, tm, a, s) : launch_mma<64, 2, false>(p, tm, a, s);
-  }
-  if (p.mt == 1) return p.terms2 ? launch_mma<128, 1, true>(p, tm, a, s) : launch_mma<128, 1, false>(p, tm, a, s);
-  return p.terms2 ? launch_mma<128, 2, true>(p, tm, a, s) : launch_mma<128, 2, false>(p, tm, a, s);
+  if (p.D == 64) return p.terms2 ? launch_mma<64, true>(p, tm, a, s) : launch_mma<64, false>(p, tm, a, s);
+  return p.terms2 ? launch_mma<128, true>(p, tm, a, s) : launch_mma<128, false>(p, tm, a, s);
 }
 
 }  // namespace eagle

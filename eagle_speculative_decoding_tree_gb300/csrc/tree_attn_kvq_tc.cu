@@ -710,25 +710,9 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
         // until every piece that has work has counted, then merge an even share of its rows from
         // L2, a warp per row.  A piece that gave up counts too: the others need not wait for it.
         const int need = 1 + min(a.splits - 1, (n_pref + a.tps - 1) / a.tps);
-        int* cnt = a.cnt + 2 * (bh * gridDim.z + rb);
         __threadfence();
         bar_sync(1, 256);
-        if (threadIdx.x == 0) {
-          atomicAdd(cnt, 1);
-          const uint64_t t0 = global_ns();
-          bool all = ld_acquire_gpu(cnt) >= need;
-          while (!all && global_ns() - t0 < 2000000000ull) {
-            __nanosleep(64);
-            all = ld_acquire_gpu(cnt) >= need;
-          }
-          if (!all) atomicOr(a.err, ERR_GROUP);
-          go = all ? 1 : 0;
-          // past the wait: the last piece to get here returns both counters to zero
-          if (atomicAdd(cnt + 1, 1) == need - 1) {
-            atomicExch(cnt, 0);
-            atomicExch(cnt + 1, 0);
-          }
-        }
+        if (threadIdx.x == 0) go = kvq_group_wait(a.cnt + 2 * (bh * gridDim.z + rb), need, a.err, ERR_GROUP) ? 1 : 0;
         bar_sync(1, 256);
         if (go) {
           const int n = min(two ? 256 : 128, RG - row0);
