@@ -167,7 +167,7 @@ struct KvqAttnPlan {
   int B, R, Hq, Hkv, G, D, P, W, out_f32;
   bool terms2;      // P as two half terms (EAGLE_ATTN_PRECISE)
   float scale;
-  bool tc;          // tcgen05 kernel
+  bool tc, few;     // tcgen05 kernels: row tiles of 128; up to 32 rows
   int wr;           // mma.sync: warps of 16 rows side by side (16 / wr share the keys); tcgen05: wr
                     // row tiles of 128
   int rows_per_cta, row_blocks, rows_pad;
@@ -200,6 +200,7 @@ struct KvqAttnArgs {
   float scale, scale_log2;
 };
 cudaError_t launch_kvq_attn_tc(const KvqAttnPlan& p, const KvqAttnArgs& a, cudaStream_t s);
+cudaError_t launch_kvq_attn_few(const KvqAttnPlan& p, const KvqAttnArgs& a, cudaStream_t s);
 cudaError_t launch_kvq_attn(const KvqAttnPlan& p, const void* q, const void* k8, const float* ks, const void* v8,
                             const float* vs, const void* tree_k, const void* tree_v, const int32_t* seq_len,
                             const int32_t* n_nodes, const uint64_t* anc_mask, void* out, float* lse, void* ws,

@@ -608,12 +608,15 @@ void plan_kvq_attn(const eagle_attn_desc* d, int num_sms, KvqAttnPlan* p) {
   p->scale = d->scale;
   const int RG = p->R * p->G;
   const int tiles = (p->P + KT - 1) / KT;
-  // the tcgen05 kernel's row tiles are 128 rows whether or not they are filled
-  p->tc = d->engine == EAGLE_ENGINE_AUTO && p->D == 128 && RG > 32 && p->G <= 4096;
+  // head_dim 128 runs on tcgen05: up to 32 rows with the keys on the 128-row side, more in row
+  // tiles of 128
+  const bool tcgen = d->engine == EAGLE_ENGINE_AUTO && p->D == 128 && p->G <= 4096;
+  p->few = tcgen && RG <= 32;
+  p->tc = tcgen && !p->few;
   p->coop = false;
-  if (p->tc) {
+  if (p->tc || p->few) {
     p->wr = RG > 128 ? 2 : 1;
-    p->rows_per_cta = p->wr * 128;
+    p->rows_per_cta = p->few ? (RG <= 16 ? 16 : 32) : p->wr * 128;
     p->row_blocks = (RG + p->rows_per_cta - 1) / p->rows_per_cta;
     // one wave of CTAs (one per SM: all of TMEM) while the groups leave room for a prefix
     // piece and the tree each, pieces of 16 tiles when they do not
@@ -691,13 +694,13 @@ cudaError_t launch_kvq_attn(const KvqAttnPlan& p, const void* q, const void* k8,
   a.rows_pad = p.rows_pad;
   a.out_f32 = p.out_f32;
   a.wr = p.wr;
-  a.tc = p.tc ? 1 : 0;
+  a.tc = p.tc || p.few ? 1 : 0;
   a.nst = p.rows_per_cta <= 64 ? MAX_ST : 4;
   a.g_inv = p.G > 1 ? static_cast<uint32_t>(((1ull << 32) + p.G - 1) / p.G) : 0u;
   a.scale = p.scale;
   a.scale_log2 = p.scale * kLog2e;
-  if (p.tc) {
-    const cudaError_t e = launch_kvq_attn_tc(p, a, s);
+  if (p.tc || p.few) {
+    const cudaError_t e = p.tc ? launch_kvq_attn_tc(p, a, s) : launch_kvq_attn_few(p, a, s);
     return e != cudaSuccess || p.coop ? e : launch_combine<128>(p, a, s);
   }
   Maps tm;

@@ -1,0 +1,586 @@
+// tree_attn_kvq_few.cu -- tree attention over the 8-bit KV cache for few query rows (R G <= 32,
+// head_dim 128: single tokens, chains) on the tcgen05 tensor cores, with keys on the 128-row side
+// of the products; tree_attn_kvq.cu has the operation.
+//
+// Few rows against a long cache are bound by the cache's bytes, so nothing else may cost much:
+//     S^T = K Q^T     M = 128 keys (K codes as they lie), N = the rows' hi | lo terms
+//     O^T = V^T P^T   M = 128 head dims (V codes as they lie, MN-major), N = the rows' P terms
+// Both read a tile's codes once, straight from the TMA ring; no tile is converted.  All rounding
+// is on the small side:
+//   q  as in tree_attn_kvq_tc.cu: a power of two puts a row's largest element in (224, 448], and
+//      q = hi + lo in e4m3 keeps bf16's bits down to elements of 2^-11 of it;
+//   p  2^PB vs / vref is rounded to a half (11 bits, steps of 2^-35 of the largest p) and that
+//      half is written as four e5m2 terms, exactly: each takes three bits, and what it leaves is
+//      multiplied by 8.  EAGLE_ATTN_PRECISE: two more terms of what the half left (2^-17 of p).
+//      The terms are columns of their own, so their scales meet in the epilogue, in fp32.
+// A row's running maximum would need every key's score; instead the exponentials are taken
+// against a reference that moves (a slow path through shared memory) when some score is more than
+// 2^kLazy above it, which a vote of the tile's threads finds out.
+//
+// One CTA per (piece, request x KV head), 320 threads:
+//   warps 0-3, 4-7  a thread is one key of the tile (a TMEM lane), for all rows; the two
+//                   warpgroups take alternate tiles and keep states of their own
+//   warp 8          TMA producer: 128-key tiles of K and V codes, ST stages each
+//   warp 9          tcgen05.mma issue: QK0 QK1 | PV0 QK2 | PV1 QK3 | ...
+// TMEM: S of the two warpgroups (hi | lo columns), then their O (one column per row and term).
+// Piece 0 is the tree (at most 32 bf16 keys), computed in fp32 on the ordinary cores; the others
+// are tps tiles of the prefix.  Pieces write fp32 partials, merged in the kernel when the grid
+// fits on the SMs (cooperative launch), else by kvq_combine_kernel.
+#include "common.cuh"
+#include "kvq.cuh"
+#include "kvq_merge.cuh"
+#include "launch.h"
+#include "sm100.cuh"
+#include "tmap.h"
+
+namespace eagle {
+namespace {
+
+using namespace sm100;
+
+constexpr int KT = 128;
+constexpr int T8 = KT * 128;  // a tile of codes, 16 KB
+constexpr int NT = 320;
+constexpr float kLazy = 4.f;  // as in tree_attn_kvq.cu
+constexpr int PB = 11;
+
+enum : int { ERR_K = 1, ERR_KE = 2, ERR_V = 4, ERR_VE = 8, ERR_S = 32, ERR_P = 64, ERR_O = 128, ERR_GROUP = 256,
+             ERR_Q = 512 };
+
+struct Maps {
+  CUtensorMap k, v;
+};
+
+template <int NR, int TERMS>
+struct Few {
+  static constexpr int NP = NR * TERMS;             // O columns of a warpgroup, bytes of a key's P
+  static constexpr int NS = 2 * NR;                 // S columns of a warpgroup
+  static constexpr int ST = NR == 32 ? 5 : 6;       // ring stages
+  static constexpr int SM_Q = 0;                    // hi rows, lo rows of 128 codes
+  static constexpr int SM_P = SM_Q + NS * 128;      // two buffers, blocks of 32 columns x 128 keys
+  static constexpr int P1 = 128 * NP;
+  static constexpr int SM_K = SM_P + 2 * P1;
+  static constexpr int SM_V = SM_K + ST * T8;
+  static constexpr int SMEM = SM_V + ST * T8 + 1024;
+  static_assert(P1 % 1024 == 0 && 2 * NS + 2 * NP <= 512, "alignment of the rings, TMEM columns");
+};
+
+// Descriptor with the 32-byte swizzle (MN-major P: rows of 32 columns, 8 keys every `sbo` bytes,
+// 32 columns every `lbo`).
+__device__ __forceinline__ uint64_t desc_sw32(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
+         (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (6ull << 61);
+}
+
+// kind::f8f6f4, fp32 accumulator, M = 128; formats e4m3 0, e5m2 1; mn: both operands MN-major.
+__host__ __device__ constexpr uint32_t idesc8(int bfmt, int mn, int n) {
+  return (1u << 4) | (static_cast<uint32_t>(bfmt) << 10) | (static_cast<uint32_t>(mn) << 15) |
+         (static_cast<uint32_t>(mn) << 16) | (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// By one elected lane of a converged warp (see tree_attn_kvq_tc.cu).
+__device__ __forceinline__ void mma8(uint32_t d, uint64_t ad, uint64_t bd, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t e4m3x2_of_half2(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+__device__ __forceinline__ uint32_t e5m2x2_of_half2(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+// Two e5m2 codes as halves: the code is a half's upper byte.
+__device__ __forceinline__ uint32_t half2_of_e5m2(uint32_t c) { return __byte_perm(c, 0, 0x1404); }
+__device__ __forceinline__ uint32_t sub_half2(uint32_t a, uint32_t b) {
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+// 8 (a - b): exact, a - b being what an e5m2 term left of a half
+__device__ __forceinline__ uint32_t rest_half2(uint32_t a, uint32_t b) {
+  const __half2 d = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b)),
+                            __floats2half2_rn(8.f, 8.f));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+// Floats as integers in the same order (NaN above everything).
+__device__ __forceinline__ int ordered(float x) {
+  const int i = __float_as_int(x);
+  return i >= 0 ? i : i ^ 0x7fffffff;
+}
+__device__ __forceinline__ float unordered(int i) { return __int_as_float(i >= 0 ? i : i ^ 0x7fffffff); }
+
+// Piece 0: the tree's own keys, fp32.  A warp per row, a lane per key, then a lane per 4 head dims.
+__device__ void tree_piece(const KvqAttnArgs& a, uint8_t* smem, int b, int bh, int h, int Rb, size_t prow0) {
+  constexpr int LD = 272;  // bytes of a row of 128 bf16: 16 past, so that 8 lanes' rows cover the banks
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint8_t* sk = smem;
+  uint8_t* sv = smem + 32 * LD;
+  const uint4* kg = reinterpret_cast<const uint4*>(a.tk + static_cast<size_t>(bh) * a.R * 128);
+  const uint4* vg = reinterpret_cast<const uint4*>(a.tv + static_cast<size_t>(bh) * a.R * 128);
+  for (int i = tid; i < Rb * 16; i += NT) {
+    *reinterpret_cast<uint4*>(sk + (i >> 4) * LD + (i & 15) * 16) = __ldg(kg + i);
+    *reinterpret_cast<uint4*>(sv + (i >> 4) * LD + (i & 15) * 16) = __ldg(vg + i);
+  }
+  __syncthreads();
+  for (int row = warp; row < Rb * a.G; row += NT / 32) {
+    const int node = row / a.G;
+    const uint4* q = reinterpret_cast<const uint4*>(
+        a.q + ((static_cast<size_t>(b) * a.R + node) * a.Hq + h * a.G + row % a.G) * 128);
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < 16; ++c) {
+      const uint4 x = __ldg(q + c), y = *reinterpret_cast<const uint4*>(sk + min(lane, Rb - 1) * LD + c * 16);
+      const uint32_t u[4] = {x.x, x.y, x.z, x.w}, w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s0 = fmaf(__uint_as_float(u[e] << 16), __uint_as_float(w[e] << 16), s0);
+        s1 = fmaf(__uint_as_float(u[e] & 0xffff0000u), __uint_as_float(w[e] & 0xffff0000u), s1);
+      }
+    }
+    const uint64_t word = a.anc_mask[(static_cast<size_t>(b) * a.R + node) * a.W];
+    const float t = lane < Rb && ((word >> lane) & 1ull) ? (s0 + s1) * a.scale_log2 : -INFINITY;
+    const float M = warp_max(t);
+    const float p = t == -INFINITY ? 0.f : ex2(t - M), l = warp_sum(p);
+    float o[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < Rb; ++j) {
+      const uint2 y = *reinterpret_cast<const uint2*>(sv + j * LD + lane * 8);
+      const float pj = __shfl_sync(0xffffffffu, p, j);
+      o[0] = fmaf(pj, __uint_as_float(y.x << 16), o[0]);
+      o[1] = fmaf(pj, __uint_as_float(y.x & 0xffff0000u), o[1]);
+      o[2] = fmaf(pj, __uint_as_float(y.y << 16), o[2]);
+      o[3] = fmaf(pj, __uint_as_float(y.y & 0xffff0000u), o[3]);
+    }
+    *reinterpret_cast<float4*>(a.part_o + (prow0 + row) * 128 + lane * 4) = make_float4(o[0], o[1], o[2], o[3]);
+    if (lane == 0) *reinterpret_cast<float2*>(a.part_ml + (prow0 + row) * 2) = make_float2(M, l);
+  }
+}
+
+template <int NR, int TERMS>
+__global__ void __launch_bounds__(NT, 1) tree_attn_kvq_few_kernel(const __grid_constant__ Maps tm, const KvqAttnArgs a) {
+  using F = Few<NR, TERMS>;
+  constexpr int ST = F::ST;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t k_full[ST], k_empty[ST], v_full[ST], v_empty[ST], s_full[2], p_full[2], q_full, o_full;
+  __shared__ uint32_t tmem_base;
+  __shared__ int go;
+  __shared__ __align__(16) float s_c[NR];      // score factors of the rows
+  __shared__ __align__(16) float s_m[2][NR];   // the warpgroups' reference maxima (-inf: none yet)
+  __shared__ __align__(16) float s_al[2][NR];  // slow path: the rows' rescale
+  __shared__ float s_red[2][4][NR];            // slow path, epilogue: the warps' maxima / sums
+
+  const int piece = blockIdx.x, bh = blockIdx.y;
+  const int b = bh / a.Hkv, h = bh % a.Hkv;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+
+  if (warp == 9) {
+    tmem_alloc(&tmem_base, 512);
+    tmem_relinquish();
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], 128);
+    }
+    mbar_init(&q_full, 8);
+    mbar_init(&o_full, 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  tc_fence_after();
+  griddep_wait();
+  griddep_launch_dependents();
+
+  int L = a.seq_len[b];
+  L = L < 0 ? 0 : (L > a.P ? a.P : L);
+  const int Rb = a.n_nodes ? min(max(a.n_nodes[b], 0), a.R) : a.R;
+  const int RG = Rb * a.G;
+  const int n_pref = (L + KT - 1) / KT;
+  const int tile0 = (piece - 1) * a.tps;
+  const int n = piece == 0 || RG == 0 ? 0 : max(0, min(a.tps, n_pref - tile0));
+  const bool tree = piece == 0 && RG > 0, work = n > 0;
+  const size_t prow0 = (static_cast<size_t>(bh) * a.splits + piece) * a.rows_pad;
+  const uint32_t tb = tmem_base;
+  auto col_s = [](int w) { return static_cast<uint32_t>(w * F::NS); };
+  auto col_o = [](int w) { return static_cast<uint32_t>(2 * F::NS + w * F::NP); };
+
+  if (tree) {
+    tree_piece(a, smem, b, bh, h, Rb, prow0);
+  } else if (!work) {
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ TMA producer (lane 0)
+    if (lane == 0) {
+      const uint64_t policy = policy_evict_first();
+      const int y0 = bh * a.P + tile0 * KT;
+      auto load = [&](const CUtensorMap& m, int at, uint64_t* bar, int t) {
+        mbar_arrive_expect_tx(bar, T8);
+        tma_load_2d_hint(smem + at, &m, 0, y0 + t * KT, bar, policy);
+      };
+      int k_in = 0, v_in = 0;
+      for (int t = 0; t < n; ++t) {
+        const int s = t % ST;
+        if (t >= ST && !wait_parity(&k_empty[s], (t / ST - 1) & 1, a.err, ERR_KE)) break;
+        load(tm.k, F::SM_K + s * T8, &k_full[s], t);
+        ++k_in;
+        if (t >= ST && !wait_parity(&v_empty[s], (t / ST - 1) & 1, a.err, ERR_VE)) break;
+        load(tm.v, F::SM_V + s * T8, &v_full[s], t);
+        ++v_in;
+      }
+      // no copy may still be landing when the CTA ends
+      for (int s = 0; s < ST && s < k_in; ++s) (void)wait_parity(&k_full[s], ((k_in - 1 - s) / ST) & 1, a.err, ERR_K);
+      for (int s = 0; s < ST && s < v_in; ++s) (void)wait_parity(&v_full[s], ((v_in - 1 - s) / ST) & 1, a.err, ERR_V);
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ tcgen05.mma issue
+    auto wait = [&](uint64_t* bar, int parity, int code) {
+      return __all_sync(0xffffffffu, wait_parity(bar, parity, a.err, code)) != 0;
+    };
+    const uint32_t tu = __shfl_sync(0xffffffffu, tb, 0);
+    const int items = __shfl_sync(0xffffffffu, n, 0);
+    const uint64_t dq = smem_desc_sw128(smem_u32(smem + F::SM_Q), 16, 1024);
+    const uint64_t dk = smem_desc_sw128(smem_u32(smem + F::SM_K), 16, 1024);
+    const uint64_t dv = smem_desc_sw128(smem_u32(smem + F::SM_V), T8, 1024);
+    const uint64_t dp = desc_sw32(smem_u32(smem + F::SM_P), 4096, 256);
+    auto qk = [&](int i) {
+      const int s = i % ST, w = i & 1;
+      if (!wait(&k_full[s], (i / ST) & 1, ERR_K)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+        mma8(tu + col_s(w), dk + s * (T8 >> 4) + ks * 2, dq + ks * 2, idesc8(0, 0, F::NS), ks > 0);
+      commit(&s_full[w]);
+      commit(&k_empty[s]);
+      return true;
+    };
+    auto pv = [&](int i) {
+      const int s = i % ST, w = i & 1;
+      if (!wait(&v_full[s], (i / ST) & 1, ERR_V)) return false;
+      if (!wait(&p_full[w], (i >> 1) & 1, ERR_P)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)  // 32 keys: 4 KB of V, 1 KB of every block of P
+        mma8(tu + col_o(w), dv + s * (T8 >> 4) + ks * 256, dp + w * (F::P1 >> 4) + ks * 64, idesc8(1, 1, F::NP),
+             (i >= 2 || ks > 0) ? 1u : 0u);
+      commit(&v_empty[s]);
+      return true;
+    };
+    bool ok = wait(&q_full, 0, ERR_Q);
+    ok = ok && qk(0) && (items < 2 || qk(1));
+#pragma unroll 1
+    for (int i = 0; i < items && ok; ++i) ok = pv(i) && (i + 2 >= items || qk(i + 2));
+    commit(&o_full);
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ softmax: a thread per key
+    const int w = warp >> 2, qd = warp & 3;
+    const int key = qd * 32 + lane;  // of a tile; TMEM lane
+    // Q: eight lanes a row, dims 8 c .. and 64 + 8 c ..
+    if (threadIdx.x < NR * 8) {
+      const int row = threadIdx.x >> 3, c = threadIdx.x & 7;
+      uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
+      if (row < RG) {
+        const uint4* src = reinterpret_cast<const uint4*>(
+            a.q + ((static_cast<size_t>(b) * a.R + row / a.G) * a.Hq + h * a.G + row % a.G) * 128 + 8 * c);
+        x0 = __ldg(src);
+        x1 = __ldg(src + 8);
+      }
+      const uint32_t u[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+      uint32_t am = 0;  // the row's largest magnitude, as bf16 bits (ordered as integers)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) am = max(am, max((u[k] << 16) & 0x7fff0000u, u[k] & 0x7fff0000u));
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
+      // a row with an element that is not finite gets NaN scores
+      const float qs = kvq_scale(fmaxf(__uint_as_float(min(am, 0x7f7f0000u)), 0x1p-100f));
+      const float mul = __uint_as_float((254u << 23) - __float_as_uint(qs));  // 1 / qs, a power of two
+      if (c == 0) s_c[row] = am < 0x7f800000u ? a.scale_log2 * qs : __uint_as_float(0x7fffffffu);
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t q2 = half2_bits(__uint_as_float(u[k] << 16) * mul, __uint_as_float(u[k] & 0xffff0000u) * mul);
+        const uint32_t h8 = e4m3x2_of_half2(q2);
+        const uint32_t l8 = e4m3x2_of_half2(sub_half2(q2, kvq_half2(h8)));
+        hi[k >> 1] = (k & 1) ? hi[k >> 1] | (h8 << 16) : h8;
+        lo[k >> 1] = (k & 1) ? lo[k >> 1] | (l8 << 16) : l8;
+      }
+      uint8_t* d1 = smem + F::SM_Q + row * 128 + (((c >> 1) ^ (row & 7)) << 4) + 8 * (c & 1);
+      uint8_t* d2 = smem + F::SM_Q + row * 128 + ((((c >> 1) + 4) ^ (row & 7)) << 4) + 8 * (c & 1);
+      *reinterpret_cast<uint2*>(d1) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(d2) = make_uint2(hi[2], hi[3]);
+      *reinterpret_cast<uint2*>(d1 + NR * 128) = make_uint2(lo[0], lo[1]);
+      *reinterpret_cast<uint2*>(d2 + NR * 128) = make_uint2(lo[2], lo[3]);
+      fence_proxy_async_smem();
+    }
+    if (threadIdx.x < 2 * NR) s_m[threadIdx.x / NR][threadIdx.x % NR] = -INFINITY;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&q_full);
+    // vref: the largest V scale of the piece; the scales of this key's blocks
+    const int nblk = (a.P + kQB - 1) / kQB, blk0 = tile0 * (KT / kQB);
+    const int n_blk = (min(L, (tile0 + n) * KT) + kQB - 1) / kQB - blk0;
+    const float* ks = a.ks + static_cast<size_t>(bh) * nblk + blk0;
+    const float* vs = a.vs + static_cast<size_t>(bh) * nblk + blk0;
+    float vref = 0.f;
+    for (int i = lane; i < n_blk; i += 32) vref = fmaxf(vref, __ldg(vs + i));
+    vref = warp_max(vref);
+    if (!(vref > 0.f)) vref = 1.f;
+    const float vinv = 1.f / vref;
+    float kn, vn;
+    auto fetch = [&](int t) {
+      const int kb = min(2 * t + (qd >> 1), n_blk - 1);
+      kn = __ldg(ks + kb);
+      vn = __ldg(vs + kb);
+    };
+    fetch(min(w, n - 1));
+    bar_sync(3, 256);  // s_c, s_m
+
+    const uint32_t lb = tb + (static_cast<uint32_t>(qd * 32) << 16);
+    float l[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) l[r] = 0.f;
+    bool ok = true;
+    for (int i = w; i < n; i += 2) {
+      const float kc = kn, lr = fmaxf(__log2f(vn * vinv), -100.f) + PB;
+      fetch(min(i + 2, n - 1));
+      const int nv = min(KT, L - (tile0 + i) * KT);
+      const bool on = key < nv;
+      // A warp whose wait gave up goes on without waiting (the error word is set, nothing is
+      // written): the others of its warpgroup may still count on it at the barriers below.
+      ok = __all_sync(0xffffffffu, ok && wait_parity(&s_full[w], (i >> 1) & 1, a.err, ERR_S));
+      tc_fence_after();
+      float t[NR];
+      float over = -INFINITY;
+#pragma unroll
+      for (int g = 0; g < NR; g += 16) {
+        uint32_t hi[16], lo[16];
+        tmem_ld16(lb + col_s(w) + g, hi);
+        tmem_ld16(lb + col_s(w) + NR + g, lo);
+        tmem_ld_wait();
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const float s = (__uint_as_float(hi[r]) + __uint_as_float(lo[r])) * (s_c[g + r] * kc);
+          t[g + r] = on ? s : -INFINITY;
+          over = fmaxf(over, t[g + r] - s_m[w][g + r]);  // +inf while there is no reference
+        }
+      }
+      // (a NaN score does not raise `over`: it spoils its row whatever the reference)
+      if (!bar_and(1 + w, 128, over <= kLazy)) {
+        int mine = 0;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          const int m = __reduce_max_sync(0xffffffffu, ordered(t[r] == t[r] ? t[r] : -INFINITY));
+          if (lane == r) mine = m;
+        }
+        if (lane < NR) s_red[w][qd][lane] = unordered(mine);
+        bar_sync(1 + w, 128);
+        if (key < NR) {
+          const float top = fmaxf(fmaxf(s_red[w][0][key], s_red[w][1][key]), fmaxf(s_red[w][2][key], s_red[w][3][key]));
+          const float old = s_m[w][key];
+          const bool up = top > old + kLazy || (old == -INFINITY && top > -INFINITY);
+          s_al[w][key] = !up || old == -INFINITY ? 1.f : ex2(old - ceilf(top));  // (no reference yet: all zero)
+          if (up) s_m[w][key] = ceilf(top);
+        }
+        bar_sync(1 + w, 128);
+#pragma unroll
+        for (int r = 0; r < NR; ++r) l[r] *= s_al[w][r];
+        if (i >= 2) {
+          // O of this warpgroup's earlier tiles: their PV finished before S of this one did
+#pragma unroll 1
+          for (int u = 0; u < TERMS; ++u)
+#pragma unroll
+            for (int g = 0; g < NR; g += 16) {
+              uint32_t x[16];
+              tmem_ld16(lb + col_o(w) + u * NR + g, x);
+              tmem_ld_wait();
+#pragma unroll
+              for (int r = 0; r < 16; ++r) x[r] = __float_as_uint(__uint_as_float(x[r]) * s_al[w][g + r]);
+              tmem_st16(lb + col_o(w) + u * NR + g, x);
+            }
+          tmem_st_wait();
+        }
+      }
+      // P terms: 16 rows at a time, 16 bytes of every term
+      const float back = ex2(-lr);
+      uint8_t* pb = smem + F::SM_P + w * F::P1 + key * 32;
+      const int flip = ((key >> 2) & 1) << 4;
+#pragma unroll
+      for (int g = 0; g < NR; g += 16) {
+        uint32_t hh[8], ll[8];
+#pragma unroll
+        for (int r = 0; r < 16; r += 2) {
+          const float m0 = s_m[w][g + r], m1 = s_m[w][g + r + 1];
+          const float p0 = ex2(t[g + r] - (m0 == -INFINITY ? 0.f : m0) + lr);
+          const float p1 = ex2(t[g + r + 1] - (m1 == -INFINITY ? 0.f : m1) + lr);
+          l[g + r] = fmaf(p0, back, l[g + r]);
+          l[g + r + 1] = fmaf(p1, back, l[g + r + 1]);
+          hh[r >> 1] = half2_bits(p0, p1);
+          if (TERMS > 4) {
+            // what the half left, by 2^11: a half's last place against its first
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hh[r >> 1]));
+            ll[r >> 1] = half2_bits((p0 - f.x) * 2048.f, (p1 - f.y) * 2048.f);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < TERMS; ++u) {
+          uint32_t c4[4];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            uint32_t& x = u < 4 ? hh[k] : ll[k];
+            const uint32_t c2 = e5m2x2_of_half2(x);
+            if (u != 3 && u != TERMS - 1) x = rest_half2(x, half2_of_e5m2(c2));
+            c4[k >> 1] = (k & 1) ? c4[k >> 1] | (c2 << 16) : c2;
+          }
+          const int col = u * NR + g;  // first of 16 columns: block col / 32, 16-byte half (col / 16) % 2
+          *reinterpret_cast<uint4*>(pb + (col >> 5) * 4096 + ((col & 16) ^ flip)) = make_uint4(c4[0], c4[1], c4[2], c4[3]);
+        }
+      }
+      if (!on) {
+        // V rows behind the prefix: zeros, whatever they hold (their P is 0)
+        ok = ok && wait_parity(&v_full[i % ST], (i / ST) & 1, a.err, ERR_V);
+        uint4* v = reinterpret_cast<uint4*>(smem + F::SM_V + (i % ST) * T8 + key * 128);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[c] = make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      mbar_arrive(&p_full[w]);
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    // ---- epilogue: the warpgroups' states meet; a thread is now one head dim
+    bool done = __all_sync(0xffffffffu, ok && wait_parity(&o_full, 0, a.err, ERR_O));
+    tc_fence_after();
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const float x = warp_sum(l[r]);
+      if (lane == 0) s_red[w][qd][r] = x;
+    }
+    done = bar_and(3, 256, done);
+    if (done) {
+      const float unit = vref * (1.f / (1 << PB));
+      const bool two = n > 1;
+      float* so = reinterpret_cast<float*>(smem + F::SM_K);  // [NR][128]: the ring is free
+      float o[NR];
+      if (w == 0 || two) {
+#pragma unroll
+        for (int g = 0; g < NR; g += 16) {
+          uint32_t x[16];
+#pragma unroll
+          for (int u = 0; u < TERMS; ++u) {
+            tmem_ld16(lb + col_o(w) + u * NR + g, x);
+            tmem_ld_wait();
+            const float f = unit * (u < 4 ? 1.f / (1 << (3 * u)) : 1.f / (1 << (11 + 3 * (u - 4))));
+#pragma unroll
+            for (int r = 0; r < 16; ++r) o[g + r] = u == 0 ? __uint_as_float(x[r]) * f : fmaf(__uint_as_float(x[r]), f, o[g + r]);
+          }
+        }
+      }
+      if (w == 1 && two) {
+#pragma unroll
+        for (int r = 0; r < NR; ++r) so[r * 128 + key] = o[r];
+      }
+      bar_sync(3, 256);
+      if (w == 0) {
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          if (r >= RG) break;
+          const float m0 = s_m[0][r], m1 = two ? s_m[1][r] : -INFINITY;
+          const float M = fmaxf(m0, m1);
+          const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - M), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
+          float v = o[r] * f0;
+          if (two) v = fmaf(so[r * 128 + key], f1, v);
+          a.part_o[(prow0 + r) * 128 + key] = v;
+          if (key == 0) {
+            const float l0 = (s_red[0][0][r] + s_red[0][1][r]) + (s_red[0][2][r] + s_red[0][3][r]);
+            const float l1 = (s_red[1][0][r] + s_red[1][1][r]) + (s_red[1][2][r] + s_red[1][3][r]);
+            *reinterpret_cast<float2*>(a.part_ml + (prow0 + r) * 2) = make_float2(M, fmaf(f0, l0, f1 * l1));
+          }
+        }
+      }
+    }
+  }
+  if (a.coop && (tree || work)) {
+    // the group's merge (request, KV head): an even share of its rows, a warp per row
+    const int need = 1 + min(a.splits - 1, (n_pref + a.tps - 1) / a.tps);
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) go = kvq_group_wait(a.cnt + 2 * bh, need, a.err, ERR_GROUP) ? 1 : 0;
+    __syncthreads();
+    if (go) {
+      const int hi = (piece + 1) * RG / need;
+      for (int k = piece * RG / need + warp; k < hi; k += NT / 32)
+        kvq_merge_row<128, 20>(a, static_cast<size_t>(bh) * a.splits * a.rows_pad + k, need,
+                               (static_cast<size_t>(b) * a.R + k / a.G) * a.Hq + h * a.G + k % a.G, lane);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tb, 512);
+  }
+}
+
+template <int NR, int TERMS>
+cudaError_t launch_few(const KvqAttnPlan& p, const Maps& tm, const KvqAttnArgs& a, cudaStream_t s) {
+  auto kern = tree_attn_kvq_few_kernel<NR, TERMS>;
+  constexpr int smem = Few<NR, TERMS>::SMEM;
+  static unsigned long long configured = 0;  // shared memory opt-in, once per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(__atomic_load_n(&configured, __ATOMIC_ACQUIRE) & (1ull << dev))) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) __atomic_fetch_or(&configured, 1ull << dev, __ATOMIC_RELEASE);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.splits, p.B * p.Hkv);
+  cfg.blockDim = dim3(NT);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeCooperative;  // all CTAs resident, or the launch fails
+  attr[1].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.coop ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, kern, tm, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kvq_attn_few(const KvqAttnPlan& p, const KvqAttnArgs& a, cudaStream_t s) {
+  Maps tm;
+  const unsigned long long rows = static_cast<unsigned long long>(p.B) * p.Hkv * p.P;
+  if (!make_tmap_2d(&tm.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.k8, 128, rows, 128, KT, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_tmap_2d(&tm.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.v8, 128, rows, 128, KT, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  if (p.rows_per_cta == 16) return p.terms2 ? launch_few<16, 6>(p, tm, a, s) : launch_few<16, 4>(p, tm, a, s);
+  return p.terms2 ? launch_few<32, 6>(p, tm, a, s) : launch_few<32, 4>(p, tm, a, s);
+}
+
+}  // namespace eagle
