@@ -452,13 +452,14 @@ class KvqLayerPointers:
         self.v, self.vs = mk(v_codes, CODES, "v_codes"), mk(v_scale, f32, "v_scale")
         self.tk, self.tv = mk(tree_k, FLOATS, "tree_k"), mk(tree_v, FLOATS, "tree_v")
         self.tensors = [list(t) for t in (k_codes, k_scale, v_codes, v_scale, tree_k, tree_v)]
+        self.addresses = tuple(ctypes.addressof(x) for x in (self.k, self.ks, self.v, self.vs, self.tk, self.tv))
 
 
 def eagle_kvq_commit(desc: CommitDesc, layers: KvqLayerPointers, n_acc, path, seq_len, commit_pos,
                      feat_cache=None, tree_feat=None, status=None, stream=None) -> None:
     """Commit the accepted path into 8-bit caches (see eagle.h: eagle_kvq_commit)."""
     _check("eagle_kvq_commit", load().eagle_kvq_commit(
-        ctypes.byref(desc), layers.k, layers.ks, layers.v, layers.vs, layers.tk, layers.tv,
+        ctypes.byref(desc), *layers.addresses,
         _ptr(n_acc, torch.int32, "n_acc"), _ptr(path, torch.int32, "path"), _ptr(seq_len, torch.int32, "seq_len"),
         _ptr(commit_pos, torch.int32, "commit_pos"), _ptr(feat_cache, FLOATS, "feat_cache"),
         _ptr(tree_feat, FLOATS, "tree_feat"), _ptr(status, torch.int32, "status"), _stream(stream)))

@@ -618,11 +618,22 @@ void plan_kvq_attn(const eagle_attn_desc* d, int num_sms, KvqAttnPlan* p) {
     p->wr = RG > 128 ? 2 : 1;
     p->rows_per_cta = p->few ? (RG <= 16 ? 16 : 32) : p->wr * 128;
     p->row_blocks = (RG + p->rows_per_cta - 1) / p->rows_per_cta;
-    // one wave of CTAs (one per SM: all of TMEM) while the groups leave room for a prefix
-    // piece and the tree each, pieces of 16 tiles when they do not
+    // Prefix pieces of a request, beside its tree.  Either one wave of CTAs (one per SM: they hold
+    // all of TMEM), or pieces of 24 tiles (32 when the groups alone fill the SMs), so that ragged
+    // requests balance: whichever is estimated shorter, a CTA costing about six tiles' time
+    // besides its own (prologue, partials).  Measured: 8 requests of 1K to 16K x 8 heads 102 us
+    // with 22 tiles, 109 with 15, 228 in one wave; 32 such 322 us with 33, 339 with 22, 359 with
+    // 15; 4 requests of 32K 131 us with 29, 163 in one wave; one of 8K 21 us in one wave.
     const long long base = static_cast<long long>(p->B) * p->Hkv * p->row_blocks;
-    long long pieces = d->num_splits > 0 ? d->num_splits : num_sms / base - 1;
-    if (pieces < 1) pieces = (tiles + 15) / 16;
+    long long pieces = d->num_splits;
+    if (pieces <= 0) {
+      const int want = base < num_sms ? 24 : 32;
+      const long long one = std::min<long long>(num_sms / base - 1, tiles);
+      const long long many = std::max(1, (tiles + want / 2) / want);
+      const long long t_one = one < 1 ? 1ll << 60 : (tiles + one - 1) / one + 6;
+      const long long t_many = base * (tiles + 6 * (many + 1)) / num_sms + want / 2;
+      pieces = t_one <= t_many ? one : many;
+    }
     pieces = std::min<long long>(std::min<long long>(pieces, tiles), 255);
     p->tps = static_cast<int>((tiles + pieces - 1) / pieces);
     p->splits = (tiles + p->tps - 1) / p->tps + 1;

@@ -9,20 +9,23 @@
 // is on the small side:
 //   q  as in tree_attn_kvq_tc.cu: a power of two puts a row's largest element in (224, 448], and
 //      q = hi + lo in e4m3 keeps bf16's bits down to elements of 2^-11 of it;
-//   p  2^PB vs / vref is rounded to a half (11 bits, steps of 2^-35 of the largest p) and that
-//      half is written as four e5m2 terms, exactly: each takes three bits, and what it leaves is
-//      multiplied by 8.  EAGLE_ATTN_PRECISE: two more terms of what the half left (2^-17 of p).
-//      The terms are columns of their own, so their scales meet in the epilogue, in fp32.
+//   p  2^PB vs / vref is rounded to a half (11 bits) and that half is written as four e5m2 terms
+//      of three bits each, exactly down to steps of 2^-31 of the largest p (the rest after the
+//      first term is multiplied by 8, past e5m2's smallest steps).  EAGLE_ATTN_PRECISE: two more
+//      terms of what the half left (2^-17 of p).  The terms are columns of their own; their
+//      scales meet in the epilogue, in fp32.
 // A row's running maximum would need every key's score; instead the exponentials are taken
 // against a reference that moves (a slow path through shared memory) when some score is more than
 // 2^kLazy above it, which a vote of the tile's threads finds out.
 //
-// One CTA per (piece, request x KV head), 320 threads:
-//   warps 0-3, 4-7  a thread is one key of the tile (a TMEM lane), for all rows; the two
-//                   warpgroups take alternate tiles and keep states of their own
-//   warp 8          TMA producer: 128-key tiles of K and V codes, ST stages each
-//   warp 9          tcgen05.mma issue: QK0 QK1 | PV0 QK2 | PV1 QK3 | ...
-// TMEM: S of the two warpgroups (hi | lo columns), then their O (one column per row and term).
+// One CTA per (piece, request x KV head):
+//   softmax warpgroups, two for every 16 rows: a thread is one key of the tile (a TMEM lane) for
+//                   its 16 rows; the two take alternate tiles and keep states of their own
+//   a TMA producer warp: 128-key tiles of K and V codes, ST stages each
+//   a warp that issues every tcgen05.mma: QK0 QK1 | QK2 PV0 | QK3 PV1 | ...
+// (32 rows a thread instead of 16 take as many instructions, but at 2.5 warps a scheduler only
+// every second cycle issued one: 61.7 us against the time below for a chain of 8 over 128K.)
+// TMEM: S of the even and the odd tiles (hi | lo columns), then O likewise (a column per row and term).
 // Piece 0 is the tree (at most 32 bf16 keys), computed in fp32 on the ordinary cores; the others
 // are tps tiles of the prefix.  Pieces write fp32 partials, merged in the kernel when the grid
 // fits on the SMs (cooperative launch), else by kvq_combine_kernel.
@@ -40,7 +43,6 @@ using namespace sm100;
 
 constexpr int KT = 128;
 constexpr int T8 = KT * 128;  // a tile of codes, 16 KB
-constexpr int NT = 320;
 constexpr float kLazy = 4.f;  // as in tree_attn_kvq.cu
 constexpr int PB = 11;
 
@@ -53,8 +55,10 @@ struct Maps {
 
 template <int NR, int TERMS>
 struct Few {
-  static constexpr int NP = NR * TERMS;             // O columns of a warpgroup, bytes of a key's P
-  static constexpr int NS = 2 * NR;                 // S columns of a warpgroup
+  static constexpr int SW = NR / 2;                 // softmax warps: NR / 16 x 2 warpgroups
+  static constexpr int NT = SW * 32 + (NR == 32 ? 128 : 64);  // threads (setmaxnreg wants whole warpgroups)
+  static constexpr int NP = NR * TERMS;             // O columns of a tile parity, bytes of a key's P
+  static constexpr int NS = 2 * NR;                 // S columns of a tile parity
   static constexpr int ST = NR == 32 ? 5 : 6;       // ring stages
   static constexpr int SM_Q = 0;                    // hi rows, lo rows of 128 codes
   static constexpr int SM_P = SM_Q + NS * 128;      // two buffers, blocks of 32 columns x 128 keys
@@ -113,11 +117,15 @@ __device__ __forceinline__ uint32_t sub_half2(uint32_t a, uint32_t b) {
   const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&d);
 }
-// 8 (a - b): exact, a - b being what an e5m2 term left of a half
-__device__ __forceinline__ uint32_t rest_half2(uint32_t a, uint32_t b) {
-  const __half2 d = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b)),
-                            __floats2half2_rn(8.f, 8.f));
+__device__ __forceinline__ uint32_t times8_half2(uint32_t a) {
+  const __half2 d = __hmul2(*reinterpret_cast<const __half2*>(&a), __floats2half2_rn(8.f, 8.f));
   return *reinterpret_cast<const uint32_t*>(&d);
+}
+__device__ __forceinline__ uint64_t twice(float x) { return f32x2(__float_as_uint(x), __float_as_uint(x)); }
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // Floats as integers in the same order (NaN above everything).
@@ -128,6 +136,7 @@ __device__ __forceinline__ int ordered(float x) {
 __device__ __forceinline__ float unordered(int i) { return __int_as_float(i >= 0 ? i : i ^ 0x7fffffff); }
 
 // Piece 0: the tree's own keys, fp32.  A warp per row, a lane per key, then a lane per 4 head dims.
+template <int NT>
 __device__ void tree_piece(const KvqAttnArgs& a, uint8_t* smem, int b, int bh, int h, int Rb, size_t prow0) {
   constexpr int LD = 272;  // bytes of a row of 128 bf16: 16 past, so that 8 lanes' rows cover the banks
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -174,16 +183,19 @@ __device__ void tree_piece(const KvqAttnArgs& a, uint8_t* smem, int b, int bh, i
 }
 
 template <int NR, int TERMS>
-__global__ void __launch_bounds__(NT, 1) tree_attn_kvq_few_kernel(const __grid_constant__ Maps tm, const KvqAttnArgs a) {
+__global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
+    tree_attn_kvq_few_kernel(const __grid_constant__ Maps tm, const KvqAttnArgs a) {
   using F = Few<NR, TERMS>;
-  constexpr int ST = F::ST;
+  constexpr int ST = F::ST, SW = F::SW, HALVES = NR / 16;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t k_full[ST], k_empty[ST], v_full[ST], v_empty[ST], s_full[2], p_full[2], q_full, o_full;
+  __shared__ uint64_t k_full[ST], k_empty[ST], v_full[ST], v_empty[ST], s_full[2], s_empty[2], p_full[2], p_empty[2], q_full, o_full;
   __shared__ uint32_t tmem_base;
   __shared__ int go;
-  __shared__ __align__(16) float s_c[NR];      // score factors of the rows
-  __shared__ __align__(16) float s_m[2][NR];   // the warpgroups' reference maxima (-inf: none yet)
+  // by tile parity:
+  __shared__ float s_m[2][NR];                 // the rows' reference maxima (-inf: none yet)
+  __shared__ __align__(16) float s_c[NR];      // (both) score factors of the rows
+  __shared__ __align__(16) float s_mu[2][NR];  // minus the reference, 0 for none
   __shared__ __align__(16) float s_al[2][NR];  // slow path: the rows' rescale
   __shared__ float s_red[2][4][NR];            // slow path, epilogue: the warps' maxima / sums
 
@@ -191,7 +203,7 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_few_kernel(const __grid_c
   const int b = bh / a.Hkv, h = bh % a.Hkv;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
-  if (warp == 9) {
+  if (warp == SW + 1) {
     tmem_alloc(&tmem_base, 512);
     tmem_relinquish();
   }
@@ -204,9 +216,11 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_few_kernel(const __grid_c
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], 128);
+      mbar_init(&s_empty[s], HALVES * 128);
+      mbar_init(&p_full[s], HALVES * 128);
+      mbar_init(&p_empty[s], 1);
     }
-    mbar_init(&q_full, 8);
+    mbar_init(&q_full, SW);
     mbar_init(&o_full, 1);
     fence_barrier_init();
   }
@@ -228,315 +242,360 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_few_kernel(const __grid_c
   auto col_s = [](int w) { return static_cast<uint32_t>(w * F::NS); };
   auto col_o = [](int w) { return static_cast<uint32_t>(2 * F::NS + w * F::NP); };
 
-  if (tree) {
-    tree_piece(a, smem, b, bh, h, Rb, prow0);
-  } else if (!work) {
-  } else if (warp == 8) {
-    // ------------------------------------------------------------ TMA producer (lane 0)
-    if (lane == 0) {
-      const uint64_t policy = policy_evict_first();
-      const int y0 = bh * a.P + tile0 * KT;
-      auto load = [&](const CUtensorMap& m, int at, uint64_t* bar, int t) {
-        mbar_arrive_expect_tx(bar, T8);
-        tma_load_2d_hint(smem + at, &m, 0, y0 + t * KT, bar, policy);
-      };
-      int k_in = 0, v_in = 0;
-      for (int t = 0; t < n; ++t) {
-        const int s = t % ST;
-        if (t >= ST && !wait_parity(&k_empty[s], (t / ST - 1) & 1, a.err, ERR_KE)) break;
-        load(tm.k, F::SM_K + s * T8, &k_full[s], t);
-        ++k_in;
-        if (t >= ST && !wait_parity(&v_empty[s], (t / ST - 1) & 1, a.err, ERR_VE)) break;
-        load(tm.v, F::SM_V + s * T8, &v_full[s], t);
-        ++v_in;
-      }
-      // no copy may still be landing when the CTA ends
-      for (int s = 0; s < ST && s < k_in; ++s) (void)wait_parity(&k_full[s], ((k_in - 1 - s) / ST) & 1, a.err, ERR_K);
-      for (int s = 0; s < ST && s < v_in; ++s) (void)wait_parity(&v_full[s], ((v_in - 1 - s) / ST) & 1, a.err, ERR_V);
-    }
-  } else if (warp == 9) {
-    // ------------------------------------------------------------ tcgen05.mma issue
-    auto wait = [&](uint64_t* bar, int parity, int code) {
-      return __all_sync(0xffffffffu, wait_parity(bar, parity, a.err, code)) != 0;
-    };
-    const uint32_t tu = __shfl_sync(0xffffffffu, tb, 0);
-    const int items = __shfl_sync(0xffffffffu, n, 0);
-    const uint64_t dq = smem_desc_sw128(smem_u32(smem + F::SM_Q), 16, 1024);
-    const uint64_t dk = smem_desc_sw128(smem_u32(smem + F::SM_K), 16, 1024);
-    const uint64_t dv = smem_desc_sw128(smem_u32(smem + F::SM_V), T8, 1024);
-    const uint64_t dp = desc_sw32(smem_u32(smem + F::SM_P), 4096, 256);
-    auto qk = [&](int i) {
-      const int s = i % ST, w = i & 1;
-      if (!wait(&k_full[s], (i / ST) & 1, ERR_K)) return false;
-      tc_fence_after();
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
-        mma8(tu + col_s(w), dk + s * (T8 >> 4) + ks * 2, dq + ks * 2, idesc8(0, 0, F::NS), ks > 0);
-      commit(&s_full[w]);
-      commit(&k_empty[s]);
-      return true;
-    };
-    auto pv = [&](int i) {
-      const int s = i % ST, w = i & 1;
-      if (!wait(&v_full[s], (i / ST) & 1, ERR_V)) return false;
-      if (!wait(&p_full[w], (i >> 1) & 1, ERR_P)) return false;
-      tc_fence_after();
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks)  // 32 keys: 4 KB of V, 1 KB of every block of P
-        mma8(tu + col_o(w), dv + s * (T8 >> 4) + ks * 256, dp + w * (F::P1 >> 4) + ks * 64, idesc8(1, 1, F::NP),
-             (i >= 2 || ks > 0) ? 1u : 0u);
-      commit(&v_empty[s]);
-      return true;
-    };
-    bool ok = wait(&q_full, 0, ERR_Q);
-    ok = ok && qk(0) && (items < 2 || qk(1));
-#pragma unroll 1
-    for (int i = 0; i < items && ok; ++i) ok = pv(i) && (i + 2 >= items || qk(i + 2));
-    commit(&o_full);
-  } else if (warp < 8) {
-    // ------------------------------------------------------------ softmax: a thread per key
-    const int w = warp >> 2, qd = warp & 3;
-    const int key = qd * 32 + lane;  // of a tile; TMEM lane
-    // Q: eight lanes a row, dims 8 c .. and 64 + 8 c ..
-    if (threadIdx.x < NR * 8) {
-      const int row = threadIdx.x >> 3, c = threadIdx.x & 7;
-      uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
-      if (row < RG) {
-        const uint4* src = reinterpret_cast<const uint4*>(
-            a.q + ((static_cast<size_t>(b) * a.R + row / a.G) * a.Hq + h * a.G + row % a.G) * 128 + 8 * c);
-        x0 = __ldg(src);
-        x1 = __ldg(src + 8);
-      }
-      const uint32_t u[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-      uint32_t am = 0;  // the row's largest magnitude, as bf16 bits (ordered as integers)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) am = max(am, max((u[k] << 16) & 0x7fff0000u, u[k] & 0x7fff0000u));
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
-      // a row with an element that is not finite gets NaN scores
-      const float qs = kvq_scale(fmaxf(__uint_as_float(min(am, 0x7f7f0000u)), 0x1p-100f));
-      const float mul = __uint_as_float((254u << 23) - __float_as_uint(qs));  // 1 / qs, a power of two
-      if (c == 0) s_c[row] = am < 0x7f800000u ? a.scale_log2 * qs : __uint_as_float(0x7fffffffu);
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t q2 = half2_bits(__uint_as_float(u[k] << 16) * mul, __uint_as_float(u[k] & 0xffff0000u) * mul);
-        const uint32_t h8 = e4m3x2_of_half2(q2);
-        const uint32_t l8 = e4m3x2_of_half2(sub_half2(q2, kvq_half2(h8)));
-        hi[k >> 1] = (k & 1) ? hi[k >> 1] | (h8 << 16) : h8;
-        lo[k >> 1] = (k & 1) ? lo[k >> 1] | (l8 << 16) : l8;
-      }
-      uint8_t* d1 = smem + F::SM_Q + row * 128 + (((c >> 1) ^ (row & 7)) << 4) + 8 * (c & 1);
-      uint8_t* d2 = smem + F::SM_Q + row * 128 + ((((c >> 1) + 4) ^ (row & 7)) << 4) + 8 * (c & 1);
-      *reinterpret_cast<uint2*>(d1) = make_uint2(hi[0], hi[1]);
-      *reinterpret_cast<uint2*>(d2) = make_uint2(hi[2], hi[3]);
-      *reinterpret_cast<uint2*>(d1 + NR * 128) = make_uint2(lo[0], lo[1]);
-      *reinterpret_cast<uint2*>(d2 + NR * 128) = make_uint2(lo[2], lo[3]);
-      fence_proxy_async_smem();
-    }
-    if (threadIdx.x < 2 * NR) s_m[threadIdx.x / NR][threadIdx.x % NR] = -INFINITY;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&q_full);
-    // vref: the largest V scale of the piece; the scales of this key's blocks
-    const int nblk = (a.P + kQB - 1) / kQB, blk0 = tile0 * (KT / kQB);
-    const int n_blk = (min(L, (tile0 + n) * KT) + kQB - 1) / kQB - blk0;
-    const float* ks = a.ks + static_cast<size_t>(bh) * nblk + blk0;
-    const float* vs = a.vs + static_cast<size_t>(bh) * nblk + blk0;
-    float vref = 0.f;
-    for (int i = lane; i < n_blk; i += 32) vref = fmaxf(vref, __ldg(vs + i));
-    vref = warp_max(vref);
-    if (!(vref > 0.f)) vref = 1.f;
-    const float vinv = 1.f / vref;
-    float kn, vn;
-    auto fetch = [&](int t) {
-      const int kb = min(2 * t + (qd >> 1), n_blk - 1);
-      kn = __ldg(ks + kb);
-      vn = __ldg(vs + kb);
-    };
-    fetch(min(w, n - 1));
-    bar_sync(3, 256);  // s_c, s_m
+  // the group's merge (request, KV head): an even share of its rows, a warp per row
+  const int need = 1 + min(a.splits - 1, (n_pref + a.tps - 1) / a.tps);
+  auto merge = [&](int warps) {
+    if (!a.coop) return;
+    __threadfence();
+    bar_sync(5, warps * 32);
+    if (threadIdx.x == 0) go = kvq_group_wait(a.cnt + 2 * bh, need, a.err, ERR_GROUP) ? 1 : 0;
+    bar_sync(5, warps * 32);
+    if (!go) return;
+    const int hi = (piece + 1) * RG / need;
+    for (int k = piece * RG / need + warp; k < hi; k += warps)
+      kvq_merge_row<128, NR == 32 ? 12 : 20>(a, static_cast<size_t>(bh) * a.splits * a.rows_pad + k, need,
+                             (static_cast<size_t>(b) * a.R + k / a.G) * a.Hq + h * a.G + k % a.G, lane);
+  };
 
-    const uint32_t lb = tb + (static_cast<uint32_t>(qd * 32) << 16);
-    float l[NR];
-#pragma unroll
-    for (int r = 0; r < NR; ++r) l[r] = 0.f;
-    bool ok = true;
-    for (int i = w; i < n; i += 2) {
-      const float kc = kn, lr = fmaxf(__log2f(vn * vinv), -100.f) + PB;
-      fetch(min(i + 2, n - 1));
-      const int nv = min(KT, L - (tile0 + i) * KT);
-      const bool on = key < nv;
-      // A warp whose wait gave up goes on without waiting (the error word is set, nothing is
-      // written): the others of its warpgroup may still count on it at the barriers below.
-      ok = __all_sync(0xffffffffu, ok && wait_parity(&s_full[w], (i >> 1) & 1, a.err, ERR_S));
-      tc_fence_after();
-      float t[NR];
-      float over = -INFINITY;
-#pragma unroll
-      for (int g = 0; g < NR; g += 16) {
-        uint32_t hi[16], lo[16];
-        tmem_ld16(lb + col_s(w) + g, hi);
-        tmem_ld16(lb + col_s(w) + NR + g, lo);
-        tmem_ld_wait();
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const float s = (__uint_as_float(hi[r]) + __uint_as_float(lo[r])) * (s_c[g + r] * kc);
-          t[g + r] = on ? s : -INFINITY;
-          over = fmaxf(over, t[g + r] - s_m[w][g + r]);  // +inf while there is no reference
+  if (tree) {
+    tree_piece<F::NT>(a, smem, b, bh, h, Rb, prow0);
+    merge(F::NT / 32);
+  } else if (warp >= SW) {
+    // registers: 96 a thread at launch with 640 threads (61440); softmax 104, the others 64
+    // (512 x 104 + 128 x 64 = 61440).  With 320 threads there are enough as it is.
+    if (HALVES == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (!work) {
+    } else if (warp == SW) {
+      // ------------------------------------------------------------ TMA producer (lane 0)
+      if (lane == 0) {
+        const uint64_t policy = policy_evict_first();
+        const int y0 = bh * a.P + tile0 * KT;
+        auto load = [&](const CUtensorMap& m, int at, uint64_t* bar, int t) {
+          mbar_arrive_expect_tx(bar, T8);
+          tma_load_2d_hint(smem + at, &m, 0, y0 + t * KT, bar, policy);
+        };
+        int k_in = 0, v_in = 0;
+        for (int t = 0; t < n; ++t) {
+          const int s = t % ST;
+          if (t >= ST && !wait_parity(&k_empty[s], (t / ST - 1) & 1, a.err, ERR_KE)) break;
+          load(tm.k, F::SM_K + s * T8, &k_full[s], t);
+          ++k_in;
+          if (t >= ST && !wait_parity(&v_empty[s], (t / ST - 1) & 1, a.err, ERR_VE)) break;
+          load(tm.v, F::SM_V + s * T8, &v_full[s], t);
+          ++v_in;
         }
+        // no copy may still be landing when the CTA ends
+        for (int s = 0; s < ST && s < k_in; ++s) (void)wait_parity(&k_full[s], ((k_in - 1 - s) / ST) & 1, a.err, ERR_K);
+        for (int s = 0; s < ST && s < v_in; ++s) (void)wait_parity(&v_full[s], ((v_in - 1 - s) / ST) & 1, a.err, ERR_V);
       }
-      // (a NaN score does not raise `over`: it spoils its row whatever the reference)
-      if (!bar_and(1 + w, 128, over <= kLazy)) {
-        int mine = 0;
+    } else if (warp == SW + 1) {
+      // ------------------------------------------------------------ tcgen05.mma issue
+      auto wait = [&](uint64_t* bar, int parity, int code) {
+        return __all_sync(0xffffffffu, wait_parity(bar, parity, a.err, code)) != 0;
+      };
+      const uint32_t tu = __shfl_sync(0xffffffffu, tb, 0);
+      const int items = __shfl_sync(0xffffffffu, n, 0);
+      const uint64_t dq = smem_desc_sw128(smem_u32(smem + F::SM_Q), 16, 1024);
+      const uint64_t dk = smem_desc_sw128(smem_u32(smem + F::SM_K), 16, 1024);
+      const uint64_t dv = smem_desc_sw128(smem_u32(smem + F::SM_V), T8, 1024);
+      const uint64_t dp = desc_sw32(smem_u32(smem + F::SM_P), 4096, 256);
+      auto qk = [&](int i) {
+        const int s = i % ST, w = i & 1;
+        if (!wait(&k_full[s], (i / ST) & 1, ERR_K)) return false;
+        tc_fence_after();
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          const int m = __reduce_max_sync(0xffffffffu, ordered(t[r] == t[r] ? t[r] : -INFINITY));
-          if (lane == r) mine = m;
-        }
-        if (lane < NR) s_red[w][qd][lane] = unordered(mine);
-        bar_sync(1 + w, 128);
-        if (key < NR) {
-          const float top = fmaxf(fmaxf(s_red[w][0][key], s_red[w][1][key]), fmaxf(s_red[w][2][key], s_red[w][3][key]));
-          const float old = s_m[w][key];
-          const bool up = top > old + kLazy || (old == -INFINITY && top > -INFINITY);
-          s_al[w][key] = !up || old == -INFINITY ? 1.f : ex2(old - ceilf(top));  // (no reference yet: all zero)
-          if (up) s_m[w][key] = ceilf(top);
-        }
-        bar_sync(1 + w, 128);
+        for (int ks = 0; ks < 4; ++ks)
+          mma8(tu + col_s(w), dk + s * (T8 >> 4) + ks * 2, dq + ks * 2, idesc8(0, 0, F::NS), ks > 0);
+        commit(&s_full[w]);
+        commit(&k_empty[s]);
+        return true;
+      };
+      auto pv = [&](int i) {
+        const int s = i % ST, w = i & 1;
+        if (!wait(&v_full[s], (i / ST) & 1, ERR_V)) return false;
+        if (!wait(&p_full[w], (i >> 1) & 1, ERR_P)) return false;
+        tc_fence_after();
 #pragma unroll
-        for (int r = 0; r < NR; ++r) l[r] *= s_al[w][r];
-        if (i >= 2) {
-          // O of this warpgroup's earlier tiles: their PV finished before S of this one did
+        for (int ks = 0; ks < 4; ++ks)  // 32 keys: 4 KB of V, 1 KB of every block of P
+          mma8(tu + col_o(w), dv + s * (T8 >> 4) + ks * 256, dp + w * (F::P1 >> 4) + ks * 64, idesc8(1, 1, F::NP),
+               (i >= 2 || ks > 0) ? 1u : 0u);
+        commit(&v_empty[s]);
+        commit(&p_empty[w]);
+        return true;
+      };
+      bool ok = wait(&q_full, 0, ERR_Q);
+      ok = ok && qk(0) && (items < 2 || qk(1));
+      // the scores of a warpgroup's next tile as soon as it has read these, under its exponentials
 #pragma unroll 1
-          for (int u = 0; u < TERMS; ++u)
+      for (int i = 0; i < items && ok; ++i) {
+        if (i + 2 < items) ok = wait(&s_empty[i & 1], (i >> 1) & 1, ERR_S) && qk(i + 2);
+        ok = ok && pv(i);
+      }
+      commit(&o_full);
+    }
+  } else {
+    if (HALVES == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    if (work) {
+      // ------------------------------------------------------------ softmax: a thread per key
+      const int w = (warp >> 2) & 1, qd = warp & 3;      // tile parity, quarter of the keys
+      const int vote = 1 + (warp >> 2), g0 = (warp >> 3) * 16;  // named barrier; the first of its rows
+      const int key = qd * 32 + lane;  // of a tile; TMEM lane
+      // Q: eight lanes a row, dims 8 c .. and 64 + 8 c ..
+      if (threadIdx.x < NR * 8) {
+        const int row = threadIdx.x >> 3, c = threadIdx.x & 7;
+        uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
+        if (row < RG) {
+          const uint4* src = reinterpret_cast<const uint4*>(
+              a.q + ((static_cast<size_t>(b) * a.R + row / a.G) * a.Hq + h * a.G + row % a.G) * 128 + 8 * c);
+          x0 = __ldg(src);
+          x1 = __ldg(src + 8);
+        }
+        const uint32_t u[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+        uint32_t am = 0;  // the row's largest magnitude, as bf16 bits (ordered as integers)
 #pragma unroll
-            for (int g = 0; g < NR; g += 16) {
-              uint32_t x[16];
-              tmem_ld16(lb + col_o(w) + u * NR + g, x);
+        for (int k = 0; k < 8; ++k) am = max(am, max((u[k] << 16) & 0x7fff0000u, u[k] & 0x7fff0000u));
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
+        // a row with an element that is not finite gets NaN scores
+        const float qs = kvq_scale(fmaxf(__uint_as_float(min(am, 0x7f7f0000u)), 0x1p-100f));
+        const float mul = __uint_as_float((254u << 23) - __float_as_uint(qs));  // 1 / qs, a power of two
+        if (c == 0)
+          s_c[row] = am < 0x7f800000u ? a.scale_log2 * qs : __uint_as_float(0x7fffffffu);
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t q2 = half2_bits(__uint_as_float(u[k] << 16) * mul, __uint_as_float(u[k] & 0xffff0000u) * mul);
+          const uint32_t h8 = e4m3x2_of_half2(q2);
+          const uint32_t l8 = e4m3x2_of_half2(sub_half2(q2, kvq_half2(h8)));
+          hi[k >> 1] = (k & 1) ? hi[k >> 1] | (h8 << 16) : h8;
+          lo[k >> 1] = (k & 1) ? lo[k >> 1] | (l8 << 16) : l8;
+        }
+        uint8_t* d1 = smem + F::SM_Q + row * 128 + (((c >> 1) ^ (row & 7)) << 4) + 8 * (c & 1);
+        uint8_t* d2 = smem + F::SM_Q + row * 128 + ((((c >> 1) + 4) ^ (row & 7)) << 4) + 8 * (c & 1);
+        *reinterpret_cast<uint2*>(d1) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(d2) = make_uint2(hi[2], hi[3]);
+        *reinterpret_cast<uint2*>(d1 + NR * 128) = make_uint2(lo[0], lo[1]);
+        *reinterpret_cast<uint2*>(d2 + NR * 128) = make_uint2(lo[2], lo[3]);
+        fence_proxy_async_smem();
+      }
+      if (threadIdx.x < 2 * NR) {
+        s_m[threadIdx.x / NR][threadIdx.x % NR] = -INFINITY;
+        s_mu[threadIdx.x / NR][threadIdx.x % NR] = 0.f;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full);
+      // vref: the largest V scale of the piece; the scales of this key's blocks
+      const int nblk = (a.P + kQB - 1) / kQB, blk0 = tile0 * (KT / kQB);
+      const int n_blk = (min(L, (tile0 + n) * KT) + kQB - 1) / kQB - blk0;
+      const float* ks = a.ks + static_cast<size_t>(bh) * nblk + blk0;
+      const float* vs = a.vs + static_cast<size_t>(bh) * nblk + blk0;
+      float vref = 0.f;
+      for (int i = lane; i < n_blk; i += 32) vref = fmaxf(vref, __ldg(vs + i));
+      vref = warp_max(vref);
+      if (!(vref > 0.f)) vref = 1.f;
+      const float vinv = 1.f / vref;
+      float kn, vn;
+      auto fetch = [&](int t) {
+        const int kb = min(2 * t + (qd >> 1), n_blk - 1);
+        kn = __ldg(ks + kb);
+        vn = __ldg(vs + kb);
+      };
+      fetch(min(w, n - 1));
+      bar_sync(5, SW * 32);  // s_c, s_m, s_mu
+
+      const uint32_t lb = tb + (static_cast<uint32_t>(qd * 32) << 16);
+      uint64_t l2[8];  // row sums, in pairs
+#pragma unroll
+      for (int r = 0; r < 8; ++r) l2[r] = 0ull;
+      bool ok = true;
+      for (int i = w; i < n; i += 2) {
+        const float kc = kn, lr = fmaxf(__log2f(vn * vinv), -100.f) + PB;
+        fetch(min(i + 2, n - 1));
+        const uint64_t kc2 = twice(kc), lr2 = twice(lr);
+        const int nv = min(KT, L - (tile0 + i) * KT);
+        const bool on = key < nv;
+        // A warp whose wait gave up goes on without waiting (the error word is set, nothing is
+        // written): the others of its warpgroup may still count on it at the barriers below.
+        ok = __all_sync(0xffffffffu, ok && wait_parity(&s_full[w], (i >> 1) & 1, a.err, ERR_S));
+        tc_fence_after();
+        // x = score - reference (log2 units) of this key and every row
+        float x[16];
+        auto scores = [&]() {
+          uint32_t hi[16], lo[16];
+          tmem_ld16(lb + col_s(w) + g0, hi);
+          tmem_ld16(lb + col_s(w) + NR + g0, lo);
+          tmem_ld_wait();
+#pragma unroll
+          for (int r = 0; r < 16; r += 2) {
+            const uint64_t c = *reinterpret_cast<const uint64_t*>(&s_c[g0 + r]);
+            const uint64_t mu = *reinterpret_cast<const uint64_t*>(&s_mu[w][g0 + r]);
+            f32x2_split(fma_f32x2(add_f32x2(f32x2(hi[r], hi[r + 1]), f32x2(lo[r], lo[r + 1])), mul_f32x2(c, kc2), mu),
+                        x[r], x[r + 1]);
+          }
+          if (nv < KT) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) x[r] = on ? x[r] : -INFINITY;
+          }
+        };
+        scores();
+        float over = i < 2 ? INFINITY : -INFINITY;  // (no reference yet)
+#pragma unroll
+        for (int r = 0; r < 16; r += 2) over = max3(over, x[r], x[r + 1]);
+        // (a NaN score does not raise `over`: it spoils its row whatever the reference)
+        const bool fits = bar_and(vote, 128, over <= kLazy);
+        // P's buffer and O: free once the product of this parity's tile before has finished
+        ok = __all_sync(0xffffffffu, ok && (i < 2 || wait_parity(&p_empty[w], ((i >> 1) - 1) & 1, a.err, ERR_P)));
+        if (!fits) {
+          int mine = 0;
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int m = __reduce_max_sync(0xffffffffu, ordered(x[r] == x[r] ? x[r] : -INFINITY));
+            if (lane == r) mine = m;
+          }
+          if (lane < 16) s_red[w][qd][g0 + lane] = unordered(mine);
+          bar_sync(vote, 128);
+          if (key < 16) {
+            const int r = g0 + key;
+            const float old = s_m[w][r];
+            const float top = fmaxf(fmaxf(s_red[w][0][r], s_red[w][1][r]), fmaxf(s_red[w][2][r], s_red[w][3][r])) - s_mu[w][r];
+            const bool up = top > old + kLazy || (old == -INFINITY && top > -INFINITY);
+            s_al[w][r] = !up || old == -INFINITY ? 1.f : ex2(old - ceilf(top));  // (no reference yet: all zero)
+            if (up) {
+              s_m[w][r] = ceilf(top);
+              s_mu[w][r] = -ceilf(top);
+            }
+          }
+          bar_sync(vote, 128);
+#pragma unroll
+          for (int r = 0; r < 8; ++r)
+            l2[r] = mul_f32x2(l2[r], *reinterpret_cast<const uint64_t*>(&s_al[w][g0 + 2 * r]));
+          if (i >= 2) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int u = 0; u < TERMS; ++u) {
+              uint32_t o[16];
+              tmem_ld16(lb + col_o(w) + u * NR + g0, o);
               tmem_ld_wait();
 #pragma unroll
-              for (int r = 0; r < 16; ++r) x[r] = __float_as_uint(__uint_as_float(x[r]) * s_al[w][g + r]);
-              tmem_st16(lb + col_o(w) + u * NR + g, x);
+              for (int r = 0; r < 16; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * s_al[w][g0 + r]);
+              tmem_st16(lb + col_o(w) + u * NR + g0, o);
             }
-          tmem_st_wait();
+            tmem_st_wait();
+          }
+          scores();  // against the new reference
         }
-      }
-      // P terms: 16 rows at a time, 16 bytes of every term
-      const float back = ex2(-lr);
-      uint8_t* pb = smem + F::SM_P + w * F::P1 + key * 32;
-      const int flip = ((key >> 2) & 1) << 4;
-#pragma unroll
-      for (int g = 0; g < NR; g += 16) {
+        tc_fence_before();
+        mbar_arrive(&s_empty[w]);
+        // P: 16 bytes of every term
+        const uint64_t back2 = twice(ex2(-lr));
         uint32_t hh[8], ll[8];
 #pragma unroll
         for (int r = 0; r < 16; r += 2) {
-          const float m0 = s_m[w][g + r], m1 = s_m[w][g + r + 1];
-          const float p0 = ex2(t[g + r] - (m0 == -INFINITY ? 0.f : m0) + lr);
-          const float p1 = ex2(t[g + r + 1] - (m1 == -INFINITY ? 0.f : m1) + lr);
-          l[g + r] = fmaf(p0, back, l[g + r]);
-          l[g + r + 1] = fmaf(p1, back, l[g + r + 1]);
+          float y0, y1;
+          f32x2_split(add_f32x2(f32x2(__float_as_uint(x[r]), __float_as_uint(x[r + 1])), lr2), y0, y1);
+          const float p0 = ex2(y0), p1 = ex2(y1);
+          const uint64_t p2 = f32x2(__float_as_uint(p0), __float_as_uint(p1));
+          l2[r >> 1] = fma_f32x2(p2, back2, l2[r >> 1]);
           hh[r >> 1] = half2_bits(p0, p1);
           if (TERMS > 4) {
             // what the half left, by 2^11: a half's last place against its first
             const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hh[r >> 1]));
-            ll[r >> 1] = half2_bits((p0 - f.x) * 2048.f, (p1 - f.y) * 2048.f);
+            f32x2_split(mul_f32x2(add_f32x2(p2, f32x2(__float_as_uint(-f.x), __float_as_uint(-f.y))), twice(2048.f)), y0,
+                        y1);
+            ll[r >> 1] = half2_bits(y0, y1);
           }
         }
+        uint8_t* pb = smem + F::SM_P + w * F::P1 + key * 32;
+        const int flip = ((key >> 2) & 1) << 4;
 #pragma unroll
         for (int u = 0; u < TERMS; ++u) {
           uint32_t c4[4];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            uint32_t& x = u < 4 ? hh[k] : ll[k];
-            const uint32_t c2 = e5m2x2_of_half2(x);
-            if (u != 3 && u != TERMS - 1) x = rest_half2(x, half2_of_e5m2(c2));
+            uint32_t& y = u < 4 ? hh[k] : ll[k];
+            const uint32_t c2 = e5m2x2_of_half2(y);
+            if (u != 3 && u != TERMS - 1) {  // exact: what an e5m2 term leaves of a half
+              y = sub_half2(y, half2_of_e5m2(c2));
+              if (u == 0) y = times8_half2(y);
+            }
             c4[k >> 1] = (k & 1) ? c4[k >> 1] | (c2 << 16) : c2;
           }
-          const int col = u * NR + g;  // first of 16 columns: block col / 32, 16-byte half (col / 16) % 2
+          const int col = u * NR + g0;  // first of 16 columns: block col / 32, 16-byte half (col / 16) % 2
           *reinterpret_cast<uint4*>(pb + (col >> 5) * 4096 + ((col & 16) ^ flip)) = make_uint4(c4[0], c4[1], c4[2], c4[3]);
         }
+        if (!on) {
+          // V rows behind the prefix: zeros, whatever they hold (their P is 0)
+          ok = ok && wait_parity(&v_full[i % ST], (i / ST) & 1, a.err, ERR_V);
+          uint4* v = reinterpret_cast<uint4*>(smem + F::SM_V + (i % ST) * T8 + key * 128);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) v[c] = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(&p_full[w]);
+        ok = __all_sync(0xffffffffu, ok);
       }
-      if (!on) {
-        // V rows behind the prefix: zeros, whatever they hold (their P is 0)
-        ok = ok && wait_parity(&v_full[i % ST], (i / ST) & 1, a.err, ERR_V);
-        uint4* v = reinterpret_cast<uint4*>(smem + F::SM_V + (i % ST) * T8 + key * 128);
+      // ---- epilogue: the parities' states meet; a thread is now one head dim for its 16 rows
+      bool done = __all_sync(0xffffffffu, ok && wait_parity(&o_full, 0, a.err, ERR_O));
+      tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] = make_uint4(0, 0, 0, 0);
+      for (int r = 0; r < 16; r += 2) {
+        float y0, y1;
+        f32x2_split(l2[r >> 1], y0, y1);
+        y0 = warp_sum(y0);
+        y1 = warp_sum(y1);
+        if (lane == 0) {
+          s_red[w][qd][g0 + r] = y0;
+          s_red[w][qd][g0 + r + 1] = y1;
+        }
       }
-      fence_proxy_async_smem();
-      tc_fence_before();
-      mbar_arrive(&p_full[w]);
-      ok = __all_sync(0xffffffffu, ok);
-    }
-    // ---- epilogue: the warpgroups' states meet; a thread is now one head dim
-    bool done = __all_sync(0xffffffffu, ok && wait_parity(&o_full, 0, a.err, ERR_O));
-    tc_fence_after();
-#pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      const float x = warp_sum(l[r]);
-      if (lane == 0) s_red[w][qd][r] = x;
-    }
-    done = bar_and(3, 256, done);
-    if (done) {
-      const float unit = vref * (1.f / (1 << PB));
-      const bool two = n > 1;
-      float* so = reinterpret_cast<float*>(smem + F::SM_K);  // [NR][128]: the ring is free
-      float o[NR];
-      if (w == 0 || two) {
-#pragma unroll
-        for (int g = 0; g < NR; g += 16) {
-          uint32_t x[16];
+      done = bar_and(5, SW * 32, done);
+      if (done) {
+        const float unit = vref * (1.f / (1 << PB));
+        const bool two = n > 1;
+        float* so = reinterpret_cast<float*>(smem + F::SM_K);  // [NR][128]: the ring is free
+        float o[16];
+        if (w == 0 || two) {
+          uint32_t y[16];
 #pragma unroll
           for (int u = 0; u < TERMS; ++u) {
-            tmem_ld16(lb + col_o(w) + u * NR + g, x);
+            tmem_ld16(lb + col_o(w) + u * NR + g0, y);
             tmem_ld_wait();
-            const float f = unit * (u < 4 ? 1.f / (1 << (3 * u)) : 1.f / (1 << (11 + 3 * (u - 4))));
+            const float f = unit * (u == 0 ? 1.f : (u < 4 ? 0.125f : 1.f / 2048.f));
 #pragma unroll
-            for (int r = 0; r < 16; ++r) o[g + r] = u == 0 ? __uint_as_float(x[r]) * f : fmaf(__uint_as_float(x[r]), f, o[g + r]);
+            for (int r = 0; r < 16; ++r) o[r] = u == 0 ? __uint_as_float(y[r]) * f : fmaf(__uint_as_float(y[r]), f, o[r]);
+          }
+        }
+        if (w == 1 && two) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) so[(g0 + r) * 128 + key] = o[r];
+        }
+        bar_sync(5, SW * 32);
+        if (w == 0) {
+#pragma unroll
+          for (int rr = 0; rr < 16; ++rr) {
+            const int r = g0 + rr;
+            if (r >= RG) break;
+            const float m0 = s_m[0][r], m1 = two ? s_m[1][r] : -INFINITY;
+            const float M = fmaxf(m0, m1);
+            const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - M), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
+            float y = o[rr] * f0;
+            if (two) y = fmaf(so[r * 128 + key], f1, y);
+            a.part_o[(prow0 + r) * 128 + key] = y;
+            if (key == 0) {
+              const float l0 = (s_red[0][0][r] + s_red[0][1][r]) + (s_red[0][2][r] + s_red[0][3][r]);
+              const float l1 = (s_red[1][0][r] + s_red[1][1][r]) + (s_red[1][2][r] + s_red[1][3][r]);
+              *reinterpret_cast<float2*>(a.part_ml + (prow0 + r) * 2) = make_float2(M, fmaf(f0, l0, f1 * l1));
+            }
           }
         }
       }
-      if (w == 1 && two) {
-#pragma unroll
-        for (int r = 0; r < NR; ++r) so[r * 128 + key] = o[r];
-      }
-      bar_sync(3, 256);
-      if (w == 0) {
-#pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          if (r >= RG) break;
-          const float m0 = s_m[0][r], m1 = two ? s_m[1][r] : -INFINITY;
-          const float M = fmaxf(m0, m1);
-          const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - M), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
-          float v = o[r] * f0;
-          if (two) v = fmaf(so[r * 128 + key], f1, v);
-          a.part_o[(prow0 + r) * 128 + key] = v;
-          if (key == 0) {
-            const float l0 = (s_red[0][0][r] + s_red[0][1][r]) + (s_red[0][2][r] + s_red[0][3][r]);
-            const float l1 = (s_red[1][0][r] + s_red[1][1][r]) + (s_red[1][2][r] + s_red[1][3][r]);
-            *reinterpret_cast<float2*>(a.part_ml + (prow0 + r) * 2) = make_float2(M, fmaf(f0, l0, f1 * l1));
-          }
-        }
-      }
-    }
-  }
-  if (a.coop && (tree || work)) {
-    // the group's merge (request, KV head): an even share of its rows, a warp per row
-    const int need = 1 + min(a.splits - 1, (n_pref + a.tps - 1) / a.tps);
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) go = kvq_group_wait(a.cnt + 2 * bh, need, a.err, ERR_GROUP) ? 1 : 0;
-    __syncthreads();
-    if (go) {
-      const int hi = (piece + 1) * RG / need;
-      for (int k = piece * RG / need + warp; k < hi; k += NT / 32)
-        kvq_merge_row<128, 20>(a, static_cast<size_t>(bh) * a.splits * a.rows_pad + k, need,
-                               (static_cast<size_t>(b) * a.R + k / a.G) * a.Hq + h * a.G + k % a.G, lane);
+      merge(SW);
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == SW + 1) {
     tc_fence_after();
     tmem_dealloc(tb, 512);
   }
@@ -557,7 +616,7 @@ cudaError_t launch_few(const KvqAttnPlan& p, const Maps& tm, const KvqAttnArgs& 
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.splits, p.B * p.Hkv);
-  cfg.blockDim = dim3(NT);
+  cfg.blockDim = dim3(Few<NR, TERMS>::NT);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];

@@ -694,9 +694,11 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
         fence_proxy_async_smem();
         bar_sync(2 + (two ? w : 0), two ? 128 : 256);
         if (qd == 0 && lane == 0 && (two || w == 0)) {
-          for (int c = 0; c < 4; ++c)
-            tma_store_2d(&tm.po, smem + ((two ? 4 * w : 0) + c) * T8, 32 * c,
-                         static_cast<int>(prow) + (two ? w * 128 : 0));
+          const int valid = RG - row0 - (two ? w * 128 : 0);  // boxes of 32 rows x 32 columns
+          for (int g = 0; g < 128 && g < valid; g += 32)
+            for (int c = 0; c < 4; ++c)
+              tma_store_2d(&tm.po, smem + ((two ? 4 * w : 0) + c) * T8 + g * 128, 32 * c,
+                           static_cast<int>(prow) + (two ? w * 128 : 0) + g);
           bulk_commit();
           if (a.coop)
             bulk_wait0();  // other CTAs of this launch read the rows
@@ -773,7 +775,7 @@ cudaError_t launch_kvq_attn_tc(const KvqAttnPlan& p, const KvqAttnArgs& a, cudaS
   const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
   if (!make_tmap_2d(&tm.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.k8, 128, rows, 128, KT, sw) ||
       !make_tmap_2d(&tm.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.v8, 128, rows, 128, KT, sw) ||
-      !make_tmap_2d(&tm.po, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, a.part_o, 128, prows, 32, 128, sw))
+      !make_tmap_2d(&tm.po, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, a.part_o, 128, prows, 32, 32, sw))
     return cudaErrorInvalidValue;
   return p.terms2 ? launch_tc<2>(p, tm, a, s) : launch_tc<1>(p, tm, a, s);
 }

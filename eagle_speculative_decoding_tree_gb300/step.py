@@ -144,12 +144,20 @@ class VerifyStep:
     target/draft logits are the synthetic LM's rows at the tree's nodes; Q, K/V and
     the uniforms are seeded normals / uniforms.  ``run`` enqueues the step;
     ``reset`` restores seq_len so that repeated runs process the same step.
+
+    ``cache_bits`` 8 keeps the prefix K/V as e4m3 codes with a scale for each 64 tokens and
+    head (``k8``, ``ks``, ``v8``, ``vs`` instead of ``kc``, ``vc``; bf16 workloads): the prefix
+    is quantised once here (eagle_kvq_write), attention reads the codes
+    (eagle_tree_attn_kvq) and the commit appends to them (eagle_kvq_commit).
     """
 
     def __init__(self, w: synth.Workload, batch: Optional[int] = None, layers: Optional[int] = None,
                  device="cuda", q_scale: float = 1.0, num_splits: int = 0, tree: Optional[dict] = None,
-                 keep_host: bool = False, precision: int = B.EAGLE_ATTN_PRECISE):
+                 keep_host: bool = False, precision: int = B.EAGLE_ATTN_PRECISE, cache_bits: int = 16):
+        if cache_bits not in (8, 16) or (cache_bits == 8 and w.dtype != "bf16"):
+            raise ValueError("cache_bits is 16, or 8 for a bf16 workload")
         self.w = w
+        self.cache_bits = cache_bits
         self.B = batch if batch is not None else w.batch
         self.L = layers if layers is not None else w.layers
         self.device = device
@@ -207,17 +215,36 @@ class VerifyStep:
         dt = B.EAGLE_F32 if w.dtype == "f32" else B.EAGLE_BF16
         self.attn_desc = B.AttnDesc(Bn, R, w.n_q_heads, w.n_kv_heads, w.head_dim, w.max_seq,
                                     1.0 / math.sqrt(w.head_dim), dt, num_splits, dt, precision)
-        self.attn_ws = torch.zeros(B.workspace_size(B.EAGLE_WS_TREE_ATTN, self.attn_desc), dtype=torch.uint8,
-                                   device=dev)
+        kind = B.EAGLE_WS_TREE_ATTN if cache_bits == 16 else B.EAGLE_WS_TREE_ATTN_KVQ
+        self.attn_ws = torch.zeros(B.workspace_size(kind, self.attn_desc), dtype=torch.uint8, device=dev)
+        if cache_bits == 8:
+            self._quantise_prefix()
         prop = B.EAGLE_PROPOSAL_SAMPLED if w.proposal == "sampled" else B.EAGLE_PROPOSAL_DELTA
         self.acc_desc = B.AcceptDesc(Bn, R, w.vocab, float(w.temperature), prop, dt, self.max_depth)
         self.acc_ws = torch.zeros(B.workspace_size(B.EAGLE_WS_ACCEPT, self.acc_desc), dtype=torch.uint8, device=dev)
         self.acc = B.AcceptBuffers.allocate(Bn, self.max_depth, dev)
         self.commit_desc = B.CommitDesc(L, Bn, w.n_kv_heads, w.head_dim, R, w.max_seq, self.max_depth, dt, 0, dt)
-        self.layers = B.LayerPointers(self.kc, self.vc, self.tk, self.tv)
+        if cache_bits == 8:
+            self.layers = B.KvqLayerPointers(self.k8, self.ks, self.v8, self.vs, self.tk, self.tv)
+        else:
+            self.layers = B.LayerPointers(self.kc, self.vc, self.tk, self.tv)
         self.commit_pos = torch.zeros(Bn, self.max_depth + 1, dtype=torch.int32, device=dev)
         self.variants = [dict(tokens=self.tokens, parent=self.parent, anc_mask=self.anc_mask, target=self.target,
                               draft=self.draft, u_accept=self.u_accept, u_final=self.u_final)]
+
+    def _quantise_prefix(self):
+        """The prefix rows of every layer into 8-bit caches, in place of the bf16 ones."""
+        w, dev = self.w, self.seq_len.device
+        self.k8, self.ks, self.v8, self.vs = [], [], [], []
+        d = B.KvqDesc(self.B, w.n_kv_heads, w.head_dim, w.max_seq, w.max_seq, B.EAGLE_BF16)
+        start = torch.zeros(self.B, dtype=torch.int32, device=dev)
+        blocks = -(-w.max_seq // B.EAGLE_KVQ_BLOCK)
+        for k, v in zip(self.kc, self.vc):
+            for codes, scale in ((self.k8, self.ks), (self.v8, self.vs)):
+                codes.append(torch.zeros(k.shape, dtype=torch.uint8, device=dev))
+                scale.append(torch.zeros(self.B, w.n_kv_heads, blocks, device=dev))
+            B.eagle_kvq_write(d, k, v, start, self.seq_len, self.k8[-1], self.ks[-1], self.v8[-1], self.vs[-1])
+        self.kc = self.vc = None
 
     # ------------------------------------------------------------------ step variants
     def add_variants(self, n: int):
@@ -259,6 +286,11 @@ class VerifyStep:
 
     # ------------------------------------------------------------------ calls
     def attn_layer(self, l: int, stream=None, lse: bool = False):
+        if self.cache_bits == 8:
+            B.eagle_tree_attn_kvq(self.attn_desc, self.q[l], self.k8[l], self.ks[l], self.v8[l], self.vs[l],
+                                  self.tk[l], self.tv[l], self.seq_len, self.anc_mask, self.out[l],
+                                  self.lse if lse else None, self.attn_ws, stream)
+            return
         B.eagle_tree_attn(self.attn_desc, self.q[l], self.kc[l], self.vc[l], self.tk[l], self.tv[l], self.seq_len,
                           self.anc_mask, self.out[l], self.lse if lse else None, self.attn_ws, stream)
 
@@ -267,8 +299,9 @@ class VerifyStep:
                        self.acc, self.acc_ws, stream)
 
     def commit(self, stream=None):
-        B.eagle_kv_commit(self.commit_desc, self.layers, self.acc.n_acc, self.acc.path, self.seq_len,
-                          self.commit_pos, status=self.acc.status, stream=stream)
+        commit = B.eagle_kvq_commit if self.cache_bits == 8 else B.eagle_kv_commit
+        commit(self.commit_desc, self.layers, self.acc.n_acc, self.acc.path, self.seq_len, self.commit_pos,
+               status=self.acc.status, stream=stream)
 
     def reset(self):
         """Restore seq_len so that the next run repeats the same step."""
@@ -286,8 +319,11 @@ class VerifyStep:
     def kv_bytes_per_layer(self) -> int:
         """Algorithmic K/V bytes one tree-attention launch must read: prefix + tree rows."""
         esz = 4 if self.w.dtype == "f32" else 2
-        rows = int(self.seq_len0.sum()) + self.B * self.R
-        return 2 * rows * self.w.n_kv_heads * self.w.head_dim * esz
+        prefix, tree = int(self.seq_len0.sum()), self.B * self.R
+        if self.cache_bits == 8:  # a byte an element, a scale for each block
+            per_row = self.w.head_dim + 4 / B.EAGLE_KVQ_BLOCK
+            return int(2 * self.w.n_kv_heads * (prefix * per_row + tree * self.w.head_dim * esz))
+        return 2 * (prefix + tree) * self.w.n_kv_heads * self.w.head_dim * esz
 
     def logit_bytes_visited(self, n_acc: np.ndarray) -> int:
         """Target rows the acceptance walk visits (n_acc + 1 per request), plus draft rows when sampled."""

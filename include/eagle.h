@@ -276,11 +276,12 @@ int eagle_tree_attn_plan(const eagle_attn_desc* d, int32_t* splits, int32_t* ker
  * empty mask) gets zeros and lse -inf.  Cache rows behind seq_len may hold anything; the
  * tree rows of existing nodes and the cache rows before seq_len take part in products with
  * weight 0 where a mask hides them, so a value there that is not finite spoils other rows.
- *   precision  EAGLE_ATTN_FAST: P enters the product with the prefix values as one half
- *              (11 significant bits: an error of 2^-11 of sum p |v| at most, an eighth of a
- *              bf16 output's own rounding); EAGLE_ATTN_PRECISE: as two halves (22 bits), either
- *              with a floor of 2^-35 of the row's largest p.  The tree's part always takes two
- *              bf16 terms.  Scores, softmax and sums are fp32.
+ *   precision  EAGLE_ATTN_FAST: P enters the product with the prefix values with 11 significant
+ *              bits (a half): an error of 2^-11 of sum p |v| at most, an eighth of a bf16
+ *              output's own rounding.  EAGLE_ATTN_PRECISE: with 17 or more, an error of 2^-17.
+ *              Either way p below 2^-30 of the row's largest may be rounded to nothing.  The
+ *              tree's part takes two bf16 terms of P (2^-16) or fp32.  Scores, softmax and sums
+ *              are fp32.
  * ws: eagle_workspace_size(EAGLE_WS_TREE_ATTN_KVQ, d) bytes, zero-filled before its first
  * use; one workspace serves one stream at a time.  Its first 4 bytes are an error word as in
  * eagle_tree_attn.

@@ -144,6 +144,11 @@ SHAPES = [
     (2, 65, 6, 2, 64, 333, [0, 333]),
     (1, 100, 12, 4, 64, 1100, [1029]),
     (1, 33, 4, 1, 128, 520, [513]),            # one row block and a bit
+    (1, 16, 2, 2, 128, 300, [260]),            # 16 rows to a KV head, and 17
+    (1, 17, 2, 2, 128, 300, [260]),
+    (2, 32, 3, 3, 128, 450, [450, 3]),         # 32 rows, as many tree keys
+    (1, 1, 32, 1, 128, 3333, [3333]),          # 32 rows of one token
+    (1, 2, 34, 2, 128, 200, [200]),            # 34 rows of two
 ]
 
 
@@ -206,6 +211,36 @@ def test_scales_of_any_kind(R):
     c.check(c.desc(False, False, 2))
     c = Case(7, 1, R, 8, 2, 128, 300, [300], scales=lambda g, s: np.zeros(s))
     c.check(c.desc(True, True))
+
+
+@pytest.mark.parametrize("R", [1, 8, 61])
+def test_growing_scores(R):
+    """Keys whose scores rise from tile to tile move every row's reference, several times."""
+    c = Case(14, 1, R, 8, 2, 128, 2000, [2000])
+    kc, ks = c.codes[0], c.scale[0]
+    for b in range(ks.shape[-1]):
+        ks[..., b] = 2.0 ** (-9 + b // 3)
+    vals = [H.values(x, s) for x, s in zip(c.codes, c.scale)]
+    f = lambda t: t.double().numpy()
+    c.ref = H.attention(f(c.q), vals[0], vals[1], f(c.tk), f(c.tv), c.seq, c.nodes, c.see, 1 / math.sqrt(128))
+    c.dev[2] = torch.from_numpy(ks).cuda()
+    c.check(c.desc(True, True))
+    c.check(c.desc(False, False, 1))
+
+
+@pytest.mark.parametrize("R", [4, 61])
+def test_rows_that_are_not_finite_spoil_only_themselves(R):
+    c = Case(15, 1, R, 8, 2, 128, 400, [390])
+    good = c.run(c.desc(True, True))[0]
+    q = c.dev[0].clone()
+    q[0, 0, 1, 5] = math.inf
+    q[0, R - 1, 6, 0] = math.nan
+    c.dev[0] = q
+    out, lse = c.run(c.desc(True, True))
+    bad = torch.zeros(1, R, 8, dtype=torch.bool, device="cuda")
+    bad[0, 0, 1] = bad[0, R - 1, 6] = True
+    assert bool(out[bad].isnan().all()) and bool(lse[bad].isnan().all())
+    assert torch.equal(out[~bad], good[~bad])
 
 
 def test_repeats_are_identical_and_lse_is_optional():
