@@ -16,23 +16,28 @@ __device__ __forceinline__ void ld_part(const float* p, float (&x)[2]) {
   asm volatile("ld.global.cg.v2.f32 {%0,%1}, [%2];" : "=f"(x[0]), "=f"(x[1]) : "l"(p));
 }
 
-// One thread of a CTA whose partials are in place (fenced): counts it into its group and waits,
-// at most two seconds, until all `need` have counted; cnt[0] published, cnt[1] past the wait, both
-// returned to zero by the last.  Only under a cooperative launch (every CTA resident).
+// The group's meeting under a cooperative launch (every CTA resident).  One thread of a CTA whose
+// partials are in place (fenced) counts it in and waits, at most two seconds, until all `need`
+// have counted (cnt[0]); past the wait one thread counts it out (cnt[1]), and the last one there
+// returns both to zero.
 __device__ __forceinline__ bool kvq_group_wait(int* cnt, int need, int* err, int code) {
   atomicAdd(cnt, 1);
-  const uint64_t t0 = sm100::global_ns();
   bool all = sm100::ld_acquire_gpu(cnt) >= need;
-  while (!all && sm100::global_ns() - t0 < 2000000000ull) {
-    __nanosleep(64);
-    all = sm100::ld_acquire_gpu(cnt) >= need;
+  if (!all) {
+    const uint64_t t0 = sm100::global_ns();
+    do {
+      __nanosleep(32);
+      all = sm100::ld_acquire_gpu(cnt) >= need;
+    } while (!all && sm100::global_ns() - t0 < 2000000000ull);
+    if (!all) atomicOr(err, code);
   }
-  if (!all) atomicOr(err, code);
+  return all;
+}
+__device__ __forceinline__ void kvq_group_leave(int* cnt, int need) {
   if (atomicAdd(cnt + 1, 1) == need - 1) {
     atomicExch(cnt, 0);
     atomicExch(cnt + 1, 0);
   }
-  return all;
 }
 
 // One warp: M = max m_s, out = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s over partials s < n at

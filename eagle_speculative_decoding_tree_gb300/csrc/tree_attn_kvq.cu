@@ -519,6 +519,7 @@ __global__ void __launch_bounds__(CW * 32, 1)
     if (threadIdx.x == 0)
       go = kvq_group_wait(a.cnt + 2 * (bh * gridDim.x + rb), need, a.err, ERR_GROUP) ? 1 : 0;
     __syncthreads();
+    if (threadIdx.x == CW * 32 - 1) kvq_group_leave(a.cnt + 2 * (bh * gridDim.x + rb), need);  // (no one waits for this)
     if (go) {
       const int n = min(rows_cta, RG - rb * rows_cta), hi = (split + 1) * n / need;
       for (int k = split * n / need + warp; k < hi; k += CW) {

@@ -250,6 +250,7 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
     bar_sync(5, warps * 32);
     if (threadIdx.x == 0) go = kvq_group_wait(a.cnt + 2 * bh, need, a.err, ERR_GROUP) ? 1 : 0;
     bar_sync(5, warps * 32);
+    if (threadIdx.x == warps * 32 - 1) kvq_group_leave(a.cnt + 2 * bh, need);  // (no one waits for this)
     if (!go) return;
     const int hi = (piece + 1) * RG / need;
     for (int k = piece * RG / need + warp; k < hi; k += warps)

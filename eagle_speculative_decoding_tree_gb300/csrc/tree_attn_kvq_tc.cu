@@ -716,6 +716,7 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
         bar_sync(1, 256);
         if (threadIdx.x == 0) go = kvq_group_wait(a.cnt + 2 * (bh * gridDim.z + rb), need, a.err, ERR_GROUP) ? 1 : 0;
         bar_sync(1, 256);
+        if (threadIdx.x == 255) kvq_group_leave(a.cnt + 2 * (bh * gridDim.z + rb), need);  // (no one waits for this)
         if (go) {
           const int n = min(two ? 256 : 128, RG - row0);
           const int hi = (piece + 1) * n / need;
