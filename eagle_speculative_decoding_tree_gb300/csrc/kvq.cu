@@ -59,28 +59,61 @@ struct Chunk<float> {
   }
 };
 
-__device__ __forceinline__ float finite_abs(float x) {  // the scale follows the finite values
-  const float m = fabsf(x);
-  return m <= 3.402823466e38f ? m : 0.f;
-}
+// The largest magnitude of a chunk as float bits (ordered as integers; NaN and infinities are at
+// or above kInf).  On the bits, two bf16 elements an instruction: the float way, with its test of
+// every element, took as many issue slots as the loads and stores together.
+constexpr uint32_t kInf = 0x7f800000u;
 
-template <typename T>
-__device__ __forceinline__ float chunk_max(const Chunk<T>& x) {
-  float f[8], m = 0.f;
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t chunk_max(const Chunk<uint16_t>& x) {
+  const uint32_t m = 0x7fff7fffu;
+  const uint32_t r = max_u16x2(max_u16x2(x.u.x & m, x.u.y & m), max_u16x2(x.u.z & m, x.u.w & m));
+  return max(r << 16, r & 0xffff0000u);
+}
+__device__ __forceinline__ uint32_t chunk_max(const Chunk<float>& x) {
+  float f[8];
   x.get(f);
+  uint32_t r = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) m = fmaxf(m, finite_abs(f[e]));
-  return m;
+  for (int e = 0; e < 8; ++e) r = max(r, __float_as_uint(f[e]) & 0x7fffffffu);
+  return r;
+}
+// ... of its finite values: what the scale follows in a block that has others.
+template <typename T>
+__device__ __forceinline__ uint32_t chunk_finite_max(const Chunk<T>& x) {
+  float f[8];
+  x.get(f);
+  uint32_t r = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t b = __float_as_uint(f[e]) & 0x7fffffffu;
+    r = b < kInf ? max(r, b) : r;
+  }
+  return r;
 }
 
+__device__ __forceinline__ uint32_t code2_of_finite(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// special: the block has values that are not finite.
 template <typename T>
-__device__ __forceinline__ uint2 chunk_codes(const Chunk<T>& x, float inv) {
+__device__ __forceinline__ uint2 chunk_codes(const Chunk<T>& x, float inv, bool special) {
   float f[8];
   x.get(f);
 #pragma unroll
   for (int e = 0; e < 8; ++e) f[e] *= inv;
-  return make_uint2(kvq_code2(f[0], f[1]) | (kvq_code2(f[2], f[3]) << 16),
-                    kvq_code2(f[4], f[5]) | (kvq_code2(f[6], f[7]) << 16));
+  if (special)
+    return make_uint2(kvq_code2(f[0], f[1]) | (kvq_code2(f[2], f[3]) << 16),
+                      kvq_code2(f[4], f[5]) | (kvq_code2(f[6], f[7]) << 16));
+  return make_uint2(code2_of_finite(f[0], f[1]) | (code2_of_finite(f[2], f[3]) << 16),
+                    code2_of_finite(f[4], f[5]) | (code2_of_finite(f[6], f[7]) << 16));
 }
 
 // The rows [base, lo) that stay in a block whose scale grew, ratio = old scale / new, by threads
@@ -101,10 +134,12 @@ __device__ __forceinline__ bool span(const eagle_kvq_desc& d, const int32_t* sta
   return first >= 0 && n >= 0 && n <= d.rows && first <= d.max_seq - n;
 }
 
+constexpr int kWriteThreads = 128;
+
 // One block of the write kernel's work list (which: K or V; block of the request's span).
 template <typename T>
 struct WriteItem {
-  static constexpr int C = 4;  // 16-byte (bf16) chunks of a thread: 64 x 128 / 8 / 256
+  static constexpr int C = 64 * 128 / 8 / kWriteThreads;  // chunks of a thread
   Chunk<T> x[C];
   uint8_t* codes;  // the head's rows
   float* scale;
@@ -131,7 +166,7 @@ struct WriteItem {
     const int total = (hi - lo) * (d.head_dim / 8);
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      const int c = threadIdx.x + i * 256;
+      const int c = threadIdx.x + i * kWriteThreads;
       if (c < total)
         x[i].load(src + static_cast<size_t>(c) * 8);
       else
@@ -144,35 +179,46 @@ struct WriteItem {
 
 // Persistent: CTA c takes the blocks c, c + grid, ... of the list
 template <typename T>
-__global__ void __launch_bounds__(256) kvq_write_kernel(const eagle_kvq_desc d, int per_head, int items, const T* k,
+__global__ void __launch_bounds__(kWriteThreads) kvq_write_kernel(const eagle_kvq_desc d, int per_head, int items, const T* k,
                                                         const T* v, const int32_t* start, const int32_t* count,
                                                         uint8_t* k8, float* ks, uint8_t* v8, float* vs,
                                                         uint32_t* status) {
-  __shared__ float red[2][8];
+  __shared__ uint32_t red[2][kWriteThreads / 32];
   WriteItem<T> cur, nxt;
   cur.fetch(d, blockIdx.x, per_head, items, k, v, start, count, k8, ks, v8, vs, status);
   int turn = 0;
   for (int item = blockIdx.x; item < items; item += gridDim.x) {
     nxt.fetch(d, item + gridDim.x, per_head, items, k, v, start, count, k8, ks, v8, vs, status);
     if (cur.lo < cur.hi) {  // the same for the whole CTA
-      float amax = 0.f;
-#pragma unroll
-      for (int i = 0; i < cur.C; ++i) amax = fmaxf(amax, chunk_max(cur.x[i]));
       const float s_old = cur.lo > cur.base ? *cur.scale : 0.f;
-      amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-      if ((threadIdx.x & 31) == 0) red[turn][threadIdx.x >> 5] = amax;
-      __syncthreads();  // (the old scale has been read; the other half of `red` is the next block's)
+      auto reduce = [&](uint32_t m) {  // over the CTA; the halves of `red` take turns
+        m = __reduce_max_sync(0xffffffffu, m);
+        if ((threadIdx.x & 31) == 0) red[turn][threadIdx.x >> 5] = m;
+        __syncthreads();
 #pragma unroll
-      for (int w = 0; w < 8; ++w) amax = fmaxf(amax, red[turn][w]);
-      turn ^= 1;
-      const float s = fmaxf(kvq_scale(amax), s_old), inv = kvq_inverse(s);
-      if (s > s_old && s_old > 0.f) move_rows(cur.codes, d.head_dim, cur.base, cur.lo, s_old * inv, threadIdx.x, 256);
+        for (int w = 0; w < kWriteThreads / 32; ++w) m = max(m, red[turn][w]);
+        turn ^= 1;
+        return m;
+      };
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < cur.C; ++i) m = max(m, chunk_max(cur.x[i]));
+      m = reduce(m);
+      const bool special = m >= kInf;
+      if (special) {
+        m = 0;
+#pragma unroll
+        for (int i = 0; i < cur.C; ++i) m = max(m, chunk_finite_max(cur.x[i]));
+        m = reduce(m);
+      }
+      const float s = fmaxf(kvq_scale(__uint_as_float(m)), s_old), inv = kvq_inverse(s);
+      if (s > s_old && s_old > 0.f) move_rows(cur.codes, d.head_dim, cur.base, cur.lo, s_old * inv, threadIdx.x, kWriteThreads);
       const int total = (cur.hi - cur.lo) * (d.head_dim / 8);
       uint2* dst = reinterpret_cast<uint2*>(cur.codes + static_cast<size_t>(cur.lo) * d.head_dim);
 #pragma unroll
       for (int i = 0; i < cur.C; ++i) {
-        const int c = threadIdx.x + i * 256;
-        if (c < total) dst[c] = chunk_codes(cur.x[i], inv);
+        const int c = threadIdx.x + i * kWriteThreads;
+        if (c < total) dst[c] = chunk_codes(cur.x[i], inv, special);
       }
       if (threadIdx.x == 0) *cur.scale = s;
     }
@@ -286,7 +332,8 @@ __global__ void __launch_bounds__(128) kvq_commit_kernel(const eagle_commit_desc
         }
     };
     fetch(0);
-    float s_old[2] = {0.f, 0.f}, amax[2] = {0.f, 0.f}, s[2];
+    float s_old[2] = {0.f, 0.f}, s[2];
+    uint32_t m[2] = {0u, 0u};
     if (lo > base) {
       s_old[0] = *scale[0];
       s_old[1] = *scale[1];
@@ -297,12 +344,29 @@ __global__ void __launch_bounds__(128) kvq_commit_kernel(const eagle_commit_desc
 #pragma unroll
       for (int w = 0; w < 2; ++w)
 #pragma unroll
-        for (int i = 0; i < C; ++i) amax[w] = fmaxf(amax[w], chunk_max(x[w][i]));
+        for (int i = 0; i < C; ++i) m[w] = max(m[w], chunk_max(x[w][i]));
+    }
+    bool special[2];
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      m[w] = __reduce_max_sync(0xffffffffu, m[w]);
+      special[w] = m[w] >= kInf;
+    }
+    if (special[0] || special[1]) {
+      uint32_t fin[2] = {0u, 0u};
+      for (int g = 0; g < rounds; ++g) {  // (again, ending with the last round's rows)
+        fetch(g * round);
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+          for (int i = 0; i < C; ++i) fin[w] = max(fin[w], chunk_finite_max(x[w][i]));
+      }
+#pragma unroll
+      for (int w = 0; w < 2; ++w) m[w] = __reduce_max_sync(0xffffffffu, fin[w]);
     }
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-      amax[w] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax[w])));
-      s[w] = fmaxf(kvq_scale(amax[w]), s_old[w]);
+      s[w] = fmaxf(kvq_scale(__uint_as_float(m[w])), s_old[w]);
       if (s[w] > s_old[w] && s_old[w] > 0.f) move_rows(codes[w], D, base, lo, s_old[w] * kvq_inverse(s[w]), lane, 32);
     }
     for (int g = rounds - 1; g >= 0; --g) {  // (the last round's rows are still in registers)
@@ -313,7 +377,7 @@ __global__ void __launch_bounds__(128) kvq_commit_kernel(const eagle_commit_desc
         for (int i = 0; i < C; ++i)
           if (row[i] >= 0)
             *reinterpret_cast<uint2*>(codes[w] + static_cast<size_t>(lo + g * round + sub + rpp * i) * D + col) =
-                chunk_codes(x[w][i], kvq_inverse(s[w]));
+                chunk_codes(x[w][i], kvq_inverse(s[w]), special[w]);
     }
     __syncwarp();  // every lane has read the old scales
     if (lane < 2) *(lane ? scale[1] : scale[0]) = lane ? s[1] : s[0];
@@ -364,11 +428,11 @@ cudaError_t launch_kvq_write(const eagle_kvq_desc& d, const void* k, const void*
   const int per_head = static_cast<int>((d.rows + 2ll * kQB - 2) / kQB);  // blocks a span of `rows` can touch
   const long long items = 2ll * per_head * d.batch * d.n_kv_heads;
   if (items > (1ll << 30)) return cudaErrorInvalidValue;
-  const int grid = static_cast<int>(std::min<long long>(items, (d.dtype == EAGLE_F32 ? 2ll : 3ll) * num_sms));  // CTAs that fit
+  const int grid = static_cast<int>(std::min<long long>(items, (d.dtype == EAGLE_F32 ? 3ll : 4ll) * num_sms));  // CTAs that fit
   if (d.dtype == EAGLE_F32)
-    return launch(kvq_write_kernel<float>, dim3(grid), 256, s, false, d, per_head, static_cast<int>(items),
+    return launch(kvq_write_kernel<float>, dim3(grid), kWriteThreads, s, false, d, per_head, static_cast<int>(items),
                   static_cast<const float*>(k), static_cast<const float*>(v), start, count, k8, ks, v8, vs, status);
-  return launch(kvq_write_kernel<uint16_t>, dim3(grid), 256, s, false, d, per_head, static_cast<int>(items),
+  return launch(kvq_write_kernel<uint16_t>, dim3(grid), kWriteThreads, s, false, d, per_head, static_cast<int>(items),
                 static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), start, count, k8, ks, v8, vs, status);
 }
 

@@ -170,6 +170,27 @@ def test_commit_matches_the_reference(L, Bn, Hk, D, P, R, maxd, dtype):
         assert bool((feat[b, seq[b] + n:] == 0).all()) and bool((feat[b, :seq[b]] == 0).all())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_values_that_are_not_finite_are_committed_as_nan(dtype):
+    """More rows than one round of a warp, some with NaN and infinities: the scale follows the
+    finite values, the others read back as NaN."""
+    L, Bn, Hk, D, P, R = 1, 1, 2, 128, 128, 40
+    ck, sk = cache(55, (Bn, Hk), P, D)
+    t, tx = rows_of(56, (Bn, Hk, R, D), dtype)
+    for r, v in ((0, np.inf), (13, np.nan), (39, -np.inf)):
+        t[0, 1, r, r] = v
+        tx[0, 1, r, r] = v
+    dev = [[torch.from_numpy(x.copy()).cuda()] for x in (ck, sk, ck, sk)]
+    d = B.CommitDesc(L, Bn, Hk, D, R, P, R - 1, DT[dtype][1], 0, B.EAGLE_F32)
+    B.eagle_kvq_commit(d, B.KvqLayerPointers(*dev, [t], [t]), i32([R - 1]), i32([np.arange(R)]), i32([50]),
+                       torch.zeros(1, R, dtype=torch.int32, device="cuda"))
+    for h in range(Hk):
+        H.append(ck[0, h], sk[0, h], tx[0, h], 50)
+    assert np.isnan(H.decode(ck)).sum() == 3
+    same(dev[0][0], dev[1][0], ck, sk)
+    same(dev[2][0], dev[3][0], ck, sk)
+
+
 def test_commit_leaves_full_and_malformed_requests():
     Bn, Hk, D, P, R = 5, 2, 64, 70, 9
     ck, sk = cache(50, (Bn, Hk), P, D)
