@@ -418,10 +418,17 @@ def eagle_ttt_attn(desc: TttDesc, q, k_trunk, v_trunk, k_branch, v_branch, out, 
 CODES = (torch.uint8, torch.float8_e4m3fn)
 
 
+def _on_current(t: torch.Tensor, name: str) -> None:
+    """The library launches on the current device: a tensor of another one is refused."""
+    if t.is_cuda and t.get_device() != (_device_index() if _device_index is not None else torch.cuda.current_device()):
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, which is not the current device")
+
+
 def eagle_kvq_write(desc: KvqDesc, k, v, start, count: Optional[torch.Tensor], k_codes, k_scale, v_codes, v_scale,
                     status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Quantise K/V rows into the 8-bit cache (see eagle.h: eagle_kvq_write).  Codes are
     uint8 or float8_e4m3fn tensors [B][Hkv][P][D], scales fp32 [B][Hkv][ceil(P / 64)]."""
+    _on_current(k, "k")
     _check("eagle_kvq_write", load().eagle_kvq_write(
         ctypes.byref(desc), _ptr(k, FLOATS, "k"), _ptr(v, FLOATS, "v"), _ptr(start, torch.int32, "start"),
         _ptr(count, torch.int32, "count"), _ptr(k_codes, CODES, "k_codes"), _ptr(k_scale, torch.float32, "k_scale"),
@@ -432,6 +439,7 @@ def eagle_kvq_write(desc: KvqDesc, k, v, start, count: Optional[torch.Tensor], k
 def eagle_kvq_read(desc: KvqDesc, k_codes, k_scale, v_codes, v_scale, start, count: Optional[torch.Tensor], k, v,
                    status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Read rows of the 8-bit cache back (see eagle.h: eagle_kvq_read)."""
+    _on_current(k_codes, "k_codes")
     _check("eagle_kvq_read", load().eagle_kvq_read(
         ctypes.byref(desc), _ptr(k_codes, CODES, "k_codes"), _ptr(k_scale, torch.float32, "k_scale"),
         _ptr(v_codes, CODES, "v_codes"), _ptr(v_scale, torch.float32, "v_scale"), _ptr(start, torch.int32, "start"),
@@ -458,6 +466,7 @@ class KvqLayerPointers:
 def eagle_kvq_commit(desc: CommitDesc, layers: KvqLayerPointers, n_acc, path, seq_len, commit_pos,
                      feat_cache=None, tree_feat=None, status=None, stream=None) -> None:
     """Commit the accepted path into 8-bit caches (see eagle.h: eagle_kvq_commit)."""
+    _on_current(n_acc, "n_acc")
     _check("eagle_kvq_commit", load().eagle_kvq_commit(
         ctypes.byref(desc), *layers.addresses,
         _ptr(n_acc, torch.int32, "n_acc"), _ptr(path, torch.int32, "path"), _ptr(seq_len, torch.int32, "seq_len"),
@@ -470,6 +479,7 @@ def eagle_tree_attn_kvq(desc: AttnDesc, q, k_codes, k_scale, v_codes, v_scale, t
                         n_nodes: Optional[torch.Tensor] = None) -> None:
     """One layer of tree attention over the 8-bit cache (see eagle.h: eagle_tree_attn_kvq)."""
     bf16 = torch.bfloat16
+    _on_current(q, "q")
     _check("eagle_tree_attn_kvq", load().eagle_tree_attn_kvq(
         ctypes.byref(desc), _ptr(q, bf16, "q"), _ptr(k_codes, CODES, "k_codes"),
         _ptr(k_scale, torch.float32, "k_scale"), _ptr(v_codes, CODES, "v_codes"),
@@ -485,6 +495,7 @@ def eagle_qk_norm_rope(desc: QkNormRopeDesc, qkv, q_weight: Optional[torch.Tenso
                        n_nodes: Optional[torch.Tensor] = None) -> None:
     """Norms of the query and key heads, rotation and tree layout (see eagle.h:
     eagle_qk_norm_rope)."""
+    _on_current(qkv, "qkv")
     _check("eagle_qk_norm_rope", load().eagle_qk_norm_rope(
         ctypes.byref(desc), _ptr(qkv, FLOATS, "qkv"), _ptr(q_weight, FLOATS, "q_weight"),
         _ptr(k_weight, FLOATS, "k_weight"), _ptr(inv_freq, torch.float32, "inv_freq"),

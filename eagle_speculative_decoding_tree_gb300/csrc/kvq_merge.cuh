@@ -7,6 +7,17 @@
 
 namespace eagle {
 
+// 128-key tiles of a piece (tcgen05) or units, the tree counted as one, of a split (mma.sync) for
+// a request of `tiles` prefix tiles; how many pieces / splits have work.
+__device__ __forceinline__ int kvq_tps(const KvqAttnArgs& a, int tiles) {
+  if (!a.even) return a.tps;
+  return a.tc ? max(1, (tiles + a.splits - 2) / (a.splits - 1)) : (tiles + a.splits) / a.splits;
+}
+__device__ __forceinline__ int kvq_pieces(const KvqAttnArgs& a, int tiles) {
+  const int tps = kvq_tps(a, tiles);
+  return min(a.splits, a.tc ? 1 + (tiles + tps - 1) / tps : (tiles + tps) / tps);
+}
+
 // Partial rows come through L2 (other SMs wrote them); volatile, so that the loads of a batch
 // stay ahead of everything that uses them.
 __device__ __forceinline__ void ld_part(const float* p, float (&x)[4]) {

@@ -174,6 +174,7 @@ struct KvqAttnPlan {
   int splits, tps;  // mma.sync: split s takes 128-key units [s tps, (s + 1) tps) of its request, the
                     // tree being the last; tcgen05: piece 0 is the tree, piece s the prefix tiles
                     // [(s - 1) tps, s tps)
+  bool even;        // instead of a fixed tps, a request's own length shared out over all splits
   bool coop;        // the whole grid fits on the SMs: splits merge in the kernel
   size_t off_err, off_cnt, off_o, off_ml, total;
 };
@@ -195,7 +196,7 @@ struct KvqAttnArgs {
   float* part_ml;  // [B*Hkv][splits][rows_pad][2]: max in log2 units, sum
   int* err;
   int* cnt;        // coop: [groups][2] published / finished pieces, zero between calls
-  int B, R, Hq, Hkv, G, P, W, splits, tps, rows_pad, out_f32, wr, tc, coop, nst;
+  int B, R, Hq, Hkv, G, P, W, splits, tps, rows_pad, out_f32, wr, tc, coop, nst, even;
   uint32_t g_inv;  // ceil(2^32 / G) for G > 1
   float scale, scale_log2;
 };

@@ -11,10 +11,10 @@
 //
 // Bound by HBM for long inputs, by latency for one tree.  A warp takes one row, or a run of its
 // heads when the rows alone would leave SMs empty (16 lanes x 8 elements = a head of 128, two
-// heads a pass; four heads of 64), with four passes' loads in
+// heads a pass; four heads of 64), with three passes' loads in
 // flight (a slot is loaded again as soon as its elements are in use).  Warps need nothing of one
-// another, so one warp's loads, another's sines and a third's stores overlap: 47 us for 8192 rows
-// of 48 heads (201 MB, 4.25 TB/s; a device copy of as many bytes takes 65 us).  A CTA per row with
+// another, so one warp's loads, another's sines and a third's stores overlap: 46 us for 8192 rows
+// of 48 heads (201 MB, 4.35 TB/s; a device copy of as many bytes takes 65 us).  A CTA per row with
 // the sines shared over its heads took 76 us, every CTA going through its load, barrier and store
 // phases alone.  The row's rot / 2 sines and cosines are computed two a lane into the warp's table
 // while the first loads are on their way to L2.
@@ -25,11 +25,24 @@
 
 #include "common.cuh"
 #include "launch.h"
+#include "sm100.cuh"
 
 namespace eagle {
 namespace {
 
+using sm100::f32x2_split;
+using sm100::fma_f32x2;
+
 constexpr int kThreads = 128;
+
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  return sm100::f32x2(__float_as_uint(lo), __float_as_uint(hi));
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
 struct RopeArgs {
   const void* qkv;
@@ -116,7 +129,7 @@ template <bool F32, int D>
 __global__ void __launch_bounds__(kThreads, F32 ? 5 : 7) qk_norm_rope_kernel(const RopeArgs a) {
   constexpr int LANES = D / 8;       // lanes of a head
   constexpr int HPP = 32 / LANES;    // heads of a pass
-  constexpr int U = F32 ? 2 : 4;     // passes whose loads are in flight together
+  constexpr int U = F32 ? 2 : 3;     // passes whose loads are in flight together
   __shared__ __align__(16) float2 table[kThreads / 32][D / 2];
   const int warp = threadIdx.x >> 5;
   const long long unit = static_cast<long long>(blockIdx.x) * (kThreads / 32) + warp;
@@ -159,8 +172,9 @@ __global__ void __launch_bounds__(kThreads, F32 ? 5 : 7) qk_norm_rope_kernel(con
       if (h < k1) x[u].load(a.qkv, src + static_cast<size_t>(h) * D);
     }
     const void* weight = kind == 0 ? a.wq : (kind == 1 ? a.wk : nullptr);
-    float c[8], s[8];
+    uint64_t c2[4], s2[4];  // in pairs
     if (kind < 2) {
+      float c[8], s[8];
       Lane8<F32> t;
       float w[8], wp[8];
 #pragma unroll
@@ -178,6 +192,11 @@ __global__ void __launch_bounds__(kThreads, F32 ? 5 : 7) qk_norm_rope_kernel(con
         c[e] = w[e] * v.x;
         s[e] = (a.interleaved ? w[e ^ 1] : wp[e]) * ((a.interleaved ? (e & 1) != 0 : second) ? v.y : -v.y);
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        c2[e] = pair(c[2 * e], c[2 * e + 1]);
+        s2[e] = pair(s[2 * e], s[2 * e + 1]);
+      }
     }
     // this lane's 16 bytes (bf16) of head h in the output of its kind
     uint8_t* out = static_cast<uint8_t*>(kind == 0 ? a.q : (kind == 1 ? a.k : a.v));
@@ -191,24 +210,38 @@ __global__ void __launch_bounds__(kThreads, F32 ? 5 : 7) qk_norm_rope_kernel(con
         float f[8];
         x[u].get(f);
         if (kind < 2) {
-          float p[8];
+          // two elements an instruction from here on
+          uint64_t f2[4], p2[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f2[e] = pair(f[2 * e], f[2 * e + 1]);
           if (a.interleaved) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) p[e] = f[e ^ 1];
+            for (int e = 0; e < 4; ++e) p2[e] = pair(f[2 * e + 1], f[2 * e]);
           } else {
+            float p[8];
             x[u].from(lane + far, LANES).get(p);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p2[e] = pair(p[2 * e], p[2 * e + 1]);
           }
           float g = 1.f;
           if (weight) {
-            float ss = 0.f;
+            uint64_t ss2 = mul_f32x2(f2[0], f2[0]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
+            for (int e = 1; e < 4; ++e) ss2 = fma_f32x2(f2[e], f2[e], ss2);
+            float s0, s1;
+            f32x2_split(ss2, s0, s1);
+            float ss = s0 + s1;
 #pragma unroll
             for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, LANES);
             g = rsqrtf(ss * (1.f / D) + a.eps);
           }
+          const uint64_t g2 = pair(g, g);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = (in ? fmaf(f[e], c[e], p[e] * s[e]) : f[e] * c[e]) * g;
+          for (int e = 0; e < 4; ++e) {
+            // (the elements that do not turn have no partner: infinities times their sine of 0)
+            const uint64_t t = mul_f32x2(f2[e], c2[e]);
+            f32x2_split(mul_f32x2(in ? fma_f32x2(p2[e], s2[e], t) : t, g2), f[2 * e], f[2 * e + 1]);
+          }
         }
         const int next = h + U * HPP;  // the slot's next head
         if (next < k1) x[u].load(a.qkv, src + static_cast<size_t>(next) * D);

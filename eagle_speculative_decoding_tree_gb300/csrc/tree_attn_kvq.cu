@@ -178,7 +178,8 @@ __global__ void __launch_bounds__(CW * 32, 1)
   const int L = prefix_len(a, b), Rb = tree_rows(a, b);
   const int RG = Rb * a.G;
   const int n_pref = (L + KT - 1) / KT;
-  const int u0 = split * a.tps, u1 = min(n_pref + 1, u0 + a.tps);
+  const int tps = kvq_tps(a, n_pref);
+  const int u0 = split * tps, u1 = min(n_pref + 1, u0 + tps);
   const int n_pt = max(0, min(u1, n_pref) - u0);
   const bool tree = u0 <= n_pref && u1 == n_pref + 1;
   if (u0 > n_pref || rb * rows_cta >= RG) return;  // nothing of this request here (the combine skips it)
@@ -513,7 +514,7 @@ __global__ void __launch_bounds__(CW * 32, 1)
   }
   if (a.coop) {
     // the group's merge (request, KV head, row block): an even share of its rows, a warp per row
-    const int need = min(a.splits, (n_pref + a.tps) / a.tps);
+    const int need = kvq_pieces(a, n_pref);
     __threadfence();
     __syncthreads();
     if (threadIdx.x == 0)
@@ -541,7 +542,7 @@ __global__ void __launch_bounds__(128) kvq_combine_kernel(const KvqAttnArgs a) {
   const int b = bh / a.Hkv, h = bh % a.Hkv;
   if (r >= tree_rows(a, b) * a.G) return;
   const int tiles = (prefix_len(a, b) + KT - 1) / KT;
-  const int n = min(a.splits, a.tc ? 1 + (tiles + a.tps - 1) / a.tps : (tiles + a.tps) / a.tps);
+  const int n = kvq_pieces(a, tiles);
   kvq_merge_row<D, 16>(a, static_cast<size_t>(bh) * a.splits * a.rows_pad + r, n,
                        (static_cast<size_t>(b) * a.R + r / a.G) * a.Hq + h * a.G + r % a.G, lane);
 }
@@ -614,7 +615,7 @@ void plan_kvq_attn(const eagle_attn_desc* d, int num_sms, KvqAttnPlan* p) {
   const bool tcgen = d->engine == EAGLE_ENGINE_AUTO && p->D == 128 && p->G <= 4096;
   p->few = tcgen && RG <= 32;
   p->tc = tcgen && !p->few;
-  p->coop = false;
+  p->coop = p->even = false;
   if (p->tc || p->few) {
     p->wr = RG > 128 ? 2 : 1;
     p->rows_per_cta = p->few ? (RG <= 16 ? 16 : 32) : p->wr * 128;
@@ -631,9 +632,12 @@ void plan_kvq_attn(const eagle_attn_desc* d, int num_sms, KvqAttnPlan* p) {
       const int want = base < num_sms ? 24 : 32;
       const long long one = std::min<long long>(num_sms / base - 1, tiles);
       const long long many = std::max(1, (tiles + want / 2) / want);
+      // (one wave also shares a request's own length out evenly: a capacity far above the lengths
+      // in use leaves no CTA idle)
       const long long t_one = one < 1 ? 1ll << 60 : (tiles + one - 1) / one + 6;
       const long long t_many = base * (tiles + 6 * (many + 1)) / num_sms + want / 2;
       pieces = t_one <= t_many ? one : many;
+      p->even = t_one <= t_many;
     }
     pieces = std::min<long long>(std::min<long long>(pieces, tiles), 255);
     p->tps = static_cast<int>((tiles + pieces - 1) / pieces);
@@ -650,6 +654,7 @@ void plan_kvq_attn(const eagle_attn_desc* d, int num_sms, KvqAttnPlan* p) {
     const long long base = static_cast<long long>(p->B) * p->Hkv * p->row_blocks;
     long long splits = d->num_splits > 0 ? d->num_splits : std::max<long long>(1, num_sms / base);
     if (d->num_splits <= 0 && p->B > 1) splits = std::max<long long>(splits, (tiles + 1) / 16);
+    p->even = p->B == 1;
     splits = std::min<long long>(std::min<long long>(splits, tiles + 1), 256);
     p->tps = static_cast<int>((tiles + splits) / splits);
     p->splits = (tiles + p->tps) / p->tps;
@@ -694,6 +699,7 @@ cudaError_t launch_kvq_attn(const KvqAttnPlan& p, const void* q, const void* k8,
   a.err = reinterpret_cast<int*>(w + p.off_err);
   a.cnt = reinterpret_cast<int*>(w + p.off_cnt);
   a.coop = p.coop ? 1 : 0;
+  a.even = p.even ? 1 : 0;
   a.B = p.B;
   a.R = p.R;
   a.Hq = p.Hq;

@@ -234,8 +234,9 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
   const int Rb = a.n_nodes ? min(max(a.n_nodes[b], 0), a.R) : a.R;
   const int RG = Rb * a.G;
   const int n_pref = (L + KT - 1) / KT;
-  const int tile0 = (piece - 1) * a.tps;
-  const int n = piece == 0 || RG == 0 ? 0 : max(0, min(a.tps, n_pref - tile0));
+  const int tps = kvq_tps(a, n_pref);
+  const int tile0 = (piece - 1) * tps;
+  const int n = piece == 0 || RG == 0 ? 0 : max(0, min(tps, n_pref - tile0));
   const bool tree = piece == 0 && RG > 0, work = n > 0;
   const size_t prow0 = (static_cast<size_t>(bh) * a.splits + piece) * a.rows_pad;
   const uint32_t tb = tmem_base;
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
   auto col_o = [](int w) { return static_cast<uint32_t>(2 * F::NS + w * F::NP); };
 
   // the group's merge (request, KV head): an even share of its rows, a warp per row
-  const int need = 1 + min(a.splits - 1, (n_pref + a.tps - 1) / a.tps);
+  const int need = kvq_pieces(a, n_pref);
   auto merge = [&](int warps) {
     if (!a.coop) return;
     __threadfence();
@@ -612,6 +613,10 @@ cudaError_t launch_few(const KvqAttnPlan& p, const Maps& tm, const KvqAttnArgs& 
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !(__atomic_load_n(&configured, __ATOMIC_ACQUIRE) & (1ull << dev))) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaFuncAttributes fa;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kern);
+    // the register split needs all of them at launch (it would wait for more for ever)
+    if (e == cudaSuccess && NR == 32 && fa.numRegs != 96) e = cudaErrorInvalidKernelImage;
     if (e != cudaSuccess) return e;
     if (dev < 64) __atomic_fetch_or(&configured, 1ull << dev, __ATOMIC_RELEASE);
   }

@@ -257,8 +257,9 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
   r.Rb = a.n_nodes ? min(max(a.n_nodes[b], 0), a.R) : a.R;
   r.tree = piece == 0;
   const int n_pref = (r.L + KT - 1) / KT;
-  r.tile0 = (piece - 1) * a.tps;
-  r.n = r.tree ? 1 : max(0, min(a.tps, n_pref - r.tile0));
+  const int tps = kvq_tps(a, n_pref);
+  r.tile0 = (piece - 1) * tps;
+  r.n = r.tree ? 1 : max(0, min(tps, n_pref - r.tile0));
   const int RG = r.Rb * a.G;
   const bool work = r.n > 0 && row0 < RG;
   const int items = work ? (two ? 2 * r.n : r.n) : 0;
@@ -711,7 +712,7 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
         // The group's merge: count this piece into its group (request, KV head, row block), wait
         // until every piece that has work has counted, then merge an even share of its rows from
         // L2, a warp per row.  A piece that gave up counts too: the others need not wait for it.
-        const int need = 1 + min(a.splits - 1, (n_pref + a.tps - 1) / a.tps);
+        const int need = kvq_pieces(a, n_pref);
         __threadfence();
         bar_sync(1, 256);
         if (threadIdx.x == 0) go = kvq_group_wait(a.cnt + 2 * (bh * gridDim.z + rb), need, a.err, ERR_GROUP) ? 1 : 0;
@@ -748,6 +749,10 @@ cudaError_t launch_tc(const KvqAttnPlan& p, const Maps& tm, const KvqAttnArgs& a
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !(__atomic_load_n(&configured, __ATOMIC_ACQUIRE) & (1ull << dev))) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    cudaFuncAttributes fa;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kern);
+    // the register split needs all of them at launch (it would wait for more for ever)
+    if (e == cudaSuccess && fa.numRegs != 128) e = cudaErrorInvalidKernelImage;
     if (e != cudaSuccess) return e;
     if (dev < 64) __atomic_fetch_or(&configured, 1ull << dev, __ATOMIC_RELEASE);
   }

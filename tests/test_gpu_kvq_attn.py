@@ -213,6 +213,14 @@ def test_scales_of_any_kind(R):
     c.check(c.desc(True, True))
 
 
+@pytest.mark.parametrize("shape", [(1, 4, 32, 8, 128, 20000, [900]), (1, 61, 32, 8, 128, 20000, [1300]),
+                                   (2, 40, 8, 2, 128, 20000, [127, 2100]), (1, 3, 4, 2, 64, 9000, [700])],
+                         ids=lambda s: "-".join(map(str, s[:6])))
+def test_capacity_far_above_the_lengths(shape):
+    c = Case(13, *shape)
+    c.check(c.desc(True, True))
+
+
 @pytest.mark.parametrize("R", [1, 8, 61])
 def test_growing_scores(R):
     """Keys whose scores rise from tile to tile move every row's reference, several times."""
