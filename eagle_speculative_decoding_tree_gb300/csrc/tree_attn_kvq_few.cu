@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
     if (!go) return;
     const int hi = (piece + 1) * RG / need;
     for (int k = piece * RG / need + warp; k < hi; k += warps)
-      kvq_merge_row<128, NR == 32 ? 12 : 20>(a, static_cast<size_t>(bh) * a.splits * a.rows_pad + k, need,
+      kvq_merge_row<128, 20>(a, static_cast<size_t>(bh) * a.splits * a.rows_pad + k, need,
                              (static_cast<size_t>(b) * a.R + k / a.G) * a.Hq + h * a.G + k % a.G, lane);
   };
 
@@ -285,6 +285,9 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
           if (t >= ST && !wait_parity(&v_empty[s], (t / ST - 1) & 1, a.err, ERR_VE)) break;
           load(tm.v, F::SM_V + s * T8, &v_full[s], t);
           ++v_in;
+          // the first tile first: with the whole ring's loads ahead of them the queries and scales
+          // would arrive last, and nothing can start without them
+          if (t == 0 && !wait_parity(&q_full, 0, a.err, ERR_Q)) break;
         }
         // no copy may still be landing when the CTA ends
         for (int s = 0; s < ST && s < k_in; ++s) (void)wait_parity(&k_full[s], ((k_in - 1 - s) / ST) & 1, a.err, ERR_K);
@@ -343,15 +346,26 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
       const int vote = 1 + (warp >> 2), g0 = (warp >> 3) * 16;  // named barrier; the first of its rows
       const int key = qd * 32 + lane;  // of a tile; TMEM lane
       // Q: eight lanes a row, dims 8 c .. and 64 + 8 c ..
+      const int row = threadIdx.x >> 3, c = threadIdx.x & 7;
+      uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
+      if (row < min(RG, NR)) {
+        const uint4* src = reinterpret_cast<const uint4*>(
+            a.q + ((static_cast<size_t>(b) * a.R + row / a.G) * a.Hq + h * a.G + row % a.G) * 128 + 8 * c);
+        x0 = __ldg(src);
+        x1 = __ldg(src + 8);
+      }
+      // vref: the largest V scale of the piece; the scales of this key's blocks
+      const int nblk = (a.P + kQB - 1) / kQB, blk0 = tile0 * (KT / kQB);
+      const int n_blk = (min(L, (tile0 + n) * KT) + kQB - 1) / kQB - blk0;
+      const float* ks = a.ks + static_cast<size_t>(bh) * nblk + blk0;
+      const float* vs = a.vs + static_cast<size_t>(bh) * nblk + blk0;
+      float vref = 0.f;
+#pragma unroll 4
+      for (int i = lane; i < n_blk; i += 32) vref = fmaxf(vref, __ldg(vs + i));
+      vref = warp_max(vref);
+      if (!(vref > 0.f)) vref = 1.f;
+      const float vinv = 1.f / vref;
       if (threadIdx.x < NR * 8) {
-        const int row = threadIdx.x >> 3, c = threadIdx.x & 7;
-        uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
-        if (row < RG) {
-          const uint4* src = reinterpret_cast<const uint4*>(
-              a.q + ((static_cast<size_t>(b) * a.R + row / a.G) * a.Hq + h * a.G + row % a.G) * 128 + 8 * c);
-          x0 = __ldg(src);
-          x1 = __ldg(src + 8);
-        }
         const uint32_t u[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
         uint32_t am = 0;  // the row's largest magnitude, as bf16 bits (ordered as integers)
 #pragma unroll
@@ -386,16 +400,6 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full);
-      // vref: the largest V scale of the piece; the scales of this key's blocks
-      const int nblk = (a.P + kQB - 1) / kQB, blk0 = tile0 * (KT / kQB);
-      const int n_blk = (min(L, (tile0 + n) * KT) + kQB - 1) / kQB - blk0;
-      const float* ks = a.ks + static_cast<size_t>(bh) * nblk + blk0;
-      const float* vs = a.vs + static_cast<size_t>(bh) * nblk + blk0;
-      float vref = 0.f;
-      for (int i = lane; i < n_blk; i += 32) vref = fmaxf(vref, __ldg(vs + i));
-      vref = warp_max(vref);
-      if (!(vref > 0.f)) vref = 1.f;
-      const float vinv = 1.f / vref;
       float kn, vn;
       auto fetch = [&](int t) {
         const int kb = min(2 * t + (qd >> 1), n_blk - 1);
@@ -538,8 +542,7 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
         ok = __all_sync(0xffffffffu, ok);
       }
       // ---- epilogue: the parities' states meet; a thread is now one head dim for its 16 rows
-      bool done = __all_sync(0xffffffffu, ok && wait_parity(&o_full, 0, a.err, ERR_O));
-      tc_fence_after();
+      // (the row sums while the last product runs)
 #pragma unroll
       for (int r = 0; r < 16; r += 2) {
         float y0, y1;
@@ -551,6 +554,8 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
           s_red[w][qd][g0 + r + 1] = y1;
         }
       }
+      bool done = __all_sync(0xffffffffu, ok && wait_parity(&o_full, 0, a.err, ERR_O));
+      tc_fence_after();
       done = bar_and(5, SW * 32, done);
       if (done) {
         const float unit = vref * (1.f / (1 << PB));
@@ -572,23 +577,26 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
 #pragma unroll
           for (int r = 0; r < 16; ++r) so[(g0 + r) * 128 + key] = o[r];
         }
+        if (w == 0 && key < 16) {  // a row's weights of the two parities, its maximum and sum
+          const int r = g0 + key;
+          const float m0 = s_m[0][r], m1 = two ? s_m[1][r] : -INFINITY;
+          const float M = fmaxf(m0, m1);
+          const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - M), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
+          s_al[0][r] = f0;
+          s_al[1][r] = f1;
+          const float l0 = (s_red[0][0][r] + s_red[0][1][r]) + (s_red[0][2][r] + s_red[0][3][r]);
+          const float l1 = (s_red[1][0][r] + s_red[1][1][r]) + (s_red[1][2][r] + s_red[1][3][r]);
+          if (r < RG) *reinterpret_cast<float2*>(a.part_ml + (prow0 + r) * 2) = make_float2(M, fmaf(f0, l0, f1 * l1));
+        }
         bar_sync(5, SW * 32);
         if (w == 0) {
+          float* po = a.part_o + (prow0 + g0) * 128 + key;
 #pragma unroll
-          for (int rr = 0; rr < 16; ++rr) {
-            const int r = g0 + rr;
-            if (r >= RG) break;
-            const float m0 = s_m[0][r], m1 = two ? s_m[1][r] : -INFINITY;
-            const float M = fmaxf(m0, m1);
-            const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - M), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
-            float y = o[rr] * f0;
-            if (two) y = fmaf(so[r * 128 + key], f1, y);
-            a.part_o[(prow0 + r) * 128 + key] = y;
-            if (key == 0) {
-              const float l0 = (s_red[0][0][r] + s_red[0][1][r]) + (s_red[0][2][r] + s_red[0][3][r]);
-              const float l1 = (s_red[1][0][r] + s_red[1][1][r]) + (s_red[1][2][r] + s_red[1][3][r]);
-              *reinterpret_cast<float2*>(a.part_ml + (prow0 + r) * 2) = make_float2(M, fmaf(f0, l0, f1 * l1));
-            }
+          for (int r = 0; r < 16; ++r) {
+            if (g0 + r >= RG) break;
+            float y = o[r] * s_al[0][g0 + r];
+            if (two) y = fmaf(so[(g0 + r) * 128 + key], s_al[1][g0 + r], y);
+            po[r * 128] = y;
           }
         }
       }

@@ -458,6 +458,24 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(src), "r"(n16) : "memory");
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at + T8), "l"(src + 64), "r"(n16) : "memory");
         }
+      }
+      // (under the copies) vref: the largest V scale of the piece
+      const float* ks = a.ks + static_cast<size_t>(bh) * nblk + r.tile0 * (KT / kQB);
+      const float* vs = a.vs + static_cast<size_t>(bh) * nblk + r.tile0 * (KT / kQB);
+      int n_blk = 0;
+      float vref = 1.f;
+      if (!r.tree) {
+        n_blk = (min(r.L, (r.tile0 + r.n) * KT) + kQB - 1) / kQB - r.tile0 * (KT / kQB);
+        float m = 0.f;
+#pragma unroll 4
+        for (int i = lane; i < n_blk; i += 32) m = fmaxf(m, __ldg(vs + i));
+        m = warp_max(m);
+        if (m > 0.f) vref = m;
+      }
+      const float vinv = 1.f / vref;
+      if (two || w == 0) {
+        const int c = lane & 7, sub = lane >> 3;
+        uint8_t* dst = smem + SM_Q + w * T16;
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncwarp();
 #pragma unroll 2
@@ -503,19 +521,6 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
         if (!two) bar_sync(1, 256);  // (A: the warp staged its own rows)
         qs = s_q[two ? w : 0][rl];
       }
-      // vref: the largest V scale of the piece
-      const float* ks = a.ks + static_cast<size_t>(bh) * nblk + r.tile0 * (KT / kQB);
-      const float* vs = a.vs + static_cast<size_t>(bh) * nblk + r.tile0 * (KT / kQB);
-      int n_blk = 0;
-      float vref = 1.f;
-      if (!r.tree) {
-        n_blk = (min(r.L, (r.tile0 + r.n) * KT) + kQB - 1) / kQB - r.tile0 * (KT / kQB);
-        float m = 0.f;
-        for (int i = lane; i < n_blk; i += 32) m = fmaxf(m, __ldg(vs + i));
-        m = warp_max(m);
-        if (m > 0.f) vref = m;
-      }
-      const float vinv = 1.f / vref;
       uint32_t tw[4] = {0u, 0u, 0u, 0u};  // the tree's visible keys
       if (r.tree && live) {
         const uint64_t* mp = a.anc_mask + (static_cast<size_t>(b) * a.R + node) * a.W;
