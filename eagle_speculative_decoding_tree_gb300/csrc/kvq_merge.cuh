@@ -20,11 +20,20 @@ __device__ __forceinline__ int kvq_pieces(const KvqAttnArgs& a, int tiles) {
 
 // Partial rows come through L2 (other SMs wrote them); volatile, so that the loads of a batch
 // stay ahead of everything that uses them.
-__device__ __forceinline__ void ld_part(const float* p, float (&x)[4]) {
-  asm volatile("ld.global.cg.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "l"(p));
+// Not `on`: zeros, nothing read.
+__device__ __forceinline__ void ld_part(const float* p, float (&x)[4], bool on) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %5, 0;\n mov.f32 %0, 0f00000000;\n mov.f32 %1, 0f00000000;\n"
+      " mov.f32 %2, 0f00000000;\n mov.f32 %3, 0f00000000;\n @q ld.global.cg.v4.f32 {%0,%1,%2,%3}, [%4];\n}\n"
+      : "=&f"(x[0]), "=&f"(x[1]), "=&f"(x[2]), "=&f"(x[3])
+      : "l"(p), "r"(on ? 1 : 0));
 }
-__device__ __forceinline__ void ld_part(const float* p, float (&x)[2]) {
-  asm volatile("ld.global.cg.v2.f32 {%0,%1}, [%2];" : "=f"(x[0]), "=f"(x[1]) : "l"(p));
+__device__ __forceinline__ void ld_part(const float* p, float (&x)[2], bool on) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %3, 0;\n mov.f32 %0, 0f00000000;\n mov.f32 %1, 0f00000000;\n"
+      " @q ld.global.cg.v2.f32 {%0,%1}, [%2];\n}\n"
+      : "=&f"(x[0]), "=&f"(x[1])
+      : "l"(p), "r"(on ? 1 : 0));
 }
 
 // The group's meeting under a cooperative launch (every CTA resident).  One thread of a CTA whose
@@ -66,10 +75,12 @@ __device__ __forceinline__ void kvq_merge_row(const KvqAttnArgs& a, size_t base,
   for (int s0 = 0; s0 < n; s0 += BATCH) {
     float x[BATCH][PER];
     const int mine = s0 + lane;
-    float ml[2] = {-INFINITY, 0.f};
-    if (lane < BATCH && mine < n) ld_part(a.part_ml + (base + static_cast<size_t>(mine) * step) * 2, ml);
+    const bool has = lane < BATCH && mine < n;
+    float ml[2];
+    ld_part(a.part_ml + (base + static_cast<size_t>(mine) * step) * 2, ml, has);
 #pragma unroll
-    for (int u = 0; u < BATCH; ++u) ld_part(po + static_cast<size_t>(min(s0 + u, n - 1)) * step * D, x[u]);
+    for (int u = 0; u < BATCH; ++u) ld_part(po + static_cast<size_t>(s0 + u) * step * D, x[u], s0 + u < n);
+    if (!has) ml[0] = -INFINITY;
     const float top = fmaxf(M, warp_max(ml[0]));
     const float old = M == -INFINITY ? 0.f : sm100::ex2(M - top);
     const float f = ml[0] == -INFINITY ? 0.f : sm100::ex2(ml[0] - top);
