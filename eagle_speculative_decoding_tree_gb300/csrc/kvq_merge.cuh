@@ -18,6 +18,20 @@ __device__ __forceinline__ int kvq_pieces(const KvqAttnArgs& a, int tiles) {
   return min(a.splits, a.tc ? 1 + (tiles + tps - 1) / tps : (tiles + tps) / tps);
 }
 
+// The tcgen05 kernels' grid (groups x row blocks, pieces): what this CTA takes.  nrb: row blocks.
+__device__ __forceinline__ void kvq_place(const KvqAttnArgs& a, int nrb, int& piece, int& bh, int& rb) {
+  int group = blockIdx.x;
+  if (a.coop) {
+    const int id = blockIdx.y * gridDim.x + blockIdx.x;
+    group = id / gridDim.y;
+    piece = id % gridDim.y;
+  } else {
+    piece = blockIdx.y + 1 < gridDim.y ? blockIdx.y + 1 : 0;
+  }
+  bh = nrb == 1 ? group : group / nrb;
+  rb = nrb == 1 ? 0 : group % nrb;
+}
+
 // Partial rows come through L2 (other SMs wrote them); volatile, so that the loads of a batch
 // stay ahead of everything that uses them.
 // Not `on`: zeros, nothing read.

@@ -596,6 +596,35 @@ cudaError_t launch_mma(const KvqAttnPlan& p, const Maps& tm, const KvqAttnArgs& 
 
 }  // namespace
 
+// Prefix pieces of a request, beside its tree, on the tcgen05 kernels (one CTA per SM: they hold
+// all of TMEM); base: groups (requests x KV heads x row blocks); a CTA costs about `extra` tiles'
+// time besides its own (prologue, partials, meeting).  Either one wave of CTAs that shares every
+// request's own length out evenly, so that a capacity far above the lengths in use leaves no CTA
+// idle; or fixed pieces.  The lengths are not known here, so each choice is judged by two cases
+// together: all requests of full length (waves of equal CTAs), and lengths spread evenly (the
+// mean work, and a tail of most of a piece).  Measured: 8 requests of 1K to 16K x 8 heads 94 to
+// 112 us with 3 to 8 pieces, 128 with 2, 228 in one wave; 32 such 275 us with 3 or 4, 299 with 6;
+// 4 requests of 32K 131 us with 9, 147 with 11, 163 in one wave; one of 8K 21 us in one wave.
+static long long choose_pieces(long long base, int tiles, int num_sms, int extra, bool* even) {
+  const long long one = std::min<long long>(num_sms / base - 1, tiles);
+  *even = one >= 1;
+  long long best = std::max<long long>(one, 1);
+  double least = one >= 1 ? 2.0 * static_cast<double>((tiles + one - 1) / one + extra) : 1e30;
+  for (int n = 1; n <= std::min(tiles, 64); ++n) {
+    const int tps = (tiles + n - 1) / n;
+    const double full = static_cast<double>((base * n + num_sms - 1) / num_sms) * (tps + extra);
+    const double spread =
+        static_cast<double>(base) / num_sms * (0.5 * tiles + extra * (0.5 * n + 1)) + 0.7 * (tps + extra);
+    const double t = full + spread + extra;  // (and a second launch)
+    if (t < least) {
+      least = t;
+      best = n;
+      *even = false;
+    }
+  }
+  return best;
+}
+
 void plan_kvq_attn(const eagle_attn_desc* d, int num_sms, KvqAttnPlan* p) {
   p->B = d->batch;
   p->R = d->rows;
@@ -620,25 +649,9 @@ void plan_kvq_attn(const eagle_attn_desc* d, int num_sms, KvqAttnPlan* p) {
     p->wr = RG > 128 ? 2 : 1;
     p->rows_per_cta = p->few ? (RG <= 16 ? 16 : 32) : p->wr * 128;
     p->row_blocks = (RG + p->rows_per_cta - 1) / p->rows_per_cta;
-    // Prefix pieces of a request, beside its tree.  Either one wave of CTAs (one per SM: they hold
-    // all of TMEM), or pieces of 24 tiles (32 when the groups alone fill the SMs), so that ragged
-    // requests balance: whichever is estimated shorter, a CTA costing about six tiles' time
-    // besides its own (prologue, partials).  Measured: 8 requests of 1K to 16K x 8 heads 102 us
-    // with 22 tiles, 109 with 15, 228 in one wave; 32 such 322 us with 33, 339 with 22, 359 with
-    // 15; 4 requests of 32K 131 us with 29, 163 in one wave; one of 8K 21 us in one wave.
     const long long base = static_cast<long long>(p->B) * p->Hkv * p->row_blocks;
     long long pieces = d->num_splits;
-    if (pieces <= 0) {
-      const int want = base < num_sms ? 24 : 32;
-      const long long one = std::min<long long>(num_sms / base - 1, tiles);
-      const long long many = std::max(1, (tiles + want / 2) / want);
-      // (one wave also shares a request's own length out evenly: a capacity far above the lengths
-      // in use leaves no CTA idle)
-      const long long t_one = one < 1 ? 1ll << 60 : (tiles + one - 1) / one + 6;
-      const long long t_many = base * (tiles + 6 * (many + 1)) / num_sms + want / 2;
-      pieces = t_one <= t_many ? one : many;
-      p->even = t_one <= t_many;
-    }
+    if (pieces <= 0) pieces = choose_pieces(base, tiles, num_sms, p->few ? 10 : 6, &p->even);
     pieces = std::min<long long>(std::min<long long>(pieces, tiles), 255);
     p->tps = static_cast<int>((tiles + pieces - 1) / pieces);
     p->splits = (tiles + p->tps - 1) / p->tps + 1;

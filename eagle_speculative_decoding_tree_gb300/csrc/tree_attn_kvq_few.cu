@@ -199,7 +199,8 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
   __shared__ __align__(16) float s_al[2][NR];  // slow path: the rows' rescale
   __shared__ float s_red[2][4][NR];            // slow path, epilogue: the warps' maxima / sums
 
-  const int piece = blockIdx.x, bh = blockIdx.y;
+  int piece, bh, rb;  // dispatch order as in tree_attn_kvq_tc.cu
+  kvq_place(a, 1, piece, bh, rb);
   const int b = bh / a.Hkv, h = bh % a.Hkv;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
@@ -629,7 +630,7 @@ cudaError_t launch_few(const KvqAttnPlan& p, const Maps& tm, const KvqAttnArgs& 
     if (dev < 64) __atomic_fetch_or(&configured, 1ull << dev, __ATOMIC_RELEASE);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.splits, p.B * p.Hkv);
+  cfg.gridDim = dim3(p.B * p.Hkv, p.splits);
   cfg.blockDim = dim3(Few<NR, TERMS>::NT);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;

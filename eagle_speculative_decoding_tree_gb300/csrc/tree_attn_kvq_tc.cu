@@ -217,7 +217,12 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
   float (*s_m)[128] = reinterpret_cast<float (*)[128]>(smem + SM_W);
   float (*s_l)[128] = reinterpret_cast<float (*)[128]>(smem + SM_W + 1024);
 
-  const int piece = blockIdx.x, bh = blockIdx.y, rb = blockIdx.z;
+  // Dispatch order.  One wave: a group's pieces next to each other.  Else every request's first
+  // prefix piece, then the second ones, ...: full pieces come before the shorter last ones of
+  // ragged requests, and the trees, the shortest, fill the end (row blocks of one piece, which
+  // read the same codes, next to each other).
+  int piece, bh, rb;
+  kvq_place(a, a.rows_pad / (a.wr * 128), piece, bh, rb);
   const int b = bh / a.Hkv, h = bh % a.Hkv;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const bool two = a.wr == 2;            // A: two row tiles
@@ -720,9 +725,9 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
         const int need = kvq_pieces(a, n_pref);
         __threadfence();
         bar_sync(1, 256);
-        if (threadIdx.x == 0) go = kvq_group_wait(a.cnt + 2 * (bh * gridDim.z + rb), need, a.err, ERR_GROUP) ? 1 : 0;
+        if (threadIdx.x == 0) go = kvq_group_wait(a.cnt + 2 * (bh * (a.rows_pad / (a.wr * 128)) + rb), need, a.err, ERR_GROUP) ? 1 : 0;
         bar_sync(1, 256);
-        if (threadIdx.x == 255) kvq_group_leave(a.cnt + 2 * (bh * gridDim.z + rb), need);  // (no one waits for this)
+        if (threadIdx.x == 255) kvq_group_leave(a.cnt + 2 * (bh * (a.rows_pad / (a.wr * 128)) + rb), need);  // (no one waits for this)
         if (go) {
           const int n = min(two ? 256 : 128, RG - row0);
           const int hi = (piece + 1) * n / need;
@@ -762,7 +767,7 @@ cudaError_t launch_tc(const KvqAttnPlan& p, const Maps& tm, const KvqAttnArgs& a
     if (dev < 64) __atomic_fetch_or(&configured, 1ull << dev, __ATOMIC_RELEASE);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.splits, p.B * p.Hkv, p.row_blocks);
+  cfg.gridDim = dim3(p.B * p.Hkv * p.row_blocks, p.splits);
   cfg.blockDim = dim3(NT);
   cfg.dynamicSmemBytes = SMEM;
   cfg.stream = s;
