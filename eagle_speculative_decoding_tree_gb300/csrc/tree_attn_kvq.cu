@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(CW * 32, 1)
       (void)wait_parity(&full[s], ((issued - 1 - s) / nst) & 1, a.err, ERR_FULL);
 
   // ---- the tree's own K/V (bf16, straight from global memory): 16-key steps shared out in
-  // the same way; P always as two bf16 terms
+  // the same way; P always as three bf16 terms
   if (tree && ok) {
     const uint16_t* kb = a.tk + static_cast<size_t>(bh) * a.R * D;
     const uint16_t* vb = a.tv + static_cast<size_t>(bh) * a.R * D;
@@ -426,12 +426,16 @@ __global__ void __launch_bounds__(CW * 32, 1)
           }
       }
       soften<D>(st, sc, lr);
-      uint32_t pa[4], pl[4];
+      uint32_t pt[3][4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float x0 = sc[k >> 1][2 * (k & 1)], x1 = sc[k >> 1][2 * (k & 1) + 1];
-        pa[k] = pack_bf(x0, x1);
-        pl[k] = pack_bf(x0 - __uint_as_float(pa[k] << 16), x1 - __uint_as_float(pa[k] & 0xffff0000u));
+        float x0 = sc[k >> 1][2 * (k & 1)], x1 = sc[k >> 1][2 * (k & 1) + 1];
+#pragma unroll
+        for (int u = 0; u < 3; ++u) {
+          pt[u][k] = pack_bf(x0, x1);
+          x0 -= __uint_as_float(pt[u][k] << 16);
+          x1 -= __uint_as_float(pt[u][k] & 0xffff0000u);
+        }
       }
 #pragma unroll
       for (int q = 0; q < VB / 4; ++q) {  // 4 head dims at a time
@@ -447,8 +451,8 @@ __global__ void __launch_bounds__(CW * 32, 1)
           const uint32_t sel = (y & 1) ? 0x7632 : 0x5410;
           const uint32_t b0 = __byte_perm(y < 2 ? w[0].x : w[0].y, y < 2 ? w[1].x : w[1].y, sel);
           const uint32_t b1 = __byte_perm(y < 2 ? w[2].x : w[2].y, y < 2 ? w[3].x : w[3].y, sel);
-          mma_bf16(st.o[4 * q + y], pa, b0, b1);
-          mma_bf16(st.o[4 * q + y], pl, b0, b1);
+#pragma unroll
+          for (int u = 0; u < 3; ++u) mma_bf16(st.o[4 * q + y], pt[u], b0, b1);
         }
       }
     }

@@ -26,7 +26,7 @@
 // take alternate tiles; their states merge in the epilogue.
 // TMEM: S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512); P overwrites S in place.
 //
-// Piece 0 is the tree itself (bf16 Q, K, V and P in two bf16 terms, one tile); the others are
+// Piece 0 is the tree itself (bf16 Q and K, V and P in halves, P always in two terms, one tile); the others are
 // tps 128-key tiles of the prefix.  Pieces write fp32 partials (TMA stores).  When the whole
 // grid fits on the SMs the launch is cooperative and the pieces of a group merge their rows in
 // the kernel (a second launch costs several microseconds); otherwise kvq_combine_kernel does.
@@ -108,11 +108,6 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ uint32_t bf2_bits(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 // Two halves to e4m3 codes (nearest even, saturating); the difference of two pairs.
 __device__ __forceinline__ uint32_t e4m3x2_of_half2(uint32_t h) {
   uint16_t r;
@@ -139,7 +134,7 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
 
 // 32 scores -> P in columns col .. (TERMS 1: 16 of them, TERMS 2: hi 16, lo 16), p = 2^(s c + o);
 // unless FULL, keys whose bit is clear get 0.  Returns the fp32 sum.
-template <int TERMS, bool BF, bool FULL>
+template <int TERMS, bool FULL>
 __device__ __forceinline__ float emit(const uint32_t (&r)[32], uint32_t col, float c, float o, uint32_t bits) {
   const uint64_t c2 = f32x2(__float_as_uint(c), __float_as_uint(c)), o2 = f32x2(__float_as_uint(o), __float_as_uint(o));
   uint64_t acc = 0ull;
@@ -157,15 +152,10 @@ __device__ __forceinline__ float emit(const uint32_t (&r)[32], uint32_t col, flo
         p1 = (bits >> (k + 1)) & 1u ? p1 : 0.f;
       }
       acc = add_f32x2(acc, f32x2(__float_as_uint(p0), __float_as_uint(p1)));
-      if (BF) {
-        hi[j] = bf2_bits(p0, p1);
-        if (TERMS == 2) lo[j] = bf2_bits(p0 - __uint_as_float(hi[j] << 16), p1 - __uint_as_float(hi[j] & 0xffff0000u));
-      } else {
-        hi[j] = half2_bits(p0, p1);
-        if (TERMS == 2) {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi[j]));
-          lo[j] = half2_bits(p0 - f.x, p1 - f.y);
-        }
+      hi[j] = half2_bits(p0, p1);
+      if (TERMS == 2) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi[j]));
+        lo[j] = half2_bits(p0 - f.x, p1 - f.y);
       }
     }
     tmem_st8(col + 8 * g, hi);
@@ -211,7 +201,7 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
   __shared__ uint64_t k_full[KST], k_empty[KST], v_full[VST], v_empty[VST], w_full[2], w_empty[2], s_full[2], p_full[2], q_full, o_full;
   __shared__ uint32_t tmem_base;
   __shared__ int go;             // group merge: every piece counted in time
-  __shared__ float s_q[2][128];  // the query rows' factors
+  __shared__ float s_q[2][128];  // the query rows' factors; tree: [0][0] the unit of V's halves
   // row maxima and sums of the two warpgroups, exchanged in the epilogue (the widened V's area,
   // free by then)
   float (*s_m)[128] = reinterpret_cast<float (*)[128]>(smem + SM_W);
@@ -343,20 +333,43 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
           }
         }
       } else if (work) {
-        // the tree's K and V tile as they are (bf16), zeros behind its rows
-        const uint16_t* kg = a.tk + static_cast<size_t>(bh) * a.R * 128;
-        const uint16_t* vg = a.tv + static_cast<size_t>(bh) * a.R * 128;
+        // The tree's K tile as it is (bf16); its V as halves, times the power of two that puts the
+        // tile's largest element in [2^14, 2^15): exact for elements down to 2^-32 of that one,
+        // in steps of 2^-39 of it below.  Zeros behind the tree's rows.
+        const uint4* kg = reinterpret_cast<const uint4*>(a.tk + static_cast<size_t>(bh) * a.R * 128);
+        const uint4* vg = reinterpret_cast<const uint4*>(a.tv + static_cast<size_t>(bh) * a.R * 128);
+        uint32_t am = 0;  // the largest finite magnitude, as float bits (ordered as integers)
+#pragma unroll 4
+        for (int i = id; i < r.Rb * 16; i += WT) {
+          const uint4 y = __ldg(vg + i);
+          const uint32_t u[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t p0 = (u[e] << 16) & 0x7fff0000u, p1 = u[e] & 0x7fff0000u;
+            am = max(am, max(p0 < 0x7f800000u ? p0 : 0u, p1 < 0x7f800000u ? p1 : 0u));
+          }
+        }
+        am = __reduce_max_sync(0xffffffffu, am);
+        if (lane == 0) s_q[1][warp - 8] = __uint_as_float(am);
+        bar_sync(4, WT);
+        for (int k = 0; k < WT / 32; ++k) am = max(am, __float_as_uint(s_q[1][k]));
+        const int x = max(static_cast<int>(am >> 23) - 127, -100);
+        const float mul = __uint_as_float(static_cast<uint32_t>(127 + 14 - x) << 23);
+        if (id == 0) s_q[0][0] = __uint_as_float(static_cast<uint32_t>(127 + x - 14) << 23);  // 1 / mul
+        auto halves = [&](uint32_t u) {
+          return half2_bits(__uint_as_float(u << 16) * mul, __uint_as_float(u & 0xffff0000u) * mul);
+        };
 #pragma unroll 2
         for (int i = id; i < KT * 16; i += WT) {
           const int row = i >> 4, c = i & 15;
-          uint4 x = make_uint4(0, 0, 0, 0), y = x;
+          uint4 k = make_uint4(0, 0, 0, 0), v = k;
           if (row < r.Rb) {
-            x = __ldg(reinterpret_cast<const uint4*>(kg + static_cast<size_t>(row) * 128) + c);
-            y = __ldg(reinterpret_cast<const uint4*>(vg + static_cast<size_t>(row) * 128) + c);
+            k = __ldg(kg + i);
+            v = __ldg(vg + i);
           }
           const int at = (c >> 3) * T8 + row * 128 + (((c & 7) ^ (row & 7)) << 4);
-          *reinterpret_cast<uint4*>(smem + SM_K + at) = x;
-          *reinterpret_cast<uint4*>(smem + SM_W + at) = y;
+          *reinterpret_cast<uint4*>(smem + SM_K + at) = k;
+          *reinterpret_cast<uint4*>(smem + SM_W + at) = make_uint4(halves(v.x), halves(v.y), halves(v.z), halves(v.w));
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -392,8 +405,8 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
 #pragma unroll 1
             for (int ks = 0; ks < 8; ++ks) {  // hi 16 columns, lo 16
               const uint32_t ac = tu + col_s(w) + (ks >> 1) * 32 + (ks & 1) * 8;
-              mma_f16_ts(tu + col_o(w), ac, dv + ks * 128, idesc(1, 1), ks > 0);
-              mma_f16_ts(tu + col_o(w), ac + 16, dv + ks * 128, idesc(1, 1), 1u);
+              mma_f16_ts(tu + col_o(w), ac, dv + ks * 128, idesc(0, 1), ks > 0);
+              mma_f16_ts(tu + col_o(w), ac + 16, dv + ks * 128, idesc(0, 1), 1u);
             }
           }
         } else {
@@ -552,7 +565,7 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
       if (!r.tree) fetch(min(tile_of(w), r.n - 1));
       for (int i = w; i < items; i += 2) {
         const int t = tile_of(i);
-        float ck[2] = {cr, cr}, lr[2] = {0.f, 0.f};
+        float ck[2] = {cr, cr}, lr[2] = {PB, PB};
         if (!r.tree) {
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
@@ -650,11 +663,11 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
           const uint32_t c0 = sc + (TERMS == 2 ? 64 : 32) * u, c1 = c0 + (TERMS == 2 ? 32 : 16);
           float sum;
           if (full)
-            sum = emit<TERMS, false, true>(x, c0, cu, off, 0u) + emit<TERMS, false, true>(y, c1, cu, off, 0u);
+            sum = emit<TERMS, true>(x, c0, cu, off, 0u) + emit<TERMS, true>(y, c1, cu, off, 0u);
           else if (r.tree)
-            sum = emit<2, true, false>(x, sc + 64 * u, cu, off, b0) + emit<2, true, false>(y, sc + 64 * u + 32, cu, off, b1);
+            sum = emit<2, false>(x, sc + 64 * u, cu, off, b0) + emit<2, false>(y, sc + 64 * u + 32, cu, off, b1);
           else
-            sum = emit<TERMS, false, false>(x, c0, cu, off, b0) + emit<TERMS, false, false>(y, c1, cu, off, b1);
+            sum = emit<TERMS, false>(x, c0, cu, off, b0) + emit<TERMS, false>(y, c1, cu, off, b1);
           l = fmaf(sum, ex2(-lu), l);
         }
         tmem_st_wait();
@@ -668,7 +681,8 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
       s_l[w][rl] = l;
       ok = bar_and(1, 256, ok);
       if (ok) {
-        const float unit = r.tree ? 1.f : vref * (1.f / (1 << PB));
+        if (r.tree) (void)wait_parity(&w_full[0], 0, a.err, ERR_W);  // (long complete: orders s_q[0][0])
+        const float unit = (r.tree ? s_q[0][0] : vref) * (1.f / (1 << PB));
         float M = m_ref, Lsum = l, fa = unit, fb = 0.f;
         const bool other = !two && items > 1;
         if (!two) {

@@ -280,8 +280,9 @@ int eagle_tree_attn_plan(const eagle_attn_desc* d, int32_t* splits, int32_t* ker
  *              bits (a half): an error of 2^-11 of sum p |v| at most, an eighth of a bf16
  *              output's own rounding.  EAGLE_ATTN_PRECISE: with 17 or more, an error of 2^-17.
  *              Either way p below 2^-30 of the row's largest may be rounded to nothing.  The
- *              tree's part takes two bf16 terms of P (2^-16) or fp32.  Scores, softmax and sums
- *              are fp32.
+ *              tree's part is precise in both: P with 22 bits or more; elements of tree_v below
+ *              2^-32 of their request's and head's largest may be rounded, to steps of 2^-39 of
+ *              that one.  Scores, softmax and sums are fp32.
  * ws: eagle_workspace_size(EAGLE_WS_TREE_ATTN_KVQ, d) bytes, zero-filled before its first
  * use; one workspace serves one stream at a time.  Its first 4 bytes are an error word as in
  * eagle_tree_attn.

@@ -10,7 +10,9 @@ Bounds (derived, u = 2^-24, per output element; A = sum p |v| of the row):
             stored as p 2^11 vs / vref (vref the largest vs) that is 2^-36 vref of a code's
             weight, the row's reference is at most twice its largest weight, so the sum is at
             least 1/2, and a code at most 448: n 2^-35 448 vref.  (A dimension in which the
-            heavy keys' values are tiny and the light ones' large sees nothing else.)
+            heavy keys' values are tiny and the light ones' large sees nothing else.)  Few rows
+            (R G <= 32, head_dim 128): 2^-17 (PRECISE), and steps of 2^-19 instead of 2^-24,
+            n 2^-30 448 vref in the worst case; these tests hold them to the smaller bound
   sums      n additions of fp32 in each of the row sum and the output: 2 * 2 u n, n the keys
   output    2^-8 |out| for bf16, 2^-24 for fp32
   lse       ds + 2 u n + 2^-21 + 2^-22 |lse|
@@ -105,14 +107,15 @@ class Case:
         assert int(ws[:4].view(torch.int32)) == 0
         return out, ls
 
-    def check(self, d):
+    def check(self, d, p_round=None):
         Bn, R, Hq, Hkv, D, P = self.dims
         out, lse = self.run(d)
         ref, rl, mass, reach = self.ref
         o, ls = out.double().cpu().numpy(), lse.double().cpu().numpy()
         n = (self.seq + self.nodes)[:, None, None]
         ds = 2 * (D + 10) * U * reach
-        p_round = 2.0 ** -16 + (2.0 ** -21 if d.precision == B.EAGLE_ATTN_PRECISE else 2.0 ** -11)
+        if p_round is None:
+            p_round = 2.0 ** -16 + (2.0 ** -21 if d.precision == B.EAGLE_ATTN_PRECISE else 2.0 ** -11)
         rel = (2 * ds + 2.0 ** -21 + p_round + 4 * U * n)[..., None]
         vmax = np.array([[max([float(x) for x in self.scale[1][b, h, : -(-int(self.seq[b]) // 64)]], default=0.0)
                           for h in range(Hkv)] for b in range(Bn)])
@@ -157,6 +160,24 @@ SHAPES = [
 def test_matches_64_bits(shape, precise, out_f32):
     c = Case(1, *shape)
     c.check(c.desc(out_f32, precise))
+
+
+@pytest.mark.parametrize("precise", [False, True])
+@pytest.mark.parametrize("shape", [(2, 8, 8, 2, 128, 64, [0, 0]), (2, 61, 8, 2, 128, 64, [0, 0]),
+                                   (1, 128, 4, 1, 128, 64, [0]), (2, 61, 8, 2, 64, 64, [0, 0])],
+                         ids=lambda s: "-".join(map(str, s[:6])))
+def test_tree_alone_is_precise(shape, precise):
+    """No prefix: P with 22 bits or more whatever the precision asked for, and tree values (here
+    over 2^-24 to 2^6, the smallest given up) as they are."""
+    c = Case(7, *shape)
+    g = np.random.default_rng(8)
+    tv = c.tv.float() * torch.from_numpy(2.0 ** g.integers(-10, 5, c.tv.shape)).float()
+    c.tv = torch.where(tv.abs() < 2.0 ** -24, 0.0, tv.clamp(-64, 64)).bfloat16()
+    f = lambda t: t.double().numpy()
+    none = np.zeros((*c.dims[:1], c.dims[3], c.dims[5], c.dims[4]))
+    c.ref = H.attention(f(c.q), none, none, f(c.tk), f(c.tv), c.seq, c.nodes, c.see, 1 / math.sqrt(c.dims[4]))
+    c.dev[6] = c.tv.cuda()
+    c.check(c.desc(True, precise), p_round=2.0 ** -21)
 
 
 @pytest.mark.parametrize("splits", [1, 2, 3, 7, 64])
