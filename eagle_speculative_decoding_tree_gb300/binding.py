@@ -424,13 +424,19 @@ def _on_current(t: torch.Tensor, name: str) -> None:
         raise ValueError(f"{name} is on cuda:{t.get_device()}, which is not the current device")
 
 
+def _element(dtype: int):
+    """The torch type of a descriptor's element type (both, where the library refuses it)."""
+    return torch.bfloat16 if dtype == EAGLE_BF16 else torch.float32 if dtype == EAGLE_F32 else FLOATS
+
+
 def eagle_kvq_write(desc: KvqDesc, k, v, start, count: Optional[torch.Tensor], k_codes, k_scale, v_codes, v_scale,
                     status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Quantise K/V rows into the 8-bit cache (see eagle.h: eagle_kvq_write).  Codes are
     uint8 or float8_e4m3fn tensors [B][Hkv][P][D], scales fp32 [B][Hkv][ceil(P / 64)]."""
     _on_current(k, "k")
+    dt = _element(desc.dtype)
     _check("eagle_kvq_write", load().eagle_kvq_write(
-        ctypes.byref(desc), _ptr(k, FLOATS, "k"), _ptr(v, FLOATS, "v"), _ptr(start, torch.int32, "start"),
+        ctypes.byref(desc), _ptr(k, dt, "k"), _ptr(v, dt, "v"), _ptr(start, torch.int32, "start"),
         _ptr(count, torch.int32, "count"), _ptr(k_codes, CODES, "k_codes"), _ptr(k_scale, torch.float32, "k_scale"),
         _ptr(v_codes, CODES, "v_codes"), _ptr(v_scale, torch.float32, "v_scale"), _ptr(status, torch.int32, "status"),
         _stream(stream)))
@@ -440,10 +446,11 @@ def eagle_kvq_read(desc: KvqDesc, k_codes, k_scale, v_codes, v_scale, start, cou
                    status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Read rows of the 8-bit cache back (see eagle.h: eagle_kvq_read)."""
     _on_current(k_codes, "k_codes")
+    dt = _element(desc.dtype)
     _check("eagle_kvq_read", load().eagle_kvq_read(
         ctypes.byref(desc), _ptr(k_codes, CODES, "k_codes"), _ptr(k_scale, torch.float32, "k_scale"),
         _ptr(v_codes, CODES, "v_codes"), _ptr(v_scale, torch.float32, "v_scale"), _ptr(start, torch.int32, "start"),
-        _ptr(count, torch.int32, "count"), _ptr(k, FLOATS, "k"), _ptr(v, FLOATS, "v"),
+        _ptr(count, torch.int32, "count"), _ptr(k, dt, "k"), _ptr(v, dt, "v"),
         _ptr(status, torch.int32, "status"), _stream(stream)))
 
 
@@ -460,6 +467,9 @@ class KvqLayerPointers:
         self.v, self.vs = mk(v_codes, CODES, "v_codes"), mk(v_scale, f32, "v_scale")
         self.tk, self.tv = mk(tree_k, FLOATS, "tree_k"), mk(tree_v, FLOATS, "tree_v")
         self.tensors = [list(t) for t in (k_codes, k_scale, v_codes, v_scale, tree_k, tree_v)]
+        self.layers, self.dtypes = n, {t.dtype for t in (*tree_k, *tree_v)}
+        if any(len(t) != n for t in self.tensors):
+            raise ValueError("as many tensors of each kind as layers")
         self.addresses = tuple(ctypes.addressof(x) for x in (self.k, self.ks, self.v, self.vs, self.tk, self.tv))
 
 
@@ -467,6 +477,10 @@ def eagle_kvq_commit(desc: CommitDesc, layers: KvqLayerPointers, n_acc, path, se
                      feat_cache=None, tree_feat=None, status=None, stream=None) -> None:
     """Commit the accepted path into 8-bit caches (see eagle.h: eagle_kvq_commit)."""
     _on_current(n_acc, "n_acc")
+    if desc.layers > layers.layers:
+        raise ValueError(f"{desc.layers} layers, pointers of {layers.layers}")
+    if layers.dtypes != {_element(desc.dtype)} and _element(desc.dtype) is not FLOATS:
+        raise ValueError("tree_k and tree_v are not of the descriptor's element type")
     _check("eagle_kvq_commit", load().eagle_kvq_commit(
         ctypes.byref(desc), *layers.addresses,
         _ptr(n_acc, torch.int32, "n_acc"), _ptr(path, torch.int32, "path"), _ptr(seq_len, torch.int32, "seq_len"),
@@ -485,8 +499,8 @@ def eagle_tree_attn_kvq(desc: AttnDesc, q, k_codes, k_scale, v_codes, v_scale, t
         _ptr(k_scale, torch.float32, "k_scale"), _ptr(v_codes, CODES, "v_codes"),
         _ptr(v_scale, torch.float32, "v_scale"), _ptr(tree_k, bf16, "tree_k"), _ptr(tree_v, bf16, "tree_v"),
         _ptr(seq_len, torch.int32, "seq_len"), _ptr(n_nodes, torch.int32, "n_nodes"),
-        _ptr(anc_mask, torch.int64, "anc_mask"), _ptr(out, FLOATS, "out"), _ptr(lse, torch.float32, "lse"),
-        _ptr(ws, name="ws"), ws.numel() * ws.element_size(), _stream(stream)))
+        _ptr(anc_mask, torch.int64, "anc_mask"), _ptr(out, _element(desc.out_dtype), "out"),
+        _ptr(lse, torch.float32, "lse"), _ptr(ws, name="ws"), ws.numel() * ws.element_size(), _stream(stream)))
 
 
 # ----------------------------------------------------------------------------- norms and rotation
@@ -496,8 +510,9 @@ def eagle_qk_norm_rope(desc: QkNormRopeDesc, qkv, q_weight: Optional[torch.Tenso
     """Norms of the query and key heads, rotation and tree layout (see eagle.h:
     eagle_qk_norm_rope)."""
     _on_current(qkv, "qkv")
+    dt = _element(desc.dtype)
     _check("eagle_qk_norm_rope", load().eagle_qk_norm_rope(
-        ctypes.byref(desc), _ptr(qkv, FLOATS, "qkv"), _ptr(q_weight, FLOATS, "q_weight"),
-        _ptr(k_weight, FLOATS, "k_weight"), _ptr(inv_freq, torch.float32, "inv_freq"),
-        _ptr(pos_id, torch.int32, "pos_id"), _ptr(n_nodes, torch.int32, "n_nodes"), _ptr(q, FLOATS, "q"),
-        _ptr(k, FLOATS, "k"), _ptr(v, FLOATS, "v"), _stream(stream)))
+        ctypes.byref(desc), _ptr(qkv, dt, "qkv"), _ptr(q_weight, dt, "q_weight"), _ptr(k_weight, dt, "k_weight"),
+        _ptr(inv_freq, torch.float32, "inv_freq"), _ptr(pos_id, torch.int32, "pos_id"),
+        _ptr(n_nodes, torch.int32, "n_nodes"), _ptr(q, dt, "q"), _ptr(k, dt, "k"), _ptr(v, dt, "v"),
+        _stream(stream)))

@@ -424,7 +424,7 @@ int eagle_kvq_commit(const eagle_commit_desc* d, void* const* k_codes_layers, fl
     return EAGLE_ERR_INVALID_ARG;
   if (d->layers > kMaxLayers || d->rows > kMaxRows || d->max_depth >= kMaxRows || !dtype_ok(d->dtype) ||
       (d->feat_dim > 0 && !dtype_ok(d->feat_dtype)) || (d->head_dim != 64 && d->head_dim != 128) ||
-      d->batch > 65535 || d->n_kv_heads > 65535)
+      static_cast<long long>(d->batch) * d->n_kv_heads > 65535)
     return EAGLE_ERR_UNSUPPORTED;
   if (!k_codes_layers || !k_scale_layers || !v_codes_layers || !v_scale_layers || !tree_k_layers || !tree_v_layers ||
       !n_acc || !path || !seq_len)

@@ -681,7 +681,9 @@ void plan_kvq_attn(const eagle_attn_desc* d, int num_sms, KvqAttnPlan* p) {
   p->off_err = 0;
   size_t off = 256;
   p->off_cnt = off;
-  if (p->coop) off += (static_cast<size_t>(p->B) * p->Hkv * p->row_blocks * 8 + 255) / 256 * 256;
+  // the meeting groups' counters, at most one group an SM: the same place whatever the descriptor,
+  // so that the partials of one never lie where another expects its counters at zero
+  off += (static_cast<size_t>(num_sms) * 8 + 255) / 256 * 256;
   p->off_o = p->off_ml = 0;
   if (p->splits > 1) {
     const size_t rows = static_cast<size_t>(p->B) * p->Hkv * p->splits * p->rows_pad;

@@ -284,8 +284,8 @@ int eagle_tree_attn_plan(const eagle_attn_desc* d, int32_t* splits, int32_t* ker
  *              2^-32 of their request's and head's largest may be rounded, to steps of 2^-39 of
  *              that one.  Scores, softmax and sums are fp32.
  * ws: eagle_workspace_size(EAGLE_WS_TREE_ATTN_KVQ, d) bytes, zero-filled before its first
- * use; one workspace serves one stream at a time.  Its first 4 bytes are an error word as in
- * eagle_tree_attn.
+ * use; one workspace serves one stream at a time, and any descriptors in turn that it is large
+ * enough for.  Its first 4 bytes are an error word as in eagle_tree_attn.
  * Unsupported: dtype not EAGLE_BF16, head_dim not 64 / 128, R > 128, Hq % Hkv != 0,
  * B * Hkv > 65535, B * Hkv * P >= 2^31, fault_test. */
 int eagle_tree_attn_kvq(const eagle_attn_desc* d, const void* q, const void* k_codes, const float* k_scale,
@@ -537,7 +537,7 @@ int eagle_kvq_read(const eagle_kvq_desc* d, const void* k_codes, const float* k_
  * seq_len[b] as eagle_kvq_write does (the scale of a begun block only grows), everything
  * else as eagle_kv_commit.  k_codes_layers, k_scale_layers, v_codes_layers, v_scale_layers,
  * tree_k_layers, tree_v_layers: HOST arrays of `layers` DEVICE pointers; d->dtype is the
- * tree K/V's element type and d->head_dim 64 or 128, batch and n_kv_heads <= 65535. */
+ * tree K/V's element type and d->head_dim 64 or 128, B * Hkv <= 65535. */
 int eagle_kvq_commit(const eagle_commit_desc* d, void* const* k_codes_layers, float* const* k_scale_layers,
                      void* const* v_codes_layers, float* const* v_scale_layers, const void* const* tree_k_layers,
                      const void* const* tree_v_layers, const int32_t* n_acc, const int32_t* path, int32_t* seq_len,

@@ -152,6 +152,9 @@ SHAPES = [
     (2, 32, 3, 3, 128, 450, [450, 3]),         # 32 rows, as many tree keys
     (1, 1, 32, 1, 128, 3333, [3333]),          # 32 rows of one token
     (1, 2, 34, 2, 128, 200, [200]),            # 34 rows of two
+    (1, 1, 4, 1, 128, 1, [1]),                 # a cache of one row, smaller than any tile
+    (1, 61, 4, 1, 128, 70, [70]),
+    (1, 61, 4, 1, 64, 3, [3]),
 ]
 
 
@@ -345,3 +348,41 @@ def test_offsets_past_32_bits():
     none = H.attention(small.q.double().numpy(), np.zeros((1, Hkv, 1, D)), np.zeros((1, Hkv, 1, D)),
                        small.tk.double().numpy(), small.tv.double().numpy(), [0], [R], small.see, 1 / math.sqrt(D))[0]
     assert np.abs(out[0].double().cpu().numpy() - none[0]).max() <= 1e-4
+
+
+def test_one_workspace_for_descriptors_in_turn():
+    """Plans that merge in the kernel (counters) and plans that do not (partials where a plan's
+    counters could be), over and over in the same workspace."""
+    cases = [Case(31, 1, 61, 32, 8, 128, 900, [896]), Case(32, 6, 61, 16, 8, 128, 2000, [2000] * 6),
+             Case(33, 1, 4, 8, 2, 128, 5000, [4999]), Case(34, 40, 2, 8, 8, 128, 600, [600] * 40),
+             Case(35, 2, 9, 8, 2, 64, 700, [700, 64])]
+    descs = [c.desc(False, False) for c in cases]
+    want = [c.run(d)[0] for c, d in zip(cases, descs)]
+    ws = torch.zeros(max(B.workspace_size(B.EAGLE_WS_TREE_ATTN_KVQ, d) for d in descs), dtype=torch.uint8, device="cuda")
+    for i in [0, 1, 2, 3, 4, 0, 2, 1, 4, 0, 3, 2, 0]:
+        assert torch.equal(cases[i].run(descs[i], ws=ws)[0], want[i])
+
+
+def test_element_types_must_be_the_descriptor_s():
+    c = Case(36, 1, 2, 2, 2, 64, 64, [10])
+    d = c.desc(True)
+    q, kc, ks, vc, vs, tk, tv, seq, mask = c.dev
+    ws = torch.zeros(B.workspace_size(B.EAGLE_WS_TREE_ATTN_KVQ, d), dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError, match="out"):
+        B.eagle_tree_attn_kvq(d, q, kc, ks, vc, vs, tk, tv, seq, mask, torch.empty_like(q), None, ws)
+    w = B.KvqDesc(1, 2, 64, 64, 2, B.EAGLE_F32)
+    with pytest.raises(ValueError, match="k has dtype"):
+        B.eagle_kvq_write(w, tk, tv, seq, None, kc, ks, vc, vs)
+    with pytest.raises(ValueError, match="k has dtype"):
+        B.eagle_kvq_read(w, kc, ks, vc, vs, seq, None, tk, tv)
+    with pytest.raises(ValueError, match="as many"):
+        B.KvqLayerPointers([kc], [ks], [vc], [vs], [tk], [])
+    lay = B.KvqLayerPointers([kc], [ks], [vc], [vs], [tk], [tv])
+    one = i32([0])
+    for layers, dt, msg in ((2, B.EAGLE_BF16, "2 layers"), (1, B.EAGLE_F32, "element type")):
+        with pytest.raises(ValueError, match=msg):
+            B.eagle_kvq_commit(B.CommitDesc(layers, 1, 2, 64, 2, 64, 0, dt, 0, dt), lay, one, one, seq, one)
+    r = B.QkNormRopeDesc(1, 2, 2, 2, 64, 64, 0, 0, 1e-6, B.EAGLE_F32)
+    with pytest.raises(ValueError, match="qkv has dtype"):
+        B.eagle_qk_norm_rope(r, torch.zeros(2, 6 * 64, dtype=torch.bfloat16, device="cuda"), None, None,
+                             torch.zeros(32, device="cuda"), i32([0, 0]), q, tk, tv)

@@ -130,6 +130,7 @@ def test_write_and_read_refuse_pointers(lib):
     (dict(head_dim=96), B.EAGLE_ERR_UNSUPPORTED), (dict(layers=129), B.EAGLE_ERR_UNSUPPORTED),
     (dict(rows=200), B.EAGLE_ERR_UNSUPPORTED), (dict(max_depth=128), B.EAGLE_ERR_UNSUPPORTED),
     (dict(layers=0), B.EAGLE_ERR_INVALID_ARG), (dict(feat_dim=8), B.EAGLE_ERR_INVALID_ARG),
+    (dict(batch=9000), B.EAGLE_ERR_UNSUPPORTED),
 ])
 def test_commit_refuses_descriptors(lib, kw, code):
     d = dict(layers=2, batch=1, n_kv_heads=8, head_dim=128, rows=61, max_seq=512, max_depth=7, dtype=1, feat_dim=0,
@@ -186,3 +187,13 @@ def test_binding_refuses_host_tensors(lib):
     with pytest.raises(ValueError, match="CUDA"):
         B.eagle_kvq_write(d, k, k, torch.zeros(1, dtype=torch.int32), None, torch.zeros(64, 64, dtype=torch.uint8),
                           torch.zeros(1), torch.zeros(64, 64, dtype=torch.uint8), torch.zeros(1))
+
+
+def test_workspace_counters_have_one_place():
+    """Descriptors that share a workspace: the first partial comes behind every counter."""
+    sizes = [B.workspace_size(B.EAGLE_WS_TREE_ATTN_KVQ, _attn(batch=b, rows=r, max_seq=p, num_splits=1))
+             for b, r, p in ((1, 61, 512), (2, 61, 512), (1, 61, 64))]
+    part = 2 * 8 * 256 * (128 * 4 + 8)  # the tree and one piece, eight heads of 256 rows
+    head = sizes[0] - part
+    assert sizes[1] - head == 2 * part and sizes[2] == sizes[0] and head % 256 == 0
+    assert head >= 256 + 8 * 148
