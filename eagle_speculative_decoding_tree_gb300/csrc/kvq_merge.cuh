@@ -74,6 +74,24 @@ __device__ __forceinline__ void kvq_group_leave(int* cnt, int need) {
   }
 }
 
+// A row's D / 32 dims of this lane, normalised; lane 0 its lse.
+template <int D>
+__device__ __forceinline__ void kvq_store_row(const KvqAttnArgs& a, size_t orow, int lane, const float (&acc)[D / 32],
+                                              float M, float lsum) {
+  const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+  const size_t at = orow * D + lane * (D / 32);
+#pragma unroll
+  for (int e = 0; e < D / 32; e += 2) {
+    if (a.out_f32) {
+      *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at + e) = make_float2(acc[e] * inv, acc[e + 1] * inv);
+    } else {
+      const __nv_bfloat162 t = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
+      *reinterpret_cast<__nv_bfloat162*>(static_cast<uint16_t*>(a.out) + at + e) = t;
+    }
+  }
+  if (a.lse && lane == 0) a.lse[orow] = (M + log2f(lsum)) * 0.69314718055994531f;
+}
+
 // One warp: M = max m_s, out = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s over partials s < n at
 // rows base + s rows_pad; D / 32 dims per lane, lane s holds piece s's weight.  BATCH partial rows
 // are in flight together (up to 32 pieces a round).  A row with no key gets zeros and lse -inf.
@@ -110,18 +128,47 @@ __device__ __forceinline__ void kvq_merge_row(const KvqAttnArgs& a, size_t base,
       for (int e = 0; e < PER; ++e) acc[e] = fmaf(g, x[u][e], acc[e]);
     }
   }
-  const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
-  const size_t at = orow * D + lane * PER;
+  kvq_store_row<D>(a, orow, lane, acc, M, lsum);
+}
+
+// The same for ROWS rows (the first m of them) of at most 16 / ROWS pieces: all their partials are
+// in flight together, lane s of the first 16 holds piece s % NP of row s / NP.
+template <int D, int ROWS, typename Orow>
+__device__ __forceinline__ void kvq_merge_rows(const KvqAttnArgs& a, size_t base, int n, int m, int lane, Orow orow) {
+  constexpr int PER = D / 32, NP = 16 / ROWS;
+  const float* po = a.part_o + base * D + lane * PER;
+  const size_t step = static_cast<size_t>(a.rows_pad);
+  const int row = lane / NP, piece = lane % NP;
+  const bool has = lane < 16 && row < m && piece < n;
+  float ml[2], x[ROWS][NP][PER];
+  ld_part(a.part_ml + (base + row + static_cast<size_t>(piece) * step) * 2, ml, has);
 #pragma unroll
-  for (int e = 0; e < PER; e += 2) {
-    if (a.out_f32) {
-      *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at + e) = make_float2(acc[e] * inv, acc[e + 1] * inv);
-    } else {
-      const __nv_bfloat162 t = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
-      *reinterpret_cast<__nv_bfloat162*>(static_cast<uint16_t*>(a.out) + at + e) = t;
+  for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+    for (int s = 0; s < NP; ++s)
+      ld_part(po + (static_cast<size_t>(s) * step + r) * D, x[r][s], r < m && s < n);
+  if (!has) ml[0] = -INFINITY;
+  float M = ml[0];
+#pragma unroll
+  for (int o = NP / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float f = ml[0] == -INFINITY ? 0.f : sm100::ex2(ml[0] - M);
+  float lsum = f * ml[1];
+#pragma unroll
+  for (int o = NP / 2; o > 0; o >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, o);
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    float acc[PER];
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int s = 0; s < NP; ++s) {
+      const float g = __shfl_sync(0xffffffffu, f, r * NP + s);
+#pragma unroll
+      for (int e = 0; e < PER; ++e) acc[e] = fmaf(g, x[r][s][e], acc[e]);
     }
+    const float Mr = __shfl_sync(0xffffffffu, M, r * NP), lr = __shfl_sync(0xffffffffu, lsum, r * NP);
+    if (r < m) kvq_store_row<D>(a, orow(r), lane, acc, Mr, lr);
   }
-  if (a.lse && lane == 0) a.lse[orow] = (M + log2f(lsum)) * 0.69314718055994531f;
 }
 
 }  // namespace eagle

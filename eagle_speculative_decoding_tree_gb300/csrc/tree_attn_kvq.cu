@@ -542,19 +542,31 @@ __global__ void __launch_bounds__(128) kvq_combine_kernel(const KvqAttnArgs a) {
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = blockIdx.x * 4 + warp, bh = blockIdx.y;
+  const int r0 = (blockIdx.x * 4 + warp) * 4, bh = blockIdx.y;
   const int b = bh / a.Hkv, h = bh % a.Hkv;
-  if (r >= tree_rows(a, b) * a.G) return;
-  const int tiles = (prefix_len(a, b) + KT - 1) / KT;
-  const int n = kvq_pieces(a, tiles);
-  kvq_merge_row<D, 16>(a, static_cast<size_t>(bh) * a.splits * a.rows_pad + r, n,
-                       (static_cast<size_t>(b) * a.R + r / a.G) * a.Hq + h * a.G + r % a.G, lane);
+  const int m = min(tree_rows(a, b) * a.G - r0, 4);
+  const int n = kvq_pieces(a, (prefix_len(a, b) + KT - 1) / KT);
+  if (m <= 0) return;
+  const size_t base = static_cast<size_t>(bh) * a.splits * a.rows_pad + r0;
+  auto orow = [&](int k) {
+    return (static_cast<size_t>(b) * a.R + (r0 + k) / a.G) * a.Hq + h * a.G + (r0 + k) % a.G;
+  };
+  if (n <= 4) {
+    kvq_merge_rows<D, 4>(a, base, n, m, lane, orow);
+  } else if (n <= 8) {
+#pragma unroll 1
+    for (int k = 0; k < m; k += 2)
+      kvq_merge_rows<D, 2>(a, base + k, n, min(m - k, 2), lane, [&](int u) { return orow(k + u); });
+  } else {
+#pragma unroll 1
+    for (int k = 0; k < m; ++k) kvq_merge_row<D, 16>(a, base + k, n, orow(k), lane);
+  }
 }
 
 template <int D>
 cudaError_t launch_combine(const KvqAttnPlan& p, const KvqAttnArgs& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((p.R * p.G + 3) / 4, p.B * p.Hkv);
+  cfg.gridDim = dim3((p.R * p.G + 15) / 16, p.B * p.Hkv);
   cfg.blockDim = dim3(128);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];

@@ -338,38 +338,55 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
         // in steps of 2^-39 of it below.  Zeros behind the tree's rows.
         const uint4* kg = reinterpret_cast<const uint4*>(a.tk + static_cast<size_t>(bh) * a.R * 128);
         const uint4* vg = reinterpret_cast<const uint4*>(a.tv + static_cast<size_t>(bh) * a.R * 128);
-        uint32_t am = 0;  // the largest finite magnitude, as float bits (ordered as integers)
-#pragma unroll 4
-        for (int i = id; i < r.Rb * 16; i += WT) {
-          const uint4 y = __ldg(vg + i);
-          const uint32_t u[4] = {y.x, y.y, y.z, y.w};
+        constexpr int U = 6;  // 16-byte pieces of a thread in flight (two rounds above 72 rows)
+        auto at = [&](int i) {
+          const int row = i >> 4, c = i & 15;
+          return (c >> 3) * T8 + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+        };
+        auto load = [&](uint4 (&x)[U], const uint4* g, int i0) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t p0 = (u[e] << 16) & 0x7fff0000u, p1 = u[e] & 0x7fff0000u;
-            am = max(am, max(p0 < 0x7f800000u ? p0 : 0u, p1 < 0x7f800000u ? p1 : 0u));
+          for (int e = 0; e < U; ++e) {
+            x[e] = make_uint4(0, 0, 0, 0);
+            if (i0 + e * WT < r.Rb * 16) x[e] = __ldg(g + i0 + e * WT);
+          }
+        };
+        uint32_t am = 0;  // the largest finite magnitude of V, as float bits (ordered as integers)
+        uint4 x[U];
+#pragma unroll 1
+        for (int i0 = id; i0 < KT * 16; i0 += U * WT) {
+          uint4 k[U];
+          load(x, vg, i0);
+          load(k, kg, i0);
+#pragma unroll
+          for (int e = 0; e < U; ++e) {
+            const uint32_t u[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+              const uint32_t p0 = (u[f] << 16) & 0x7fff0000u, p1 = u[f] & 0x7fff0000u;
+              am = max(am, max(p0 < 0x7f800000u ? p0 : 0u, p1 < 0x7f800000u ? p1 : 0u));
+            }
+            if (i0 + e * WT < KT * 16) *reinterpret_cast<uint4*>(smem + SM_K + at(i0 + e * WT)) = k[e];
           }
         }
         am = __reduce_max_sync(0xffffffffu, am);
         if (lane == 0) s_q[1][warp - 8] = __uint_as_float(am);
         bar_sync(4, WT);
         for (int k = 0; k < WT / 32; ++k) am = max(am, __float_as_uint(s_q[1][k]));
-        const int x = max(static_cast<int>(am >> 23) - 127, -100);
-        const float mul = __uint_as_float(static_cast<uint32_t>(127 + 14 - x) << 23);
-        if (id == 0) s_q[0][0] = __uint_as_float(static_cast<uint32_t>(127 + x - 14) << 23);  // 1 / mul
+        const int ex = max(static_cast<int>(am >> 23) - 127, -100);
+        const float mul = __uint_as_float(static_cast<uint32_t>(127 + 14 - ex) << 23);
+        if (id == 0) s_q[0][0] = __uint_as_float(static_cast<uint32_t>(127 + ex - 14) << 23);  // 1 / mul
         auto halves = [&](uint32_t u) {
           return half2_bits(__uint_as_float(u << 16) * mul, __uint_as_float(u & 0xffff0000u) * mul);
         };
-#pragma unroll 2
-        for (int i = id; i < KT * 16; i += WT) {
-          const int row = i >> 4, c = i & 15;
-          uint4 k = make_uint4(0, 0, 0, 0), v = k;
-          if (row < r.Rb) {
-            k = __ldg(kg + i);
-            v = __ldg(vg + i);
-          }
-          const int at = (c >> 3) * T8 + row * 128 + (((c & 7) ^ (row & 7)) << 4);
-          *reinterpret_cast<uint4*>(smem + SM_K + at) = k;
-          *reinterpret_cast<uint4*>(smem + SM_W + at) = make_uint4(halves(v.x), halves(v.y), halves(v.z), halves(v.w));
+#pragma unroll 1
+        for (int n = (KT * 16 - 1) / (U * WT); n >= 0; --n) {  // (the last round's is still in registers)
+          const int i0 = id + n * U * WT;
+          if (n < (KT * 16 - 1) / (U * WT)) load(x, vg, i0);
+#pragma unroll
+          for (int e = 0; e < U; ++e)
+            if (i0 + e * WT < KT * 16)
+              *reinterpret_cast<uint4*>(smem + SM_W + at(i0 + e * WT)) =
+                  make_uint4(halves(x[e].x), halves(x[e].y), halves(x[e].z), halves(x[e].w));
         }
         fence_proxy_async_smem();
         __syncwarp();
