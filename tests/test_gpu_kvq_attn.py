@@ -386,3 +386,27 @@ def test_element_types_must_be_the_descriptor_s():
     with pytest.raises(ValueError, match="qkv has dtype"):
         B.eagle_qk_norm_rope(r, torch.zeros(2, 6 * 64, dtype=torch.bfloat16, device="cuda"), None, None,
                              torch.zeros(32, device="cuda"), i32([0, 0]), q, tk, tv)
+
+
+@pytest.mark.parametrize("precise", [False, True])
+@pytest.mark.parametrize("shape,nodes", [
+    ((21, 61, 32, 8, 128, 1100, [0, 1, 127, 128, 129, 1100, 640, 3, 1000, 900, 0, 0, 77, 256, 1099, 512, 333, 64, 65, 800, 1]), None),
+    ((20, 61, 32, 8, 128, 700, [700] * 20), [61, 1, 33, 32, 0, 16, 60, 5, 61, 61, 31, 40, 2, 61, 0, 0, 61, 33, 12, 50]),
+    ((9, 100, 34, 17, 128, 400, [0, 0, 0, 400, 0, 0, 399, 0, 1]), [100, 0, 64, 65, 1, 0, 100, 3, 128 - 28]),
+    ((3, 128, 64, 4, 128, 600, [600, 20, 0]), None),              # 2048 rows a group, eight row blocks
+    ((160, 33, 8, 8, 128, 64, [i % 65 for i in range(160)]), None),  # one row tile a group, many short groups
+    ((40, 40, 8, 2, 128, 2000, [2000] + [5] * 39), None),         # a long request among short ones
+], ids=["lengths", "nodes", "empty", "blocks", "short", "one-long"])
+def test_batches_of_many_groups(shape, nodes, precise):
+    """More groups than fit on the SMs at once: pieces of every length, a combine launch."""
+    c = Case(41, *shape, nodes=nodes)
+    c.check(c.desc(precise, precise))
+
+
+def test_batches_of_many_groups_repeat_exactly():
+    c = Case(42, 24, 61, 16, 8, 128, 1500, list(range(100, 100 + 24 * 58, 58)), nodes=[61, 20, 33, 48] * 6)
+    d = c.desc(False, False)
+    ws = torch.zeros(B.workspace_size(B.EAGLE_WS_TREE_ATTN_KVQ, d), dtype=torch.uint8, device="cuda")
+    first = c.run(d, ws=ws)[0]
+    for _ in range(20):
+        assert torch.equal(c.run(d, ws=ws)[0], first)
