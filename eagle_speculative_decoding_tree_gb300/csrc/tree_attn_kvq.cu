@@ -17,13 +17,17 @@
 // The reference maximum is kept in log2 units and rounded up to an integer, so that with
 // power-of-two scales every exponent offset is exact.
 //
+// head_dim 128 runs on the tcgen05 kernels (tree_attn_kvq_tc.cu, up to 32 rows a KV head
+// tree_attn_kvq_few.cu); the kernel here serves head_dim 64, EAGLE_ENGINE_MMA_SYNC and groups of
+// more than 4096 query heads.
+//
 // Kernel (the split-KV shape of tree_attn.cu).  One CTA per (row block, split, request x KV
 // head), sixteen warps of 16 query rows each: 128-key tiles of codes stream through a TMA ring
 // (128-byte swizzle, 64-byte for head_dim 64; one thread refills a stage once its warps are past
 // it), and a warp takes 16-key steps of them: the codes go from shared memory to registers once
 // and become mma.sync m16n8k16 half fragments there, which is cheaper than writing a half tile
-// back when there are few rows.  That is the bytes-bound case (R G <= 32 rows of a decode or
-// chain step); a step is a chain of some 2000 cycles, so it takes sixteen warps' steps to keep
+// back when there are few rows.  That is the bytes-bound case (few rows: a decode or chain
+// step); a step is a chain of some 2000 cycles, so it takes sixteen warps' steps to keep
 // up with HBM.  The fragments' orders are free choices: a thread's 16 bytes of a key are 16 head
 // dims of the contraction, Q is stored to match; keys within a step are permuted by exchanging
 // bits 0 and 2 so that the swizzled reads fall in different banks.
@@ -621,7 +625,8 @@ cudaError_t launch_mma(const KvqAttnPlan& p, const Maps& tm, const KvqAttnArgs& 
 // mean work, and a tail of most of a piece).  Measured: 8 requests of 1K to 16K x 8 heads 94 to
 // 112 us with 3 to 8 pieces, 128 with 2, 228 in one wave; 32 such 275 us with 3 or 4, 299 with 6;
 // 4 requests of 32K 131 us with 9, 147 with 11, 163 in one wave; one of 8K 21 us in one wave.
-static long long choose_pieces(long long base, int tiles, int num_sms, int extra, bool* even) {
+// The plan's cost, in tiles' time, in *cost.
+static long long choose_pieces(long long base, int tiles, int num_sms, int extra, bool* even, double* cost) {
   const long long one = std::min<long long>(num_sms / base - 1, tiles);
   *even = one >= 1;
   long long best = std::max<long long>(one, 1);
@@ -638,6 +643,7 @@ static long long choose_pieces(long long base, int tiles, int num_sms, int extra
       *even = false;
     }
   }
+  *cost = least;
   return best;
 }
 
@@ -662,12 +668,31 @@ void plan_kvq_attn(const eagle_attn_desc* d, int num_sms, KvqAttnPlan* p) {
   p->tc = tcgen && !p->few;
   p->coop = p->even = false;
   if (p->tc || p->few) {
+    const long long groups = static_cast<long long>(p->B) * p->Hkv, pairs = (RG + 255) / 256, blocks = (RG + 127) / 128;
+    long long pieces = d->num_splits;
+    double cost = 0.;
     p->wr = RG > 128 ? 2 : 1;
+    if (pieces <= 0) pieces = choose_pieces(p->few ? groups : groups * (p->wr == 2 ? pairs : blocks), tiles, num_sms,
+                                            p->few ? 10 : 6, &p->even, &cost);
+    if (d->num_splits <= 0 && p->tc && p->wr == 2) {
+      // Or a CTA for every 128 rows, with half as many pieces.  The codes are then read (from L2) and
+      // widened twice, a row tile's 128 keys taking 1800 cycles instead of 1350, but a CTA has half
+      // the query tile to stage and all of them together half the partials to exchange.  Measured
+      // (8 KV heads, 61 nodes x 4): over 512 keys 14.7 against 19.6 us, 8K 19.0 against 20.7, 16K 26.8
+      // against 28.8, 24K 35.0 against 34.3; 4 requests of 4K 32 against 39; 32 of 1K to 16K 277
+      // against 270.
+      bool even;
+      double alone;
+      const long long n = choose_pieces(groups * blocks, tiles, num_sms, 4, &even, &alone);
+      if (0.65 * alone < cost) {
+        p->wr = 1;
+        pieces = n;
+        p->even = even;
+      }
+    }
     p->rows_per_cta = p->few ? (RG <= 16 ? 16 : 32) : p->wr * 128;
     p->row_blocks = (RG + p->rows_per_cta - 1) / p->rows_per_cta;
-    const long long base = static_cast<long long>(p->B) * p->Hkv * p->row_blocks;
-    long long pieces = d->num_splits;
-    if (pieces <= 0) pieces = choose_pieces(base, tiles, num_sms, p->few ? 10 : 6, &p->even);
+    const long long base = groups * p->row_blocks;
     pieces = std::min<long long>(std::min<long long>(pieces, tiles), 255);
     p->tps = static_cast<int>((tiles + pieces - 1) / pieces);
     p->splits = (tiles + p->tps - 1) / p->tps + 1;

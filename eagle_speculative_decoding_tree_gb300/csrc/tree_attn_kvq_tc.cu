@@ -21,15 +21,16 @@
 //   warp 14         TMA producer of the two code rings.
 //   warp 15         issues every tcgen05.mma: QK0 QK1 | PV0 QK2 | PV1 QK3 | ...
 // Items alternate between the warpgroups, so one tile's products run under the other's softmax.
-// With more than 128 rows (A) warpgroup w has rows 128 w .. and both take every tile: the
-// codes are read and widened once for 256 rows.  With fewer (B) both have the same rows and
-// take alternate tiles; their states merge in the epilogue.
+// With 256 rows a CTA (A) warpgroup w has rows 128 w .. and both take every tile: the codes are
+// read and widened once for 256 rows.  With 128 (B; up to 128 rows a KV head, and more over short
+// prefixes: plan_kvq_attn) both have the same rows and take alternate tiles; their states merge in
+// the epilogue.
 // TMEM: S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512); P overwrites S in place.
 //
-// Piece 0 is the tree itself (bf16 Q and K, V and P in halves, P always in two terms, one tile); the others are
-// tps 128-key tiles of the prefix.  Pieces write fp32 partials (TMA stores).  When the whole
-// grid fits on the SMs the launch is cooperative and the pieces of a group merge their rows in
-// the kernel (a second launch costs several microseconds); otherwise kvq_combine_kernel does.
+// Piece 0 is the tree itself (bf16 Q and K, V and P in halves, P always in two terms, one tile);
+// the others are tps 128-key tiles of the prefix.  Pieces write fp32 partials (TMA stores).  When the
+// whole grid fits on the SMs the launch is cooperative and the pieces of a group merge their rows
+// in the kernel (a second launch costs several microseconds); otherwise kvq_combine_kernel does.
 #include "common.cuh"
 #include "kvq.cuh"
 #include "kvq_merge.cuh"
@@ -53,6 +54,7 @@ constexpr int SM_W = SM_V + VST * T8;   // widened V, two stages
 constexpr int SMEM = SM_W + 2 * T16 + 1024;
 constexpr int NT = 512;
 constexpr int WT = 192;                 // widening threads (six warps)
+constexpr int QW = 14;                  // warps that stage the query tile: softmax and widening
 constexpr float kLazy = 4.f;            // as in tree_attn_kvq.cu
 constexpr int PB = 11;
 
@@ -183,7 +185,7 @@ __device__ __forceinline__ float to_half(const uint32_t (&r)[32], uint32_t (&p)[
   return a0 + a1;
 }
 
-// row / G for row < 2^16: a multiplication by ceil(2^32 / G) (a division costs as much as the
+// row / G for row G < 2^32: a multiplication by ceil(2^32 / G) (a division costs as much as the
 // rest of a row's staging).
 __device__ __forceinline__ int node_of(const KvqAttnArgs& a, int row) {
   return a.G == 1 ? row : static_cast<int>(__umulhi(static_cast<uint32_t>(row), a.g_inv));
@@ -215,8 +217,7 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
   kvq_place(a, a.rows_pad / (a.wr * 128), piece, bh, rb);
   const int b = bh / a.Hkv, h = bh % a.Hkv;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const bool two = a.wr == 2;            // A: two row tiles
-  const int row0 = rb * (two ? 256 : 128);
+  const int row0 = rb * a.wr * 128;
 
   if (warp == 15) {
     tmem_alloc(&tmem_base, 512);
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
       mbar_init(&s_full[s], 1);
       mbar_init(&p_full[s], 128);
     }
-    mbar_init(&q_full, 8);
+    mbar_init(&q_full, QW);
     mbar_init(&o_full, 1);
     fence_barrier_init();
   }
@@ -256,12 +257,79 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
   r.tile0 = (piece - 1) * tps;
   r.n = r.tree ? 1 : max(0, min(tps, n_pref - r.tile0));
   const int RG = r.Rb * a.G;
+  const bool two = a.wr == 2 && RG - row0 > 128;  // A: two row tiles
   const bool work = r.n > 0 && row0 < RG;
   const int items = work ? (two ? 2 * r.n : r.n) : 0;
   auto tile_of = [&](int i) { return two ? i >> 1 : i; };
   auto last_of = [&](int i) { return !two || (i & 1); };  // the tile's last item
   const uint32_t tb = tmem_base;
   const int nblk = (a.P + kQB - 1) / kQB;
+
+  if (warp < QW && work) {
+    // ------------------------------------------------------------ Q: four rows at a time, eight lanes a row
+    // All copies are asynchronous, 128 bytes of a row by its eight lanes: dims 8 c .. and 64 + 8 c ..
+    // in swizzled rows of 64 bf16 dims.  That is the tree's final form; a prefix piece's codes (128 to
+    // a row) then replace them in place: some 290 issue cycles for four rows, most of them in the
+    // e4m3 conversions, so every warp that would wait takes part (61 nodes over 2K, one query head
+    // a KV head: 15.5 us, 16.7 by the softmax warps alone).
+    // (Loops rolled: straight-line code that runs once costs its instruction fetches.)
+    const int c = lane & 7, sub = lane >> 3, units = two ? 64 : 32;
+    const uint32_t d0 = smem_u32(smem + SM_Q);
+#pragma unroll 1
+    for (int u = warp; u < units; u += QW) {
+      const int lr = (u & 31) * 4 + sub, qr = row0 + u * 4 + sub;
+      const int nd = node_of(a, qr), n16 = qr < RG ? 16 : 0;  // 0: zero fill, nothing read
+      const uint16_t* src =
+          n16 ? a.q + ((static_cast<size_t>(b) * a.R + nd) * a.Hq + h * a.G + (qr - nd * a.G)) * 128 + 8 * c : a.q;
+      const uint32_t at = d0 + (u >> 5) * T16 + lr * 128 + ((c ^ (lr & 7)) << 4);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(src), "r"(n16) : "memory");
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at + T8), "l"(src + 64), "r"(n16) : "memory");
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+#pragma unroll 1
+    for (int u = warp; u < units && !r.tree; u += QW) {
+      const int lr = (u & 31) * 4 + sub;
+      if (row0 + u * 4 >= RG) {  // zeros in either form
+        if (c == 0) s_q[u >> 5][lr] = 1.f;
+        continue;
+      }
+      uint8_t* dst = smem + SM_Q + (u >> 5) * T16;
+      const uint8_t* d = dst + lr * 128 + ((c ^ (lr & 7)) << 4);
+      const uint4 x0 = *reinterpret_cast<const uint4*>(d), x1 = *reinterpret_cast<const uint4*>(d + T8);
+      const uint32_t x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+      uint32_t am = 0;  // the row's largest magnitude, as bf16 bits (ordered as integers)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) am = max(am, max((x[k] << 16) & 0x7fff0000u, x[k] & 0x7fff0000u));
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
+      // largest element in (224, 448]: the power of two of a cache block's scale; a row with
+      // an element that is not finite gets NaN scores
+      const float qs = kvq_scale(fmaxf(__uint_as_float(min(am, 0x7f7f0000u)), 0x1p-100f));
+      const float mul = __uint_as_float((254u << 23) - __float_as_uint(qs));  // 1 / qs, a power of two
+      if (c == 0) s_q[u >> 5][lr] = am < 0x7f800000u ? qs : __uint_as_float(0x7fffffffu);
+      uint32_t hi[4], lo[4];  // words 0, 1: dims 8 c ..; 2, 3: dims 64 + 8 c ..
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        // exact as halves (bf16's 8 bits, magnitudes up to 448), and so is what hi leaves
+        const uint32_t q2 = half2_bits(__uint_as_float(x[k] << 16) * mul, __uint_as_float(x[k] & 0xffff0000u) * mul);
+        const uint32_t h8 = e4m3x2_of_half2(q2);
+        const uint32_t l8 = e4m3x2_of_half2(sub_half2(q2, kvq_half2(h8)));
+        hi[k >> 1] = (k & 1) ? hi[k >> 1] | (h8 << 16) : h8;
+        lo[k >> 1] = (k & 1) ? lo[k >> 1] | (l8 << 16) : l8;
+      }
+      // (every lane of the row has its elements: the maximum's shuffles came between)
+      uint8_t* d1 = dst + lr * 128 + (((c >> 1) ^ (lr & 7)) << 4) + 8 * (c & 1);
+      uint8_t* d2 = dst + lr * 128 + ((((c >> 1) + 4) ^ (lr & 7)) << 4) + 8 * (c & 1);
+      *reinterpret_cast<uint2*>(d1) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(d2) = make_uint2(hi[2], hi[3]);
+      *reinterpret_cast<uint2*>(d1 + T8) = make_uint2(lo[0], lo[1]);
+      *reinterpret_cast<uint2*>(d2 + T8) = make_uint2(lo[2], lo[3]);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&q_full);
+  }
 
   // registers: 128 a thread at launch (65536); the softmax takes 176 each, the others keep 80
   // (256 x 176 + 256 x 80 = 65536)
@@ -429,7 +497,8 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
         } else {
           auto qk = [&](int i) {
             const int t = tile_of(i), w = i & 1, s = t % KST;
-            if (!wait(&k_full[s], (t / KST) & 1, ERR_K)) return false;
+            // (A: the first row tile's item has waited for both; a wait costs what a product does)
+            if ((!two || !w) && !wait(&k_full[s], (t / KST) & 1, ERR_K)) return false;
             tc_fence_after();
             const uint64_t q = dq + (two ? w * (T16 >> 4) : 0), k = dk + s * (T8 >> 4);
 #pragma unroll
@@ -443,7 +512,7 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
           };
           auto pv = [&](int i) {
             const int t = tile_of(i), w = i & 1;
-            if (!wait(&w_full[t & 1], (t >> 1) & 1, ERR_W)) return false;
+            if ((!two || !w) && !wait(&w_full[t & 1], (t >> 1) & 1, ERR_W)) return false;
             if (!wait(&p_full[w], (i >> 1) & 1, ERR_P)) return false;
             tc_fence_after();
             const uint64_t v = dv + (t & 1) * (T16 >> 4);
@@ -473,28 +542,7 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
       const int row = row0 + (two ? w * 128 : 0) + rl;
       const bool live = row < RG;
       const int node = live ? node_of(a, row) : 0;
-      // Q: A every warpgroup stages its rows; B warpgroup 0 alone (the rows are the same).  Eight
-      // lanes take a row.
-      if (two || w == 0) {
-        uint8_t* dst = smem + SM_Q + w * T16;
-        const int c = lane & 7, sub = lane >> 3;
-        // All copies are asynchronous, the whole tile in flight, 128 bytes of a row by its eight
-        // lanes: dims 8 c .. and 64 + 8 c .. in swizzled rows of 64 bf16 dims.  That is the tree's
-        // final form; a prefix piece's codes (128 to a row) then replace them in place.
-        // (Loops rolled: straight-line code that runs once costs its instruction fetches.)
-        const uint32_t d0 = smem_u32(dst);
-#pragma unroll 1
-        for (int e = 0; e < 8; ++e) {
-          const int lr = qd * 32 + e * 4 + sub, qr = row0 + w * 128 + lr;
-          const int nd = node_of(a, qr), n16 = qr < RG ? 16 : 0;  // 0: zero fill, nothing read
-          const uint16_t* src =
-              n16 ? a.q + ((static_cast<size_t>(b) * a.R + nd) * a.Hq + h * a.G + (qr - nd * a.G)) * 128 + 8 * c : a.q;
-          const uint32_t at = d0 + lr * 128 + ((c ^ (lr & 7)) << 4);
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(src), "r"(n16) : "memory");
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at + T8), "l"(src + 64), "r"(n16) : "memory");
-        }
-      }
-      // (under the copies) vref: the largest V scale of the piece
+      // vref: the largest V scale of the piece
       const float* ks = a.ks + static_cast<size_t>(bh) * nblk + r.tile0 * (KT / kQB);
       const float* vs = a.vs + static_cast<size_t>(bh) * nblk + r.tile0 * (KT / kQB);
       int n_blk = 0;
@@ -508,54 +556,9 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
         if (m > 0.f) vref = m;
       }
       const float vinv = 1.f / vref;
-      if (two || w == 0) {
-        const int c = lane & 7, sub = lane >> 3;
-        uint8_t* dst = smem + SM_Q + w * T16;
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        __syncwarp();
-#pragma unroll 2
-        for (int e = 0; e < 8 && !r.tree; ++e) {
-          const int lr = qd * 32 + e * 4 + sub;
-          const uint8_t* d = dst + lr * 128 + ((c ^ (lr & 7)) << 4);
-          const uint4 x0 = *reinterpret_cast<const uint4*>(d), x1 = *reinterpret_cast<const uint4*>(d + T8);
-          const uint32_t u[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-          uint32_t am = 0;  // the row's largest magnitude, as bf16 bits (ordered as integers)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) am = max(am, max((u[k] << 16) & 0x7fff0000u, u[k] & 0x7fff0000u));
-#pragma unroll
-          for (int o = 4; o > 0; o >>= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
-          // largest element in (224, 448]: the power of two of a cache block's scale; a row with
-          // an element that is not finite gets NaN scores
-          const float qs = kvq_scale(fmaxf(__uint_as_float(min(am, 0x7f7f0000u)), 0x1p-100f));
-          const float mul = __uint_as_float((254u << 23) - __float_as_uint(qs));  // 1 / qs, a power of two
-          if (c == 0) s_q[w][lr] = am < 0x7f800000u ? qs : __uint_as_float(0x7fffffffu);
-          uint32_t hi[4], lo[4];  // words 0, 1: dims 8 c ..; 2, 3: dims 64 + 8 c ..
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            // exact as halves (bf16's 8 bits, magnitudes up to 448), and so is what hi leaves
-            const uint32_t q2 = half2_bits(__uint_as_float(u[k] << 16) * mul, __uint_as_float(u[k] & 0xffff0000u) * mul);
-            const uint32_t h8 = e4m3x2_of_half2(q2);
-            const uint32_t l8 = e4m3x2_of_half2(sub_half2(q2, kvq_half2(h8)));
-            hi[k >> 1] = (k & 1) ? hi[k >> 1] | (h8 << 16) : h8;
-            lo[k >> 1] = (k & 1) ? lo[k >> 1] | (l8 << 16) : l8;
-          }
-          // (every lane of the row has its elements: the maximum's shuffles came between)
-          uint8_t* d1 = dst + lr * 128 + (((c >> 1) ^ (lr & 7)) << 4) + 8 * (c & 1);
-          uint8_t* d2 = dst + lr * 128 + ((((c >> 1) + 4) ^ (lr & 7)) << 4) + 8 * (c & 1);
-          *reinterpret_cast<uint2*>(d1) = make_uint2(hi[0], hi[1]);
-          *reinterpret_cast<uint2*>(d2) = make_uint2(hi[2], hi[3]);
-          *reinterpret_cast<uint2*>(d1 + T8) = make_uint2(lo[0], lo[1]);
-          *reinterpret_cast<uint2*>(d2 + T8) = make_uint2(lo[2], lo[3]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
-      if (lane == 0) mbar_arrive(&q_full);
-      float qs = 1.f;
-      if (!r.tree) {
-        if (!two) bar_sync(1, 256);  // (A: the warp staged its own rows)
-        qs = s_q[two ? w : 0][rl];
-      }
+      // (orders every warp's s_q; a query tile that never came shows at the first scores)
+      (void)wait_parity(&q_full, 0, a.err, ERR_Q);
+      const float qs = r.tree ? 1.f : s_q[two ? w : 0][rl];
       uint32_t tw[4] = {0u, 0u, 0u, 0u};  // the tree's visible keys
       if (r.tree && live) {
         const uint64_t* mp = a.anc_mask + (static_cast<size_t>(b) * a.R + node) * a.W;
