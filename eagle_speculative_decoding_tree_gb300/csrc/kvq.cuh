@@ -51,6 +51,23 @@ __device__ __forceinline__ float2 kvq_float2(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// A query row's elements as two e4m3 terms, x = hi + lo: two halves (magnitudes up to 448, exact) to
+// the upper bytes of two halves each.  Times 2^-8 a half's exponent field is e4m3's (subnormals
+// too), and a code is its bits 13 .. 7 and the sign: cut off for hi, which leaves lo the other four
+// of bf16's eight bits; lo is rounded (it has to be below 2^-11 of the row's largest element).
+// Integer instructions (conversions to and from e4m3: 32 requests of 1K to 16K 262.7 against
+// 261.6 us, 61 nodes over 2K 15.6 against 15.4).
+__device__ __forceinline__ void kvq_split2(uint32_t h, uint32_t& hi, uint32_t& lo) {
+  const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h), __floats2half2_rn(0x1p-8f, 0x1p-8f));
+  const uint32_t q = *reinterpret_cast<const uint32_t*>(&v), t = q & 0xff80ff80u;
+  const __half2 d = __hsub2(v, *reinterpret_cast<const __half2*>(&t));
+  const uint32_t l = *reinterpret_cast<const uint32_t*>(&d) + 0x00400040u;
+  hi = (q << 1) | (q & 0x80008000u);
+  lo = (l << 1) | (l & 0x80008000u);
+}
+// The codes of two such pairs.
+__device__ __forceinline__ uint32_t kvq_pack(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7531); }
+
 // Four codes of one scale to the codes of a larger one: ratio = old scale / new scale.
 __device__ __forceinline__ uint32_t kvq_move4(uint32_t w, float ratio) {
   const float2 a = kvq_float2(w), b = kvq_float2(w >> 16);

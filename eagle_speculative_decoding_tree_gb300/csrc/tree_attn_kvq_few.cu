@@ -10,10 +10,12 @@
 //   q  as in tree_attn_kvq_tc.cu: a power of two puts a row's largest element in (224, 448], and
 //      q = hi + lo in e4m3 keeps bf16's bits down to elements of 2^-11 of it;
 //   p  2^PB vs / vref is rounded to a half (11 bits) and that half is written as four e5m2 terms
-//      of three bits each, exactly down to steps of 2^-31 of the largest p (the rest after the
+//      of three bits each, exactly down to steps of 2^-30 of the largest p (the rest after the
 //      first term is multiplied by 8, past e5m2's smallest steps).  EAGLE_ATTN_PRECISE: two more
-//      terms of what the half left (2^-17 of p).  The terms are columns of their own; their
-//      scales meet in the epilogue, in fp32.
+//      terms of what the half left (2^-17 of p).  A term is the upper byte of what is left of the
+//      half, cut off, and rounded for the last of them and PRECISE's: integer instructions
+//      (conversions to e5m2: 58.0 against 56.8 us for the chain of 8 over 128K).  The terms are
+//      columns of their own; their scales meet in the epilogue, in fp32.
 // A row's running maximum would need every key's score; instead the exponentials are taken
 // against a reference that moves (a slow path through shared memory) when some score is more than
 // 2^kLazy above it, which a vote of the tile's threads finds out.
@@ -24,10 +26,10 @@
 //   a TMA producer warp: 128-key tiles of K and V codes, ST stages each
 //   a warp that issues every tcgen05.mma: QK0 QK1 | QK2 PV0 | QK3 PV1 | ...
 // (32 rows a thread instead of 16 take as many instructions, but at 2.5 warps a scheduler only
-// every second cycle issued one: 61.7 us against 58 for a chain of 8 over 128K.)
+// every second cycle issued one: 61.7 us against 58.0 for a chain of 8 over 128K.)
 // TMEM: S of the even and the odd tiles (hi | lo columns), then O likewise (a column per row and term).
 // Measured (8 KV heads, 4 query heads each, graph replay): one token over 128K tokens 46 us (5.8
-// TB/s, 86 % of a device copy's rate), over 8K 9.7; a chain of 8 over 128K, fp32 and precise, 58 us
+// TB/s, 86 % of a device copy's rate), over 8K 9.7; a chain of 8 over 128K, fp32 and precise, 57 us
 // (the loop takes 1450 cycles a tile where HBM takes 1390; launch, first tile and merge 15 us).
 // Piece 0 is the tree (at most 32 bf16 keys), computed in fp32 on the ordinary cores; the others
 // are tps tiles of the prefix.  Pieces write fp32 partials, merged in the kernel when the grid
@@ -104,18 +106,8 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ uint32_t e4m3x2_of_half2(uint32_t h) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
-  return r;
-}
-__device__ __forceinline__ uint32_t e5m2x2_of_half2(uint32_t h) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
-  return r;
-}
-// Two e5m2 codes as halves: the code is a half's upper byte.
-__device__ __forceinline__ uint32_t half2_of_e5m2(uint32_t c) { return __byte_perm(c, 0, 0x1404); }
+// An e5m2 code is a half's upper byte: two mantissa bits of ten.  Half a step of it, for two halves.
+constexpr uint32_t kHalfStep = 0x00800080u;
 __device__ __forceinline__ uint32_t sub_half2(uint32_t a, uint32_t b) {
   const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&d);
@@ -383,12 +375,15 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
           s_c[row] = am < 0x7f800000u ? a.scale_log2 * qs : __uint_as_float(0x7fffffffu);
         uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t q2 = half2_bits(__uint_as_float(u[k] << 16) * mul, __uint_as_float(u[k] & 0xffff0000u) * mul);
-          const uint32_t h8 = e4m3x2_of_half2(q2);
-          const uint32_t l8 = e4m3x2_of_half2(sub_half2(q2, kvq_half2(h8)));
-          hi[k >> 1] = (k & 1) ? hi[k >> 1] | (h8 << 16) : h8;
-          lo[k >> 1] = (k & 1) ? lo[k >> 1] | (l8 << 16) : l8;
+        for (int k = 0; k < 4; ++k) {
+          uint32_t h[2], l[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t v = u[2 * k + e];
+            kvq_split2(half2_bits(__uint_as_float(v << 16) * mul, __uint_as_float(v & 0xffff0000u) * mul), h[e], l[e]);
+          }
+          hi[k] = kvq_pack(h[0], h[1]);
+          lo[k] = kvq_pack(l[0], l[1]);
         }
         uint8_t* d1 = smem + F::SM_Q + row * 128 + (((c >> 1) ^ (row & 7)) << 4) + 8 * (c & 1);
         uint8_t* d2 = smem + F::SM_Q + row * 128 + ((((c >> 1) + 4) ^ (row & 7)) << 4) + 8 * (c & 1);
@@ -521,14 +516,18 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
         for (int u = 0; u < TERMS; ++u) {
           uint32_t c4[4];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            uint32_t& y = u < 4 ? hh[k] : ll[k];
-            const uint32_t c2 = e5m2x2_of_half2(y);
-            if (u != 3 && u != TERMS - 1) {  // exact: what an e5m2 term leaves of a half
-              y = sub_half2(y, half2_of_e5m2(c2));
-              if (u == 0) y = times8_half2(y);
+          for (int k = 0; k < 4; ++k) {
+            uint32_t &y0 = u < 4 ? hh[2 * k] : ll[2 * k], &y1 = u < 4 ? hh[2 * k + 1] : ll[2 * k + 1];
+            const uint32_t t0 = u < 3 ? y0 : y0 + kHalfStep, t1 = u < 3 ? y1 : y1 + kHalfStep;
+            c4[k] = __byte_perm(t0, t1, 0x7531);  // the upper bytes
+            if (u != 3 && u != TERMS - 1) {       // exact: what a term leaves of a half
+              y0 = sub_half2(y0, t0 & 0xff00ff00u);
+              y1 = sub_half2(y1, t1 & 0xff00ff00u);
+              if (u == 0) {
+                y0 = times8_half2(y0);
+                y1 = times8_half2(y1);
+              }
             }
-            c4[k >> 1] = (k & 1) ? c4[k >> 1] | (c2 << 16) : c2;
           }
           const int col = u * NR + g0;  // first of 16 columns: block col / 32, 16-byte half (col / 16) % 2
           *reinterpret_cast<uint4*>(pb + (col >> 5) * 4096 + ((col & 16) ^ flip)) = make_uint4(c4[0], c4[1], c4[2], c4[3]);

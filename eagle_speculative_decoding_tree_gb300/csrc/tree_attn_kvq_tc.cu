@@ -116,17 +116,6 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// Two halves to e4m3 codes (nearest even, saturating); the difference of two pairs.
-__device__ __forceinline__ uint32_t e4m3x2_of_half2(uint32_t h) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
-  return r;
-}
-__device__ __forceinline__ uint32_t sub_half2(uint32_t a, uint32_t b) {
-  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&d);
-}
-
 __device__ __forceinline__ float max32(const uint32_t (&a)[32]) {
   float m[11];
 #pragma unroll
@@ -275,9 +264,8 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
     // ------------------------------------------------------------ Q: four rows at a time, eight lanes a row
     // All copies are asynchronous, 128 bytes of a row by its eight lanes: dims 8 c .. and 64 + 8 c ..
     // in swizzled rows of 64 bf16 dims.  That is the tree's final form; a prefix piece's codes (128 to
-    // a row) then replace them in place: some 290 issue cycles for four rows, most of them in the
-    // e4m3 conversions, so every warp that would wait takes part (61 nodes over 2K, one query head
-    // a KV head: 15.5 us, 16.7 by the softmax warps alone).
+    // a row) then replace them in place: every warp that would wait takes part (61 nodes over 2K, one
+    // query head a KV head: 15.5 us, 16.7 by the softmax warps alone).
     // (Loops rolled: straight-line code that runs once costs its instruction fetches.)
     const int c = lane & 7, sub = lane >> 3, units = two ? 64 : 32;
     const uint32_t d0 = smem_u32(smem + SM_Q);
@@ -316,13 +304,15 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
       if (c == 0) s_q[u >> 5][lr] = am < 0x7f800000u ? qs : __uint_as_float(0x7fffffffu);
       uint32_t hi[4], lo[4];  // words 0, 1: dims 8 c ..; 2, 3: dims 64 + 8 c ..
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        // exact as halves (bf16's 8 bits, magnitudes up to 448), and so is what hi leaves
-        const uint32_t q2 = half2_bits(__uint_as_float(x[k] << 16) * mul, __uint_as_float(x[k] & 0xffff0000u) * mul);
-        const uint32_t h8 = e4m3x2_of_half2(q2);
-        const uint32_t l8 = e4m3x2_of_half2(sub_half2(q2, kvq_half2(h8)));
-        hi[k >> 1] = (k & 1) ? hi[k >> 1] | (h8 << 16) : h8;
-        lo[k >> 1] = (k & 1) ? lo[k >> 1] | (l8 << 16) : l8;
+      for (int k = 0; k < 4; ++k) {
+        uint32_t h[2], l[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t v = x[2 * k + e];
+          kvq_split2(half2_bits(__uint_as_float(v << 16) * mul, __uint_as_float(v & 0xffff0000u) * mul), h[e], l[e]);
+        }
+        hi[k] = kvq_pack(h[0], h[1]);
+        lo[k] = kvq_pack(l[0], l[1]);
       }
       // (every lane of the row has its elements: the maximum's shuffles came between)
       uint8_t* d1 = dst + lr * 128 + (((c >> 1) ^ (lr & 7)) << 4) + 8 * (c & 1);
