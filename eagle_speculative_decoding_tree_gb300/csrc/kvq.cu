@@ -243,8 +243,8 @@ __global__ void __launch_bounds__(256) kvq_read_kernel(const eagle_kvq_desc d, c
     if (status && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(status, EAGLE_STATUS_CACHE_FULL);
     return;
   }
-  const int per = D / E;
-  const long long total = static_cast<long long>(n) * per;
+  const int lg = 31 - __clz(D / E);  // a row's pieces: a power of two (64-bit divisions cost more than all else here)
+  const long long total = static_cast<long long>(n) << lg;
   const int nblk = (d.max_seq + kQB - 1) / kQB;
   const uint8_t* src = (blockIdx.z ? v8 : k8) + (static_cast<size_t>(bh) * d.max_seq + first) * D;
   const float* sc = (blockIdx.z ? vs : ks) + static_cast<size_t>(bh) * nblk;
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(256) kvq_read_kernel(const eagle_kvq_desc d, c
       w[u].x = __ldg(reinterpret_cast<const uint32_t*>(src) + c);
     else
       w[u] = __ldg(reinterpret_cast<const uint2*>(src) + c);
-    s[u] = __ldg(sc + (first + static_cast<int>(c / per)) / kQB);
+    s[u] = __ldg(sc + (first + static_cast<int>(c >> lg)) / kQB);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -294,9 +294,8 @@ __global__ void __launch_bounds__(128) kvq_commit_kernel(const eagle_commit_desc
                                                          const void* tree_feat) {
   constexpr int C = 4;
   const int lane = threadIdx.x & 31;
-  const long long id = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int per = d.n_kv_heads * d.batch;
-  const int l = static_cast<int>(id / per), bh = static_cast<int>(id % per), b = bh / d.n_kv_heads, h = bh % d.n_kv_heads;
+  const int id = blockIdx.x * 4 + (threadIdx.x >> 5), per = d.n_kv_heads * d.batch;  // (layers <= 128, per <= 65535)
+  const int l = id / per, bh = id % per, b = bh / d.n_kv_heads, h = bh % d.n_kv_heads;
   sm100::griddep_wait();
   sm100::griddep_launch_dependents();
   if (l >= d.layers || !commit_fits(d, n_acc, seq_len, b)) return;

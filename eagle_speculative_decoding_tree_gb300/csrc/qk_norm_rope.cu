@@ -56,7 +56,7 @@ struct RopeArgs {
   void* v;
   int rows, hq, hkv, rot, interleaved;
   int run, runs;  // heads a warp takes, runs of them in a row
-  long long units;
+  int units;
   long long stride;
   float eps;
 };
@@ -132,13 +132,13 @@ __global__ void __launch_bounds__(kThreads, F32 ? 5 : 7) qk_norm_rope_kernel(con
   constexpr int U = F32 ? 2 : 3;     // passes whose loads are in flight together
   __shared__ __align__(16) float2 table[kThreads / 32][D / 2];
   const int warp = threadIdx.x >> 5;
-  const long long unit = static_cast<long long>(blockIdx.x) * (kThreads / 32) + warp;
+  const int unit = blockIdx.x * (kThreads / 32) + warp;
   if (unit >= a.units) return;
-  const size_t row = static_cast<size_t>(unit / a.runs);
-  const int b = static_cast<int>(row / a.rows), r = static_cast<int>(row % a.rows);
+  const int row32 = unit / a.runs, b = row32 / a.rows, r = row32 % a.rows;
+  const size_t row = static_cast<size_t>(row32);
   if (a.n_nodes && r >= a.n_nodes[b]) return;  // rows past the request's tree are not written
   const int sub = (threadIdx.x & 31) / LANES, lane = threadIdx.x % LANES;
-  const int h_begin = static_cast<int>(unit % a.runs) * a.run;
+  const int h_begin = (unit - row32 * a.runs) * a.run;
   const int h_end = min(h_begin + a.run, a.hq + 2 * a.hkv);
   const size_t src = row * a.stride + static_cast<size_t>(lane) * 8;
   if (h_begin + sub < h_end)
@@ -281,9 +281,9 @@ cudaError_t launch_qk_norm_rope(const eagle_qk_norm_rope_desc& d, const void* qk
   long long split = std::min<long long>((want + rows - 1) / rows, (heads + pass - 1) / pass);
   a.run = static_cast<int>(((heads + split - 1) / split + pass - 1) / pass * pass);
   a.runs = (heads + a.run - 1) / a.run;
-  a.units = rows * a.runs;
-  const long long grid = (a.units + kThreads / 32 - 1) / (kThreads / 32);
-  if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
+  if (rows * a.runs > 0x7ffffff0ll) return cudaErrorInvalidValue;  // (more than any device holds)
+  a.units = static_cast<int>(rows * a.runs);
+  const int grid = (a.units + kThreads / 32 - 1) / (kThreads / 32);
   const bool f32 = d.dtype == EAGLE_F32;
   if (d.head_dim == 64)
     f32 ? qk_norm_rope_kernel<true, 64><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a)
