@@ -29,8 +29,8 @@
 // every second cycle issued one: 61.7 us against 58.0 for a chain of 8 over 128K.)
 // TMEM: S of the even and the odd tiles (hi | lo columns), then O likewise (a column per row and term).
 // Measured (8 KV heads, 4 query heads each, graph replay): one token over 128K tokens 46 us (5.8
-// TB/s, 86 % of a device copy's rate), over 8K 9.7; a chain of 8 over 128K, fp32 and precise, 57 us
-// (the loop takes 1450 cycles a tile where HBM takes 1390; launch, first tile and merge 15 us).
+// TB/s, 86 % of a device copy's rate), over 8K 9.7; a chain of 8 over 128K, fp32 and precise, 54 us
+// (the loop's waits and product issue take about as long a tile as HBM does).
 // Piece 0 is the tree (at most 32 bf16 keys), computed in fp32 on the ordinary cores; the others
 // are tps tiles of the prefix.  Pieces write fp32 partials, merged in the kernel when the grid
 // fits on the SMs (cooperative launch), else by kvq_combine_kernel.
@@ -51,7 +51,7 @@ constexpr int T8 = KT * 128;  // a tile of codes, 16 KB
 constexpr float kLazy = 4.f;  // as in tree_attn_kvq.cu
 constexpr int PB = 11;
 
-enum : int { ERR_K = 1, ERR_KE = 2, ERR_V = 4, ERR_VE = 8, ERR_S = 32, ERR_P = 64, ERR_O = 128, ERR_GROUP = 256,
+enum : int { ERR_K = 1, ERR_KE = 2, ERR_VE = 8, ERR_S = 32, ERR_P = 64, ERR_O = 128, ERR_GROUP = 256,
              ERR_Q = 512 };
 
 struct Maps {
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
   constexpr int ST = F::ST, SW = F::SW, HALVES = NR / 16;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t k_full[ST], k_empty[ST], v_full[ST], v_empty[ST], s_full[2], s_empty[2], p_full[2], p_empty[2], q_full, o_full;
+  __shared__ uint64_t full[ST], k_empty[ST], v_empty[ST], s_full[2], s_empty[2], p_full[2], p_empty[2], q_full, o_full;
   __shared__ uint32_t tmem_base;
   __shared__ int go;
   // by tile parity:
@@ -205,9 +205,8 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < ST; ++s) {
-      mbar_init(&k_full[s], 1);
+      mbar_init(&full[s], 2);  // a tile's K and V (one wait for both: 56.8 -> 54.4 us for a chain of 8 over 128K)
       mbar_init(&k_empty[s], 1);
-      mbar_init(&v_full[s], 1);
       mbar_init(&v_empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -276,18 +275,18 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
         for (int t = 0; t < n; ++t) {
           const int s = t % ST;
           if (t >= ST && !wait_parity(&k_empty[s], (t / ST - 1) & 1, a.err, ERR_KE)) break;
-          load(tm.k, F::SM_K + s * T8, &k_full[s], t);
+          load(tm.k, F::SM_K + s * T8, &full[s], t);
           ++k_in;
           if (t >= ST && !wait_parity(&v_empty[s], (t / ST - 1) & 1, a.err, ERR_VE)) break;
-          load(tm.v, F::SM_V + s * T8, &v_full[s], t);
+          load(tm.v, F::SM_V + s * T8, &full[s], t);
           ++v_in;
           // the first tile first: with the whole ring's loads ahead of them the queries and scales
           // would arrive last, and nothing can start without them
           if (t == 0 && !wait_parity(&q_full, 0, a.err, ERR_Q)) break;
         }
         // no copy may still be landing when the CTA ends
-        for (int s = 0; s < ST && s < k_in; ++s) (void)wait_parity(&k_full[s], ((k_in - 1 - s) / ST) & 1, a.err, ERR_K);
-        for (int s = 0; s < ST && s < v_in; ++s) (void)wait_parity(&v_full[s], ((v_in - 1 - s) / ST) & 1, a.err, ERR_V);
+        if (k_in > v_in) mbar_arrive(&full[v_in % ST]);  // (gave up between the two)
+        for (int s = 0; s < ST && s < k_in; ++s) (void)wait_parity(&full[s], ((k_in - 1 - s) / ST) & 1, a.err, ERR_K);
       }
     } else if (warp == SW + 1) {
       // ------------------------------------------------------------ tcgen05.mma issue
@@ -302,7 +301,7 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
       const uint64_t dp = desc_sw32(smem_u32(smem + F::SM_P), 4096, 256);
       auto qk = [&](int i) {
         const int s = i % ST, w = i & 1;
-        if (!wait(&k_full[s], (i / ST) & 1, ERR_K)) return false;
+        if (!wait(&full[s], (i / ST) & 1, ERR_K)) return false;
         tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
@@ -313,7 +312,6 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
       };
       auto pv = [&](int i) {
         const int s = i % ST, w = i & 1;
-        if (!wait(&v_full[s], (i / ST) & 1, ERR_V)) return false;
         if (!wait(&p_full[w], (i >> 1) & 1, ERR_P)) return false;
         tc_fence_after();
 #pragma unroll
@@ -534,7 +532,7 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
         }
         if (!on) {
           // V rows behind the prefix: zeros, whatever they hold (their P is 0)
-          ok = ok && wait_parity(&v_full[i % ST], (i / ST) & 1, a.err, ERR_V);
+          ok = ok && wait_parity(&full[i % ST], (i / ST) & 1, a.err, ERR_K);
           uint4* v = reinterpret_cast<uint4*>(smem + F::SM_V + (i % ST) * T8 + key * 128);
 #pragma unroll
           for (int c = 0; c < 8; ++c) v[c] = make_uint4(0, 0, 0, 0);
