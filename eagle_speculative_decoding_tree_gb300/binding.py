@@ -418,10 +418,26 @@ def eagle_ttt_attn(desc: TttDesc, q, k_trunk, v_trunk, k_branch, v_branch, out, 
 CODES = (torch.uint8, torch.float8_e4m3fn)
 
 
-def _on_current(t: torch.Tensor, name: str) -> None:
-    """The library launches on the current device: a tensor of another one is refused."""
-    if t.is_cuda and t.get_device() != (_device_index() if _device_index is not None else torch.cuda.current_device()):
+def _device() -> int:
+    """The current device, which the library launches on; -2 where there is none (no tensor is on it)."""
+    try:
+        return _device_index() if _device_index is not None else torch.cuda.current_device()
+    except (RuntimeError, AssertionError):
+        return -2
+
+
+def _at(t: Optional[torch.Tensor], dtype, name: str, dev: int) -> Optional[int]:
+    """_ptr of a tensor that must be on device `dev`."""
+    if t is None:
+        return None
+    if t.get_device() == dev and t.is_contiguous():
+        d = t.dtype
+        if d is dtype or (type(dtype) is tuple and d in dtype):
+            return t.data_ptr()
+    p = _ptr(t, dtype, name)
+    if t.get_device() != dev:
         raise ValueError(f"{name} is on cuda:{t.get_device()}, which is not the current device")
+    return p
 
 
 def _element(dtype: int):
@@ -433,25 +449,27 @@ def eagle_kvq_write(desc: KvqDesc, k, v, start, count: Optional[torch.Tensor], k
                     status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Quantise K/V rows into the 8-bit cache (see eagle.h: eagle_kvq_write).  Codes are
     uint8 or float8_e4m3fn tensors [B][Hkv][P][D], scales fp32 [B][Hkv][ceil(P / 64)]."""
-    _on_current(k, "k")
+    dev = _device()
     dt = _element(desc.dtype)
     _check("eagle_kvq_write", load().eagle_kvq_write(
-        ctypes.byref(desc), _ptr(k, dt, "k"), _ptr(v, dt, "v"), _ptr(start, torch.int32, "start"),
-        _ptr(count, torch.int32, "count"), _ptr(k_codes, CODES, "k_codes"), _ptr(k_scale, torch.float32, "k_scale"),
-        _ptr(v_codes, CODES, "v_codes"), _ptr(v_scale, torch.float32, "v_scale"), _ptr(status, torch.int32, "status"),
+        ctypes.byref(desc), _at(k, dt, "k", dev), _at(v, dt, "v", dev), _at(start, torch.int32, "start", dev),
+        _at(count, torch.int32, "count", dev), _at(k_codes, CODES, "k_codes", dev),
+        _at(k_scale, torch.float32, "k_scale", dev), _at(v_codes, CODES, "v_codes", dev),
+        _at(v_scale, torch.float32, "v_scale", dev), _at(status, torch.int32, "status", dev),
         _stream(stream)))
 
 
 def eagle_kvq_read(desc: KvqDesc, k_codes, k_scale, v_codes, v_scale, start, count: Optional[torch.Tensor], k, v,
                    status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Read rows of the 8-bit cache back (see eagle.h: eagle_kvq_read)."""
-    _on_current(k_codes, "k_codes")
+    dev = _device()
     dt = _element(desc.dtype)
     _check("eagle_kvq_read", load().eagle_kvq_read(
-        ctypes.byref(desc), _ptr(k_codes, CODES, "k_codes"), _ptr(k_scale, torch.float32, "k_scale"),
-        _ptr(v_codes, CODES, "v_codes"), _ptr(v_scale, torch.float32, "v_scale"), _ptr(start, torch.int32, "start"),
-        _ptr(count, torch.int32, "count"), _ptr(k, dt, "k"), _ptr(v, dt, "v"),
-        _ptr(status, torch.int32, "status"), _stream(stream)))
+        ctypes.byref(desc), _at(k_codes, CODES, "k_codes", dev), _at(k_scale, torch.float32, "k_scale", dev),
+        _at(v_codes, CODES, "v_codes", dev), _at(v_scale, torch.float32, "v_scale", dev),
+        _at(start, torch.int32, "start", dev), _at(count, torch.int32, "count", dev), _at(k, dt, "k", dev),
+        _at(v, dt, "v", dev),
+        _at(status, torch.int32, "status", dev), _stream(stream)))
 
 
 class KvqLayerPointers:
@@ -468,6 +486,7 @@ class KvqLayerPointers:
         self.tk, self.tv = mk(tree_k, FLOATS, "tree_k"), mk(tree_v, FLOATS, "tree_v")
         self.tensors = [list(t) for t in (k_codes, k_scale, v_codes, v_scale, tree_k, tree_v)]
         self.layers, self.dtypes = n, {t.dtype for t in (*tree_k, *tree_v)}
+        self.devices = {t.get_device() for ts in self.tensors for t in ts}
         if any(len(t) != n for t in self.tensors):
             raise ValueError("as many tensors of each kind as layers")
         self.addresses = tuple(ctypes.addressof(x) for x in (self.k, self.ks, self.v, self.vs, self.tk, self.tv))
@@ -476,16 +495,19 @@ class KvqLayerPointers:
 def eagle_kvq_commit(desc: CommitDesc, layers: KvqLayerPointers, n_acc, path, seq_len, commit_pos,
                      feat_cache=None, tree_feat=None, status=None, stream=None) -> None:
     """Commit the accepted path into 8-bit caches (see eagle.h: eagle_kvq_commit)."""
-    _on_current(n_acc, "n_acc")
+    dev = _device()
+    if layers.devices != {dev}:
+        raise ValueError(f"layer tensors on devices {sorted(layers.devices)}, the current one is {dev}")
     if desc.layers > layers.layers:
         raise ValueError(f"{desc.layers} layers, pointers of {layers.layers}")
     if layers.dtypes != {_element(desc.dtype)} and _element(desc.dtype) is not FLOATS:
         raise ValueError("tree_k and tree_v are not of the descriptor's element type")
     _check("eagle_kvq_commit", load().eagle_kvq_commit(
         ctypes.byref(desc), *layers.addresses,
-        _ptr(n_acc, torch.int32, "n_acc"), _ptr(path, torch.int32, "path"), _ptr(seq_len, torch.int32, "seq_len"),
-        _ptr(commit_pos, torch.int32, "commit_pos"), _ptr(feat_cache, FLOATS, "feat_cache"),
-        _ptr(tree_feat, FLOATS, "tree_feat"), _ptr(status, torch.int32, "status"), _stream(stream)))
+        _at(n_acc, torch.int32, "n_acc", dev), _at(path, torch.int32, "path", dev),
+        _at(seq_len, torch.int32, "seq_len", dev), _at(commit_pos, torch.int32, "commit_pos", dev),
+        _at(feat_cache, FLOATS, "feat_cache", dev),
+        _at(tree_feat, FLOATS, "tree_feat", dev), _at(status, torch.int32, "status", dev), _stream(stream)))
 
 
 def eagle_tree_attn_kvq(desc: AttnDesc, q, k_codes, k_scale, v_codes, v_scale, tree_k, tree_v, seq_len, anc_mask,
@@ -493,14 +515,15 @@ def eagle_tree_attn_kvq(desc: AttnDesc, q, k_codes, k_scale, v_codes, v_scale, t
                         n_nodes: Optional[torch.Tensor] = None) -> None:
     """One layer of tree attention over the 8-bit cache (see eagle.h: eagle_tree_attn_kvq)."""
     bf16 = torch.bfloat16
-    _on_current(q, "q")
+    dev = _device()
     _check("eagle_tree_attn_kvq", load().eagle_tree_attn_kvq(
-        ctypes.byref(desc), _ptr(q, bf16, "q"), _ptr(k_codes, CODES, "k_codes"),
-        _ptr(k_scale, torch.float32, "k_scale"), _ptr(v_codes, CODES, "v_codes"),
-        _ptr(v_scale, torch.float32, "v_scale"), _ptr(tree_k, bf16, "tree_k"), _ptr(tree_v, bf16, "tree_v"),
-        _ptr(seq_len, torch.int32, "seq_len"), _ptr(n_nodes, torch.int32, "n_nodes"),
-        _ptr(anc_mask, torch.int64, "anc_mask"), _ptr(out, _element(desc.out_dtype), "out"),
-        _ptr(lse, torch.float32, "lse"), _ptr(ws, name="ws"), ws.numel() * ws.element_size(), _stream(stream)))
+        ctypes.byref(desc), _at(q, bf16, "q", dev), _at(k_codes, CODES, "k_codes", dev),
+        _at(k_scale, torch.float32, "k_scale", dev), _at(v_codes, CODES, "v_codes", dev),
+        _at(v_scale, torch.float32, "v_scale", dev), _at(tree_k, bf16, "tree_k", dev),
+        _at(tree_v, bf16, "tree_v", dev), _at(seq_len, torch.int32, "seq_len", dev),
+        _at(n_nodes, torch.int32, "n_nodes", dev), _at(anc_mask, torch.int64, "anc_mask", dev),
+        _at(out, _element(desc.out_dtype), "out", dev), _at(lse, torch.float32, "lse", dev),
+        _at(ws, ws.dtype, "ws", dev), ws.numel() * ws.element_size(), _stream(stream)))
 
 
 # ----------------------------------------------------------------------------- norms and rotation
@@ -509,10 +532,11 @@ def eagle_qk_norm_rope(desc: QkNormRopeDesc, qkv, q_weight: Optional[torch.Tenso
                        n_nodes: Optional[torch.Tensor] = None) -> None:
     """Norms of the query and key heads, rotation and tree layout (see eagle.h:
     eagle_qk_norm_rope)."""
-    _on_current(qkv, "qkv")
+    dev = _device()
     dt = _element(desc.dtype)
     _check("eagle_qk_norm_rope", load().eagle_qk_norm_rope(
-        ctypes.byref(desc), _ptr(qkv, dt, "qkv"), _ptr(q_weight, dt, "q_weight"), _ptr(k_weight, dt, "k_weight"),
-        _ptr(inv_freq, torch.float32, "inv_freq"), _ptr(pos_id, torch.int32, "pos_id"),
-        _ptr(n_nodes, torch.int32, "n_nodes"), _ptr(q, dt, "q"), _ptr(k, dt, "k"), _ptr(v, dt, "v"),
+        ctypes.byref(desc), _at(qkv, dt, "qkv", dev), _at(q_weight, dt, "q_weight", dev),
+        _at(k_weight, dt, "k_weight", dev),
+        _at(inv_freq, torch.float32, "inv_freq", dev), _at(pos_id, torch.int32, "pos_id", dev),
+        _at(n_nodes, torch.int32, "n_nodes", dev), _at(q, dt, "q", dev), _at(k, dt, "k", dev), _at(v, dt, "v", dev),
         _stream(stream)))
