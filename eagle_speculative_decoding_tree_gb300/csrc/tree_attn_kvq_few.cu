@@ -27,9 +27,10 @@
 //   a warp that issues every tcgen05.mma: QK0 QK1 | QK2 PV0 | QK3 PV1 | ...
 // (32 rows a thread instead of 16 take as many instructions, but at 2.5 warps a scheduler only
 // every second cycle issued one: 61.7 us against 58.0 for a chain of 8 over 128K.)
-// TMEM: S of the even and the odd tiles (hi | lo columns), then O likewise (a column per row and term).
+// TMEM: S of four tiles (hi | lo columns, or one), then O of the even and the odd tiles (a column per
+// row and term of P).
 // Measured (8 KV heads, 4 query heads each, graph replay): one token over 128K tokens 46 us (5.8
-// TB/s, 86 % of a device copy's rate), over 8K 9.7; a chain of 8 over 128K, fp32 and precise, 54 us
+// TB/s, 86 % of a device copy's rate), over 8K 9.7; a chain of 8 over 128K, fp32 and precise, 53.6 us
 // (the loop's waits and product issue take about as long a tile as HBM does).
 // Piece 0 is the tree (at most 32 bf16 keys), computed in fp32 on the ordinary cores; the others
 // are tps tiles of the prefix.  Pieces write fp32 partials, merged in the kernel when the grid
@@ -63,15 +64,20 @@ struct Few {
   static constexpr int SW = NR / 2;                 // softmax warps: NR / 16 x 2 warpgroups
   static constexpr int NT = SW * 32 + (NR == 32 ? 128 : 64);  // threads (setmaxnreg wants whole warpgroups)
   static constexpr int NP = NR * TERMS;             // O columns of a tile parity, bytes of a key's P
-  static constexpr int NS = 2 * NR;                 // S columns of a tile parity
+  // Q's terms: columns of their own in S, or twice as many products into the same ones.  The first for
+  // 16 rows (one token over 128K: 45.6 us, the second 46.2), the second for 32 (a chain of 8 over 8K 13.0
+  // us, the first 13.3; six terms of P leave TMEM no room for the first: 53.5, with two S buffers and a
+  // wait for each of them 54.5).
+  static constexpr bool ONE_S = NR == 32;
+  static constexpr int NS = ONE_S ? NR : 2 * NR;    // S columns of a tile
   static constexpr int ST = NR == 32 ? 5 : 6;       // ring stages
   static constexpr int SM_Q = 0;                    // hi rows, lo rows of 128 codes
-  static constexpr int SM_P = SM_Q + NS * 128;      // two buffers, blocks of 32 columns x 128 keys
+  static constexpr int SM_P = SM_Q + 2 * NR * 128;      // two buffers, blocks of 32 columns x 128 keys
   static constexpr int P1 = 128 * NP;
   static constexpr int SM_K = SM_P + 2 * P1;
   static constexpr int SM_V = SM_K + ST * T8;
   static constexpr int SMEM = SM_V + ST * T8 + 1024;
-  static_assert(P1 % 1024 == 0 && 2 * NS + 2 * NP <= 512, "alignment of the rings, TMEM columns");
+  static_assert(P1 % 1024 == 0 && 4 * NS + 2 * NP <= 512, "alignment of the rings, TMEM columns");
 };
 
 // Descriptor with the 32-byte swizzle (MN-major P: rows of 32 columns, 8 keys every `sbo` bytes,
@@ -184,7 +190,7 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
   constexpr int ST = F::ST, SW = F::SW, HALVES = NR / 16;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t full[ST], k_empty[ST], v_empty[ST], s_full[2], s_empty[2], p_full[2], p_empty[2], q_full, o_full;
+  __shared__ uint64_t full[ST], k_empty[ST], v_empty[ST], s_full[4], p_full[2], p_empty[2], q_full, o_full;
   __shared__ uint32_t tmem_base;
   __shared__ int go;
   // by tile parity:
@@ -209,9 +215,8 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
       mbar_init(&k_empty[s], 1);
       mbar_init(&v_empty[s], 1);
     }
+    for (int s = 0; s < 4; ++s) mbar_init(&s_full[s], 1);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&s_full[s], 1);
-      mbar_init(&s_empty[s], HALVES * 128);
       mbar_init(&p_full[s], HALVES * 128);
       mbar_init(&p_empty[s], 1);
     }
@@ -235,8 +240,8 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
   const bool tree = piece == 0 && RG > 0, work = n > 0;
   const size_t prow0 = (static_cast<size_t>(bh) * a.splits + piece) * a.rows_pad;
   const uint32_t tb = tmem_base;
-  auto col_s = [](int w) { return static_cast<uint32_t>(w * F::NS); };
-  auto col_o = [](int w) { return static_cast<uint32_t>(2 * F::NS + w * F::NP); };
+  auto col_s = [](int i) { return static_cast<uint32_t>((i & 3) * F::NS); };
+  auto col_o = [](int w) { return static_cast<uint32_t>(4 * F::NS + w * F::NP); };
 
   // the group's merge (request, KV head): an even share of its rows, a warp per row
   const int need = kvq_pieces(a, n_pref);
@@ -300,13 +305,16 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
       const uint64_t dv = smem_desc_sw128(smem_u32(smem + F::SM_V), T8, 1024);
       const uint64_t dp = desc_sw32(smem_u32(smem + F::SM_P), 4096, 256);
       auto qk = [&](int i) {
-        const int s = i % ST, w = i & 1;
+        // into the S of tile i - 4, which the softmax has read: its P came before PV(i - 4)
+        const int s = i % ST;
         if (!wait(&full[s], (i / ST) & 1, ERR_K)) return false;
         tc_fence_after();
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          mma8(tu + col_s(w), dk + s * (T8 >> 4) + ks * 2, dq + ks * 2, idesc8(0, 0, F::NS), ks > 0);
-        commit(&s_full[w]);
+        for (int term = 0; term < (F::ONE_S ? 2 : 1); ++term)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            mma8(tu + col_s(i), dk + s * (T8 >> 4) + ks * 2, dq + term * (NR * 8) + ks * 2, idesc8(0, 0, F::NS), term + ks > 0);
+        commit(&s_full[i & 3]);
         commit(&k_empty[s]);
         return true;
       };
@@ -324,10 +332,10 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
       };
       bool ok = wait(&q_full, 0, ERR_Q);
       ok = ok && qk(0) && (items < 2 || qk(1));
-      // the scores of a warpgroup's next tile as soon as it has read these, under its exponentials
+      // the scores of a warpgroup's next tile come under its exponentials
 #pragma unroll 1
       for (int i = 0; i < items && ok; ++i) {
-        if (i + 2 < items) ok = wait(&s_empty[i & 1], (i >> 1) & 1, ERR_S) && qk(i + 2);
+        if (i + 2 < items) ok = qk(i + 2);
         ok = ok && pv(i);
       }
       commit(&o_full);
@@ -419,21 +427,22 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
         const bool on = key < nv;
         // A warp whose wait gave up goes on without waiting (the error word is set, nothing is
         // written): the others of its warpgroup may still count on it at the barriers below.
-        ok = __all_sync(0xffffffffu, ok && wait_parity(&s_full[w], (i >> 1) & 1, a.err, ERR_S));
+        ok = __all_sync(0xffffffffu, ok && wait_parity(&s_full[i & 3], (i >> 2) & 1, a.err, ERR_S));
         tc_fence_after();
         // x = score - reference (log2 units) of this key and every row
         float x[16];
         auto scores = [&]() {
           uint32_t hi[16], lo[16];
-          tmem_ld16(lb + col_s(w) + g0, hi);
-          tmem_ld16(lb + col_s(w) + NR + g0, lo);
+          tmem_ld16(lb + col_s(i) + g0, hi);
+          if (!F::ONE_S) tmem_ld16(lb + col_s(i) + NR + g0, lo);
           tmem_ld_wait();
 #pragma unroll
           for (int r = 0; r < 16; r += 2) {
             const uint64_t c = *reinterpret_cast<const uint64_t*>(&s_c[g0 + r]);
             const uint64_t mu = *reinterpret_cast<const uint64_t*>(&s_mu[w][g0 + r]);
-            f32x2_split(fma_f32x2(add_f32x2(f32x2(hi[r], hi[r + 1]), f32x2(lo[r], lo[r + 1])), mul_f32x2(c, kc2), mu),
-                        x[r], x[r + 1]);
+            uint64_t sum = f32x2(hi[r], hi[r + 1]);
+            if (!F::ONE_S) sum = add_f32x2(sum, f32x2(lo[r], lo[r + 1]));
+            f32x2_split(fma_f32x2(sum, mul_f32x2(c, kc2), mu), x[r], x[r + 1]);
           }
           if (nv < KT) {
 #pragma unroll
@@ -487,8 +496,6 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
           }
           scores();  // against the new reference
         }
-        tc_fence_before();
-        mbar_arrive(&s_empty[w]);
         // P: 16 bytes of every term
         const uint64_t back2 = twice(ex2(-lr));
         uint32_t hh[8], ll[8];
