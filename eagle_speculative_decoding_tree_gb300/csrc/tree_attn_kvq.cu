@@ -622,9 +622,9 @@ cudaError_t launch_mma(const KvqAttnPlan& p, const Maps& tm, const KvqAttnArgs& 
 // request's own length out evenly, so that a capacity far above the lengths in use leaves no CTA
 // idle; or fixed pieces.  The lengths are not known here, so each choice is judged by two cases
 // together: all requests of full length (waves of equal CTAs), and lengths spread evenly (the
-// mean work, and a tail of most of a piece).  Measured: 8 requests of 1K to 16K x 8 heads 94 to
-// 112 us with 3 to 8 pieces, 128 with 2, 228 in one wave; 32 such 275 us with 3 or 4, 299 with 6;
-// 4 requests of 32K 131 us with 9, 147 with 11, 163 in one wave; one of 8K 21 us in one wave.
+// mean work, and a tail of most of a piece).  Measured: 8 requests of 1K to 16K x 8 heads 88 to
+// 102 us with 3 to 8 pieces, 120 with 2, 210 with 1; 32 such 253 to 255 us with 3 or 4, 261 with 2,
+// 276 with 6; 32 of 8K each 260 us with the 2 taken here, 241 with 1; one of 8K 18.8 us in one wave.
 // The plan's cost, in tiles' time, in *cost.
 static long long choose_pieces(long long base, int tiles, int num_sms, int extra, bool* even, double* cost) {
   const long long one = std::min<long long>(num_sms / base - 1, tiles);
