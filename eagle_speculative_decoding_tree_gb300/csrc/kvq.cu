@@ -267,9 +267,8 @@ __global__ void __launch_bounds__(256) kvq_read_kernel(const eagle_kvq_desc d, c
     const long long c = c0 + u * 256;
     if (c >= total) continue;
     const float2 a = kvq_float2(w[u].x), e = kvq_float2(w[u].x >> 16);
-    // a scale of 0 marks a block of zeros, whatever its codes
     const float z = s[u];
-    auto val = [&](float code) { return z > 0.f ? code * z : 0.f; };
+    auto val = [&](float code) { return code * z; };  // (a NaN code under any scale, 0 too, is NaN)
     if (F32) {
       reinterpret_cast<float4*>(dst)[c] = make_float4(val(a.x), val(a.y), val(e.x), val(e.y));
     } else {

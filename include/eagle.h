@@ -501,7 +501,8 @@ int eagle_kv_commit(const eagle_commit_desc* d, void* const* k_cache_layers, voi
  * values; 0 for a block of zeros, >= 2^-126), so a stored value is the nearest e4m3 multiple of s
  * and an error of at most 2^-4 of the value, or 2^-10 s where it is small.  A value that
  * is not finite is stored as NaN.  eagle_tree_attn_kvq and eagle_kvq_read take any finite
- * scale >= 0 (0: the block is zeros). */
+ * scale >= 0.  Under 0, the scale of a block without a finite value but zeros, NaN codes are
+ * NaN and all others 0. */
 #define EAGLE_KVQ_BLOCK 64
 
 typedef struct {
