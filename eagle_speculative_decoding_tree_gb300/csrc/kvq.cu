@@ -120,8 +120,8 @@ __device__ __forceinline__ uint2 chunk_codes(const Chunk<T>& x, float inv, bool 
                     code2_of_finite(f[4], f[5]) | (code2_of_finite(f[6], f[7]) << 16));
 }
 
-// The rows [base, lo) that stay in a block whose scale grew, ratio = old scale / new, by threads
-// tid of n.
+// The rows [base, lo) that stay in a block whose scale grew, ratio = old scale / new (0 for rows
+// under a scale of 0: whatever their finite codes, they are zeros), by threads tid of n.
 __device__ __forceinline__ void move_rows(uint8_t* codes, int D, int base, int lo, float ratio, int tid, int n) {
   uint2* old = reinterpret_cast<uint2*>(codes + static_cast<size_t>(base) * D);
   for (int c = tid; c < (lo - base) * (D / 8); c += n) {
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kWriteThreads) kvq_write_kernel(const eagle_kv
         m = reduce(m);
       }
       const float s = fmaxf(kvq_scale(__uint_as_float(m)), s_old), inv = kvq_inverse(s);
-      if (s > s_old && s_old > 0.f) move_rows(cur.codes, d.head_dim, cur.base, cur.lo, s_old * inv, threadIdx.x, kWriteThreads);
+      if (s > s_old && cur.lo > cur.base) move_rows(cur.codes, d.head_dim, cur.base, cur.lo, s_old * inv, threadIdx.x, kWriteThreads);
       const int total = (cur.hi - cur.lo) * (d.head_dim / 8);
       uint2* dst = reinterpret_cast<uint2*>(cur.codes + static_cast<size_t>(cur.lo) * d.head_dim);
 #pragma unroll
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(128) kvq_commit_kernel(const eagle_commit_desc
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       s[w] = fmaxf(kvq_scale(__uint_as_float(m[w])), s_old[w]);
-      if (s[w] > s_old[w] && s_old[w] > 0.f) move_rows(codes[w], D, base, lo, s_old[w] * kvq_inverse(s[w]), lane, 32);
+      if (s[w] > s_old[w] && lo > base) move_rows(codes[w], D, base, lo, s_old[w] * kvq_inverse(s[w]), lane, 32);
     }
     for (int g = rounds - 1; g >= 0; --g) {  // (the last round's rows are still in registers)
       if (g < rounds - 1) fetch(g * round);

@@ -71,3 +71,25 @@ def test_rows_without_a_finite_value_read_back_as_nan(D, how, dtype, odt):
     y = np.full((2, 5, D), 3.0)
     put(how, D, P, dev, y, 64 + n, dtype)
     assert same(read(D, P, dev, 64, n + 5, odt), np.concatenate((want, y), 1))
+
+
+@pytest.mark.parametrize("how", ["write", "commit"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_rows_under_a_scale_of_zero_stay_zeros_when_it_grows(D, how):
+    """A cache whose block has a scale of 0 and codes that are not 0 (another writer's): zeros, also
+    behind an append that gives the block a scale; NaN codes stay NaN."""
+    P = 128
+    g = np.random.default_rng(3)
+    codes = g.integers(0, 126, (1, 3, P, D)).astype(np.uint8)
+    codes[0, 2, 4] = 0x7f
+    dev = [torch.from_numpy(codes.copy()).cuda(), torch.zeros(1, 3, 2, device="cuda")]
+    dev += [y.clone() for y in dev]
+    want = np.zeros((3, 10, D))
+    want[2, 4] = np.nan
+    assert same(read(D, P, dev, 0, 10, "f32"), want)
+    y = np.full((3, 6, D), 3.0)
+    y[1] = 0.0  # no scale for this head
+    put(how, D, P, dev, y, 10, "bf16")
+    got = read(D, P, dev, 0, 16, "f32")
+    assert same(got, np.concatenate((want, y), 1))
+    assert same(values(dev)[:, :16], got)
