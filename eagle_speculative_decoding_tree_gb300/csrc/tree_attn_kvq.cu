@@ -11,7 +11,8 @@
 //     [2^14, 2^15): bf16 to half is then exact down to 2^-39 of that element;
 //   - ks multiplies the scores of its block (fp32);
 //   - vs / vref, vref the largest vs of the CTA's key range, goes into the exponent of P, so
-//     one accumulator serves blocks of different scales; the row sum takes it out again.
+//     one accumulator serves blocks of different scales; the row sum takes it out again.  (Where
+//     the tree shares it, its V gets a scale as a cache block's would be.)
 //     P <= 2^15 in half: 11 significant bits down to 2^-25 of the largest p, steps of 2^-35
 //     of it below.
 // The reference maximum is kept in log2 units and rounded up to an integer, so that with
@@ -162,6 +163,7 @@ __global__ void __launch_bounds__(CW * 32, 1)
   uint8_t* sq = ring + nst * 2 * TILE;
   __shared__ uint64_t full[MAX_ST], empty[MAX_ST];
   __shared__ float s_qs[CW * 16], s_m[CW][16], s_l[CW][16], s_vr[CW];
+  __shared__ uint32_t s_tv[CW];
   __shared__ int go;
 
   const int rb = blockIdx.x, split = blockIdx.y, bh = blockIdx.z;
@@ -204,11 +206,28 @@ __global__ void __launch_bounds__(CW * 32, 1)
   int issued = 0;  // thread 0: tiles whose loads have gone out; the first before anything else is read
   if (threadIdx.x == 0)
     for (; issued < min(n_pt, nst); ++issued) load_tile(issued);
-  // vref: the largest V scale of the key range
+  // vref: the largest V scale of the key range; the tree's is chosen as a cache block's (vt)
   float vm = 0.f;
   for (int i = threadIdx.x; i < n_blk; i += CW * 32) vm = fmaxf(vm, __ldg(vs + i));
+  uint32_t tm_bits = 0;  // the largest finite magnitude of the tree's V, as float bits
+  if (tree) {
+    const uint4* tvg = reinterpret_cast<const uint4*>(a.tv + static_cast<size_t>(bh) * a.R * D);
+    for (int i = threadIdx.x; i < Rb * (D / 8); i += CW * 32) {
+      const uint4 x = __ldg(tvg + i);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t p0 = (w[e] << 16) & 0x7fff0000u, p1 = w[e] & 0x7fff0000u;
+        tm_bits = max(tm_bits, max(p0 < 0x7f800000u ? p0 : 0u, p1 < 0x7f800000u ? p1 : 0u));
+      }
+    }
+  }
   vm = warp_max(vm);
-  if (lane == 0) s_vr[warp] = vm;
+  tm_bits = __reduce_max_sync(0xffffffffu, tm_bits);
+  if (lane == 0) {
+    s_vr[warp] = vm;
+    s_tv[warp] = tm_bits;
+  }
 
   // Q rows as scaled halves: row r, element e at r * stride + 2 e
   for (int r = warp; r < rows_cta; r += CW) {
@@ -242,8 +261,14 @@ __global__ void __launch_bounds__(CW * 32, 1)
   }
   __syncthreads();
   float vref = s_vr[0];
+  uint32_t tv_max = s_tv[0];
 #pragma unroll
-  for (int w = 1; w < CW; ++w) vref = fmaxf(vref, s_vr[w]);
+  for (int w = 1; w < CW; ++w) {
+    vref = fmaxf(vref, s_vr[w]);
+    tv_max = max(tv_max, s_tv[w]);
+  }
+  const float vt = kvq_scale(__uint_as_float(tv_max));
+  vref = fmaxf(vref, vt);
   if (!(vref > 0.f)) vref = 1.f;
   const float vinv = 1.f / vref;
 
@@ -399,7 +424,15 @@ __global__ void __launch_bounds__(CW * 32, 1)
       qp[i] = a.q + ((static_cast<size_t>(b) * a.R + node) * a.Hq + hq) * D + 16 * c;
       mp[i] = a.anc_mask + (static_cast<size_t>(b) * a.R + node) * a.W;
     }
-    const float lr = PB - __log2f(vref);
+    // V enters as v / vt (a power of two: exact in bf16 down to 2^-126 of the largest), at most 448
+    // like a code: with V as it is P would have to hold 1 / vref, beyond fp32 for tiny scales.
+    const float lr = fmaxf(__log2f(vt * vinv), -100.f) + PB;
+    const __nv_bfloat162 vti = __float2bfloat162_rn(kvq_inverse(vt));
+    auto scaled = [&](uint2 u) {
+      const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&u.x), vti);
+      const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&u.y), vti);
+      return make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+    };
     for (int step = wkey; step * 16 < Rb; step += wk) {
       float sc[2][4];
 #pragma unroll
@@ -447,7 +480,7 @@ __global__ void __launch_bounds__(CW * 32, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int key = step * 16 + (i >> 1) * 8 + 2 * c + (i & 1);
-          w[i] = key < Rb ? *reinterpret_cast<const uint2*>(vb + static_cast<size_t>(key) * D + VB * g + 4 * q)
+          w[i] = key < Rb ? scaled(*reinterpret_cast<const uint2*>(vb + static_cast<size_t>(key) * D + VB * g + 4 * q))
                           : make_uint2(0u, 0u);
         }
 #pragma unroll
