@@ -28,6 +28,10 @@ __device__ __forceinline__ float kvq_scale(float amax) {
 // 1 / s for a power-of-two scale (1 for the scale of a block of zeros).
 __device__ __forceinline__ float kvq_inverse(float s) { return s > 0.f ? 1.f / s : 1.f; }
 
+// The V scale that an accumulator's others refer to: the largest of its keys, at least the
+// smallest normal number (its inverse is finite then).
+__device__ __forceinline__ float kvq_vref(float largest) { return fmaxf(largest, 0x1p-126f); }
+
 // Two floats to e4m3 codes, nearest even, `lo` in the low byte.  A value that is not finite
 // becomes the NaN code: it must not read back as an ordinary number.
 __device__ __forceinline__ uint32_t kvq_code2(float lo, float hi) {

@@ -268,8 +268,7 @@ __global__ void __launch_bounds__(CW * 32, 1)
     tv_max = max(tv_max, s_tv[w]);
   }
   const float vt = kvq_scale(__uint_as_float(tv_max));
-  vref = fmaxf(vref, vt);
-  if (!(vref > 0.f)) vref = 1.f;
+  vref = kvq_vref(fmaxf(vref, vt));
   const float vinv = 1.f / vref;
 
   bool ok = true;
@@ -516,7 +515,7 @@ __global__ void __launch_bounds__(CW * 32, 1)
         *reinterpret_cast<float4*>(so + (g + 8 * i) * D + ((((VB * (2 * c + e) + j) >> 2) ^ g) << 2)) =
             make_float4(st.o[j][2 * i + e], st.o[j + 1][2 * i + e], st.o[j + 2][2 * i + e], st.o[j + 3][2 * i + e]);
   __syncthreads();
-  const float unit = vref * (1.f / (1 << PB));
+  const float unit = vref * (1.f / (1 << PB));  // (not into 1 / lsum: for the smallest vref that has few bits)
   constexpr int QD = D / 4;  // threads of a row, 4 dims each
   for (int idx = threadIdx.x; idx < rows_cta * QD; idx += CW * 32) {
     const int r = idx / QD, q = idx % QD;
@@ -542,14 +541,14 @@ __global__ void __launch_bounds__(CW * 32, 1)
           make_float4(acc.x * unit, acc.y * unit, acc.z * unit, acc.w * unit);
       if (q == 0) *reinterpret_cast<float2*>(a.part_ml + prow * 2) = make_float2(M, lsum);
     } else {
-      const float inv = lsum == 0.f ? 0.f : unit / lsum;  // a row whose mask leaves nothing: zeros, lse -inf
+      const float inv = lsum == 0.f ? 0.f : 1.f / lsum;  // a row whose mask leaves nothing: zeros, lse -inf
+      acc = make_float4(acc.x * inv * unit, acc.y * inv * unit, acc.z * inv * unit, acc.w * inv * unit);
       const size_t orow = (static_cast<size_t>(b) * a.R + row / a.G) * a.Hq + h * a.G + row % a.G;
       if (a.out_f32)
-        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow * D + 4 * q) =
-            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow * D + 4 * q) = acc;
       else
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + 4 * q) =
-            make_uint2(pack_bf(acc.x * inv, acc.y * inv), pack_bf(acc.z * inv, acc.w * inv));
+            make_uint2(pack_bf(acc.x, acc.y), pack_bf(acc.z, acc.w));
       if (a.lse && q == 0) a.lse[orow] = (M + log2f(lsum)) * 0.69314718055994531f;
     }
   }

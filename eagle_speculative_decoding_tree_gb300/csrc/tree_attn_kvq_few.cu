@@ -364,8 +364,7 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
       float vref = 0.f;
 #pragma unroll 4
       for (int i = lane; i < n_blk; i += 32) vref = fmaxf(vref, __ldg(vs + i));
-      vref = warp_max(vref);
-      if (!(vref > 0.f)) vref = 1.f;
+      vref = kvq_vref(warp_max(vref));
       const float vinv = 1.f / vref;
       if (threadIdx.x < NR * 8) {
         const uint32_t u[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};

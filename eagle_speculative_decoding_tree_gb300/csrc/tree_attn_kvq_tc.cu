@@ -548,8 +548,7 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
         float m = 0.f;
 #pragma unroll 4
         for (int i = lane; i < n_blk; i += 32) m = fmaxf(m, __ldg(vs + i));
-        m = warp_max(m);
-        if (m > 0.f) vref = m;
+        vref = kvq_vref(warp_max(m));
       }
       const float vinv = 1.f / vref;
       // (orders every warp's s_q; a query tile that never came shows at the first scores)

@@ -100,3 +100,17 @@ def test_tiny_v_scales_beside_a_tree(kern, vs, splits):
     settle(c)
     for precise in (False, True):
         check(c, c.desc(True, precise, splits, engine), few_rows(kern))
+
+
+@pytest.mark.parametrize("vs", [-128, -130, -140])
+@pytest.mark.parametrize("kern", KERNELS, ids=name)
+def test_v_scales_below_the_normal_numbers(kern, vs):
+    """Another writer's scales (any finite one is taken); 2^-149 is fp32's smallest step, and a row
+    is rounded to it a few times."""
+    R, Hq, Hkv, D, engine = kern
+    c = Case(52, 1, R, Hq, Hkv, D, 200, [200])
+    c.scale[1][:] = 2.0 ** vs
+    c.tv = torch.zeros_like(c.tv)
+    settle(c)
+    for splits in (0, 1):
+        check(c, c.desc(True, True, splits, engine), few_rows(kern), tiny=2.0 ** -146)
