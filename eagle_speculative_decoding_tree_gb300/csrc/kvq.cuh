@@ -32,6 +32,28 @@ __device__ __forceinline__ float kvq_inverse(float s) { return s > 0.f ? 1.f / s
 // smallest normal number (its inverse is finite then).
 __device__ __forceinline__ float kvq_vref(float largest) { return fmaxf(largest, 0x1p-126f); }
 
+// log2 of a key's V scale against vref, what its P carries in the exponent.  At least -100, so that
+// row sums of p = P 2^-ld stay in fp32: a smaller scale counts as 2^-100 vref.
+__device__ __forceinline__ float kvq_ld(float vs, float vinv) { return fmaxf(__log2f(vs * vinv), -100.f); }
+
+// A row's reference follows the largest score + kvq_toward(ld), not the largest score alone: P's
+// largest is then within 2^4 of what weighs most in the sum of P V, however small its V scale is
+// against the others of the piece, and P's fewer bits cut only what is small against that.  (With
+// the largest score alone, keys with all the weight under a scale of 2^-32 vref came out with four
+// bits or none.)  Scales within 2^4 of vref, as in ordinary caches, do not move it: following ld all
+// the way made the references move more often there, 120 against 112 us for 61 nodes over 128K.
+__device__ __forceinline__ float kvq_toward(float ld) { return fminf(ld + 4.f, 0.f); }
+
+// A row sum far above its reference, as where the weight is under small V scales, brought below
+// 2^18 by moving the reference (log2 units) up: the factor for what else refers to it.
+__device__ __forceinline__ float kvq_settle(float& m, float& l) {
+  const int e = max(static_cast<int>(__float_as_uint(l) >> 23) - (127 + 17), 0);
+  const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+  m += static_cast<float>(e);
+  l *= f;
+  return f;
+}
+
 // Two floats to e4m3 codes, nearest even, `lo` in the low byte.  A value that is not finite
 // becomes the NaN code: it must not read back as an ordinary number.
 __device__ __forceinline__ uint32_t kvq_code2(float lo, float hi) {

@@ -13,8 +13,8 @@
 //   - vs / vref, vref the largest vs of the CTA's key range, goes into the exponent of P, so
 //     one accumulator serves blocks of different scales; the row sum takes it out again.  (Where
 //     the tree shares it, its V gets a scale as a cache block's would be.)
-//     P <= 2^15 in half: 11 significant bits down to 2^-25 of the largest p, steps of 2^-35
-//     of it below.
+//     P <= 2^15 in half: 11 significant bits down to 2^-24 of the row's largest p, steps of 2^-34
+//     of it below, or 2^4 times as much of the largest p vs where that is less (kvq_toward).
 // The reference maximum is kept in log2 units and rounded up to an integer, so that with
 // power-of-two scales every exponent offset is exact.
 //
@@ -53,7 +53,7 @@ constexpr int KT = 128;       // keys per tile
 constexpr int MAX_ST = 6;     // ring stages: 6 up to 64 rows a CTA, 4 beyond (the query rows' space)
 constexpr int CW = 16;        // warps
 // A row's reference moves when its maximum grew by more than 2^kLazy, and P is stored as
-// p 2^PB <= 2^15: a half's smallest step then is 2^-35 of the largest p.  A larger kLazy saves
+// p 2^PB vs / vref <= 2^15: a half's smallest step then is 2^-34 of the largest p.  A larger kLazy saves
 // rescales, which are rare already at 2^4, and costs that range.
 constexpr float kLazy = 4.f;
 constexpr int PB = 11;
@@ -103,18 +103,18 @@ struct RowState {
   float m[2], l[2];
 };
 
-// Scores t (log2 units, masked -inf) of 16 keys: moves the reference maxima if they must, turns
-// t into p 2^lr (in place) and adds the row sums.
+// Scores t (log2 units, masked -inf) of 16 keys: moves the references if they must (see kvq_toward),
+// turns t into P = p 2^(ld + PB) (in place) and adds the row sums.
 template <int D>
-__device__ __forceinline__ void soften(RowState<D>& st, float (&t)[2][4], float lr) {
-  const float back = ex2(-lr);
+__device__ __forceinline__ void soften(RowState<D>& st, float (&t)[2][4], float ld) {
+  const float lr = ld + PB, back = ex2(-lr), toward = kvq_toward(ld);
   float m_new[2];
   bool move = false;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     float mx = fmaxf(fmaxf(t[0][2 * i], t[0][2 * i + 1]), fmaxf(t[1][2 * i], t[1][2 * i + 1]));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) + toward;
     const bool up = mx > st.m[i] + kLazy || (st.m[i] == -INFINITY && mx > -INFINITY);
     m_new[i] = up ? ceilf(mx) : st.m[i];
     move |= up;
@@ -339,8 +339,7 @@ __global__ void __launch_bounds__(CW * 32, 1)
           sc[j][e] *= cr[e >> 1] * ksb;
           if (nk < 16 && 8 * j + cs + 4 * (e & 1) >= nk) sc[j][e] = -INFINITY;
         }
-      const float lr = fmaxf(__log2f(vsb * vinv), -100.f) + PB;
-      soften<D>(st, sc, lr);
+      soften<D>(st, sc, kvq_ld(vsb, vinv));
       uint32_t pa[4], pl[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -425,7 +424,7 @@ __global__ void __launch_bounds__(CW * 32, 1)
     }
     // V enters as v / vt (a power of two: exact in bf16 down to 2^-126 of the largest), at most 448
     // like a code: with V as it is P would have to hold 1 / vref, beyond fp32 for tiny scales.
-    const float lr = fmaxf(__log2f(vt * vinv), -100.f) + PB;
+    const float ld = kvq_ld(vt, vinv);
     const __nv_bfloat162 vti = __float2bfloat162_rn(kvq_inverse(vt));
     auto scaled = [&](uint2 u) {
       const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&u.x), vti);
@@ -461,7 +460,7 @@ __global__ void __launch_bounds__(CW * 32, 1)
             sc[j][2 * i + e] = on ? sc[j][2 * i + e] * a.scale_log2 : -INFINITY;
           }
       }
-      soften<D>(st, sc, lr);
+      soften<D>(st, sc, ld);
       uint32_t pt[3][4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -535,6 +534,8 @@ __global__ void __launch_bounds__(CW * 32, 1)
       acc.x = fmaf(f, x.x, acc.x), acc.y = fmaf(f, x.y, acc.y);
       acc.z = fmaf(f, x.z, acc.z), acc.w = fmaf(f, x.w, acc.w);
     }
+    const float back = kvq_settle(M, lsum);
+    acc.x *= back, acc.y *= back, acc.z *= back, acc.w *= back;
     if (a.splits > 1) {
       const size_t prow = (static_cast<size_t>(bh) * a.splits + split) * a.rows_pad + row;
       *reinterpret_cast<float4*>(a.part_o + prow * D + 4 * q) =

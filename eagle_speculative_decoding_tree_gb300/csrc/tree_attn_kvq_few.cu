@@ -10,15 +10,15 @@
 //   q  as in tree_attn_kvq_tc.cu: a power of two puts a row's largest element in (224, 448], and
 //      q = hi + lo in e4m3 keeps bf16's bits down to elements of 2^-11 of it;
 //   p  2^PB vs / vref is rounded to a half (11 bits) and that half is written as four e5m2 terms
-//      of three bits each, exactly down to steps of 2^-30 of the largest p (the rest after the
+//      of three bits each, exactly down to steps of 2^-29 of the largest p (the rest after the
 //      first term is multiplied by 8, past e5m2's smallest steps).  EAGLE_ATTN_PRECISE: two more
 //      terms of what the half left (2^-17 of p).  A term is the upper byte of what is left of the
 //      half, cut off, and rounded for the last of them and PRECISE's: integer instructions
 //      (conversions to e5m2: 58.0 against 56.8 us for the chain of 8 over 128K).  The terms are
 //      columns of their own; their scales meet in the epilogue, in fp32.
 // A row's running maximum would need every key's score; instead the exponentials are taken
-// against a reference that moves (a slow path through shared memory) when some score is more than
-// 2^kLazy above it, which a vote of the tile's threads finds out.
+// against a reference that moves (a slow path through shared memory) when some score (a small V scale
+// counted in: kvq_toward) is more than 2^kLazy above it, which a vote of the tile's threads finds out.
 //
 // One CTA per (piece, request x KV head):
 //   softmax warpgroups, two for every 16 rows: a thread is one key of the tile (a TMEM lane) for
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
       for (int r = 0; r < 8; ++r) l2[r] = 0ull;
       bool ok = true;
       for (int i = w; i < n; i += 2) {
-        const float kc = kn, lr = fmaxf(__log2f(vn * vinv), -100.f) + PB;
+        const float kc = kn, ld = kvq_ld(vn, vinv), lr = ld + PB;
         fetch(min(i + 2, n - 1));
         const uint64_t kc2 = twice(kc), lr2 = twice(lr);
         const int nv = min(KT, L - (tile0 + i) * KT);
@@ -453,14 +453,14 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
 #pragma unroll
         for (int r = 0; r < 16; r += 2) over = max3(over, x[r], x[r + 1]);
         // (a NaN score does not raise `over`: it spoils its row whatever the reference)
-        const bool fits = bar_and(vote, 128, over <= kLazy);
+        const bool fits = bar_and(vote, 128, over + kvq_toward(ld) <= kLazy);
         // P's buffer and O: free once the product of this parity's tile before has finished
         ok = __all_sync(0xffffffffu, ok && (i < 2 || wait_parity(&p_empty[w], ((i >> 1) - 1) & 1, a.err, ERR_P)));
         if (!fits) {
           int mine = 0;
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
-            const int m = __reduce_max_sync(0xffffffffu, ordered(x[r] == x[r] ? x[r] : -INFINITY));
+            const int m = __reduce_max_sync(0xffffffffu, ordered(x[r] == x[r] ? x[r] + kvq_toward(ld) : -INFINITY));
             if (lane == r) mine = m;
           }
           if (lane < 16) s_red[w][qd][g0 + lane] = unordered(mine);
@@ -587,13 +587,15 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
         if (w == 0 && key < 16) {  // a row's weights of the two parities, its maximum and sum
           const int r = g0 + key;
           const float m0 = s_m[0][r], m1 = two ? s_m[1][r] : -INFINITY;
-          const float M = fmaxf(m0, m1);
+          float M = fmaxf(m0, m1);
           const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - M), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M);
-          s_al[0][r] = f0;
-          s_al[1][r] = f1;
           const float l0 = (s_red[0][0][r] + s_red[0][1][r]) + (s_red[0][2][r] + s_red[0][3][r]);
           const float l1 = (s_red[1][0][r] + s_red[1][1][r]) + (s_red[1][2][r] + s_red[1][3][r]);
-          if (r < RG) *reinterpret_cast<float2*>(a.part_ml + (prow0 + r) * 2) = make_float2(M, fmaf(f0, l0, f1 * l1));
+          float l = fmaf(f0, l0, f1 * l1);
+          const float back = kvq_settle(M, l);
+          s_al[0][r] = f0 * back;
+          s_al[1][r] = f1 * back;
+          if (r < RG) *reinterpret_cast<float2*>(a.part_ml + (prow0 + r) * 2) = make_float2(M, l);
         }
         bar_sync(5, SW * 32);
         if (w == 0) {

@@ -580,12 +580,13 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
       if (!r.tree) fetch(min(tile_of(w), r.n - 1));
       for (int i = w; i < items; i += 2) {
         const int t = tile_of(i);
-        float ck[2] = {cr, cr}, lr[2] = {PB, PB};
+        float ck[2] = {cr, cr}, lr[2] = {PB, PB}, to[2] = {0.f, 0.f};
         if (!r.tree) {
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             ck[u] = cr * kn[u];
-            lr[u] = fmaxf(__log2f(vn[u] * vinv), -100.f) + PB;
+            lr[u] = kvq_ld(vn[u], vinv) + PB;
+            to[u] = kvq_toward(lr[u] - PB);
           }
           fetch(min(tile_of(i + 2), r.n - 1));
         }
@@ -610,14 +611,14 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
           float mx = max32(x);
           float s0 = to_half(x, p0, 0, ck[0], lr[0] - mu);
           tmem_ld32(sc + 64, x);
-          mx = fmaxf(mx, max32(y)) * ck[0];
+          mx = fmaf(fmaxf(mx, max32(y)), ck[0], to[0]);
           s0 += to_half(y, p0, 16, ck[0], lr[0] - mu);
           tmem_ld_wait();
           tmem_ld32(sc + 96, y);
           float mz = max32(x);
           float s1 = to_half(x, p1, 0, ck[1], lr[1] - mu);
           tmem_ld_wait();
-          mz = fmaxf(mz, max32(y)) * ck[1];
+          mz = fmaf(fmaxf(mz, max32(y)), ck[1], to[1]);
           s1 += to_half(y, p1, 16, ck[1], lr[1] - mu);
           const float top = fmaxf(mx, mz);
           if (!__any_sync(0xffffffffu, !(top <= m_ref + kLazy))) {
@@ -647,7 +648,7 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
             }
           }
           const float mx = fmaxf(max32(x), max32(y));
-          if (mx != -INFINITY) top = fmaxf(top, mx * (u ? ck[1] : ck[0]));
+          if (mx != -INFINITY) top = fmaxf(top, fmaf(mx, u ? ck[1] : ck[0], u ? to[1] : to[0]));
         }
         const bool up = top > m_ref + kLazy || (m_ref == -INFINITY && top > -INFINITY);
         const bool scale_o = up && m_ref != -INFINITY;
@@ -709,6 +710,9 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
           fa *= unit;
           fb *= unit;
         }
+        const float back = kvq_settle(M, Lsum);
+        fa *= back;
+        fb *= back;
         // slices of 32 dims staged as 128-byte-swizzled rows over the Q area and both code
         // rings (every product has finished), then one TMA store each
         for (int c = two ? 0 : 2 * w; c < (two ? 4 : 2 * w + 2); ++c) {

@@ -279,10 +279,12 @@ int eagle_tree_attn_plan(const eagle_attn_desc* d, int32_t* splits, int32_t* ker
  *   precision  EAGLE_ATTN_FAST: P enters the product with the prefix values with 11 significant
  *              bits (a half): an error of 2^-11 of sum p |v| at most, an eighth of a bf16
  *              output's own rounding.  EAGLE_ATTN_PRECISE: with 17 or more, an error of 2^-17.
- *              Either way p below 2^-30 of the row's largest may be rounded to nothing.  The
- *              tree's part is precise in both: P with 22 bits or more; elements of tree_v below
- *              2^-32 of their request's and head's largest may be rounded, to steps of 2^-39 of
- *              that one.  Scores, softmax and sums are fp32.
+ *              Either way a key may be rounded to nothing if its p times its V scale is below
+ *              2^-30 of the row's largest p times the head's largest V scale, and below 2^-26 of
+ *              the row's largest p times V scale.  V scales below 2^-100 of the head's largest
+ *              count as that.  The tree's part is precise in both: P with 22 bits or more;
+ *              elements of tree_v below 2^-32 of their request's and head's largest may be
+ *              rounded, to steps of 2^-39 of that one.  Scores, softmax and sums are fp32.
  * ws: eagle_workspace_size(EAGLE_WS_TREE_ATTN_KVQ, d) bytes, zero-filled before its first
  * use; one workspace serves one stream at a time, and any descriptors in turn that it is large
  * enough for.  Its first 4 bytes are an error word as in eagle_tree_attn.

@@ -9,10 +9,10 @@ two terms of their own:
             2^-10 or less: 2^-14 / 224 < 2^-21.  PRECISE: the largest in (28672, 57344], the last
             term in steps of 2^-16: 2^-17 / 28672 < 2^-31.  mma.sync: halves with the largest at or
             above 2^14, in steps of 2^-24: 2^-25 / 2^14 = 2^-39
-  weight    P is stored as p vs / vref 2^c with c such that the row's largest p vs is at least 2^10
-            there; its smallest step is 2^-24 (few rows, head_dim 128: 2^-19), half of which is 2^-35
-            (2^-30) of the largest p vs = `top`: n keys of codes up to 448 are off by
-            n 2^-35 448 top (n 2^-30 448 top) in all, whatever the other scales of the piece
+  weight    P is stored as p vs / vref 2^c with c such that the row's largest p vs is at least 2^6
+            there; its smallest step is 2^-24 (few rows, head_dim 128: 2^-19), half of which is 2^-31
+            (2^-26) of the largest p vs = `top`: n keys of codes up to 448 are off by
+            n 2^-31 448 top (n 2^-26 448 top) in all, whatever the other scales of the piece
 """
 import math
 
@@ -73,7 +73,7 @@ def check(c, d, few, dq=0.0, tiny=1e-37):
     ds = 2 * (D + 10) * U * reach + dq * np.abs(f(c.q)).max(-1) * most / math.sqrt(D)
     p_round = 2.0 ** -16 + (2.0 ** -21 if d.precision == B.EAGLE_ATTN_PRECISE else 2.0 ** -11)
     rel = (2 * ds + 2.0 ** -21 + p_round + 4 * U * n)[..., None]
-    floor = (n * (2.0 ** -30 if few else 2.0 ** -35) * 448 * weighted_top(c))[..., None]
+    floor = (n * (2.0 ** -26 if few else 2.0 ** -31) * 448 * weighted_top(c))[..., None]
     tol = rel * mass + floor + (2.0 ** -8 if d.out_dtype == B.EAGLE_BF16 else 2.0 ** -24) * np.abs(ref) + tiny
     assert np.isfinite(o).all() and np.isfinite(ls).all()
     worst = (np.abs(o - ref) / tol).max()
@@ -114,3 +114,42 @@ def test_v_scales_below_the_normal_numbers(kern, vs):
     settle(c)
     for splits in (0, 1):
         check(c, c.desc(True, True, splits, engine), few_rows(kern), tiny=2.0 ** -146)
+
+
+@pytest.mark.parametrize("first", [True, False], ids=["first", "last"])
+@pytest.mark.parametrize("ratio", [14, 24, 32, 60, 90])
+@pytest.mark.parametrize("kern", KERNELS, ids=name)
+def test_the_heavy_keys_scale_is_far_below_another_one(kern, ratio, first):
+    """One block of keys has all the weight and a V scale 2^-ratio of the others'; the heads of odd
+    index look away from it, at the others."""
+    R, Hq, Hkv, D, engine = kern
+    L = 320
+    c = Case(53, 1, R, Hq, Hkv, D, L, [L])
+    g = np.random.default_rng(54)
+    u = np.sign(g.normal(size=D))
+    a = 2.0 if ratio <= 32 else (3.0 if ratio <= 60 else 4.0)  # weights apart by 2^(2 a sqrt(D) / ln 2)
+    a *= 128 // D
+    sign = np.where(np.arange(Hq) % 2 == 0, 1.0, -1.0) if Hq > 1 else np.ones(1)
+    c.q = bf16(np.broadcast_to(u * sign[:, None], (1, R, Hq, D)).copy())
+    rows = slice(0, 64) if first else slice(256, 320)
+    k = np.broadcast_to(-a * u, (1, Hkv, L, D)).copy()
+    k[:, :, rows] = a * u
+    c.codes[0], c.scale[0][:] = H.encode(k), 1.0
+    c.scale[1][:] = 1.0
+    c.scale[1][:, :, 0 if first else 4] = 2.0 ** -ratio
+    c.tk = bf16(np.zeros(c.tk.shape))                       # the tree's keys: in between, without values
+    c.tv = torch.zeros_like(c.tv)
+    settle(c)
+    for splits in (1, 2):
+        for precise in (False, True):
+            check(c, c.desc(True, precise, splits, engine), few_rows(kern))
+
+
+@pytest.mark.parametrize("kern", KERNELS, ids=name)
+def test_scales_over_2_to_the_60_at_random(kern):
+    R, Hq, Hkv, D, engine = kern
+    c = Case(55, 2, R, Hq, Hkv, D, 1000, [1000, 700], q_size=6.0)
+    c.scale[1][:] = 2.0 ** np.random.default_rng(56).integers(-60, 1, c.scale[1].shape)
+    settle(c)
+    for splits in (0, 1, 3):
+        check(c, c.desc(True, True, splits, engine), few_rows(kern))
