@@ -77,19 +77,49 @@ __device__ __forceinline__ float2 kvq_float2(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// A query row's elements as two e4m3 terms, x = hi + lo: two halves (magnitudes up to 448, exact) to
-// the upper bytes of two halves each.  Times 2^-8 a half's exponent field is e4m3's (subnormals
-// too), and a code is its bits 13 .. 7 and the sign: cut off for hi, which leaves lo the other four
-// of bf16's eight bits; lo is rounded (it has to be below 2^-11 of the row's largest element).
-// Integer instructions (conversions to and from e4m3: 32 requests of 1K to 16K 262.7 against
-// 261.6 us, 61 nodes over 2K 15.6 against 15.4).
+// A query row's elements as 8-bit terms of their own products with the codes, two halves to the
+// upper bytes of two halves each.  A term is what is left so far, rounded to its format's significant
+// bits, and what it leaves is exact in a half; an e5m2 code is a half's upper byte, an e4m3 code the
+// bits 13 .. 7 and the sign of a half times 2^-8 (subnormals too).  Integer instructions (conversions
+// to and from e4m3 for the two terms: 32 requests of 1K to 16K 262.7 against 261.6 us, 61 nodes over
+// 2K 15.6 against 15.4).
+//
+// Two terms (EAGLE_ATTN_FAST; the row's largest element in (224, 448]): e4m3 holds four of bf16's
+// eight bits, and rounding leaves a rest of at most eight units, which three bits hold: e5m2, down to
+// steps of 2^-16; or, where the terms' products are columns of their own (APART), 2^4 times it as
+// e4m3.  Exact down to elements of 2^-13 of the row's largest; below, the first term is off by 2^-10 at
+// most, the second's steps in it are 2^-13: 2^-14, below 2^-21 of the row's largest.
+template <bool APART>
 __device__ __forceinline__ void kvq_split2(uint32_t h, uint32_t& hi, uint32_t& lo) {
-  const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h), __floats2half2_rn(0x1p-8f, 0x1p-8f));
-  const uint32_t q = *reinterpret_cast<const uint32_t*>(&v), t = q & 0xff80ff80u;
-  const __half2 d = __hsub2(v, *reinterpret_cast<const __half2*>(&t));
-  const uint32_t l = *reinterpret_cast<const uint32_t*>(&d) + 0x00400040u;
-  hi = (q << 1) | (q & 0x80008000u);
-  lo = (l << 1) | (l & 0x80008000u);
+  const auto as_half = [](uint32_t x) { return *reinterpret_cast<const __half2*>(&x); };
+  const auto as_bits = [](__half2 x) { return *reinterpret_cast<const uint32_t*>(&x); };
+  const auto both = [](float x) { return __floats2half2_rn(x, x); };
+  const uint32_t t = (as_bits(__hmul2(as_half(h), both(0x1p-8f))) + 0x00400040u) & 0xff80ff80u;
+  const __half2 d = __hfma2(as_half(t), both(-256.f), as_half(h));
+  hi = (t << 1) | (t & 0x80008000u);
+  if (APART) {
+    const uint32_t l = as_bits(__hmul2(d, both(0x1p-4f))) + 0x00400040u;
+    lo = (l << 1) | (l & 0x80008000u);
+  } else {
+    lo = as_bits(d) + 0x00800080u;
+  }
+}
+constexpr float kApart = 0x1p-4f;  // what the second term counts when APART
+
+// Three terms (EAGLE_ATTN_PRECISE; the row's largest element in (28672, 57344]), all e5m2: exact down
+// to elements of 2^-23 of the row's largest, below that off by 2^-17, less than 2^-31 of it.
+__device__ __forceinline__ void kvq_split3(uint32_t h, uint32_t (&t)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    t[i] = h + 0x00800080u;
+    const uint32_t c = t[i] & 0xff00ff00u;
+    const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&c));
+    h = *reinterpret_cast<const uint32_t*>(&d);
+  }
+}
+// The power of two that a row with the largest magnitude `am` is divided by for either.
+__device__ __forceinline__ float kvq_qscale(uint32_t am, bool three) {
+  return kvq_scale(fmaxf(__uint_as_float(min(am, 0x7f7f0000u)), 0x1p-100f)) * (three ? 0x1p-7f : 1.f);
 }
 // The codes of two such pairs.
 __device__ __forceinline__ uint32_t kvq_pack(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7531); }

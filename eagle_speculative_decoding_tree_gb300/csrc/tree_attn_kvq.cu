@@ -8,7 +8,8 @@
 // How the 8-bit operands meet the tensor cores.  A code is exact as a half, so the prefix
 // products run in half precision inputs with fp32 accumulators and the scales stay outside:
 //   - a query row is multiplied by a power of two that puts its largest element in
-//     [2^14, 2^15): bf16 to half is then exact down to 2^-39 of that element;
+//     [2^14, 2^15): bf16 to half is then exact down to elements of 2^-31 of that one, and off by
+//     2^-39 of it at most below;
 //   - ks multiplies the scores of its block (fp32);
 //   - vs / vref, vref the largest vs of the CTA's key range, goes into the exponent of P, so
 //     one accumulator serves blocks of different scales; the row sum takes it out again.  (Where

@@ -3,12 +3,12 @@
 // of the products; tree_attn_kvq.cu has the operation.
 //
 // Few rows against a long cache are bound by the cache's bytes, so nothing else may cost much:
-//     S^T = K Q^T     M = 128 keys (K codes as they lie), N = the rows' hi | lo terms
+//     S^T = K Q^T     M = 128 keys (K codes as they lie), N = the rows' terms
 //     O^T = V^T P^T   M = 128 head dims (V codes as they lie, MN-major), N = the rows' P terms
 // Both read a tile's codes once, straight from the TMA ring; no tile is converted.  All rounding
 // is on the small side:
-//   q  as in tree_attn_kvq_tc.cu: a power of two puts a row's largest element in (224, 448], and
-//      q = hi + lo in e4m3 keeps bf16's bits down to elements of 2^-11 of it;
+//   q  as in tree_attn_kvq_tc.cu: two terms keep bf16's bits down to elements of 2^-13 of the row's
+//      largest, EAGLE_ATTN_PRECISE's three down to 2^-23;
 //   p  2^PB vs / vref is rounded to a half (11 bits) and that half is written as four e5m2 terms
 //      of three bits each, exactly down to steps of 2^-29 of the largest p (the rest after the
 //      first term is multiplied by 8, past e5m2's smallest steps).  EAGLE_ATTN_PRECISE: two more
@@ -27,7 +27,7 @@
 //   a warp that issues every tcgen05.mma: QK0 QK1 | QK2 PV0 | QK3 PV1 | ...
 // (32 rows a thread instead of 16 take as many instructions, but at 2.5 warps a scheduler only
 // every second cycle issued one: 61.7 us against 58.0 for a chain of 8 over 128K.)
-// TMEM: S of four tiles (hi | lo columns, or one), then O of the even and the odd tiles (a column per
+// TMEM: S of four tiles (a column per row and term of Q, or per row), then O of the even and the odd tiles (a column per
 // row and term of P).
 // Measured (8 KV heads, 4 query heads each, graph replay): one token over 128K tokens 46 us (5.8
 // TB/s, 86 % of a device copy's rate), over 8K 9.7; a chain of 8 over 128K, fp32 and precise, 53.6 us
@@ -64,20 +64,21 @@ struct Few {
   static constexpr int SW = NR / 2;                 // softmax warps: NR / 16 x 2 warpgroups
   static constexpr int NT = SW * 32 + (NR == 32 ? 128 : 64);  // threads (setmaxnreg wants whole warpgroups)
   static constexpr int NP = NR * TERMS;             // O columns of a tile parity, bytes of a key's P
-  // Q's terms: columns of their own in S, or twice as many products into the same ones.  The first for
+  static constexpr int QT = TERMS > 4 ? 3 : 2;      // terms of Q
+  // Q's terms: columns of their own in S, or as many more products into the same ones.  The first for
   // 16 rows (one token over 128K: 45.6 us, the second 46.2), the second for 32 (a chain of 8 over 8K 13.0
   // us, the first 13.3; six terms of P leave TMEM no room for the first: 53.5, with two S buffers and a
   // wait for each of them 54.5).
   static constexpr bool ONE_S = NR == 32;
-  static constexpr int NS = ONE_S ? NR : 2 * NR;    // S columns of a tile
+  static constexpr int NS = ONE_S ? NR : QT * NR;   // S columns of a tile
   static constexpr int ST = NR == 32 ? 5 : 6;       // ring stages
-  static constexpr int SM_Q = 0;                    // hi rows, lo rows of 128 codes
-  static constexpr int SM_P = SM_Q + 2 * NR * 128;      // two buffers, blocks of 32 columns x 128 keys
+  static constexpr int SM_Q = 0;                    // the terms' rows of 128 codes
+  static constexpr int SM_P = SM_Q + QT * NR * 128;     // two buffers, blocks of 32 columns x 128 keys
   static constexpr int P1 = 128 * NP;
   static constexpr int SM_K = SM_P + 2 * P1;
   static constexpr int SM_V = SM_K + ST * T8;
   static constexpr int SMEM = SM_V + ST * T8 + 1024;
-  static_assert(P1 % 1024 == 0 && 4 * NS + 2 * NP <= 512, "alignment of the rings, TMEM columns");
+  static_assert(P1 % 1024 == 0 && SM_P % 1024 == 0 && SMEM <= 232448 - 4096 && 4 * NS + 2 * NP <= 512, "alignment of the rings, TMEM columns");
 };
 
 // Descriptor with the 32-byte swizzle (MN-major P: rows of 32 columns, 8 keys every `sbo` bytes,
@@ -310,10 +311,11 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
         if (!wait(&full[s], (i / ST) & 1, ERR_K)) return false;
         tc_fence_after();
 #pragma unroll
-        for (int term = 0; term < (F::ONE_S ? 2 : 1); ++term)
+        for (int term = 0; term < (F::ONE_S ? F::QT : 1); ++term)
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma8(tu + col_s(i), dk + s * (T8 >> 4) + ks * 2, dq + term * (NR * 8) + ks * 2, idesc8(0, 0, F::NS), term + ks > 0);
+          for (int ks = 0; ks < 4; ++ks)  // (two terms: e4m3 the first, or both in columns of their own)
+            mma8(tu + col_s(i), dk + s * (T8 >> 4) + ks * 2, dq + term * (NR * 8) + ks * 2,
+                 idesc8(F::QT == 3 || term ? 1 : 0, 0, F::NS), term + ks > 0);
         commit(&s_full[i & 3]);
         commit(&k_empty[s]);
         return true;
@@ -374,28 +376,33 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
         // a row with an element that is not finite gets NaN scores
-        const float qs = kvq_scale(fmaxf(__uint_as_float(min(am, 0x7f7f0000u)), 0x1p-100f));
+        const float qs = kvq_qscale(am, F::QT == 3);
         const float mul = __uint_as_float((254u << 23) - __float_as_uint(qs));  // 1 / qs, a power of two
         if (c == 0)
           s_c[row] = am < 0x7f800000u ? a.scale_log2 * qs : __uint_as_float(0x7fffffffu);
-        uint32_t hi[4], lo[4];
+        uint32_t tq[F::QT][4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          uint32_t h[2], l[2];
+          uint32_t t[2][3];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const uint32_t v = u[2 * k + e];
-            kvq_split2(half2_bits(__uint_as_float(v << 16) * mul, __uint_as_float(v & 0xffff0000u) * mul), h[e], l[e]);
+            const uint32_t h = half2_bits(__uint_as_float(v << 16) * mul, __uint_as_float(v & 0xffff0000u) * mul);
+            if (F::QT == 3)
+              kvq_split3(h, t[e]);
+            else
+              kvq_split2<!F::ONE_S>(h, t[e][0], t[e][1]);
           }
-          hi[k] = kvq_pack(h[0], h[1]);
-          lo[k] = kvq_pack(l[0], l[1]);
+#pragma unroll
+          for (int i = 0; i < F::QT; ++i) tq[i][k] = kvq_pack(t[0][i], t[1][i]);
         }
         uint8_t* d1 = smem + F::SM_Q + row * 128 + (((c >> 1) ^ (row & 7)) << 4) + 8 * (c & 1);
         uint8_t* d2 = smem + F::SM_Q + row * 128 + ((((c >> 1) + 4) ^ (row & 7)) << 4) + 8 * (c & 1);
-        *reinterpret_cast<uint2*>(d1) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2*>(d2) = make_uint2(hi[2], hi[3]);
-        *reinterpret_cast<uint2*>(d1 + NR * 128) = make_uint2(lo[0], lo[1]);
-        *reinterpret_cast<uint2*>(d2 + NR * 128) = make_uint2(lo[2], lo[3]);
+#pragma unroll
+        for (int i = 0; i < F::QT; ++i) {
+          *reinterpret_cast<uint2*>(d1 + i * NR * 128) = make_uint2(tq[i][0], tq[i][1]);
+          *reinterpret_cast<uint2*>(d2 + i * NR * 128) = make_uint2(tq[i][2], tq[i][3]);
+        }
         fence_proxy_async_smem();
       }
       if (threadIdx.x < 2 * NR) {
@@ -431,16 +438,19 @@ __global__ void __launch_bounds__(Few<NR, TERMS>::NT, 1)
         // x = score - reference (log2 units) of this key and every row
         float x[16];
         auto scores = [&]() {
-          uint32_t hi[16], lo[16];
+          uint32_t hi[16], lo[16], third[16];
           tmem_ld16(lb + col_s(i) + g0, hi);
           if (!F::ONE_S) tmem_ld16(lb + col_s(i) + NR + g0, lo);
+          if (!F::ONE_S && F::QT == 3) tmem_ld16(lb + col_s(i) + 2 * NR + g0, third);
           tmem_ld_wait();
 #pragma unroll
           for (int r = 0; r < 16; r += 2) {
             const uint64_t c = *reinterpret_cast<const uint64_t*>(&s_c[g0 + r]);
             const uint64_t mu = *reinterpret_cast<const uint64_t*>(&s_mu[w][g0 + r]);
             uint64_t sum = f32x2(hi[r], hi[r + 1]);
-            if (!F::ONE_S) sum = add_f32x2(sum, f32x2(lo[r], lo[r + 1]));
+            if (!F::ONE_S && F::QT == 2) sum = fma_f32x2(f32x2(lo[r], lo[r + 1]), twice(kApart), sum);
+            if (!F::ONE_S && F::QT == 3)
+              sum = add_f32x2(add_f32x2(sum, f32x2(lo[r], lo[r + 1])), f32x2(third[r], third[r + 1]));
             f32x2_split(fma_f32x2(sum, mul_f32x2(c, kc2), mu), x[r], x[r + 1]);
           }
           if (nv < KT) {

@@ -2,11 +2,11 @@
 // (head_dim 128), for trees of many rows; tree_attn_kvq.cu has the operation and the
 // few-row kernel.
 //
-// Q K^T takes the codes as they come: kind::f8f6f4 with both operands e4m3.  A query row is
-// multiplied by a power of two that puts its largest element in (224, 448] and split into two
-// e4m3 terms, q = hi + lo: four bits each hold bf16's eight exactly, down to elements of 2^-11
-// of the largest, and 2^-19 of it below.  Two products at twice the half rate cost what one
-// half product would, and K is never converted.  P V takes halves (11 bits in one term, against
+// Q K^T takes the codes as they come: kind::f8f6f4.  A query row is multiplied by a power of two
+// and split into terms of three or four bits that hold bf16's eight (kvq_split2, kvq_split3): two,
+// exact down to elements of 2^-13 of the row's largest, or for EAGLE_ATTN_PRECISE three, exact down
+// to 2^-23 of it.  Two products at twice the half rate cost what one half product would, and K is
+// never converted.  P V takes halves (11 bits in one term, against
 // the four of an e4m3 P): six warps widen each V tile from e4m3 to half, exactly, into a
 // second ring.  The scales stay outside as in tree_attn_kvq.cu: ks on the scores of its 64
 // keys, vs / vref in the exponent of P.
@@ -52,12 +52,20 @@ using namespace sm100;
 constexpr int KT = 128;
 constexpr int T8 = KT * 128;    // a tile of codes, 16 KB
 constexpr int T16 = 2 * T8;     // a tile of halves, 32 KB: two 64-dim halves of 128-byte rows
-constexpr int KST = 3, VST = 3; // ring stages of K and V codes
-constexpr int SM_Q = 0;                 // two row tiles: hi | lo codes (or bf16 halves), 64 KB
-constexpr int SM_K = SM_Q + 2 * T16;
-constexpr int SM_V = SM_K + KST * T8;
-constexpr int SM_W = SM_V + VST * T8;   // widened V, two stages
-constexpr int SMEM = SM_W + 2 * T16 + 1024;
+// Shared memory by terms of P (EAGLE_ATTN_FAST 1, PRECISE 2): two row tiles of Q's terms (or bf16
+// halves), the rings of K and V codes, widened V (two stages).  The third term of Q takes a stage of
+// either ring.
+template <int TERMS>
+struct Lay {
+  static constexpr int QT = TERMS == 2 ? 3 : 2;   // terms of Q
+  static constexpr int KST = TERMS == 2 ? 2 : 3, VST = KST;
+  static constexpr int QB = QT * T8;              // a row tile's Q
+  static constexpr int SM_Q = 0;
+  static constexpr int SM_K = SM_Q + 2 * QB;
+  static constexpr int SM_V = SM_K + KST * T8;
+  static constexpr int SM_W = SM_V + VST * T8;
+  static constexpr int SMEM = SM_W + 2 * T16 + 1024;
+};
 constexpr int NT = 512;
 constexpr int WT = 192;                 // widening threads (six warps)
 constexpr int QW = 14;                  // warps that stage the query tile: softmax and widening
@@ -74,7 +82,7 @@ struct Maps {
 __device__ __forceinline__ uint32_t col_s(int w) { return static_cast<uint32_t>(w) * 128u; }
 __device__ __forceinline__ uint32_t col_o(int w) { return 256u + static_cast<uint32_t>(w) * 128u; }
 
-// Instruction descriptors: fp32 accumulator; operand formats in bits 7 and 10 (f8f6f4: e4m3 0;
+// Instruction descriptors: fp32 accumulator; operand formats in bits 7 and 10 (f8f6f4: e4m3 0, e5m2 1;
 // f16: half 0, bf16 1).
 __host__ __device__ constexpr uint32_t idesc(int fmt, int b_mn) {
   return (1u << 4) | (static_cast<uint32_t>(fmt) << 7) | (static_cast<uint32_t>(fmt) << 10) |
@@ -193,6 +201,8 @@ struct Range {
 
 template <int TERMS>
 __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_constant__ Maps tm, const KvqAttnArgs a) {
+  using Y = Lay<TERMS>;
+  constexpr int KST = Y::KST, VST = Y::VST, QB = Y::QB, SM_Q = Y::SM_Q, SM_K = Y::SM_K, SM_V = Y::SM_V, SM_W = Y::SM_W;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t k_full[KST], k_empty[KST], v_full[VST], v_empty[VST], w_full[2], w_empty[2], s_full[2], p_full[2], q_full, o_full;
@@ -275,7 +285,7 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
       const int nd = node_of(a, qr), n16 = qr < RG ? 16 : 0;  // 0: zero fill, nothing read
       const uint16_t* src =
           n16 ? a.q + ((static_cast<size_t>(b) * a.R + nd) * a.Hq + h * a.G + (qr - nd * a.G)) * 128 + 8 * c : a.q;
-      const uint32_t at = d0 + (u >> 5) * T16 + lr * 128 + ((c ^ (lr & 7)) << 4);
+      const uint32_t at = d0 + (u >> 5) * QB + lr * 128 + ((c ^ (lr & 7)) << 4);
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(src), "r"(n16) : "memory");
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at + T8), "l"(src + 64), "r"(n16) : "memory");
     }
@@ -284,11 +294,12 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
 #pragma unroll 1
     for (int u = warp; u < units && !r.tree; u += QW) {
       const int lr = (u & 31) * 4 + sub;
+      uint8_t* dst = smem + SM_Q + (u >> 5) * QB;
       if (row0 + u * 4 >= RG) {  // zeros in either form
+        if (TERMS == 2) *reinterpret_cast<uint4*>(dst + 2 * T8 + lr * 128 + c * 16) = make_uint4(0, 0, 0, 0);
         if (c == 0) s_q[u >> 5][lr] = 1.f;
         continue;
       }
-      uint8_t* dst = smem + SM_Q + (u >> 5) * T16;
       const uint8_t* d = dst + lr * 128 + ((c ^ (lr & 7)) << 4);
       const uint4 x0 = *reinterpret_cast<const uint4*>(d), x1 = *reinterpret_cast<const uint4*>(d + T8);
       const uint32_t x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
@@ -297,30 +308,34 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
       for (int k = 0; k < 8; ++k) am = max(am, max((x[k] << 16) & 0x7fff0000u, x[k] & 0x7fff0000u));
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
-      // largest element in (224, 448]: the power of two of a cache block's scale; a row with
-      // an element that is not finite gets NaN scores
-      const float qs = kvq_scale(fmaxf(__uint_as_float(min(am, 0x7f7f0000u)), 0x1p-100f));
+      // a row with an element that is not finite gets NaN scores
+      const float qs = kvq_qscale(am, TERMS == 2);
       const float mul = __uint_as_float((254u << 23) - __float_as_uint(qs));  // 1 / qs, a power of two
       if (c == 0) s_q[u >> 5][lr] = am < 0x7f800000u ? qs : __uint_as_float(0x7fffffffu);
-      uint32_t hi[4], lo[4];  // words 0, 1: dims 8 c ..; 2, 3: dims 64 + 8 c ..
+      uint32_t tq[Y::QT][4];  // words 0, 1: dims 8 c ..; 2, 3: dims 64 + 8 c ..
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        uint32_t h[2], l[2];
+        uint32_t t[2][3];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const uint32_t v = x[2 * k + e];
-          kvq_split2(half2_bits(__uint_as_float(v << 16) * mul, __uint_as_float(v & 0xffff0000u) * mul), h[e], l[e]);
+          const uint32_t h = half2_bits(__uint_as_float(v << 16) * mul, __uint_as_float(v & 0xffff0000u) * mul);
+          if (TERMS == 2)
+            kvq_split3(h, t[e]);
+          else
+            kvq_split2<false>(h, t[e][0], t[e][1]);
         }
-        hi[k] = kvq_pack(h[0], h[1]);
-        lo[k] = kvq_pack(l[0], l[1]);
+#pragma unroll
+        for (int i = 0; i < Y::QT; ++i) tq[i][k] = kvq_pack(t[0][i], t[1][i]);
       }
       // (every lane of the row has its elements: the maximum's shuffles came between)
       uint8_t* d1 = dst + lr * 128 + (((c >> 1) ^ (lr & 7)) << 4) + 8 * (c & 1);
       uint8_t* d2 = dst + lr * 128 + ((((c >> 1) + 4) ^ (lr & 7)) << 4) + 8 * (c & 1);
-      *reinterpret_cast<uint2*>(d1) = make_uint2(hi[0], hi[1]);
-      *reinterpret_cast<uint2*>(d2) = make_uint2(hi[2], hi[3]);
-      *reinterpret_cast<uint2*>(d1 + T8) = make_uint2(lo[0], lo[1]);
-      *reinterpret_cast<uint2*>(d2 + T8) = make_uint2(lo[2], lo[3]);
+#pragma unroll
+      for (int i = 0; i < Y::QT; ++i) {
+        *reinterpret_cast<uint2*>(d1 + i * T8) = make_uint2(tq[i][0], tq[i][1]);
+        *reinterpret_cast<uint2*>(d2 + i * T8) = make_uint2(tq[i][2], tq[i][3]);
+      }
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -476,7 +491,7 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
 #pragma unroll 1
             for (int ks = 0; ks < 8; ++ks) {
               const uint64_t off = (ks >> 2) * (T8 >> 4) + (ks & 3) * 2;
-              mma_f16_ss(tu + col_s(w), dq + w * (T16 >> 4) + off, dk + off, idesc(1, 0), ks > 0);
+              mma_f16_ss(tu + col_s(w), dq + w * (QB >> 4) + off, dk + off, idesc(1, 0), ks > 0);
             }
             commit(&s_full[w]);
           }
@@ -496,12 +511,13 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
             // (A: the first row tile's item has waited for both; a wait costs what a product does)
             if ((!two || !w) && !wait(&k_full[s], (t / KST) & 1, ERR_K)) return false;
             tc_fence_after();
-            const uint64_t q = dq + (two ? w * (T16 >> 4) : 0), k = dk + s * (T8 >> 4);
+            const uint64_t q = dq + (two ? w * (QB >> 4) : 0), k = dk + s * (T8 >> 4);
 #pragma unroll
-            for (int term = 0; term < 2; ++term)
+            for (int term = 0; term < Y::QT; ++term)
 #pragma unroll
-              for (int ks = 0; ks < 4; ++ks)
-                mma_f8_ss(tu + col_s(w), q + term * (T8 >> 4) + ks * 2, k + ks * 2, idesc(0, 0), term + ks > 0);
+              for (int ks = 0; ks < 4; ++ks)  // (the first of two terms is e4m3, as the codes; all others e5m2)
+                mma_f8_ss(tu + col_s(w), q + term * (T8 >> 4) + ks * 2, k + ks * 2,
+                          idesc(0, 0) | (TERMS == 2 || term ? 1u << 7 : 0u), term + ks > 0);
             commit(&s_full[w]);
             if (last_of(i)) commit(&k_empty[s]);
             return true;
@@ -786,6 +802,7 @@ __global__ void __launch_bounds__(NT, 1) tree_attn_kvq_tc_kernel(const __grid_co
 template <int TERMS>
 cudaError_t launch_tc(const KvqAttnPlan& p, const Maps& tm, const KvqAttnArgs& a, cudaStream_t s) {
   auto kern = tree_attn_kvq_tc_kernel<TERMS>;
+  constexpr int SMEM = Lay<TERMS>::SMEM;
   static unsigned long long configured = 0;  // shared memory opt-in, once per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

@@ -284,7 +284,10 @@ int eagle_tree_attn_plan(const eagle_attn_desc* d, int32_t* splits, int32_t* ker
  *              the row's largest p times V scale.  V scales below 2^-100 of the head's largest
  *              count as that.  The tree's part is precise in both: P with 22 bits or more;
  *              elements of tree_v below 2^-32 of their request's and head's largest may be
- *              rounded, to steps of 2^-39 of that one.  Scores, softmax and sums are fp32.
+ *              rounded, to steps of 2^-39 of that one.  Scores, softmax and sums are fp32; against
+ *              the prefix, elements of a query row enter them as they are down to 2^-13 (FAST) or
+ *              2^-23 (PRECISE) of the row's largest, and off by at most 2^-21 or 2^-31 of that one
+ *              below (head_dim 64 and EAGLE_ENGINE_MMA_SYNC: 2^-31 and 2^-39 in both).
  * ws: eagle_workspace_size(EAGLE_WS_TREE_ATTN_KVQ, d) bytes, zero-filled before its first
  * use; one workspace serves one stream at a time, and any descriptors in turn that it is large
  * enough for.  Its first 4 bytes are an error word as in eagle_tree_attn.

@@ -153,3 +153,20 @@ def test_scales_over_2_to_the_60_at_random(kern):
     settle(c)
     for splits in (0, 1, 3):
         check(c, c.desc(True, True, splits, engine), few_rows(kern))
+
+
+@pytest.mark.parametrize("size", [50, 2.0 ** 12, 2.0 ** 16])
+@pytest.mark.parametrize("kern", KERNELS, ids=name)
+def test_query_rows_with_a_large_element(kern, size):
+    """One channel of every query row is `size` times the others and meets keys that have nothing in
+    it: the scores come from the small elements."""
+    R, Hq, Hkv, D, engine = kern
+    c = Case(57, 2, R, Hq, Hkv, D, 200, [200, 65])
+    c.q[..., 7] *= size
+    c.q[:, :, 0, 7] = size
+    c.codes[0][..., 7] = 0
+    c.tk[..., 7] = 0.0
+    settle(c)
+    wide = D == 128 and engine == 0
+    check(c, c.desc(True, True, 0, engine), few_rows(kern), dq=2.0 ** -31 if wide else 2.0 ** -39)
+    check(c, c.desc(True, False, 0, engine), few_rows(kern), dq=2.0 ** -21 if wide else 2.0 ** -39)
