@@ -143,7 +143,7 @@ class VerifyStep:
     The tree (tokens, parents, ancestor masks) comes from ``build_tree`` on the GPU;
     target/draft logits are the synthetic LM's rows at the tree's nodes; Q, K/V and
     the uniforms are seeded normals / uniforms.  ``run`` enqueues the step;
-    ``reset`` restores seq_len so that repeated runs process the same step.
+    ``reset`` restores what a commit changed so that repeated runs process the same step.
 
     ``cache_bits`` 8 keeps the prefix K/V as e4m3 codes with a scale for each 64 tokens and
     head (``k8``, ``ks``, ``v8``, ``vs`` instead of ``kc``, ``vc``; bf16 workloads): the prefix
@@ -235,16 +235,26 @@ class VerifyStep:
     def _quantise_prefix(self):
         """The prefix rows of every layer into 8-bit caches, in place of the bf16 ones."""
         w, dev = self.w, self.seq_len.device
-        self.k8, self.ks, self.v8, self.vs = [], [], [], []
-        d = B.KvqDesc(self.B, w.n_kv_heads, w.head_dim, w.max_seq, w.max_seq, B.EAGLE_BF16)
-        start = torch.zeros(self.B, dtype=torch.int32, device=dev)
-        blocks = -(-w.max_seq // B.EAGLE_KVQ_BLOCK)
-        for k, v in zip(self.kc, self.vc):
-            for codes, scale in ((self.k8, self.ks), (self.v8, self.vs)):
-                codes.append(torch.zeros(k.shape, dtype=torch.uint8, device=dev))
-                scale.append(torch.zeros(self.B, w.n_kv_heads, blocks, device=dev))
-            B.eagle_kvq_write(d, k, v, start, self.seq_len, self.k8[-1], self.ks[-1], self.v8[-1], self.vs[-1])
+        Bn, H, D, P, blk = self.B, w.n_kv_heads, w.head_dim, w.max_seq, B.EAGLE_KVQ_BLOCK
+        nblk = -(-P // blk)
+        # one tensor for K and V of all layers; the calls take a layer's part
+        self._codes = torch.zeros(2, self.L, Bn, H, P, D, dtype=torch.uint8, device=dev)
+        self._scales = torch.zeros(2, self.L, Bn, H, nblk, device=dev)
+        self.k8, self.v8 = (list(t) for t in self._codes)
+        self.ks, self.vs = (list(t) for t in self._scales)
+        d = B.KvqDesc(Bn, H, D, P, P, B.EAGLE_BF16)
+        start = torch.zeros(Bn, dtype=torch.int32, device=dev)
+        for l in range(self.L):
+            B.eagle_kvq_write(d, self.kc[l], self.vc[l], start, self.seq_len, self.k8[l], self.ks[l], self.v8[l],
+                              self.vs[l])
         self.kc = self.vc = None
+        # A commit may move the codes of each prefix's last block to a larger scale: reset() puts them back.
+        last = (self.seq_len.long() // blk).clamp(max=nblk - 1)
+        rows = (last[:, None] * blk + torch.arange(blk, device=dev)).clamp(max=P - 1)
+        self._last_rows = rows[:, None, :, None].expand(2, self.L, Bn, H, blk, D)
+        self._last_block = last[:, None, None].expand(2, self.L, Bn, H, 1)
+        self._last_codes = self._codes.gather(4, self._last_rows)
+        self._last_scale = self._scales.gather(4, self._last_block)
 
     # ------------------------------------------------------------------ step variants
     def add_variants(self, n: int):
@@ -304,8 +314,11 @@ class VerifyStep:
                status=self.acc.status, stream=stream)
 
     def reset(self):
-        """Restore seq_len so that the next run repeats the same step."""
+        """Restore seq_len (and an 8-bit cache's last prefix blocks) so that the next run repeats the same step."""
         self.seq_len.copy_(self.seq_len_init)
+        if self.cache_bits == 8:
+            self._codes.scatter_(4, self._last_rows, self._last_codes)
+            self._scales.scatter_(4, self._last_block, self._last_scale)
 
     def run(self, stream=None, reset: bool = True):
         if reset:
