@@ -146,7 +146,7 @@ class VerifyStep:
     ``reset`` restores what a commit changed so that repeated runs process the same step.
 
     ``cache_bits`` 8 keeps the prefix K/V as e4m3 codes with a scale for each 64 tokens and
-    head (``k8``, ``ks``, ``v8``, ``vs`` instead of ``kc``, ``vc``; bf16 workloads): the prefix
+    head (``k8``, ``ks``, ``v8``, ``vs`` instead of ``kc``, ``vc``; bf16 workloads): each layer's prefix
     is quantised once here (eagle_kvq_write), attention reads the codes
     (eagle_tree_attn_kvq) and the commit appends to them (eagle_kvq_commit).
     """
@@ -201,13 +201,20 @@ class VerifyStep:
         # per-layer attention tensors
         self.q, self.kc, self.vc, self.tk, self.tv, self.out = [], [], [], [], [], []
         self.host = [] if keep_host else None
+        if cache_bits == 8:
+            self._allocate_codes()
         for l in range(L):
             q, kc, vc, tk, tv = synth.attn_tensors(w, l, Bn, self.seq_len0, R, q_scale)
             if keep_host:
                 self.host.append((q, kc, vc, tk, tv))
             self.q.append(_to_dev(q, w.dtype, dev))
-            self.kc.append(_to_dev(kc, w.dtype, dev))
-            self.vc.append(_to_dev(vc, w.dtype, dev))
+            kc, vc = _to_dev(kc, w.dtype, dev), _to_dev(vc, w.dtype, dev)
+            if cache_bits == 8:
+                B.eagle_kvq_write(self._write_desc, kc, vc, self._zero, self.seq_len, self.k8[l], self.ks[l],
+                                  self.v8[l], self.vs[l])
+            else:
+                self.kc.append(kc)
+                self.vc.append(vc)
             self.tk.append(_to_dev(tk, w.dtype, dev))
             self.tv.append(_to_dev(tv, w.dtype, dev))
             self.out.append(torch.empty_like(self.q[-1]))
@@ -218,7 +225,8 @@ class VerifyStep:
         kind = B.EAGLE_WS_TREE_ATTN if cache_bits == 16 else B.EAGLE_WS_TREE_ATTN_KVQ
         self.attn_ws = torch.zeros(B.workspace_size(kind, self.attn_desc), dtype=torch.uint8, device=dev)
         if cache_bits == 8:
-            self._quantise_prefix()
+            self.kc = self.vc = None
+            self._keep_last_blocks()
         prop = B.EAGLE_PROPOSAL_SAMPLED if w.proposal == "sampled" else B.EAGLE_PROPOSAL_DELTA
         self.acc_desc = B.AcceptDesc(Bn, R, w.vocab, float(w.temperature), prop, dt, self.max_depth)
         self.acc_ws = torch.zeros(B.workspace_size(B.EAGLE_WS_ACCEPT, self.acc_desc), dtype=torch.uint8, device=dev)
@@ -232,27 +240,25 @@ class VerifyStep:
         self.variants = [dict(tokens=self.tokens, parent=self.parent, anc_mask=self.anc_mask, target=self.target,
                               draft=self.draft, u_accept=self.u_accept, u_final=self.u_final)]
 
-    def _quantise_prefix(self):
-        """The prefix rows of every layer into 8-bit caches, in place of the bf16 ones."""
+    def _allocate_codes(self):
+        """8-bit caches: one tensor for K and V of all layers; the calls take a layer's part."""
         w, dev = self.w, self.seq_len.device
-        Bn, H, D, P, blk = self.B, w.n_kv_heads, w.head_dim, w.max_seq, B.EAGLE_KVQ_BLOCK
-        nblk = -(-P // blk)
-        # one tensor for K and V of all layers; the calls take a layer's part
-        self._codes = torch.zeros(2, self.L, Bn, H, P, D, dtype=torch.uint8, device=dev)
-        self._scales = torch.zeros(2, self.L, Bn, H, nblk, device=dev)
+        nblk = -(-w.max_seq // B.EAGLE_KVQ_BLOCK)
+        self._codes = torch.zeros(2, self.L, self.B, w.n_kv_heads, w.max_seq, w.head_dim, dtype=torch.uint8, device=dev)
+        self._scales = torch.zeros(2, self.L, self.B, w.n_kv_heads, nblk, device=dev)
         self.k8, self.v8 = (list(t) for t in self._codes)
         self.ks, self.vs = (list(t) for t in self._scales)
-        d = B.KvqDesc(Bn, H, D, P, P, B.EAGLE_BF16)
-        start = torch.zeros(Bn, dtype=torch.int32, device=dev)
-        for l in range(self.L):
-            B.eagle_kvq_write(d, self.kc[l], self.vc[l], start, self.seq_len, self.k8[l], self.ks[l], self.v8[l],
-                              self.vs[l])
-        self.kc = self.vc = None
-        # A commit may move the codes of each prefix's last block to a larger scale: reset() puts them back.
-        last = (self.seq_len.long() // blk).clamp(max=nblk - 1)
-        rows = (last[:, None] * blk + torch.arange(blk, device=dev)).clamp(max=P - 1)
-        self._last_rows = rows[:, None, :, None].expand(2, self.L, Bn, H, blk, D)
-        self._last_block = last[:, None, None].expand(2, self.L, Bn, H, 1)
+        self._write_desc = B.KvqDesc(self.B, w.n_kv_heads, w.head_dim, w.max_seq, w.max_seq, B.EAGLE_BF16)
+        self._zero = torch.zeros(self.B, dtype=torch.int32, device=dev)
+
+    def _keep_last_blocks(self):
+        """A commit may move the codes of each prefix's last block to a larger scale: reset() puts them back."""
+        w, dev, blk = self.w, self.seq_len.device, B.EAGLE_KVQ_BLOCK
+        last = (self.seq_len.long() // blk).clamp(max=self._scales.shape[-1] - 1)
+        rows = (last[:, None] * blk + torch.arange(blk, device=dev)).clamp(max=w.max_seq - 1)
+        lead = (2, self.L, self.B, w.n_kv_heads)
+        self._last_rows = rows[:, None, :, None].expand(*lead, blk, w.head_dim)
+        self._last_block = last[:, None, None].expand(*lead, 1)
         self._last_codes = self._codes.gather(4, self._last_rows)
         self._last_scale = self._scales.gather(4, self._last_block)
 

@@ -54,3 +54,18 @@ def test_variants_do_not_depend_on_those_before():
         st.use_variant(k)
         st.run()
         assert all(torch.equal(a, b) for a, b in zip(want[k], result(st)))
+
+
+def test_construction_holds_one_layer_in_16_bits_at_a_time():
+    """Peak memory of building the step: the codes and about one layer's bf16 cache beside what stays."""
+    w = synth.WORKLOADS["llama8b"].with_(prefix=8192, vocab=2048)
+    layers = 8
+    VerifyStep(w, batch=1, layers=1, cache_bits=8)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    torch.cuda.reset_peak_memory_stats()
+    st = VerifyStep(w, batch=1, layers=layers, cache_bits=8)
+    torch.cuda.synchronize()
+    layer = 2 * w.n_kv_heads * w.max_seq * w.head_dim * 2  # one layer's K and V in bf16
+    over = torch.cuda.max_memory_allocated() - torch.cuda.memory_allocated()
+    assert st.L == layers and over <= 3 * layer  # (this layer's, the one before's, copies on their way)
