@@ -106,20 +106,25 @@ int check_accept_desc(const eagle_accept_desc* d) {
   return EAGLE_OK;
 }
 
-// eagle_tree_attn's envelope, bf16 only; TMA row coordinates are 32-bit.
+// eagle_tree_attn's envelope, bf16 only; TMA row coordinates are 32-bit, and so are the ends of tiles.
 int check_kvq_attn_desc(const eagle_attn_desc* d) {
   const int rc = check_attn_desc(d);
   if (rc != EAGLE_OK) return rc;
   if (d->dtype != EAGLE_BF16 || d->fault_test != 0) return EAGLE_ERR_UNSUPPORTED;
   if (d->engine != EAGLE_ENGINE_AUTO && d->engine != EAGLE_ENGINE_MMA_SYNC) return EAGLE_ERR_INVALID_ARG;
-  if (static_cast<long long>(d->batch) * d->n_kv_heads * d->max_seq >= (1ll << 31)) return EAGLE_ERR_UNSUPPORTED;
+  if (static_cast<long long>(d->batch) * d->n_kv_heads * d->max_seq > (1ll << 31) - 128) return EAGLE_ERR_UNSUPPORTED;
   return EAGLE_OK;
 }
+
+// The ends of a cache's blocks are 32-bit.
+bool kvq_capacity_ok(int max_seq) { return max_seq <= 0x7fffffff - (EAGLE_KVQ_BLOCK - 1); }
 
 int check_kvq_desc(const eagle_kvq_desc* d) {
   if (!d || d->batch < 1 || d->n_kv_heads < 1 || d->max_seq < 1 || d->rows < 1) return EAGLE_ERR_INVALID_ARG;
   if (d->head_dim != 64 && d->head_dim != 128) return d->head_dim < 1 ? EAGLE_ERR_INVALID_ARG : EAGLE_ERR_UNSUPPORTED;
-  if (!dtype_ok(d->dtype) || static_cast<long long>(d->batch) * d->n_kv_heads > 65535) return EAGLE_ERR_UNSUPPORTED;
+  const long long heads = static_cast<long long>(d->batch) * d->n_kv_heads;
+  if (!dtype_ok(d->dtype) || heads > 65535 || !kvq_capacity_ok(d->max_seq)) return EAGLE_ERR_UNSUPPORTED;
+  if (2 * heads * kvq_span_blocks(d->rows) > (1ll << 30)) return EAGLE_ERR_UNSUPPORTED;  // (32-bit work items)
   return EAGLE_OK;
 }
 
@@ -424,7 +429,7 @@ int eagle_kvq_commit(const eagle_commit_desc* d, void* const* k_codes_layers, fl
     return EAGLE_ERR_INVALID_ARG;
   if (d->layers > kMaxLayers || d->rows > kMaxRows || d->max_depth >= kMaxRows || !dtype_ok(d->dtype) ||
       (d->feat_dim > 0 && !dtype_ok(d->feat_dtype)) || (d->head_dim != 64 && d->head_dim != 128) ||
-      static_cast<long long>(d->batch) * d->n_kv_heads > 65535)
+      static_cast<long long>(d->batch) * d->n_kv_heads > 65535 || !kvq_capacity_ok(d->max_seq))
     return EAGLE_ERR_UNSUPPORTED;
   if (!k_codes_layers || !k_scale_layers || !v_codes_layers || !v_scale_layers || !tree_k_layers || !tree_v_layers ||
       !n_acc || !path || !seq_len)
@@ -462,7 +467,8 @@ int eagle_qk_norm_rope(const eagle_qk_norm_rope_desc* d, const void* qkv, const 
   if ((d->head_dim != 64 && d->head_dim != 128) || d->rot_dim % 16 || !dtype_ok(d->dtype) || d->batch > 65535)
     return EAGLE_ERR_UNSUPPORTED;
   const long long width = (static_cast<long long>(d->n_q_heads) + 2ll * d->n_kv_heads) * d->head_dim;
-  if (width > (1ll << 30)) return EAGLE_ERR_UNSUPPORTED;
+  if (width > (1ll << 30) || static_cast<long long>(d->batch) * d->rows > 0x7ffffff0ll)  // (32-bit row numbers)
+    return EAGLE_ERR_UNSUPPORTED;
   if (d->rot_dim > d->head_dim || (d->row_stride > 0 && d->row_stride < width)) return EAGLE_ERR_INVALID_ARG;
   if (d->row_stride % 8) return EAGLE_ERR_ALIGNMENT;
   if (!qkv || !inv_freq || !pos_id || !q || !k || !v) return EAGLE_ERR_INVALID_ARG;

@@ -427,9 +427,8 @@ cudaError_t launch(void (*k)(P...), dim3 grid, int threads, cudaStream_t s, bool
 cudaError_t launch_kvq_write(const eagle_kvq_desc& d, const void* k, const void* v, const int32_t* start,
                              const int32_t* count, uint8_t* k8, float* ks, uint8_t* v8, float* vs, uint32_t* status,
                              int num_sms, cudaStream_t s) {
-  const int per_head = static_cast<int>((d.rows + 2ll * kQB - 2) / kQB);  // blocks a span of `rows` can touch
+  const int per_head = static_cast<int>(kvq_span_blocks(d.rows));
   const long long items = 2ll * per_head * d.batch * d.n_kv_heads;
-  if (items > (1ll << 30)) return cudaErrorInvalidValue;
   const int grid = static_cast<int>(std::min<long long>(items, (d.dtype == EAGLE_F32 ? 3ll : 4ll) * num_sms));  // CTAs that fit
   if (d.dtype == EAGLE_F32)
     return launch(kvq_write_kernel<float>, dim3(grid), kWriteThreads, s, false, d, per_head, static_cast<int>(items),

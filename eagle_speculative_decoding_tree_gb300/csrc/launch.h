@@ -152,6 +152,8 @@ struct KvqCommitArgs {
   const void* tree_k[kMaxLayers];
   const void* tree_v[kMaxLayers];
 };
+// Blocks that a span of `rows` cache rows can touch.
+inline long long kvq_span_blocks(int rows) { return (rows + 2ll * EAGLE_KVQ_BLOCK - 2) / EAGLE_KVQ_BLOCK; }
 cudaError_t launch_kvq_write(const eagle_kvq_desc& d, const void* k, const void* v, const int32_t* start,
                              const int32_t* count, uint8_t* k8, float* ks, uint8_t* v8, float* vs, uint32_t* status,
                              int num_sms, cudaStream_t s);

@@ -281,7 +281,6 @@ cudaError_t launch_qk_norm_rope(const eagle_qk_norm_rope_desc& d, const void* qk
   long long split = std::min<long long>((want + rows - 1) / rows, (heads + pass - 1) / pass);
   a.run = static_cast<int>(((heads + split - 1) / split + pass - 1) / pass * pass);
   a.runs = (heads + a.run - 1) / a.run;
-  if (rows * a.runs > 0x7ffffff0ll) return cudaErrorInvalidValue;  // (more than any device holds)
   a.units = static_cast<int>(rows * a.runs);
   const int grid = (a.units + kThreads / 32 - 1) / (kThreads / 32);
   const bool f32 = d.dtype == EAGLE_F32;

@@ -292,7 +292,7 @@ int eagle_tree_attn_plan(const eagle_attn_desc* d, int32_t* splits, int32_t* ker
  * use; one workspace serves one stream at a time, and any descriptors in turn that it is large
  * enough for.  Its first 4 bytes are an error word as in eagle_tree_attn.
  * Unsupported: dtype not EAGLE_BF16, head_dim not 64 / 128, R > 128, Hq % Hkv != 0,
- * B * Hkv > 65535, B * Hkv * P >= 2^31, fault_test. */
+ * B * Hkv > 65535, B * Hkv * P > 2^31 - 128, fault_test. */
 int eagle_tree_attn_kvq(const eagle_attn_desc* d, const void* q, const void* k_codes, const float* k_scale,
                         const void* v_codes, const float* v_scale, const void* tree_k, const void* tree_v,
                         const int32_t* seq_len, const int32_t* n_nodes, const uint64_t* anc_mask, void* out,
@@ -316,7 +316,7 @@ int eagle_tree_attn_kvq(const eagle_attn_desc* d, const void* q, const void* k_c
  * Inputs and outputs must not overlap. */
 typedef struct {
   int32_t batch;       /* B, 1..65535 */
-  int32_t rows;        /* R >= 1 */
+  int32_t rows;        /* R >= 1; B * R < 2^31 - 15 */
   int32_t n_q_heads;   /* Hq */
   int32_t n_kv_heads;  /* Hkv */
   int32_t head_dim;    /* D: 64 or 128 */
@@ -514,8 +514,8 @@ typedef struct {
   int32_t batch;      /* B, B * Hkv <= 65535 */
   int32_t n_kv_heads; /* Hkv */
   int32_t head_dim;   /* D: 64 or 128 */
-  int32_t max_seq;    /* P: cache capacity per request */
-  int32_t rows;       /* N: rows per request of k / v */
+  int32_t max_seq;    /* P: cache capacity per request, at most 2^31 - 64 */
+  int32_t rows;       /* N: rows per request of k / v; B * Hkv * N at most 2^34 */
   int32_t dtype;      /* element type of k / v */
 } eagle_kvq_desc;
 
@@ -543,7 +543,7 @@ int eagle_kvq_read(const eagle_kvq_desc* d, const void* k_codes, const float* k_
  * seq_len[b] as eagle_kvq_write does (the scale of a begun block only grows), everything
  * else as eagle_kv_commit.  k_codes_layers, k_scale_layers, v_codes_layers, v_scale_layers,
  * tree_k_layers, tree_v_layers: HOST arrays of `layers` DEVICE pointers; d->dtype is the
- * tree K/V's element type and d->head_dim 64 or 128, B * Hkv <= 65535. */
+ * tree K/V's element type and d->head_dim 64 or 128, B * Hkv <= 65535, P <= 2^31 - 64. */
 int eagle_kvq_commit(const eagle_commit_desc* d, void* const* k_codes_layers, float* const* k_scale_layers,
                      void* const* v_codes_layers, float* const* v_scale_layers, const void* const* tree_k_layers,
                      const void* const* tree_v_layers, const int32_t* n_acc, const int32_t* path, int32_t* seq_len,
