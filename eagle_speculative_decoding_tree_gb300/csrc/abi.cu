@@ -435,6 +435,8 @@ int eagle_kvq_commit(const eagle_commit_desc* d, void* const* k_codes_layers, fl
       !n_acc || !path || !seq_len)
     return EAGLE_ERR_INVALID_ARG;
   if (d->feat_dim > 0 && (!feat_cache || !tree_feat)) return EAGLE_ERR_INVALID_ARG;
+  if (!aligned(n_acc, 4) || !aligned(path, 4) || !aligned(seq_len, 4) || !aligned(commit_pos, 4) || !aligned(status, 4))
+    return EAGLE_ERR_ALIGNMENT;
   KvqCommitArgs a;
   memset(&a, 0, sizeof a);
   for (int l = 0; l < d->layers; ++l) {

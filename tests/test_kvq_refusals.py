@@ -1,5 +1,5 @@
-"""The 8-bit KV cache entry points without a GPU: sizes behind their 32-bit arithmetic are
-refused on the host, with the documented code."""
+"""The 8-bit KV cache entry points without a GPU: sizes behind their 32-bit arithmetic and misaligned
+index arrays are refused on the host, with the documented codes."""
 import ctypes
 
 import pytest
@@ -42,6 +42,12 @@ def _commit(lib, d, **kw):
 @pytest.mark.parametrize("max_seq", [TOP, TOP - 62])
 def test_commit_refuses_sizes(lib, max_seq):
     assert _commit(lib, B.CommitDesc(1, 1, 1, 64, 61, max_seq, 7, 1, 0, 1)) == B.EAGLE_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("name", ["n_acc", "path", "seq_len", "commit_pos", "status"])
+def test_commit_refuses_misaligned_index_arrays(lib, name):
+    for off in (1, 2):
+        assert _commit(lib, B.CommitDesc(1, 1, 1, 64, 61, 512, 7, 1, 0, 1), **{name: A + off}) == B.EAGLE_ERR_ALIGNMENT
 
 
 def test_norm_rope_refuses_sizes(lib):
