@@ -19,10 +19,10 @@
 // (one block at a time leaves HBM idle through every block's reduction).  A commit is a few rows
 // for each of layers x requests x heads blocks, bound by the latency of its dependent loads
 // (lengths, path, rows), so it takes a warp per block and all of them at once.
-// Measured (8 heads x 128, bf16): 8192 rows written in 7.7 us from L2, 12.7 from HBM (50 MB; a CTA per
-// block, one block at a time, took 15.5 from L2), 32 requests of 375 to 750 rows 31.9 us, 8192 rows
-// read back in 6.9; 32 layers' accepted path of one request committed in 5.0 us, of 32 requests in
-// 11.6 (74 by a CTA per block).
+// Measured (8 heads x 128, bf16): 8192 rows written in 7.9 us from L2, 12.5 from HBM (50 MB; a CTA per
+// block, one block at a time, took 15.5 from L2), 32 requests of 511 to 1021 rows 31.9 us, 8192 rows
+// read back in 6.3; 32 layers' accepted path of one request committed in 5.3 us, of 32 requests in
+// 11.8 (74 by a CTA per block).
 #include <algorithm>
 
 #include "common.cuh"

@@ -658,7 +658,8 @@ cudaError_t launch_mma(const KvqAttnPlan& p, const Maps& tm, const KvqAttnArgs& 
 // together: all requests of full length (waves of equal CTAs), and lengths spread evenly (the
 // mean work, and a tail of most of a piece).  Measured: 8 requests of 1K to 16K x 8 heads 88 to
 // 102 us with 3 to 8 pieces, 120 with 2, 210 with 1; 32 such 253 to 255 us with 3 or 4, 261 with 2,
-// 276 with 6; 32 of 8K each 260 us with the 2 taken here, 241 with 1; one of 8K 18.8 us in one wave.
+// 276 with 6; 32 of 8K each 259 us with the 2 taken here, 238 with 1 (full lengths alone would
+// choose 1; the two cases together do not); one of 8K 19.1 us in one wave.
 // The plan's cost, in tiles' time, in *cost.
 static long long choose_pieces(long long base, int tiles, int num_sms, int extra, bool* even, double* cost) {
   const long long one = std::min<long long>(num_sms / base - 1, tiles);

@@ -30,8 +30,8 @@
 // TMEM: S of four tiles (a column per row and term of Q, or per row), then O of the even and the odd tiles (a column per
 // row and term of P).
 // Measured (8 KV heads, 4 query heads each, graph replay): one token over 128K tokens 46 us (5.8
-// TB/s, 86 % of a device copy's rate), over 8K 9.7; a chain of 8 over 128K, fp32 and precise, 53.6 us
-// (the loop's waits and product issue take about as long a tile as HBM does).
+// TB/s, 86 % of a device copy's rate), over 8K 9.7; a chain of 8 over 128K, fp32 and precise, 56.5 us,
+// 2 of them for Q's third term (the loop's waits and product issue take about as long a tile as HBM does).
 // Piece 0 is the tree (at most 32 bf16 keys), computed in fp32 on the ordinary cores; the others
 // are tps tiles of the prefix.  Pieces write fp32 partials, merged in the kernel when the grid
 // fits on the SMs (cooperative launch), else by kvq_combine_kernel.

@@ -34,9 +34,9 @@
 //
 // Bound by the products and the chain S -> P -> PV -> next S (P takes S's place in TMEM): 2690
 // cycles for 256 rows x 128 keys against 2048 of products (two e4m3 ones and one half one, 64
-// cycles per 128 x 128 x 32 bytes).  Measured, graph replay: 61 nodes x 4 heads x 8 over 128K 113 us
-// (1150 TFLOP/s), over 8K 18.8 us (half of it staging, partials and merge), 32 requests of 1K to 16K
-// 263 us.
+// cycles per 128 x 128 x 32 bytes).  Measured, graph replay, FAST (PRECISE): 61 nodes x 4 heads x 8 over
+// 128K 112 us (144), 1170 TFLOP/s, over 8K 19.1 us (21.1; half of it staging, partials and merge), 32
+// requests of 1K to 16K 262 us (348).
 #include "common.cuh"
 #include "kvq.cuh"
 #include "kvq_merge.cuh"
