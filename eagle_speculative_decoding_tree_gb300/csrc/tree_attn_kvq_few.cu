@@ -27,8 +27,8 @@
 //   a warp that issues every tcgen05.mma: QK0 QK1 | QK2 PV0 | QK3 PV1 | ...
 // (32 rows a thread instead of 16 take as many instructions, but at 2.5 warps a scheduler only
 // every second cycle issued one: 61.7 us against 58.0 for a chain of 8 over 128K.)
-// TMEM: S of four tiles (a column per row and term of Q, or per row), then O of the even and the odd tiles (a column per
-// row and term of P).
+// TMEM: S of four tiles (a column per row and term of Q, or per row), then O of the even and the odd
+// tiles (a column per row and term of P).
 // Measured (8 KV heads, 4 query heads each, graph replay): one token over 128K tokens 46 us (5.8
 // TB/s, 86 % of a device copy's rate), over 8K 9.7; a chain of 8 over 128K, fp32 and precise, 56.5 us,
 // 2 of them for Q's third term (the loop's waits and product issue take about as long a tile as HBM does).
@@ -78,7 +78,8 @@ struct Few {
   static constexpr int SM_K = SM_P + 2 * P1;
   static constexpr int SM_V = SM_K + ST * T8;
   static constexpr int SMEM = SM_V + ST * T8 + 1024;
-  static_assert(P1 % 1024 == 0 && SM_P % 1024 == 0 && SMEM <= 232448 - 4096 && 4 * NS + 2 * NP <= 512, "alignment of the rings, TMEM columns");
+  static_assert(P1 % 1024 == 0 && SM_P % 1024 == 0, "alignment of the rings");
+  static_assert(SMEM <= 232448 - 4096 && 4 * NS + 2 * NP <= 512, "shared memory, TMEM columns");
 };
 
 // Descriptor with the 32-byte swizzle (MN-major P: rows of 32 columns, 8 keys every `sbo` bytes,
