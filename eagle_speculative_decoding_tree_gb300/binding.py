@@ -34,7 +34,8 @@ EXPORTED_SYMBOLS = ("eagle_tree_build", "eagle_tree_attn", "eagle_accept", "eagl
                     "eagle_last_cuda_error_string", "eagle_tree_attn_plan", "eagle_accept_noalloc",
                     "eagle_selftest_ff_log", "eagle_lmhead_stats", "eagle_ttt_attn", "eagle_tree_build_head",
                     "eagle_kvq_write", "eagle_kvq_read", "eagle_kvq_commit", "eagle_tree_attn_kvq",
-                    "eagle_qk_norm_rope")
+                    "eagle_qk_norm_rope", "eagle_paged_write", "eagle_paged_commit", "eagle_paged_attn",
+                    "eagle_paged_weights", "eagle_paged_evict")
 
 
 class TreeDesc(ctypes.Structure):
@@ -102,6 +103,39 @@ class QkNormRopeDesc(ctypes.Structure):
                [("eps", ctypes.c_float), ("dtype", ctypes.c_int32)]
 
 
+EAGLE_WS_PAGED_ATTN, EAGLE_WS_PAGED_COMMIT, EAGLE_WS_PAGED_EVICT = 6, 7, 8
+EAGLE_STATUS_BAD_PAGE = 0x20
+
+
+class PagedDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "n_kv_heads", "head_dim", "page_size", "n_pages", "max_pages",
+                                              "rows", "dtype")]
+
+
+class PagedCommitDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("layers", "batch", "n_kv_heads", "head_dim", "page_size", "n_pages",
+                                              "max_pages", "rows", "max_depth", "dtype", "feat_dim", "feat_dtype")]
+
+
+class PagedAttnDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "rows", "n_q_heads", "n_kv_heads", "head_dim", "page_size",
+                                              "n_pages", "max_pages")] + \
+               [("scale", ctypes.c_float), ("softcap", ctypes.c_float)] + \
+               [(n, ctypes.c_int32) for n in ("window", "dtype", "out_dtype", "precision", "engine")]
+
+
+class PagedWeightsDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "rows", "n_q_heads", "n_kv_heads", "head_dim", "page_size",
+                                              "n_pages", "max_pages", "max_depth")] + \
+               [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class PagedEvictDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("layers", "batch", "n_kv_heads", "head_dim", "page_size", "n_pages",
+                                              "max_pages", "limit", "budget", "sink", "recent", "dtype")]
+
+
 # ----------------------------------------------------------------------------- loading
 _lib = None
 
@@ -136,6 +170,11 @@ def load() -> ctypes.CDLL:
         L.eagle_kvq_commit.argtypes = [ctypes.POINTER(CommitDesc)] + [vp] * 14
         L.eagle_tree_attn_kvq.argtypes = [ctypes.POINTER(AttnDesc)] + [vp] * 13 + [sz, vp]
         L.eagle_qk_norm_rope.argtypes = [ctypes.POINTER(QkNormRopeDesc)] + [vp] * 10
+        L.eagle_paged_write.argtypes = [ctypes.POINTER(PagedDesc)] + [vp] * 9
+        L.eagle_paged_commit.argtypes = [ctypes.POINTER(PagedCommitDesc)] + [vp] * 13 + [sz, vp]
+        L.eagle_paged_attn.argtypes = [ctypes.POINTER(PagedAttnDesc)] + [vp] * 14 + [sz, vp]
+        L.eagle_paged_weights.argtypes = [ctypes.POINTER(PagedWeightsDesc)] + [vp] * 12
+        L.eagle_paged_evict.argtypes = [ctypes.POINTER(PagedEvictDesc)] + [vp] * 9 + [sz, vp]
         L.eagle_workspace_size.argtypes = [i32, vp]
         L.eagle_workspace_size.restype = sz
         L.eagle_status_string.argtypes = [i32]
@@ -150,7 +189,8 @@ def load() -> ctypes.CDLL:
         for f in (L.eagle_tree_build, L.eagle_tree_build_head, L.eagle_tree_attn, L.eagle_accept, L.eagle_kv_commit,
                   L.eagle_tree_frontier_rows, L.eagle_tree_max_frontier, L.eagle_tree_attn_plan,
                   L.eagle_accept_noalloc, L.eagle_kvq_write, L.eagle_kvq_read, L.eagle_kvq_commit,
-                  L.eagle_tree_attn_kvq, L.eagle_qk_norm_rope):
+                  L.eagle_tree_attn_kvq, L.eagle_qk_norm_rope, L.eagle_paged_write, L.eagle_paged_commit,
+                  L.eagle_paged_attn, L.eagle_paged_weights, L.eagle_paged_evict):
             f.restype = ctypes.c_int
         _lib = L
     return _lib
@@ -366,6 +406,9 @@ class LayerPointers:
         self.k, self.v = mk(k_cache, "k_cache"), mk(v_cache, "v_cache")
         self.tk, self.tv = mk(tree_k, "tree_k"), mk(tree_v, "tree_v")
         self.tensors = (list(k_cache), list(v_cache), list(tree_k), list(tree_v))
+        every = [t for ts in self.tensors for t in ts]
+        self.layers = min(len(ts) for ts in self.tensors)
+        self.dtypes, self.devices = {t.dtype for t in every}, {t.get_device() for t in every}
 
 
 def eagle_kv_commit(desc: CommitDesc, layers: LayerPointers, n_acc, path, seq_len, commit_pos,
@@ -524,6 +567,106 @@ def eagle_tree_attn_kvq(desc: AttnDesc, q, k_codes, k_scale, v_codes, v_scale, t
         _at(n_nodes, torch.int32, "n_nodes", dev), _at(anc_mask, torch.int64, "anc_mask", dev),
         _at(out, _element(desc.out_dtype), "out", dev), _at(lse, torch.float32, "lse", dev),
         _at(ws, ws.dtype, "ws", dev), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+# ----------------------------------------------------------------------------- paged KV cache
+def eagle_paged_write(desc: PagedDesc, k, v, page_table, start, count: Optional[torch.Tensor], k_pages, v_pages,
+                      status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """K/V rows [B][Hkv][N][D] into the pages (see eagle.h: eagle_paged_write)."""
+    dev = _device()
+    dt = _element(desc.dtype)
+    _check("eagle_paged_write", load().eagle_paged_write(
+        ctypes.byref(desc), _at(k, dt, "k", dev), _at(v, dt, "v", dev), _at(page_table, torch.int32, "page_table", dev),
+        _at(start, torch.int32, "start", dev), _at(count, torch.int32, "count", dev), _at(k_pages, dt, "k_pages", dev),
+        _at(v_pages, dt, "v_pages", dev), _at(status, torch.int32, "status", dev), _stream(stream)))
+
+
+def eagle_paged_commit(desc: PagedCommitDesc, layers: LayerPointers, page_table, n_acc, path, seq_len, commit_pos, ws,
+                       feat_pages=None, tree_feat=None, status=None, stream=None) -> None:
+    """Commit the accepted path into pages (see eagle.h: eagle_paged_commit); layers: LayerPointers of every
+    layer's k_pages, v_pages, tree_k and tree_v."""
+    dev = _device()
+    _layers_fit(layers, desc.layers, dev, _element(desc.dtype))
+    f = _element(desc.feat_dtype)
+    _check("eagle_paged_commit", load().eagle_paged_commit(
+        ctypes.byref(desc), layers.k, layers.v, layers.tk, layers.tv, _at(page_table, torch.int32, "page_table", dev),
+        _at(n_acc, torch.int32, "n_acc", dev), _at(path, torch.int32, "path", dev),
+        _at(seq_len, torch.int32, "seq_len", dev), _at(commit_pos, torch.int32, "commit_pos", dev),
+        _at(feat_pages, f, "feat_pages", dev), _at(tree_feat, f, "tree_feat", dev),
+        _at(status, torch.int32, "status", dev), _at(ws, ws.dtype, "ws", dev), ws.numel() * ws.element_size(),
+        _stream(stream)))
+
+
+def eagle_paged_attn(desc: PagedAttnDesc, q, k_pages, v_pages, page_table, tree_k, tree_v, seq_len, anc_mask, out,
+                     lse: Optional[torch.Tensor], ws: torch.Tensor, stream=None,
+                     n_nodes: Optional[torch.Tensor] = None, slopes: Optional[torch.Tensor] = None,
+                     status: Optional[torch.Tensor] = None) -> None:
+    """One layer of attention over a paged cache (see eagle.h: eagle_paged_attn); tree_k, tree_v and anc_mask may
+    be None together."""
+    dev = _device()
+    dt = _element(desc.dtype)
+    _check("eagle_paged_attn", load().eagle_paged_attn(
+        ctypes.byref(desc), _at(q, dt, "q", dev), _at(k_pages, dt, "k_pages", dev), _at(v_pages, dt, "v_pages", dev),
+        _at(page_table, torch.int32, "page_table", dev), _at(tree_k, dt, "tree_k", dev), _at(tree_v, dt, "tree_v", dev),
+        _at(seq_len, torch.int32, "seq_len", dev), _at(n_nodes, torch.int32, "n_nodes", dev),
+        _at(anc_mask, torch.int64, "anc_mask", dev), _at(slopes, torch.float32, "slopes", dev),
+        _at(out, _element(desc.out_dtype), "out", dev), _at(lse, torch.float32, "lse", dev),
+        _at(status, torch.int32, "status", dev), _at(ws, ws.dtype, "ws", dev), ws.numel() * ws.element_size(),
+        _stream(stream)))
+
+
+def eagle_paged_weights(desc: PagedWeightsDesc, q, lse, k_pages, page_table, seq_len, n_acc: Optional[torch.Tensor],
+                        path: Optional[torch.Tensor], prior: Optional[torch.Tensor], weights, stream=None,
+                        slopes: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None) -> None:
+    """Accumulated attention weights of the cached tokens (see eagle.h: eagle_paged_weights)."""
+    dev = _device()
+    dt = _element(desc.dtype)
+    f32 = torch.float32
+    _check("eagle_paged_weights", load().eagle_paged_weights(
+        ctypes.byref(desc), _at(q, dt, "q", dev), _at(lse, f32, "lse", dev), _at(k_pages, dt, "k_pages", dev),
+        _at(page_table, torch.int32, "page_table", dev), _at(seq_len, torch.int32, "seq_len", dev),
+        _at(n_acc, torch.int32, "n_acc", dev), _at(path, torch.int32, "path", dev), _at(slopes, f32, "slopes", dev),
+        _at(prior, f32, "prior", dev), _at(weights, f32, "weights", dev), _at(status, torch.int32, "status", dev),
+        _stream(stream)))
+
+
+def _layers_fit(layers, n: int, dev: int, dtype) -> None:
+    """Layer pointers built once: as many layers as the descriptor says, its element type, the current device."""
+    if layers.layers < n:
+        raise ValueError(f"{n} layers, pointers of {layers.layers}")
+    if layers.devices != {dev}:
+        raise ValueError(f"layer tensors on devices {sorted(layers.devices)}, the current one is {dev}")
+    if layers.dtypes != {dtype} and dtype is not FLOATS:
+        raise ValueError("layer tensors are not of the descriptor's element type")
+
+
+class PagedLayerPointers:
+    """HOST arrays of per-layer device pointers for eagle_paged_evict (built once, reused)."""
+
+    def __init__(self, k_pages: Sequence[torch.Tensor], v_pages: Sequence[torch.Tensor],
+                 weights: Sequence[torch.Tensor]):
+        n = len(k_pages)
+        mk = lambda ts, dt, nm: (ctypes.c_void_p * n)(*[_ptr(t, dt, nm) for t in ts])
+        self.k, self.v, self.w = mk(k_pages, FLOATS, "k_pages"), mk(v_pages, FLOATS, "v_pages"), \
+            mk(weights, torch.float32, "weights")
+        self.tensors = [list(t) for t in (k_pages, v_pages, weights)]
+        if any(len(t) != n for t in self.tensors):
+            raise ValueError("as many tensors of each kind as layers")
+        self.layers, self.dtypes = n, {t.dtype for t in (*k_pages, *v_pages)}
+        self.devices = {t.get_device() for ts in self.tensors for t in ts}
+
+
+def eagle_paged_evict(desc: PagedEvictDesc, layers: PagedLayerPointers, page_table, spare, seq_len, kept, ws,
+                      status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Cut long requests down to their heaviest tokens (see eagle.h: eagle_paged_evict)."""
+    dev = _device()
+    _layers_fit(layers, desc.layers, dev, _element(desc.dtype))
+    i32 = torch.int32
+    _check("eagle_paged_evict", load().eagle_paged_evict(
+        ctypes.byref(desc), layers.k, layers.v, layers.w, _at(page_table, i32, "page_table", dev),
+        _at(spare, i32, "spare", dev), _at(seq_len, i32, "seq_len", dev), _at(kept, i32, "kept", dev),
+        _at(status, i32, "status", dev), _at(ws, ws.dtype, "ws", dev), ws.numel() * ws.element_size(),
+        _stream(stream)))
 
 
 # ----------------------------------------------------------------------------- norms and rotation

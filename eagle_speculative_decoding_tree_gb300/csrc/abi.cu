@@ -6,6 +6,7 @@
 
 #include "common.cuh"
 #include "launch.h"
+#include "paged.h"
 
 using namespace eagle;
 
@@ -197,6 +198,9 @@ size_t eagle_workspace_size(int which, const void* desc) {
     }
     case EAGLE_WS_TTT_ATTN:
       return check_ttt_desc(static_cast<const eagle_ttt_desc*>(desc)) == EAGLE_OK ? 256 : 0;
+    case EAGLE_WS_PAGED_ATTN:
+    case EAGLE_WS_PAGED_COMMIT:
+    case EAGLE_WS_PAGED_EVICT: return paged_workspace_size(which, desc);
     default: return 0;
   }
 }

@@ -83,6 +83,7 @@ enum {
 #define EAGLE_STATUS_PATH_OVERFLOW 0x2u /* accepted path deeper than max_depth: truncated */
 #define EAGLE_STATUS_CACHE_FULL 0x4u    /* seq_len + n_acc + 1 > max_seq: that request was not committed */
 #define EAGLE_STATUS_BAD_TOKEN 0x8u     /* a draft token outside [0, V): treated as rejected */
+#define EAGLE_STATUS_BAD_PAGE 0x20u     /* a page table entry outside [0, n_pages) */
 #define EAGLE_STATUS_TIMEOUT 0x10u      /* eagle_accept: a bounded wait between the CTAs of a request
                                            gave up (2 s); that request's outputs were not written */
 
@@ -124,7 +125,10 @@ enum {
   EAGLE_WS_TREE_ATTN = 2,
   EAGLE_WS_ACCEPT = 3,
   EAGLE_WS_TTT_ATTN = 4,
-  EAGLE_WS_TREE_ATTN_KVQ = 5 /* desc: eagle_attn_desc, as eagle_tree_attn_kvq takes it */
+  EAGLE_WS_TREE_ATTN_KVQ = 5, /* desc: eagle_attn_desc, as eagle_tree_attn_kvq takes it */
+  EAGLE_WS_PAGED_ATTN = 6,    /* desc: eagle_paged_attn_desc */
+  EAGLE_WS_PAGED_COMMIT = 7,  /* desc: eagle_paged_commit_desc */
+  EAGLE_WS_PAGED_EVICT = 8    /* desc: eagle_paged_evict_desc */
 };
 
 /* ---------------------------------------------------------------- tree build */
@@ -548,6 +552,175 @@ int eagle_kvq_commit(const eagle_commit_desc* d, void* const* k_codes_layers, fl
                      void* const* v_codes_layers, float* const* v_scale_layers, const void* const* tree_k_layers,
                      const void* const* tree_v_layers, const int32_t* n_acc, const int32_t* path, int32_t* seq_len,
                      int32_t* commit_pos, void* feat_cache, const void* tree_feat, uint32_t* status, void* stream);
+
+/* ---------------------------------------------------------------- paged KV cache */
+/* The prefix K/V cache in pages: requests of any length share one pool a layer, instead of each
+ * paying for the longest (the pages this library follows keep one contiguous run a request; they
+ * have no counterpart).  Per layer and for K and V each
+ *     pages      [n_pages][Hkv][T][D]   T = page_size tokens: 16, 32, 64 or 128
+ * and, for all layers together,
+ *     page_table int32 [B][max_pages]   cache row r of request b is row r % T of page
+ *                                       page_table[b][r / T]
+ * so a request holds up to max_pages * T rows.  Entries behind the rows that a call touches are
+ * not read.  An entry outside [0, n_pages) sets EAGLE_STATUS_BAD_PAGE; nothing is written for
+ * its rows, and readers take page 0 instead (that request's results are then not valid).
+ * Requests may share pages that are only read (a common prefix); a page that a call writes must
+ * belong to one request.  `status` (DEVICE, may be NULL) is ORed into; the caller clears it.
+ * Common limits: head_dim 64 or 128, B <= 65535, Hkv <= 1024, max_pages * T <= 2^31 - 256,
+ * n_pages * Hkv * T <= 2^31 - 256 (EAGLE_ERR_UNSUPPORTED otherwise). */
+typedef struct {
+  int32_t batch;      /* B */
+  int32_t n_kv_heads; /* Hkv */
+  int32_t head_dim;   /* D: 64 or 128 */
+  int32_t page_size;  /* T */
+  int32_t n_pages;    /* pages of the pool */
+  int32_t max_pages;  /* entries of a request's table */
+  int32_t rows;       /* N: rows per request of k / v; Hkv * N <= 2^30 */
+  int32_t dtype;      /* element type of k, v and the pages */
+} eagle_paged_desc;
+
+/* Rows 0 .. count[b] - 1 of k, v [B][Hkv][N][D] into cache rows start[b] .. start[b] + count[b] - 1
+ * (a prompt, a chunk of one, or a new token).  start [B], count [B] int32 DEVICE (count NULL: N rows
+ * each).  A request whose span is not inside [0, max_pages T], or whose count is not in [0, N], is
+ * left untouched and EAGLE_STATUS_CACHE_FULL is set. */
+int eagle_paged_write(const eagle_paged_desc* d, const void* k, const void* v, const int32_t* page_table,
+                      const int32_t* start, const int32_t* count, void* k_pages, void* v_pages, uint32_t* status,
+                      void* stream);
+
+typedef struct {
+  int32_t layers;      /* L, 1..128 */
+  int32_t batch;       /* B */
+  int32_t n_kv_heads;  /* Hkv */
+  int32_t head_dim;    /* D: 64 or 128 */
+  int32_t page_size;   /* T */
+  int32_t n_pages;     /* of every layer's pool */
+  int32_t max_pages;
+  int32_t rows;        /* R, 1..128 */
+  int32_t max_depth;   /* path arrays hold max_depth + 1 entries */
+  int32_t dtype;       /* K/V element type */
+  int32_t feat_dim;    /* feature row width; 0 = no feature rows */
+  int32_t feat_dtype;  /* feature element type */
+} eagle_paged_commit_desc;
+
+/* eagle_kv_commit into pages: tree row path[b][m] of tree_k/v_layers[l] ([B][Hkv][R][D]) to cache row
+ * seq_len[b] + m, m = 0..n_acc[b]; the feature rows tree_feat [B][R][F] to feat_pages [n_pages][T][F];
+ * commit_pos and seq_len as eagle_kv_commit, in the same launch.  A request whose commit would pass
+ * max_pages T is left untouched and flagged EAGLE_STATUS_CACHE_FULL.
+ *   k_pages_layers, v_pages_layers, tree_k_layers, tree_v_layers: HOST arrays of `layers` DEVICE pointers.
+ *   ws: eagle_workspace_size(EAGLE_WS_PAGED_COMMIT, d) bytes, zero-filled before its first use; calls leave
+ *   it zero.  One workspace serves one stream at a time. */
+int eagle_paged_commit(const eagle_paged_commit_desc* d, void* const* k_pages_layers, void* const* v_pages_layers,
+                       const void* const* tree_k_layers, const void* const* tree_v_layers,
+                       const int32_t* page_table, const int32_t* n_acc, const int32_t* path, int32_t* seq_len,
+                       int32_t* commit_pos, void* feat_pages, const void* tree_feat, uint32_t* status, void* ws,
+                       size_t ws_bytes, void* stream);
+
+typedef struct {
+  int32_t batch;       /* B; B * Hkv <= 65535 */
+  int32_t rows;        /* R: new tokens per request, 1..128 (1: one token; a chain; a draft tree) */
+  int32_t n_q_heads;   /* Hq, a multiple of n_kv_heads */
+  int32_t n_kv_heads;  /* Hkv */
+  int32_t head_dim;    /* D: 64 or 128 */
+  int32_t page_size;   /* T */
+  int32_t n_pages;
+  int32_t max_pages;
+  float scale;         /* softmax scale, usually 1/sqrt(D) */
+  float softcap;       /* c > 0: scores become c tanh(scale q.k / c); 0: none */
+  int32_t window;      /* w > 0: only keys at a distance below w; 0: all */
+  int32_t dtype;       /* element type of q, the pages and the tree K/V */
+  int32_t out_dtype;   /* element type of out: EAGLE_F32, or EAGLE_BF16 when dtype is EAGLE_BF16 */
+  int32_t precision;   /* EAGLE_ATTN_PRECISE or EAGLE_ATTN_FAST (ignored for fp32 inputs) */
+  int32_t engine;      /* EAGLE_ENGINE_AUTO, or EAGLE_ENGINE_MMA_SYNC: not the tcgen05 kernel */
+} eagle_paged_attn_desc;
+
+/* Attention of the new tokens over a paged cache.  Row i of request b, query head hq, attends to the
+ * prefix keys j < seq_len[b] of KV head hq / G and to the tree keys a < n_nodes[b] whose bit is set in
+ * anc_mask[b][i], as eagle_tree_attn, with scores
+ *     s = scale q.k;   s = c tanh(s / c) if softcap;   s = s - slopes[hq] * dist if slopes
+ * and only keys with dist < window if window > 0.  With depth_i = (bits of row i's mask among the
+ * n_nodes[b] first) - 1, node i stands at position seq_len[b] + depth_i: dist is seq_len[b] + depth_i - j
+ * to prefix key j, depth_i - depth_a to tree key a.  Distances count cache rows (after an eviction: the
+ * rows kept).
+ *   q [B][R][Hq][D]; k_pages, v_pages, page_table; tree_k, tree_v [B][Hkv][R][D] and anc_mask [B][R][W] as
+ *   eagle_tree_attn, or all three NULL: the new tokens attend to the prefix alone (their own K/V is in the
+ *   pages already; every row then counts as depth -1); seq_len [B] (clamped to [0, max_pages T]);
+ *   n_nodes [B], may be NULL; slopes [Hq] fp32 DEVICE, may be NULL; out [B][R][Hq][D]; lse [B][R][Hq] fp32,
+ *   may be NULL.  Rows i >= n_nodes[b] of out and lse are left untouched.
+ * A row with no key gets zeros and lse -inf.  Cache rows behind seq_len may hold anything; rows before it
+ * and the rows of existing nodes may take part in products with weight 0 where a mask or the window hides
+ * them, so a value there that is not finite spoils other rows.  Pages that lie wholly before the window of
+ * every row are not read.  fp32 sums and softmax; precision as eagle_tree_attn.
+ * ws: eagle_workspace_size(EAGLE_WS_PAGED_ATTN, d) bytes, zero-filled before its first use; one workspace
+ * serves one stream at a time, and any descriptors in turn that it is large enough for.  Its first 4 bytes
+ * are an error word that a bounded wait ORs a bit into when it gives up (2 s).
+ * Unsupported: the common limits, R > 128, Hq % Hkv != 0, bf16 out with fp32 inputs. */
+int eagle_paged_attn(const eagle_paged_attn_desc* d, const void* q, const void* k_pages, const void* v_pages,
+                     const int32_t* page_table, const void* tree_k, const void* tree_v, const int32_t* seq_len,
+                     const int32_t* n_nodes, const uint64_t* anc_mask, const float* slopes, void* out, float* lse,
+                     uint32_t* status, void* ws, size_t ws_bytes, void* stream);
+
+typedef struct {
+  int32_t batch;       /* B; B * Hkv <= 65535 */
+  int32_t rows;        /* R: rows per request of q and lse, 1..128 */
+  int32_t n_q_heads;   /* Hq, a multiple of n_kv_heads */
+  int32_t n_kv_heads;  /* Hkv */
+  int32_t head_dim;    /* D: 64 or 128 */
+  int32_t page_size;   /* T */
+  int32_t n_pages;
+  int32_t max_pages;
+  int32_t max_depth;   /* path arrays hold max_depth + 1 entries */
+  float scale, softcap; /* as the attention's */
+  int32_t window;
+  int32_t dtype;       /* element type of q and k_pages */
+} eagle_paged_weights_desc;
+
+/* What every cached token got of the accepted rows' attention, added up (the measure that eagle_paged_evict
+ * goes by).  Call it after the commit: the path's n = n_acc[b] + 1 rows are then the last of the seq_len[b]
+ * cache rows, and path row m stands at position p_m = seq_len[b] - n + m.  For every KV head h and row j < seq_len[b]:
+ *     weights[j] = prior[j] + sum over m with p_m >= j, query heads hq of h:  exp(s(m, hq, j) - lse[b][path[b][m]][hq])
+ * s as in eagle_paged_attn with dist = p_m - j; for the n newest rows prior counts as 0 and is not read.
+ *   q, lse: eagle_paged_attn's, [B][R][Hq][D] and [B][R][Hq] fp32; seq_len [B]: after the commit; n_acc [B],
+ *   path [B][max_depth+1] as eagle_accept wrote them, or both NULL: rows 0 .. R - 1 in order.
+ *   prior, weights: pages of fp32 [n_pages][Hkv][T] under the same table; prior NULL counts as 0; prior and
+ *   weights may be the same.  Rows j >= seq_len[b] of weights are left as they were.
+ * A request whose n_acc is not in [0, max_depth], whose path leaves [0, R) (EAGLE_STATUS_BAD_TREE) or whose
+ * seq_len is not in [n, max_pages T] (EAGLE_STATUS_CACHE_FULL) is left untouched. */
+int eagle_paged_weights(const eagle_paged_weights_desc* d, const void* q, const float* lse, const void* k_pages,
+                        const int32_t* page_table, const int32_t* seq_len, const int32_t* n_acc, const int32_t* path,
+                        const float* slopes, const float* prior, float* weights, uint32_t* status, void* stream);
+
+typedef struct {
+  int32_t layers;      /* L, 1..128; L * B * Hkv <= 2^24 */
+  int32_t batch;       /* B */
+  int32_t n_kv_heads;  /* Hkv */
+  int32_t head_dim;    /* D: 64 or 128 */
+  int32_t page_size;   /* T */
+  int32_t n_pages;     /* of every layer's pool */
+  int32_t max_pages;
+  int32_t limit;       /* requests with more rows than this are cut down, limit >= budget */
+  int32_t budget;      /* N >= 1: rows that are left */
+  int32_t sink;        /* first rows that always stay */
+  int32_t recent;      /* last rows that always stay; sink + recent <= budget */
+  int32_t dtype;       /* K/V element type */
+} eagle_paged_evict_desc;
+
+/* Cut every request with seq_len[b] > limit down to `budget` rows: each layer and KV head keeps the first
+ * `sink` rows, the last `recent` and those of the largest weights between them (the lower row first where
+ * weights are equal; NaN counts as the smallest), in their order.  K, V and weights of the kept rows move to
+ * the request's spare pages, which then change places with the first ceil(budget / T) entries of its table
+ * row, so that the pages it had are the spare ones of its next eviction; seq_len[b] = budget.  The old pages'
+ * contents stay.
+ *   k_pages_layers, v_pages_layers, weights_layers: HOST arrays of `layers` DEVICE pointers (weights: fp32 pages
+ *   [n_pages][Hkv][T]).  page_table [B][max_pages], spare [B][ceil(budget / T)], seq_len [B]: in and out;
+ *   kept int32 [L][B][Hkv][budget]: the kept rows' old numbers.
+ * Requests of at most `limit` rows are left as they are, kept and spare too; one of more than max_pages T
+ * rows is left and flagged EAGLE_STATUS_CACHE_FULL, one whose spare page is not in [0, n_pages) is left and
+ * flagged EAGLE_STATUS_BAD_PAGE.  A request's spare pages must not be among the pages of the call otherwise.
+ * ws: eagle_workspace_size(EAGLE_WS_PAGED_EVICT, d) bytes, zero-filled before its first use; calls leave it
+ * zero.  One workspace serves one stream at a time. */
+int eagle_paged_evict(const eagle_paged_evict_desc* d, void* const* k_pages_layers, void* const* v_pages_layers,
+                      float* const* weights_layers, int32_t* page_table, int32_t* spare, int32_t* seq_len,
+                      int32_t* kept, uint32_t* status, void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------- misc */
 /* Scratch bytes a call needs (which = EAGLE_WS_*, desc = the matching desc); 0 on a
