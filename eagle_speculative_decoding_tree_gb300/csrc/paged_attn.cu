@@ -16,18 +16,19 @@ constexpr int W = 8;    // warps
 constexpr int CK = 8;   // keys
 constexpr int ST = 3;   // ring stages of a warp
 
-template <typename T, int D, int RB>
+template <int D, int RB>
 struct Simt {
-  static constexpr int KB = CK * D * sizeof(T);     // bytes of a stage's K
+  static constexpr int KB = CK * D * 4;             // bytes of a stage's K
   static constexpr int FOLD = RB < 8 ? RB : 8;      // rows folded at a time
   static constexpr int SM_O = W * ST * 2 * KB;
   static constexpr int SM_M = SM_O + W * FOLD * D * 4;
   static constexpr int SMEM = SM_M + 2 * W * RB * 4;
 };
 
-template <typename T, int D, int RB, bool SHAPED>
+template <int D, int RB, bool SHAPED>
 __global__ void __launch_bounds__(W * 32, 1) paged_attn_simt_kernel(const PagedAttnArgs a) {
-  using S = Simt<T, D, RB>;
+  using S = Simt<D, RB>;
+  using T = float;
   constexpr int N = D / 32, RG = RB / 4;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[W][ST];
@@ -223,22 +224,22 @@ __global__ void __launch_bounds__(W * 32, 1) paged_attn_simt_kernel(const PagedA
   for (; used < issued; ++used) (void)sm100::wait_parity(&full[warp][used % ST], (used / ST) & 1, a.err, 1);
 }
 
-template <typename T, int D, int RB>
+template <int D, int RB>
 cudaError_t launch_simt(const PagedAttnArgs& a, bool shaped, int ctas, cudaStream_t s) {
   static unsigned long long conf[2] = {0, 0};
-  auto kern = shaped ? paged_attn_simt_kernel<T, D, RB, true> : paged_attn_simt_kernel<T, D, RB, false>;
-  const int smem = Simt<T, D, RB>::SMEM;
+  auto kern = shaped ? paged_attn_simt_kernel<D, RB, true> : paged_attn_simt_kernel<D, RB, false>;
+  const int smem = Simt<D, RB>::SMEM;
   const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kern), smem, conf[shaped]);
   return e != cudaSuccess ? e : launch_pdl(kern, dim3(ctas), dim3(W * 32), smem, s, a);
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_simt_rows(const PagedAttnArgs& a, bool shaped, int rows, int ctas, cudaStream_t s) {
-  return rows <= 4 ? launch_simt<T, D, 4>(a, shaped, ctas, s) : launch_simt<T, D, 16>(a, shaped, ctas, s);
+  return rows <= 4 ? launch_simt<D, 4>(a, shaped, ctas, s) : launch_simt<D, 16>(a, shaped, ctas, s);
 }
 
 constexpr size_t kHead = 256;  // the error word
-constexpr int kMaxRB = 16;
+constexpr int kMaxRB = 32;  // rows of a block, in every kernel
 
 }  // namespace
 
@@ -279,11 +280,11 @@ cudaError_t launch_paged_attn(const eagle_paged_attn_desc& d, const void* q, con
   a.out_f32 = d.out_dtype == EAGLE_F32;
   const bool shaped = d.softcap > 0.f || d.window > 0 || slopes;
   const int rows = d.rows * a.G;
-  if (d.dtype == EAGLE_F32)
-    return d.head_dim == 128 ? launch_simt_rows<float, 128>(a, shaped, rows, sms, s)
-                             : launch_simt_rows<float, 64>(a, shaped, rows, sms, s);
-  return d.head_dim == 128 ? launch_simt_rows<uint16_t, 128>(a, shaped, rows, sms, s)
-                           : launch_simt_rows<uint16_t, 64>(a, shaped, rows, sms, s);
+  if (d.dtype == EAGLE_BF16)
+    return launch_paged_attn_mma(a, d.head_dim, static_cast<long long>(d.n_pages) * d.n_kv_heads * d.page_size, shaped,
+                                 d.precision == EAGLE_ATTN_PRECISE, sms, s);
+  return d.head_dim == 128 ? launch_simt_rows<128>(a, shaped, rows, sms, s)
+                           : launch_simt_rows<64>(a, shaped, rows, sms, s);
 }
 
 }  // namespace eagle

@@ -39,6 +39,10 @@ struct PagedAttnArgs {
   int out_f32;
 };
 
+// paged_attn_mma.cu: bf16, row blocks of 16 (R G <= 16) or 32.
+cudaError_t launch_paged_attn_mma(const PagedAttnArgs& a, int head_dim, long long pool_rows, bool shaped, bool precise,
+                                  int ctas, cudaStream_t s);
+
 struct PagedRequest {
   int L, Rb;    // prefix and tree rows
   int k0;       // first key of the list (a multiple of 16)

@@ -1,4 +1,4 @@
-// tmap.h -- tensor maps of the 8-bit KV cache kernels (host).
+// tmap.h -- tensor maps of the 8-bit and the paged KV cache kernels (host).
 #pragma once
 
 #include <cuda.h>
@@ -29,6 +29,21 @@ inline bool make_tmap_2d(CUtensorMap* m, CUtensorMapDataType dt, int esz, const 
   const cuuint32_t es[2] = {1, 1};
   return fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows of `dim` (64 or 128) bf16 elements as [dim / 64][rows][64], boxes of all halves of `box_rows` rows, each
+// half's rows of 128 bytes swizzled; zero fill.
+inline bool make_tmap_halves(CUtensorMap* m, const void* base, int dim, unsigned long long rows, unsigned box_rows) {
+  auto fn = tmap_encode_fn();
+  if (!fn) return false;
+  const unsigned halves = static_cast<unsigned>(dim) / 64;
+  const cuuint64_t dims[3] = {64, rows, halves};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(dim) * 2, 128};
+  const cuuint32_t box[3] = {64, box_rows, halves};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace eagle
