@@ -174,16 +174,6 @@ __device__ __forceinline__ void load_part(const float* p, float (&x)[2]) {
   const float2 v = *reinterpret_cast<const float2*>(p);
   x[0] = v.x, x[1] = v.y;
 }
-__device__ __forceinline__ void load_part(const uint16_t* p, float (&x)[4]) {
-  const uint2 v = *reinterpret_cast<const uint2*>(p);
-  x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xffff0000u);
-  x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xffff0000u);
-}
-__device__ __forceinline__ void load_part(const uint16_t* p, float (&x)[2]) {
-  const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
-  x[0] = __uint_as_float(v << 16), x[1] = __uint_as_float(v & 0xffff0000u);
-}
-
 // 32 values a lane -> lane i gets the sum over the lanes of value i.
 __device__ __forceinline__ float spread_sum(float (&x)[32], int lane) {
 #pragma unroll

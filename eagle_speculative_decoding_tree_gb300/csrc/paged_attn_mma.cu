@@ -16,6 +16,7 @@
 #include <cstring>
 
 #include "paged_attn.cuh"
+#include "paged_mma.cuh"
 #include "tmap.h"
 
 namespace eagle {
@@ -42,39 +43,6 @@ struct Few {
 struct Maps {
   CUtensorMap k, v, tk, tv;  // rows of D as [D / 64][rows][64], boxes of 16 rows
 };
-
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-  const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&t);
-}
-
-// Bits of a mask row among the first n nodes.
-__device__ __forceinline__ int bits_below(const uint64_t* w, int words, int n) {
-  int c = 0;
-  for (int i = 0; i < words; ++i) {
-    const int live = n - 64 * i;
-    c += __popcll(live >= 64 ? w[i] : live > 0 ? w[i] & ((1ull << live) - 1) : 0ull);
-  }
-  return c;
-}
 
 template <int D, int MT, bool SHAPED, bool PRECISE>
 __global__ void __launch_bounds__(W * 32, 1)
