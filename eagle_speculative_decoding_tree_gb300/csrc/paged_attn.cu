@@ -45,14 +45,15 @@ __global__ void __launch_bounds__(W * 32, 1) paged_attn_simt_kernel(const PagedA
   __syncwarp();
   sm100::griddep_wait();
   sm100::griddep_launch_dependents();
-  PagedList list = paged_list(a, RB, blockIdx.x, gridDim.x);
+  PagedList list = paged_list(a, blockIdx.x, gridDim.x);
   const T* kg = static_cast<const T*>(a.k);
   const T* vg = static_cast<const T*>(a.v);
   int issued = 0, used = 0;  // chunks
   bool first = true, ok = true;
   while (list.at < list.end) {
-    const PagedSegment s = paged_next(a, list, RB);
-    const int pk = (s.rq.L - s.rq.k0 + 15) & ~15;               // list positions of the prefix
+    const PagedSegment s = paged_next(a, list);
+    if (s.t0 >= s.t1) continue;
+    const int pk = s.rq.pk;
     const int nk = pk + (a.tk ? s.rq.Rb : 0);
     const int c_end = min(s.t1 * kUnit, nk);
     // this warp's chunks: positions c0, c0 + W CK, ..
@@ -91,23 +92,16 @@ __global__ void __launch_bounds__(W * 32, 1) paged_attn_simt_kernel(const PagedA
     for (int r = 0; r < RB; ++r) {
 #pragma unroll
       for (int e = 0; e < N; ++e) q[r][e] = o[r][e] = 0.f;
-      if (s.rb * RB + r < n_rows)
-        load_part(static_cast<const T*>(a.q) + paged_out_row(a, s, s.rb * RB + r) * D + lane * N, q[r]);
+      if (s.row0 + r < n_rows)
+        load_part(static_cast<const T*>(a.q) + paged_out_row(a, s, s.row0 + r) * D + lane * N, q[r]);
     }
 #pragma unroll
     for (int g = 0; g < RG; ++g) {
       m[g] = -INFINITY;
       l[g] = 0.f;
-      const int row = min(s.rb * RB + 4 * g + (lane >> 3), n_rows - 1);
+      const int row = min(s.row0 + 4 * g + (lane >> 3), n_rows - 1);
       slope[g] = a.shape.slopes ? a.shape.slopes[s.h * a.G + row % a.G] * kLog2e : 0.f;
-      depth[g] = -1;
-      if (a.tk) {
-        const uint64_t* w = a.anc_mask + (static_cast<size_t>(s.b) * a.R + row / a.G) * a.W;
-        for (int i = 0; i < a.W; ++i) {
-          const int live = s.rq.Rb - 64 * i;
-          depth[g] += __popcll(live >= 64 ? w[i] : live > 0 ? w[i] & ((1ull << live) - 1) : 0ull);
-        }
-      }
+      depth[g] = a.tk ? paged_depth(a, s, row / a.G) : -1;
     }
     for (int at = c0; at < c_end; at += W * CK) {
       if (!wanted(at)) continue;
@@ -122,12 +116,7 @@ __global__ void __launch_bounds__(W * 32, 1) paged_attn_simt_kernel(const PagedA
       const int key = lane & 7;
       int kdepth = 0;  // of the lane's tree key
       if (tree && SHAPED && key < valid) {
-        const uint64_t* w = a.anc_mask + (static_cast<size_t>(s.b) * a.R + at - pk + key) * a.W;
-        kdepth = -1;
-        for (int i = 0; i < a.W; ++i) {
-          const int live = s.rq.Rb - 64 * i;
-          kdepth += __popcll(live >= 64 ? w[i] : live > 0 ? w[i] & ((1ull << live) - 1) : 0ull);
-        }
+        kdepth = paged_depth(a, s, at - pk + key);
       }
 #pragma unroll
       for (int g = 0; g < RG; ++g) {
@@ -145,7 +134,7 @@ __global__ void __launch_bounds__(W * 32, 1) paged_attn_simt_kernel(const PagedA
           }
         }
         const float raw = spread_sum(x, lane);
-        const int row = s.rb * RB + 4 * g + (lane >> 3);
+        const int row = s.row0 + 4 * g + (lane >> 3);
         bool on = key < valid && row < n_rows;
         int dist = s.rq.L + depth[g] - (s.rq.k0 + at + key);
         if (tree && on) {
@@ -203,7 +192,7 @@ __global__ void __launch_bounds__(W * 32, 1) paged_attn_simt_kernel(const PagedA
         s_l[warp * RB + 4 * g + (lane >> 3)] = x;
       }
     }
-    const bool whole = s.t0 == 0 && s.t1 == s.rq.units;
+    const bool whole = s.whole();
     const int slot = 2 * blockIdx.x + (first ? 0 : 1);
 #pragma unroll
     for (int f0 = 0; f0 < RB; f0 += S::FOLD) {
@@ -217,7 +206,7 @@ __global__ void __launch_bounds__(W * 32, 1) paged_attn_simt_kernel(const PagedA
         paged_fold_row<W, RB, D>(a, s, whole, slot, f0 + warp, lane, s_m, s_l, s_o + warp * D, S::FOLD * D);
       __syncthreads();
     }
-    if (!whole) paged_arrive<W, RB, D>(a, list, s, &s_last);
+    if (!whole) paged_arrive<W, RB, D>(a, s, &s_last);
     first = false;
   }
   // (a wait that gave up: nothing may still be landing)
@@ -225,8 +214,9 @@ __global__ void __launch_bounds__(W * 32, 1) paged_attn_simt_kernel(const PagedA
 }
 
 template <int D, int RB>
-cudaError_t launch_simt(const PagedAttnArgs& a, bool shaped, int ctas, cudaStream_t s) {
+cudaError_t launch_simt(PagedAttnArgs a, bool shaped, int ctas, cudaStream_t s) {
   static unsigned long long conf[2] = {0, 0};
+  a.rpb = RB;
   auto kern = shaped ? paged_attn_simt_kernel<D, RB, true> : paged_attn_simt_kernel<D, RB, false>;
   const int smem = Simt<D, RB>::SMEM;
   const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kern), smem, conf[shaped]);
@@ -239,13 +229,19 @@ cudaError_t launch_simt_rows(const PagedAttnArgs& a, bool shaped, int rows, int 
 }
 
 constexpr size_t kHead = 256;  // the error word
-constexpr int kMaxRB = 32;  // rows of a block, in every kernel
+
+// Draft trees go to the tensor cores proper, few rows to the kernels that are bound by the cache's bytes.
+bool use_tc(const eagle_paged_attn_desc& d) {
+  const int G = d.n_q_heads / d.n_kv_heads;
+  return d.dtype == EAGLE_BF16 && d.head_dim == 128 && G <= 128 && d.rows * G > 32 && d.engine == EAGLE_ENGINE_AUTO;
+}
+size_t slot_rows(const eagle_paged_attn_desc& d) { return use_tc(d) ? 128 : d.dtype == EAGLE_BF16 ? 32 : 16; }
 
 }  // namespace
 
 size_t paged_attn_ws(const eagle_paged_attn_desc& d, int sms) {
   const size_t slots = 2 * static_cast<size_t>(sms);
-  return kHead + slots * 16 + slots * kMaxRB * (static_cast<size_t>(d.head_dim) * 4 + 8);
+  return kHead + slots * 16 + slots * slot_rows(d) * (static_cast<size_t>(d.head_dim) * 4 + 8);
 }
 
 cudaError_t launch_paged_attn(const eagle_paged_attn_desc& d, const void* q, const void* k_pages, const void* v_pages,
@@ -270,16 +266,20 @@ cudaError_t launch_paged_attn(const eagle_paged_attn_desc& d, const void* q, con
   uint8_t* w = static_cast<uint8_t*>(ws);
   a.err = reinterpret_cast<int*>(w);
   a.count = reinterpret_cast<unsigned*>(w + kHead);
+  a.leave = a.count + slots;
   a.part_ml = reinterpret_cast<float*>(w + kHead + slots * 16);
-  a.part_o = a.part_ml + slots * kMaxRB * 2;
+  a.part_o = a.part_ml + slots * slot_rows(d) * 2;
   a.B = d.batch;
   a.R = d.rows;
   a.Hq = d.n_q_heads;
   a.G = d.n_q_heads / d.n_kv_heads;
   a.W = (d.rows + 63) / 64;
+  a.align = a.pad = 16;
   a.out_f32 = d.out_dtype == EAGLE_F32;
   const bool shaped = d.softcap > 0.f || d.window > 0 || slopes;
   const int rows = d.rows * a.G;
+  if (use_tc(d))
+    return launch_paged_attn_tc(a, d.n_pages, shaped, d.precision == EAGLE_ATTN_PRECISE, sms, s);
   if (d.dtype == EAGLE_BF16)
     return launch_paged_attn_mma(a, d.head_dim, static_cast<long long>(d.n_pages) * d.n_kv_heads * d.page_size, shaped,
                                  d.precision == EAGLE_ATTN_PRECISE, sms, s);

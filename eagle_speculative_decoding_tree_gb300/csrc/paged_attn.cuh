@@ -9,13 +9,16 @@
 // whole groups are written as they are, of the others the CTA leaves partials (row maxima, sums and
 // unnormalised outputs, fp32) in one of its two slots, and the group's last CTA to arrive (a counter) joins
 // them, in the order of the list: results do not depend on which one that is.  No CTA waits for another.
+// With kSplitFrom CTAs a group or more, shares end with the groups: each group has CTAs in proportion to its
+// units, and a CTA one segment.
 #pragma once
 
 #include "paged.cuh"
 
 namespace eagle {
 
-constexpr int kUnit = 128;  // keys
+constexpr int kUnit = 128;    // keys
+constexpr int kSplitFrom = 3; // CTAs a group from which each CTA has a part of one group only
 
 struct PagedAttnArgs {
   PagedGeom g;
@@ -33,55 +36,61 @@ struct PagedAttnArgs {
   uint32_t* status;
   int* err;
   unsigned* count;   // [2 CTAs]: arrivals, by the group's first CTA and its slot
+  unsigned* leave;   // [2 CTAs]: CTAs past their wait (tcgen05)
   float* part_o;     // [2 CTAs][RB][D]
   float* part_ml;    // [2 CTAs][RB][2]
   int B, R, Hq, G, W;
+  int rpb;           // rows of a block
+  int align, pad;    // the list's first key and the prefix's positions are multiples of these
   int out_f32;
 };
 
 // paged_attn_mma.cu: bf16, row blocks of 16 (R G <= 16) or 32.
-cudaError_t launch_paged_attn_mma(const PagedAttnArgs& a, int head_dim, long long pool_rows, bool shaped, bool precise,
+cudaError_t launch_paged_attn_mma(PagedAttnArgs a, int head_dim, long long pool_rows, bool shaped, bool precise,
                                   int ctas, cudaStream_t s);
+// paged_attn_tc.cu: bf16, head_dim 128, G <= 128, row blocks of 128 / G nodes.
+cudaError_t launch_paged_attn_tc(PagedAttnArgs a, int n_pages, bool shaped, bool precise, int ctas, cudaStream_t s);
 
 struct PagedRequest {
   int L, Rb;    // prefix and tree rows
-  int k0;       // first key of the list (a multiple of 16)
+  int k0;       // first key of the list
+  int pk;       // list positions of the prefix (the tree's keys come behind them)
   int units;    // per group
   int blocks;   // row blocks
 };
 
-__device__ __forceinline__ PagedRequest paged_request(const PagedAttnArgs& a, int b, int rows_per_block) {
+__device__ __forceinline__ PagedRequest paged_request(const PagedAttnArgs& a, int b) {
   PagedRequest r;
   r.L = min(max(a.seq_len[b], 0), a.g.capacity);
   r.Rb = a.n_nodes ? min(max(a.n_nodes[b], 0), a.R) : a.R;
-  // the row that stands furthest back is at depth 0, or -1 where its mask is empty
-  r.k0 = a.shape.window > 0 ? max(0, r.L - a.shape.window) & ~15 : 0;
-  const int keys = ((r.L - r.k0 + 15) & ~15) + (a.tk ? r.Rb : 0);
-  r.units = max(1, (keys + kUnit - 1) / kUnit);
-  r.blocks = (r.Rb * a.G + rows_per_block - 1) / rows_per_block;
+  // the row that stands furthest back is at depth 0 (without a tree: -1)
+  r.k0 = a.shape.window > 0 ? max(0, r.L - a.shape.window + (a.tk ? 1 : 0)) & ~(a.align - 1) : 0;
+  r.pk = (r.L - r.k0 + a.pad - 1) & ~(a.pad - 1);
+  r.units = max(1, (r.pk + (a.tk ? r.Rb : 0) + kUnit - 1) / kUnit);
+  r.blocks = (r.Rb * a.G + a.rpb - 1) / a.rpb;
   return r;
 }
 
-// A CTA's place in the list.  Every warp keeps its own copy, in step.
+// A part of a group that one CTA takes.
 struct PagedSegment {
-  int b, h, rb;        // group
+  int b, h, row0;      // group; its first row
   PagedRequest rq;
   int t0, t1;          // units of the group
-  long long first;     // the group's first unit in the list
+  int c0, c1;          // the group's first and last CTA
+  int slot0;           // the first CTA's slot; the others use theirs 0
+  __device__ bool whole() const { return t0 == 0 && t1 == rq.units; }
 };
 
+// A CTA's place in the list.  Every warp keeps its own copy, in step.
 struct PagedList {
-  long long total, at, end;
-  int ctas;            // CTAs with work: each has a unit or more
-  int b0;              // requests before this one (a multiple of 32) are done
+  long long total;     // units
+  int groups, ctas;    // ctas: those with work, each a unit or more
+  bool split;          // each CTA has a part of one group
+  long long at, end;   // units (split: at = the CTA, end = at + 1)
+  int b0;              // requests before this one (a multiple of 32) are done:
   long long base;      // their units
+  int gbase;           // and groups
 };
-
-__device__ __forceinline__ long long paged_request_units(const PagedAttnArgs& a, int b, int rows_per_block) {
-  if (b >= a.B) return 0;
-  const PagedRequest r = paged_request(a, b, rows_per_block);
-  return static_cast<long long>(r.units) * r.blocks * a.g.Hkv;
-}
 
 __device__ __forceinline__ long long shfl_ll(long long v, int lane) {
   const unsigned lo = __shfl_sync(0xffffffffu, static_cast<unsigned>(v), lane);
@@ -94,70 +103,125 @@ __device__ __forceinline__ long long list_start(long long total, int cta, int ct
 __device__ __forceinline__ int list_owner(long long total, long long u, int ctas) {
   return static_cast<int>(((u + 1) * ctas - 1) / total);
 }
+// split: the first CTA of group g, whose first unit is u: one a group, the others by units
+__device__ __forceinline__ int split_start(const PagedList& l, int g, long long u) {
+  return g + static_cast<int>((l.ctas - l.groups) * u / l.total);
+}
 
-__device__ __forceinline__ PagedList paged_list(const PagedAttnArgs& a, int rows_per_block, int cta, int ctas) {
+__device__ __forceinline__ PagedList paged_list(const PagedAttnArgs& a, int cta, int ctas) {
   const int lane = threadIdx.x & 31;
   long long mine = 0;
-  for (int b = lane; b < a.B; b += 32) mine += paged_request_units(a, b, rows_per_block);
+  int groups = 0;
+  for (int b = lane; b < a.B; b += 32) {
+    const PagedRequest r = paged_request(a, b);
+    groups += r.blocks * a.g.Hkv;
+    mine += static_cast<long long>(r.units) * r.blocks * a.g.Hkv;
+  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += shfl_ll(mine, lane ^ o);
+  for (int o = 16; o > 0; o >>= 1) {
+    mine += shfl_ll(mine, lane ^ o);
+    groups += __shfl_xor_sync(0xffffffffu, groups, o);
+  }
   PagedList l;
   l.total = mine;
+  l.groups = groups;
   l.ctas = static_cast<int>(min(static_cast<long long>(ctas), l.total));
+  l.split = groups * kSplitFrom <= l.ctas;
   l.at = l.end = 0;
   if (cta < l.ctas) {
-    l.at = list_start(l.total, cta, l.ctas);
-    l.end = list_start(l.total, cta + 1, l.ctas);
+    l.at = l.split ? cta : list_start(l.total, cta, l.ctas);
+    l.end = l.split ? cta + 1 : list_start(l.total, cta + 1, l.ctas);
   }
-  l.b0 = 0;
+  l.b0 = l.gbase = 0;
   l.base = 0;
   return l;
 }
 
 // The segment at l.at (l.at < l.end); l.at moves behind it.
-__device__ __forceinline__ PagedSegment paged_next(const PagedAttnArgs& a, PagedList& l, int rows_per_block) {
+__device__ __forceinline__ PagedSegment paged_next(const PagedAttnArgs& a, PagedList& l) {
   const int lane = threadIdx.x & 31;
   PagedSegment s;
+  long long first;   // the request's first unit, then the group's
+  int g;
   for (;;) {
-    const long long mine = paged_request_units(a, l.b0 + lane, rows_per_block);
-    long long inc = mine;
+    long long inc = 0;
+    int ginc = 0;
+    if (l.b0 + lane < a.B) {
+      const PagedRequest r = paged_request(a, l.b0 + lane);
+      ginc = r.blocks * a.g.Hkv;
+      inc = static_cast<long long>(r.units) * ginc;
+    }
+    const long long mine = inc;
+    const int gmine = ginc;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long x = shfl_ll(inc, max(lane - o, 0));
-      if (lane >= o) inc += x;
+      const int y = __shfl_sync(0xffffffffu, ginc, max(lane - o, 0));
+      if (lane >= o) {
+        inc += x;
+        ginc += y;
+      }
     }
-    const unsigned past = __ballot_sync(0xffffffffu, l.base + inc > l.at);
-    if (past || l.b0 + 32 >= a.B) {
-      const int at = past ? __ffs(past) - 1 : 31;
+    const long long past = l.split ? split_start(l, l.gbase + ginc, l.base + inc) : l.base + inc;
+    const unsigned m = __ballot_sync(0xffffffffu, past > l.at);
+    if (m || l.b0 + 32 >= a.B) {
+      const int at = m ? __ffs(m) - 1 : 31;
       s.b = min(l.b0 + at, a.B - 1);
-      s.first = l.base + shfl_ll(inc - mine, at);
+      first = l.base + shfl_ll(inc - mine, at);
+      g = l.gbase + __shfl_sync(0xffffffffu, ginc - gmine, at);
       break;
     }
     l.base += shfl_ll(inc, 31);
+    l.gbase += __shfl_sync(0xffffffffu, ginc, 31);
     l.b0 += 32;
   }
-  s.rq = paged_request(a, s.b, rows_per_block);
-  const int group = static_cast<int>((l.at - s.first) / s.rq.units);
-  s.first += static_cast<long long>(group) * s.rq.units;
-  s.h = group / max(1, s.rq.blocks);
-  s.rb = group - s.h * s.rq.blocks;
-  s.t0 = static_cast<int>(l.at - s.first);
-  s.t1 = static_cast<int>(min(static_cast<long long>(s.rq.units), s.t0 + (l.end - l.at)));
-  l.at += s.t1 - s.t0;
+  s.rq = paged_request(a, s.b);
+  const int n = s.rq.units;
+  int i;  // group of the request
+  if (l.split) {
+    int lo = 0, hi = s.rq.blocks * a.g.Hkv - 1;  // the last one that starts at this CTA or before
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (split_start(l, g + mid, first + static_cast<long long>(mid) * n) <= l.at)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    i = lo;
+    first += static_cast<long long>(i) * n;
+    s.c0 = split_start(l, g + i, first);
+    s.c1 = split_start(l, g + i + 1, first + n) - 1;
+    s.slot0 = 2 * s.c0;
+    // (a group of fewer units than CTAs: some have none, and nothing to leave)
+    const int k = min(s.c1 - s.c0 + 1, n), j = static_cast<int>(l.at) - s.c0;
+    s.c1 = s.c0 + k - 1;
+    s.t0 = j < k ? static_cast<int>(static_cast<long long>(n) * j / k) : n;
+    s.t1 = j < k ? static_cast<int>(static_cast<long long>(n) * (j + 1) / k) : n;
+    l.at = l.end;
+  } else {
+    i = static_cast<int>((l.at - first) / n);
+    first += static_cast<long long>(i) * n;
+    s.t0 = static_cast<int>(l.at - first);
+    s.t1 = static_cast<int>(min(static_cast<long long>(n), s.t0 + (l.end - l.at)));
+    l.at += s.t1 - s.t0;
+    s.c0 = list_owner(l.total, first, l.ctas);
+    s.c1 = list_owner(l.total, first + n - 1, l.ctas);
+    s.slot0 = 2 * s.c0 + (list_start(l.total, s.c0, l.ctas) == first ? 0 : 1);
+  }
+  s.h = i / s.rq.blocks;
+  s.row0 = (i - s.h * s.rq.blocks) * a.rpb;
   return s;
 }
 
-// Where a group's partials are.
-struct PagedJoin {
-  int c0, c1;  // first and last CTA
-  int slot0;   // the first CTA's slot; the others use theirs 0
-};
-__device__ __forceinline__ PagedJoin paged_join(const PagedList& l, const PagedSegment& s) {
-  PagedJoin j;
-  j.c0 = list_owner(l.total, s.first, l.ctas);
-  j.c1 = list_owner(l.total, s.first + s.rq.units - 1, l.ctas);
-  j.slot0 = 2 * j.c0 + (list_start(l.total, j.c0, l.ctas) == s.first ? 0 : 1);
-  return j;
+// How far a tree node stands behind the prefix: the bits of its mask row among the request's nodes, less one.
+__device__ __forceinline__ int paged_depth(const PagedAttnArgs& a, const PagedSegment& s, int node) {
+  const uint64_t* w = a.anc_mask + (static_cast<size_t>(s.b) * a.R + node) * a.W;
+  int c = 0;
+  for (int i = 0; i < a.W; ++i) {
+    const int live = s.rq.Rb - 64 * i;
+    c += __popcll(live >= 64 ? w[i] : live > 0 ? w[i] & ((1ull << live) - 1) : 0ull);
+  }
+  return max(c - 1, 0);
 }
 
 // A row's place in out ([B][R][Hq] rows) and lse.
@@ -229,7 +293,7 @@ __device__ __forceinline__ void paged_fold_row(const PagedAttnArgs& a, const Pag
 #pragma unroll
     for (int e = 0; e < N; ++e) o[e] = fmaf(f, s_o[w * step + lane * N + e], o[e]);
   }
-  const int at = s.rb * RB + row;
+  const int at = s.row0 + row;
   if (at >= s.rq.Rb * a.G) return;
   if (whole) {
     paged_store<D>(a, paged_out_row(a, s, at), lane, o, m, l);
@@ -244,18 +308,17 @@ __device__ __forceinline__ void paged_fold_row(const PagedAttnArgs& a, const Pag
 
 // A row of a group joined from its CTAs' slots, by one warp.
 template <int RB, int D>
-__device__ __forceinline__ void paged_join_row(const PagedAttnArgs& a, const PagedSegment& s, const PagedJoin& j,
-                                               int row, int lane) {
+__device__ __forceinline__ void paged_join_row(const PagedAttnArgs& a, const PagedSegment& s, int row, int lane) {
   constexpr int N = D / 32, BATCH = 8;
   float m = -INFINITY, l = 0.f, o[N];
 #pragma unroll
   for (int e = 0; e < N; ++e) o[e] = 0.f;
-  const int n = j.c1 - j.c0 + 1;
+  const int n = s.c1 - s.c0 + 1;
   for (int i0 = 0; i0 < n; i0 += 32) {
     const int mine = i0 + lane;
     float2 ml = make_float2(-INFINITY, 0.f);
     if (mine < n) {
-      const size_t slot = mine == 0 ? j.slot0 : 2 * (j.c0 + mine);
+      const size_t slot = mine == 0 ? s.slot0 : 2 * (s.c0 + mine);
       ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + (slot * RB + row) * 2));
     }
     const float top = fmaxf(m, warp_max(ml.x));
@@ -270,7 +333,7 @@ __device__ __forceinline__ void paged_join_row(const PagedAttnArgs& a, const Pag
 #pragma unroll
       for (int u = 0; u < BATCH; ++u) {
         const int i = min(i0 + u0 + u, n - 1);
-        const size_t slot = i == 0 ? j.slot0 : 2 * (j.c0 + i);
+        const size_t slot = i == 0 ? s.slot0 : 2 * (s.c0 + i);
         const float* po = a.part_o + (slot * RB + row) * D + lane * N;
 #pragma unroll
         for (int e = 0; e < N / 2; ++e) x[u][e] = __ldcg(reinterpret_cast<const float2*>(po) + e);
@@ -288,28 +351,26 @@ __device__ __forceinline__ void paged_join_row(const PagedAttnArgs& a, const Pag
       }
     }
   }
-  paged_store<D>(a, paged_out_row(a, s, s.rb * RB + row), lane, o, m, l);
+  paged_store<D>(a, paged_out_row(a, s, s.row0 + row), lane, o, m, l);
 }
 
 // The end of a segment whose group other CTAs share: this CTA's partials are written; the last CTA of the
 // group joins them.  By all W warps of the CTA (barrier 0).
 template <int W, int RB, int D>
-__device__ __forceinline__ void paged_arrive(const PagedAttnArgs& a, const PagedList& l, const PagedSegment& s,
-                                             int* s_last) {
-  const PagedJoin j = paged_join(l, s);
+__device__ __forceinline__ void paged_arrive(const PagedAttnArgs& a, const PagedSegment& s, int* s_last) {
   __threadfence();
   __syncthreads();
   if (threadIdx.x == 0) {
-    const unsigned n = j.c1 - j.c0 + 1;
-    const bool last = atomicAdd(a.count + j.slot0, 1u) == n - 1;
-    if (last) a.count[j.slot0] = 0;
+    const unsigned n = s.c1 - s.c0 + 1;
+    const bool last = atomicAdd(a.count + s.slot0, 1u) == n - 1;
+    if (last) a.count[s.slot0] = 0;
     __threadfence();
     *s_last = last;
   }
   __syncthreads();
   if (!*s_last) return;
-  const int rows = min(RB, s.rq.Rb * a.G - s.rb * RB);
-  for (int row = threadIdx.x >> 5; row < rows; row += W) paged_join_row<RB, D>(a, s, j, row, threadIdx.x & 31);
+  const int rows = min(RB, s.rq.Rb * a.G - s.row0);
+  for (int row = threadIdx.x >> 5; row < rows; row += W) paged_join_row<RB, D>(a, s, row, threadIdx.x & 31);
 }
 
 }  // namespace eagle

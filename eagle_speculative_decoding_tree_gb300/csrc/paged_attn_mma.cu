@@ -68,15 +68,16 @@ __global__ void __launch_bounds__(W * 32, 1)
   __syncwarp();
   sm100::griddep_wait();
   sm100::griddep_launch_dependents();
-  PagedList list = paged_list(a, F::RB, blockIdx.x, gridDim.x);
+  PagedList list = paged_list(a, blockIdx.x, gridDim.x);
   int issued = 0, used = 0;  // chunks
   bool first = true, ok = true;
   // ldmatrix addresses: K chunk (keys, then dims), V chunk (dims, then keys); a half of 64 dims is 16 rows of 128 bytes
   const int k_key = ((lane >> 4) << 3) + (lane & 7), k_c = (lane >> 3) & 1;
   const int v_key = (((lane >> 3) & 1) << 3) + (lane & 7), v_c = lane >> 4;
   while (list.at < list.end) {
-    const PagedSegment s = paged_next(a, list, F::RB);
-    const int pk = (s.rq.L - s.rq.k0 + 15) & ~15;
+    const PagedSegment s = paged_next(a, list);
+    if (s.t0 >= s.t1) continue;
+    const int pk = s.rq.pk;
     const int c_end = min(s.t1 * kUnit, pk + (a.tk ? s.rq.Rb : 0)), c0 = s.t0 * kUnit + warp * CK;
     // rows of the pool or of the tree where a chunk begins
     auto row_of = [&](int at) {
@@ -98,7 +99,7 @@ __global__ void __launch_bounds__(W * 32, 1)
     if (lane == 0 && next < c_end) next_row = row_of(next);  // (on its way while the first chunks are computed)
 
     // ---- rows
-    const int n_rows = s.rq.Rb * a.G, row0 = s.rb * F::RB;
+    const int n_rows = s.rq.Rb * a.G, row0 = s.row0;
     uint32_t qf[MT == 1 ? KS : 1][4];
     const uint16_t* qg = static_cast<const uint16_t*>(a.q);
     if (MT == 1) {
@@ -133,12 +134,8 @@ __global__ void __launch_bounds__(W * 32, 1)
         l[t][i] = 0.f;
         const int row = min(row0 + 16 * t + qr + 8 * i, n_rows - 1);
         slope[t][i] = 0.f;
-        depth[t][i] = -1;
-        if (SHAPED) {
-          if (a.shape.slopes) slope[t][i] = a.shape.slopes[s.h * a.G + row % a.G] * kLog2e;
-          if (a.tk)
-            depth[t][i] += bits_below(a.anc_mask + (static_cast<size_t>(s.b) * a.R + row / a.G) * a.W, a.W, s.rq.Rb);
-        }
+        depth[t][i] = SHAPED && a.tk ? paged_depth(a, s, row / a.G) : -1;
+        if (SHAPED && a.shape.slopes) slope[t][i] = a.shape.slopes[s.h * a.G + row % a.G] * kLog2e;
       }
     }
 
@@ -181,10 +178,7 @@ __global__ void __launch_bounds__(W * 32, 1)
 #pragma unroll
           for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int key = min(at - pk + 8 * n + 2 * qc + e, a.R - 1);
-              kd[n][e] = bits_below(a.anc_mask + (static_cast<size_t>(s.b) * a.R + key) * a.W, a.W, s.rq.Rb) - 1;
-            }
+            for (int e = 0; e < 2; ++e) kd[n][e] = paged_depth(a, s, min(at - pk + 8 * n + 2 * qc + e, a.R - 1));
         }
 #pragma unroll
         for (int t = 0; t < MT; ++t)
@@ -314,14 +308,14 @@ __global__ void __launch_bounds__(W * 32, 1)
         }
       }
     __syncthreads();
-    const bool whole = s.t0 == 0 && s.t1 == s.rq.units;
+    const bool whole = s.whole();
     const int slot = 2 * blockIdx.x + (first ? 0 : 1);
     for (int r = warp; r < F::RB && row0 + r < n_rows; r += W)
       paged_fold_row<W, F::RB, D>(a, s, whole, slot, r, lane, s_m, s_l, reinterpret_cast<float*>(smem) + r * F::LD,
                                   F::RING / 4);
     sm100::fence_proxy_async_smem();  // the ring is TMA's again
     if (!whole)
-      paged_arrive<W, F::RB, D>(a, list, s, &s_last);
+      paged_arrive<W, F::RB, D>(a, s, &s_last);
     else
       __syncthreads();
     first = false;
@@ -346,7 +340,7 @@ cudaError_t launch_mma_kind(const PagedAttnArgs& a, const Maps& tm, bool shaped,
 
 }  // namespace
 
-cudaError_t launch_paged_attn_mma(const PagedAttnArgs& a, int head_dim, long long pool_rows, bool shaped, bool precise,
+cudaError_t launch_paged_attn_mma(PagedAttnArgs a, int head_dim, long long pool_rows, bool shaped, bool precise,
                                   int ctas, cudaStream_t s) {
   Maps tm;
   const long long tree_rows = static_cast<long long>(a.B) * a.g.Hkv * a.R;
@@ -358,6 +352,7 @@ cudaError_t launch_paged_attn_mma(const PagedAttnArgs& a, int head_dim, long lon
                !make_tmap_halves(&tm.tv, a.tv, head_dim, tree_rows, CK)))
     return cudaErrorInvalidValue;
   const bool two = a.R * a.G > 16;
+  a.rpb = two ? 32 : 16;
   if (head_dim == 128)
     return two ? launch_mma_kind<128, 2>(a, tm, shaped, precise, ctas, s)
                : launch_mma_kind<128, 1>(a, tm, shaped, precise, ctas, s);

@@ -1,4 +1,4 @@
-// paged_mma.cuh -- warp-level matrix instructions and tree masks of the paged kernels.
+// paged_mma.cuh -- warp-level matrix instructions of the paged kernels.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -27,16 +27,6 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&t);
-}
-
-// Bits of a mask row among the first n nodes.
-__device__ __forceinline__ int bits_below(const uint64_t* w, int words, int n) {
-  int c = 0;
-  for (int i = 0; i < words; ++i) {
-    const int live = n - 64 * i;
-    c += __popcll(live >= 64 ? w[i] : live > 0 ? w[i] & ((1ull << live) - 1) : 0ull);
-  }
-  return c;
 }
 
 }  // namespace eagle

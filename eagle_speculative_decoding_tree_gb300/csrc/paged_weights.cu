@@ -61,12 +61,13 @@ __global__ void __launch_bounds__(W * 32) paged_weights_simt_kernel(const Weight
   __syncwarp();
   sm100::griddep_wait();
   sm100::griddep_launch_dependents();
-  PagedList list = paged_list(a.list, 1, blockIdx.x, gridDim.x);
+  PagedList list = paged_list(a.list, blockIdx.x, gridDim.x);
   const T* kg = static_cast<const T*>(a.list.k);
-  int issued = 0, used = 0, err = 0;
+  int issued = 0, used = 0;
   bool ok = true;
   while (list.at < list.end && ok) {
-    const PagedSegment s = paged_next(a.list, list, 1);
+    const PagedSegment s = paged_next(a.list, list);
+    if (s.t0 >= s.t1) continue;
     const int n = path_rows(a, s.b, lane);
     if (n == 0) continue;
     const int L = s.rq.L, c_end = min(s.t1 * kUnit, L), c0 = s.t0 * kUnit + warp * CK;
@@ -83,7 +84,7 @@ __global__ void __launch_bounds__(W * 32) paged_weights_simt_kernel(const Weight
     const int rows = n * a.G, key = lane & 7;
     for (int at = c0; at < c_end; at += W * CK) {
       const int stage = used % ST;
-      ok = __all_sync(0xffffffffu, sm100::wait_parity(&full[warp][stage], (used / ST) & 1, &err, 1));
+      ok = __all_sync(0xffffffffu, sm100::wait_parity(&full[warp][stage], (used / ST) & 1, nullptr, 0));
       if (!ok) break;
       ++used;
       const T* ks = reinterpret_cast<const T*>(ring + stage * KB);
@@ -132,8 +133,8 @@ __global__ void __launch_bounds__(W * 32) paged_weights_simt_kernel(const Weight
       }
     }
   }
-  for (; used < issued; ++used) (void)sm100::wait_parity(&full[warp][used % ST], (used / ST) & 1, &err, 1);
-  if (err && a.list.status) atomicOr(a.list.status, EAGLE_STATUS_TIMEOUT);
+  for (int i = used; i < issued; ++i) (void)sm100::wait_parity(&full[warp][i % ST], (i / ST) & 1, nullptr, 0);
+  if (!ok && lane == 0 && a.list.status) atomicOr(a.list.status, EAGLE_STATUS_TIMEOUT);
 }
 
 // ---------------------------------------------------------------- bf16
@@ -168,12 +169,13 @@ __global__ void __launch_bounds__(W * 32, 1)
   __syncwarp();
   sm100::griddep_wait();
   sm100::griddep_launch_dependents();
-  PagedList list = paged_list(a.list, 1, blockIdx.x, gridDim.x);
-  int issued = 0, used = 0, err = 0;
+  PagedList list = paged_list(a.list, blockIdx.x, gridDim.x);
+  int issued = 0, used = 0;
   bool ok = true;
   const int k_key = ((lane >> 4) << 3) + (lane & 7), k_c = (lane >> 3) & 1;
   while (list.at < list.end && ok) {
-    const PagedSegment s = paged_next(a.list, list, 1);
+    const PagedSegment s = paged_next(a.list, list);
+    if (s.t0 >= s.t1) continue;
     const int n = path_rows(a, s.b, lane);
     if (n == 0) continue;
     const int L = s.rq.L, c_end = min(s.t1 * kUnit, L), c0 = s.t0 * kUnit + warp * MK, rows = n * a.G;
@@ -217,7 +219,7 @@ __global__ void __launch_bounds__(W * 32, 1)
         }
       for (int at = c0; at < c_end; at += W * MK) {
         const int stage = used % F::ST;
-        ok = __all_sync(0xffffffffu, sm100::wait_parity(&full[warp][stage], (used / F::ST) & 1, &err, 1));
+        ok = __all_sync(0xffffffffu, sm100::wait_parity(&full[warp][stage], (used / F::ST) & 1, nullptr, 0));
         if (!ok) break;
         ++used;
         float sc[MT][2][4];
@@ -279,8 +281,8 @@ __global__ void __launch_bounds__(W * 32, 1)
       }
     }
   }
-  for (; used < issued; ++used) (void)sm100::wait_parity(&full[warp][used % F::ST], (used / F::ST) & 1, &err, 1);
-  if (err && a.list.status) atomicOr(a.list.status, EAGLE_STATUS_TIMEOUT);
+  for (int i = used; i < issued; ++i) (void)sm100::wait_parity(&full[warp][i % F::ST], (i / F::ST) & 1, nullptr, 0);
+  if (!ok && lane == 0 && a.list.status) atomicOr(a.list.status, EAGLE_STATUS_TIMEOUT);
 }
 
 template <int D, int MT, bool SHAPED>
@@ -319,7 +321,8 @@ cudaError_t launch_paged_weights(const eagle_paged_weights_desc& d, const void* 
   a.list.seq_len = seq_len;
   a.list.status = status;
   a.list.B = d.batch;
-  a.list.R = a.list.G = 1;
+  a.list.R = a.list.G = a.list.rpb = 1;
+  a.list.align = a.list.pad = 16;
   a.shape = score_shape(d.scale, d.softcap, d.window, slopes);
   a.q = q;
   a.lse = lse;

@@ -638,7 +638,7 @@ typedef struct {
  * anc_mask[b][i], as eagle_tree_attn, with scores
  *     s = scale q.k;   s = c tanh(s / c) if softcap;   s = s - slopes[hq] * dist if slopes
  * and only keys with dist < window if window > 0.  With depth_i = (bits of row i's mask among the
- * n_nodes[b] first) - 1, node i stands at position seq_len[b] + depth_i: dist is seq_len[b] + depth_i - j
+ * n_nodes[b] first) - 1 (0 for an empty row), node i stands at position seq_len[b] + depth_i: dist is seq_len[b] + depth_i - j
  * to prefix key j, depth_i - depth_a to tree key a.  Distances count cache rows (after an eviction: the
  * rows kept).
  *   q [B][R][Hq][D]; k_pages, v_pages, page_table; tree_k, tree_v [B][Hkv][R][D] and anc_mask [B][R][W] as

@@ -78,7 +78,7 @@ def attention(q, k, v, tk, tv, see, L, n, scale, cap=0.0, window=0, slopes=None,
     H, G = k.shape[0], q.shape[1] // k.shape[0]
     if tk is not None:
         see = see[:n, :n]
-        depth = see.sum(1) - 1
+        depth = np.maximum(see.sum(1) - 1, 0)
         k, v = np.concatenate((k, tk[:, :n]), 1), np.concatenate((v, tv[:, :n]), 1)
         dist = np.concatenate((L + depth[:, None] - np.arange(L), depth[:, None] - depth), 1)
         on = np.concatenate((np.ones((n, L), bool), see), 1)
