@@ -69,6 +69,7 @@ cudaError_t launch_paged_write(const eagle_paged_desc& d, const void* k, const v
                                const int32_t* start, const int32_t* count, void* k_pages, void* v_pages,
                                uint32_t* status, cudaStream_t s);
 
+size_t paged_commit_ws(const eagle_paged_commit_desc& d);
 cudaError_t launch_paged_commit(const eagle_paged_commit_desc& d, const CommitArgs& a, const int32_t* table,
                                 const int32_t* n_acc, const int32_t* path, int32_t* seq_len, int32_t* commit_pos,
                                 void* feat_pages, const void* tree_feat, uint32_t* status, void* ws, cudaStream_t s);
@@ -81,7 +82,7 @@ struct PagedEvictArgs {
 size_t paged_evict_ws(const eagle_paged_evict_desc& d);
 cudaError_t launch_paged_evict(const eagle_paged_evict_desc& d, const PagedEvictArgs& a, int32_t* table,
                                int32_t* spare, int32_t* seq_len, int32_t* kept, uint32_t* status, void* ws,
-                               cudaStream_t s);
+                               int sms, cudaStream_t s);
 
 cudaError_t launch_paged_weights(const eagle_paged_weights_desc& d, const void* q, const float* lse,
                                  const void* k_pages, const int32_t* table, const int32_t* seq_len,

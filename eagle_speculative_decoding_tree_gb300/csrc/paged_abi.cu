@@ -42,6 +42,12 @@ int check_scores(int rows, int hq, int hkv, float scale, float cap, int window, 
   return EAGLE_OK;
 }
 
+// The units that the kernels divide among themselves (128 keys of a row block of 16 or more) are counted in 32 bits.
+bool units_ok(int batch, int heads, long long rows, int max_pages, int page_size) {
+  const long long keys = static_cast<long long>(max_pages) * page_size / 128 + 2;
+  return static_cast<long long>(batch) * heads * ((rows + 15) / 16) <= 0x7fffffffll / keys;
+}
+
 int check_attn(const eagle_paged_attn_desc* d) {
   if (!d) return EAGLE_ERR_INVALID_ARG;
   int rc = check_paged_geometry(d->batch, d->n_kv_heads, d->head_dim, d->page_size, d->n_pages, d->max_pages);
@@ -51,7 +57,9 @@ int check_attn(const eagle_paged_attn_desc* d) {
       (d->engine != EAGLE_ENGINE_AUTO && d->engine != EAGLE_ENGINE_MMA_SYNC))
     return EAGLE_ERR_INVALID_ARG;
   if (!dtype_ok(d->out_dtype) || (d->dtype == EAGLE_F32 && d->out_dtype != EAGLE_F32) ||
-      static_cast<long long>(d->batch) * d->n_kv_heads > 65535)
+      static_cast<long long>(d->batch) * d->n_kv_heads > 65535 ||
+      !units_ok(d->batch, d->n_kv_heads, static_cast<long long>(d->rows) * (d->n_q_heads / d->n_kv_heads), d->max_pages,
+                d->page_size))
     return EAGLE_ERR_UNSUPPORTED;
   return EAGLE_OK;
 }
@@ -61,7 +69,9 @@ int check_weights(const eagle_paged_weights_desc* d) {
   int rc = check_paged_geometry(d->batch, d->n_kv_heads, d->head_dim, d->page_size, d->n_pages, d->max_pages);
   if (rc == EAGLE_OK) rc = check_scores(d->rows, d->n_q_heads, d->n_kv_heads, d->scale, d->softcap, d->window, d->dtype);
   if (rc != EAGLE_OK) return rc;
-  if (d->max_depth >= kMaxRows || static_cast<long long>(d->batch) * d->n_kv_heads > 65535) return EAGLE_ERR_UNSUPPORTED;
+  if (d->max_depth >= kMaxRows || static_cast<long long>(d->batch) * d->n_kv_heads > 65535 ||
+      !units_ok(d->batch, d->n_kv_heads, 1, d->max_pages, d->page_size))
+    return EAGLE_ERR_UNSUPPORTED;
   return EAGLE_OK;
 }
 
@@ -97,8 +107,10 @@ size_t eagle::paged_workspace_size(int which, const void* desc) {
     const eagle_paged_attn_desc* d = static_cast<const eagle_paged_attn_desc*>(desc);
     return check_attn(d) == EAGLE_OK ? paged_attn_ws(*d, sms()) : 0;
   }
-  if (which == EAGLE_WS_PAGED_COMMIT)
-    return check_commit(static_cast<const eagle_paged_commit_desc*>(desc)) == EAGLE_OK ? 16 : 0;
+  if (which == EAGLE_WS_PAGED_COMMIT) {
+    const eagle_paged_commit_desc* d = static_cast<const eagle_paged_commit_desc*>(desc);
+    return check_commit(d) == EAGLE_OK ? paged_commit_ws(*d) : 0;
+  }
   if (which == EAGLE_WS_PAGED_EVICT) {
     const eagle_paged_evict_desc* d = static_cast<const eagle_paged_evict_desc*>(desc);
     return check_evict(d) == EAGLE_OK ? paged_evict_ws(*d) : 0;
@@ -151,7 +163,7 @@ int eagle_paged_commit(const eagle_paged_commit_desc* d, void* const* k_pages_la
     const size_t need = bytes % 16 == 0 ? 16 : 2;
     if (!aligned(feat_pages, need) || !aligned(tree_feat, need)) return EAGLE_ERR_ALIGNMENT;
   }
-  if (!ws || ws_bytes < 16) return EAGLE_ERR_WORKSPACE;
+  if (!ws || ws_bytes < paged_commit_ws(*d)) return EAGLE_ERR_WORKSPACE;
   return report_cuda_error(launch_paged_commit(*d, a, page_table, n_acc, path, seq_len, commit_pos,
                                                d->feat_dim > 0 ? feat_pages : nullptr, tree_feat, status, ws,
                                                static_cast<cudaStream_t>(stream)));
@@ -213,7 +225,7 @@ int eagle_paged_evict(const eagle_paged_evict_desc* d, void* const* k_pages_laye
   }
   if (!ws || ws_bytes < paged_evict_ws(*d)) return EAGLE_ERR_WORKSPACE;
   return report_cuda_error(launch_paged_evict(*d, a, page_table, spare, seq_len, kept, status, ws,
-                                              static_cast<cudaStream_t>(stream)));
+                                              sms(), static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

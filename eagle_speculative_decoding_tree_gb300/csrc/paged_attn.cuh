@@ -81,132 +81,143 @@ struct PagedSegment {
   __device__ bool whole() const { return t0 == 0 && t1 == rq.units; }
 };
 
-// A CTA's place in the list.  Every warp keeps its own copy, in step.
+// A CTA's place in the list.  Every warp keeps its own copy, in step.  (Counts of units are 32-bit: the entry points
+// refuse more.)
 struct PagedList {
-  long long total;     // units
-  int groups, ctas;    // ctas: those with work, each a unit or more
+  int total, groups;   // units, groups
+  int ctas;            // CTAs with work: each a unit or more
+  int per, more;       // units a CTA, and how many CTAs have one more
   bool split;          // each CTA has a part of one group
-  long long at, end;   // units (split: at = the CTA, end = at + 1)
+  unsigned pace;       // split: CTAs a unit, 0.32 fixed point, behind one a group
+  int at, end;         // units (split: at = the CTA, end = at + 1)
   int b0;              // requests before this one (a multiple of 32) are done:
-  long long base;      // their units
-  int gbase;           // and groups
+  int base, gbase;     // their units and groups
+  int inc, ginc;       // the lane's request b0 + lane: units and groups up to it, from b0 on
 };
 
-__device__ __forceinline__ long long shfl_ll(long long v, int lane) {
-  const unsigned lo = __shfl_sync(0xffffffffu, static_cast<unsigned>(v), lane);
-  const unsigned hi = __shfl_sync(0xffffffffu, static_cast<unsigned>(static_cast<unsigned long long>(v) >> 32), lane);
-  return static_cast<long long>((static_cast<unsigned long long>(hi) << 32) | lo);
-}
-
-__device__ __forceinline__ long long list_start(long long total, int cta, int ctas) { return total * cta / ctas; }
+__device__ __forceinline__ int list_start(const PagedList& l, int cta) { return cta * l.per + min(cta, l.more); }
 // the CTA that has unit u
-__device__ __forceinline__ int list_owner(long long total, long long u, int ctas) {
-  return static_cast<int>(((u + 1) * ctas - 1) / total);
+__device__ __forceinline__ int list_owner(const PagedList& l, int u) {
+  const int k = l.more * (l.per + 1);
+  return u < k ? u / (l.per + 1) : l.more + (u - k) / l.per;
 }
 // split: the first CTA of group g, whose first unit is u: one a group, the others by units
-__device__ __forceinline__ int split_start(const PagedList& l, int g, long long u) {
-  return g + static_cast<int>((l.ctas - l.groups) * u / l.total);
+__device__ __forceinline__ int split_start(const PagedList& l, int g, int u) {
+  return g + min(static_cast<int>(__umulhi(static_cast<unsigned>(u), l.pace)), l.ctas - l.groups);
+}
+
+// inc, ginc of the 32 requests from l.b0 on
+__device__ __forceinline__ void list_scan(const PagedAttnArgs& a, PagedList& l) {
+  const int lane = threadIdx.x & 31;
+  l.inc = l.ginc = 0;
+  if (l.b0 + lane < a.B) {
+    const PagedRequest r = paged_request(a, l.b0 + lane);
+    l.ginc = r.blocks * a.g.Hkv;
+    l.inc = r.units * l.ginc;
+  }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, l.inc, o), y = __shfl_up_sync(0xffffffffu, l.ginc, o);
+    if (lane >= o) {
+      l.inc += x;
+      l.ginc += y;
+    }
+  }
 }
 
 __device__ __forceinline__ PagedList paged_list(const PagedAttnArgs& a, int cta, int ctas) {
-  const int lane = threadIdx.x & 31;
-  long long mine = 0;
-  int groups = 0;
-  for (int b = lane; b < a.B; b += 32) {
-    const PagedRequest r = paged_request(a, b);
-    groups += r.blocks * a.g.Hkv;
-    mine += static_cast<long long>(r.units) * r.blocks * a.g.Hkv;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    mine += shfl_ll(mine, lane ^ o);
-    groups += __shfl_xor_sync(0xffffffffu, groups, o);
-  }
   PagedList l;
-  l.total = mine;
-  l.groups = groups;
-  l.ctas = static_cast<int>(min(static_cast<long long>(ctas), l.total));
-  l.split = groups * kSplitFrom <= l.ctas;
-  l.at = l.end = 0;
-  if (cta < l.ctas) {
-    l.at = l.split ? cta : list_start(l.total, cta, l.ctas);
-    l.end = l.split ? cta + 1 : list_start(l.total, cta + 1, l.ctas);
+  l.total = l.groups = 0;
+  for (l.b0 = a.B > 32 ? 32 : a.B; l.b0 < a.B; l.b0 += 32) {  // all but the first 32
+    list_scan(a, l);
+    l.total += __shfl_sync(0xffffffffu, l.inc, 31);
+    l.groups += __shfl_sync(0xffffffffu, l.ginc, 31);
   }
-  l.b0 = l.gbase = 0;
-  l.base = 0;
+  l.b0 = l.base = l.gbase = 0;
+  list_scan(a, l);
+  l.total += __shfl_sync(0xffffffffu, l.inc, 31);
+  l.groups += __shfl_sync(0xffffffffu, l.ginc, 31);
+  l.ctas = min(ctas, l.total);
+  l.split = l.groups * kSplitFrom <= l.ctas;
+  l.per = l.more = l.at = l.end = 0;
+  l.pace = 0;
+  if (cta >= l.ctas) return l;
+  if (l.split) {
+    // a little above (ctas - groups) / total 2^32: equal groups get equal numbers
+    l.pace = static_cast<unsigned>(static_cast<float>(l.ctas - l.groups) / static_cast<float>(l.total) * 4294972000.f);
+    l.at = cta;
+    l.end = cta + 1;
+  } else {
+    l.per = l.total / l.ctas;
+    l.more = l.total - l.per * l.ctas;
+    l.at = list_start(l, cta);
+    l.end = list_start(l, cta + 1);
+  }
   return l;
 }
 
-// The segment at l.at (l.at < l.end); l.at moves behind it.
+// The segment at l.at (l.at < l.end); l.at moves behind it.  It may be empty (t0 = t1).
 __device__ __forceinline__ PagedSegment paged_next(const PagedAttnArgs& a, PagedList& l) {
-  const int lane = threadIdx.x & 31;
   PagedSegment s;
-  long long first;   // the request's first unit, then the group's
-  int g;
+  int first, g, prev, gprev;  // the request's first unit and group
   for (;;) {
-    long long inc = 0;
-    int ginc = 0;
-    if (l.b0 + lane < a.B) {
-      const PagedRequest r = paged_request(a, l.b0 + lane);
-      ginc = r.blocks * a.g.Hkv;
-      inc = static_cast<long long>(r.units) * ginc;
-    }
-    const long long mine = inc;
-    const int gmine = ginc;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = shfl_ll(inc, max(lane - o, 0));
-      const int y = __shfl_sync(0xffffffffu, ginc, max(lane - o, 0));
-      if (lane >= o) {
-        inc += x;
-        ginc += y;
-      }
-    }
-    const long long past = l.split ? split_start(l, l.gbase + ginc, l.base + inc) : l.base + inc;
+    const int past = l.split ? split_start(l, l.gbase + l.ginc, l.base + l.inc) : l.base + l.inc;
     const unsigned m = __ballot_sync(0xffffffffu, past > l.at);
-    if (m || l.b0 + 32 >= a.B) {
-      const int at = m ? __ffs(m) - 1 : 31;
-      s.b = min(l.b0 + at, a.B - 1);
-      first = l.base + shfl_ll(inc - mine, at);
-      g = l.gbase + __shfl_sync(0xffffffffu, ginc - gmine, at);
+    const bool last = l.b0 + 32 >= a.B;
+    if (m || last) {
+      // (split: a CTA behind the last group's is given that group, and finds nothing there)
+      int at = m ? __ffs(m) - 1 : 31;
+      if (!m) at = __ffs(__ballot_sync(0xffffffffu, l.ginc == __shfl_sync(0xffffffffu, l.ginc, 31))) - 1;
+      prev = __shfl_sync(0xffffffffu, l.inc, max(at - 1, 0));
+      gprev = __shfl_sync(0xffffffffu, l.ginc, max(at - 1, 0));
+      s.b = l.b0 + at;
+      first = l.base + (at ? prev : 0);
+      g = l.gbase + (at ? gprev : 0);
       break;
     }
-    l.base += shfl_ll(inc, 31);
-    l.gbase += __shfl_sync(0xffffffffu, ginc, 31);
+    l.base += __shfl_sync(0xffffffffu, l.inc, 31);
+    l.gbase += __shfl_sync(0xffffffffu, l.ginc, 31);
     l.b0 += 32;
+    list_scan(a, l);
   }
   s.rq = paged_request(a, s.b);
   const int n = s.rq.units;
   int i;  // group of the request
+  if (s.rq.blocks == 0) {  // (the last requests have no rows, and the CTA is behind the last group's)
+    s.h = s.row0 = s.t0 = s.t1 = s.c0 = s.c1 = s.slot0 = 0;
+    l.at = l.end;
+    return s;
+  }
   if (l.split) {
     int lo = 0, hi = s.rq.blocks * a.g.Hkv - 1;  // the last one that starts at this CTA or before
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (split_start(l, g + mid, first + static_cast<long long>(mid) * n) <= l.at)
+      if (split_start(l, g + mid, first + mid * n) <= l.at)
         lo = mid;
       else
         hi = mid - 1;
     }
     i = lo;
-    first += static_cast<long long>(i) * n;
+    first += i * n;
     s.c0 = split_start(l, g + i, first);
     s.c1 = split_start(l, g + i + 1, first + n) - 1;
     s.slot0 = 2 * s.c0;
     // (a group of fewer units than CTAs: some have none, and nothing to leave)
-    const int k = min(s.c1 - s.c0 + 1, n), j = static_cast<int>(l.at) - s.c0;
+    const int k = min(s.c1 - s.c0 + 1, n), j = l.at - s.c0;
     s.c1 = s.c0 + k - 1;
-    s.t0 = j < k ? static_cast<int>(static_cast<long long>(n) * j / k) : n;
-    s.t1 = j < k ? static_cast<int>(static_cast<long long>(n) * (j + 1) / k) : n;
+    const int q = n / k, r = n - q * k;
+    s.t0 = j < k ? j * q + min(j, r) : n;
+    s.t1 = j < k ? s.t0 + q + (j < r ? 1 : 0) : n;
     l.at = l.end;
   } else {
-    i = static_cast<int>((l.at - first) / n);
-    first += static_cast<long long>(i) * n;
-    s.t0 = static_cast<int>(l.at - first);
-    s.t1 = static_cast<int>(min(static_cast<long long>(n), s.t0 + (l.end - l.at)));
+    i = (l.at - first) / n;
+    first += i * n;
+    s.t0 = l.at - first;
+    s.t1 = min(n, s.t0 + (l.end - l.at));
     l.at += s.t1 - s.t0;
-    s.c0 = list_owner(l.total, first, l.ctas);
-    s.c1 = list_owner(l.total, first + n - 1, l.ctas);
-    s.slot0 = 2 * s.c0 + (list_start(l.total, s.c0, l.ctas) == first ? 0 : 1);
+    s.c0 = list_owner(l, first);
+    s.c1 = list_owner(l, first + n - 1);
+    s.slot0 = 2 * s.c0 + (list_start(l, s.c0) == first ? 0 : 1);
   }
   s.h = i / s.rq.blocks;
   s.row0 = (i - s.h * s.rq.blocks) * a.rpb;
@@ -306,52 +317,66 @@ __device__ __forceinline__ void paged_fold_row(const PagedAttnArgs& a, const Pag
   }
 }
 
-// A row of a group joined from its CTAs' slots, by one warp.
-template <int RB, int D>
-__device__ __forceinline__ void paged_join_row(const PagedAttnArgs& a, const PagedSegment& s, int row, int lane) {
-  constexpr int N = D / 32, BATCH = 8;
-  float m = -INFINITY, l = 0.f, o[N];
-#pragma unroll
-  for (int e = 0; e < N; ++e) o[e] = 0.f;
+// ROWS rows of a group joined from its CTAs' slots, by one warp: rows row, row + step, .. (those below `rows`).
+// The partial rows of BATCH CTAs are requested before their weights are known.
+template <int RB, int D, int ROWS, int BATCH>
+__device__ __forceinline__ void paged_join_rows(const PagedAttnArgs& a, const PagedSegment& s, int row, int step,
+                                                int rows, int lane) {
+  constexpr int N = D / 32;
   const int n = s.c1 - s.c0 + 1;
-  for (int i0 = 0; i0 < n; i0 += 32) {
+  float m[ROWS], l[ROWS], o[ROWS][N];
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k) {
+    m[k] = -INFINITY;
+    l[k] = 0.f;
+#pragma unroll
+    for (int e = 0; e < N; ++e) o[k][e] = 0.f;
+  }
+  auto slot_of = [&](int i) { return static_cast<size_t>(i == 0 ? s.slot0 : 2 * (s.c0 + i)) * RB; };
+#pragma unroll 1
+  for (int i0 = 0; i0 < n; i0 += BATCH) {
+    float2 x[ROWS][BATCH][N / 2], ml[ROWS];
     const int mine = i0 + lane;
-    float2 ml = make_float2(-INFINITY, 0.f);
-    if (mine < n) {
-      const size_t slot = mine == 0 ? s.slot0 : 2 * (s.c0 + mine);
-      ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + (slot * RB + row) * 2));
-    }
-    const float top = fmaxf(m, warp_max(ml.x));
-    const float old = m == -INFINITY ? 0.f : sm100::ex2(m - top);
-    const float f = ml.x == -INFINITY ? 0.f : sm100::ex2(ml.x - top);
-    m = top;
-    l = fmaf(l, old, warp_sum(f * ml.y));
 #pragma unroll
-    for (int e = 0; e < N; ++e) o[e] *= old;
-    for (int u0 = 0; u0 < 32 && i0 + u0 < n; u0 += BATCH) {
-      float2 x[BATCH][N / 2];
+    for (int k = 0; k < ROWS; ++k) {
+      const int r = min(row + k * step, rows - 1);
+      ml[k] = make_float2(-INFINITY, 0.f);
+      if (lane < BATCH && mine < n) ml[k] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + (slot_of(mine) + r) * 2));
 #pragma unroll
       for (int u = 0; u < BATCH; ++u) {
-        const int i = min(i0 + u0 + u, n - 1);
-        const size_t slot = i == 0 ? s.slot0 : 2 * (s.c0 + i);
-        const float* po = a.part_o + (slot * RB + row) * D + lane * N;
+        const float2* po =
+            reinterpret_cast<const float2*>(a.part_o + (slot_of(min(i0 + u, n - 1)) + r) * D + lane * N);
 #pragma unroll
-        for (int e = 0; e < N / 2; ++e) x[u][e] = __ldcg(reinterpret_cast<const float2*>(po) + e);
+        for (int e = 0; e < N / 2; ++e) x[k][u][e] = __ldcg(po + e);
       }
+    }
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      const float top = fmaxf(m[k], warp_max(ml[k].x));
+      const float old = m[k] == -INFINITY ? 0.f : sm100::ex2(m[k] - top);
+      const float f = ml[k].x == -INFINITY ? 0.f : sm100::ex2(ml[k].x - top);
+      m[k] = top;
+      l[k] = fmaf(l[k], old, warp_sum(f * ml[k].y));
+#pragma unroll
+      for (int e = 0; e < N; ++e) o[k][e] *= old;
 #pragma unroll
       for (int u = 0; u < BATCH; ++u) {
-        const float g = __shfl_sync(0xffffffffu, f, (u0 + u) & 31);
-        if (i0 + u0 + u < n) {
+        const float g = __shfl_sync(0xffffffffu, f, u);
+        if (i0 + u < n) {  // (the others' row is there twice)
 #pragma unroll
           for (int e = 0; e < N / 2; ++e) {
-            o[2 * e] = fmaf(g, x[u][e].x, o[2 * e]);
-            o[2 * e + 1] = fmaf(g, x[u][e].y, o[2 * e + 1]);
+            o[k][2 * e] = fmaf(g, x[k][u][e].x, o[k][2 * e]);
+            o[k][2 * e + 1] = fmaf(g, x[k][u][e].y, o[k][2 * e + 1]);
           }
         }
       }
     }
   }
-  paged_store<D>(a, paged_out_row(a, s, s.row0 + row), lane, o, m, l);
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k) {
+    const int r = row + k * step;
+    if (r < rows) paged_store<D>(a, paged_out_row(a, s, s.row0 + r), lane, o[k], m[k], l[k]);
+  }
 }
 
 // The end of a segment whose group other CTAs share: this CTA's partials are written; the last CTA of the
@@ -370,7 +395,8 @@ __device__ __forceinline__ void paged_arrive(const PagedAttnArgs& a, const Paged
   __syncthreads();
   if (!*s_last) return;
   const int rows = min(RB, s.rq.Rb * a.G - s.row0);
-  for (int row = threadIdx.x >> 5; row < rows; row += W) paged_join_row<RB, D>(a, s, row, threadIdx.x & 31);
+  for (int row = threadIdx.x >> 5; row < rows; row += W)
+    paged_join_rows<RB, D, 1, 20>(a, s, row, W, rows, threadIdx.x & 31);
 }
 
 }  // namespace eagle

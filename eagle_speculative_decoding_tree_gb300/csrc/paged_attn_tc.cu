@@ -463,7 +463,8 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
         atomicExch(a.leave + s.slot0, 0u);
       }
       const int rows = min(a.rpb, s.rq.Rb * a.G - s.row0), me = static_cast<int>(blockIdx.x) - s.c0;
-      for (int r = rows * me / n + warp; r < rows * (me + 1) / n; r += 8) paged_join_row<RB, 128>(a, s, r, lane);
+      const int hi = rows * (me + 1) / n;
+      for (int r = rows * me / n + warp; r < hi; r += 16) paged_join_rows<RB, 128, 2, 10>(a, s, r, 8, hi, lane);
     }
   }
   tc_fence_before();

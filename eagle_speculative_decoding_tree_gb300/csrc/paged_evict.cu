@@ -1,13 +1,14 @@
 // paged_evict.cu -- eviction from a paged cache by accumulated attention weight (eagle_paged_evict).
 //
-//   select   one CTA per (layer, request, KV head): the `need` heaviest of the rows between the first `sink`
+//   select   one CTA per (request, layer, KV head): the `need` heaviest of the rows between the first `sink`
 //            and the last `recent`.  Weights become 32-bit keys in the same order; the key of the last one
-//            kept is found bit by bit from the top (a radix select: 11, 11 and 10 bits, a histogram in shared
-//            memory each), and one more pass writes the kept rows' numbers in order.  The keys stay in shared
-//            memory when they fit, so that the weights are read once.
-//   move     32 kept rows of K and V a CTA (16 KB in flight) to the request's spare pages.  Out of place:
-//            rows need no order among themselves, and what another request shares stays as it is.  The last
-//            CTA of a request to finish swaps the pages and sets the length.
+//            kept is found from the top (a radix select: 11, 11 and 10 bits, a histogram in shared memory
+//            each), and one more pass writes the kept rows' numbers in order.  The keys stay in shared memory
+//            when they fit, so that the weights are read once, four a load and all loads of a thread together.
+//   move     each CTA takes an even share of all requests' pieces of 32 kept rows; 16 KB of K and V are in
+//            flight a piece, and the next piece's rows are looked up under them.  Out of place, to the
+//            request's spare pages: rows need no order among themselves, and what another request shares
+//            stays as it is.  The last CTA of a request to finish swaps the pages and sets the length.
 // Bound by the kept rows' bytes, read and written once.
 #include "paged.cuh"
 
@@ -20,7 +21,8 @@ constexpr int BINS = 2048;
 constexpr int KEYS = 24576;        // keys held in shared memory (96 KB: two CTAs an SM)
 constexpr int SELECT_SMEM = KEYS * 4;
 constexpr int MT = 256;            // move: threads
-constexpr int MR = 32;             // rows a CTA
+constexpr int MR = 32;             // rows of a piece
+constexpr int MC = 4;              // CTAs an SM
 
 // Weights as unsigned keys in the same order; NaN is the smallest, both zeros are one.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -37,7 +39,7 @@ struct EvictArgs {
   int32_t* seq_len;
   int32_t* kept;
   uint32_t* status;
-  unsigned* count;  // [B] move CTAs done
+  unsigned* count;  // [B] pieces moved, and behind them the CTAs that are done
   unsigned* ready;  // [B] 1: to be moved
 };
 
@@ -82,9 +84,8 @@ __global__ void __launch_bounds__(ST) evict_select_kernel(const EvictArgs a, con
   sm100::griddep_wait();
   sm100::griddep_launch_dependents();
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  const int group = blockIdx.x;  // (l * B + b) * Hkv + h
-  const int h = group % a.g.Hkv, lb = group / a.g.Hkv;
-  const int b = lb % a.batch, l = lb / a.batch;
+  const int h = blockIdx.x % a.g.Hkv, bl = blockIdx.x / a.g.Hkv;
+  const int l = bl % a.layers, b = bl / a.layers;
   const int L = a.seq_len[b];
   if (!evict_over(a, L)) {
     if (t == 0 && L > a.g.capacity && a.status) atomicOr(a.status, EAGLE_STATUS_CACHE_FULL);
@@ -101,32 +102,50 @@ __global__ void __launch_bounds__(ST) evict_select_kernel(const EvictArgs a, con
     return;
   }
   if (t == 0 && l == 0 && h == 0) a.ready[b] = 1;
-  int32_t* out = a.kept + static_cast<size_t>(group) * a.budget;
+  int32_t* out = a.kept + ((static_cast<size_t>(l) * a.batch + b) * a.g.Hkv + h) * a.budget;
   for (int i = t; i < a.sink; i += ST) out[i] = i;
   for (int i = t; i < a.recent; i += ST) out[a.budget - a.recent + i] = L - a.recent + i;
-  const int n = L - a.sink - a.recent;            // candidates (L > limit >= budget >= sink + recent)
-  int need = a.budget - a.sink - a.recent;        // of which these stay: need < n
+  const int lo = a.sink, hi = L - a.recent;       // candidates: rows lo .. hi - 1
+  int need = a.budget - a.sink - a.recent;        // of which these stay, fewer than there are (L > limit >= budget)
   if (need == 0) return;
   const float* w = p.w[l];
-  const bool held = n <= KEYS;
-  auto load_key = [&](int i) { return weight_key(w[paged_row_or_zero(a.g, b, h, a.sink + i, a.status)]); };
-  auto key_at = [&](int i) { return held ? keys[i] : load_key(i); };
+  const bool held = hi <= KEYS;
+  // four keys from row j (a multiple of 4, so of one page) on
+  auto load_keys = [&](int j) {
+    const float4 x = *reinterpret_cast<const float4*>(w + paged_row_or_zero(a.g, b, h, j, a.status));
+    return make_uint4(weight_key(x.x), weight_key(x.y), weight_key(x.z), weight_key(x.w));
+  };
+  auto key_at = [&](int j) { return held ? keys[j] : weight_key(w[paged_row_or_zero(a.g, b, h, j, a.status)]); };
   uint32_t prefix = 0;  // the threshold's bits so far
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int bits = pass == 2 ? 10 : 11, low = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     for (int i = t; i < BINS; i += ST) hist[i] = 0;
     __syncthreads();
-    for (int i = t; i < n; i += ST) {
-      uint32_t k;
-      if (pass == 0) {
-        k = load_key(i);
-        if (held) keys[i] = k;
-      } else {
-        k = key_at(i);
-      }
+    auto count = [&](uint32_t k) {
       if (pass == 0 || (k >> (low + bits)) == (prefix >> (low + bits)))
         atomicAdd(&hist[(k >> low) & ((1u << bits) - 1)], 1u);
+    };
+    if (pass == 0 || !held) {
+      constexpr int U = 4;
+      for (int j0 = (lo & ~3) + 4 * t; j0 < hi; j0 += 4 * ST * U) {
+        uint4 k[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (j0 + 4 * ST * u < hi) k[u] = load_keys(j0 + 4 * ST * u);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int j = j0 + 4 * ST * u;
+          if (j >= hi) break;
+          if (held) *reinterpret_cast<uint4*>(keys + j) = k[u];
+          const uint32_t x[4] = {k[u].x, k[u].y, k[u].z, k[u].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (j + e >= lo && j + e < hi) count(x[e]);
+        }
+      }
+    } else {
+      for (int j = lo + t; j < hi; j += ST) count(keys[j]);
     }
     __syncthreads();
     const int bin = find_bin(hist, 1 << bits, need, s_scan, s_bin);
@@ -134,10 +153,11 @@ __global__ void __launch_bounds__(ST) evict_select_kernel(const EvictArgs a, con
     __syncthreads();
   }
   // need: how many keys equal to the threshold stay (the lowest rows).  A warp takes a run of candidates.
-  const int per = (n + SW - 1) / SW, i0 = min(n, warp * per), i1 = min(n, i0 + per);
+  const int per = (hi - lo + SW - 1) / SW, j0 = min(hi, lo + warp * per), j1 = min(hi, j0 + per);
   int gt = 0, eq = 0;
-  for (int i = i0 + lane; i < i1; i += 32) {
-    const uint32_t k = key_at(i);
+#pragma unroll 4
+  for (int j = j0 + lane; j < j1; j += 32) {
+    const uint32_t k = key_at(j);
     gt += k > prefix;
     eq += k == prefix;
   }
@@ -157,95 +177,139 @@ __global__ void __launch_bounds__(ST) evict_select_kernel(const EvictArgs a, con
     eq += s_eq[i];
   }
   const unsigned below = (1u << lane) - 1;
-  for (int i = i0; i < i1; i += 32) {
+#pragma unroll 2
+  for (int i = j0; i < j1; i += 32) {
     const int j = i + lane;
-    const uint32_t k = j < i1 ? key_at(j) : 0u;
-    const bool is_gt = j < i1 && k > prefix, is_eq = j < i1 && k == prefix;
+    const uint32_t k = j < j1 ? key_at(j) : 0u;
+    const bool is_gt = j < j1 && k > prefix, is_eq = j < j1 && k == prefix;
     const unsigned mg = __ballot_sync(0xffffffffu, is_gt), me = __ballot_sync(0xffffffffu, is_eq);
     const int e = eq + __popc(me & below);
-    if (is_gt || (is_eq && e < need)) out[a.sink + gt + __popc(mg & below) + min(e, need)] = a.sink + j;
+    if (is_gt || (is_eq && e < need)) out[a.sink + gt + __popc(mg & below) + min(e, need)] = j;
     gt += __popc(mg);
     eq += __popc(me);
   }
 }
 
-// grid: (layer, request, head) x chunks of MR kept rows.
-__global__ void __launch_bounds__(MT) evict_move_kernel(const EvictArgs a, const PagedEvictArgs p, int chunks, int vshift) {
+// Pieces of MR kept rows, in the order request (those to be moved), layer, head, piece.
+__global__ void __launch_bounds__(MT, MC) evict_move_kernel(const EvictArgs a, const PagedEvictArgs p, int chunks,
+                                                            int vshift) {
+  __shared__ int s_src[2][MR], s_dst[2][MR];
+  __shared__ bool last;
   sm100::griddep_wait();
   sm100::griddep_launch_dependents();
-  const int t = threadIdx.x;
-  const int group = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
-  const int h = group % a.g.Hkv, lb = group / a.g.Hkv;
-  const int b = lb % a.batch, l = lb / a.batch;
-  if (!a.ready[b]) return;
-  __shared__ int s_src[MR], s_dst[MR];
-  __shared__ bool last;
-  const int n0 = chunk * MR, rows = min(MR, a.budget - n0);
-  if (t < rows) {
-    const int r = a.kept[static_cast<size_t>(group) * a.budget + n0 + t], to = n0 + t;
-    const int src = paged_row_or_zero(a.g, b, h, r, a.status);
-    const int page = a.spare[static_cast<size_t>(b) * a.spare_pages + (to >> a.g.shift)];
-    const int dst = ((page * a.g.Hkv + h) << a.g.shift) + (to & ((1 << a.g.shift) - 1));
-    s_src[t] = src;
-    s_dst[t] = dst;
-    p.w[l][dst] = p.w[l][src];
+  const int t = threadIdx.x, lane = t & 31;
+  const int per_request = a.layers * a.g.Hkv * chunks;
+  int live = 0;  // requests to be moved
+  for (int b = 0; b < a.batch; b += 32)
+    live += __popc(__ballot_sync(0xffffffffu, b + lane < a.batch && __ldcg(a.ready + b + lane) != 0));
+  const long long total = static_cast<long long>(live) * per_request;
+  const int u0 = static_cast<int>(total * blockIdx.x / gridDim.x), u1 = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x);
+  // the n-th request to be moved, by every warp for itself
+  auto request = [&](int n) {
+    for (int b = 0;; b += 32) {
+      const unsigned m = __ballot_sync(0xffffffffu, b + lane < a.batch && __ldcg(a.ready + b + lane) != 0);
+      if (n < __popc(m)) return b + static_cast<int>(__fns(m, 0, n + 1));
+      n -= __popc(m);
+    }
+  };
+  // a piece's rows: looked up by threads 0 .. MR - 1
+  auto look_up = [&](int b, int v, int buf) {  // v: piece of the request
+    const int group = v / chunks, n0 = (v - group * chunks) * MR, rows = min(MR, a.budget - n0);
+    const int l = group / a.g.Hkv, h = group - l * a.g.Hkv;
+    if (t < rows) {
+      const int to = n0 + t;
+      const int r = a.kept[((static_cast<size_t>(l) * a.batch + b) * a.g.Hkv + h) * a.budget + to];
+      const int page = a.spare[static_cast<size_t>(b) * a.spare_pages + (to >> a.g.shift)];
+      const int src = paged_row_or_zero(a.g, b, h, r, a.status);
+      const int dst = ((page * a.g.Hkv + h) << a.g.shift) + (to & ((1 << a.g.shift) - 1));
+      s_src[buf][t] = src;
+      s_dst[buf][t] = dst;
+      p.w[l][dst] = p.w[l][src];
+    }
+  };
+  int n = u0 / per_request, v = u0 - n * per_request, b = 0, buf = 0, mine = 0;
+  if (u0 < u1) {
+    b = request(n);
+    look_up(b, v, buf);
   }
-  __syncthreads();
-  const uint4* k = static_cast<const uint4*>(p.k[l]);
-  const uint4* v = static_cast<const uint4*>(p.v[l]);
-  const int total = rows << vshift, mask = (1 << vshift) - 1;
-  constexpr int U = 2;  // (a vector of K and of V each)
-  for (int i0 = t; i0 < total; i0 += MT * U) {
-    uint4 xk[U], xv[U];
+  for (int u = u0; u < u1; ++u) {
+    __syncthreads();  // (the piece's rows are there, and the other buffer's readers are done)
+    const int group = v / chunks, rows = min(MR, a.budget - (v - group * chunks) * MR), l = group / a.g.Hkv;
+    const uint4* k = static_cast<const uint4*>(p.k[l]);
+    const uint4* vv = static_cast<const uint4*>(p.v[l]);
+    const int vectors = rows << vshift, mask = (1 << vshift) - 1;
+    constexpr int U = 4;  // (a vector of K and of V each: all of a piece of 256-byte rows)
+    const int at_b = b;
+    bool ends = u + 1 == u1;
+    for (int i0 = t; i0 < vectors || i0 == t; i0 += MT * U) {
+      uint4 xk[U], xv[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * MT;
-      if (i < total) {
-        const size_t at = (static_cast<size_t>(s_src[i >> vshift]) << vshift) + (i & mask);
-        xk[u] = k[at];
-        xv[u] = v[at];
+      for (int x = 0; x < U; ++x) {
+        const int i = i0 + x * MT;
+        if (i < vectors) {
+          const size_t at = (static_cast<size_t>(s_src[buf][i >> vshift]) << vshift) + (i & mask);
+          xk[x] = __ldcs(k + at);
+          xv[x] = __ldcs(vv + at);
+        }
+      }
+      if (i0 == t && u + 1 < u1) {  // the next piece, under the loads
+        const bool over = v + 1 == per_request;
+        if (over) {
+          ends = true;
+          b = request(++n);
+        }
+        v = over ? 0 : v + 1;
+        look_up(b, v, buf ^ 1);
+      }
+#pragma unroll
+      for (int x = 0; x < U; ++x) {
+        const int i = i0 + x * MT;
+        if (i < vectors) {
+          const size_t at = (static_cast<size_t>(s_dst[buf][i >> vshift]) << vshift) + (i & mask);
+          __stcs(static_cast<uint4*>(p.k[l]) + at, xk[x]);
+          __stcs(static_cast<uint4*>(p.v[l]) + at, xv[x]);
+        }
       }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * MT;
-      if (i < total) {
-        const size_t at = (static_cast<size_t>(s_dst[i >> vshift]) << vshift) + (i & mask);
-        static_cast<uint4*>(p.k[l])[at] = xk[u];
-        static_cast<uint4*>(p.v[l])[at] = xv[u];
-      }
-    }
-  }
-  __syncthreads();  // (everyone has the pages)
-  if (t == 0) {
+    buf ^= 1;
+    ++mine;
+    if (!ends) continue;
+    // this CTA's last piece of the request
     __threadfence();
-    const unsigned all = static_cast<unsigned>(a.layers) * a.g.Hkv * chunks;
-    last = atomicAdd(&a.count[b], 1u) == all - 1;
+    __syncthreads();
+    if (t == 0) last = atomicAdd(&a.count[at_b], static_cast<unsigned>(mine)) == static_cast<unsigned>(per_request - mine);
+    mine = 0;
+    __syncthreads();
+    if (!last) continue;
+    __threadfence();
+    for (int i = t; i < a.spare_pages; i += MT) {
+      int32_t* x = a.table + static_cast<size_t>(at_b) * a.g.max_pages + i;
+      int32_t* y = a.spare + static_cast<size_t>(at_b) * a.spare_pages + i;
+      const int32_t old = *x;
+      *x = *y;
+      *y = old;
+    }
+    if (t == 0) {
+      a.seq_len[at_b] = a.budget;
+      a.count[at_b] = 0;
+    }
   }
+  // the flags: by the last CTA of all, which have found their requests by them
+  __syncthreads();
+  if (t == 0) last = atomicAdd(a.count + a.batch, 1u) == gridDim.x - 1;
   __syncthreads();
   if (!last) return;
-  __threadfence();
-  for (int i = t; i < a.spare_pages; i += MT) {
-    int32_t* x = a.table + static_cast<size_t>(b) * a.g.max_pages + i;
-    int32_t* y = a.spare + static_cast<size_t>(b) * a.spare_pages + i;
-    const int32_t old = *x;
-    *x = *y;
-    *y = old;
-  }
-  if (t == 0) {
-    a.seq_len[b] = a.budget;
-    a.count[b] = 0;
-    a.ready[b] = 0;
-  }
+  for (int i = t; i < a.batch; i += MT) a.ready[i] = 0;
+  if (t == 0) a.count[a.batch] = 0;
 }
 
 }  // namespace
 
-size_t paged_evict_ws(const eagle_paged_evict_desc& d) { return static_cast<size_t>(d.batch) * 8; }
+size_t paged_evict_ws(const eagle_paged_evict_desc& d) { return (static_cast<size_t>(d.batch) * 8 + 4 + 15) / 16 * 16; }
 
 cudaError_t launch_paged_evict(const eagle_paged_evict_desc& d, const PagedEvictArgs& p, int32_t* table,
                                int32_t* spare, int32_t* seq_len, int32_t* kept, uint32_t* status, void* ws,
-                               cudaStream_t s) {
+                               int sms, cudaStream_t s) {
   EvictArgs a;
   a.g = paged_geom(table, d.n_pages, d.max_pages, d.page_size, d.n_kv_heads);
   a.layers = d.layers;
@@ -261,7 +325,7 @@ cudaError_t launch_paged_evict(const eagle_paged_evict_desc& d, const PagedEvict
   a.kept = kept;
   a.status = status;
   a.count = static_cast<unsigned*>(ws);
-  a.ready = a.count + d.batch;
+  a.ready = a.count + d.batch + 1;
   static unsigned long long configured = 0;
   cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(evict_select_kernel), SELECT_SMEM, configured);
   if (e != cudaSuccess) return e;
@@ -269,7 +333,9 @@ cudaError_t launch_paged_evict(const eagle_paged_evict_desc& d, const PagedEvict
   e = launch_pdl(evict_select_kernel, dim3(groups), dim3(ST), SELECT_SMEM, s, a, p);
   if (e != cudaSuccess) return e;
   const int bytes = d.head_dim * (d.dtype == EAGLE_F32 ? 4 : 2);
-  return launch_pdl(evict_move_kernel, dim3(static_cast<unsigned>(groups) * chunks), dim3(MT), 0, s, a, p, chunks,
+  const long long pieces = static_cast<long long>(groups) * chunks;
+  const int ctas = static_cast<int>(pieces < sms * MC ? pieces : sms * MC);
+  return launch_pdl(evict_move_kernel, dim3(ctas), dim3(MT), 0, s, a, p, chunks,
                     bytes == 128 ? 3 : bytes == 256 ? 4 : 5);
 }
 

@@ -52,14 +52,16 @@ __global__ void __launch_bounds__(WT) paged_write_kernel(const PagedGeom g, int 
   }
 }
 
-constexpr int CT = 256;  // threads: one 16-byte vector of K and one of V each
+constexpr int CT = 256;  // threads: a 16-byte vector of K and one of V each, of every layer
 
 __device__ __forceinline__ bool paged_commit_fits(const eagle_paged_commit_desc& d, int capacity, int na, int L) {
   return na >= 0 && na <= d.max_depth && L >= 0 && L <= capacity - 1 - na;
 }
 
-// grid (vectors of a request's path rows / CT, B, L).  Every CTA reads the old lengths; the last one to
-// finish (a counter in ws) writes the new ones, so that one launch does (a second one for them: 1.5 us more).
+constexpr int CL = 4;    // layers a CTA takes: 8 loads a thread in flight
+
+// grid (vectors of a request's path rows / CT, B, L / CL).  Every CTA reads the old length; the last one of its
+// request to finish (counters in ws) writes the new one, so that one launch does.
 __global__ void __launch_bounds__(CT) paged_commit_kernel(const eagle_paged_commit_desc d, const PagedGeom g,
                                                           const CommitArgs a, int vshift, const int32_t* n_acc,
                                                           const int32_t* path, int32_t* seq_len, int32_t* commit_pos,
@@ -67,9 +69,10 @@ __global__ void __launch_bounds__(CT) paged_commit_kernel(const eagle_paged_comm
                                                           uint32_t* status, unsigned* counter) {
   sm100::griddep_wait();
   sm100::griddep_launch_dependents();
-  const int b = blockIdx.y, l = blockIdx.z, maxp = d.max_depth + 1;
+  const int b = blockIdx.y, l0 = blockIdx.z * CL, maxp = d.max_depth + 1;
   const int na = n_acc[b], L = seq_len[b];
-  if (paged_commit_fits(d, g.capacity, na, L)) {
+  const bool fits = paged_commit_fits(d, g.capacity, na, L);
+  if (fits) {
     // vectors in the order path row, head, vector
     const int at = blockIdx.x * CT + threadIdx.x;
     const int c = at & ((1 << vshift) - 1), row = at >> vshift;
@@ -77,17 +80,25 @@ __global__ void __launch_bounds__(CT) paged_commit_kernel(const eagle_paged_comm
     if (m <= na) {
       const int node = path[static_cast<size_t>(b) * maxp + m];
       const int y = paged_row(g, b, h, L + m);
-      if (node >= 0 && node < d.rows) {
+      if (node >= 0 && node < d.rows && y >= 0) {
         const size_t src = (((static_cast<size_t>(b) * g.Hkv + h) * d.rows + node) << vshift) + c;
-        const uint4 xk = static_cast<const uint4*>(a.tree_k[l])[src];
-        const uint4 xv = static_cast<const uint4*>(a.tree_v[l])[src];
-        if (y >= 0) {
-          static_cast<uint4*>(a.k_cache[l])[(static_cast<size_t>(y) << vshift) + c] = xk;
-          static_cast<uint4*>(a.v_cache[l])[(static_cast<size_t>(y) << vshift) + c] = xv;
-        }
+        const size_t dst = (static_cast<size_t>(y) << vshift) + c;
+        uint4 xk[CL], xv[CL];
+#pragma unroll
+        for (int i = 0; i < CL; ++i)
+          if (l0 + i < d.layers) {
+            xk[i] = static_cast<const uint4*>(a.tree_k[l0 + i])[src];
+            xv[i] = static_cast<const uint4*>(a.tree_v[l0 + i])[src];
+          }
+#pragma unroll
+        for (int i = 0; i < CL; ++i)
+          if (l0 + i < d.layers) {
+            static_cast<uint4*>(a.k_cache[l0 + i])[dst] = xk[i];
+            static_cast<uint4*>(a.v_cache[l0 + i])[dst] = xv[i];
+          }
       }
     }
-    if (l == 0 && d.feat_dim > 0 && blockIdx.x == 0) {
+    if (l0 == 0 && d.feat_dim > 0 && blockIdx.x == 0) {
       const size_t bytes = static_cast<size_t>(d.feat_dim) * (d.feat_dtype == EAGLE_F32 ? 4 : 2);
       for (int i = 0; i <= na; ++i) {
         const int node = path[static_cast<size_t>(b) * maxp + i];
@@ -108,32 +119,26 @@ __global__ void __launch_bounds__(CT) paged_commit_kernel(const eagle_paged_comm
     }
   }
   __shared__ bool last;
-  __syncthreads();  // (everyone has the old lengths)
+  __syncthreads();  // (everyone has the old length)
   if (threadIdx.x == 0) {
     __threadfence();
-    const unsigned total = gridDim.x * gridDim.y * gridDim.z;
-    last = atomicAdd(counter, 1u) == total - 1;
-    if (last) *counter = 0;
+    last = atomicAdd(counter + b, 1u) == gridDim.x * gridDim.z - 1;
+    if (last) counter[b] = 0;
   }
   __syncthreads();
   if (!last) return;
-  __threadfence();
-  for (int i = threadIdx.x; i < d.batch; i += CT) {
-    const int nb = n_acc[i], Lb = *const_cast<volatile int32_t*>(seq_len + i);
-    const bool ok = paged_commit_fits(d, g.capacity, nb, Lb);
-    uint32_t st = ok ? 0 : EAGLE_STATUS_CACHE_FULL;
-    for (int m = 0; m < maxp; ++m) {
-      const bool on = ok && m <= nb;
-      if (on) {
-        const int node = path[static_cast<size_t>(i) * maxp + m];
-        if (node < 0 || node >= d.rows) st |= EAGLE_STATUS_BAD_TREE;
-        if (paged_row(g, i, 0, Lb + m) < 0) st |= EAGLE_STATUS_BAD_PAGE;
-      }
-      if (commit_pos) commit_pos[static_cast<size_t>(i) * maxp + m] = on ? Lb + m : -1;
+  uint32_t st = fits ? 0 : EAGLE_STATUS_CACHE_FULL;
+  for (int m = threadIdx.x; m < maxp; m += CT) {
+    const bool on = fits && m <= na;
+    if (on) {
+      const int node = path[static_cast<size_t>(b) * maxp + m];
+      if (node < 0 || node >= d.rows) st |= EAGLE_STATUS_BAD_TREE;
+      if (paged_row(g, b, 0, L + m) < 0) st |= EAGLE_STATUS_BAD_PAGE;
     }
-    if (ok) seq_len[i] = Lb + nb + 1;
-    if (st && status) atomicOr(status, st);
+    if (commit_pos) commit_pos[static_cast<size_t>(b) * maxp + m] = on ? L + m : -1;
   }
+  if (fits && threadIdx.x == 0) seq_len[b] = L + na + 1;
+  if (st && status) atomicOr(status, st);
 }
 
 int vector_shift(int head_dim, int dtype) {  // 16-byte vectors of a row: 8, 16 or 32
@@ -155,13 +160,15 @@ cudaError_t launch_paged_write(const eagle_paged_desc& d, const void* k, const v
                     static_cast<uint4*>(v_pages), status);
 }
 
+size_t paged_commit_ws(const eagle_paged_commit_desc& d) { return (static_cast<size_t>(d.batch) * 4 + 15) / 16 * 16; }
+
 cudaError_t launch_paged_commit(const eagle_paged_commit_desc& d, const CommitArgs& a, const int32_t* table,
                                 const int32_t* n_acc, const int32_t* path, int32_t* seq_len, int32_t* commit_pos,
                                 void* feat_pages, const void* tree_feat, uint32_t* status, void* ws, cudaStream_t s) {
   const PagedGeom g = paged_geom(table, d.n_pages, d.max_pages, d.page_size, d.n_kv_heads);
   const int vshift = vector_shift(d.head_dim, d.dtype);
   const int vectors = ((d.max_depth + 1) * d.n_kv_heads) << vshift;
-  const dim3 grid((vectors + CT - 1) / CT, d.batch, d.layers);
+  const dim3 grid((vectors + CT - 1) / CT, d.batch, (d.layers + CL - 1) / CL);
   return launch_pdl(paged_commit_kernel, grid, dim3(CT), 0, s, d, g, a, vshift, n_acc, path, seq_len, commit_pos,
                     static_cast<uint8_t*>(feat_pages), static_cast<const uint8_t*>(tree_feat), status,
                     static_cast<unsigned*>(ws));

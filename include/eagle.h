@@ -653,7 +653,8 @@ typedef struct {
  * ws: eagle_workspace_size(EAGLE_WS_PAGED_ATTN, d) bytes, zero-filled before its first use; one workspace
  * serves one stream at a time, and any descriptors in turn that it is large enough for.  Its first 4 bytes
  * are an error word that a bounded wait ORs a bit into when it gives up (2 s).
- * Unsupported: the common limits, R > 128, Hq % Hkv != 0, bf16 out with fp32 inputs. */
+ * Unsupported: the common limits, R > 128, Hq % Hkv != 0, R Hq > 2^20, bf16 out with fp32 inputs,
+ * B Hkv ceil(R G / 16) (max_pages T / 128 + 2) > 2^31 - 1. */
 int eagle_paged_attn(const eagle_paged_attn_desc* d, const void* q, const void* k_pages, const void* v_pages,
                      const int32_t* page_table, const void* tree_k, const void* tree_v, const int32_t* seq_len,
                      const int32_t* n_nodes, const uint64_t* anc_mask, const float* slopes, void* out, float* lse,
@@ -684,7 +685,9 @@ typedef struct {
  *   prior, weights: pages of fp32 [n_pages][Hkv][T] under the same table; prior NULL counts as 0; prior and
  *   weights may be the same.  Rows j >= seq_len[b] of weights are left as they were.
  * A request whose n_acc is not in [0, max_depth], whose path leaves [0, R) (EAGLE_STATUS_BAD_TREE) or whose
- * seq_len is not in [n, max_pages T] (EAGLE_STATUS_CACHE_FULL) is left untouched. */
+ * seq_len is not in [n, max_pages T] (EAGLE_STATUS_CACHE_FULL) is left untouched.
+ * Unsupported: the common limits, R or max_depth + 1 > 128, Hq % Hkv != 0, R Hq > 2^20,
+ * B Hkv (max_pages T / 128 + 2) > 2^31 - 1. */
 int eagle_paged_weights(const eagle_paged_weights_desc* d, const void* q, const float* lse, const void* k_pages,
                         const int32_t* page_table, const int32_t* seq_len, const int32_t* n_acc, const int32_t* path,
                         const float* slopes, const float* prior, float* weights, uint32_t* status, void* stream);
