@@ -317,66 +317,47 @@ __device__ __forceinline__ void paged_fold_row(const PagedAttnArgs& a, const Pag
   }
 }
 
-// ROWS rows of a group joined from its CTAs' slots, by one warp: rows row, row + step, .. (those below `rows`).
-// The partial rows of BATCH CTAs are requested before their weights are known.
-template <int RB, int D, int ROWS, int BATCH>
-__device__ __forceinline__ void paged_join_rows(const PagedAttnArgs& a, const PagedSegment& s, int row, int step,
-                                                int rows, int lane) {
-  constexpr int N = D / 32;
+// A row of a group joined from its CTAs' slots, by one warp.  The partial rows of BATCH CTAs are requested before
+// their weights are known.
+template <int RB, int D>
+__device__ __forceinline__ void paged_join_row(const PagedAttnArgs& a, const PagedSegment& s, int row, int lane) {
+  constexpr int N = D / 32, BATCH = 20;
   const int n = s.c1 - s.c0 + 1;
-  float m[ROWS], l[ROWS], o[ROWS][N];
+  float m = -INFINITY, l = 0.f, o[N];
 #pragma unroll
-  for (int k = 0; k < ROWS; ++k) {
-    m[k] = -INFINITY;
-    l[k] = 0.f;
-#pragma unroll
-    for (int e = 0; e < N; ++e) o[k][e] = 0.f;
-  }
-  auto slot_of = [&](int i) { return static_cast<size_t>(i == 0 ? s.slot0 : 2 * (s.c0 + i)) * RB; };
+  for (int e = 0; e < N; ++e) o[e] = 0.f;
+  auto place = [&](int i) { return static_cast<size_t>(i == 0 ? s.slot0 : 2 * (s.c0 + i)) * RB + row; };
 #pragma unroll 1
   for (int i0 = 0; i0 < n; i0 += BATCH) {
-    float2 x[ROWS][BATCH][N / 2], ml[ROWS];
+    float2 x[BATCH][N / 2], ml = make_float2(-INFINITY, 0.f);
     const int mine = i0 + lane;
+    if (lane < BATCH && mine < n) ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + place(mine));
 #pragma unroll
-    for (int k = 0; k < ROWS; ++k) {
-      const int r = min(row + k * step, rows - 1);
-      ml[k] = make_float2(-INFINITY, 0.f);
-      if (lane < BATCH && mine < n) ml[k] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + (slot_of(mine) + r) * 2));
+    for (int u = 0; u < BATCH; ++u) {
+      const float2* po = reinterpret_cast<const float2*>(a.part_o + place(min(i0 + u, n - 1)) * D + lane * N);
 #pragma unroll
-      for (int u = 0; u < BATCH; ++u) {
-        const float2* po =
-            reinterpret_cast<const float2*>(a.part_o + (slot_of(min(i0 + u, n - 1)) + r) * D + lane * N);
-#pragma unroll
-        for (int e = 0; e < N / 2; ++e) x[k][u][e] = __ldcg(po + e);
-      }
+      for (int e = 0; e < N / 2; ++e) x[u][e] = __ldcg(po + e);
     }
+    const float top = fmaxf(m, warp_max(ml.x));
+    const float old = m == -INFINITY ? 0.f : sm100::ex2(m - top);
+    const float f = ml.x == -INFINITY ? 0.f : sm100::ex2(ml.x - top);
+    m = top;
+    l = fmaf(l, old, warp_sum(f * ml.y));
 #pragma unroll
-    for (int k = 0; k < ROWS; ++k) {
-      const float top = fmaxf(m[k], warp_max(ml[k].x));
-      const float old = m[k] == -INFINITY ? 0.f : sm100::ex2(m[k] - top);
-      const float f = ml[k].x == -INFINITY ? 0.f : sm100::ex2(ml[k].x - top);
-      m[k] = top;
-      l[k] = fmaf(l[k], old, warp_sum(f * ml[k].y));
+    for (int e = 0; e < N; ++e) o[e] *= old;
 #pragma unroll
-      for (int e = 0; e < N; ++e) o[k][e] *= old;
+    for (int u = 0; u < BATCH; ++u) {
+      const float g = __shfl_sync(0xffffffffu, f, u);
+      if (i0 + u < n) {  // (the others' row is there twice)
 #pragma unroll
-      for (int u = 0; u < BATCH; ++u) {
-        const float g = __shfl_sync(0xffffffffu, f, u);
-        if (i0 + u < n) {  // (the others' row is there twice)
-#pragma unroll
-          for (int e = 0; e < N / 2; ++e) {
-            o[k][2 * e] = fmaf(g, x[k][u][e].x, o[k][2 * e]);
-            o[k][2 * e + 1] = fmaf(g, x[k][u][e].y, o[k][2 * e + 1]);
-          }
+        for (int e = 0; e < N / 2; ++e) {
+          o[2 * e] = fmaf(g, x[u][e].x, o[2 * e]);
+          o[2 * e + 1] = fmaf(g, x[u][e].y, o[2 * e + 1]);
         }
       }
     }
   }
-#pragma unroll
-  for (int k = 0; k < ROWS; ++k) {
-    const int r = row + k * step;
-    if (r < rows) paged_store<D>(a, paged_out_row(a, s, s.row0 + r), lane, o[k], m[k], l[k]);
-  }
+  paged_store<D>(a, paged_out_row(a, s, s.row0 + row), lane, o, m, l);
 }
 
 // The end of a segment whose group other CTAs share: this CTA's partials are written; the last CTA of the
@@ -395,8 +376,7 @@ __device__ __forceinline__ void paged_arrive(const PagedAttnArgs& a, const Paged
   __syncthreads();
   if (!*s_last) return;
   const int rows = min(RB, s.rq.Rb * a.G - s.row0);
-  for (int row = threadIdx.x >> 5; row < rows; row += W)
-    paged_join_rows<RB, D, 1, 20>(a, s, row, W, rows, threadIdx.x & 31);
+  for (int row = threadIdx.x >> 5; row < rows; row += W) paged_join_row<RB, D>(a, s, row, threadIdx.x & 31);
 }
 
 }  // namespace eagle

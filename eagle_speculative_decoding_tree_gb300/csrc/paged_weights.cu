@@ -139,28 +139,31 @@ __global__ void __launch_bounds__(W * 32) paged_weights_simt_kernel(const Weight
 
 // ---------------------------------------------------------------- bf16
 constexpr int MK = 16;  // keys a warp takes at a time
+constexpr int MW = 12;  // warps
 
 template <int D>
 struct Few {
   static constexpr int KB = MK * D * 2;
-  static constexpr int ST = D == 128 ? 6 : 8;  // stages of a warp
-  static constexpr int SM_P = W * ST * KB;     // prior weights, 16 of them a stage
-  static constexpr int SMEM = SM_P + W * ST * MK * 4 + 1024;
+  static constexpr int ST = D == 128 ? 4 : 8;  // stages of a warp
+  static constexpr int SM_P = MW * ST * KB;     // prior weights, 16 of them a stage
+  static constexpr int SM_Y = SM_P + MW * ST * MK * 4;
+  static constexpr int SMEM = SM_Y + MW * ST * 4 + 1024;
 };
 
 template <int D, int MT, bool SHAPED>
-__global__ void __launch_bounds__(W * 32, 1)
+__global__ void __launch_bounds__(MW * 32, 1)
     paged_weights_mma_kernel(const __grid_constant__ CUtensorMap tk, const WeightArgs a) {
   using F = Few<D>;
   constexpr int KS = D / 16, RB = 16 * MT;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t full[W][F::ST];
+  __shared__ uint64_t full[MW][F::ST];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int qr = lane >> 2, qc = lane & 3;
   uint8_t* ring = smem + warp * (F::ST * F::KB);
   float* sp = reinterpret_cast<float*>(smem + F::SM_P) + warp * (F::ST * MK);
   const uint32_t ring32 = sm100::smem_u32(ring);
+  int* sy = reinterpret_cast<int*>(smem + F::SM_Y) + warp * F::ST;  // the stages' rows of the pool, -1: a bad page
   if (lane == 0) {
     sm100::prefetch_tmap(&tk);
     for (int i = 0; i < F::ST; ++i) sm100::mbar_init(&full[warp][i], 1);
@@ -184,6 +187,11 @@ __global__ void __launch_bounds__(W * 32, 1)
       auto issue = [&](int at, int y) {
         if (lane == 0) {
           const int stage = issued % F::ST;
+          sy[stage] = y;
+          if (y < 0) {  // page 0 in its place, and nothing written
+            if (a.list.status) atomicOr(a.list.status, EAGLE_STATUS_BAD_PAGE);
+            y = 0;
+          }
           uint64_t* bar = &full[warp][stage];
           sm100::mbar_arrive_expect_tx(bar, F::KB + (prior ? MK * 4 : 0));
           sm100::tma_load_3d(ring + stage * F::KB, &tk, 0, y, 0, bar);
@@ -191,9 +199,9 @@ __global__ void __launch_bounds__(W * 32, 1)
         }
         ++issued;
       };
-      auto row_of = [&](int at) { return paged_row_or_zero(a.list.g, s.b, s.h, at, a.list.status); };
+      auto row_of = [&](int at) { return paged_row(a.list.g, s.b, s.h, at); };
       int next = c0, next_row = 0;
-      for (int i = 0; i < F::ST && next < c_end; ++i, next += W * MK) issue(next, lane == 0 ? row_of(next) : 0);
+      for (int i = 0; i < F::ST && next < c_end; ++i, next += MW * MK) issue(next, lane == 0 ? row_of(next) : 0);
       if (lane == 0 && next < c_end) next_row = row_of(next);
       // the rows: queries, softmax sums (inf: no row), positions
       uint32_t qf[MT][KS][4];
@@ -217,7 +225,7 @@ __global__ void __launch_bounds__(W * 32, 1)
           slope[t][i] = SHAPED && a.shape.slopes ? a.shape.slopes[s.h * a.G + g] * kLog2e : 0.f;
           pos[t][i] = L - n + mm;
         }
-      for (int at = c0; at < c_end; at += W * MK) {
+      for (int at = c0; at < c_end; at += MW * MK) {
         const int stage = used % F::ST;
         ok = __all_sync(0xffffffffu, sm100::wait_parity(&full[warp][stage], (used / F::ST) & 1, nullptr, 0));
         if (!ok) break;
@@ -260,7 +268,7 @@ __global__ void __launch_bounds__(W * 32, 1)
         if (lane < 8) {  // lane: half of the chunk, pair of keys
           const int k = 8 * (lane >> 2) + 2 * (lane & 3);
           const float g0 = lane < 4 ? got[0] : got[2], g1 = lane < 4 ? got[1] : got[3];
-          const int y = paged_row(a.list.g, s.b, s.h, at);
+          const int y = sy[stage];
           const int old = r0 == 0 ? L - n : L;  // rows whose prior counts
           const float2 p = *reinterpret_cast<const float2*>(sp + stage * MK + k);
           if (y >= 0) {
@@ -271,7 +279,7 @@ __global__ void __launch_bounds__(W * 32, 1)
         __syncwarp();
         if (next < c_end) {
           issue(next, next_row);
-          next += W * MK;
+          next += MW * MK;
           if (lane == 0 && next < c_end) next_row = row_of(next);
         }
       }
@@ -291,7 +299,7 @@ cudaError_t launch_mma(const WeightArgs& a, const CUtensorMap& tk, int ctas, cud
   auto kern = paged_weights_mma_kernel<D, MT, SHAPED>;
   constexpr int smem = Few<D>::SMEM;
   const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kern), smem, conf);
-  return e != cudaSuccess ? e : launch_pdl(kern, dim3(ctas), dim3(W * 32), smem, s, tk, a);
+  return e != cudaSuccess ? e : launch_pdl(kern, dim3(ctas), dim3(MW * 32), smem, s, tk, a);
 }
 
 template <int D>
