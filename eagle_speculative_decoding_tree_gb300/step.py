@@ -149,15 +149,27 @@ class VerifyStep:
     head (``k8``, ``ks``, ``v8``, ``vs`` instead of ``kc``, ``vc``; bf16 workloads): each layer's prefix
     is quantised once here (eagle_kvq_write), attention reads the codes
     (eagle_tree_attn_kvq) and the commit appends to them (eagle_kvq_commit).
+
+    ``page_size`` 16, 32, 64 or 128 keeps it in pages of that many tokens (``kp``, ``vp`` per layer and one
+    ``table``): eagle_paged_write, eagle_paged_attn and eagle_paged_commit instead.  ``evict`` (limit,
+    budget, sink, recent) then ends a step with eviction: every layer's tokens collect the accepted
+    rows' attention weights (``weights``, eagle_paged_weights), and requests longer than `limit` are cut
+    down to `budget` tokens (eagle_paged_evict; ``kept`` has the tokens that stayed).
     """
 
     def __init__(self, w: synth.Workload, batch: Optional[int] = None, layers: Optional[int] = None,
                  device="cuda", q_scale: float = 1.0, num_splits: int = 0, tree: Optional[dict] = None,
-                 keep_host: bool = False, precision: int = B.EAGLE_ATTN_PRECISE, cache_bits: int = 16):
+                 keep_host: bool = False, precision: int = B.EAGLE_ATTN_PRECISE, cache_bits: int = 16,
+                 page_size: int = 0, evict: Optional[tuple] = None):
         if cache_bits not in (8, 16) or (cache_bits == 8 and w.dtype != "bf16"):
             raise ValueError("cache_bits is 16, or 8 for a bf16 workload")
+        if page_size not in (0, 16, 32, 64, 128) or (page_size and cache_bits == 8):
+            raise ValueError("page_size is 16, 32, 64 or 128, for a 16-bit cache (0: no pages)")
+        if evict is not None and not page_size:
+            raise ValueError("evict is for a paged cache")
         self.w = w
         self.cache_bits = cache_bits
+        self.page_size, self.evict = page_size, evict
         self.B = batch if batch is not None else w.batch
         self.L = layers if layers is not None else w.layers
         self.device = device
@@ -203,6 +215,8 @@ class VerifyStep:
         self.host = [] if keep_host else None
         if cache_bits == 8:
             self._allocate_codes()
+        if page_size:
+            self._allocate_pages()
         for l in range(L):
             q, kc, vc, tk, tv = synth.attn_tensors(w, l, Bn, self.seq_len0, R, q_scale)
             if keep_host:
@@ -212,6 +226,9 @@ class VerifyStep:
             if cache_bits == 8:
                 B.eagle_kvq_write(self._write_desc, kc, vc, self._zero, self.seq_len, self.k8[l], self.ks[l],
                                   self.v8[l], self.vs[l])
+            elif page_size:
+                B.eagle_paged_write(self._write_desc, kc, vc, self.table, self._zero, self.seq_len, self.kp[l],
+                                    self.vp[l])
             else:
                 self.kc.append(kc)
                 self.vc.append(vc)
@@ -223,6 +240,11 @@ class VerifyStep:
         self.attn_desc = B.AttnDesc(Bn, R, w.n_q_heads, w.n_kv_heads, w.head_dim, w.max_seq,
                                     1.0 / math.sqrt(w.head_dim), dt, num_splits, dt, precision)
         kind = B.EAGLE_WS_TREE_ATTN if cache_bits == 16 else B.EAGLE_WS_TREE_ATTN_KVQ
+        if page_size:
+            kind = B.EAGLE_WS_PAGED_ATTN
+            self.attn_desc = B.PagedAttnDesc(Bn, R, w.n_q_heads, w.n_kv_heads, w.head_dim, page_size, self.n_pages,
+                                             self.max_pages, 1.0 / math.sqrt(w.head_dim), 0.0, 0, dt, dt, precision,
+                                             B.EAGLE_ENGINE_AUTO)
         self.attn_ws = torch.zeros(B.workspace_size(kind, self.attn_desc), dtype=torch.uint8, device=dev)
         if cache_bits == 8:
             self.kc = self.vc = None
@@ -232,7 +254,9 @@ class VerifyStep:
         self.acc_ws = torch.zeros(B.workspace_size(B.EAGLE_WS_ACCEPT, self.acc_desc), dtype=torch.uint8, device=dev)
         self.acc = B.AcceptBuffers.allocate(Bn, self.max_depth, dev)
         self.commit_desc = B.CommitDesc(L, Bn, w.n_kv_heads, w.head_dim, R, w.max_seq, self.max_depth, dt, 0, dt)
-        if cache_bits == 8:
+        if page_size:
+            self._paged_commit(dt)
+        elif cache_bits == 8:
             self.layers = B.KvqLayerPointers(self.k8, self.ks, self.v8, self.vs, self.tk, self.tv)
         else:
             self.layers = B.LayerPointers(self.kc, self.vc, self.tk, self.tv)
@@ -250,6 +274,44 @@ class VerifyStep:
         self.ks, self.vs = (list(t) for t in self._scales)
         self._write_desc = B.KvqDesc(self.B, w.n_kv_heads, w.head_dim, w.max_seq, w.max_seq, B.EAGLE_BF16)
         self._zero = torch.zeros(self.B, dtype=torch.int32, device=dev)
+
+    def _allocate_pages(self):
+        """One pool a layer for K and V; each request's pages scattered over it, and spare ones for evictions."""
+        w, dev, T, Bn = self.w, self.seq_len.device, self.page_size, self.B
+        self.max_pages = -(-w.max_seq // T)
+        spare = -(-self.evict[1] // T) if self.evict else 0
+        self.n_pages = Bn * (self.max_pages + spare)
+        order = torch.from_numpy(synth.rng(w.config_id, 9300, T, Bn).permutation(self.n_pages).astype(np.int32)).to(dev)
+        self.table = order[:Bn * self.max_pages].reshape(Bn, self.max_pages).contiguous()
+        self.spare = order[Bn * self.max_pages:].reshape(Bn, spare).contiguous()
+        self._table0, self._spare0 = self.table.clone(), self.spare.clone()
+        dt = torch.float32 if w.dtype == "f32" else torch.bfloat16
+        shape = (self.n_pages, w.n_kv_heads, T, w.head_dim)
+        self.kp, self.vp = ([torch.zeros(shape, dtype=dt, device=dev) for _ in range(self.L)] for _ in range(2))
+        code = B.EAGLE_F32 if w.dtype == "f32" else B.EAGLE_BF16
+        self._write_desc = B.PagedDesc(Bn, w.n_kv_heads, w.head_dim, T, self.n_pages, self.max_pages, w.max_seq, code)
+        self._zero = torch.zeros(Bn, dtype=torch.int32, device=dev)
+
+    def _paged_commit(self, dt: int):
+        """Descriptors, pointers and buffers of a paged step's commit, weights and eviction."""
+        w, Bn, T, R, dev = self.w, self.B, self.page_size, self.R, self.seq_len.device
+        ws = lambda kind, d: torch.zeros(B.workspace_size(kind, d), dtype=torch.uint8, device=dev)
+        self.commit_desc = B.PagedCommitDesc(self.L, Bn, w.n_kv_heads, w.head_dim, T, self.n_pages, self.max_pages, R,
+                                             self.max_depth, dt, 0, dt)
+        self.layers = B.LayerPointers(self.kp, self.vp, self.tk, self.tv)
+        self.commit_ws = ws(B.EAGLE_WS_PAGED_COMMIT, self.commit_desc)
+        if not self.evict:
+            return
+        limit, budget, sink, recent = self.evict
+        self.lse_layers = [torch.empty_like(self.lse) for _ in range(self.L)]
+        self.weights = [torch.zeros(self.n_pages, w.n_kv_heads, T, device=dev) for _ in range(self.L)]
+        self.kept = torch.zeros(self.L, Bn, w.n_kv_heads, budget, dtype=torch.int32, device=dev)
+        self.weights_desc = B.PagedWeightsDesc(Bn, R, w.n_q_heads, w.n_kv_heads, w.head_dim, T, self.n_pages,
+                                               self.max_pages, self.max_depth, 1.0 / math.sqrt(w.head_dim), 0.0, 0, dt)
+        self.evict_desc = B.PagedEvictDesc(self.L, Bn, w.n_kv_heads, w.head_dim, T, self.n_pages, self.max_pages, limit,
+                                           budget, sink, recent, dt)
+        self.evict_layers = B.PagedLayerPointers(self.kp, self.vp, self.weights)
+        self.evict_ws = ws(B.EAGLE_WS_PAGED_EVICT, self.evict_desc)
 
     def _keep_last_blocks(self):
         """A commit may move the codes of each prefix's last block to a larger scale: reset() puts them back."""
@@ -307,6 +369,12 @@ class VerifyStep:
                                   self.tk[l], self.tv[l], self.seq_len, self.anc_mask, self.out[l],
                                   self.lse if lse else None, self.attn_ws, stream)
             return
+        if self.page_size:
+            out_lse = self.lse_layers[l] if self.evict else self.lse if lse else None
+            B.eagle_paged_attn(self.attn_desc, self.q[l], self.kp[l], self.vp[l], self.table, self.tk[l], self.tv[l],
+                               self.seq_len, self.anc_mask, self.out[l], out_lse, self.attn_ws, stream,
+                               status=self.acc.status)
+            return
         B.eagle_tree_attn(self.attn_desc, self.q[l], self.kc[l], self.vc[l], self.tk[l], self.tv[l], self.seq_len,
                           self.anc_mask, self.out[l], self.lse if lse else None, self.attn_ws, stream)
 
@@ -315,13 +383,34 @@ class VerifyStep:
                        self.acc, self.acc_ws, stream)
 
     def commit(self, stream=None):
+        if self.page_size:
+            B.eagle_paged_commit(self.commit_desc, self.layers, self.table, self.acc.n_acc, self.acc.path, self.seq_len,
+                                 self.commit_pos, self.commit_ws, status=self.acc.status, stream=stream)
+            return
         commit = B.eagle_kvq_commit if self.cache_bits == 8 else B.eagle_kv_commit
         commit(self.commit_desc, self.layers, self.acc.n_acc, self.acc.path, self.seq_len, self.commit_pos,
                status=self.acc.status, stream=stream)
 
+    def add_weights(self, l: int, stream=None):
+        """Layer l's tokens collect the accepted rows' attention weights (after the commit)."""
+        B.eagle_paged_weights(self.weights_desc, self.q[l], self.lse_layers[l], self.kp[l], self.table, self.seq_len,
+                              self.acc.n_acc, self.acc.path, self.weights[l], self.weights[l], stream,
+                              status=self.acc.status)
+
+    def evict_long(self, stream=None):
+        """Requests longer than the limit are cut down to the budget."""
+        B.eagle_paged_evict(self.evict_desc, self.evict_layers, self.table, self.spare, self.seq_len, self.kept,
+                            self.evict_ws, status=self.acc.status, stream=stream)
+
     def reset(self):
-        """Restore seq_len (and an 8-bit cache's last prefix blocks) so that the next run repeats the same step."""
+        """Restore seq_len (and an 8-bit cache's last prefix blocks, or the page tables and weights) so that the
+        next run repeats the same step."""
         self.seq_len.copy_(self.seq_len_init)
+        if self.evict:
+            self.table.copy_(self._table0)
+            self.spare.copy_(self._spare0)
+            for w in self.weights:
+                w.zero_()
         if self.cache_bits == 8:
             self._codes.scatter_(4, self._last_rows, self._last_codes)
             self._scales.scatter_(4, self._last_block, self._last_scale)
@@ -333,6 +422,10 @@ class VerifyStep:
             self.attn_layer(l, stream)
         self.accept(stream)
         self.commit(stream)
+        if self.evict:
+            for l in range(self.L):
+                self.add_weights(l, stream)
+            self.evict_long(stream)
 
     # ------------------------------------------------------------------ accounting
     def kv_bytes_per_layer(self) -> int:
