@@ -5,10 +5,10 @@
 //            kept is found from the top (a radix select: 11, 11 and 10 bits, a histogram in shared memory
 //            each), and one more pass writes the kept rows' numbers in order.  The keys stay in shared memory
 //            when they fit, so that the weights are read once, four a load and all loads of a thread together.
-//   move     each CTA takes an even share of all requests' pieces of 32 kept rows; 16 KB of K and V are in
-//            flight a piece, and the next piece's rows are looked up under them.  Out of place, to the
-//            request's spare pages: rows need no order among themselves, and what another request shares
-//            stays as it is.  The last CTA of a request to finish swaps the pages and sets the length.
+//   move     each CTA takes an even share of all requests' pieces of 64 kept rows.  One warp looks the next
+//            piece's rows up (three loads that wait for one another) and moves their weights, the others copy
+//            K and V, 64 bytes a thread in flight.  Out of place, to the request's spare pages: rows need no
+//            order among themselves, and what another request shares stays as it is.  The last CTA of a request to finish swaps the pages and sets the length.
 // Bound by the kept rows' bytes, read and written once.
 #include "paged.cuh"
 
@@ -20,8 +20,8 @@ constexpr int SW = ST / 32;
 constexpr int BINS = 2048;
 constexpr int KEYS = 24576;        // keys held in shared memory (96 KB: two CTAs an SM)
 constexpr int SELECT_SMEM = KEYS * 4;
-constexpr int MT = 256;            // move: threads
-constexpr int MR = 32;             // rows of a piece
+constexpr int MT = 256;            // move: threads that copy
+constexpr int MR = 64;             // rows of a piece
 constexpr int MC = 4;              // CTAs an SM
 
 // Weights as unsigned keys in the same order; NaN is the smallest, both zeros are one.
@@ -145,7 +145,14 @@ __global__ void __launch_bounds__(ST) evict_select_kernel(const EvictArgs a, con
         }
       }
     } else {
-      for (int j = lo + t; j < hi; j += ST) count(keys[j]);
+#pragma unroll 4
+      for (int j0 = (lo & ~3) + 4 * t; j0 < hi; j0 += 4 * ST) {
+        const uint4 k = *reinterpret_cast<const uint4*>(keys + j0);
+        const uint32_t x[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (j0 + e >= lo && j0 + e < hi) count(x[e]);
+      }
     }
     __syncthreads();
     const int bin = find_bin(hist, 1 << bits, need, s_scan, s_bin);
@@ -191,7 +198,7 @@ __global__ void __launch_bounds__(ST) evict_select_kernel(const EvictArgs a, con
 }
 
 // Pieces of MR kept rows, in the order request (those to be moved), layer, head, piece.
-__global__ void __launch_bounds__(MT, MC) evict_move_kernel(const EvictArgs a, const PagedEvictArgs p, int chunks,
+__global__ void __launch_bounds__(MT + 32, MC) evict_move_kernel(const EvictArgs a, const PagedEvictArgs p, int chunks,
                                                             int vshift) {
   __shared__ int s_src[2][MR], s_dst[2][MR];
   __shared__ bool last;
@@ -212,62 +219,71 @@ __global__ void __launch_bounds__(MT, MC) evict_move_kernel(const EvictArgs a, c
       n -= __popc(m);
     }
   };
-  // a piece's rows: looked up by threads 0 .. MR - 1
+  // a piece's rows (by the warp behind the others, two each), and their weights
   auto look_up = [&](int b, int v, int buf) {  // v: piece of the request
-    const int group = v / chunks, n0 = (v - group * chunks) * MR, rows = min(MR, a.budget - n0);
+    const int group = v / chunks, n0 = (v - group * chunks) * MR;
     const int l = group / a.g.Hkv, h = group - l * a.g.Hkv;
-    if (t < rows) {
-      const int to = n0 + t;
-      const int r = a.kept[((static_cast<size_t>(l) * a.batch + b) * a.g.Hkv + h) * a.budget + to];
-      const int page = a.spare[static_cast<size_t>(b) * a.spare_pages + (to >> a.g.shift)];
-      const int src = paged_row_or_zero(a.g, b, h, r, a.status);
-      const int dst = ((page * a.g.Hkv + h) << a.g.shift) + (to & ((1 << a.g.shift) - 1));
-      s_src[buf][t] = src;
-      s_dst[buf][t] = dst;
-      p.w[l][dst] = p.w[l][src];
+    const int32_t* kept = a.kept + ((static_cast<size_t>(l) * a.batch + b) * a.g.Hkv + h) * a.budget;
+    int r[2], page[2], src[2], dst[2];
+    float w[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int to = min(n0 + lane + 32 * e, a.budget - 1);
+      r[e] = kept[to];
+      page[e] = a.spare[static_cast<size_t>(b) * a.spare_pages + (to >> a.g.shift)];
+      dst[e] = ((page[e] * a.g.Hkv + h) << a.g.shift) + (to & ((1 << a.g.shift) - 1));
     }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) src[e] = paged_row_or_zero(a.g, b, h, r[e], a.status);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      s_src[buf][lane + 32 * e] = src[e];
+      s_dst[buf][lane + 32 * e] = dst[e];
+      w[e] = p.w[l][src[e]];
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (n0 + lane + 32 * e < a.budget) p.w[l][dst[e]] = w[e];
   };
   int n = u0 / per_request, v = u0 - n * per_request, b = 0, buf = 0, mine = 0;
   if (u0 < u1) {
     b = request(n);
-    look_up(b, v, buf);
+    if (t >= MT) look_up(b, v, buf);
   }
   for (int u = u0; u < u1; ++u) {
     __syncthreads();  // (the piece's rows are there, and the other buffer's readers are done)
-    const int group = v / chunks, rows = min(MR, a.budget - (v - group * chunks) * MR), l = group / a.g.Hkv;
-    const uint4* k = static_cast<const uint4*>(p.k[l]);
-    const uint4* vv = static_cast<const uint4*>(p.v[l]);
-    const int vectors = rows << vshift, mask = (1 << vshift) - 1;
-    constexpr int U = 4;  // (a vector of K and of V each: all of a piece of 256-byte rows)
-    const int at_b = b;
-    bool ends = u + 1 == u1;
-    for (int i0 = t; i0 < vectors || i0 == t; i0 += MT * U) {
-      uint4 xk[U], xv[U];
+    const int group = v / chunks, rows = min(MR, a.budget - (v - group * chunks) * MR), l = group / a.g.Hkv, at_b = b;
+    const bool over = v + 1 == per_request, ends = over || u + 1 == u1;
+    v = over ? 0 : v + 1;
+    if (over && u + 1 < u1) b = request(++n);
+    if (t >= MT) {
+      if (u + 1 < u1) look_up(b, v, buf ^ 1);
+    } else {
+      const uint4* k = static_cast<const uint4*>(p.k[l]);
+      const uint4* vv = static_cast<const uint4*>(p.v[l]);
+      uint4* kd = static_cast<uint4*>(p.k[l]);
+      uint4* vd = static_cast<uint4*>(p.v[l]);
+      const int vectors = rows << vshift, mask = (1 << vshift) - 1;
+      constexpr int U = 2;  // a vector of K and one of V each
+      for (int i0 = t; i0 < vectors; i0 += MT * U) {
+        uint4 xk[U], xv[U];
 #pragma unroll
-      for (int x = 0; x < U; ++x) {
-        const int i = i0 + x * MT;
-        if (i < vectors) {
-          const size_t at = (static_cast<size_t>(s_src[buf][i >> vshift]) << vshift) + (i & mask);
-          xk[x] = __ldcs(k + at);
-          xv[x] = __ldcs(vv + at);
+        for (int x = 0; x < U; ++x) {
+          const int i = i0 + x * MT;
+          if (i < vectors) {
+            const size_t at = (static_cast<size_t>(s_src[buf][i >> vshift]) << vshift) + (i & mask);
+            xk[x] = __ldcs(k + at);
+            xv[x] = __ldcs(vv + at);
+          }
         }
-      }
-      if (i0 == t && u + 1 < u1) {  // the next piece, under the loads
-        const bool over = v + 1 == per_request;
-        if (over) {
-          ends = true;
-          b = request(++n);
-        }
-        v = over ? 0 : v + 1;
-        look_up(b, v, buf ^ 1);
-      }
 #pragma unroll
-      for (int x = 0; x < U; ++x) {
-        const int i = i0 + x * MT;
-        if (i < vectors) {
-          const size_t at = (static_cast<size_t>(s_dst[buf][i >> vshift]) << vshift) + (i & mask);
-          __stcs(static_cast<uint4*>(p.k[l]) + at, xk[x]);
-          __stcs(static_cast<uint4*>(p.v[l]) + at, xv[x]);
+        for (int x = 0; x < U; ++x) {
+          const int i = i0 + x * MT;
+          if (i < vectors) {
+            const size_t at = (static_cast<size_t>(s_dst[buf][i >> vshift]) << vshift) + (i & mask);
+            __stcs(kd + at, xk[x]);
+            __stcs(vd + at, xv[x]);
+          }
         }
       }
     }
@@ -282,7 +298,7 @@ __global__ void __launch_bounds__(MT, MC) evict_move_kernel(const EvictArgs a, c
     __syncthreads();
     if (!last) continue;
     __threadfence();
-    for (int i = t; i < a.spare_pages; i += MT) {
+    for (int i = t; i < a.spare_pages; i += MT + 32) {
       int32_t* x = a.table + static_cast<size_t>(at_b) * a.g.max_pages + i;
       int32_t* y = a.spare + static_cast<size_t>(at_b) * a.spare_pages + i;
       const int32_t old = *x;
@@ -299,7 +315,7 @@ __global__ void __launch_bounds__(MT, MC) evict_move_kernel(const EvictArgs a, c
   if (t == 0) last = atomicAdd(a.count + a.batch, 1u) == gridDim.x - 1;
   __syncthreads();
   if (!last) return;
-  for (int i = t; i < a.batch; i += MT) a.ready[i] = 0;
+  for (int i = t; i < a.batch; i += MT + 32) a.ready[i] = 0;
   if (t == 0) a.count[a.batch] = 0;
 }
 
@@ -335,7 +351,7 @@ cudaError_t launch_paged_evict(const eagle_paged_evict_desc& d, const PagedEvict
   const int bytes = d.head_dim * (d.dtype == EAGLE_F32 ? 4 : 2);
   const long long pieces = static_cast<long long>(groups) * chunks;
   const int ctas = static_cast<int>(pieces < sms * MC ? pieces : sms * MC);
-  return launch_pdl(evict_move_kernel, dim3(ctas), dim3(MT), 0, s, a, p, chunks,
+  return launch_pdl(evict_move_kernel, dim3(ctas), dim3(MT + 32), 0, s, a, p, chunks,
                     bytes == 128 ? 3 : bytes == 256 ? 4 : 5);
 }
 
