@@ -18,8 +18,7 @@ namespace {
 constexpr int ST = 512;            // select: threads
 constexpr int SW = ST / 32;
 constexpr int BINS = 2048;
-constexpr int KEYS = 24576;        // keys held in shared memory (96 KB: two CTAs an SM)
-constexpr int SELECT_SMEM = KEYS * 4;
+constexpr int KEYS = 24576;        // most keys held in shared memory (96 KB: two CTAs an SM; 16384 and below: three)
 constexpr int MT = 256;            // move: threads that copy
 constexpr int MR = 64;             // rows of a piece
 constexpr int MC = 4;              // CTAs an SM
@@ -77,7 +76,7 @@ __device__ __forceinline__ int find_bin(const unsigned* hist, int bins, int& nee
   return s_bin[0];
 }
 
-__global__ void __launch_bounds__(ST) evict_select_kernel(const EvictArgs a, const PagedEvictArgs p) {
+__global__ void __launch_bounds__(ST, 3) evict_select_kernel(const EvictArgs a, const PagedEvictArgs p, int room) {
   extern __shared__ uint32_t keys[];
   __shared__ unsigned hist[BINS];
   __shared__ int s_scan[SW], s_bin[2], s_bad, s_gt[SW], s_eq[SW];
@@ -109,7 +108,7 @@ __global__ void __launch_bounds__(ST) evict_select_kernel(const EvictArgs a, con
   int need = a.budget - a.sink - a.recent;        // of which these stay, fewer than there are (L > limit >= budget)
   if (need == 0) return;
   const float* w = p.w[l];
-  const bool held = hi <= KEYS;
+  const bool held = hi <= room;
   // four keys from row j (a multiple of 4, so of one page) on
   auto load_keys = [&](int j) {
     const float4 x = *reinterpret_cast<const float4*>(w + paged_row_or_zero(a.g, b, h, j, a.status));
@@ -343,10 +342,11 @@ cudaError_t launch_paged_evict(const eagle_paged_evict_desc& d, const PagedEvict
   a.count = static_cast<unsigned*>(ws);
   a.ready = a.count + d.batch + 1;
   static unsigned long long configured = 0;
-  cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(evict_select_kernel), SELECT_SMEM, configured);
+  cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(evict_select_kernel), KEYS * 4, configured);
   if (e != cudaSuccess) return e;
   const int groups = d.layers * d.batch * d.n_kv_heads, chunks = (d.budget + MR - 1) / MR;
-  e = launch_pdl(evict_select_kernel, dim3(groups), dim3(ST), SELECT_SMEM, s, a, p);
+  const int room = a.g.capacity < KEYS ? a.g.capacity : KEYS;  // (a multiple of 16)
+  e = launch_pdl(evict_select_kernel, dim3(groups), dim3(ST), static_cast<size_t>(room) * 4, s, a, p, room);
   if (e != cudaSuccess) return e;
   const int bytes = d.head_dim * (d.dtype == EAGLE_F32 ? 4 : 2);
   const long long pieces = static_cast<long long>(groups) * chunks;
