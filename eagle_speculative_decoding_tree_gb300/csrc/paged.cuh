@@ -29,15 +29,18 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// A raw dot product as a score in log2 units.  The cap: c tanh(x) = c - 2 c / (1 + e^2x), in which
-// neither end overflows (e^2x = inf: c, 0: -c); off by a few roundings of c, as c tanh itself in fp32.
-// slope_log2 = slope * log2 e (0: none), dist the row's position minus the key's.
+// The cap in log2 units: c tanh(x) = c - 2 c / (1 + e^2x), in which neither end overflows (e^2x = inf: c, 0: -c); off by
+// a few roundings of c, as c tanh itself in fp32.
+__device__ __forceinline__ float cap_score(const ScoreShape& s, float raw) {
+  return fmaf(-2.f * s.cap_log2, rcp_approx(1.f + sm100::ex2(raw * s.cap_mul)), s.cap_log2);
+}
+
+// A raw dot product as a score in log2 units; slope_log2 = slope * log2 e (0: none), dist the row's position minus the
+// key's.
 template <bool SHAPED>
 __device__ __forceinline__ float shape_score(const ScoreShape& s, float raw, float slope_log2, int dist) {
   if (!SHAPED) return raw * s.scale_log2;
-  float t = raw * s.scale_log2;
-  if (s.cap_log2 > 0.f)
-    t = fmaf(-2.f * s.cap_log2, rcp_approx(1.f + sm100::ex2(raw * s.cap_mul)), s.cap_log2);
+  float t = s.cap_log2 > 0.f ? cap_score(s, raw) : raw * s.scale_log2;
   t = fmaf(-slope_log2, static_cast<float>(dist), t);
   return s.window > 0 && dist >= s.window ? -INFINITY : t;
 }
@@ -50,22 +53,29 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-// Launch with programmatic stream serialization (the kernel waits before it reads or writes).
+// Launch with programmatic stream serialization (the kernel waits before it reads or writes); coop: all CTAs resident.
 template <typename... KArgs, typename... Args>
-inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
-                              Args... args) {
+inline cudaError_t launch_pdl_coop(void (*kern)(KArgs...), bool coop, dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                                   Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeCooperative;
+  attr[1].val.cooperative = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = coop ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                              Args... args) {
+  return launch_pdl_coop(kern, false, grid, block, smem, s, args...);
 }
 
 // Opt-in to `smem` bytes of dynamic shared memory, once per kernel and device.

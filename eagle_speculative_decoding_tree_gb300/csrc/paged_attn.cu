@@ -275,6 +275,7 @@ cudaError_t launch_paged_attn(const eagle_paged_attn_desc& d, const void* q, con
   a.G = d.n_q_heads / d.n_kv_heads;
   a.W = (d.rows + 63) / 64;
   a.align = a.pad = 16;
+  a.together = 0;
   a.out_f32 = d.out_dtype == EAGLE_F32;
   const bool shaped = d.softcap > 0.f || d.window > 0 || slopes;
   const int rows = d.rows * a.G;

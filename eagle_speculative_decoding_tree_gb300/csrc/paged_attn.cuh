@@ -8,7 +8,8 @@
 // requests look like.  A CTA's share covers the end of one group, whole groups, and the beginning of another;
 // whole groups are written as they are, of the others the CTA leaves partials (row maxima, sums and
 // unnormalised outputs, fp32) in one of its two slots, and the group's last CTA to arrive (a counter) joins
-// them, in the order of the list: results do not depend on which one that is.  No CTA waits for another.
+// them, in the order of the list: results do not depend on which one that is.  No CTA waits for another, but where a
+// join is so long that its CTAs share it (`together`, a cooperative launch).
 // With kSplitFrom CTAs a group or more, shares end with the groups: each group has CTAs in proportion to its
 // units, and a CTA one segment.
 #pragma once
@@ -36,13 +37,14 @@ struct PagedAttnArgs {
   uint32_t* status;
   int* err;
   unsigned* count;   // [2 CTAs]: arrivals, by the group's first CTA and its slot
-  unsigned* leave;   // [2 CTAs]: CTAs past their wait (tcgen05)
+  unsigned* leave;   // [2 CTAs]: CTAs past their wait, where they wait
   float* part_o;     // [2 CTAs][RB][D]
   float* part_ml;    // [2 CTAs][RB][2]
   int B, R, Hq, G, W;
   int rpb;           // rows of a block
   int align, pad;    // the list's first key and the prefix's positions are multiples of these
   int out_f32;
+  int together;      // from this many CTAs a group on, they join their partials together (0: never)
 };
 
 // paged_attn_mma.cu: bf16, row blocks of 16 (R G <= 16) or 32.
@@ -317,24 +319,25 @@ __device__ __forceinline__ void paged_fold_row(const PagedAttnArgs& a, const Pag
   }
 }
 
-// A row of a group joined from its CTAs' slots, by one warp.  The partial rows of BATCH CTAs are requested before
+// A row's state from slots i0 .. i1 - 1 of its group, by one warp.  The partial rows of BATCH CTAs are requested before
 // their weights are known.
 template <int RB, int D>
-__device__ __forceinline__ void paged_join_row(const PagedAttnArgs& a, const PagedSegment& s, int row, int lane) {
+__device__ __forceinline__ void paged_join_state(const PagedAttnArgs& a, const PagedSegment& s, int row, int lane, int i0,
+                                                 int i1, float& m, float& l, float (&o)[D / 32]) {
   constexpr int N = D / 32, BATCH = 20;
-  const int n = s.c1 - s.c0 + 1;
-  float m = -INFINITY, l = 0.f, o[N];
+  m = -INFINITY;
+  l = 0.f;
 #pragma unroll
   for (int e = 0; e < N; ++e) o[e] = 0.f;
   auto place = [&](int i) { return static_cast<size_t>(i == 0 ? s.slot0 : 2 * (s.c0 + i)) * RB + row; };
 #pragma unroll 1
-  for (int i0 = 0; i0 < n; i0 += BATCH) {
+  for (; i0 < i1; i0 += BATCH) {
     float2 x[BATCH][N / 2], ml = make_float2(-INFINITY, 0.f);
     const int mine = i0 + lane;
-    if (lane < BATCH && mine < n) ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + place(mine));
+    if (lane < BATCH && mine < i1) ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + place(mine));
 #pragma unroll
     for (int u = 0; u < BATCH; ++u) {
-      const float2* po = reinterpret_cast<const float2*>(a.part_o + place(min(i0 + u, n - 1)) * D + lane * N);
+      const float2* po = reinterpret_cast<const float2*>(a.part_o + place(min(i0 + u, i1 - 1)) * D + lane * N);
 #pragma unroll
       for (int e = 0; e < N / 2; ++e) x[u][e] = __ldcg(po + e);
     }
@@ -348,7 +351,7 @@ __device__ __forceinline__ void paged_join_row(const PagedAttnArgs& a, const Pag
 #pragma unroll
     for (int u = 0; u < BATCH; ++u) {
       const float g = __shfl_sync(0xffffffffu, f, u);
-      if (i0 + u < n) {  // (the others' row is there twice)
+      if (i0 + u < i1) {  // (the others' row is there twice)
 #pragma unroll
         for (int e = 0; e < N / 2; ++e) {
           o[2 * e] = fmaf(g, x[u][e].x, o[2 * e]);
@@ -357,7 +360,6 @@ __device__ __forceinline__ void paged_join_row(const PagedAttnArgs& a, const Pag
       }
     }
   }
-  paged_store<D>(a, paged_out_row(a, s, s.row0 + row), lane, o, m, l);
 }
 
 // The end of a segment whose group other CTAs share: this CTA's partials are written; the last CTA of the
@@ -376,7 +378,33 @@ __device__ __forceinline__ void paged_arrive(const PagedAttnArgs& a, const Paged
   __syncthreads();
   if (!*s_last) return;
   const int rows = min(RB, s.rq.Rb * a.G - s.row0);
-  for (int row = threadIdx.x >> 5; row < rows; row += W) paged_join_row<RB, D>(a, s, row, threadIdx.x & 31);
+  for (int row = threadIdx.x >> 5; row < rows; row += W) {
+    float m, l, o[D / 32];
+    paged_join_state<RB, D>(a, s, row, threadIdx.x & 31, 0, s.c1 - s.c0 + 1, m, l, o);
+    paged_store<D>(a, paged_out_row(a, s, s.row0 + row), threadIdx.x & 31, o, m, l);
+  }
+}
+
+// Waits (one thread; cooperative launch) until the group's CTAs have left their partials; the last one past it returns
+// the counters to zero.
+__device__ __forceinline__ bool paged_wait(const PagedAttnArgs& a, const PagedSegment& s, int err) {
+  const int n = s.c1 - s.c0 + 1;
+  const int* count = reinterpret_cast<const int*>(a.count + s.slot0);
+  bool all = sm100::ld_acquire_gpu(count) >= n;
+  const uint64_t t0 = sm100::global_ns();
+  while (!all && sm100::global_ns() - t0 < 2000000000ull) {
+    __nanosleep(32);
+    all = sm100::ld_acquire_gpu(count) >= n;
+  }
+  if (!all) {
+    atomicOr(a.err, err);
+    return false;
+  }
+  if (atomicAdd(a.leave + s.slot0, 1u) == static_cast<unsigned>(n) - 1) {
+    atomicExch(a.count + s.slot0, 0u);
+    atomicExch(a.leave + s.slot0, 0u);
+  }
+  return true;
 }
 
 }  // namespace eagle

@@ -53,6 +53,7 @@ __global__ void __launch_bounds__(W * 32, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t full[W][F::ST];
   __shared__ int s_last;
+  __shared__ PagedSegment s_part[2];  // segments that are joined together
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int qr = lane >> 2, qc = lane & 3;  // a fragment's row and column pair
   uint8_t* ring = smem + warp * F::RING;
@@ -70,6 +71,7 @@ __global__ void __launch_bounds__(W * 32, 1)
   sm100::griddep_launch_dependents();
   PagedList list = paged_list(a, blockIdx.x, gridDim.x);
   int issued = 0, used = 0;  // chunks
+  int parts = 0;
   bool first = true, ok = true;
   // ldmatrix addresses: K chunk (keys, then dims), V chunk (dims, then keys); a half of 64 dims is 16 rows of 128 bytes
   const int k_key = ((lane >> 4) << 3) + (lane & 7), k_c = (lane >> 3) & 1;
@@ -314,11 +316,44 @@ __global__ void __launch_bounds__(W * 32, 1)
       paged_fold_row<W, F::RB, D>(a, s, whole, slot, r, lane, s_m, s_l, reinterpret_cast<float*>(smem) + r * F::LD,
                                   F::RING / 4);
     sm100::fence_proxy_async_smem();  // the ring is TMA's again
-    if (!whole)
-      paged_arrive<W, F::RB, D>(a, s, &s_last);
-    else
+    if (whole) {
       __syncthreads();
+    } else if (a.together && s.c1 - s.c0 + 1 >= a.together) {
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        atomicAdd(a.count + s.slot0, 1u);
+        s_part[parts & 1] = s;
+      }
+      ++parts;
+    } else {
+      paged_arrive<W, F::RB, D>(a, s, &s_last);
+    }
     first = false;
+  }
+  // ---- long joins: a share of the rows each, a part of the partials a warp
+  float* so = reinterpret_cast<float*>(smem);  // [warp][D], the ring is free
+  for (int i = 0; i < parts; ++i) {
+    __syncthreads();
+    const PagedSegment& s = s_part[i];
+    if (threadIdx.x == 0) s_last = paged_wait(a, s, 2);
+    __syncthreads();
+    if (!s_last) continue;
+    const int n = s.c1 - s.c0 + 1, me = static_cast<int>(blockIdx.x) - s.c0;
+    const int rows = min(F::RB, s.rq.Rb * a.G - s.row0);
+    for (int r = rows * me / n; r < rows * (me + 1) / n; ++r) {
+      float m, l, o[D / 32];
+      paged_join_state<F::RB, D>(a, s, r, lane, n * warp / W, n * (warp + 1) / W, m, l, o);
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) so[warp * D + lane * (D / 32) + e] = o[e];
+      if (lane == 0) {
+        s_m[warp * F::RB + r] = m;
+        s_l[warp * F::RB + r] = l;
+      }
+      __syncthreads();
+      if (warp == 0) paged_fold_row<W, F::RB, D>(a, s, true, 0, r, lane, s_m, s_l, so, D);
+      __syncthreads();
+    }
   }
 }
 
@@ -328,7 +363,7 @@ cudaError_t launch_mma(const PagedAttnArgs& a, const Maps& tm, int ctas, cudaStr
   auto kern = paged_attn_mma_kernel<D, MT, SHAPED, PRECISE>;
   constexpr int smem = Few<D, MT>::SMEM;
   const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kern), smem, conf);
-  return e != cudaSuccess ? e : launch_pdl(kern, dim3(ctas), dim3(W * 32), smem, s, tm, a);
+  return e != cudaSuccess ? e : launch_pdl_coop(kern, a.together > 0, dim3(ctas), dim3(W * 32), smem, s, tm, a);
 }
 
 template <int D, int MT>
@@ -353,6 +388,10 @@ cudaError_t launch_paged_attn_mma(PagedAttnArgs a, int head_dim, long long pool_
     return cudaErrorInvalidValue;
   const bool two = a.R * a.G > 16;
   a.rpb = two ? 32 : 16;
+  // One CTA joins 40 partials of 16 rows in about 4 us; the others' wait costs about as much.  (Only a call of so few
+  // heads can have such groups, and it alone pays for a cooperative launch: MQA over 130K 37 -> 25 us.)
+  constexpr int kTogether = 40;
+  a.together = a.B * a.g.Hkv * kTogether <= ctas ? kTogether : 0;
   if (head_dim == 128)
     return two ? launch_mma_kind<128, 2>(a, tm, shaped, precise, ctas, s)
                : launch_mma_kind<128, 1>(a, tm, shaped, precise, ctas, s);

@@ -69,16 +69,48 @@ __device__ __forceinline__ int tile_valid(const PagedAttnArgs& a, const PagedSeg
   return at < s.rq.pk ? min(kUnit, s.rq.L - s.rq.k0 - at) : a.tk ? s.rq.Rb : 0;
 }
 
-// 32 raw scores of keys j0 .. of a row into log2 units.
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// 32 raw scores of a row into log2 units; the first key is at distance dist0 (kdepth: tree keys' depths).
 __device__ __forceinline__ void shape32(const ScoreShape& sh, uint32_t (&r)[32], float slope, int dist0, int depth,
                                         const int8_t* kdepth) {
+  if (sh.cap_log2 > 0.f) {
+    float most = 0.f;
+#pragma unroll
+    for (int j = 0; j < 32; j += 2)
+      most = max3(most, fabsf(__uint_as_float(r[j])), fabsf(__uint_as_float(r[j + 1])));
+    // Scores well below the cap, the usual case: a polynomial, two scores an instruction (the formula's two special
+    // functions a score make it 1.9 times the time of a tile).
+    if (__all_sync(0xffffffffu, most <= sh.cap_small)) {
+      uint64_t p[5];
+#pragma unroll
+      for (int i = 0; i < 5; ++i) p[i] = f32x2(__float_as_uint(sh.p[i]), __float_as_uint(sh.p[i]));
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) {
+        const uint64_t x = f32x2(r[j], r[j + 1]), y = mul_f32x2(x, x);
+        const uint64_t q = fma_f32x2(y, fma_f32x2(y, fma_f32x2(y, fma_f32x2(y, p[4], p[3]), p[2]), p[1]), p[0]);
+        float t0, t1;
+        f32x2_split(mul_f32x2(x, q), t0, t1);
+        r[j] = __float_as_uint(t0);
+        r[j + 1] = __float_as_uint(t1);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(cap_score(sh, __uint_as_float(r[j])));
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * sh.scale_log2);
+  }
+  if (sh.slopes == nullptr) return;
 #pragma unroll
   for (int j = 0; j < 32; ++j) {
     const int dist = kdepth ? depth - kdepth[j] : dist0 - j;
-    float t = __uint_as_float(r[j]) * sh.scale_log2;
-    if (sh.cap_log2 > 0.f)
-      t = fmaf(-2.f * sh.cap_log2, rcp_approx(1.f + ex2(__uint_as_float(r[j]) * sh.cap_mul)), sh.cap_log2);
-    r[j] = __float_as_uint(fmaf(-slope, static_cast<float>(dist), t));
+    r[j] = __float_as_uint(fmaf(-slope, static_cast<float>(dist), __uint_as_float(r[j])));
   }
 }
 
@@ -368,6 +400,10 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
         tmem_ld_wait();
         shaped(s0, 0);
         shaped(s1, 1);
+        if (SHAPED) {  // (they are read again below)
+          tmem_st32(sc, s0);
+          tmem_st32(sc + 32, s1);
+        }
         shaped(s2, 2);
         shaped(s3, 3);
         const float mx = fmaxf(max64(s0, s1), max64(s2, s3));
@@ -394,11 +430,14 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
         // keys 64..127 first: their P goes where S has been read; keys 0..63 are read again
         float ls = emit_p32<PRECISE>(s2, sc + 64, sl2x2, nmux2);
         ls += emit_p32<PRECISE>(s3, sc + 80, sl2x2, nmux2);
+        if (SHAPED) tmem_st_wait();
         tmem_ld32(sc, s0);
         tmem_ld32(sc + 32, s1);
         tmem_ld_wait();
-        shaped(s0, 0);
-        shaped(s1, 1);
+        if (!SHAPED && !full) {
+          mask_keys(s0, km[0]);
+          mask_keys(s1, km[1]);
+        }
         ls += emit_p32<PRECISE>(s0, sc, sl2x2, nmux2);
         ls += emit_p32<PRECISE>(s1, sc + 16, sl2x2, nmux2);
         l += ls;
@@ -492,25 +531,11 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
     for (int i = 0; i < parts; ++i) {
       const PagedSegment s = part[i];
       const int n = s.c1 - s.c0 + 1;
-      if (threadIdx.x == 0) {
-        bool all = ld_acquire_gpu(reinterpret_cast<const int*>(a.count + s.slot0)) >= n;
-        const uint64_t t0 = global_ns();
-        while (!all && global_ns() - t0 < 2000000000ull) {
-          __nanosleep(32);
-          all = ld_acquire_gpu(reinterpret_cast<const int*>(a.count + s.slot0)) >= n;
-        }
-        if (!all) atomicOr(a.err, ERR_GROUP);
-        bar.go = all;
-      }
+      if (threadIdx.x == 0) bar.go = paged_wait(a, s, ERR_GROUP);
       bar_sync(1, 256);
       const bool go = bar.go != 0;
       bar_sync(1, 256);
       if (!go) continue;
-      // past the wait, the last CTA returns the counters to zero
-      if (threadIdx.x == 0 && atomicAdd(a.leave + s.slot0, 1u) == static_cast<unsigned>(n) - 1) {
-        atomicExch(a.count + s.slot0, 0u);
-        atomicExch(a.leave + s.slot0, 0u);
-      }
       const int rows = min(a.rpb, s.rq.Rb * a.G - s.row0), me = static_cast<int>(blockIdx.x) - s.c0;
       // 128 pieces of 4 dims x 32 rows, a warp each
       for (int v = 128 * me / n + warp; v < 128 * (me + 1) / n; v += 8) join_piece(a, s, n, v >> 2, (v & 3) * 32 + lane, rows);
@@ -528,22 +553,8 @@ template <bool PRECISE, bool SHAPED>
 cudaError_t launch_tc(const PagedAttnArgs& a, const Maps& tm, int ctas, cudaStream_t s) {
   static unsigned long long conf = 0;
   auto kern = paged_attn_tc_kernel<PRECISE, SHAPED>;
-  cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kern), SMEM_ALLOC, conf);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(NT);
-  cfg.dynamicSmemBytes = SMEM_ALLOC;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeCooperative;
-  attr[1].val.cooperative = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, kern, tm, a);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kern), SMEM_ALLOC, conf);
+  return e != cudaSuccess ? e : launch_pdl_coop(kern, true, dim3(ctas), dim3(NT), SMEM_ALLOC, s, tm, a);
 }
 
 }  // namespace

@@ -98,8 +98,9 @@ SHAPES = [
     dict(seq=[100, 31], R=5, Hq=6, Hkv=2), dict(seq=[333], R=33, Hq=28, Hkv=4, T=32),
     dict(seq=[40] * 37, Hq=4, Hkv=2), dict(seq=[260, 3], R=17, D=64, Hq=8, Hkv=2, T=128, nodes=[17, 2]),
     dict(seq=[600, 1], R=3, Hq=64, Hkv=1, T=64), dict(seq=[4097], Hq=2, Hkv=1), dict(seq=[70, 20], R=2, Hq=130, Hkv=1),
+    dict(seq=[6000], Hq=16, Hkv=1, T=64), dict(seq=[9001, 0], R=2, Hq=16, Hkv=1), dict(seq=[7000], D=64, Hq=9, Hkv=1, R=3),
 ]
-SCORES = [dict(), dict(cap=30.0), dict(window=50), dict(slopes=True), dict(cap=5.0, window=333, slopes=True),
+SCORES = [dict(), dict(cap=30.0), dict(cap=200.0), dict(window=50), dict(slopes=True), dict(cap=5.0, window=333, slopes=True),
           dict(window=1), dict(window=16, slopes=True)]
 
 
