@@ -236,15 +236,21 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
       }
       if (s.t0 >= s.t1) break;
       const int T = 1 << a.g.shift;
+      // lane: box lane / 2, half lane % 2 of a tile; its row of the pool (or of the tree), looked up a tile ahead
+      auto row_of = [&](int u) {
+        const int valid = tile_valid(a, s, u);
+        if (u * kUnit >= s.rq.pk) return (s.b * a.g.Hkv + s.h) * a.R;
+        return (lane >> 1) << a.g.shift < valid
+                   ? paged_row_or_zero(a.g, s.b, s.h, s.rq.k0 + u * kUnit + ((lane >> 1) << a.g.shift), a.status)
+                   : 0;
+      };
+      int y_next = row_of(s.t0);
       for (int u = s.t0; u < s.t1 && ok; ++u, ++tile) {
         const bool tree = u * kUnit >= s.rq.pk;
         const int valid = tile_valid(a, s, u), n = tree ? 1 : (valid + T - 1) >> a.g.shift;  // boxes of a half
-        // lane: box lane / 2, half lane % 2
         const bool mine = lane < 2 * n && valid > 0;
-        int y = 0;
-        if (mine)
-          y = tree ? (s.b * a.g.Hkv + s.h) * a.R
-                   : paged_row_or_zero(a.g, s.b, s.h, s.rq.k0 + u * kUnit + ((lane >> 1) << a.g.shift), a.status);
+        const int y = y_next;
+        if (u + 1 < s.t1) y_next = row_of(u + 1);
         const int at = (lane & 1) * HALF + (lane >> 1) * T * 128;
         const uint32_t bytes = valid <= 0 ? 0 : tree ? TILE : n * T * 256;
         const int ks = tile % KST, vs = tile % VST;
