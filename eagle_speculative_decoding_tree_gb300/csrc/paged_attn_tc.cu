@@ -114,70 +114,81 @@ __device__ __forceinline__ void shape32(const ScoreShape& sh, uint32_t (&r)[32],
   }
 }
 
-// P pieces (8 apart, from v on; those below v1) of 4 dims x 32 rows of a group, from its n partials, by one warp: a lane
-// is a row.  BATCH partials of every piece are in flight together.
-template <int BATCH, int P>
-__device__ __forceinline__ void join_pieces(const PagedAttnArgs& a, const PagedSegment& s, int n, int v, int v1, int lane,
-                                            int rows) {
-  float m[P], l[P], o[P][4];
+// This CTA's share of a group's rows from the group's n partials, in pieces of 4 C dims x 32 rows, a warp each: a lane is a
+// row.  BATCH partials are in flight together.
+template <int BATCH, int C>
+__device__ __forceinline__ void join_share(const PagedAttnArgs& a, const PagedSegment& s, int n, int me, int warp, int lane,
+                                           int rows) {
+  constexpr int U = 128 / C;
+  for (int v = U * me / n + warp; v < U * (me + 1) / n; v += 8) {
+    const int row = (v & 3) * 32 + lane, c = (v >> 2) * C;
+    if (row >= rows) continue;
+    float m = -INFINITY, l = 0.f, o[C][4];
 #pragma unroll
-  for (int k = 0; k < P; ++k) {
-    m[k] = -INFINITY;
-    l[k] = o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0.f;
-  }
+    for (int k = 0; k < C; ++k) o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0.f;
 #pragma unroll 1
-  for (int i0 = 0; i0 < n; i0 += BATCH) {
-    float4 x[P][BATCH];
-    float2 ml[P][BATCH];
-#pragma unroll
-    for (int k = 0; k < P; ++k) {
-      const int piece = min(v + 8 * k, v1 - 1), row = min((piece & 3) * 32 + lane, rows - 1), c = piece >> 2;
+    for (int i0 = 0; i0 < n; i0 += BATCH) {
+      float4 x[BATCH][C];
+      float2 ml[BATCH];
 #pragma unroll
       for (int u = 0; u < BATCH; ++u) {
         const int i = min(i0 + u, n - 1);
         const size_t slot = i == 0 ? s.slot0 : 2 * (s.c0 + i);
-        ml[k][u] = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + slot * RB + row);
-        x[k][u] = __ldcg(reinterpret_cast<const float4*>(a.part_o) + (slot * 32 + c) * RB + row);
+        ml[u] = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + slot * RB + row);
+#pragma unroll
+        for (int k = 0; k < C; ++k) x[u][k] = __ldcg(reinterpret_cast<const float4*>(a.part_o) + (slot * 32 + c + k) * RB + row);
       }
-    }
+      float top = m;
 #pragma unroll
-    for (int k = 0; k < P; ++k) {
-      float top = m[k];
+      for (int u = 0; u < BATCH; ++u) top = fmaxf(top, ml[u].x);  // (the last one may be there twice)
+      const float old = m == -INFINITY ? 0.f : ex2(m - top);
+      m = top;
+      l *= old;
 #pragma unroll
-      for (int u = 0; u < BATCH; ++u) top = fmaxf(top, ml[k][u].x);  // (the last one may be there twice)
-      const float old = m[k] == -INFINITY ? 0.f : ex2(m[k] - top);
-      m[k] = top;
-      l[k] *= old;
+      for (int k = 0; k < C; ++k) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[k][e] *= old;
+        for (int e = 0; e < 4; ++e) o[k][e] *= old;
+      }
 #pragma unroll
       for (int u = 0; u < BATCH; ++u) {
         if (i0 + u >= n) continue;
-        const float f = ml[k][u].x == -INFINITY ? 0.f : ex2(ml[k][u].x - top);
-        l[k] = fmaf(f, ml[k][u].y, l[k]);
-        o[k][0] = fmaf(f, x[k][u].x, o[k][0]);
-        o[k][1] = fmaf(f, x[k][u].y, o[k][1]);
-        o[k][2] = fmaf(f, x[k][u].z, o[k][2]);
-        o[k][3] = fmaf(f, x[k][u].w, o[k][3]);
+        const float f = ml[u].x == -INFINITY ? 0.f : ex2(ml[u].x - top);
+        l = fmaf(f, ml[u].y, l);
+#pragma unroll
+        for (int k = 0; k < C; ++k) {
+          o[k][0] = fmaf(f, x[u][k].x, o[k][0]);
+          o[k][1] = fmaf(f, x[u][k].y, o[k][1]);
+          o[k][2] = fmaf(f, x[u][k].z, o[k][2]);
+          o[k][3] = fmaf(f, x[u][k].w, o[k][3]);
+        }
       }
     }
-  }
-#pragma unroll
-  for (int k = 0; k < P; ++k) {
-    const int piece = v + 8 * k, row = (piece & 3) * 32 + lane, c = piece >> 2;
-    if (piece >= v1 || row >= rows) continue;
-    const float inv = l[k] > 0.f ? 1.f / l[k] : (l[k] == l[k] ? 0.f : l[k]);
+    const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
     const size_t orow = paged_out_row(a, s, s.row0 + row);
     if (a.out_f32) {
-      reinterpret_cast<float4*>(a.out)[orow * 32 + c] =
-          make_float4(o[k][0] * inv, o[k][1] * inv, o[k][2] * inv, o[k][3] * inv);
+#pragma unroll
+      for (int k = 0; k < C; ++k)
+        reinterpret_cast<float4*>(a.out)[orow * 32 + c + k] =
+            make_float4(o[k][0] * inv, o[k][1] * inv, o[k][2] * inv, o[k][3] * inv);
     } else {
-      const __nv_bfloat162 t0 = __floats2bfloat162_rn(o[k][0] * inv, o[k][1] * inv);
-      const __nv_bfloat162 t1 = __floats2bfloat162_rn(o[k][2] * inv, o[k][3] * inv);
-      reinterpret_cast<uint2*>(a.out)[orow * 32 + c] =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&t0), *reinterpret_cast<const uint32_t*>(&t1));
+      uint32_t w[2 * C];
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        const __nv_bfloat162 t0 = __floats2bfloat162_rn(o[k][0] * inv, o[k][1] * inv);
+        const __nv_bfloat162 t1 = __floats2bfloat162_rn(o[k][2] * inv, o[k][3] * inv);
+        w[2 * k] = *reinterpret_cast<const uint32_t*>(&t0);
+        w[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&t1);
+      }
+      uint2* dst = reinterpret_cast<uint2*>(a.out) + orow * 32 + c;
+      if (C == 1) {
+        dst[0] = make_uint2(w[0], w[1]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < C; k += 2)
+          *reinterpret_cast<uint4*>(dst + k) = make_uint4(w[2 * k], w[2 * k + 1], w[2 * k + 2], w[(2 * k + 3) % (2 * C)]);
+      }
     }
-    if (a.lse && c == 0) a.lse[orow] = (m[k] + log2f(l[k])) * 0.69314718055994531f;
+    if (a.lse && c == 0) a.lse[orow] = (m + log2f(l)) * 0.69314718055994531f;
   }
 }
 
@@ -562,15 +573,12 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
       bar_sync(1, 256);
       if (!go) continue;
       const int rows = min(a.rpb, s.rq.Rb * a.G - s.row0), me = static_cast<int>(blockIdx.x) - s.c0;
-      // 128 pieces of 4 dims x 32 rows; few partials: more pieces together (one at a time, two CTAs took 10 us)
-      const int v0 = 128 * me / n + warp, v1 = 128 * (me + 1) / n;
-      if (n <= 2) {
-        for (int v = v0; v < v1; v += 32) join_pieces<2, 4>(a, s, n, v, v1, lane, rows);
-      } else if (n <= 4) {
-        for (int v = v0; v < v1; v += 16) join_pieces<4, 2>(a, s, n, v, v1, lane, rows);
-      } else {
-        for (int v = v0; v < v1; v += 8) join_pieces<10, 1>(a, s, n, v, v1, lane, rows);
-      }
+      if (n <= 2)
+        join_share<2, 4>(a, s, n, me, warp, lane, rows);
+      else if (n <= 4)
+        join_share<4, 2>(a, s, n, me, warp, lane, rows);
+      else
+        join_share<10, 1>(a, s, n, me, warp, lane, rows);
     }
   }
   tc_fence_before();
