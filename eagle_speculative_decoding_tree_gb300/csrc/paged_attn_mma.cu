@@ -22,15 +22,16 @@
 namespace eagle {
 namespace {
 
-constexpr int W = 8;         // warps
 constexpr int CK = 16;       // keys
 constexpr float kLazy = 8.f; // log2
 
 template <int D, int MT>
 struct Few {
+  // warps (the registers of D = 128 leave room for 8; half a row is half the bytes a chunk's latency is paid for)
+  static constexpr int W = D == 128 ? 8 : 12;
   static constexpr int RB = 16 * MT;                 // rows
   static constexpr int KB = CK * D * 2;              // K of a stage
-  static constexpr int ST = D == 128 ? 3 : 6;        // stages of a warp
+  static constexpr int ST = D == 128 ? 3 : 4;        // stages of a warp
   static constexpr int RING = ST * 2 * KB;
   static constexpr int LD = D + 8;                   // floats of an output row in shared memory (no bank twice)
   static constexpr int SM_Q = W * RING;              // MT = 2: Q, rows of D, 16-byte chunks swizzled
@@ -45,9 +46,10 @@ struct Maps {
 };
 
 template <int D, int MT, bool SHAPED, bool PRECISE>
-__global__ void __launch_bounds__(W * 32, 1)
+__global__ void __launch_bounds__(Few<D, MT>::W * 32, 1)
     paged_attn_mma_kernel(const __grid_constant__ Maps tm, const PagedAttnArgs a) {
   using F = Few<D, MT>;
+  constexpr int W = F::W;
   constexpr int KS = D / 16, NT = D / 8;  // steps of QK's dims, 8-dim tiles of O
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -363,7 +365,7 @@ cudaError_t launch_mma(const PagedAttnArgs& a, const Maps& tm, int ctas, cudaStr
   auto kern = paged_attn_mma_kernel<D, MT, SHAPED, PRECISE>;
   constexpr int smem = Few<D, MT>::SMEM;
   const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kern), smem, conf);
-  return e != cudaSuccess ? e : launch_pdl_coop(kern, a.together > 0, dim3(ctas), dim3(W * 32), smem, s, tm, a);
+  return e != cudaSuccess ? e : launch_pdl_coop(kern, a.together > 0, dim3(ctas), dim3(Few<D, MT>::W * 32), smem, s, tm, a);
 }
 
 template <int D, int MT>
