@@ -98,7 +98,10 @@ SHAPES = [
     dict(seq=[100, 31], R=5, Hq=6, Hkv=2), dict(seq=[333], R=33, Hq=28, Hkv=4, T=32),
     dict(seq=[40] * 37, Hq=4, Hkv=2), dict(seq=[260, 3], R=17, D=64, Hq=8, Hkv=2, T=128, nodes=[17, 2]),
     dict(seq=[600, 1], R=3, Hq=64, Hkv=1, T=64), dict(seq=[4097], Hq=2, Hkv=1), dict(seq=[70, 20], R=2, Hq=130, Hkv=1),
-    dict(seq=[6000], Hq=16, Hkv=1, T=64), dict(seq=[9001, 0], R=2, Hq=16, Hkv=1), dict(seq=[7000], D=64, Hq=9, Hkv=1, R=3),
+    dict(seq=[300, 77], R=2, Hq=100, Hkv=1, T=64), dict(seq=[222], R=2, Hq=256, Hkv=2),
+    dict(seq=[(37 * i) % 500 for i in range(41)], R=20, Hq=8, Hkv=2, T=64, nodes=[(7 * i) % 21 for i in range(41)]),
+    dict(seq=[(53 * i) % 300 for i in range(70)], R=3, Hq=8, Hkv=2, D=64, nodes=[i % 4 for i in range(70)]),
+    dict(seq=[900, 31, 1500], R=17, Hq=28, Hkv=4, D=64), dict(seq=[6000], Hq=16, Hkv=1, T=64), dict(seq=[9001, 0], R=2, Hq=16, Hkv=1), dict(seq=[7000], D=64, Hq=9, Hkv=1, R=3),
 ]
 SCORES = [dict(), dict(cap=30.0), dict(cap=200.0), dict(window=50), dict(slopes=True), dict(cap=5.0, window=333, slopes=True),
           dict(window=1), dict(window=16, slopes=True)]
@@ -172,6 +175,46 @@ def test_attention_flags_bad_pages(dtype, R):
         table[1, 2] = bad
         assert run_attn(c, table=table)[0] == B.EAGLE_STATUS_BAD_PAGE
         check_attn(c, only=(0, 2))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("R", [1, 61])
+def test_attention_without_rows(R, dtype):
+    """Requests without nodes: nothing is written."""
+    c = attn_case(435, [100, 0, 50], R=R, nodes=[0, 0, 0], dtype=dtype, out="f32")
+    assert run_attn(c)[0] == 0
+    assert (c["out"] == 7).all() and (c["lse"] == 7).all()
+
+
+@pytest.mark.parametrize("R", [1, 61])
+def test_attention_optional_arguments(R):
+    """No lse, no status: the same output."""
+    c = attn_case(436, [333, 20], R=R)
+    ws = run_attn(c)[1]
+    want = c["out"].clone()
+    B.eagle_paged_attn(c["desc"], c["q"], c["kp"], c["vp"], H.i32(c["table"]), c["tk"], c["tv"], H.i32(c["seq"]),
+                       c["mask"], c["out"].zero_(), None, ws)
+    assert torch.equal(c["out"], want)
+
+
+@pytest.mark.parametrize("R,Hkv", [(1, 8), (61, 8), (1, 1)])
+def test_attention_on_two_streams(R, Hkv):
+    """Calls on two streams with workspaces of their own, back to back: the same bits as alone."""
+    cases = [attn_case(437 + i, [2000, 700], R=R, Hq=32, Hkv=Hkv, T=64) for i in range(2)]
+    want, args = [], []
+    for c in cases:
+        ws = run_attn(c)[1]
+        want.append(c["out"].clone())
+        args.append((H.i32(c["table"]), H.i32(c["seq"]), ws))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(5):
+        for c, (table, seq, ws), st in zip(cases, args, streams):
+            B.eagle_paged_attn(c["desc"], c["q"], c["kp"], c["vp"], table, c["tk"], c["tv"], seq, c["mask"], c["out"],
+                               c["lse"], ws, st)
+    torch.cuda.synchronize()
+    for c, w, a in zip(cases, want, args):
+        assert torch.equal(c["out"], w) and int(a[2][:4].view(torch.int32)) == 0
 
 
 def test_attention_clamps_lengths():
