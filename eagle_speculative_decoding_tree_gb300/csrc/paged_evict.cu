@@ -45,12 +45,19 @@ struct EvictArgs {
 __device__ __forceinline__ bool evict_over(const EvictArgs& a, int L) { return L > a.limit && L <= a.g.capacity; }
 
 // The bin that holds the `need`-th largest key (counted from the top bin), for all threads; need becomes its
-// rank among that bin's keys.
-__device__ __forceinline__ int find_bin(const unsigned* hist, int bins, int& need, int* s_scan, int* s_bin) {
+// rank among that bin's keys.  The histogram is left at zero.
+template <int BITS>
+__device__ __forceinline__ int find_bin(unsigned* hist, int& need, int* s_scan, int* s_bin) {
+  constexpr int PER = (1 << BITS) / ST;  // bins a thread, from the top
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  const int per = bins / ST;  // 4 or 2, from the top
-  int mine = 0;
-  for (int i = 0; i < per; ++i) mine += hist[bins - 1 - (t * per + i)];
+  unsigned* first = hist + (1 << BITS) - (t + 1) * PER;  // (the thread's lowest bin)
+  int c[PER], mine = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    c[i] = first[PER - 1 - i];
+    first[PER - 1 - i] = 0;
+    mine += c[i];
+  }
   int inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -59,17 +66,23 @@ __device__ __forceinline__ int find_bin(const unsigned* hist, int bins, int& nee
   }
   if (lane == 31) s_scan[warp] = inc;
   __syncthreads();
-  int before = inc - mine;
-  for (int w = 0; w < warp; ++w) before += s_scan[w];
-  if (before < need && need <= before + mine) {
-    int left = need - before, i = 0;
-    for (;; ++i) {
-      const int c = hist[bins - 1 - (t * per + i)];
-      if (left <= c) break;
-      left -= c;
+  const int of_warp = lane < SW ? s_scan[lane] : 0;
+  int up = of_warp;  // the warps' sums, added up
+#pragma unroll
+  for (int o = 1; o < SW; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, up, o);
+    if (lane >= o) up += x;
+  }
+  int left = need - (__shfl_sync(0xffffffffu, up - of_warp, warp) + inc - mine);
+  if (left > 0 && left <= mine) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (left > 0 && left <= c[i]) {
+        s_bin[0] = (1 << BITS) - 1 - (t * PER + i);
+        s_bin[1] = left;
+      }
+      left -= c[i];
     }
-    s_bin[0] = bins - 1 - (t * per + i);
-    s_bin[1] = left;
   }
   __syncthreads();
   need = s_bin[1];
@@ -114,58 +127,60 @@ __global__ void __launch_bounds__(ST, 3) evict_select_kernel(const EvictArgs a, 
     const float4 x = *reinterpret_cast<const float4*>(w + paged_row_or_zero(a.g, b, h, j, a.status));
     return make_uint4(weight_key(x.x), weight_key(x.y), weight_key(x.z), weight_key(x.w));
   };
-  auto key_at = [&](int j) { return held ? keys[j] : weight_key(w[paged_row_or_zero(a.g, b, h, j, a.status)]); };
+  const int va = lo >> 2, vb = (hi + 3) >> 2;     // in fours; the first and the last may hold others' rows
+  auto keys_of = [&](int v) { return held ? *reinterpret_cast<const uint4*>(keys + 4 * v) : load_keys(4 * v); };
   uint32_t prefix = 0;  // the threshold's bits so far
+  for (int i = t; i < BINS; i += ST) hist[i] = 0;
+  __syncthreads();
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int bits = pass == 2 ? 10 : 11, low = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    for (int i = t; i < BINS; i += ST) hist[i] = 0;
-    __syncthreads();
-    auto count = [&](uint32_t k) {
-      if (pass == 0 || (k >> (low + bits)) == (prefix >> (low + bits)))
-        atomicAdd(&hist[(k >> low) & ((1u << bits) - 1)], 1u);
+    auto count = [&](uint4 k, int v) {
+      const uint32_t x[4] = {k.x, k.y, k.z, k.w};
+      const bool edge = v == va || v == vb - 1;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if ((pass == 0 || (x[e] >> (low + bits)) == (prefix >> (low + bits))) &&
+            (!edge || (4 * v + e >= lo && 4 * v + e < hi)))
+          atomicAdd(&hist[(x[e] >> low) & ((1u << bits) - 1)], 1u);
     };
-    if (pass == 0 || !held) {
-      constexpr int U = 4;
-      for (int j0 = (lo & ~3) + 4 * t; j0 < hi; j0 += 4 * ST * U) {
-        uint4 k[U];
+    constexpr int U = 4;
+    for (int v0 = va + t; v0 < vb; v0 += ST * U) {
+      uint4 k[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (j0 + 4 * ST * u < hi) k[u] = load_keys(j0 + 4 * ST * u);
+      for (int u = 0; u < U; ++u)
+        if (v0 + ST * u < vb) k[u] = pass == 0 ? load_keys(4 * (v0 + ST * u)) : keys_of(v0 + ST * u);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int j = j0 + 4 * ST * u;
-          if (j >= hi) break;
-          if (held) *reinterpret_cast<uint4*>(keys + j) = k[u];
-          const uint32_t x[4] = {k[u].x, k[u].y, k[u].z, k[u].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (j + e >= lo && j + e < hi) count(x[e]);
-        }
-      }
-    } else {
-#pragma unroll 4
-      for (int j0 = (lo & ~3) + 4 * t; j0 < hi; j0 += 4 * ST) {
-        const uint4 k = *reinterpret_cast<const uint4*>(keys + j0);
-        const uint32_t x[4] = {k.x, k.y, k.z, k.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (j0 + e >= lo && j0 + e < hi) count(x[e]);
+      for (int u = 0; u < U; ++u) {
+        const int v = v0 + ST * u;
+        if (v >= vb) break;
+        if (pass == 0 && held) *reinterpret_cast<uint4*>(keys + 4 * v) = k[u];
+        count(k[u], v);
       }
     }
     __syncthreads();
-    const int bin = find_bin(hist, 1 << bits, need, s_scan, s_bin);
+    const int bin = pass == 2 ? find_bin<10>(hist, need, s_scan, s_bin) : find_bin<11>(hist, need, s_scan, s_bin);
     prefix |= static_cast<uint32_t>(bin) << low;
     __syncthreads();
   }
-  // need: how many keys equal to the threshold stay (the lowest rows).  A warp takes a run of candidates.
-  const int per = (hi - lo + SW - 1) / SW, j0 = min(hi, lo + warp * per), j1 = min(hi, j0 + per);
+  // need: how many keys equal to the threshold stay (the lowest rows).  A warp takes a run of fours.
+  const int per = (vb - va + SW - 1) / SW, w0 = min(vb, va + warp * per), w1 = min(vb, w0 + per);
+  auto flags = [&](int v, unsigned& gt, unsigned& eq) {  // of four rows, a bit each
+    const uint4 k = keys_of(v);
+    gt = (k.x > prefix ? 1u : 0u) | (k.y > prefix ? 2u : 0u) | (k.z > prefix ? 4u : 0u) | (k.w > prefix ? 8u : 0u);
+    eq = (k.x == prefix ? 1u : 0u) | (k.y == prefix ? 2u : 0u) | (k.z == prefix ? 4u : 0u) | (k.w == prefix ? 8u : 0u);
+    unsigned in = 15u;
+    if (v == va) in &= 15u << (lo & 3);
+    if (v == vb - 1) in &= 15u >> (4 * vb - hi);
+    gt &= in;
+    eq &= in;
+  };
   int gt = 0, eq = 0;
-#pragma unroll 4
-  for (int j = j0 + lane; j < j1; j += 32) {
-    const uint32_t k = key_at(j);
-    gt += k > prefix;
-    eq += k == prefix;
+  for (int v = w0 + lane; v < w1; v += 32) {
+    unsigned g, e;
+    flags(v, g, e);
+    gt += __popc(g);
+    eq += __popc(e);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -182,17 +197,31 @@ __global__ void __launch_bounds__(ST, 3) evict_select_kernel(const EvictArgs a, 
     gt += s_gt[i];
     eq += s_eq[i];
   }
-  const unsigned below = (1u << lane) - 1;
-#pragma unroll 2
-  for (int i = j0; i < j1; i += 32) {
-    const int j = i + lane;
-    const uint32_t k = j < j1 ? key_at(j) : 0u;
-    const bool is_gt = j < j1 && k > prefix, is_eq = j < j1 && k == prefix;
-    const unsigned mg = __ballot_sync(0xffffffffu, is_gt), me = __ballot_sync(0xffffffffu, is_eq);
-    const int e = eq + __popc(me & below);
-    if (is_gt || (is_eq && e < need)) out[a.sink + gt + __popc(mg & below) + min(e, need)] = j;
-    gt += __popc(mg);
-    eq += __popc(me);
+  for (int v0 = w0; v0 < w1; v0 += 32) {
+    const int v = v0 + lane;
+    unsigned g = 0, e = 0;
+    if (v < w1) flags(v, g, e);
+    const int mine = __popc(g) | (__popc(e) << 16);
+    int inc = mine;  // (at most 128 each)
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    int G = gt + ((inc - mine) & 0xffff), E = eq + ((inc - mine) >> 16);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if ((g >> x) & 1) {
+        out[a.sink + G + min(E, need)] = 4 * v + x;
+        ++G;
+      } else if ((e >> x) & 1) {
+        if (E < need) out[a.sink + G + E] = 4 * v + x;
+        ++E;
+      }
+    }
+    const int all = __shfl_sync(0xffffffffu, inc, 31);
+    gt += all & 0xffff;
+    eq += all >> 16;
   }
 }
 
