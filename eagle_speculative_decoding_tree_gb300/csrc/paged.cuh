@@ -53,6 +53,16 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
+// sm100::tma_load_3d with an L2 cache policy.
+__device__ __forceinline__ void tma_load_3d_hint(void* dst, const void* tmap, int x, int y, int z, uint64_t* bar,
+                                                 uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, "
+      "{%2, %3, %4}], [%5], %6;" ::"r"(sm100::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(sm100::smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
 // Launch with programmatic stream serialization (the kernel waits before it reads or writes); coop: all CTAs resident.
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_pdl_coop(void (*kern)(KArgs...), bool coop, dim3 grid, dim3 block, size_t smem, cudaStream_t s,

@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(Few<D, MT>::W * 32, 1)
   sm100::griddep_wait();
   sm100::griddep_launch_dependents();
   PagedList list = paged_list(a, blockIdx.x, gridDim.x);
+  const uint64_t policy = sm100::policy_evict_first();
   int issued = 0, used = 0;  // chunks
   int parts = 0;
   bool first = true, ok = true;
@@ -93,8 +94,8 @@ __global__ void __launch_bounds__(Few<D, MT>::W * 32, 1)
         uint64_t* bar = &full[warp][issued % F::ST];
         uint8_t* dst = ring + (issued % F::ST) * 2 * F::KB;
         sm100::mbar_arrive_expect_tx(bar, 2 * F::KB);
-        sm100::tma_load_3d(dst, at < pk ? &tm.k : &tm.tk, 0, y, 0, bar);
-        sm100::tma_load_3d(dst + F::KB, at < pk ? &tm.v : &tm.tv, 0, y, 0, bar);
+        tma_load_3d_hint(dst, at < pk ? &tm.k : &tm.tk, 0, y, 0, bar, policy);
+        tma_load_3d_hint(dst + F::KB, at < pk ? &tm.v : &tm.tv, 0, y, 0, bar, policy);
       }
       ++issued;
     };

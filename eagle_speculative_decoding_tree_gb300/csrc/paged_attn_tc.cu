@@ -255,6 +255,7 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
   if (warp == 8) {
     // ------------------------------------------------------------ TMA
     int k_in = 0, v_in = 0, q_in = 0;  // loads issued
+    const uint64_t policy = policy_evict_first();  // (what the step reads next stays in L2: the logits, 20 us of a step)
     PagedList list = paged_list(a, blockIdx.x, gridDim.x);
     while (ok) {
       PagedSegment s;
@@ -289,7 +290,8 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
         if (lane == 0) mbar_arrive_expect_tx(&bar.k_full[ks], bytes);
         ++k_in;
         __syncwarp();
-        if (mine) tma_load_2d(smem + SM_K + ks * TILE + at, tree ? &tm.tk : &tm.k, 64 * (lane & 1), y, &bar.k_full[ks]);
+        if (mine)
+          tma_load_2d_hint(smem + SM_K + ks * TILE + at, tree ? &tm.tk : &tm.k, 64 * (lane & 1), y, &bar.k_full[ks], policy);
         if (u == s.t0) {  // the rows, behind the first keys
           if (seg > 0) ok = __all_sync(0xffffffffu, wait_parity(&bar.q_empty, (seg - 1) & 1, a.err, ERR_QE));
           if (!ok) break;
@@ -304,7 +306,8 @@ __global__ void __launch_bounds__(NT, 1) paged_attn_tc_kernel(const __grid_const
         if (lane == 0) mbar_arrive_expect_tx(&bar.v_full[vs], bytes);
         ++v_in;
         __syncwarp();
-        if (mine) tma_load_2d(smem + SM_V + vs * TILE + at, tree ? &tm.tv : &tm.v, 64 * (lane & 1), y, &bar.v_full[vs]);
+        if (mine)
+          tma_load_2d_hint(smem + SM_V + vs * TILE + at, tree ? &tm.tv : &tm.v, 64 * (lane & 1), y, &bar.v_full[vs], policy);
       }
       ++seg;
     }
