@@ -230,10 +230,15 @@ cudaError_t launch_simt_rows(const PagedAttnArgs& a, bool shaped, int rows, int 
 
 constexpr size_t kHead = 256;  // the error word
 
-// Draft trees go to the tensor cores proper, few rows to the kernels that are bound by the cache's bytes.
+// Draft trees go to the tensor cores proper, few rows to the kernel that is bound by the cache's bytes.  17 to 32 rows, two
+// row tiles there: a chain of 8 x 4 heads over 1K, 8K, 64K and 128K takes 17.4, 25.0, 56.5 and 92.7 us with it, 12.9, 18.3,
+// 57 and 100 on tcgen05 (its joins are shared; its softmax is slower than HBM); 16 requests of 0.5K to 9K 84 and 76.5; on
+// one KV head (2 x 16 rows over 8K) 11.6 and 15.6.
 bool use_tc(const eagle_paged_attn_desc& d) {
-  const int G = d.n_q_heads / d.n_kv_heads;
-  return d.dtype == EAGLE_BF16 && d.head_dim == 128 && G <= 128 && d.rows * G > 32 && d.engine == EAGLE_ENGINE_AUTO;
+  const int G = d.n_q_heads / d.n_kv_heads, rows = d.rows * G;
+  if (d.dtype != EAGLE_BF16 || d.head_dim != 128 || G > 128 || d.engine != EAGLE_ENGINE_AUTO) return false;
+  return rows > 32 || (rows > 16 && d.batch * d.n_kv_heads >= 4 &&
+                       static_cast<long long>(d.max_pages) * d.page_size <= 65536 + 128);
 }
 size_t slot_rows(const eagle_paged_attn_desc& d) { return use_tc(d) ? 128 : d.dtype == EAGLE_BF16 ? 32 : 16; }
 

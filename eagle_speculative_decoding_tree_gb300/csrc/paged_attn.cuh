@@ -4,8 +4,8 @@
 // The work is a list of units: 128 keys (counted from the first one that any row may see; the tree's own
 // keys behind them) of one group, a group being a request, a KV head and a block of query rows.  The groups
 // follow one another (row block, request, head: so that the row blocks of a head, which read the same keys, are
-// at work at the same time and share them through L2; 16 requests of 61 rows over 4.5K: 151 -> 127 us), and each
-// CTA takes an even share of the whole list, so that
+// at work at the same time and share them through L2: one CTA after the other asked HBM for a tile of 64 KB every
+// 1.7 us an SM, 5.8 TB/s), and each CTA takes an even share of the whole list, so that
 // ragged lengths need no sorting and no choice of a split: every SM has the same number of keys, whatever the
 // requests look like.  A CTA's share covers the end of one group, whole groups, and the beginning of another;
 // whole groups are written as they are, of the others the CTA leaves partials (row maxima, sums and
@@ -13,7 +13,8 @@
 // them, in the order of the list: results do not depend on which one that is.  No CTA waits for another, but where a
 // join is so long that its CTAs share it (`together`, a cooperative launch).
 // With kSplitFrom CTAs a group or more, shares end with the groups: each group has CTAs in proportion to its
-// units, and a CTA one segment.
+// units, and a CTA one segment (one token over 8K 15.8 -> 13.0 us, 61 rows 32.5 -> 24.7; 4 requests of 61 rows, two CTAs a
+// group, which stay with even shares: 62.7 and 63.0).
 #pragma once
 
 #include "paged.cuh"

@@ -391,10 +391,11 @@ cudaError_t launch_paged_attn_mma(PagedAttnArgs a, int head_dim, long long pool_
     return cudaErrorInvalidValue;
   const bool two = a.R * a.G > 16;
   a.rpb = two ? 32 : 16;
-  // One CTA joins 40 partials of 16 rows in about 4 us; the others' wait costs about as much.  (Only a call of so few
-  // heads can have such groups, and it alone pays for a cooperative launch: MQA over 130K 37 -> 25 us.)
-  constexpr int kTogether = 40;
-  a.together = a.B * a.g.Hkv * kTogether <= ctas ? kTogether : 0;
+  // Groups of so many CTAs share their join (16 heads on one KV head over 12K, 95 CTAs: 20.2 -> 10.4 us; one token of 8
+  // heads over 8K, 19 CTAs: 13.6 instead of 13.0; four tokens, 16 rows: 15.9 instead of 16.4).  Only calls of few heads
+  // can have such groups, and they alone pay for a cooperative launch.
+  const int together = two ? 14 : 20;
+  a.together = a.B * a.g.Hkv * together <= ctas ? together : 0;
   if (head_dim == 128)
     return two ? launch_mma_kind<128, 2>(a, tm, shaped, precise, ctas, s)
                : launch_mma_kind<128, 1>(a, tm, shaped, precise, ctas, s);

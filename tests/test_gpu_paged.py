@@ -601,3 +601,14 @@ def test_evict_flags():
         assert np.array_equal(new[pages], want[0][pages])
         rest = np.setdiff1d(np.arange(len(new)), pages)
         assert np.array_equal(new[rest], y[rest])
+
+
+@pytest.mark.parametrize("R,G,Hkv,extra", [(8, 4, 8, 1), (8, 4, 8, 5000), (5, 4, 4, 1), (2, 16, 1, 1), (3, 7, 4, 5000)])
+def test_attention_of_chains_in_every_kernel(R, G, Hkv, extra):
+    """17 to 32 rows a KV head: short tables, long ones and the MMA_SYNC engine take different kernels."""
+    for engine in (B.EAGLE_ENGINE_AUTO, B.EAGLE_ENGINE_MMA_SYNC):
+        c = attn_case(500 + R, [1300, 2, 400], R=R, Hq=G * Hkv, Hkv=Hkv, T=16, engine=engine, extra_pages=extra, out="f32")
+        c["see"] = np.broadcast_to(np.tril(np.ones((R, R), bool)), c["see"].shape).copy()
+        c["mask"] = H.words(c["see"])
+        assert run_attn(c)[0] == 0
+        check_attn(c)
