@@ -241,11 +241,12 @@ __global__ void __launch_bounds__(MT + 32, MC) evict_move_kernel(const EvictArgs
   const int u0 = static_cast<int>(total * blockIdx.x / gridDim.x), u1 = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x);
   // the n-th request to be moved, by every warp for itself
   auto request = [&](int n) {
-    for (int b = 0;; b += 32) {
+    for (int b = 0; b < a.batch; b += 32) {
       const unsigned m = __ballot_sync(0xffffffffu, b + lane < a.batch && __ldcg(a.ready + b + lane) != 0);
       if (n < __popc(m)) return b + static_cast<int>(__fns(m, 0, n + 1));
       n -= __popc(m);
     }
+    return 0;  // (not met: there are `live` of them)
   };
   // a piece's rows (by the warp behind the others, two each), and their weights
   auto look_up = [&](int b, int v, int buf) {  // v: piece of the request
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__(MT + 32, MC) evict_move_kernel(const EvictArgs
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int to = min(n0 + lane + 32 * e, a.budget - 1);
-      r[e] = kept[to];
+      r[e] = min(max(kept[to], 0), a.g.capacity - 1);
       page[e] = a.spare[static_cast<size_t>(b) * a.spare_pages + (to >> a.g.shift)];
       dst[e] = ((page[e] * a.g.Hkv + h) << a.g.shift) + (to & ((1 << a.g.shift) - 1));
     }
