@@ -203,6 +203,7 @@ __global__ void __launch_bounds__(MW * 32, 1)
       int next = c0, next_row = 0;
       for (int i = 0; i < F::ST && next < c_end; ++i, next += MW * MK) issue(next, lane == 0 ? row_of(next) : 0);
       if (lane == 0 && next < c_end) next_row = row_of(next);
+      const bool two = rows - r0 > 16;  // (a short path in a deep tree: the second tile has no rows)
       // the rows: queries, softmax sums (inf: no row), positions
       uint32_t qf[MT][KS][4];
       float z[MT][2], slope[MT][2];
@@ -242,6 +243,7 @@ __global__ void __launch_bounds__(MW * 32, 1)
           ldsm4(b, ring32 + stage * F::KB + (ks >> 2) * (MK * 128) + k_key * 128 + ((c ^ (k_key & 7)) << 4));
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
+            if (t && !two) continue;
             mma(sc[t][0], qf[t][ks], b[0], b[1]);
             mma(sc[t][1], qf[t][ks], b[2], b[3]);
           }
@@ -249,7 +251,8 @@ __global__ void __launch_bounds__(MW * 32, 1)
         const bool newest = at + MK > L - n;  // some rows do not see some of these keys
         float got[4] = {0.f, 0.f, 0.f, 0.f};  // keys 2 qc, 2 qc + 1, and 8 further on
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
+        for (int t = 0; t < MT; ++t) {
+          if (t && !two) continue;
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -261,6 +264,7 @@ __global__ void __launch_bounds__(MW * 32, 1)
               if (newest && dist < 0) x = -INFINITY;
               got[e] += sm100::ex2(x);
             }
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
