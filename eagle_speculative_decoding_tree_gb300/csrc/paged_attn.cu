@@ -1,12 +1,13 @@
-// paged_attn.cu -- attention over a paged cache on the ordinary cores (eagle_paged_attn): fp32 caches, and the
-// choice of a kernel.
+// paged_attn.cu -- attention over a paged cache (eagle_paged_attn): the choice of a kernel, and fp32 for up to four query
+// rows of a KV head, on the ordinary cores.
 //
-// A warp takes 8 keys at a time, of K and of V (one bulk copy each: a page's rows of a head are contiguous), in a
-// ring of its own, so that warps meet only at the end of a segment.  Its lanes are the head dims: a lane holds its
+// A warp takes 8 keys at a time, of K and of V (one bulk copy each: a page's rows of a head are contiguous),
+// in a ring of its own, so that warps meet only at the end of a segment.  Its lanes are the head dims: a lane holds its
 // part of four query rows and multiplies 8 keys' parts by them; 32 sums (4 rows x 8 keys) then go to 32 lanes in
 // 31 exchanges, each of which halves what a lane has left to sum.  The softmax is that of a lane's score, with the
-// running maximum and sum of its row; p goes back to all lanes by shuffles, against V's parts.  RB = 4 rows (one
-// token of a group of 4 heads) are bound by the cache's bytes, 16 by the multiplications.
+// running maximum and sum of its row; p goes back to all lanes by shuffles, against V's parts.  Bound by the cache's
+// bytes and the exchanges: one token over 32K, 8 KV heads x 128, 50.7 us, 78 % of measured HBM.  (More rows: 16 at a time
+// took 293 us for 61 x 4 rows over 4K, paged_attn_mma32.cu 114.)
 #include "paged_attn.cuh"
 
 namespace eagle {
@@ -223,11 +224,6 @@ cudaError_t launch_simt(PagedAttnArgs a, bool shaped, int ctas, cudaStream_t s) 
   return e != cudaSuccess ? e : launch_pdl(kern, dim3(ctas), dim3(W * 32), smem, s, a);
 }
 
-template <int D>
-cudaError_t launch_simt_rows(const PagedAttnArgs& a, bool shaped, int rows, int ctas, cudaStream_t s) {
-  return rows <= 4 ? launch_simt<D, 4>(a, shaped, ctas, s) : launch_simt<D, 16>(a, shaped, ctas, s);
-}
-
 constexpr size_t kHead = 256;  // the error word
 
 // Draft trees go to the tensor cores proper, few rows to the kernel that is bound by the cache's bytes.  17 to 32 rows, two
@@ -240,7 +236,7 @@ bool use_tc(const eagle_paged_attn_desc& d) {
   return rows > 32 || (rows > 16 && d.batch * d.n_kv_heads >= 4 &&
                        static_cast<long long>(d.max_pages) * d.page_size <= 65536 + 128);
 }
-size_t slot_rows(const eagle_paged_attn_desc& d) { return use_tc(d) ? 128 : d.dtype == EAGLE_BF16 ? 32 : 16; }
+size_t slot_rows(const eagle_paged_attn_desc& d) { return use_tc(d) ? 128 : 32; }
 
 }  // namespace
 
@@ -289,8 +285,10 @@ cudaError_t launch_paged_attn(const eagle_paged_attn_desc& d, const void* q, con
   if (d.dtype == EAGLE_BF16)
     return launch_paged_attn_mma(a, d.head_dim, static_cast<long long>(d.n_pages) * d.n_kv_heads * d.page_size, shaped,
                                  d.precision == EAGLE_ATTN_PRECISE, sms, s);
-  return d.head_dim == 128 ? launch_simt_rows<128>(a, shaped, rows, sms, s)
-                           : launch_simt_rows<64>(a, shaped, rows, sms, s);
+  if (rows > 4)
+    return launch_paged_attn_mma32(a, d.head_dim, static_cast<long long>(d.n_pages) * d.n_kv_heads * d.page_size, shaped,
+                                   sms, s);
+  return d.head_dim == 128 ? launch_simt<128, 4>(a, shaped, sms, s) : launch_simt<64, 4>(a, shaped, sms, s);
 }
 
 }  // namespace eagle

@@ -53,6 +53,9 @@ struct PagedAttnArgs {
 // paged_attn_mma.cu: bf16, row blocks of 16 (R G <= 16) or 32.
 cudaError_t launch_paged_attn_mma(PagedAttnArgs a, int head_dim, long long pool_rows, bool shaped, bool precise,
                                   int ctas, cudaStream_t s);
+// paged_attn_mma32.cu: fp32, row blocks as above.
+cudaError_t launch_paged_attn_mma32(PagedAttnArgs a, int head_dim, long long pool_rows, bool shaped, int ctas,
+                                    cudaStream_t s);
 // paged_attn_tc.cu: bf16, head_dim 128, G <= 128, row blocks of 128 / G nodes.
 cudaError_t launch_paged_attn_tc(PagedAttnArgs a, int n_pages, bool shaped, bool precise, int ctas, cudaStream_t s);
 

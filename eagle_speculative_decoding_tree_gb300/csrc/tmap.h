@@ -31,19 +31,20 @@ inline bool make_tmap_2d(CUtensorMap* m, CUtensorMapDataType dt, int esz, const 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows of `dim` (64 or 128) bf16 elements as [dim / 64][rows][64], boxes of all halves of `box_rows` rows, each
-// half's rows of 128 bytes swizzled; zero fill.
-inline bool make_tmap_halves(CUtensorMap* m, const void* base, int dim, unsigned long long rows, unsigned box_rows) {
+// Rows of `dim` (64 or 128) bf16 (esz 2) or fp32 (4) elements in parts of 128 bytes, [parts][rows][128 bytes]; boxes of
+// all parts of `box_rows` rows, each part's rows swizzled; zero fill.
+inline bool make_tmap_halves(CUtensorMap* m, const void* base, int dim, unsigned long long rows, unsigned box_rows,
+                             int esz = 2) {
   auto fn = tmap_encode_fn();
   if (!fn) return false;
-  const unsigned halves = static_cast<unsigned>(dim) / 64;
-  const cuuint64_t dims[3] = {64, rows, halves};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(dim) * 2, 128};
-  const cuuint32_t box[3] = {64, box_rows, halves};
+  const unsigned per = 128u / esz, parts = static_cast<unsigned>(dim) / per;
+  const cuuint64_t dims[3] = {per, rows, parts};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(dim) * esz, 128};
+  const cuuint32_t box[3] = {per, box_rows, parts};
   const cuuint32_t es[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return fn(m, esz == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(base),
+            dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace eagle

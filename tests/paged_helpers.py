@@ -111,6 +111,13 @@ def attention(q, k, v, tk, tv, see, L, n, scale, cap=0.0, window=0, slopes=None,
     return out, lse, e_out, e_lse
 
 
+def fp32_kinds(rows):
+    """(adds, weights' relative error) of fp32 attention over so many rows of a KV head: up to four, sums of products
+    by pairs.  Above, three tf32 products a product (12 of 2^-24), four steps of dims in twelve instructions of nine
+    terms each, cut off at 24 bits, and four sums of those; against V, 12 and three instructions' 27, and one sum."""
+    return (9, 0.0) if rows <= 4 else (12 + 108 + 4, 40 * U32)
+
+
 def check_attention(out, lse, ref, bf16, p_error):
     """out bf16: half a step of the result more; p_error: what the weights may be off by, relative (2^-17 where they
     enter the product as two bf16 terms, 2^-9 as one, 0 in fp32), against the sum of p |v|."""

@@ -75,6 +75,9 @@ def check_attn(c, only=None):
     tk, tv = (H.f64(c["tk"]), H.f64(c["tv"])) if c["tk"] is not None else (None, None)
     sl = None if c["slopes"] is None else H.f64(c["slopes"])
     bf = c["outt"] == "bf16"
+    adds, rel = H.fp32_kinds(c["R"] * c["q"].shape[2] // c["Hkv"])
+    if c["dtype"] == "bf16":
+        adds, rel = 144, 2.0 ** (-16 if c["precision"] == B.EAGLE_ATTN_PRECISE else -8)
     for b, L in enumerate(c["seq"]):
         n = c["R"] if c["nodes"] is None else c["nodes"][b]
         assert (out[b, n:] == 7.0).all() and (lse[b, n:] == 7.0).all()
@@ -82,10 +85,9 @@ def check_attn(c, only=None):
             continue
         k, v = H.rows_of(kp, c["table"][b], L), H.rows_of(vp, c["table"][b], L)
         ref = H.attention(q[b], k, v, None if tk is None else tk[b], None if tv is None else tv[b], c["see"][b], L, n,
-                          c["scale"], c["cap"], c["window"], sl, 9 if c["dtype"] == "f32" else 144)
+                          c["scale"], c["cap"], c["window"], sl, adds)
         mass = H.attention(q[b], k, np.abs(v), None if tk is None else tk[b], None if tv is None else np.abs(tv[b]),
                            c["see"][b], L, n, c["scale"], c["cap"], c["window"], sl)[0]
-        rel = 0 if c["dtype"] == "f32" else 2.0 ** (-16 if c["precision"] == B.EAGLE_ATTN_PRECISE else -8)
         H.check_attention(out[b, :n], lse[b, :n], ref, bf, rel * mass)
 
 

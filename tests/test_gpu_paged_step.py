@@ -30,10 +30,10 @@ def check_layer(st, l, see, seq, table, lse):
     out, z = H.f64(st.out[l]), H.f64(lse)
     for b in range(st.B):
         k, v = H.rows_of(kp, table[b], seq[b]), H.rows_of(vp, table[b], seq[b])
-        adds = 144 if bf else 9
+        adds, rel = (144, 2.0 ** -16) if bf else H.fp32_kinds(st.R * w.group)
         ref = H.attention(q[b], k, v, tk[b], tv[b], see[b], seq[b], st.R, 1 / math.sqrt(w.head_dim), adds=adds)
         mass = H.attention(q[b], k, np.abs(v), tk[b], np.abs(tv[b]), see[b], seq[b], st.R, 1 / math.sqrt(w.head_dim))[0]
-        H.check_attention(out[b], z[b], ref, bf, (2.0 ** -16 if bf else 0) * mass)
+        H.check_attention(out[b], z[b], ref, bf, rel * mass)
 
 
 @pytest.mark.parametrize("name,prefix,layers,batch,page", [("llama8b", 333, 2, 1, 64), ("concurrency", 200, 2, 3, 16),
