@@ -30,17 +30,19 @@ __device__ __forceinline__ float rcp_approx(float x) {
 }
 
 // The cap in log2 units: c tanh(x) = c - 2 c / (1 + e^2x), in which neither end overflows (e^2x = inf: c, 0: -c); off by
-// a few roundings of c, as c tanh itself in fp32.
+// a few roundings of c, 2e-6 at 30, which a bf16 result does not show.  EXACT (fp32): c tanhf(x), off by a few of itself.
+template <bool EXACT = false>
 __device__ __forceinline__ float cap_score(const ScoreShape& s, float raw) {
+  if (EXACT) return s.cap_log2 * tanhf(raw * s.cap_x);
   return fmaf(-2.f * s.cap_log2, rcp_approx(1.f + sm100::ex2(raw * s.cap_mul)), s.cap_log2);
 }
 
 // A raw dot product as a score in log2 units; slope_log2 = slope * log2 e (0: none), dist the row's position minus the
 // key's.
-template <bool SHAPED>
+template <bool SHAPED, bool EXACT = false>
 __device__ __forceinline__ float shape_score(const ScoreShape& s, float raw, float slope_log2, int dist) {
   if (!SHAPED) return raw * s.scale_log2;
-  float t = s.cap_log2 > 0.f ? cap_score(s, raw) : raw * s.scale_log2;
+  float t = s.cap_log2 > 0.f ? cap_score<EXACT>(s, raw) : raw * s.scale_log2;
   t = fmaf(-slope_log2, static_cast<float>(dist), t);
   return s.window > 0 && dist >= s.window ? -INFINITY : t;
 }

@@ -49,6 +49,7 @@ inline PagedGeom paged_geom(const int32_t* table, int n_pages, int max_pages, in
 struct ScoreShape {
   float scale_log2;  // scale * log2 e (no cap)
   float cap_log2;    // cap * log2 e; 0: none
+  float cap_x;       // scale / cap
   float cap_mul;     // 2 log2 e * scale / cap
   // where |raw| <= cap_small the capped score is raw (p[0] + p[1] raw^2 + .. + p[4] raw^8): tanh's Taylor polynomial,
   // off by less than 2.5e-7 of itself for arguments up to 0.35
@@ -64,6 +65,7 @@ inline ScoreShape score_shape(float scale, float cap, int window, const float* s
   s.cap_log2 = static_cast<float>(cap * log2e);
   s.cap_mul = cap > 0.f ? static_cast<float>(2.0 * log2e * scale / cap) : 0.f;
   const double x = cap > 0.f ? static_cast<double>(scale) / cap : 0.0;  // tanh's argument is raw x
+  s.cap_x = static_cast<float>(x);
   s.cap_small = x > 0.0 ? static_cast<float>(0.35 / x) : 0.f;
   const double c[5] = {1.0, -1.0 / 3, 2.0 / 15, -17.0 / 315, 62.0 / 2835};
   double xx = scale * log2e;

@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(W * 32, 1) paged_attn_simt_kernel(const PagedA
           on = (bits[(at - pk) >> 3] >> key) & 1;
           dist = depth[g] - kdepth;
         }
-        const float t = on ? shape_score<SHAPED>(a.shape, raw, slope[g], dist) : -INFINITY;
+        const float t = on ? shape_score<SHAPED, true>(a.shape, raw, slope[g], dist) : -INFINITY;
         float top = t;
 #pragma unroll
         for (int d = 4; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));

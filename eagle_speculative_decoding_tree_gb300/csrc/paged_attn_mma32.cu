@@ -3,8 +3,8 @@
 //
 // A product of two fp32 numbers is taken as three of tf32 (11 bits): x = b + s with b = x rounded to tf32 and s the rest,
 // and x y = b b + b s + s b, off by 3 2^-22 of |x y| at most (both s rounded, s s left out).  The instructions' own sums
-// are cut off, not rounded, so that they are kept short: four steps of a score's dims, one chunk's keys of an output;
-// the sums of those are ordinary fp32 additions.
+// are cut off, not rounded, so that they are kept short: two steps of a score's dims, one chunk's keys of an output;
+// the sums of those are ordinary fp32 additions.  (Products with a small part, 2^-11 of the others, have sums of their own.)
 //     S = Q K^T   A = Q from shared memory, B = K's rows as they lie (ldmatrix moves 32-bit elements as well)
 //     O += P V    A = P, S's registers as they lie: key 2 c of a lane's column c is the product's key c, 2 c + 1 its c + 4;
 //                 B = V, element by element, the same keys
@@ -152,40 +152,41 @@ __global__ void __launch_bounds__(Few<D, MT>::W * 32, 1)
       const int valid = tree ? min(CK, s.rq.Rb - (at - pk)) : min(CK, s.rq.L - s.rq.k0 - at);
       // ---- S
       float sc[MT][4];
+      float rest[MT][4];  // of the products with a small part
 #pragma unroll
-      for (int t = 0; t < MT; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
+      for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int k4 = 0; k4 < KS; k4 += 4) {
-        float part[MT][4];
+        for (int e = 0; e < 4; ++e) sc[t][e] = rest[t][e] = 0.f;
 #pragma unroll
-        for (int t = 0; t < MT; ++t) part[t][0] = part[t][1] = part[t][2] = part[t][3] = 0.f;
+      for (int k2 = 0; k2 < KS; k2 += 2) {
+        uint32_t b[4], bb[4], bs[4];  // two steps' K
+        const int c = 2 * k2 + (lane >> 3), key = lane & 7;
+        ldsm4(b, kb + (c >> 3) * (CK * 128) + key * 128 + (((c & 7) ^ key) << 4));
 #pragma unroll
-        for (int k2 = k4; k2 < k4 + 4; k2 += 2) {
-          uint32_t b[4], bb[4], bs[4];  // two steps' K
-          const int c = 2 * k2 + (lane >> 3), key = lane & 7;
-          ldsm4(b, kb + (c >> 3) * (CK * 128) + key * 128 + (((c & 7) ^ key) << 4));
+        for (int e = 0; e < 4; ++e) split(__uint_as_float(b[e]), bb[e], bs[e]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) split(__uint_as_float(b[e]), bb[e], bs[e]);
+        for (int t = 0; t < MT; ++t) {
+          float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int ks = k2; ks < k2 + 2; ++ks)
+          for (int ks = k2; ks < k2 + 2; ++ks) {
+            uint32_t q[4], qb[4], qs[4];
+            const int r = 16 * t + (lane & 15), qch = 2 * ks + (lane >> 4);
+            ldsm4(q, q32 + r * (D * 4) + ((qch ^ (r & 7)) << 4));
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
-              uint32_t q[4], qb[4], qs[4];
-              const int r = 16 * t + (lane & 15), qch = 2 * ks + (lane >> 4);
-              ldsm4(q, q32 + r * (D * 4) + ((qch ^ (r & 7)) << 4));
+            for (int e = 0; e < 4; ++e) split(__uint_as_float(q[e]), qb[e], qs[e]);
+            const int e = 2 * (ks - k2);
+            mma32(rest[t], qs, bb[e], bb[e + 1]);
+            mma32(rest[t], qb, bs[e], bs[e + 1]);
+            mma32(part, qb, bb[e], bb[e + 1]);
+          }
 #pragma unroll
-              for (int e = 0; e < 4; ++e) split(__uint_as_float(q[e]), qb[e], qs[e]);
-              const int e = 2 * (ks - k2);
-              mma32(part[t], qs, bb[e], bb[e + 1]);
-              mma32(part[t], qb, bs[e], bs[e + 1]);
-              mma32(part[t], qb, bb[e], bb[e + 1]);
-            }
+          for (int e = 0; e < 4; ++e) sc[t][e] += part[e];
         }
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[t][e] += part[t][e];
       }
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[t][e] += rest[t][e];
       // ---- scores in log2 units, -inf where hidden
       if (SHAPED || tree || valid < CK) {
         int kd[2] = {0, 0};  // depths of the lane's tree keys
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(Few<D, MT>::W * 32, 1)
               const int key = 2 * qc + e;
               float& x = sc[t][2 * i + e];
               const int dist = tree ? depth[t][i] - kd[e] : s.rq.L + depth[t][i] - (s.rq.k0 + at + key);
-              if (SHAPED) x = shape_score<true>(a.shape, x, slope[t][i], dist);
+              if (SHAPED) x = shape_score<true, true>(a.shape, x, slope[t][i], dist);
               x = (bits >> key) & 1 ? x : -INFINITY;
             }
           }

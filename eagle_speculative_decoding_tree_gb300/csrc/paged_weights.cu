@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(W * 32) paged_weights_simt_kernel(const Weight
         const int dist = L - n + mm - (at + key);
         const float z = a.lse[(static_cast<size_t>(s.b) * a.R + node) * a.Hq + s.h * a.G + g];
         const float slope = SHAPED && a.shape.slopes ? a.shape.slopes[s.h * a.G + g] * kLog2e : 0.f;
-        const float t = shape_score<SHAPED>(a.shape, raw, slope, dist);
+        const float t = shape_score<SHAPED, true>(a.shape, raw, slope, dist);
         if (row < rows && dist >= 0 && z != -INFINITY) got += sm100::ex2(t - z * kLog2e);
       }
       got += __shfl_xor_sync(0xffffffffu, got, 8);

@@ -649,7 +649,8 @@ typedef struct {
  * A row with no key gets zeros and lse -inf.  Cache rows behind seq_len may hold anything; rows before it
  * and the rows of existing nodes may take part in products with weight 0 where a mask or the window hides
  * them, so a value there that is not finite spoils other rows.  Pages that lie wholly before the window of
- * every row are not read.  fp32 sums and softmax; precision as eagle_tree_attn.
+ * every row are not read.  fp32 sums and softmax; precision as eagle_tree_attn; fp32 inputs, from five rows of a
+ * KV head on: every product of two numbers off by at most 2^-20 of itself (three tf32 products).
  * ws: eagle_workspace_size(EAGLE_WS_PAGED_ATTN, d) bytes, zero-filled before its first use; one workspace
  * serves one stream at a time, and any descriptors in turn that it is large enough for.  Its first 4 bytes
  * are an error word that a bounded wait ORs a bit into when it gives up (2 s).

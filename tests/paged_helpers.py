@@ -113,9 +113,10 @@ def attention(q, k, v, tk, tv, see, L, n, scale, cap=0.0, window=0, slopes=None,
 
 def fp32_kinds(rows):
     """(adds, weights' relative error) of fp32 attention over so many rows of a KV head: up to four, sums of products
-    by pairs.  Above, three tf32 products a product (12 of 2^-24), four steps of dims in twelve instructions of nine
-    terms each, cut off at 24 bits, and four sums of those; against V, 12 and three instructions' 27, and one sum."""
-    return (9, 0.0) if rows <= 4 else (12 + 108 + 4, 40 * U32)
+    by pairs.  Above, three tf32 products a product (12 of 2^-24), two steps of dims in two instructions of nine terms
+    each, cut off at 24 bits, eight sums of those and one of the small products'; against V, 12 and three instructions'
+    27, and one sum."""
+    return (9, 0.0) if rows <= 4 else (12 + 18 + 8 + 1, 40 * U32)
 
 
 def check_attention(out, lse, ref, bf16, p_error):
