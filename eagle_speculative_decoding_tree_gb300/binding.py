@@ -409,6 +409,7 @@ class LayerPointers:
         every = [t for ts in self.tensors for t in ts]
         self.layers = min(len(ts) for ts in self.tensors)
         self.dtypes, self.devices = {t.dtype for t in every}, {t.get_device() for t in every}
+        self.addresses = tuple(ctypes.addressof(x) for x in (self.k, self.v, self.tk, self.tv))
 
 
 def eagle_kv_commit(desc: CommitDesc, layers: LayerPointers, n_acc, path, seq_len, commit_pos,
@@ -589,7 +590,7 @@ def eagle_paged_commit(desc: PagedCommitDesc, layers: LayerPointers, page_table,
     _layers_fit(layers, desc.layers, dev, _element(desc.dtype))
     f = _element(desc.feat_dtype)
     _check("eagle_paged_commit", load().eagle_paged_commit(
-        ctypes.byref(desc), layers.k, layers.v, layers.tk, layers.tv, _at(page_table, torch.int32, "page_table", dev),
+        ctypes.byref(desc), *layers.addresses, _at(page_table, torch.int32, "page_table", dev),
         _at(n_acc, torch.int32, "n_acc", dev), _at(path, torch.int32, "path", dev),
         _at(seq_len, torch.int32, "seq_len", dev), _at(commit_pos, torch.int32, "commit_pos", dev),
         _at(feat_pages, f, "feat_pages", dev), _at(tree_feat, f, "tree_feat", dev),
@@ -654,6 +655,7 @@ class PagedLayerPointers:
             raise ValueError("as many tensors of each kind as layers")
         self.layers, self.dtypes = n, {t.dtype for t in (*k_pages, *v_pages)}
         self.devices = {t.get_device() for ts in self.tensors for t in ts}
+        self.addresses = tuple(ctypes.addressof(x) for x in (self.k, self.v, self.w))
 
 
 def eagle_paged_evict(desc: PagedEvictDesc, layers: PagedLayerPointers, page_table, spare, seq_len, kept, ws,
@@ -663,7 +665,7 @@ def eagle_paged_evict(desc: PagedEvictDesc, layers: PagedLayerPointers, page_tab
     _layers_fit(layers, desc.layers, dev, _element(desc.dtype))
     i32 = torch.int32
     _check("eagle_paged_evict", load().eagle_paged_evict(
-        ctypes.byref(desc), layers.k, layers.v, layers.w, _at(page_table, i32, "page_table", dev),
+        ctypes.byref(desc), *layers.addresses, _at(page_table, i32, "page_table", dev),
         _at(spare, i32, "spare", dev), _at(seq_len, i32, "seq_len", dev), _at(kept, i32, "kept", dev),
         _at(status, i32, "status", dev), _at(ws, ws.dtype, "ws", dev), ws.numel() * ws.element_size(),
         _stream(stream)))
