@@ -614,3 +614,16 @@ def test_attention_of_chains_in_every_kernel(R, G, Hkv, extra):
         c["mask"] = H.words(c["see"])
         assert run_attn(c)[0] == 0
         check_attn(c)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("R,Hq,Hkv", [(8, 32, 8), (1, 16, 2), (4, 16, 4)])
+def test_attention_joins_of_many_partials(R, Hq, Hkv, dtype):
+    """One request over all CTAs, behind a table too long for the tree kernel: its CTAs share the join."""
+    c = attn_case(600 + R, [5003], R=R, Hq=Hq, Hkv=Hkv, T=16, extra_pages=4500, dtype=dtype, out="f32", cap=40.0)
+    first = None
+    for _ in range(2):
+        assert run_attn(c)[0] == 0
+        first = c["out"].clone() if first is None else first
+        assert torch.equal(c["out"], first)
+    check_attn(c)
