@@ -115,13 +115,13 @@ __device__ __forceinline__ int split_start(const PagedList& l, int g, int u) {
   return g + min(static_cast<int>(__umulhi(static_cast<unsigned>(u), l.pace)), l.ctas - l.groups);
 }
 
-// inc, ginc of the 32 requests from l.b0 on, of row block l.plane; all: of all row blocks
-__device__ __forceinline__ void list_scan(const PagedAttnArgs& a, PagedList& l, bool all = false) {
+// inc, ginc of the 32 requests from l.b0 on, of row block l.plane
+__device__ __forceinline__ void list_scan(const PagedAttnArgs& a, PagedList& l) {
   const int lane = threadIdx.x & 31;
   l.inc = l.ginc = 0;
   if (l.b0 + lane < a.B) {
     const PagedRequest r = paged_request(a, l.b0 + lane);
-    l.ginc = (all ? r.blocks : r.blocks > l.plane ? 1 : 0) * a.g.Hkv;
+    l.ginc = r.blocks > l.plane ? a.g.Hkv : 0;
     l.inc = r.units * l.ginc;
   }
 #pragma unroll
@@ -137,14 +137,25 @@ __device__ __forceinline__ void list_scan(const PagedAttnArgs& a, PagedList& l, 
 __device__ __forceinline__ PagedList paged_list(const PagedAttnArgs& a, int cta, int ctas) {
   PagedList l;
   l.total = l.groups = l.plane = 0;
-  const bool once = a.B <= 32 && a.R * a.G <= a.rpb;  // (the common case: one scan does)
-  for (l.b0 = 0; l.b0 < a.B; l.b0 += 32) {
-    list_scan(a, l, !once);
-    l.total += __shfl_sync(0xffffffffu, l.inc, 31);
-    l.groups += __shfl_sync(0xffffffffu, l.ginc, 31);
-  }
   l.b0 = l.base = l.gbase = 0;
-  if (!once) list_scan(a, l);
+  if (a.B <= 32 && a.R * a.G <= a.rpb) {  // (the common case: one scan does)
+    list_scan(a, l);
+    l.total = __shfl_sync(0xffffffffu, l.inc, 31);
+    l.groups = __shfl_sync(0xffffffffu, l.ginc, 31);
+  } else {
+#pragma unroll 4
+    for (int b = threadIdx.x & 31; b < a.B; b += 32) {
+      const PagedRequest r = paged_request(a, b);
+      l.groups += r.blocks * a.g.Hkv;
+      l.total += r.units * r.blocks * a.g.Hkv;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      l.groups += __shfl_xor_sync(0xffffffffu, l.groups, o);
+      l.total += __shfl_xor_sync(0xffffffffu, l.total, o);
+    }
+    list_scan(a, l);
+  }
   l.ctas = min(ctas, l.total);
   l.split = l.groups * kSplitFrom <= l.ctas;
   l.per = l.more = l.at = l.end = 0;
